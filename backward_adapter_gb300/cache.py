@@ -1,0 +1,174 @@
+"""A quantized K/V cache: written, read back and attended to in place (fa_cache_write, fa_cache_read, fa_decode).
+
+The cache is four planes: k_q, v_q (int8 [B, Hkv, S, D] for q8_0, uint8 [B, Hkv, S, D / 2] for q4_0) and k_d, v_d
+(float16 [B, Hkv, S, D / 32]); new_cache makes them, and fwd_q8 / bwd_q8 / fwd_q4 / bwd_q4 train over them.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import fa_train as ft
+
+FORMATS = {"q8_0": ft.FA_KV_Q8_0, "q4_0": ft.FA_KV_Q4_0}
+
+
+def new_cache(B: int, Hkv: int, S: int, D: int, fmt: str = "q8_0", device="cuda"):
+    """Planes (k_q, k_d, v_q, v_d) of a cache whose values are all 0, with room for S keys per sequence."""
+    if fmt not in FORMATS:
+        raise ValueError(f"fmt {fmt!r}: 'q8_0' or 'q4_0'")
+    if D % 32 != 0:
+        raise ValueError(f"D {D}: a multiple of 32")
+    planes = []
+    for _ in range(2):
+        if fmt == "q4_0":
+            planes.append(torch.full((B, Hkv, S, D // 2), 0x88, dtype=torch.uint8, device=device))
+        else:
+            planes.append(torch.zeros((B, Hkv, S, D), dtype=torch.int8, device=device))
+        planes.append(torch.zeros((B, Hkv, S, D // 32), dtype=torch.float16, device=device))
+    return tuple(planes)
+
+
+def _cache(k_q, k_d, v_q, v_d) -> ft.FaCache:
+    """fa_cache of the planes; the format follows from the values' dtype."""
+    if k_q.dim() != 4:
+        raise ValueError(f"k_q must be 4-D (got {k_q.dim()}-D)")
+    B, Hkv, S, width = k_q.shape
+    if k_q.dtype == torch.uint8:
+        fmt, D = ft.FA_KV_Q4_0, 2 * width
+    elif k_q.dtype == torch.int8:
+        fmt, D = ft.FA_KV_Q8_0, width
+    else:
+        raise TypeError(f"k_q has dtype {k_q.dtype}: int8 (q8_0) or uint8 (q4_0)")
+    if v_q.dtype != k_q.dtype:
+        raise TypeError(f"v_q has dtype {v_q.dtype}, expected {k_q.dtype}")
+    if k_d.dtype != torch.float16 or v_d.dtype != torch.float16:
+        raise TypeError("k_d and v_d must be float16 [B, Hkv, S, D / 32]")
+    if v_q.shape != k_q.shape:
+        raise ValueError(f"v_q has shape {tuple(v_q.shape)}, expected {tuple(k_q.shape)}")
+    scales = (B, Hkv, S, D // 32)
+    if k_d.shape != scales or v_d.shape != scales:
+        raise ValueError(f"k_d, v_d have shapes {tuple(k_d.shape)}, {tuple(v_d.shape)}, expected {scales}")
+    device = k_q.device
+    if k_d.device != device or v_q.device != device or v_d.device != device:
+        raise ValueError("the planes of a cache must be on one device")
+    ft._need_cuda(k_q, k_d, v_q, v_d)
+    return ft.FaCache(B, Hkv, S, D, fmt, 0, k_q.data_ptr(), k_d.data_ptr(), v_q.data_ptr(), v_d.data_ptr())
+
+
+def _rows_shape(c: ft.FaCache, n: int, layout: str):
+    if layout == "bhsd":
+        return (c.B, c.Hkv, n, c.D)
+    if layout == "bshd":
+        return (c.B, n, c.Hkv, c.D)
+    raise ValueError(f"layout {layout!r}: 'bhsd' or 'bshd'")
+
+
+def _per_sequence(name: str, t: torch.Tensor, c: ft.FaCache, device) -> int:
+    if t.dtype != torch.int64:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.int64")
+    if t.shape != (c.B,):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(c.B,)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def cache_write(k, v, k_q, k_d, v_q, v_d, begin, count=None, *, layout: str = "bhsd", stream=None) -> None:
+    """Quantizes new rows of K and V into the cache: row r of sequence b becomes key begin[b] + r.
+
+    k, v: [B, Hkv, n, D] (or [B, n, Hkv, D] with layout "bshd"), bfloat16 or float32, strided like qk_norm_rope's
+    inputs. begin: an int for every sequence, or int64 [B] on the device (a row that would land outside the cache is
+    not written and is reported by device_status()). count: int64 [B] on the device: only the first count[b] rows of
+    sequence b are written. Nothing else in the cache changes.
+    """
+    lib = ft.load_library()
+    c = _cache(k_q, k_d, v_q, v_d)
+    device = k_q.device
+    n = k.shape[2 if layout == "bhsd" else 1] if k.dim() == 4 else -1
+    shape = _rows_shape(c, n, layout)
+    for name, t in (("k", k), ("v", v)):
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if v.dtype != k.dtype:
+        raise TypeError(f"v has dtype {v.dtype}, expected {k.dtype}")
+    at, first = (_per_sequence("begin", begin, c, device), 0) if isinstance(begin, torch.Tensor) else (None, int(begin))
+    counts = None if count is None else _per_sequence("count", count, c, device)
+    ft._launch(device, lib.fa_cache_write, c, ft._view(k, layout), ft._view(v, layout), ft._dtype_code(k), n, at, first,
+               counts, ft._stream(device, stream))
+
+
+def cache_read(k_q, k_d, v_q, v_d, begin: int = 0, n_rows=None, *, dtype=torch.bfloat16, layout: str = "bhsd", k=None,
+               v=None, stream=None):
+    """The values of keys begin .. begin + n_rows - 1 (default: to the end) of every sequence and head: (k, v)
+    [B, Hkv, n_rows, D] (or [B, n_rows, Hkv, D]) in dtype (bfloat16 or float32), or written into the given k and v."""
+    lib = ft.load_library()
+    c = _cache(k_q, k_d, v_q, v_d)
+    device = k_q.device
+    begin = int(begin)
+    n = c.S - begin if n_rows is None else int(n_rows)
+    if begin < 0 or n < 0 or begin + n > c.S:
+        raise ValueError(f"rows [{begin}, {begin + n}) outside the {c.S} keys")
+    shape = _rows_shape(c, n, layout)
+    k = torch.empty(shape, dtype=dtype, device=device) if k is None else k
+    v = torch.empty(shape, dtype=k.dtype, device=device) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype != k.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {k.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    ft._launch(device, lib.fa_cache_read, c, begin, n, ft._dtype_code(k), ft._view(k, layout), ft._view(v, layout),
+               ft._stream(device, stream))
+    return k, v
+
+
+def decode(q, k_q, k_d, v_q, v_d, lengths=None, *, scale=None, window: int = 0, layout: str = "bhsd", out=None,
+           lse=None, workspace=None, stream=None):
+    """Attention of the newest Sq tokens (1 to 16) of every sequence over its quantized cache: (O, LSE [B, Hq, Sq]).
+
+    q: bfloat16 [B, Hq, Sq, D] (or [B, Sq, Hq, D] with layout "bshd"). lengths: int64 [B] on the device, the keys of
+    each sequence with the Sq tokens' own among them (without: all S keys); query i sits at lengths[b] - Sq + i and sees
+    the keys up to its position, with window > 0 only the last `window` before it. A query that sees no key gets O = 0
+    and LSE = 0.
+    """
+    lib = ft.load_library()
+    c = _cache(k_q, k_d, v_q, v_d)
+    device = k_q.device
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q has dtype {q.dtype}, expected torch.bfloat16")
+    if q.dim() != 4:
+        raise ValueError(f"q must be 4-D (got {q.dim()}-D)")
+    if layout == "bhsd":
+        B, Hq, Sq, D = q.shape
+    elif layout == "bshd":
+        B, Sq, Hq, D = q.shape
+    else:
+        raise ValueError(f"layout {layout!r}: 'bhsd' or 'bshd'")
+    if B != c.B or D != c.D:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected batch {c.B} and {c.D} features as in the cache")
+    if q.device != device:
+        raise ValueError(f"q is on {q.device}, the cache on {device}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != device:
+        raise ValueError(f"out must be {q.dtype} {tuple(q.shape)} on {device}")
+    if lse is None:
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=device)
+    elif lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != device:
+        raise ValueError(f"lse must be float32 {(B, Hq, Sq)} on {device}")
+    ft._need_cuda(q, out, lse)
+    at = None if lengths is None else _per_sequence("lengths", lengths, c, device)
+    p = ft.FaDecodeParams(Hq, Sq, int(window), ft.FA_LAYOUT_BSHD if layout == "bshd" else ft.FA_LAYOUT_BHSD,
+                          1.0 / math.sqrt(D) if scale is None else float(scale), 0)
+    ws_bytes = int(lib.fa_decode_workspace_size(p, c))
+    ws = ft._scratch(ws_bytes, device, workspace, stream)
+    ft._launch(device, lib.fa_decode, p, q.data_ptr(), c, at, out.data_ptr(), lse.data_ptr(), ft._ptr(ws), ws_bytes,
+               ft._stream(device, stream))
+    return out, lse

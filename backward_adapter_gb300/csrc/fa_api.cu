@@ -10,13 +10,14 @@
 #include <cstring>
 #include <mutex>
 
-#include "fa_train.h"
-#include "fa_internal.h"
+#include "fa_check.h"
 
 namespace fa {
 namespace {
 
 thread_local char g_last_error[256] = "";
+
+}  // namespace
 
 void set_error(const char* fmt, ...) {
   va_list ap;
@@ -25,15 +26,9 @@ void set_error(const char* fmt, ...) {
   va_end(ap);
 }
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+void clear_error() { g_last_error[0] = '\0'; }
 
-constexpr int kMaxSeq = 1 << 24;
-// Largest element count of one tensor (2^40: terabytes, more than a GB300 holds). Keeps every byte
-// count of the validation and every 64-bit offset in the kernels far from overflow.
-constexpr double kMaxElems = 1099511627776.0;
-
-bool too_large(double a, double b, double c, double d) { return a * b * c * d > kMaxElems; }
+namespace {
 
 fa_status check_params(const fa_params* p, Shape& s) {
   g_last_error[0] = '\0';
@@ -60,7 +55,8 @@ fa_status check_params(const fa_params* p, Shape& s) {
   if (p->deterministic != 0 && p->deterministic != 1) {
     set_error("deterministic=%d must be 0 or 1", p->deterministic); return FA_ERR_INVALID_ARG;
   }
-  if (p->kv_format != FA_KV_DTYPE && p->kv_format != FA_KV_Q8_0 && p->kv_format != FA_KV_F16) {
+  if (p->kv_format != FA_KV_DTYPE && p->kv_format != FA_KV_Q8_0 && p->kv_format != FA_KV_F16 &&
+      p->kv_format != FA_KV_Q4_0) {
     set_error("kv_format=%d invalid", p->kv_format); return FA_ERR_INVALID_ARG;
   }
   if (p->kv_format == FA_KV_F16 && p->dtype != FA_BF16) {
@@ -101,7 +97,7 @@ size_t mask_bytes(const Shape& s) {
   return (size_t)s.mask_batch * s.Sq * s.Sk * (s.mask_kind == MK_ADD ? 4 : 1);
 }
 
-struct Span { const void* p; size_t n; const char* name; };
+}  // namespace
 
 bool overlaps(const Span& a, const Span& b) {
   if (a.p == nullptr || b.p == nullptr || a.n == 0 || b.n == 0) return false;
@@ -125,6 +121,35 @@ fa_status check_buffers(const Span* in, int nin, const Span* out, int nout) {
   return FA_OK;
 }
 
+// Bytes from the first to the last element of the view's rows, the dimensions ordered by stride.
+fa_status check_view(const fa_view* v, int B, int S, int H, int D, size_t es, bool written, const char* name, Span& out) {
+  out = Span{nullptr, 0, name};
+  if (B == 0 || S == 0 || H == 0) return FA_OK;
+  if (v == nullptr || v->ptr == nullptr) { set_error("%s is NULL", name); return FA_ERR_INVALID_ARG; }
+  struct Dim { int64_t n, stride; } d[3] = {{B, v->stride_b}, {S, v->stride_s}, {H, v->stride_h}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (d[j].stride > d[j + 1].stride) { const Dim t = d[j]; d[j] = d[j + 1]; d[j + 1] = t; }
+  int64_t extent = D;   // elements from the first row's first to the last row's last, so far
+  for (const Dim& x : d) {
+    if (x.n == 1) continue;
+    if (x.stride < 0 || (double)x.stride * (double)(x.n - 1) > kMaxElems) {
+      set_error("%s has a stride of %lld elements: not negative, and at most 2^40 elements in all", name,
+                (long long)x.stride);
+      return FA_ERR_INVALID_ARG;
+    }
+    if ((size_t)x.stride * es % 16 != 0) {
+      set_error("%s has a stride of %lld elements, not a multiple of 16 bytes", name, (long long)x.stride);
+      return FA_ERR_INVALID_ARG;
+    }
+    if (written && x.stride < extent) { set_error("rows of output %s overlap", name); return FA_ERR_INVALID_ARG; }
+    extent += x.stride * (x.n - 1);
+  }
+  out.p = v->ptr;
+  out.n = (size_t)extent * es;
+  return FA_OK;
+}
+
 fa_status check_ws(void* ws, size_t ws_bytes, size_t need, const Span* bufs, int n) {
   if (ws_bytes < need) { set_error("workspace %zu bytes < %zu needed", ws_bytes, need); return FA_ERR_WORKSPACE; }
   if (need == 0) return FA_OK;
@@ -141,6 +166,8 @@ fa_status cuda_status(cudaError_t e, const char* what) {
   set_error("%s: %s", what, cudaGetErrorString(e));
   return FA_ERR_CUDA;
 }
+
+namespace {
 
 // The tcgen05 path takes bf16 inputs; fp32 inputs stay on the SIMT fp32 path.
 bool use_tc_fwd(const Shape& s) { return s.dtype == DT_BF16 && tc_fwd_supported(s); }
@@ -192,7 +219,7 @@ FwdPlan plan_fwd(const Shape& s) {
     off = align_up(off + p.tilemap_bytes);
   }
   if (p.tensor_core && s.kv_format != FA_KV_DTYPE) {
-    // the q8_0 or f16 cache as bf16 K then V (read by every query tile of the forward)
+    // the q8_0, q4_0 or f16 cache as bf16 K then V (read by every query tile of the forward)
     p.kvbf_off = off;
     p.kvbf_bytes = 2 * (size_t)s.B * s.Hkv * s.Sk * s.D * 2;
     off = align_up(off + p.kvbf_bytes);
@@ -243,7 +270,7 @@ BwdPlan plan_bwd(const Shape& s) {
       p.cnt_bytes = (size_t)s.B * s.Hkv * split.n_slots * 2 * 4;
       off = align_up(off + p.cnt_bytes);
     }
-    if (s.kv_format == FA_KV_F16) {
+    if (s.kv_format == FA_KV_F16 || s.kv_format == FA_KV_Q4_0) {
       p.kvbf_off = off;
       p.kvbf_bytes = 2 * (size_t)s.B * s.Hkv * s.Sk * s.D * 2;
       off = align_up(off + p.kvbf_bytes);
@@ -271,32 +298,42 @@ size_t fa_train_bwd_workspace_size(const fa_params* p) {
   return plan_bwd(s).total;
 }
 
-// The K/V inputs of a call: tensors in the params' dtype or fp16, or a q8_0 cache (value and scale planes).
+// The K/V inputs of a call: tensors in the params' dtype or fp16, or a q8_0 or q4_0 cache (value and
+// scale planes).
 struct KvIn {
   const void* k;
   const void* v;
   const fa_kv_q8* q8;
+  const fa_kv_q4* q4 = nullptr;
 };
 
-// Appends the K/V input spans to `in` (2 for tensors, 4 for a q8_0 cache).
+// Appends the K/V input spans to `in` (2 for tensors, 4 for a quantized cache).
 static fa_status kv_spans(const Shape& s, const KvIn& kv, Span* in, int& n) {
-  const bool q8 = s.kv_format == FA_KV_Q8_0;
+  const bool q8 = s.kv_format == FA_KV_Q8_0, q4 = s.kv_format == FA_KV_Q4_0;
   if ((kv.q8 != nullptr) != q8) {
     set_error(q8 ? "kv_format is FA_KV_Q8_0: use the _q8 entry points" : "the _q8 entry points need kv_format FA_KV_Q8_0");
     return FA_ERR_INVALID_ARG;
   }
-  if (kv.q8 == nullptr) {
+  if ((kv.q4 != nullptr) != q4) {
+    set_error(q4 ? "kv_format is FA_KV_Q4_0: use the _q4 entry points" : "the _q4 entry points need kv_format FA_KV_Q4_0");
+    return FA_ERR_INVALID_ARG;
+  }
+  if (!q8 && !q4) {
     const size_t es = s.kv_format == FA_KV_F16 ? 2 : elem_size(s);
     in[n++] = {kv.k, kv_bytes(s, es), "k"};
     in[n++] = {kv.v, kv_bytes(s, es), "v"};
     return FA_OK;
   }
-  if (s.dtype != DT_BF16) { set_error("a q8_0 K/V cache needs bf16 queries (dtype=%d)", s.dtype); return FA_ERR_UNSUPPORTED; }
+  if (s.dtype != DT_BF16) {
+    set_error("a %s K/V cache needs bf16 queries (dtype=%d)", q8 ? "q8_0" : "q4_0", s.dtype);
+    return FA_ERR_UNSUPPORTED;
+  }
   const size_t scales = (size_t)s.B * s.Hkv * s.Sk * (s.D / 32) * 2;
-  in[n++] = {kv.q8->k_q, kv_bytes(s, 1), "k_q"};
-  in[n++] = {kv.q8->k_d, scales, "k_d"};
-  in[n++] = {kv.q8->v_q, kv_bytes(s, 1), "v_q"};
-  in[n++] = {kv.q8->v_d, scales, "v_d"};
+  const size_t values = q8 ? kv_bytes(s, 1) : kv_bytes(s, 1) / 2;
+  in[n++] = {q8 ? (const void*)kv.q8->k_q : kv.q4->k_q, values, "k_q"};
+  in[n++] = {q8 ? kv.q8->k_d : kv.q4->k_d, scales, "k_d"};
+  in[n++] = {q8 ? (const void*)kv.q8->v_q : kv.q4->v_q, values, "v_q"};
+  in[n++] = {q8 ? kv.q8->v_d : kv.q4->v_d, scales, "v_d"};
   return FA_OK;
 }
 
@@ -309,6 +346,24 @@ static fa_status cast_f16_cache(const Shape& s, const KvIn& kv, char* dst, cudaS
   cudaError_t e = launch_f16_to_bf16(kv.k, dst, n, st);
   if (e == cudaSuccess) e = launch_f16_to_bf16(kv.v, vdst, n, st);
   if (e != cudaSuccess) return cuda_status(e, "f16 cache cast launch");
+  k = dst;
+  v = vdst;
+  return FA_OK;
+}
+
+// A q4_0 cache expanded to bf16 K then V at `dst`, in the call's layout, likewise.
+static fa_status expand_q4_cache(const Shape& s, const fa_kv_q4& kv, char* dst, cudaStream_t st, const void*& k,
+                                 const void*& v) {
+  char* vdst = dst + kv_bytes(s, 2);
+  CacheView c{s.B, s.Hkv, s.Sk, s.D, true, const_cast<uint8_t*>(kv.k_q), const_cast<uint16_t*>(kv.k_d),
+              const_cast<uint8_t*>(kv.v_q), const_cast<uint16_t*>(kv.v_d)};
+  const RowView base = s.layout ? RowView{nullptr, (long long)s.Sk * s.Hkv * s.D, (long long)s.Hkv * s.D, s.D}
+                                : RowView{nullptr, (long long)s.Hkv * s.Sk * s.D, s.D, (long long)s.Sk * s.D};
+  RowView kd = base, vd = base;
+  kd.ptr = dst;
+  vd.ptr = vdst;
+  cudaError_t e = launch_cache_read(c, 0, s.Sk, DT_BF16, kd, vd, st);
+  if (e != cudaSuccess) return cuda_status(e, "q4_0 cache expansion launch");
   k = dst;
   v = vdst;
   return FA_OK;
@@ -341,6 +396,8 @@ static fa_status fwd_common(const fa_params* p, const void* q, const KvIn& kv, c
   cudaError_t e = cudaSuccess;
   if (s.kv_format == FA_KV_F16 && (st = cast_f16_cache(s, kv, (char*)ws + plan.kvbf_off, a.stream, a.k, a.v)) != FA_OK)
     return st;
+  if (kv.q4 != nullptr && (st = expand_q4_cache(s, *kv.q4, (char*)ws + plan.kvbf_off, a.stream, a.k, a.v)) != FA_OK)
+    return st;
   if (kv.q8 != nullptr) {
     // every query tile reads every key tile: dequantize the cache once, then run the bf16 kernel on it
     char* kbf = (char*)ws + plan.kvbf_off;
@@ -365,6 +422,12 @@ fa_status fa_train_fwd_q8(const fa_params* p, const void* q, const fa_kv_q8* kv,
                           float* lse, void* ws, size_t ws_bytes, void* stream) {
   if (kv == nullptr) { g_last_error[0] = '\0'; set_error("kv is NULL"); return FA_ERR_INVALID_ARG; }
   return fwd_common(p, q, KvIn{nullptr, nullptr, kv}, mask, o, lse, ws, ws_bytes, stream);
+}
+
+fa_status fa_train_fwd_q4(const fa_params* p, const void* q, const fa_kv_q4* kv, const void* mask, void* o,
+                          float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (kv == nullptr) { g_last_error[0] = '\0'; set_error("kv is NULL"); return FA_ERR_INVALID_ARG; }
+  return fwd_common(p, q, KvIn{nullptr, nullptr, nullptr, kv}, mask, o, lse, ws, ws_bytes, stream);
 }
 
 // Rows of the accumulator written back out by the fused SET_ROWS backward (n_rows == 0: none).
@@ -427,6 +490,8 @@ static fa_status bwd_common(const fa_params* p, const void* q, const KvIn& kv, c
   BwdArgs a{s, q, kv.k, kv.v, mask, o, lse, dO, dq, dk, dv, accum, cs};
   if (s.kv_format == FA_KV_F16 && (st = cast_f16_cache(s, kv, (char*)ws + plan.kvbf_off, cs, a.k, a.v)) != FA_OK)
     return st;
+  if (kv.q4 != nullptr && (st = expand_q4_cache(s, *kv.q4, (char*)ws + plan.kvbf_off, cs, a.k, a.v)) != FA_OK)
+    return st;
   if (kv.q8 != nullptr) {
     a.kq = kv.q8->k_q;
     a.kd = kv.q8->k_d;
@@ -467,6 +532,22 @@ fa_status fa_train_bwd_accum_q8(const fa_params* p, const void* q, const fa_kv_q
   if (kv == nullptr) { g_last_error[0] = '\0'; set_error("kv is NULL"); return FA_ERR_INVALID_ARG; }
   return bwd_common(p, q, KvIn{nullptr, nullptr, kv}, mask, o, lse, dO, dq, dk_acc, dv_acc, true, ws, ws_bytes,
                     stream);
+}
+
+fa_status fa_train_bwd_q4(const fa_params* p, const void* q, const fa_kv_q4* kv, const void* mask, const void* o,
+                          const float* lse, const void* dO, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (kv == nullptr) { g_last_error[0] = '\0'; set_error("kv is NULL"); return FA_ERR_INVALID_ARG; }
+  return bwd_common(p, q, KvIn{nullptr, nullptr, nullptr, kv}, mask, o, lse, dO, dq, dk, dv, false, ws, ws_bytes,
+                    stream);
+}
+
+fa_status fa_train_bwd_accum_q4(const fa_params* p, const void* q, const fa_kv_q4* kv, const void* mask,
+                                const void* o, const float* lse, const void* dO, void* dq, float* dk_acc,
+                                float* dv_acc, void* ws, size_t ws_bytes, void* stream) {
+  if (kv == nullptr) { g_last_error[0] = '\0'; set_error("kv is NULL"); return FA_ERR_INVALID_ARG; }
+  return bwd_common(p, q, KvIn{nullptr, nullptr, nullptr, kv}, mask, o, lse, dO, dq, dk_acc, dv_acc, true, ws,
+                    ws_bytes, stream);
 }
 
 fa_status fa_train_bwd_accum_rows(const fa_params* p, const void* q, const void* k, const void* v, const void* mask,

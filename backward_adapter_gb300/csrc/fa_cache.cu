@@ -1,0 +1,260 @@
+// Writing and reading back a quantized K/V cache (fa_cache_write, fa_cache_read): the chunk's K and
+// V go into the cached window that the attention entry points read in place (llama.cpp PR #57,
+// commit 2394a4c). Both passes touch every byte once and are bound by HBM, or by their launch when
+// a few rows are written.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "fa_check.h"
+#include "fa_device.cuh"
+#include "kv_quant.cuh"
+
+namespace fa {
+namespace {
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]),
+                                            tc::pack_bf16x2(x[4], x[5]), tc::pack_bf16x2(x[6], x[7]));
+}
+
+// A thread quantizes 8 features of one row, four lanes a block of 32. blockIdx.y: 0 for K, 1 for V.
+template <typename T, int D, bool Q4>
+__global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k, RowView v, int n_rows,
+                                                          const int64_t* __restrict__ begin, long long begin_all,
+                                                          const int64_t* __restrict__ count, unsigned* status) {
+  constexpr int LANES = D / 8;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long g = i / LANES;
+  const int l = (int)(i % LANES);
+  const RowView src = blockIdx.y ? v : k;
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  bool on = false;
+  size_t row = 0;
+  if (g < (long long)c.B * c.Hkv * n_rows) {
+    const int r = (int)(g % n_rows), bh = (int)(g / n_rows), h = bh % c.Hkv, b = bh / c.Hkv;
+    const long long first = begin != nullptr ? __ldg(begin + b) : begin_all;
+    if (count == nullptr || r < __ldg(count + b)) {
+      if (first < c.S && first + r >= 0 && first + r < c.S) {
+        on = true;
+        row = (size_t)bh * c.S + (size_t)(first + r);
+        load8(static_cast<const T*>(src.ptr) + b * src.sb + r * src.ss + h * src.sh + 8 * l, x);
+      } else if (l == 0 && status != nullptr) {
+        atomicCAS(status, 0u, 0x40000000u | kSiteCacheRow);
+      }
+    }
+  }
+  uint32_t lo, hi;
+  const __half d = quantize_block<Q4>(x, lo, hi);
+  if constexpr (Q4) {
+    // lanes 2 and 3 hold features 16 .. 31, whose four bits sit above those of features 0 .. 15
+    lo |= __shfl_down_sync(0xffffffffu, lo, 2) << 4;
+    hi |= __shfl_down_sync(0xffffffffu, hi, 2) << 4;
+  }
+  if (!on) return;
+  const int blk = l / 4, part = l % 4;
+  uint8_t* values = static_cast<uint8_t*>(blockIdx.y ? c.v_q : c.k_q);
+  if (!Q4 || part < 2)
+    *reinterpret_cast<uint2*>(values + row * (Q4 ? D / 2 : D) + (Q4 ? 16 * blk + 8 * part : 8 * l)) = make_uint2(lo, hi);
+  if (part == 0) (blockIdx.y ? c.v_d : c.k_d)[row * (D / 32) + blk] = __half_as_ushort(d);
+}
+
+// A thread reads 16 features of one row: half a block's bytes. blockIdx.y: 0 for K, 1 for V.
+template <typename T, int D, bool Q4>
+__global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long begin, int n_rows, RowView k, RowView v) {
+  constexpr int PARTS = D / 16;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long g = i / PARTS;
+  const int part = (int)(i % PARTS);
+  if (g >= (long long)c.B * c.Hkv * n_rows) return;
+  const int r = (int)(g % n_rows), bh = (int)(g / n_rows), h = bh % c.Hkv, b = bh / c.Hkv;
+  const RowView dst = blockIdx.y ? v : k;
+  const size_t row = (size_t)bh * c.S + (size_t)(begin + r);
+  const uint8_t* values = static_cast<const uint8_t*>(blockIdx.y ? c.v_q : c.k_q);
+  const float d = __half2float(__ushort_as_half(__ldg((blockIdx.y ? c.v_d : c.k_d) + row * (D / 32) + part / 2)));
+  T* out = static_cast<T*>(dst.ptr) + b * dst.sb + r * dst.ss + h * dst.sh;
+  float x[8], y[8];
+  if constexpr (Q4) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(values + row * (D / 2) + 8 * part));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = q4_low(j < 4 ? w.x : w.y, j % 4) * d;
+      y[j] = q4_high(j < 4 ? w.x : w.y, j % 4) * d;
+    }
+    out += part / 2 * 32 + part % 2 * 8;
+    store8(out, x);
+    store8(out + 16, y);
+  } else {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(values + row * D + 16 * part));
+    const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = s8_to_f32(u[j / 4], j % 4) * d;
+      y[j] = s8_to_f32(u[2 + j / 4], j % 4) * d;
+    }
+    out += 16 * part;
+    store8(out, x);
+    store8(out + 8, y);
+  }
+}
+
+// Blocks of 256 threads over `per_row` threads for each row; 0 when there are too many for a grid.
+unsigned blocks_for(long long rows, int per_row) {
+  const long long n = (rows * per_row + 255) / 256;
+  return n > 0x7fffffffLL ? 0u : (unsigned)n;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowView& v, int dtype, int n_rows,
+                               const int64_t* begin, long long begin_all, const int64_t* count, unsigned* status,
+                               cudaStream_t st) {
+  const unsigned n = blocks_for((long long)c.B * c.Hkv * n_rows, c.D / 8);
+  if (n == 0) return cudaErrorInvalidConfiguration;
+  auto go = [&](auto kernel) { kernel<<<dim3(n, 2), 256, 0, st>>>(c, k, v, n_rows, begin, begin_all, count, status); };
+  auto by_format = [&](auto t, auto dim) {
+    using T = decltype(t);
+    constexpr int D = decltype(dim)::value;
+    if (c.q4) go(cache_write_kernel<T, D, true>);
+    else go(cache_write_kernel<T, D, false>);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dtype == DT_BF16) c.D == 64 ? by_format(__nv_bfloat16{}, D64{}) : by_format(__nv_bfloat16{}, D128{});
+  else c.D == 64 ? by_format(float{}, D64{}) : by_format(float{}, D128{});
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, int dtype, const RowView& k,
+                              const RowView& v, cudaStream_t st) {
+  const unsigned n = blocks_for((long long)c.B * c.Hkv * n_rows, c.D / 16);
+  if (n == 0) return cudaErrorInvalidConfiguration;
+  auto go = [&](auto kernel) { kernel<<<dim3(n, 2), 256, 0, st>>>(c, begin, n_rows, k, v); };
+  auto by_format = [&](auto t, auto dim) {
+    using T = decltype(t);
+    constexpr int D = decltype(dim)::value;
+    if (c.q4) go(cache_read_kernel<T, D, true>);
+    else go(cache_read_kernel<T, D, false>);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dtype == DT_BF16) c.D == 64 ? by_format(__nv_bfloat16{}, D64{}) : by_format(__nv_bfloat16{}, D128{});
+  else c.D == 64 ? by_format(float{}, D64{}) : by_format(float{}, D128{});
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+fa_status check_cache(const fa_cache* c, CacheView& out) {
+  if (c == nullptr) { set_error("cache is NULL"); return FA_ERR_INVALID_ARG; }
+  if (c->B < 1 || c->B > 65535 || c->Hkv < 1 || c->Hkv > 65535) {
+    set_error("cache B=%d, Hkv=%d: each in [1, 65535]", c->B, c->Hkv); return FA_ERR_INVALID_ARG;
+  }
+  if (c->S < 1 || c->S > kMaxSeq) { set_error("cache S=%d outside [1, %d]", c->S, kMaxSeq); return FA_ERR_INVALID_ARG; }
+  if (c->D <= 0) { set_error("D=%d must be positive", c->D); return FA_ERR_INVALID_ARG; }
+  if (c->D != 64 && c->D != 128) { set_error("D=%d unsupported (64 or 128)", c->D); return FA_ERR_UNSUPPORTED; }
+  if (c->kv_format != FA_KV_Q8_0 && c->kv_format != FA_KV_Q4_0) {
+    set_error("cache kv_format=%d: FA_KV_Q8_0 or FA_KV_Q4_0", c->kv_format); return FA_ERR_INVALID_ARG;
+  }
+  if (c->reserved != 0) { set_error("reserved field must be 0"); return FA_ERR_INVALID_ARG; }
+  if (too_large(c->B, c->Hkv, c->S, c->D)) {
+    set_error("a cache of these shapes would hold more than 2^40 elements"); return FA_ERR_INVALID_ARG;
+  }
+  out = CacheView{c->B, c->Hkv, c->S, c->D, c->kv_format == FA_KV_Q4_0, c->k_q, c->k_d, c->v_q, c->v_d};
+  return FA_OK;
+}
+
+void cache_spans(const CacheView& c, Span out[4]) {
+  const size_t n = (size_t)c.B * c.Hkv * c.S * c.D;
+  out[0] = {c.k_q, c.q4 ? n / 2 : n, "k_q"};
+  out[1] = {c.k_d, n / 16, "k_d"};   // one fp16 for 32 features
+  out[2] = {c.v_q, c.q4 ? n / 2 : n, "v_q"};
+  out[3] = {c.v_d, n / 16, "v_d"};
+}
+
+namespace {
+
+fa_status check_rows(const CacheView& c, const fa_view* k, const fa_view* v, int dtype, int n_rows, bool written,
+                     Span out[2]) {
+  if (dtype != FA_F32 && dtype != FA_BF16) { set_error("dtype=%d invalid", dtype); return FA_ERR_INVALID_ARG; }
+  if (n_rows < 0 || n_rows > kMaxSeq) { set_error("n_rows=%d outside [0, %d]", n_rows, kMaxSeq); return FA_ERR_INVALID_ARG; }
+  if (too_large(c.B, c.Hkv, n_rows, c.D)) {
+    set_error("K or V would hold more than 2^40 elements"); return FA_ERR_INVALID_ARG;
+  }
+  const size_t es = dtype == FA_BF16 ? 2 : 4;
+  fa_status st = check_view(k, c.B, n_rows, c.Hkv, c.D, es, written, "k", out[0]);
+  return st != FA_OK ? st : check_view(v, c.B, n_rows, c.Hkv, c.D, es, written, "v", out[1]);
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_cache_write(const fa_cache* c, const fa_view* k, const fa_view* v, int32_t dtype, int32_t n_rows,
+                         const int64_t* begin, int64_t begin_all, const int64_t* count, void* stream) {
+  clear_error();
+  CacheView cv;
+  fa_status st = check_cache(c, cv);
+  if (st != FA_OK) return st;
+  Span in[4], out[4];
+  if ((st = check_rows(cv, k, v, dtype, n_rows, false, in)) != FA_OK) return st;
+  if (begin == nullptr && (begin_all < 0 || begin_all > cv.S - n_rows)) {
+    set_error("rows [%lld, +%d) outside the %d keys", (long long)begin_all, n_rows, cv.S); return FA_ERR_INVALID_ARG;
+  }
+  if ((uintptr_t)begin % 8 != 0 || (uintptr_t)count % 8 != 0) {
+    set_error("begin and count must be 8-byte aligned"); return FA_ERR_INVALID_ARG;
+  }
+  if (n_rows == 0) return FA_OK;
+  cache_spans(cv, out);
+  if ((st = check_buffers(in, 2, out, 4)) != FA_OK) return st;
+  in[2] = {begin, (size_t)cv.B * 8, "begin"};
+  in[3] = {count, (size_t)cv.B * 8, "count"};
+  for (int o = 0; o < 4; ++o)
+    for (int i = 2; i < 4; ++i)
+      if (overlaps(out[o], in[i])) { set_error("output %s overlaps input %s", out[o].name, in[i].name); return FA_ERR_INVALID_ARG; }
+  return cuda_status(launch_cache_write(cv, row_view(k), row_view(v), dtype, n_rows, begin, begin_all, count,
+                                        device_status_ptr(), (cudaStream_t)stream),
+                     "cache write launch");
+}
+
+fa_status fa_cache_read(const fa_cache* c, int64_t begin, int32_t n_rows, int32_t dtype, const fa_view* k,
+                        const fa_view* v, void* stream) {
+  clear_error();
+  CacheView cv;
+  fa_status st = check_cache(c, cv);
+  if (st != FA_OK) return st;
+  Span in[4], out[2];
+  if ((st = check_rows(cv, k, v, dtype, n_rows, true, out)) != FA_OK) return st;
+  if (begin < 0 || begin > cv.S - n_rows) {
+    set_error("rows [%lld, +%d) outside the %d keys", (long long)begin, n_rows, cv.S); return FA_ERR_INVALID_ARG;
+  }
+  if (n_rows == 0) return FA_OK;
+  cache_spans(cv, in);
+  if ((st = check_buffers(in, 4, out, 2)) != FA_OK) return st;
+  return cuda_status(launch_cache_read(cv, begin, n_rows, dtype, row_view(k), row_view(v), (cudaStream_t)stream),
+                     "cache read launch");
+}
+
+}  // extern "C"

@@ -82,7 +82,7 @@ struct FwdPlan {
   size_t tilemap_off, tilemap_bytes;
   size_t part_o_off, part_o_bytes;     // fp32 [splits, B, Hq, Sq, D]
   size_t part_ml_off, part_ml_bytes;   // fp32 [splits, B, Hq, Sq, 2]
-  size_t kvbf_off, kvbf_bytes;         // q8_0 or f16 cache: bf16 K then V (q8_0: [B, Hkv, Sk, D]; f16: the layout)
+  size_t kvbf_off, kvbf_bytes;         // q8_0, q4_0 or f16 cache: bf16 K then V (q8_0: [B, Hkv, Sk, D]; else the layout)
   size_t total;
 };
 
@@ -94,7 +94,7 @@ struct BwdPlan {
   size_t turn_off, turn_bytes;   // deterministic: int32 [groups, B, Hq, ceil(Sq / 128)] dQ turn counters
   size_t part_off, part_bytes;   // split key tiles: fp32 dV/dK partials [B * Hkv, slots, 2, D / 4, 128] float4
   size_t cnt_off, cnt_bytes;     // split key tiles: int32 [B * Hkv, slots, 2] part tickets / partials written
-  size_t kvbf_off, kvbf_bytes;   // f16 cache: bf16 K then V, in the call's layout
+  size_t kvbf_off, kvbf_bytes;   // f16 or q4_0 cache: bf16 K then V, in the call's layout
   size_t total;
 };
 
@@ -176,6 +176,31 @@ cudaError_t launch_mask_classify(const Shape& s, const void* mask, uint8_t* tile
 cudaError_t launch_q8_dequant(const Shape& s, const int8_t* xq, const void* xd, void* out, cudaStream_t st);
 // fp16 -> bf16, n elements (a multiple of 8; 16-byte aligned buffers), rounded to nearest even.
 cudaError_t launch_f16_to_bf16(const void* x, void* out, long long n, cudaStream_t st);
+
+// Rows of a strided tensor (fa_view): (b, s, h) starts at ptr + b * sb + s * ss + h * sh elements.
+struct RowView {
+  void* ptr;
+  long long sb, ss, sh;
+};
+
+// A quantized cache (fa_cache): the planes of q8_0, or of q4_0 when q4.
+struct CacheView {
+  int B, Hkv, S, D;
+  bool q4;
+  void* k_q;
+  uint16_t* k_d;
+  void* v_q;
+  uint16_t* v_d;
+};
+constexpr unsigned kSiteCacheRow = 951;
+constexpr unsigned kSiteDecodeLength = 952;
+// fa_cache_write: begin (device) or begin_all when NULL; count (device) or n_rows when NULL.
+cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowView& v, int dtype, int n_rows,
+                               const int64_t* begin, long long begin_all, const int64_t* count, unsigned* status,
+                               cudaStream_t st);
+// fa_cache_read: keys [begin, begin + n_rows) of every head as values in dtype.
+cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, int dtype, const RowView& k,
+                              const RowView& v, cudaStream_t st);
 
 // SET_ROWS backward gather (fa_set_rows_backward): out[bh, r, :] = acc[bh, idx[r], :].
 constexpr unsigned kSiteRowIndex = 950;

@@ -20,14 +20,16 @@ LIB_PATH = os.path.join(_PKG, "libfa_train.so")
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE, FA_ERR_CUDA = range(5)
 FA_F32, FA_BF16 = 0, 1
 FA_MASK_NONE, FA_MASK_ADD_F32, FA_MASK_BOOL_U8 = 0, 1, 2
-FA_KV_DTYPE, FA_KV_Q8_0, FA_KV_F16 = 0, 1, 2
+FA_KV_DTYPE, FA_KV_Q8_0, FA_KV_F16, FA_KV_Q4_0 = 0, 1, 2, 4
 FA_LAYOUT_BHSD, FA_LAYOUT_BSHD = 0, 1
 
 EXPORTED = ("fa_train_fwd_workspace_size", "fa_train_bwd_workspace_size", "fa_train_fwd", "fa_train_bwd",
             "fa_train_bwd_accum", "fa_status_str", "fa_last_error", "fa_profile_set_events",
             "fa_profile_launch_count", "fa_device_status", "fa_train_bwd_noalloc", "fa_train_selftest_wait",
             "fa_set_rows_backward", "fa_train_bwd_accum_rows", "fa_train_fwd_q8", "fa_train_bwd_q8",
-            "fa_train_bwd_accum_q8", "fa_train_bwd_plan", "fa_train_fwd_plan")
+            "fa_train_bwd_accum_q8", "fa_train_bwd_plan", "fa_train_fwd_plan", "fa_train_fwd_q4", "fa_train_bwd_q4",
+            "fa_train_bwd_accum_q4", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
+            "fa_cache_write", "fa_cache_read", "fa_decode", "fa_decode_workspace_size")
 FA_KERNEL_FWD, FA_KERNEL_BWD_MAIN, FA_KERNEL_BWD_DSUM, FA_KERNEL_BWD_DQ_CONVERT, FA_KERNEL_MASK_CLASSIFY = range(5)
 
 
@@ -44,6 +46,34 @@ class FaKvQ8(ctypes.Structure):
     """fa_kv_q8: device pointers of a q8_0 K/V cache (int8 values, fp16 scales per 32 features)."""
     _fields_ = [("k_q", ctypes.c_void_p), ("k_d", ctypes.c_void_p), ("v_q", ctypes.c_void_p),
                 ("v_d", ctypes.c_void_p)]
+
+
+class FaKvQ4(ctypes.Structure):
+    """fa_kv_q4: device pointers of a q4_0 K/V cache (two values a byte, fp16 scales per 32 features)."""
+    _fields_ = FaKvQ8._fields_
+
+
+class FaView(ctypes.Structure):
+    """fa_view: rows of a strided tensor, strides in elements."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class FaRopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "S", "Hq", "Hkv", "D", "dtype", "w_dtype", "rot", "interleaved",
+                                              "norm")] + \
+               [("eps", ctypes.c_float), ("factor", ctypes.c_float), ("offset", ctypes.c_int64),
+                ("pos_stride_b", ctypes.c_int64), ("reserved", ctypes.c_int32)]
+
+
+class FaCache(ctypes.Structure):
+    """fa_cache: the shape, format and device pointers of a quantized K/V cache."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hkv", "S", "D", "kv_format", "reserved")] + FaKvQ8._fields_
+
+
+class FaDecodeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("Hq", "Sq", "window", "layout")] + \
+               [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class FaError(RuntimeError):
@@ -101,6 +131,28 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_train_bwd_q8.restype = st
     lib.fa_train_bwd_accum_q8.argtypes = [P, vp, KV, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fa_train_bwd_accum_q8.restype = st
+    K4 = ctypes.POINTER(FaKvQ4)
+    lib.fa_train_fwd_q4.argtypes = [P, vp, K4, vp, vp, vp, vp, sz, vp]
+    lib.fa_train_fwd_q4.restype = st
+    lib.fa_train_bwd_q4.argtypes = [P, vp, K4, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fa_train_bwd_q4.restype = st
+    lib.fa_train_bwd_accum_q4.argtypes = [P, vp, K4, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fa_train_bwd_accum_q4.restype = st
+    V, R, C, DP = (ctypes.POINTER(t) for t in (FaView, FaRopeParams, FaCache, FaDecodeParams))
+    lib.fa_qk_norm_rope.argtypes = [R, V, V, vp, vp, vp, vp, V, V, vp]
+    lib.fa_qk_norm_rope.restype = st
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [R]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd.argtypes = [R, V, V, V, V, vp, vp, vp, vp, V, V, vp, vp, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.restype = st
+    lib.fa_cache_write.argtypes = [C, V, V, i32, i32, vp, i64, vp, vp]
+    lib.fa_cache_write.restype = st
+    lib.fa_cache_read.argtypes = [C, i64, i32, i32, V, V, vp]
+    lib.fa_cache_read.restype = st
+    lib.fa_decode_workspace_size.argtypes = [DP, C]
+    lib.fa_decode_workspace_size.restype = sz
+    lib.fa_decode.argtypes = [DP, vp, C, vp, vp, vp, vp, sz, vp]
+    lib.fa_decode.restype = st
     lib.fa_train_bwd_plan.argtypes = [P, ctypes.POINTER(i32), i32, ctypes.POINTER(i32)]
     lib.fa_train_bwd_plan.restype = st
     lib.fa_train_fwd_plan.argtypes = [P, ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)]
@@ -235,6 +287,37 @@ def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> Optional[torc
     if ws is not None and ws.numel() * ws.element_size() >= nbytes:
         return ws
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
+    """As _workspace, for a call on a stream of its own too: memory taken here is not handed out again before
+    that stream is done with it."""
+    got = _workspace(nbytes, device, ws)
+    if stream is not None and got is not None and got is not ws:
+        s = _stream(device, stream)
+        if s != torch.cuda.current_stream(device).cuda_stream:
+            got.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(s, device))
+    return got
+
+
+def _view(t: torch.Tensor, layout: str) -> FaView:
+    """fa_view of a 4-D tensor in layout "bhsd" or "bshd", read or written where it is."""
+    b, x, y, d = t.stride()
+    if not t.is_cuda or (d != 1 and t.shape[3] > 1):
+        raise ValueError("every tensor must be a CUDA tensor whose features are contiguous")
+    return FaView(t.data_ptr(), b, y, x) if layout == "bhsd" else FaView(t.data_ptr(), b, x, y)
+
+
+def _launch(device: torch.device, call, *args) -> None:
+    """A call of the C ABI on `device`, as _on_device (which costs a few microseconds: skipped where
+    the device is current already)."""
+    if device.index == torch.cuda.current_device():
+        status = call(*args)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args)
+    if status != FA_OK:
+        _check(status)
 
 
 def _need_cuda(*ts):
@@ -385,8 +468,21 @@ def _kv_q8(k_q, k_d, v_q, v_d) -> FaKvQ8:
     return FaKvQ8(k_q.data_ptr(), k_d.data_ptr(), v_q.data_ptr(), v_d.data_ptr())
 
 
-def _cache_shape_view(k_q, layout):
+def _kv_q4(k_q, k_d, v_q, v_d) -> FaKvQ4:
+    if k_q.dtype != torch.uint8 or v_q.dtype != torch.uint8:
+        raise TypeError("k_q and v_q must be uint8 [B, Hkv, Sk, D / 2]")
+    if k_d.dtype != torch.float16 or v_d.dtype != torch.float16:
+        raise TypeError("k_d and v_d must be float16 [B, Hkv, Sk, D / 32]")
+    return FaKvQ4(k_q.data_ptr(), k_d.data_ptr(), v_q.data_ptr(), v_d.data_ptr())
+
+
+def _cache_shape_view(k_q, layout, q4: bool = False):
     """The cache planes are [B, Hkv, Sk, ...] whatever the layout of Q: a view for the shapes only."""
+    if q4:   # two features a byte
+        if k_q.dim() != 4:
+            raise ValueError(f"k_q must be 4-D (got {k_q.dim()}-D)")
+        B, Hkv, Sk, half = k_q.shape
+        k_q = torch.empty((B, Hkv, Sk, 2 * half), dtype=k_q.dtype, device="meta")
     return k_q if layout == "bhsd" else k_q.transpose(1, 2)
 
 
@@ -396,24 +492,71 @@ def _q8_expect(p: FaParams, k_q, k_d, v_q, v_d):
             "k_d": (k_d, scales, torch.float16), "v_d": (v_d, scales, torch.float16)}
 
 
-def fwd_q8(q, k_q, k_d, v_q, v_d, mask=None, *, scale=None, causal=False, q_offset=None, window=0, layout="bhsd",
-           out=None, lse=None, workspace=None, stream=None):
-    """Forward over a q8_0 K/V cache (int8 values k_q/v_q, fp16 scales k_d/v_d per 32 features)."""
+def _q4_expect(p: FaParams, k_q, k_d, v_q, v_d):
+    planes, scales = (p.B, p.Hkv, p.Sk, p.D // 2), (p.B, p.Hkv, p.Sk, p.D // 32)
+    return {"k_q": (k_q, planes, torch.uint8), "v_q": (v_q, planes, torch.uint8),
+            "k_d": (k_d, scales, torch.float16), "v_d": (v_d, scales, torch.float16)}
+
+
+def _fwd_cache(q4, q, k_q, k_d, v_q, v_d, mask, scale, causal, q_offset, window, layout, out, lse, workspace, stream):
     lib = load_library()
     mview, _, _ = _mask_view(mask)
-    kv = _kv_q8(k_q, k_d, v_q, v_d)
-    p = make_params(q, _cache_shape_view(k_q, layout), mask, scale=scale, causal=causal, q_offset=q_offset,
-                    window=window, kv_format=FA_KV_Q8_0, layout=layout)
+    kv = _kv_q4(k_q, k_d, v_q, v_d) if q4 else _kv_q8(k_q, k_d, v_q, v_d)
+    p = make_params(q, _cache_shape_view(k_q, layout, q4), mask, scale=scale, causal=causal, q_offset=q_offset,
+                    window=window, kv_format=FA_KV_Q4_0 if q4 else FA_KV_Q8_0, layout=layout)
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty((p.B, p.Hq, p.Sq), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check_tensors(q, **_common_expect(p, layout, q, mask=mask, o=out, lse=lse), **_q8_expect(p, k_q, k_d, v_q, v_d))
+    _check_tensors(q, **_common_expect(p, layout, q, mask=mask, o=out, lse=lse),
+                   **(_q4_expect if q4 else _q8_expect)(p, k_q, k_d, v_q, v_d))
     _need_cuda(q, mview, out, lse, k_q, k_d, v_q, v_d)
     ws_bytes = fwd_workspace_size(p)
     ws = _workspace(ws_bytes, q.device, workspace)
+    call = lib.fa_train_fwd_q4 if q4 else lib.fa_train_fwd_q8
     with _on_device(q):
-        _check(lib.fa_train_fwd_q8(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(out), _ptr(lse),
-                                   _ptr(ws), ws_bytes, _stream(q.device, stream)))
+        _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                    _stream(q.device, stream)))
     return out, lse
+
+
+def _bwd_cache(q4, q, k_q, k_d, v_q, v_d, o, lse, do, mask, scale, causal, q_offset, window, deterministic, layout, dq,
+               dk, dv, dk_acc, dv_acc, workspace, stream):
+    lib = load_library()
+    mview, _, _ = _mask_view(mask)
+    kv = _kv_q4(k_q, k_d, v_q, v_d) if q4 else _kv_q8(k_q, k_d, v_q, v_d)
+    shape = tuple(_cache_shape_view(k_q, layout, q4).shape)   # dK / dV in the call's layout
+    p = make_params(q, _cache_shape_view(k_q, layout, q4), mask, scale=scale, causal=causal, q_offset=q_offset,
+                    window=window, deterministic=deterministic, kv_format=FA_KV_Q4_0 if q4 else FA_KV_Q8_0,
+                    layout=layout)
+    dq = torch.empty_like(q) if dq is None else dq
+    if (dk_acc is None) != (dv_acc is None):
+        raise ValueError("give both dk_acc and dv_acc, or neither")
+    ks = _kv_shape(p, layout)
+    _check_tensors(q, **_common_expect(p, layout, q, mask=mask, o=o, lse=lse, do=do, dq=dq),
+                   **(_q4_expect if q4 else _q8_expect)(p, k_q, k_d, v_q, v_d), dk_acc=(dk_acc, ks, torch.float32),
+                   dv_acc=(dv_acc, ks, torch.float32), dk=(dk, ks, q.dtype), dv=(dv, ks, q.dtype))
+    _need_cuda(q, o, lse, do, mview, dq, dk_acc, dv_acc, dk, dv, k_q, k_d, v_q, v_d)
+    ws_bytes = bwd_workspace_size(p)
+    ws = _workspace(ws_bytes, q.device, workspace)
+    if dk_acc is not None:
+        call = lib.fa_train_bwd_accum_q4 if q4 else lib.fa_train_bwd_accum_q8
+        with _on_device(q):
+            _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
+                        _ptr(dk_acc), _ptr(dv_acc), _ptr(ws), ws_bytes, _stream(q.device, stream)))
+        return dq
+    dk = torch.empty(shape, dtype=q.dtype, device=q.device) if dk is None else dk
+    dv = torch.empty(shape, dtype=q.dtype, device=q.device) if dv is None else dv
+    call = lib.fa_train_bwd_q4 if q4 else lib.fa_train_bwd_q8
+    with _on_device(q):
+        _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
+                    _ptr(dk), _ptr(dv), _ptr(ws), ws_bytes, _stream(q.device, stream)))
+    return dq, dk, dv
+
+
+def fwd_q8(q, k_q, k_d, v_q, v_d, mask=None, *, scale=None, causal=False, q_offset=None, window=0, layout="bhsd",
+           out=None, lse=None, workspace=None, stream=None):
+    """Forward over a q8_0 K/V cache (int8 values k_q/v_q, fp16 scales k_d/v_d per 32 features)."""
+    return _fwd_cache(False, q, k_q, k_d, v_q, v_d, mask, scale, causal, q_offset, window, layout, out, lse, workspace,
+                      stream)
 
 
 def bwd_q8(q, k_q, k_d, v_q, v_d, o, lse, do, mask=None, *, scale=None, causal=False, q_offset=None, window=0,
@@ -421,34 +564,23 @@ def bwd_q8(q, k_q, k_d, v_q, v_d, o, lse, do, mask=None, *, scale=None, causal=F
            stream=None):
     """Backward over a q8_0 K/V cache. With dk_acc/dv_acc (fp32) the gradients of the dequantized
     K/V are added into them (returns dQ); otherwise returns (dQ, dK, dV) in q's dtype."""
-    lib = load_library()
-    mview, _, _ = _mask_view(mask)
-    kv = _kv_q8(k_q, k_d, v_q, v_d)
-    p = make_params(q, _cache_shape_view(k_q, layout), mask, scale=scale, causal=causal, q_offset=q_offset,
-                    window=window, deterministic=deterministic, kv_format=FA_KV_Q8_0, layout=layout)
-    dq = torch.empty_like(q) if dq is None else dq
-    if (dk_acc is None) != (dv_acc is None):
-        raise ValueError("give both dk_acc and dv_acc, or neither")
-    ks = _kv_shape(p, layout)
-    _check_tensors(q, **_common_expect(p, layout, q, mask=mask, o=o, lse=lse, do=do, dq=dq),
-                   **_q8_expect(p, k_q, k_d, v_q, v_d), dk_acc=(dk_acc, ks, torch.float32),
-                   dv_acc=(dv_acc, ks, torch.float32), dk=(dk, ks, q.dtype), dv=(dv, ks, q.dtype))
-    _need_cuda(q, o, lse, do, mview, dq, dk_acc, dv_acc, dk, dv, k_q, k_d, v_q, v_d)
-    ws_bytes = bwd_workspace_size(p)
-    ws = _workspace(ws_bytes, q.device, workspace)
-    if dk_acc is not None:
-        with _on_device(q):
-            _check(lib.fa_train_bwd_accum_q8(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse),
-                                             _ptr(do), _ptr(dq), _ptr(dk_acc), _ptr(dv_acc), _ptr(ws), ws_bytes,
-                                             _stream(q.device, stream)))
-        return dq
-    shape = tuple(_cache_shape_view(k_q, layout).shape)   # dK / dV in the call's layout
-    dk = torch.empty(shape, dtype=q.dtype, device=q.device) if dk is None else dk
-    dv = torch.empty(shape, dtype=q.dtype, device=q.device) if dv is None else dv
-    with _on_device(q):
-        _check(lib.fa_train_bwd_q8(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse),
-                                   _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws_bytes, _stream(q.device, stream)))
-    return dq, dk, dv
+    return _bwd_cache(False, q, k_q, k_d, v_q, v_d, o, lse, do, mask, scale, causal, q_offset, window, deterministic,
+                      layout, dq, dk, dv, dk_acc, dv_acc, workspace, stream)
+
+
+def fwd_q4(q, k_q, k_d, v_q, v_d, mask=None, *, scale=None, causal=False, q_offset=None, window=0, layout="bhsd",
+           out=None, lse=None, workspace=None, stream=None):
+    """Forward over a q4_0 K/V cache (uint8 k_q/v_q [B, Hkv, Sk, D / 2], fp16 scales k_d/v_d per 32 features)."""
+    return _fwd_cache(True, q, k_q, k_d, v_q, v_d, mask, scale, causal, q_offset, window, layout, out, lse, workspace,
+                      stream)
+
+
+def bwd_q4(q, k_q, k_d, v_q, v_d, o, lse, do, mask=None, *, scale=None, causal=False, q_offset=None, window=0,
+           deterministic=False, layout="bhsd", dq=None, dk=None, dv=None, dk_acc=None, dv_acc=None, workspace=None,
+           stream=None):
+    """Backward over a q4_0 K/V cache: as bwd_q8."""
+    return _bwd_cache(True, q, k_q, k_d, v_q, v_d, o, lse, do, mask, scale, causal, q_offset, window, deterministic,
+                      layout, dq, dk, dv, dk_acc, dv_acc, workspace, stream)
 
 
 def set_rows_backward(acc: torch.Tensor, idx: torch.Tensor, out_dtype=torch.bfloat16, out=None, stream=None):

@@ -90,7 +90,7 @@ typedef enum fa_mask_kind {
 typedef enum fa_kv_format {
   FA_KV_DTYPE = 0, /* K and V are tensors in p->dtype */
   FA_KV_Q8_0 = 1,  /* K and V are a q8_0 cache (fa_kv_q8, the _q8 entry points) */
-  FA_KV_F16 = 2    /* K and V are an fp16 cache (IEEE binary16) in p->layout, passed to the plain
+  FA_KV_F16 = 2,   /* K and V are an fp16 cache (IEEE binary16) in p->layout, passed to the plain
                       entry points; needs p->dtype == FA_BF16. llama.cpp PR #57, commit 2394a4c:
                       attention reads the cache in place, in the cache's own type (f16 or q8_0).
                       The library rounds K and V to bf16 (to nearest even) into its workspace
@@ -98,6 +98,7 @@ typedef enum fa_kv_format {
                       op then computes as on that bf16 K/V, and dK / dV (bf16, or added into the
                       fp32 accumulators) are the gradients with respect to it. The workspace-size
                       queries include the copy: 2 x B x Hkv x Sk x D x 2 bytes. */
+  FA_KV_Q4_0 = 4   /* K and V are a q4_0 cache (fa_kv_q4, the _q4 entry points; 3 is not used) */
 } fa_kv_format;
 
 typedef enum fa_layout {
@@ -125,7 +126,8 @@ typedef struct fa_params {
                             (its per-key-tile partials are added in a fixed order); dK/dV always are.
                             Costs some backward speed and workspace. */
   int32_t kv_format;  /* fa_kv_format: FA_KV_DTYPE or FA_KV_F16 for the plain entry points,
-                         FA_KV_Q8_0 for the _q8 ones (it sizes the workspace) */
+                         FA_KV_Q8_0 for the _q8 ones, FA_KV_Q4_0 for the _q4 ones (it sizes the
+                         workspace) */
   int32_t layout;     /* fa_layout of Q, K, V, O, dO, dQ, dK, dV (and of dk_acc / dv_acc, dk_rows /
                          dv_rows); LSE is always [B, Hq, Sq] and a q8_0 cache's planes always
                          [B, Hkv, Sk, ...] */
@@ -202,6 +204,178 @@ FA_API fa_status fa_train_bwd_q8(const fa_params* p, const void* q, const fa_kv_
 FA_API fa_status fa_train_bwd_accum_q8(const fa_params* p, const void* q, const fa_kv_q8* kv, const void* mask,
                                        const void* o, const float* lse, const void* dO, void* dq, float* dk_acc,
                                        float* dv_acc, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A 4-bit K/V cache in ggml's q4_0 blocks, split like fa_kv_q8 into a value plane and a scale
+ * plane. Per (batch, key/value head, key) and block of 32 consecutive features: one fp16 scale d
+ * and 16 bytes, byte j holding feature j in its low and feature j + 16 in its high four bits; the
+ * value of a feature is d * (bits - 8). DEVICE pointers, 16-byte aligned:
+ *   k_q, v_q: uint8 [B, Hkv, Sk, D / 2]; k_d, v_d: fp16 (IEEE binary16 bits) [B, Hkv, Sk, D / 32].
+ */
+typedef struct fa_kv_q4 {
+  const uint8_t* k_q;
+  const uint16_t* k_d;
+  const uint8_t* v_q;
+  const uint16_t* v_d;
+} fa_kv_q4;
+
+/*
+ * The op with K and V read from a q4_0 cache: as the _q8 entry points, with p->kv_format ==
+ * FA_KV_Q4_0 and p->dtype == FA_BF16 (else FA_ERR_UNSUPPORTED). The values are rounded to bf16 (to
+ * nearest even) and the op computes on that bf16 K/V; dK and dV are the gradients with respect to
+ * it. Forward and backward both expand the cache once into a bf16 copy in their workspace
+ * (2 x B x Hkv x Sk x D x 2 bytes, included in the workspace-size queries).
+ */
+FA_API fa_status fa_train_fwd_q4(const fa_params* p, const void* q, const fa_kv_q4* kv, const void* mask,
+                                 void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+FA_API fa_status fa_train_bwd_q4(const fa_params* p, const void* q, const fa_kv_q4* kv, const void* mask,
+                                 const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                                 void* ws, size_t ws_bytes, void* stream);
+FA_API fa_status fa_train_bwd_accum_q4(const fa_params* p, const void* q, const fa_kv_q4* kv, const void* mask,
+                                       const void* o, const float* lse, const void* dO, void* dq, float* dk_acc,
+                                       float* dv_acc, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A tensor of B x S rows of H heads of D features, the D features of a head contiguous and
+ * everything else strided (in elements): the row of (b, s, h) starts at
+ * ptr + b * stride_b + s * stride_s + h * stride_h. It describes [B, H, S, D] and [B, S, H, D]
+ * tensors and the query, key or value part of a fused projection's output. ptr is a DEVICE
+ * pointer, 16-byte aligned; the strides are not negative and a multiple of 16 bytes (those of a
+ * dimension of size 1 are not looked at). In an output no two rows overlap.
+ */
+typedef struct fa_view {
+  void* ptr;
+  int64_t stride_b;
+  int64_t stride_s;
+  int64_t stride_h;
+} fa_view;
+
+/*
+ * RMS norm of every query and key head and the rotary position, in one pass over Q and K; what the
+ * attention entry points take as q and k. For a row x[D] (one head of one token) at position p:
+ *     n[d] = x[d] * w[d] / sqrt(mean(x^2) + eps)                       (norm == 1; else n = x)
+ *     (y[a], y[b]) = factor * (n[a] cos t - n[b] sin t, n[b] cos t + n[a] sin t),  t = p * inv_freq[i]
+ * for the pairs i < rot / 2 of the first `rot` features: (a, b) = (i, i + rot / 2), or
+ * (2 i, 2 i + 1) when interleaved; the features at rot and above are n. Statistics and products are
+ * 32-bit, the angle's reduction is exact for |p| < 2^31, and y is rounded once. inv_freq carries any
+ * scaling for long contexts; `factor` is the one that goes with it (1 without).
+ */
+typedef struct fa_rope_params {
+  int32_t B;           /* 1 .. 65535 */
+  int32_t S;           /* tokens per sequence, 0 .. 2^24 (0 makes the call a no-op) */
+  int32_t Hq;          /* query heads, 0 .. 65535 */
+  int32_t Hkv;         /* key heads, 0 .. 65535; one of the two at least 1 */
+  int32_t D;           /* 64 or 128 */
+  int32_t dtype;       /* fa_dtype of x, y and their gradients */
+  int32_t w_dtype;     /* fa_dtype of the norm weights: dtype or FA_F32 */
+  int32_t rot;         /* rotated features: a multiple of 8, 0 .. D */
+  int32_t interleaved; /* 0: pairs (i, i + rot / 2); 1: pairs (2 i, 2 i + 1) */
+  int32_t norm;        /* 1: RMS norm with weights; 0: rotation alone */
+  float eps;           /* > 0, finite (norm == 1) */
+  float factor;        /* finite */
+  int64_t offset;      /* without positions: token s sits at offset + s */
+  int64_t pos_stride_b; /* positions of sequence b start at positions + b * pos_stride_b */
+  int32_t reserved;    /* must be 0 */
+} fa_rope_params;
+
+/*
+ * positions: int64 (8-byte aligned; element (b, s) at b * pos_stride_b + s) or NULL; inv_freq:
+ * fp32 [rot / 2] (NULL when rot == 0); q_weight, k_weight: [D] in w_dtype, 16-byte aligned (NULL
+ * when norm == 0). The views of a side with no heads are not looked at and may be NULL. Outputs
+ * overlap neither the inputs nor each other.
+ */
+FA_API fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_view* k, const void* q_weight,
+                                 const void* k_weight, const float* inv_freq, const int64_t* positions,
+                                 const fa_view* q_out, const fa_view* k_out, void* stream);
+
+/*
+ * Its backward: from the gradients dy of the outputs, and the inputs, writes the gradients of the
+ * inputs (rounded once) and, when norm == 1, of the weights (fp32 [D], overwritten): with g = dy
+ * rotated back (and times factor), r = 1 / sqrt(mean(x^2) + eps), t = g * w:
+ *     dx = r * (t - x * r^2 * mean(t * x));   dw = sum over b, s, h of g * x * r.
+ * dw is summed in 32 bits in a fixed order: results are the same from run to run. `ws` is scratch
+ * of fa_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned. q and k are not read when
+ * norm == 0 (their views may be NULL then, as may ws, dq_weight and dk_weight).
+ */
+FA_API size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params* p);
+FA_API fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, const fa_view* dk_out,
+                                     const fa_view* q, const fa_view* k, const void* q_weight, const void* k_weight,
+                                     const float* inv_freq, const int64_t* positions, const fa_view* dq,
+                                     const fa_view* dk, float* dq_weight, float* dk_weight, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * A quantized K/V cache that is written, read back and attended to in place (llama.cpp PR #57,
+ * commit 2394a4c: the chunk's K/V are written into the cached window and attention reads that
+ * window). The planes are those of fa_kv_q8 (kv_format FA_KV_Q8_0) or fa_kv_q4 (FA_KV_Q4_0).
+ */
+typedef struct fa_cache {
+  int32_t B;         /* 1 .. 65535 */
+  int32_t Hkv;       /* 1 .. 65535 */
+  int32_t S;         /* keys a sequence has room for, 1 .. 2^24 */
+  int32_t D;         /* 64 or 128 */
+  int32_t kv_format; /* FA_KV_Q8_0 or FA_KV_Q4_0 */
+  int32_t reserved;  /* must be 0 */
+  void* k_q;
+  uint16_t* k_d;
+  void* v_q;
+  uint16_t* v_d;
+} fa_cache;
+
+/*
+ * Quantizes n_rows new rows of K and V per sequence as it writes them: row r of sequence b goes to
+ * key begin[b] + r (begin: int64 [B] in device memory, or NULL: begin_all for every sequence, which
+ * the call checks: 0 <= begin_all, begin_all + n_rows <= S). With count (int64 [B] in device memory,
+ * or NULL) only the first count[b] rows of sequence b are written (a padded batch); every other key of
+ * the cache keeps its contents. k, v: views with S = n_rows, H = Hkv, elements of dtype (fa_dtype).
+ * Blocks of 32 features, in 32-bit arithmetic:
+ *   q8_0: d = fp16(max |x| / 127), q = round(x / d) to nearest even, held to [-127, 127];
+ *   q4_0: d = fp16(m / -8), m the value of the largest magnitude (of several: the one of the lowest
+ *         index), bits = round(x / d) + 8, held to [0, 15].
+ * d is held to fp16's largest finite value; where d is 0 the block's values are 0. A value that is
+ * not a number counts as 0, an infinite one as the largest finite number of its sign. A begin or
+ * count from device memory cannot be checked before the launch: a row whose key would lie outside
+ * [0, S) is not written, and 0x40000000 | 951 is recorded in the status word (a count outside
+ * [0, n_rows] is taken as the nearer end of that range). n_rows == 0 is a no-op.
+ */
+FA_API fa_status fa_cache_write(const fa_cache* c, const fa_view* k, const fa_view* v, int32_t dtype, int32_t n_rows,
+                                const int64_t* begin, int64_t begin_all, const int64_t* count, void* stream);
+
+/*
+ * Reads keys begin .. begin + n_rows - 1 of every sequence and head back as values (d * q, rounded
+ * once to dtype) into views with S = n_rows, H = Hkv. Needs 0 <= begin, begin + n_rows <= S.
+ */
+FA_API fa_status fa_cache_read(const fa_cache* c, int64_t begin, int32_t n_rows, int32_t dtype, const fa_view* k,
+                               const fa_view* v, void* stream);
+
+/*
+ * Attention of the newest Sq tokens of every sequence over its quantized cache, read in place: the
+ * serving form, for single tokens and short drafts. Sequence b has lengths[b] keys, the Sq tokens'
+ * own among them: query i sits at position lengths[b] - Sq + i and sees the keys j at or before it
+ * (with window w > 0 only those with position - j <= w). A query that sees no key (a position below
+ * zero, a length of 0) gets O = 0 and LSE = 0. Keys at or past a sequence's length are not read.
+ * The products are exact in the stored integers and the scales are applied in 32 bits (K and V are
+ * not rounded to bf16 as they are on the training path).
+ */
+typedef struct fa_decode_params {
+  int32_t Hq;        /* query heads, a multiple of the cache's Hkv, at most 65535 */
+  int32_t Sq;        /* query tokens per sequence, 0 .. 16 (0 makes the call a no-op) */
+  int32_t window;    /* 0: none */
+  int32_t layout;    /* fa_layout of q and o (contiguous, bf16); lse is [B, Hq, Sq] */
+  float scale;       /* softmax scale, finite */
+  int32_t reserved;  /* must be 0 */
+} fa_decode_params;
+
+/* Bytes of scratch fa_decode needs (256-byte aligned; 0 when none). */
+FA_API size_t fa_decode_workspace_size(const fa_decode_params* p, const fa_cache* c);
+
+/*
+ * lengths: int64 [B] in device memory, or NULL: every sequence has c->S keys. A length outside
+ * [0, S] is taken as the nearer end of that range, and 0x40000000 | 952 is recorded in the status
+ * word. o: bf16, lse: fp32.
+ */
+FA_API fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c, const int64_t* lengths,
+                           void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * SET_ROWS backward: the gradient of the rows a chunk wrote into its cached K/V window
@@ -296,7 +470,8 @@ FA_API fa_status fa_train_bwd_noalloc(const fa_params* p, const void* q, const v
  * the first problem recorded since the last read: 0x80000000 | site when the wait
  * `site` ran out of its time limit (the kernel then stopped early and its outputs
  * are invalid), 0x40000000 | site when a kernel met a device-side argument it
- * could not use (site 950: a row index of fa_set_rows_backward outside [0, S)).
+ * could not use (site 950: a row index of fa_set_rows_backward outside [0, S); 951: a row of
+ * fa_cache_write outside the cache; 952: a length of fa_decode outside [0, S]).
  * Synchronous (waits for the device to finish the copy). Returns FA_ERR_CUDA if
  * no device is usable.
  */
