@@ -4,24 +4,30 @@
 // Mathematics. With G = Hq / Hkv query heads on a key/value head, the R = G * Sq query rows of one
 // head all read the same keys. A block of 32 features of a key is d * n with whole numbers n, so
 //     s_j = scale * sum_blocks d_jb <n_jb, q_b>,   o = sum_j sum_blocks (p_j d_jb) n_jb :
-// the tensor cores multiply the whole numbers, exact in bf16, by q and by p * d, and the scales
-// never touch the 8- or 4-bit data. Scores, softmax statistics and sums are fp32; p * d is rounded
-// to bf16 for the second product (off by 2^-9 at most, as every key's weight on the training path).
+// the tensor cores multiply the whole numbers, exact as fp16, by q and by p * d, and the scales never
+// touch the 8- or 4-bit data. Scores, softmax statistics and sums are fp32. Query rows are scaled by a
+// power of two to the top of fp16's range, where a bf16 value down to 2^-28 of the row's largest is
+// exact; p * d is rounded to fp16, 2^-12 of its value, with a power of two of its own that keeps it
+// below 2^15 whatever the scales are (see `level`).
 //
 // What bounds it: the planes are read once, 144 bytes a key for D = 128 in 4 bits, so HBM; next to
 // that the instructions that turn packed bits into operands. Keys are the 16 rows of an
 // mma.sync m16n8k16 and query rows its 8 columns: with 4 query rows a head a tcgen05 tile of 128
-// rows would be 3% full, and its operands would have to be written to shared memory as bf16 first,
-// four times the bytes that are read.
+// rows would be 3% full, and its operands would have to be written to shared memory as 16-bit numbers
+// first, four times the bytes that are read.
 //
-// A 4-bit number b becomes a bf16 by two instructions for two of them: its bits are put below the
-// leading one of 16.0, which makes 16 + b. For K the difference to b - 8 is a multiple of the sum of
-// a block's q, the products' starting value; for V it is subtracted (an exact bf16 operation),
-// since there the difference would be far larger than what is summed.
+// From bits to operands: ldmatrix hands a lane the packed words of its operand rows, for V with two
+// keys side by side (transposed). The bits of two numbers are then put below the leading one of a
+// power of two (one logic instruction: 1024 + b and 64 + b place a low and a high nibble without a
+// shift of their own), and the power and the format's offset are taken off again by a packed
+// subtraction, exact, on the other pipe.
 //
-// Every warp walks its own tiles of 32 keys through its own ring of shared memory (cp.async, no
-// block barriers), with its own running maximum; a block's warps are joined in shared memory, and
-// the blocks of a sequence, each a fixed number of keys, by a second kernel.
+// Split: the tiles of 32 keys of all sequences and heads are one list, cut into equal slices, one for
+// each block that the SMs hold at a time; a slice holds the end of one head, whole heads and the
+// beginning of another. A block's warps take tiles in turn, each through its own ring of shared memory
+// (cp.async, no block barriers) with its own running maximum, and are joined in shared memory at the
+// end of a head; heads that several blocks share are joined by a second kernel. Where every head is a
+// few tiles long a block takes one head, and there is no second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,8 +44,10 @@ namespace fa {
 namespace {
 
 constexpr int kMaxTokens = 16;
-constexpr int kWarps = 4;
-constexpr int kTile = 32;   // keys a warp takes at a time
+constexpr int kMostWarps = 8;
+constexpr int kTile = 32;         // keys a warp takes at a time
+constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct DecodeArgs {
   CacheView c;
@@ -47,14 +55,14 @@ struct DecodeArgs {
   __nv_bfloat16* o;
   float* lse;
   const int64_t* lengths;
-  float* part_o;         // [B, Hq, Sq, splits, D]: unnormalised, relative to part_ml's maximum
-  float2* part_ml;       // [B, Hq, Sq, splits]: maximum (of scores in base 2) and sum
+  // slices only: what blocks leave of heads that they share, two slots a block, and the list
+  float* part_o;         // [row blocks, blocks, 2, rows, D]: unnormalised
+  float2* part_ml;       // [row blocks, blocks, 2, rows]: what the weights are relative to (base 2), and their sum
+  int* list;             // [B + 1]: tiles before sequence b, per key/value head
   unsigned* status;
   float scale2;          // scale * log2(e)
   int Hq, Sq, window, layout;
   int G, R;              // query heads and rows of a key/value head
-  int span;              // keys of a block
-  int splits;            // blocks of a (sequence, head)
 };
 
 // The keys a sequence's queries may see: [lo, len), lo on a tile's border.
@@ -80,17 +88,28 @@ __device__ __forceinline__ size_t q_offset(const DecodeArgs& a, int b, int h, in
   return (a.layout ? ((size_t)b * a.Sq + i) * a.Hq + head : ((size_t)b * a.Hq + head) * a.Sq + i) * a.c.D;
 }
 
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+// Zeros, and nothing read, where not `on`.
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool on) {
+__device__ __forceinline__ void cp_async_small_if(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
 }
 
@@ -104,13 +123,33 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+// Four 8 x 8 matrices of 16-bit elements, lane i naming row i % 8 of matrix i / 8: of matrix j lane
+// (g, t) gets elements 2 t, 2 t + 1 of row g, or, transposed, element g of rows 2 t and 2 t + 1.
+template <bool TRANS>
+__device__ __forceinline__ void load_matrices(uint32_t at, uint32_t (&x)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+}
 
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -119,16 +158,34 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Four-bit numbers of both halves of x at bit `at`, as the bf16 pair 16 + b.
-template <int AT>
-__device__ __forceinline__ uint32_t nibbles(uint32_t x) {
-  const uint32_t y = AT < 3 ? x << (3 - AT) : x >> (AT - 3);
-  return (y & 0x00780078u) | 0x41804180u;
-}
-__device__ __forceinline__ uint32_t minus24(uint32_t x) {
-  const __nv_bfloat162 k = __halves2bfloat162(__ushort_as_bfloat16(0x41C0), __ushort_as_bfloat16(0x41C0));
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), k);
+// x - k for both fp16 halves of x, k the bits of the constant.
+template <uint16_t K>
+__device__ __forceinline__ uint32_t sub_f16(uint32_t x) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __halves2half2(__ushort_as_half(K), __ushort_as_half(K)));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Fp16 operands from the packed words of a block. 4 bits, one word: the numbers of bytes (0, 2) and
+// (1, 3), first those of the low nibbles, then of the high ones.
+__device__ __forceinline__ void pairs_q4(uint32_t w, uint32_t (&f)[4]) {
+  const uint32_t h = w >> 8;
+  f[0] = sub_f16<0x6408>((w & 0x000f000fu) | 0x64006400u);   // 1024 + b - 1032
+  f[1] = sub_f16<0x6408>((h & 0x000f000fu) | 0x64006400u);
+  f[2] = sub_f16<0x5480>((w & 0x00f000f0u) | 0x54005400u);   // 64 + b - 72
+  f[3] = sub_f16<0x5480>((h & 0x00f000f0u) | 0x54005400u);
+}
+// 8 bits, one word of each half block: bytes (A, B) and (C, D) of the first, then of the second.
+template <int A, int B, int C, int D>
+__device__ __forceinline__ void pairs_q8(uint32_t w0, uint32_t w1, uint32_t (&f)[4]) {
+  const uint32_t a = w0 ^ 0x80808080u, b = w1 ^ 0x80808080u;
+  f[0] = sub_f16<0x6480>(__byte_perm(a, 0x64646464u, 0x4040 | A | B << 8));   // 1024 + (n + 128) - 1152
+  f[1] = sub_f16<0x6480>(__byte_perm(a, 0x64646464u, 0x4040 | C | D << 8));
+  f[2] = sub_f16<0x6480>(__byte_perm(b, 0x64646464u, 0x4040 | A | B << 8));
+  f[3] = sub_f16<0x6480>(__byte_perm(b, 0x64646464u, 0x4040 | C | D << 8));
 }
 
 // Where things are in a ring slot, and how a row's 16-byte pieces are permuted there so that the
@@ -144,365 +201,474 @@ struct Slot {
   static constexpr int VD_OFF = KD_OFF + kTile * SC;
   static constexpr int BYTES = VD_OFF + kTile * SC;
   static constexpr int STAGES = BYTES <= 5120 ? 3 : 2;
-  __device__ static __forceinline__ int piece(int row, int p) {
-    constexpr int PER = 128 / ROW;                // rows in 128 bytes
-    return p ^ ((row / PER) & (PIECES - 1));
-  }
+  // Piece p of a row is at piece p ^ (row / PER) % PIECES, PER the rows in 128 bytes: the rows of a
+  // matrix then meet no bank twice. Rows 8 apart are permuted alike.
+  static constexpr int PER = 128 / ROW;
+  __device__ static __forceinline__ int permuted(unsigned row) { return (int)(row / PER % PIECES); }
 };
 
+// The scales of a key, as they are and as floats.
 template <int NB>
-__device__ __forceinline__ void load_scales(uint32_t at, float (&d)[NB]) {
+__device__ __forceinline__ uint32_t load_scales(uint32_t at, float (&d)[NB]) {
   if constexpr (NB == 4) {
     const uint2 u = lds64(at);
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
     d[0] = a.x; d[1] = a.y; d[2] = b.x; d[3] = b.y;
+    return u.x | u.y;
   } else {
     const uint32_t u = lds32(at);
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u));
     d[0] = a.x; d[1] = a.y;
+    return u;
   }
 }
 
-// One block: `span` keys of one (sequence, key/value head), for NT * 8 of its query rows.
-template <int D, bool Q4, int NT>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(DecodeArgs a) {
+// Warps of a block and blocks an SM holds: as many as registers and the rings of shared memory leave room for
+// (kernels of the widest rows, 128 features in 8 bits, take smaller blocks to fill it).
+constexpr int warps_of(int D, bool q4) { return D == 128 && !q4 ? 4 : 8; }
+constexpr int held_of(int D, bool q4, int nt) {
+  return D == 128 ? (q4 ? (nt == 1 ? 2 : 1) : (nt == 1 ? 3 : 2)) : (q4 && nt == 1 ? 3 : 2);
+}
+
+// Slices of the list of `total` tiles over n blocks: where slice i begins, and the slice of a tile.
+__device__ __forceinline__ long long slice_begin(int i, long long total, int n) { return i * total / n; }
+__device__ __forceinline__ int slice_of(long long tile, long long total, int n) { return (int)(((tile + 1) * n - 1) / total); }
+
+// Tiles before each sequence, per key/value head, into list[0 .. B] in shared memory (all threads).
+__device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool report) {
+  __shared__ int warp_sum[kMostWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int before = 0;
+  for (int b0 = 0; b0 < a.c.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < a.c.B) {
+      const Range kr = key_range(a, b, report);
+      n = (kr.len - kr.lo + kTile - 1) / kTile;
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) x += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (b < a.c.B) list[b] = before + x - n;
+    before += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) list[a.c.B] = before;
+  __syncthreads();
+}
+
+// A block's work: SLICES: slice blockIdx.x of the list; else the head blockIdx.x. NT * 8 query rows from
+// blockIdx.y * NT * 8 on.
+template <int D, bool Q4, int NT, bool SLICES>
+__global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) decode_kernel(DecodeArgs a) {
   using S = Slot<D, Q4>;
-  constexpr int NB = S::NB;
+  constexpr int NB = S::NB, kWarps = warps_of(D, Q4);
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int list[SLICES ? kMaxListed + 1 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x % a.splits, head = blockIdx.x / a.splits;   // head: of all sequences
-  const int b = head / a.c.Hkv, h = head % a.c.Hkv;
   const int r0 = blockIdx.y * NT * 8;
-  const Range kr = key_range(a, b, split == 0 && h == 0 && r0 == 0 && threadIdx.x == 0);
-  const int k0 = kr.lo + split * a.span;
-  if (k0 >= kr.len && a.splits > 1) return;       // the joining kernel knows
-  const int k1 = min(kr.len, k0 + a.span);
-  const int tiles = k0 < k1 ? (k1 - k0 + kTile - 1) / kTile : 0;
-  const size_t plane = (size_t)head * a.c.S;
-
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::STAGES * S::BYTES);
-  auto load = [&](int tile, int slot) {
-    const int first = k0 + tile * kTile;
-    const uint32_t at = ring + slot * S::BYTES;
-#pragma unroll
-    for (int i = 0; i < S::PIECES; ++i) {
-      const int c = lane + 32 * i, row = c / S::PIECES, p = c % S::PIECES;
-      const bool on = first + row < k1;
-      const size_t src = (plane + (on ? first + row : 0)) * S::ROW + 16 * p;
-      const uint32_t dst = at + row * S::ROW + 16 * S::piece(row, p);
-      cp_async16(dst, static_cast<const uint8_t*>(a.c.k_q) + src, on);
-      cp_async16(dst + S::V_OFF, static_cast<const uint8_t*>(a.c.v_q) + src, on);
-    }
-    const bool on = first + lane < k1;
-    const size_t src = (plane + (on ? first + lane : 0)) * NB;
-    cp_async_small<S::SC>(at + S::KD_OFF + lane * S::SC, a.c.k_d + src, on);
-    cp_async_small<S::SC>(at + S::VD_OFF + lane * S::SC, a.c.v_d + src, on);
-  };
-  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  const bool report = r0 == 0 && (!SLICES || blockIdx.x == 0);
+  // the matrix row that this lane names: key `lane` of a tile
+  const uint32_t mrow = lane * S::ROW;
+  const int mperm = S::permuted(lane);
 
+  // Tiles [first_tile, first_tile + tiles) of one head: the sums go to o and lse when `whole`, else to slot `part`.
+  auto head_part = [&](int b, int h, const Range kr, int first_tile, int tiles, bool whole, int part) {
+    const int k0 = kr.lo + first_tile * kTile;
+    const size_t plane = ((size_t)b * a.c.Hkv + h) * a.c.S;
+    // lane's part of a tile's loads: pieces lane, lane + 32, ... of the numbers, key `lane`'s scales
+    const unsigned lrow = (unsigned)lane / S::PIECES;
+    const int lpiece = lane % S::PIECES;
+    auto load = [&](int tile, int slot) {
+      const int first = k0 + tile * kTile;
+      const uint32_t at = ring + slot * S::BYTES;
+      const size_t src = (plane + first) * S::ROW + 16 * lane;
+      const uint8_t* kq = static_cast<const uint8_t*>(a.c.k_q) + src;
+      const uint8_t* vq = static_cast<const uint8_t*>(a.c.v_q) + src;
+      const size_t sc = (plane + first + lane) * NB;
+      if (first + kTile <= kr.len) {
 #pragma unroll
-  for (int i = 0; i < S::STAGES - 1; ++i) {
-    if (warp + i * kWarps < tiles) load(warp + i * kWarps, i);
-    commit();
-  }
-
-  // the query rows as operands: lane (g, t) holds, of row g, the features that its part of a key's
-  // block holds
-  uint32_t qf[NT][NB][2][2];
-  float bias[NT][NB][2];   // -24 * (sum of a block's q) of columns 2 t and 2 t + 1
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = r0 + n * 8 + g;
-    const __nv_bfloat16* src = a.q + (r < a.R ? q_offset(a, b, h, r) : 0);
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      float sum = 0.f;
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int f0 = 32 * k + (Q4 ? 16 * st + 4 * t + j : 8 * t + 4 * st + 2 * j), f1 = f0 + (Q4 ? 2 : 1);
-          uint32_t v = 0;
-          if (r < a.R) v = (uint32_t)__bfloat16_as_ushort(src[f0]) | ((uint32_t)__bfloat16_as_ushort(src[f1]) << 16);
-          qf[n][k][st][j] = v;
-          sum += __uint_as_float(v << 16) + __uint_as_float(v & 0xffff0000u);
+        for (int i = 0; i < S::PIECES; ++i) {
+          const unsigned row = lrow + i * (32 / S::PIECES);
+          const uint32_t dst = at + row * S::ROW + 16 * (lpiece ^ S::permuted(row));
+          cp_async16(dst, kq + 512 * i);
+          cp_async16(dst + S::V_OFF, vq + 512 * i);
         }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      bias[n][k][0] = Q4 ? -24.f * __shfl_sync(0xffffffffu, sum, 8 * t) : 0.f;
-      bias[n][k][1] = Q4 ? -24.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4) : 0.f;
-    }
-  }
+        cp_async_small<S::SC>(at + S::KD_OFF + lane * S::SC, a.c.k_d + sc);
+        cp_async_small<S::SC>(at + S::VD_OFF + lane * S::SC, a.c.v_d + sc);
+        return;
+      }
+      // the last tile: keys past the end are zeros, and not read
+#pragma unroll
+      for (int i = 0; i < S::PIECES; ++i) {
+        const unsigned row = lrow + i * (32 / S::PIECES);
+        const uint32_t dst = at + row * S::ROW + 16 * (lpiece ^ S::permuted(row));
+        const bool on = first + (int)row < kr.len;
+        cp_async16_if(dst, on ? kq + 512 * i : static_cast<const uint8_t*>(a.c.k_q), on);
+        cp_async16_if(dst + S::V_OFF, on ? vq + 512 * i : static_cast<const uint8_t*>(a.c.v_q), on);
+      }
+      const bool on = first + lane < kr.len;
+      cp_async_small_if<S::SC>(at + S::KD_OFF + lane * S::SC, on ? a.c.k_d + sc : a.c.k_d, on);
+      cp_async_small_if<S::SC>(at + S::VD_OFF + lane * S::SC, on ? a.c.v_d + sc : a.c.v_d, on);
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
-  float acc[NT][2 * NB][4];   // rows: features of block k, half-tile m; columns: query rows 2 t, 2 t + 1
-  float mx[NT][2], sum[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int i = 0; i < 2 * NB; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[n][i][j] = 0.f;
-    mx[n][0] = mx[n][1] = -CUDART_INF_F;
-    sum[n][0] = sum[n][1] = 0.f;
-  }
-  // a tile is on an edge when some query row does not see all of it
-  const int all_to = kr.len - a.Sq, all_from = a.window > 0 ? kr.len - 1 - a.window : 0;
-
-  int slot = 0;
-  for (int tile = warp; tile < tiles; tile += kWarps) {
-    {
-      const int next = tile + (S::STAGES - 1) * kWarps;
-      if (next < tiles) load(next, slot == 0 ? S::STAGES - 1 : slot - 1);
+    for (int i = 0; i < S::STAGES - 1; ++i) {
+      if (warp + i * kWarps < tiles) load(warp + i * kWarps, i);
       commit();
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
-    __syncwarp();
-    const uint32_t at = ring + slot * S::BYTES;
-    const int first = k0 + tile * kTile;
-    const bool edge = first + kTile - 1 > all_to || first < all_from;
 
-    // scores of 2 x 16 keys
-    float s[NT][2][4];
+    // the query rows as operands: lane (g, t) holds, of row g, the features whose numbers its words
+    // of a key's block hold; each row by a power of two at the top of fp16's range, with the softmax
+    // scale's sign
+    uint32_t qf[NT][NB][2][2];
+    float unscale[NT][2];   // scores in base 2, of columns 2 t and 2 t + 1: the products by this; not negative
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      float d0[NB], d1[NB];
-      load_scales<NB>(at + S::KD_OFF + (16 * m + g) * S::SC, d0);
-      load_scales<NB>(at + S::KD_OFF + (16 * m + g + 8) * S::SC, d1);
+    for (int n = 0; n < NT; ++n) {
+      const int r = r0 + n * 8 + g;
+      const __nv_bfloat16* src = a.q + (r < a.R ? q_offset(a, b, h, r) : 0) + 4 * t;
+      uint2 raw[NB][2];   // features 4 t .. 4 t + 3 of each half block
+      float top = 0.f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int k = 0; k < NB; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][m][j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        uint32_t f[2][4];   // [row g or g + 8][two k-steps of two registers]
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int row = 16 * m + g + 8 * u;
-          if constexpr (Q4) {
-            const uint32_t w = lds32(at + row * S::ROW + 16 * S::piece(row, k) + 4 * t);
-            f[u][0] = nibbles<0>(w);
-            f[u][1] = nibbles<8>(w);
-            f[u][2] = nibbles<4>(w);
-            f[u][3] = nibbles<12>(w);
-          } else {
-            const uint2 w = lds64(at + row * S::ROW + 16 * S::piece(row, 2 * k + (t >> 1)) + 8 * (t & 1));
-            const uint32_t x = w.x ^ 0x80808080u, y = w.y ^ 0x80808080u;
-            f[u][0] = tc::pack_bf16x2(s8_to_f32(x, 0), s8_to_f32(x, 1));
-            f[u][1] = tc::pack_bf16x2(s8_to_f32(x, 2), s8_to_f32(x, 3));
-            f[u][2] = tc::pack_bf16x2(s8_to_f32(y, 0), s8_to_f32(y, 1));
-            f[u][3] = tc::pack_bf16x2(s8_to_f32(y, 2), s8_to_f32(y, 3));
-          }
+        for (int st = 0; st < 2; ++st) {
+          raw[k][st] = make_uint2(0, 0);
+          if (r < a.R) raw[k][st] = __ldg(reinterpret_cast<const uint2*>(src + 32 * k + 16 * st));
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(raw[k][st].x)), fabsf(bf16_hi(raw[k][st].x))),
+                                 fmaxf(fabsf(bf16_lo(raw[k][st].y)), fabsf(bf16_hi(raw[k][st].y)))));
         }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(14 - e) for a top in [2^e, 2^(e + 1)); exponents held to what 2^x and 2^-x both have
+      const int e = (int)(__float_as_uint(top) >> 23) - 127;
+      const int up = top > 0.f && e < 128 ? min(14 - e, 126) : 0;
+      const float f = copysignf(__uint_as_float((uint32_t)(127 + up) << 23), a.scale2);
+      const float back = __uint_as_float((uint32_t)(127 - up) << 23) * fabsf(a.scale2);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float c[4] = {bias[n][k][0], bias[n][k][1], bias[n][k][0], bias[n][k][1]};
-          mma(c, f[0][0], f[1][0], f[0][1], f[1][1], qf[n][k][0][0], qf[n][k][0][1]);
-          mma(c, f[0][2], f[1][2], f[0][3], f[1][3], qf[n][k][1][0], qf[n][k][1][1]);
-          s[n][m][0] = fmaf(d0[k], c[0], s[n][m][0]);
-          s[n][m][1] = fmaf(d0[k], c[1], s[n][m][1]);
-          s[n][m][2] = fmaf(d1[k], c[2], s[n][m][2]);
-          s[n][m][3] = fmaf(d1[k], c[3], s[n][m][3]);
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const float x0 = bf16_lo(raw[k][st].x) * f, x1 = bf16_hi(raw[k][st].x) * f;
+          const float x2 = bf16_lo(raw[k][st].y) * f, x3 = bf16_hi(raw[k][st].y) * f;
+          qf[n][k][st][0] = Q4 ? pack_f16x2(x0, x2) : pack_f16x2(x0, x1);
+          qf[n][k][st][1] = Q4 ? pack_f16x2(x1, x3) : pack_f16x2(x2, x3);
         }
-      }
+      unscale[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      unscale[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
 
-    // softmax weights, relative to the running maximum of each column
-    uint32_t hidden[NT];   // bit 4 m + j: pair j of half m
+    float acc[NT][2 * NB][4];   // rows: features 16 i + 2 g (and + 1); columns: query rows 2 t, 2 t + 1
+    float mx[NT][2];            // largest product seen
+    float base[NT][2];          // weights are 2^(score - base), base = largest score - level
+    float sum[NT][2];           // of this lane's weights
+    uint32_t fields[NT][2];     // exponent fields (at bit 10) of the V scales of all keys seen, or-ed
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][m][j] *= a.scale2;
-      hidden[n] = 0;
-      if (edge) {
+        for (int j = 0; j < 4; ++j) acc[n][i][j] = 0.f;
+      mx[n][0] = mx[n][1] = base[n][0] = base[n][1] = -CUDART_INF_F;
+      sum[n][0] = sum[n][1] = 0.f;
+      fields[n][0] = fields[n][1] = 0;
+    }
+    // keys that every query row sees: [all_from, all_to]
+    const int all_to = kr.len - a.Sq, all_from = a.window > 0 ? kr.len - 1 - a.window : 0;
+
+    // One tile, in the ring at `at`, from key `first` on. EDGE: some query row does not see all of it.
+    auto step = [&](auto on_edge, uint32_t at, int first) {
+      constexpr bool EDGE = decltype(on_edge)::value;
+      // products of 2 x 16 keys
+      float s[NT][2][4];
+      float d[4][NB];   // of keys g, g + 8, g + 16, g + 24
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int pos = kr.len - a.Sq + (r0 + n * 8 + 2 * t + j) % a.Sq;
+      for (int i = 0; i < 4; ++i) load_scales<NB>(at + S::KD_OFF + (8 * i + g) * S::SC, d[i]);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+      for (int k = 0; k < NB; ++k) {
+        uint32_t f[4][4];   // [keys 8 i ..][pairs]
+        if constexpr (Q4) {
+          uint32_t w[4];
+          load_matrices<false>(at + mrow + 16 * (k ^ mperm), w);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int key = first + 16 * m + g + 8 * u;
-              if (key > pos || (a.window > 0 && pos - key > a.window)) {
-                s[n][m][2 * u + j] = -CUDART_INF_F;
-                hidden[n] |= 1u << (4 * m + 2 * u + j);
+          for (int i = 0; i < 4; ++i) pairs_q4(w[i], f[i]);
+        } else {
+          uint32_t w[4], x[4];
+          load_matrices<false>(at + mrow + 16 * ((2 * k) ^ mperm), w);
+          load_matrices<false>(at + mrow + 16 * ((2 * k + 1) ^ mperm), x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pairs_q8<0, 1, 2, 3>(w[i], x[i], f[i]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            float c[4];
+            mma_f16_first(c, f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1], qf[n][k][0][0], qf[n][k][0][1]);
+            mma_f16(c, f[2 * m][2], f[2 * m + 1][2], f[2 * m][3], f[2 * m + 1][3], qf[n][k][1][0], qf[n][k][1][1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              s[n][m][j] = k == 0 ? d[2 * m + j / 2][k] * c[j] : fmaf(d[2 * m + j / 2][k], c[j], s[n][m][j]);
+          }
+      }
+
+      // The V scales. The level of a column is 29 - (the or of their exponent fields), which is no less than any of
+      // them: a scale is below 2^(15 - level), a weight at most 2^level, and their product below 2^15.
+      uint32_t bits[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t raw = load_scales<NB>(at + S::VD_OFF + (8 * i + g) * S::SC, d[i]);
+        bits[i] = (raw | raw >> 16) & 0x7c00u;
+      }
+      uint32_t all = 0;
+      if constexpr (!EDGE) all = __reduce_or_sync(0xffffffffu, bits[0] | bits[1] | bits[2] | bits[3]);
+
+      uint32_t hidden[NT];   // bit 4 m + j: pair j of half m
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        hidden[n] = 0;
+        if constexpr (EDGE) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int pos = kr.len - a.Sq + (r0 + n * 8 + 2 * t + j) % a.Sq;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int key = first + 16 * m + g + 8 * u;
+                if (key > pos || (a.window > 0 && pos - key > a.window)) {
+                  s[n][m][2 * u + j] = -CUDART_INF_F;
+                  hidden[n] |= 1u << (4 * m + 2 * u + j);
+                }
               }
-            }
+          }
         }
-      }
-      float top[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        top[j] = fmaxf(fmaxf(s[n][0][j], s[n][0][j + 2]), fmaxf(s[n][1][j], s[n][1][j + 2]));
-        top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
-        top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
-        top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-      }
-      const bool up = top[0] > mx[n][0] || top[1] > mx[n][1];
-      if (__any_sync(0xffffffffu, up)) {
-        float f[2];
+        float now[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float now = fmaxf(mx[n][j], top[j]);
-          f[j] = now > mx[n][j] ? exp2_fast(mx[n][j] - now) : 1.f;   // 0 from a maximum of -inf
-          mx[n][j] = now;
-          sum[n][j] *= f[j];
-        }
+          float top = fmaxf(fmaxf(s[n][0][j], s[n][0][j + 2]), fmaxf(s[n][1][j], s[n][1][j + 2]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          mx[n][j] = fmaxf(mx[n][j], top);
+          if constexpr (EDGE) {   // of the keys that this column sees
+            all = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) {
-          acc[n][i][0] *= f[0];
-          acc[n][i][1] *= f[1];
-          acc[n][i][2] *= f[0];
-          acc[n][i][3] *= f[1];
+            for (int i = 0; i < 4; ++i) all |= (hidden[n] >> (2 * i + j)) & 1u ? 0u : bits[i];
+            all |= __shfl_xor_sync(0xffffffffu, all, 4);
+            all |= __shfl_xor_sync(0xffffffffu, all, 8);
+            all |= __shfl_xor_sync(0xffffffffu, all, 16);
+          }
+          fields[n][j] |= all;
+          const float level = fmaf((float)(int)fields[n][j], -1.f / 1024, 29.f);
+          now[j] = mx[n][j] == -CUDART_INF_F ? -level : fmaf(mx[n][j], unscale[n][j], -level);
         }
-      }
+        if (__any_sync(0xffffffffu, now[0] != base[n][0] || now[1] != base[n][1])) {
+          float f[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float base = mx[n][j] == -CUDART_INF_F ? 0.f : mx[n][j];   // nothing seen so far: all weights 0
+          for (int j = 0; j < 2; ++j) {
+            f[j] = exp2_fast(base[n][j] - now[j]);   // 0 from a base of -inf
+            base[n][j] = now[j];
+            sum[n][j] *= f[j];
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * NB; ++i) {
+            acc[n][i][0] *= f[0];
+            acc[n][i][1] *= f[1];
+            acc[n][i][2] *= f[0];
+            acc[n][i][3] *= f[1];
+          }
+        }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float p = exp2_fast(s[n][m][2 * u + j] - base);
-            s[n][m][2 * u + j] = p;
-            sum[n][j] += p;
+          for (int j = 0; j < 4; ++j) {
+            float p = exp2_fast(fmaf(s[n][m][j], unscale[n][j & 1], -base[n][j & 1]));
+            if constexpr (EDGE) p = (hidden[n] >> (4 * m + j)) & 1u ? 0.f : p;
+            s[n][m][j] = p;
+            sum[n][j & 1] += p;
           }
       }
-    }
 
-    // o += V^T (p d)
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      float d0[NB], d1[NB];
-      load_scales<NB>(at + S::VD_OFF + (16 * m + g) * S::SC, d0);
-      load_scales<NB>(at + S::VD_OFF + (16 * m + g + 8) * S::SC, d1);
+      // o += V^T (p d)
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        uint32_t f[2][4];   // [keys 2 t, 2 t + 1 or those + 8][features]
+        uint32_t f[4][4];   // [keys 8 i ..][features 2 g, 2 g + 1, 16 + 2 g, 17 + 2 g]
+        if constexpr (Q4) {
+          uint32_t x[4];
+          load_matrices<true>(at + S::V_OFF + mrow + 16 * (k ^ mperm), x);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int row = 16 * m + 8 * u + 2 * t;
-          if constexpr (Q4) {
-            // bytes 2 g, 2 g + 1 of the block, of two keys
-            const uint32_t wa = lds32(at + S::V_OFF + row * S::ROW + 16 * S::piece(row, k) + 4 * (g >> 1));
-            const uint32_t wb = lds32(at + S::V_OFF + (row + 1) * S::ROW + 16 * S::piece(row + 1, k) + 4 * (g >> 1));
-            const uint32_t x = __byte_perm(wa, wb, (g & 1) ? 0x7632u : 0x5410u);
-            f[u][0] = minus24(nibbles<0>(x));    // feature 2 g
-            f[u][1] = minus24(nibbles<8>(x));    // 2 g + 1
-            f[u][2] = minus24(nibbles<4>(x));    // 16 + 2 g
-            f[u][3] = minus24(nibbles<12>(x));   // 17 + 2 g
-          } else {
-            const int p = 2 * k + (g >> 2);
-            const uint32_t x = lds32(at + S::V_OFF + row * S::ROW + 16 * S::piece(row, p) + 4 * (g & 3)) ^ 0x80808080u;
-            const uint32_t y =
-                lds32(at + S::V_OFF + (row + 1) * S::ROW + 16 * S::piece(row + 1, p) + 4 * (g & 3)) ^ 0x80808080u;
+          for (int i = 0; i < 4; ++i) pairs_q4(x[i], f[i]);
+        } else {
+          uint32_t x[4], y[4];
+          load_matrices<true>(at + S::V_OFF + mrow + 16 * ((2 * k) ^ mperm), x);
+          load_matrices<true>(at + S::V_OFF + mrow + 16 * ((2 * k + 1) ^ mperm), y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[u][i] = tc::pack_bf16x2(s8_to_f32(x, i), s8_to_f32(y, i));   // 4 g + i
-          }
+          for (int i = 0; i < 4; ++i) pairs_q8<0, 2, 1, 3>(x[i], y[i], f[i]);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float w[4] = {s[n][m][0] * d0[k], s[n][m][1] * d0[k], s[n][m][2] * d1[k], s[n][m][3] * d1[k]};
-          if (edge) {   // a hidden key's scale may be anything
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = (hidden[n] >> (4 * m + j)) & 1u ? 0.f : w[j];
+          for (int m = 0; m < 2; ++m) {
+            float w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] = s[n][m][j] * d[2 * m + j / 2][k];
+              if constexpr (EDGE) w[j] = (hidden[n] >> (4 * m + j)) & 1u ? 0.f : w[j];   // its scale may be anything
+            }
+            const uint32_t b0 = transpose8x8(pack_f16x2(w[0], w[1]));
+            const uint32_t b1 = transpose8x8(pack_f16x2(w[2], w[3]));
+            mma_f16(acc[n][2 * k], f[2 * m][0], f[2 * m][1], f[2 * m + 1][0], f[2 * m + 1][1], b0, b1);
+            mma_f16(acc[n][2 * k + 1], f[2 * m][2], f[2 * m][3], f[2 * m + 1][2], f[2 * m + 1][3], b0, b1);
           }
-          const uint32_t b0 = transpose8x8(tc::pack_bf16x2(w[0], w[1]));
-          const uint32_t b1 = transpose8x8(tc::pack_bf16x2(w[2], w[3]));
-          mma(acc[n][2 * k], f[0][0], f[0][1], f[1][0], f[1][1], b0, b1);
-          mma(acc[n][2 * k + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0, b1);
-        }
       }
-    }
-    __syncwarp();   // the slot is read: the next load into it may begin
-    slot = slot == S::STAGES - 1 ? 0 : slot + 1;
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+    };
 
-  // join the block's warps: [warp][query row][D], and their maxima and sums
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(smem);
-  float2* sml = reinterpret_cast<float2*>(smem + kWarps * NT * 8 * D * 4);
+    int slot = 0;
+    for (int tile = warp; tile < tiles; tile += kWarps) {
+      {
+        const int next = tile + (S::STAGES - 1) * kWarps;
+        if (next < tiles) load(next, slot == 0 ? S::STAGES - 1 : slot - 1);
+        commit();
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
+      __syncwarp();
+      const uint32_t at = ring + slot * S::BYTES;
+      const int first = k0 + tile * kTile;
+      if (first + kTile - 1 > all_to || first < all_from) step(std::true_type{}, at, first);
+      else step(std::false_type{}, at, first);
+      __syncwarp();   // the slot is read: the next load into it may begin
+      slot = slot == S::STAGES - 1 ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+
+    // join the block's warps: [warp][query row][D], and what their weights are relative to and their sums
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(smem);
+    float2* sml = reinterpret_cast<float2*>(smem + kWarps * NT * 8 * D * 4);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float l = sum[n][j];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const int col = n * 8 + 2 * t + j;
-      if (g == 0) sml[warp * NT * 8 + col] = make_float2(mx[n][j], l);
-      float* row = so + ((size_t)warp * NT * 8 + col) * D;
+      for (int j = 0; j < 2; ++j) {
+        float l = sum[n][j];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int col = n * 8 + 2 * t + j;
+        if (g == 0) sml[warp * NT * 8 + col] = make_float2(base[n][j], l);
+        float* row = so + (warp * NT * 8 + col) * D;
 #pragma unroll
-      for (int i = 0; i < 2 * NB; ++i) {
-        const int f = 32 * (i / 2) + (Q4 ? 16 * (i % 2) + 2 * g : 4 * g + 2 * (i % 2));
-        *reinterpret_cast<float2*>(row + f) = make_float2(acc[n][i][j], acc[n][i][j + 2]);
+        for (int i = 0; i < 2 * NB; ++i)
+          *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(acc[n][i][j], acc[n][i][j + 2]);
+      }
+    __syncthreads();
+    constexpr int PER = D / 4;   // threads of a row
+    for (int i = threadIdx.x; i < NT * 8 * PER; i += kWarps * 32) {
+      const int col = i / PER, f = i % PER * 4, r = r0 + col;
+      if (r >= a.R) continue;
+      float top = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * NT * 8 + col].x);
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = sml[w * NT * 8 + col];
+        const float k = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
+        const float4 x = *reinterpret_cast<const float4*>(so + (w * NT * 8 + col) * D + f);
+        l = fmaf(k, ml.y, l);
+        o.x = fmaf(k, x.x, o.x);
+        o.y = fmaf(k, x.y, o.y);
+        o.z = fmaf(k, x.z, o.z);
+        o.w = fmaf(k, x.w, o.w);
+      }
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(a.o + q_offset(a, b, h, r) + f) =
+            make_uint2(tc::pack_bf16x2(o.x * inv, o.y * inv), tc::pack_bf16x2(o.z * inv, o.w * inv));
+        if (f == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : (top + log2f(l)) * kLn2;
+      } else {
+        const size_t at = (((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 + part) * (NT * 8) + col;
+        *reinterpret_cast<float4*>(a.part_o + at * D + f) = o;
+        if (f == 0) a.part_ml[at] = make_float2(top, l);
       }
     }
-  __syncthreads();
-  constexpr int PER = D / 4;   // threads of a row
-  for (int i = threadIdx.x; i < NT * 8 * PER; i += kWarps * 32) {
-    const int col = i / PER, f = i % PER * 4, r = r0 + col;
-    if (r >= a.R) continue;
-    float top = -CUDART_INF_F;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * NT * 8 + col].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = sml[w * NT * 8 + col];
-      const float k = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);
-      const float4 x = *reinterpret_cast<const float4*>(so + ((size_t)w * NT * 8 + col) * D + f);
-      l = fmaf(k, ml.y, l);
-      o.x = fmaf(k, x.x, o.x);
-      o.y = fmaf(k, x.y, o.y);
-      o.z = fmaf(k, x.z, o.z);
-      o.w = fmaf(k, x.w, o.w);
-    }
-    const size_t row = ((size_t)b * a.Hq + h * a.G) * a.Sq + r;   // of lse and the partials
-    if (a.splits > 1) {
-      const size_t at = row * a.splits + split;
-      *reinterpret_cast<float4*>(a.part_o + at * D + f) = o;
-      if (f == 0) a.part_ml[at] = make_float2(top, l);
-    } else {
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-      uint2 u = make_uint2(tc::pack_bf16x2(o.x * inv, o.y * inv), tc::pack_bf16x2(o.z * inv, o.w * inv));
-      *reinterpret_cast<uint2*>(a.o + q_offset(a, b, h, r) + f) = u;
-      if (f == 0) a.lse[row] = l == 0.f ? 0.f : (top + log2f(l)) * 0.6931471805599453f;
+    __syncthreads();   // the ring is free for the next head
+  };
+
+  if constexpr (!SLICES) {
+    const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
+    const Range kr = key_range(a, b, report && h == 0 && threadIdx.x == 0);
+    head_part(b, h, kr, 0, (kr.len - kr.lo + kTile - 1) / kTile, true, 0);
+  } else {
+    make_list(a, list, report);
+    if (report)   // for the joining kernel
+      for (int i = threadIdx.x; i <= a.c.B; i += kWarps * 32) a.list[i] = list[i];
+    const long long total = (long long)list[a.c.B] * a.c.Hkv;
+    long long at = slice_begin(blockIdx.x, total, gridDim.x);
+    const long long begin = at, end = slice_begin(blockIdx.x + 1, total, gridDim.x);
+    while (at < end) {
+      int b = 0, last = a.c.B - 1;   // the last sequence that begins at or before tile `at`
+      while (b < last) {
+        const int mid = (b + last + 1) / 2;
+        if ((long long)list[mid] * a.c.Hkv <= at) b = mid;
+        else last = mid - 1;
+      }
+      const int n = list[b + 1] - list[b];
+      const long long off = at - (long long)list[b] * a.c.Hkv;
+      const int h = (int)(off / n), tile = (int)(off % n);
+      const int take = (int)min((long long)(n - tile), end - at);
+      head_part(b, h, key_range(a, b, false), tile, take, take == n, at != begin);
+      at += take;
     }
   }
 }
 
-// Joins the blocks of one query row: 8 warps take its blocks in turn, four features a lane (D = 128)
-// or two (D = 64), and are joined in order.
+// Joins what several blocks left of one query row's head: the warps of a block take the parts in turn, and are
+// joined in order. A head that one block had is finished; one without keys is zeros.
 template <int D>
-__global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a) {
+__global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int blocks, int rows_per) {
   constexpr int F = D / 32;
   __shared__ float so[8][D];
   __shared__ float2 sml[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row = blockIdx.x;
   const int i = (int)(row % a.Sq), head = (int)(row / a.Sq % a.Hq), b = (int)(row / a.Sq / a.Hq);
-  const Range kr = key_range(a, b, false);
-  const int n = kr.len > kr.lo ? (kr.len - kr.lo + a.span - 1) / a.span : 0;
+  const int h = head / a.G, r = head % a.G * a.Sq + i;   // row of the key/value head
+  const long long total = (long long)a.list[a.c.B] * a.c.Hkv;
+  const int n = a.list[b + 1] - a.list[b];
+  const long long begin = (long long)a.list[b] * a.c.Hkv + (long long)h * n, end = begin + n;
+  const int c0 = n > 0 ? slice_of(begin, total, blocks) : 0, c1 = n > 0 ? slice_of(end - 1, total, blocks) : 0;
+  if (n > 0 && c0 == c1) return;
+  const int first_part = slice_begin(c0, total, blocks) != begin;   // of c0: its first head's, or its last's
   float top = -CUDART_INF_F, l = 0.f, o[F];
 #pragma unroll
   for (int j = 0; j < F; ++j) o[j] = 0.f;
-  for (int s = warp; s < n; s += 8) {
-    const size_t at = (size_t)row * a.splits + s;
-    const float2 ml = a.part_ml[at];
-    if (ml.x == -CUDART_INF_F && ml.y == 0.f) continue;   // saw nothing (a sum that is not a number stays one)
-    const float now = fmaxf(top, ml.x), k0 = exp2_fast(top - now), k1 = exp2_fast(ml.x - now);
-    top = now;
-    l = l * k0 + ml.y * k1;
+  if (n > 0)
+    for (int c = c0 + warp; c <= c1; c += 8) {
+      if (slice_begin(c, total, blocks) == slice_begin(c + 1, total, blocks)) continue;   // more blocks than tiles
+      const size_t at = (((size_t)(r / rows_per) * blocks + c) * 2 + (c == c0 ? first_part : 0)) * rows_per + r % rows_per;
+      const float2 ml = a.part_ml[at];
+      const float now = fmaxf(top, ml.x), k0 = exp2_fast(top - now), k1 = exp2_fast(ml.x - now);
+      top = now;
+      l = l * k0 + ml.y * k1;
 #pragma unroll
-    for (int j = 0; j < F; ++j) o[j] = o[j] * k0 + a.part_o[at * D + lane * F + j] * k1;
-  }
+      for (int j = 0; j < F; ++j) o[j] = o[j] * k0 + a.part_o[at * D + lane * F + j] * k1;
+    }
   if (lane == 0) sml[warp] = make_float2(top, l);
 #pragma unroll
   for (int j = 0; j < F; ++j) so[warp][lane * F + j] = o[j];
@@ -513,19 +679,21 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a) {
   l = 0.f;
   float x = 0.f;
   for (int w = 0; w < 8; ++w) {
-    if (sml[w].x == -CUDART_INF_F && sml[w].y == 0.f) continue;
+    if (sml[w].x == -CUDART_INF_F) continue;   // a warp without a part
     const float k = exp2_fast(sml[w].x - top);
     l = fmaf(k, sml[w].y, l);
     x = fmaf(k, so[w][threadIdx.x], x);
   }
   const size_t at = (a.layout ? ((size_t)b * a.Sq + i) * a.Hq + head : (size_t)row) * D;
   a.o[at + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-  if (threadIdx.x == 0) a.lse[row] = l == 0.f ? 0.f : (top + log2f(l)) * 0.6931471805599453f;
+  if (threadIdx.x == 0) a.lse[row] = l == 0.f ? 0.f : (top + log2f(l)) * kLn2;
 }
 
 struct DecodePlan {
-  int nt, span, splits, row_blocks;
-  size_t ml_off, total;
+  int nt, row_blocks;
+  bool slices;
+  long long blocks;
+  size_t ml_off, list_off, total;
 };
 
 DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
@@ -533,18 +701,24 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
   const int R = p->Hq / c.Hkv * p->Sq;
   d.nt = R <= 8 ? 1 : 2;
   d.row_blocks = (R + 8 * d.nt - 1) / (8 * d.nt);
-  const long long most = p->window > 0 && p->window < c.S ? (long long)p->window + p->Sq + kTile - 1 : c.S;
+  const long long most = p->window > 0 ? (long long)p->window + p->Sq + kTile - 1 : c.S;
   const int keys = (int)(most < c.S ? most : c.S);
-  const long long heads = (long long)c.B * c.Hkv * d.row_blocks;
-  // keys of a block: enough blocks for several on every SM, down to two tiles a warp
-  d.span = 1024;
-  while (d.span > 2 * kWarps * kTile && heads * ((keys + d.span - 1) / d.span) < 6LL * sm_count()) d.span /= 2;
-  if (keys <= 512) d.span = 512;   // one block, and no joining kernel
-  d.splits = (keys + d.span - 1) / d.span;
-  if (d.splits > 1) {
-    const size_t rows = (size_t)c.B * p->Hq * p->Sq * d.splits;
+  const int tiles = (keys + kTile - 1) / kTile;
+  const long long heads = (long long)c.B * c.Hkv;
+  // One head a block when a head is at most four tiles a warp (no second kernel), and when the list of
+  // sequences is too long for shared memory (heads enough for every SM then).
+  const int warps = warps_of(c.D, c.q4);
+  d.slices = tiles > 4 * warps && c.B <= kMaxListed;
+  d.blocks = heads;
+  if (d.slices) {
+    // as many blocks as the SMs hold at a time, no slice below a tile a warp
+    const long long all = (long long)held_of(c.D, c.q4, d.nt) * sm_count() / d.row_blocks, some = heads * tiles / warps;
+    d.blocks = all < some ? all : some;
+    if (d.blocks < 1) d.blocks = 1;
+    const size_t rows = (size_t)d.row_blocks * d.blocks * 2 * d.nt * 8;
     d.ml_off = align_up(rows * c.D * 4);
-    d.total = d.ml_off + align_up(rows * 8);
+    d.list_off = d.ml_off + align_up(rows * 8);
+    d.total = d.list_off + align_up(((size_t)c.B + 1) * 4);
   }
   return d;
 }
@@ -564,14 +738,15 @@ fa_status check_decode(const fa_decode_params* p, const fa_cache* c, CacheView& 
   return FA_OK;
 }
 
-template <int D, bool Q4, int NT>
+template <int D, bool Q4, int NT, bool SLICES>
 cudaError_t launch_decode(const DecodeArgs& a, dim3 grid, cudaStream_t st) {
   using S = Slot<D, Q4>;
-  constexpr int ring = kWarps * S::STAGES * S::BYTES, join = kWarps * NT * 8 * (D * 4 + 8);
+  constexpr int kWarps = warps_of(D, Q4), ring = kWarps * S::STAGES * S::BYTES, join = kWarps * NT * 8 * (D * 4 + 8);
   constexpr int bytes = ring > join ? ring : join;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, Q4, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  auto kernel = decode_kernel<D, Q4, NT, SLICES>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, Q4, NT><<<grid, kWarps * 32, bytes, st>>>(a);
+  kernel<<<grid, kWarps * 32, bytes, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -616,7 +791,10 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   a.lse = lse;
   a.lengths = lengths;
   a.part_o = static_cast<float*>(ws);
-  a.part_ml = plan.splits > 1 ? reinterpret_cast<float2*>(static_cast<char*>(ws) + plan.ml_off) : nullptr;
+  if (plan.slices) {
+    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + plan.ml_off);
+    a.list = reinterpret_cast<int*>(static_cast<char*>(ws) + plan.list_off);
+  }
   a.status = device_status_ptr();
   a.scale2 = p->scale * 1.4426950408889634f;
   a.Hq = p->Hq;
@@ -625,25 +803,24 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   a.layout = p->layout;
   a.G = p->Hq / cv.Hkv;
   a.R = a.G * p->Sq;
-  a.span = plan.span;
-  a.splits = plan.splits;
-  const long long blocks = (long long)cv.B * cv.Hkv * plan.splits;
-  if (plan.row_blocks > 65535 || blocks > 0x7fffffffLL || rows > 0x7fffffffULL) { set_error("too many query rows for one launch"); return FA_ERR_UNSUPPORTED; }
-  const dim3 grid((unsigned)blocks, (unsigned)plan.row_blocks);
+  if (plan.row_blocks > 65535 || plan.blocks > 0x7fffffffLL || rows > 0x7fffffffULL) { set_error("too many query rows for one launch"); return FA_ERR_UNSUPPORTED; }
+  const dim3 grid((unsigned)plan.blocks, (unsigned)plan.row_blocks);
   cudaStream_t cs = (cudaStream_t)stream;
   auto go = [&](auto dim, auto q4) {
     constexpr int D = decltype(dim)::value;
     constexpr bool Q4 = decltype(q4)::value;
-    return plan.nt == 1 ? launch_decode<D, Q4, 1>(a, grid, cs) : launch_decode<D, Q4, 2>(a, grid, cs);
+    if (plan.nt == 1) return plan.slices ? launch_decode<D, Q4, 1, true>(a, grid, cs) : launch_decode<D, Q4, 1, false>(a, grid, cs);
+    return plan.slices ? launch_decode<D, Q4, 2, true>(a, grid, cs) : launch_decode<D, Q4, 2, false>(a, grid, cs);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
   cudaError_t e;
   if (cv.q4) e = cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
   else e = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
-  if (e == cudaSuccess && plan.splits > 1) {
-    if (cv.D == 64) decode_join_kernel<64><<<(unsigned)rows, 256, 0, cs>>>(a);
-    else decode_join_kernel<128><<<(unsigned)rows, 256, 0, cs>>>(a);
+  if (e == cudaSuccess && plan.slices) {
+    const int blocks = (int)plan.blocks, per = plan.nt * 8;
+    if (cv.D == 64) decode_join_kernel<64><<<(unsigned)rows, 256, 0, cs>>>(a, blocks, per);
+    else decode_join_kernel<128><<<(unsigned)rows, 256, 0, cs>>>(a, blocks, per);
     count_launches(1);
     e = cudaGetLastError();
   }

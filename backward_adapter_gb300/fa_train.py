@@ -277,7 +277,8 @@ def _on_device(t: torch.Tensor):
 
 def _stream(device: torch.device, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        # the handle alone: building the stream's Python object takes longer than a launch
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -311,7 +312,7 @@ def _view(t: torch.Tensor, layout: str) -> FaView:
 def _launch(device: torch.device, call, *args) -> None:
     """A call of the C ABI on `device`, as _on_device (which costs a few microseconds: skipped where
     the device is current already)."""
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         status = call(*args)
     else:
         with torch.cuda.device(device):

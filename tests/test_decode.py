@@ -1,11 +1,14 @@
 """Attention of the newest tokens over a quantized cache (fa_decode) against the fp64 oracle.
 
 Tolerances, from the data of each case. A score is a sum of D products of whole numbers and q in fp32, block by block:
-with Q_b the sum of |q| over a block, its partial sums stay below 55 Q_b (4 bits: numbers of 16 .. 31 and a starting value of
-24 sums; 127 Q_b in 8 bits), and one accumulation of 17 terms is off by at most 17 truncations, 2^-19 of that for the two of a
-block. So a score is off by at most E = 2^-19 scale sum_b |d_b| W Q_b (W = 55 or 127) over the keys a query sees; LSE by E and
-the roundings of a logarithm near it, 2^-20 (1 + |LSE|). A weight is off by the factor e^(+-E) and, rounded to bf16 as an
-operand, by 2^-8; the result is rounded to bf16, 2^-8: |dO| <= (2^-8 + 2 E + 2^-16) * sum p |v| / sum p + 2^-8 |O|.
+with Q_b the sum of |q| over a block, its partial sums stay below W Q_b (W = 8 in 4 bits, 127 in 8), and one accumulation of
+17 terms is off by at most 17 truncations, 2^-19 of that for the two of a block and the sum over blocks.
+So a score is off by at most E = 2^-19 scale sum_b |d_b| W Q_b over the keys a query sees; LSE by E and
+the roundings of a logarithm near it, 2^-20 (1 + |LSE|). A weight p is off by the factor e^(+-E); p * d is rounded to fp16 in
+units in which the largest weight is 2^level and every product below 2^15, with level = 29 - (the or of the exponent fields of
+the V scales it is summed with): off by 2^-11 / 2 of its value or, where that is subnormal, by 2^-25. The whole numbers are at
+most W, sum p is at least 1, and the result is rounded to bf16, 2^-8 of its value, so with n keys
+    |dO| <= (2^-12 + 2 E + 2^-16) sum p |v| / sum p + n W 2^(-25 - level) + 2^-8 |O|.
 """
 import math
 
@@ -29,7 +32,7 @@ def score_error(q, planes, lengths, scale, window):
     """E of the module's comment for every (b, head, token)."""
     B, Hq, Sq, D = q.shape
     d = np.abs(planes[1].cpu().numpy().astype(np.float64))
-    w = 55.0 if planes[0].dtype == torch.uint8 else 127.0
+    w = 8.0 if planes[0].dtype == torch.uint8 else 127.0
     G = Hq // d.shape[1]
     e = np.zeros((B, Hq, Sq))
     qb = np.abs(q.reshape(B, Hq, Sq, D // 32, 32)).sum(-1)
@@ -44,6 +47,24 @@ def score_error(q, planes, lengths, scale, window):
     return e
 
 
+def weight_step(planes, lengths, Hq, Sq, window):
+    """n W 2^(-25 - level) of the module's comment for every (b, head, token)."""
+    bits = planes[3].cpu().numpy().view(np.uint16).astype(np.int64)
+    bits = np.bitwise_or.reduce((bits >> 10) & 31, axis=-1)   # [B, Hkv, S]
+    w = 8.0 if planes[0].dtype == torch.uint8 else 127.0
+    B, Hkv, _ = bits.shape
+    out = np.zeros((B, Hq, Sq))
+    for b in range(B):
+        for i in range(Sq):
+            pos = int(lengths[b]) - Sq + i
+            first = max(0, pos - window) if window > 0 else 0
+            if pos < first:
+                continue
+            fields = np.bitwise_or.reduce(bits[b, :, first:pos + 1], axis=-1)
+            out[b, :, i] = np.repeat((pos + 1 - first) * w * 2.0 ** (fields - 54.0), Hq // Hkv)
+    return out
+
+
 def check(q, planes, lengths, got, scale=None, window=0):
     o, lse = (t.double().cpu().numpy() for t in got)
     qn = q.double().cpu().numpy()
@@ -55,9 +76,9 @@ def check(q, planes, lengths, got, scale=None, window=0):
     E = score_error(qn, planes, n, scale, window)
     bad = np.abs(lse - want_lse) > E + 2.0 ** -20 * (1 + np.abs(want_lse))
     assert not bad.any(), (np.abs(lse - want_lse).max(), E.max())
-    e = E[..., None]
+    e, step = E[..., None], weight_step(planes, n, q.shape[1], q.shape[2], window)[..., None]
     err = np.abs(o - want)
-    assert np.all(err <= (2.0 ** -8 + 2 * e + 2.0 ** -16) * size + 2.0 ** -8 * np.abs(want)), err.max()
+    assert np.all(err <= (2.0 ** -12 + 2 * e + 2.0 ** -16) * size + step + 2.0 ** -8 * np.abs(want)), err.max()
     empty = want_lse == 0
     if empty.any():
         assert np.all(o[empty & (np.abs(want).sum(-1) == 0)] == 0)
@@ -84,7 +105,11 @@ SHAPES = {
     "draft_of_16": (1, 6, 2, 150, 64, 16, [77], 0),
     "split": (2, 8, 2, 1500, 128, 1, [1500, 700], 0),
     "split_ragged": (5, 4, 4, 1111, 64, 1, [0, 1, 257, 512, 1111], 0),
-    "split_draft": (2, 4, 1, 900, 128, 3, [900, 2], 0),
+    "split_draft": (2, 4, 1, 1900, 128, 3, [1900, 2], 0),
+    "split_group_of_40": (2, 40, 1, 1300, 64, 1, [1300, 33], 0),
+    "split_heads": (3, 16, 8, 1200, 128, 1, [1200, 64, 1055], 0),
+    "split_short_lengths": (7, 4, 2, 4000, 64, 1, [33, 1, 0, 64, 2, 31, 65], 0),
+    "split_all_empty": (2, 4, 2, 4000, 64, 1, [0, 0], 0),
     "window": (3, 4, 2, 1000, 128, 1, [1000, 40, 555], 100),
     "window_of_1": (2, 4, 2, 400, 64, 1, [400, 1], 1),
     "window_draft": (2, 4, 2, 800, 64, 4, [799, 3], 33),
@@ -157,7 +182,7 @@ def test_lengths_outside_the_cache_are_held_to_it_and_reported():
 
 @pytest.mark.gpu
 def test_no_tokens_and_given_outputs():
-    q, planes = make(2, 4, 2, 1000, 64, 1, "q4_0", 11)
+    q, planes = make(2, 4, 2, 1400, 64, 1, "q4_0", 11)
     o, lse = kv.decode(q[:, :, :0].contiguous(), *planes)
     assert o.shape == (2, 4, 0, 64) and lse.shape == (2, 4, 0)
     want = kv.decode(q, *planes)
