@@ -23,11 +23,11 @@
 // subtraction, exact, on the other pipe.
 //
 // Split: the tiles of 32 keys of all sequences and heads are one list, cut into equal slices, one for
-// each block that the SMs hold at a time; a slice holds the end of one head, whole heads and the
-// beginning of another. A block's warps take tiles in turn, each through its own ring of shared memory
-// (cp.async, no block barriers) with its own running maximum, and are joined in shared memory at the
-// end of a head; heads that several blocks share are joined by a second kernel. Where every head is a
-// few tiles long a block takes one head, and there is no second kernel.
+// each block that the SMs hold at a time, and those into one run of tiles for each warp: the end of one
+// head, whole heads and the beginning of another. A warp walks its run through its own ring of shared
+// memory (cp.async) with its own running maximum and waits for no other; heads that it shares with its
+// block's other warps are joined when all are done, those that blocks share by a second kernel. Where
+// every head is a few tiles long a block takes one head, and there is no second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,6 +49,10 @@ constexpr int kTile = 32;         // keys a warp takes at a time
 constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Masks of the low and the high nibbles of bytes 0 and 2. They come as kernel arguments: (x & mask) | one is a
+// single instruction with one constant known to the compiler, and two instructions with two.
+struct Masks { uint32_t low, high; };
+
 struct DecodeArgs {
   CacheView c;
   const __nv_bfloat16* q;
@@ -58,11 +62,14 @@ struct DecodeArgs {
   // slices only: what blocks leave of heads that they share, two slots a block, and the list
   float* part_o;         // [row blocks, blocks, 2, rows, D]: unnormalised
   float2* part_ml;       // [row blocks, blocks, 2, rows]: what the weights are relative to (base 2), and their sum
+  float* warp_o;         // what a warp leaves of a head that ends inside its run: as part_o, [row blocks, blocks, warps, rows, D]
+  float2* warp_ml;
   int* list;             // [B + 1]: tiles before sequence b, per key/value head
   unsigned* status;
   float scale2;          // scale * log2(e)
   int Hq, Sq, window, layout;
   int G, R;              // query heads and rows of a key/value head
+  Masks masks;
 };
 
 // The keys a sequence's queries may see: [lo, len), lo on a tile's border.
@@ -171,12 +178,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // Fp16 operands from the packed words of a block. 4 bits, one word: the numbers of bytes (0, 2) and
 // (1, 3), first those of the low nibbles, then of the high ones.
-__device__ __forceinline__ void pairs_q4(uint32_t w, uint32_t (&f)[4]) {
+__device__ __forceinline__ void pairs_q4(uint32_t w, Masks m, uint32_t (&f)[4]) {
   const uint32_t h = w >> 8;
-  f[0] = sub_f16<0x6408>((w & 0x000f000fu) | 0x64006400u);   // 1024 + b - 1032
-  f[1] = sub_f16<0x6408>((h & 0x000f000fu) | 0x64006400u);
-  f[2] = sub_f16<0x5480>((w & 0x00f000f0u) | 0x54005400u);   // 64 + b - 72
-  f[3] = sub_f16<0x5480>((h & 0x00f000f0u) | 0x54005400u);
+  f[0] = sub_f16<0x6408>((w & m.low) | 0x64006400u);   // 1024 + b - 1032
+  f[1] = sub_f16<0x6408>((h & m.low) | 0x64006400u);
+  f[2] = sub_f16<0x5480>((w & m.high) | 0x54005400u);   // 64 + b - 72
+  f[3] = sub_f16<0x5480>((h & m.high) | 0x54005400u);
 }
 // 8 bits, one word of each half block: bytes (A, B) and (C, D) of the first, then of the second.
 template <int A, int B, int C, int D>
@@ -228,7 +235,7 @@ __device__ __forceinline__ uint32_t load_scales(uint32_t at, float (&d)[NB]) {
 // (kernels of the widest rows, 128 features in 8 bits, take smaller blocks to fill it).
 constexpr int warps_of(int D, bool q4) { return D == 128 && !q4 ? 4 : 8; }
 constexpr int held_of(int D, bool q4, int nt) {
-  return D == 128 ? (q4 ? (nt == 1 ? 2 : 1) : (nt == 1 ? 3 : 2)) : (q4 && nt == 1 ? 3 : 2);
+  return D == 128 && !q4 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1);
 }
 
 // Slices of the list of `total` tiles over n blocks: where slice i begins, and the slice of a tile.
@@ -268,38 +275,64 @@ __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool r
   __syncthreads();
 }
 
+// Row r of a head from a warp's sums (D / 32 features a lane): the result, or what is left of it.
+template <int D>
+__device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int r, const float (&o)[D / 32], float l,
+                                          float top, bool whole, float* part_o, float2* part_ml) {
+  constexpr int F = D / 32;
+  const int lane = threadIdx.x & 31;
+  if (!whole) {
+#pragma unroll
+    for (int j = 0; j < F; ++j) part_o[lane * F + j] = o[j];
+    if (lane == 0) *part_ml = make_float2(top, l);
+    return;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + q_offset(a, b, h, r) + lane * F);
+#pragma unroll
+  for (int j = 0; j < F; j += 2) dst[j / 2] = tc::pack_bf16x2(o[j] * inv, o[j + 1] * inv);
+  if (lane == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : (top + log2f(l)) * kLn2;
+}
+
 // A block's work: SLICES: slice blockIdx.x of the list; else the head blockIdx.x. NT * 8 query rows from
 // blockIdx.y * NT * 8 on.
 template <int D, bool Q4, int NT, bool SLICES>
 __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) decode_kernel(DecodeArgs a) {
   using S = Slot<D, Q4>;
-  constexpr int NB = S::NB, kWarps = warps_of(D, Q4);
+  constexpr int NB = S::NB, kWarps = warps_of(D, Q4), ROWS = NT * 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int list[SLICES ? kMaxListed + 1 : 1];
+  // the heads whose sums the block's warps leave unfinished, in the order of their tiles: two for each
+  // warp, the one its run begins in and the one it ends in (-1: none), and how many tiles they had
+  __shared__ int left_head[2 * kWarps], left_tiles[2 * kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int r0 = blockIdx.y * NT * 8;
+  const int r0 = blockIdx.y * ROWS;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::STAGES * S::BYTES);
   const bool report = r0 == 0 && (!SLICES || blockIdx.x == 0);
   // the matrix row that this lane names: key `lane` of a tile
   const uint32_t mrow = lane * S::ROW;
   const int mperm = S::permuted(lane);
+  const Masks masks = a.masks;
 
-  // Tiles [first_tile, first_tile + tiles) of one head: the sums go to o and lse when `whole`, else to slot `part`.
-  auto head_part = [&](int b, int h, const Range kr, int first_tile, int tiles, bool whole, int part) {
+  float acc[NT][2 * NB][4];   // rows: features 16 i + 2 g (and + 1); columns: query rows 2 t, 2 t + 1
+  float base[NT][2];          // weights are 2^(score - base), base = largest score - level
+  float sum[NT][2];           // of this lane's weights
+
+  // The sums over tiles [first_tile, first_tile + tiles) of one head.
+  auto run = [&](int b, int h, const Range kr, int first_tile, int tiles) {
     const int k0 = kr.lo + first_tile * kTile;
-    const size_t plane = ((size_t)b * a.c.Hkv + h) * a.c.S;
     // lane's part of a tile's loads: pieces lane, lane + 32, ... of the numbers, key `lane`'s scales
     const unsigned lrow = (unsigned)lane / S::PIECES;
     const int lpiece = lane % S::PIECES;
-    auto load = [&](int tile, int slot) {
-      const int first = k0 + tile * kTile;
-      const uint32_t at = ring + slot * S::BYTES;
-      const size_t src = (plane + first) * S::ROW + 16 * lane;
-      const uint8_t* kq = static_cast<const uint8_t*>(a.c.k_q) + src;
-      const uint8_t* vq = static_cast<const uint8_t*>(a.c.v_q) + src;
-      const size_t sc = (plane + first + lane) * NB;
-      if (first + kTile <= kr.len) {
+    const size_t begin = ((size_t)b * a.c.Hkv + h) * a.c.S + k0;
+    const uint8_t* kq = static_cast<const uint8_t*>(a.c.k_q) + begin * S::ROW + 16 * lane;
+    const uint8_t* vq = static_cast<const uint8_t*>(a.c.v_q) + begin * S::ROW + 16 * lane;
+    const uint16_t* kd = a.c.k_d + (begin + lane) * NB;
+    const uint16_t* vd = a.c.v_d + (begin + lane) * NB;
+    int loaded = k0;   // the first key of the next tile to load
+    auto load = [&](uint32_t at) {
+      if (loaded + kTile <= kr.len) {
 #pragma unroll
         for (int i = 0; i < S::PIECES; ++i) {
           const unsigned row = lrow + i * (32 / S::PIECES);
@@ -307,28 +340,32 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
           cp_async16(dst, kq + 512 * i);
           cp_async16(dst + S::V_OFF, vq + 512 * i);
         }
-        cp_async_small<S::SC>(at + S::KD_OFF + lane * S::SC, a.c.k_d + sc);
-        cp_async_small<S::SC>(at + S::VD_OFF + lane * S::SC, a.c.v_d + sc);
-        return;
-      }
-      // the last tile: keys past the end are zeros, and not read
+        cp_async_small<S::SC>(at + S::KD_OFF + lane * S::SC, kd);
+        cp_async_small<S::SC>(at + S::VD_OFF + lane * S::SC, vd);
+      } else {   // the last tile: keys past the end are zeros, and not read
 #pragma unroll
-      for (int i = 0; i < S::PIECES; ++i) {
-        const unsigned row = lrow + i * (32 / S::PIECES);
-        const uint32_t dst = at + row * S::ROW + 16 * (lpiece ^ S::permuted(row));
-        const bool on = first + (int)row < kr.len;
-        cp_async16_if(dst, on ? kq + 512 * i : static_cast<const uint8_t*>(a.c.k_q), on);
-        cp_async16_if(dst + S::V_OFF, on ? vq + 512 * i : static_cast<const uint8_t*>(a.c.v_q), on);
+        for (int i = 0; i < S::PIECES; ++i) {
+          const unsigned row = lrow + i * (32 / S::PIECES);
+          const uint32_t dst = at + row * S::ROW + 16 * (lpiece ^ S::permuted(row));
+          const bool on = loaded + (int)row < kr.len;
+          cp_async16_if(dst, on ? kq + 512 * i : static_cast<const uint8_t*>(a.c.k_q), on);
+          cp_async16_if(dst + S::V_OFF, on ? vq + 512 * i : static_cast<const uint8_t*>(a.c.v_q), on);
+        }
+        const bool on = loaded + lane < kr.len;
+        cp_async_small_if<S::SC>(at + S::KD_OFF + lane * S::SC, on ? kd : a.c.k_d, on);
+        cp_async_small_if<S::SC>(at + S::VD_OFF + lane * S::SC, on ? vd : a.c.v_d, on);
       }
-      const bool on = first + lane < kr.len;
-      cp_async_small_if<S::SC>(at + S::KD_OFF + lane * S::SC, on ? a.c.k_d + sc : a.c.k_d, on);
-      cp_async_small_if<S::SC>(at + S::VD_OFF + lane * S::SC, on ? a.c.v_d + sc : a.c.v_d, on);
+      loaded += kTile;
+      kq += kTile * S::ROW;
+      vq += kTile * S::ROW;
+      kd += kTile * NB;
+      vd += kTile * NB;
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
 #pragma unroll
     for (int i = 0; i < S::STAGES - 1; ++i) {
-      if (warp + i * kWarps < tiles) load(warp + i * kWarps, i);
+      if (i < tiles) load(ring + i * S::BYTES);
       commit();
     }
 
@@ -372,10 +409,7 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
       unscale[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
 
-    float acc[NT][2 * NB][4];   // rows: features 16 i + 2 g (and + 1); columns: query rows 2 t, 2 t + 1
     float mx[NT][2];            // largest product seen
-    float base[NT][2];          // weights are 2^(score - base), base = largest score - level
-    float sum[NT][2];           // of this lane's weights
     uint32_t fields[NT][2];     // exponent fields (at bit 10) of the V scales of all keys seen, or-ed
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -405,7 +439,7 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
           uint32_t w[4];
           load_matrices<false>(at + mrow + 16 * (k ^ mperm), w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pairs_q4(w[i], f[i]);
+          for (int i = 0; i < 4; ++i) pairs_q4(w[i], masks, f[i]);
         } else {
           uint32_t w[4], x[4];
           load_matrices<false>(at + mrow + 16 * ((2 * k) ^ mperm), w);
@@ -512,7 +546,7 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
           uint32_t x[4];
           load_matrices<true>(at + S::V_OFF + mrow + 16 * (k ^ mperm), x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pairs_q4(x[i], f[i]);
+          for (int i = 0; i < 4; ++i) pairs_q4(x[i], masks, f[i]);
         } else {
           uint32_t x[4], y[4];
           load_matrices<true>(at + S::V_OFF + mrow + 16 * ((2 * k) ^ mperm), x);
@@ -539,12 +573,9 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
     };
 
     int slot = 0;
-    for (int tile = warp; tile < tiles; tile += kWarps) {
-      {
-        const int next = tile + (S::STAGES - 1) * kWarps;
-        if (next < tiles) load(next, slot == 0 ? S::STAGES - 1 : slot - 1);
-        commit();
-      }
+    for (int tile = 0; tile < tiles; ++tile) {
+      if (tile + S::STAGES - 1 < tiles) load(ring + (slot == 0 ? S::STAGES - 1 : slot - 1) * S::BYTES);
+      commit();
       asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
       __syncwarp();
       const uint32_t at = ring + slot * S::BYTES;
@@ -554,73 +585,70 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
       __syncwarp();   // the slot is read: the next load into it may begin
       slot = slot == S::STAGES - 1 ? 0 : slot + 1;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-
-    // join the block's warps: [warp][query row][D], and what their weights are relative to and their sums
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);
-    float2* sml = reinterpret_cast<float2*>(smem + kWarps * NT * 8 * D * 4);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float l = sum[n][j];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const int col = n * 8 + 2 * t + j;
-        if (g == 0) sml[warp * NT * 8 + col] = make_float2(base[n][j], l);
-        float* row = so + (warp * NT * 8 + col) * D;
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i)
-          *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(acc[n][i][j], acc[n][i][j + 2]);
+        sum[n][j] += __shfl_xor_sync(0xffffffffu, sum[n][j], 4);
+        sum[n][j] += __shfl_xor_sync(0xffffffffu, sum[n][j], 8);
+        sum[n][j] += __shfl_xor_sync(0xffffffffu, sum[n][j], 16);
       }
-    __syncthreads();
-    constexpr int PER = D / 4;   // threads of a row
-    for (int i = threadIdx.x; i < NT * 8 * PER; i += kWarps * 32) {
-      const int col = i / PER, f = i % PER * 4, r = r0 + col;
-      if (r >= a.R) continue;
-      float top = -CUDART_INF_F;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * NT * 8 + col].x);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = sml[w * NT * 8 + col];
-        const float k = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
-        const float4 x = *reinterpret_cast<const float4*>(so + (w * NT * 8 + col) * D + f);
-        l = fmaf(k, ml.y, l);
-        o.x = fmaf(k, x.x, o.x);
-        o.y = fmaf(k, x.y, o.y);
-        o.z = fmaf(k, x.z, o.z);
-        o.w = fmaf(k, x.w, o.w);
-      }
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(a.o + q_offset(a, b, h, r) + f) =
-            make_uint2(tc::pack_bf16x2(o.x * inv, o.y * inv), tc::pack_bf16x2(o.z * inv, o.w * inv));
-        if (f == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : (top + log2f(l)) * kLn2;
-      } else {
-        const size_t at = (((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 + part) * (NT * 8) + col;
-        *reinterpret_cast<float4*>(a.part_o + at * D + f) = o;
-        if (f == 0) a.part_ml[at] = make_float2(top, l);
-      }
-    }
-    __syncthreads();   // the ring is free for the next head
   };
 
+  // The sums of the last run as they are, rows of D.
+  auto put = [&](float* o, float2* ml) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = n * 8 + 2 * t + j;
+        if (g == 0) ml[col] = make_float2(base[n][j], sum[n][j]);
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i)
+          *reinterpret_cast<float2*>(o + col * D + 16 * i + 2 * g) = make_float2(acc[n][i][j], acc[n][i][j + 2]);
+      }
+  };
+  // ... as the result of a head.
+  auto finish = [&](int b, int h) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = r0 + n * 8 + 2 * t + j;
+        if (r >= a.R) continue;
+        const float l = sum[n][j], inv = l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat16* o = a.o + q_offset(a, b, h, r) + 2 * g;
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i)
+          *reinterpret_cast<uint32_t*>(o + 16 * i) = tc::pack_bf16x2(acc[n][i][j] * inv, acc[n][i][j + 2] * inv);
+        if (g == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : (base[n][j] + log2f(l)) * kLn2;
+      }
+  };
+
+  float* so = reinterpret_cast<float*>(smem);   // [warp][rows][D], once every warp is done with its ring
+  float2* sml = reinterpret_cast<float2*>(smem + kWarps * ROWS * D * 4);
+  const size_t block = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (lane < 2) left_head[2 * warp + lane] = -1;
+  __syncwarp();
+
+  long long slice = 0;   // the first tile of the block
+  bool keep = false;     // the last run is of a head that is left to the block
   if constexpr (!SLICES) {
     const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
     const Range kr = key_range(a, b, report && h == 0 && threadIdx.x == 0);
-    head_part(b, h, kr, 0, (kr.len - kr.lo + kTile - 1) / kTile, true, 0);
+    const int n = (kr.len - kr.lo + kTile - 1) / kTile, first = n * warp / kWarps;
+    run(b, h, kr, first, n * (warp + 1) / kWarps - first);
+    keep = true;
+    if (lane == 0) left_head[2 * warp + 1] = blockIdx.x;
   } else {
     make_list(a, list, report);
     if (report)   // for the joining kernel
       for (int i = threadIdx.x; i <= a.c.B; i += kWarps * 32) a.list[i] = list[i];
     const long long total = (long long)list[a.c.B] * a.c.Hkv;
-    long long at = slice_begin(blockIdx.x, total, gridDim.x);
-    const long long begin = at, end = slice_begin(blockIdx.x + 1, total, gridDim.x);
+    slice = slice_begin(blockIdx.x, total, gridDim.x);
+    const int tiles = (int)(slice_begin(blockIdx.x + 1, total, gridDim.x) - slice);
+    long long at = slice + (long long)tiles * warp / kWarps;
+    const long long end = slice + (long long)tiles * (warp + 1) / kWarps;
     while (at < end) {
       int b = 0, last = a.c.B - 1;   // the last sequence that begins at or before tile `at`
       while (b < last) {
@@ -632,68 +660,145 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
       const long long off = at - (long long)list[b] * a.c.Hkv;
       const int h = (int)(off / n), tile = (int)(off % n);
       const int take = (int)min((long long)(n - tile), end - at);
-      head_part(b, h, key_range(a, b, false), tile, take, take == n, at != begin);
+      run(b, h, key_range(a, b, false), tile, take);
       at += take;
+      if (take == n) {
+        finish(b, h);
+        continue;
+      }
+      keep = at == end;   // the run's last head stays in registers; its first goes to memory
+      if (lane == 0) {
+        left_head[2 * warp + keep] = b * a.c.Hkv + h;
+        left_tiles[2 * warp + keep] = take;
+      }
+      if (!keep) put(a.warp_o + (block * kWarps + warp) * ROWS * D, a.warp_ml + (block * kWarps + warp) * ROWS);
     }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  if (keep) put(so + warp * ROWS * D, sml + warp * ROWS);
+  __syncthreads();
+
+  // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k, which is of warp
+  // k / 2 (the head its run begins in, in memory, and the one it ends in, in shared memory).
+  const int my_head = lane < 2 * kWarps ? left_head[lane] : -1;
+  const int my_tiles = SLICES && my_head >= 0 ? left_tiles[lane] : 0;
+  const int rows = min(ROWS, a.R - r0);
+  int unit = warp;   // counts down the rows until this warp's next one
+  for (uint32_t rest = __ballot_sync(0xffffffffu, my_head >= 0); rest != 0;) {
+    const int head = __shfl_sync(0xffffffffu, my_head, __ffs(rest) - 1);
+    const bool mine = my_head == head;
+    const uint32_t parts = __ballot_sync(0xffffffffu, mine);
+    rest &= ~parts;
+    const int b = head / a.c.Hkv, h = head % a.c.Hkv;
+    bool whole = true;
+    int part = 0;
+    if constexpr (SLICES) {
+      const int n = list[b + 1] - list[b];
+      whole = __reduce_add_sync(0xffffffffu, mine ? my_tiles : 0) == n;
+      part = (long long)list[b] * a.c.Hkv + (long long)h * n > slice;   // it begins inside the slice
+    }
+    for (; unit < rows; unit += kWarps) {
+      const int col = unit, r = r0 + col;
+      float2 ml = make_float2(-CUDART_INF_F, 0.f);
+      if (mine) ml = (SLICES && !(lane & 1)) ? a.warp_ml[(block * kWarps + lane / 2) * ROWS + col] : sml[lane / 2 * ROWS + col];
+      const float top = warp_max(ml.x);
+      const float w = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
+      const float l = warp_sum(w * ml.y);
+      float o[D / 32];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
+#pragma unroll 1
+      for (uint32_t m = parts; m != 0; m &= m - 1) {
+        const int k = __ffs(m) - 1;
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float* src = k & 1 ? so + k / 2 * ROWS * D : a.warp_o + (block * kWarps + k / 2) * ROWS * D;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) o[j] = fmaf(wk, src[col * D + lane * (D / 32) + j], o[j]);
+      }
+      store_row<D>(a, b, h, r, o, l, top, whole, a.part_o + (block * 2 + part) * ROWS * D + col * D,
+                   a.part_ml + (block * 2 + part) * ROWS + col);
+    }
+    unit -= rows;
   }
 }
 
-// Joins what several blocks left of one query row's head: the warps of a block take the parts in turn, and are
-// joined in order. A head that one block had is finished; one without keys is zeros.
-template <int D>
-__global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int blocks, int rows_per) {
+// Joins what several blocks left of one query row's head: the row's warps take the parts in turn, and are joined in
+// order. A head that one block had is finished; one without keys is zeros.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int blocks, int rows_per, long long all_rows) {
   constexpr int F = D / 32;
   __shared__ float so[8][D];
   __shared__ float2 sml[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS;
+  const long long row = blockIdx.x * (8LL / WARPS) + (threadIdx.x >> 5) / WARPS;
+  if (row >= all_rows) return;
   const int i = (int)(row % a.Sq), head = (int)(row / a.Sq % a.Hq), b = (int)(row / a.Sq / a.Hq);
   const int h = head / a.G, r = head % a.G * a.Sq + i;   // row of the key/value head
   const long long total = (long long)a.list[a.c.B] * a.c.Hkv;
   const int n = a.list[b + 1] - a.list[b];
-  const long long begin = (long long)a.list[b] * a.c.Hkv + (long long)h * n, end = begin + n;
-  const int c0 = n > 0 ? slice_of(begin, total, blocks) : 0, c1 = n > 0 ? slice_of(end - 1, total, blocks) : 0;
-  if (n > 0 && c0 == c1) return;
-  const int first_part = slice_begin(c0, total, blocks) != begin;   // of c0: its first head's, or its last's
+  const long long begin = (long long)a.list[b] * a.c.Hkv + (long long)h * n;
+  int c0 = 0, c1 = -1, first_part = 0;
+  if (n > 0) {
+    c0 = slice_of(begin, total, blocks);
+    c1 = slice_of(begin + n - 1, total, blocks);
+    if (c0 == c1) return;
+    first_part = slice_begin(c0, total, blocks) != begin;   // of c0: the head its slice begins in, or ends in
+  }
+  const size_t parts = (size_t)(r / rows_per) * blocks;
   float top = -CUDART_INF_F, l = 0.f, o[F];
 #pragma unroll
   for (int j = 0; j < F; ++j) o[j] = 0.f;
-  if (n > 0)
-    for (int c = c0 + warp; c <= c1; c += 8) {
-      if (slice_begin(c, total, blocks) == slice_begin(c + 1, total, blocks)) continue;   // more blocks than tiles
-      const size_t at = (((size_t)(r / rows_per) * blocks + c) * 2 + (c == c0 ? first_part : 0)) * rows_per + r % rows_per;
-      const float2 ml = a.part_ml[at];
-      const float now = fmaxf(top, ml.x), k0 = exp2_fast(top - now), k1 = exp2_fast(ml.x - now);
-      top = now;
-      l = l * k0 + ml.y * k1;
+  for (int c = c0 + warp; c <= c1; c += 32 * WARPS) {   // 32 parts at a time, one of them for each lane to look at
+    const int mine = c + lane * WARPS;
+    const size_t at = ((parts + mine) * 2 + (mine == c0 ? first_part : 0)) * rows_per + r % rows_per;
+    float2 ml = make_float2(-CUDART_INF_F, 0.f);
+    // with more blocks than tiles some have none
+    const bool on = mine <= c1 && slice_begin(mine, total, blocks) != slice_begin(mine + 1, total, blocks);
+    if (on) ml = a.part_ml[at];
+    const float now = fmaxf(top, warp_max(ml.x)), back = top == -CUDART_INF_F ? 0.f : exp2_fast(top - now);
+    const float w = on ? exp2_fast(ml.x - now) : 0.f;
+    top = now;
+    l = l * back + warp_sum(w * ml.y);
 #pragma unroll
-      for (int j = 0; j < F; ++j) o[j] = o[j] * k0 + a.part_o[at * D + lane * F + j] * k1;
+    for (int j = 0; j < F; ++j) o[j] *= back;
+    const int count = min(32, (c1 - c) / WARPS + 1);
+#pragma unroll 8
+    for (int k = 0; k < count; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const size_t from = __shfl_sync(0xffffffffu, at, k);
+      if (!__shfl_sync(0xffffffffu, (int)on, k)) continue;
+#pragma unroll
+      for (int j = 0; j < F; ++j) o[j] = fmaf(wk, a.part_o[from * D + lane * F + j], o[j]);
     }
-  if (lane == 0) sml[warp] = make_float2(top, l);
-#pragma unroll
-  for (int j = 0; j < F; ++j) so[warp][lane * F + j] = o[j];
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  top = -CUDART_INF_F;
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, sml[w].x);
-  l = 0.f;
-  float x = 0.f;
-  for (int w = 0; w < 8; ++w) {
-    if (sml[w].x == -CUDART_INF_F) continue;   // a warp without a part
-    const float k = exp2_fast(sml[w].x - top);
-    l = fmaf(k, sml[w].y, l);
-    x = fmaf(k, so[w][threadIdx.x], x);
   }
-  const size_t at = (a.layout ? ((size_t)b * a.Sq + i) * a.Hq + head : (size_t)row) * D;
-  a.o[at + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-  if (threadIdx.x == 0) a.lse[row] = l == 0.f ? 0.f : (top + log2f(l)) * kLn2;
+  if constexpr (WARPS > 1) {
+    if (lane == 0) sml[warp] = make_float2(top, l);
+#pragma unroll
+    for (int j = 0; j < F; ++j) so[warp][lane * F + j] = o[j];
+    __syncthreads();
+    if (warp != 0) return;
+    const float2 ml = lane < WARPS ? sml[lane] : make_float2(-CUDART_INF_F, 0.f);
+    top = warp_max(ml.x);
+    const float w = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a part
+    l = warp_sum(w * ml.y);
+#pragma unroll
+    for (int j = 0; j < F; ++j) o[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+      for (int j = 0; j < F; ++j) o[j] = fmaf(wk, so[k][lane * F + j], o[j]);
+    }
+  }
+  store_row<D>(a, b, h, r, o, l, top, true, nullptr, nullptr);
 }
 
 struct DecodePlan {
   int nt, row_blocks;
   bool slices;
   long long blocks;
-  size_t ml_off, list_off, total;
+  size_t part_ml, warp_o, warp_ml, list, total;   // offsets in the workspace; part_o is at 0
 };
 
 DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
@@ -715,10 +820,12 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
     const long long all = (long long)held_of(c.D, c.q4, d.nt) * sm_count() / d.row_blocks, some = heads * tiles / warps;
     d.blocks = all < some ? all : some;
     if (d.blocks < 1) d.blocks = 1;
-    const size_t rows = (size_t)d.row_blocks * d.blocks * 2 * d.nt * 8;
-    d.ml_off = align_up(rows * c.D * 4);
-    d.list_off = d.ml_off + align_up(rows * 8);
-    d.total = d.list_off + align_up(((size_t)c.B + 1) * 4);
+    const size_t rows = (size_t)d.row_blocks * d.blocks * d.nt * 8;
+    d.part_ml = align_up(2 * rows * c.D * 4);
+    d.warp_o = d.part_ml + align_up(2 * rows * 8);
+    d.warp_ml = d.warp_o + align_up(warps * rows * c.D * 4);
+    d.list = d.warp_ml + align_up(warps * rows * 8);
+    d.total = d.list + align_up(((size_t)c.B + 1) * 4);
   }
   return d;
 }
@@ -792,8 +899,11 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   a.lengths = lengths;
   a.part_o = static_cast<float*>(ws);
   if (plan.slices) {
-    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + plan.ml_off);
-    a.list = reinterpret_cast<int*>(static_cast<char*>(ws) + plan.list_off);
+    char* w = static_cast<char*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(w + plan.part_ml);
+    a.warp_o = reinterpret_cast<float*>(w + plan.warp_o);
+    a.warp_ml = reinterpret_cast<float2*>(w + plan.warp_ml);
+    a.list = reinterpret_cast<int*>(w + plan.list);
   }
   a.status = device_status_ptr();
   a.scale2 = p->scale * 1.4426950408889634f;
@@ -801,6 +911,7 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   a.Sq = p->Sq;
   a.window = p->window;
   a.layout = p->layout;
+  a.masks = Masks{0x000f000fu, 0x00f000f0u};
   a.G = p->Hq / cv.Hkv;
   a.R = a.G * p->Sq;
   if (plan.row_blocks > 65535 || plan.blocks > 0x7fffffffLL || rows > 0x7fffffffULL) { set_error("too many query rows for one launch"); return FA_ERR_UNSUPPORTED; }
@@ -818,9 +929,13 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   if (cv.q4) e = cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
   else e = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
   if (e == cudaSuccess && plan.slices) {
+    // a warp for a row where blocks have heads enough that one is in two or three parts, else a block of eight
     const int blocks = (int)plan.blocks, per = plan.nt * 8;
-    if (cv.D == 64) decode_join_kernel<64><<<(unsigned)rows, 256, 0, cs>>>(a, blocks, per);
-    else decode_join_kernel<128><<<(unsigned)rows, 256, 0, cs>>>(a, blocks, per);
+    const bool few = (long long)cv.B * cv.Hkv * 4 >= plan.blocks;
+    const unsigned n = (unsigned)(few ? (rows + 7) / 8 : rows);
+    auto join = cv.D == 64 ? (few ? decode_join_kernel<64, 1> : decode_join_kernel<64, 8>)
+                           : (few ? decode_join_kernel<128, 1> : decode_join_kernel<128, 8>);
+    join<<<n, 256, 0, cs>>>(a, blocks, per, (long long)rows);
     count_launches(1);
     e = cudaGetLastError();
   }
