@@ -2,11 +2,13 @@
 // (fa_qk_norm_rope, fa_qk_norm_rope_bwd): what turns a projection's output into the q and k of the
 // attention entry points, and their gradients back into the projection's.
 //
-// Work: a row (one head of one token) is read once and written once, bound by HBM. D / 8 lanes hold
-// it, each with the two runs of four features that form four rotated pairs, so that a rotation never
-// leaves a lane: features 4 l .. and rot / 2 + 4 l .. for pairs (i, i + rot / 2), and 8 l .. 8 l + 7
-// for interleaved pairs and for the features that are not rotated. Such a group of lanes stays with
-// one token for several heads, which share the token's cosines and sines.
+// Work: a row (one head of one token) is read once and written once, bound by HBM. D / (2 E) lanes hold
+// it, each with the two runs of E features that form E rotated pairs, so that a rotation never leaves a
+// lane: features E l .. and rot / 2 + E l .. for pairs (i, i + rot / 2), and 2 E l .. for interleaved
+// pairs and for the features that are not rotated. E is 8 in a long bf16 forward (see run_of), else 4. Such a group of lanes stays with one token for several heads, which share the token's cosines
+// and sines. The next heads' rows are on their way to a ring in shared memory meanwhile, each lane's bytes
+// in slots of its own (cp.async; nothing to wait for but one's own copies): held in registers they would
+// cost the occupancy that hides their latency.
 //
 // Angles: t = p * f for whole positions p. In turns, f / 2 pi is a fixed-point fraction F of 64 bits
 // and p * F modulo 2^64 is the angle modulo a turn, without any rounding that grows with p.
@@ -44,23 +46,62 @@ struct RopeArgs {
   float* dw;            // backward: partial weight gradients [2][blocks][D]
 };
 
-__device__ __forceinline__ void load4(const float* p, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* x) {
-  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
-  x[0] = __uint_as_float(a.x << 16);
-  x[1] = __uint_as_float(a.x & 0xffff0000u);
-  x[2] = __uint_as_float(a.y << 16);
-  x[3] = __uint_as_float(a.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]));
-}
+// E consecutive features as they are in memory, their values, and back.
+template <typename T, int E>
+struct Run {
+  static constexpr int BYTES = E * sizeof(T), UNIT = BYTES < 16 ? BYTES : 16, UNITS = BYTES / UNIT;
+  uint32_t u[BYTES / 4];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 8; ++i) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p) + i);
+      u[2 * i] = a.x; u[2 * i + 1] = a.y;
+    }
+  }
+  // The run's units are 256 * UNIT bytes apart in shared memory, the threads' side by side.
+  __device__ __forceinline__ static void copy(uint32_t slot, const T* p) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      const char* src = reinterpret_cast<const char*>(p) + i * UNIT;
+      if constexpr (UNIT == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + i * 256 * UNIT), "l"(src) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot + i * 256 * UNIT), "l"(src) : "memory");
+    }
+  }
+  __device__ __forceinline__ void fetch(uint32_t slot) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      uint32_t* v = u + i * UNIT / 4;
+      if constexpr (UNIT == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(slot + i * 256 * UNIT) : "memory");
+      else
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(slot + i * 256 * UNIT) : "memory");
+    }
+  }
+  __device__ __forceinline__ void values(float* x) const {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(u[i]);
+      else x[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, const float* x) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i) {
+      if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(x[i]);
+      else u[i] = tc::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    }
+    if constexpr (UNIT == 16) {
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+    } else {
+      *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    }
+  }
+};
 
 // f / 2 pi as a 64-bit fraction of a turn (whole turns dropped): f = m 2^e with a 24-bit m, and
 // m * floor(2^66 / 2 pi) shifted to the binary point. Off by at most 2^-64 turns.
@@ -86,184 +127,278 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 // What a lane of a token's group needs: where its two runs of features are, and its angles.
-template <int D>
+template <int E, bool INTER>
 struct Lane {
   int c0, c1;
   bool turns;
-  float cs[4], sn[4];
+  float cs[E], sn[E];
 
-  __device__ __forceinline__ Lane(const RopeArgs& a, int l, long long b, int s) {
-    const RopeShape& r = a.s;
-    turns = 4 * l < r.half;
-    c0 = turns && !r.interleaved ? 4 * l : 8 * l;
-    c1 = turns && !r.interleaved ? r.half + 4 * l : 8 * l + 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) { cs[j] = 1.f; sn[j] = 0.f; }
+  __device__ __forceinline__ Lane(const RopeArgs& a, int l) {
+    turns = E * l < a.s.half;
+    c0 = turns && !INTER ? E * l : 2 * E * l;
+    c1 = turns && !INTER ? a.s.half + E * l : 2 * E * l + E;
+  }
+  __device__ __forceinline__ void angles(const RopeArgs& a, int l, long long b, int s) {
     if (!turns) return;
+    const RopeShape& r = a.s;
     const long long p = a.positions != nullptr ? __ldg(a.positions + b * r.pos_stride_b + s) : r.offset + s;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned long long t = (unsigned long long)p * turn_fraction(__ldg(a.inv_freq + 4 * l + j));
-      float sine, cosine;   // the top 32 bits, signed: half turns of [-1, 1)
-      sincospif((float)(int)(t >> 32) * 4.6566128730773926e-10f, &sine, &cosine);
-      cs[j] = cosine * r.factor;
-      sn[j] = sine * r.factor;
+    for (int j = 0; j < E; ++j) {
+      const unsigned long long t = (unsigned long long)p * turn_fraction(__ldg(a.inv_freq + E * l + j));
+      // the top 32 bits, signed: half turns of [-1, 1)
+      sincospif((float)(int)(t >> 32) * 4.6566128730773926e-10f, &sn[j], &cs[j]);
+      cs[j] *= r.factor;
+      sn[j] *= r.factor;
     }
   }
 
-  // The four pairs are (x[2 j], x[2 j + 1]) when interleaved, (x[j], x[4 + j]) otherwise.
-  __device__ __forceinline__ void rotate(float (&x)[8], bool interleaved, float sign) const {
-    if (!turns) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float& u = interleaved ? x[2 * j] : x[j];
-      float& v = interleaved ? x[2 * j + 1] : x[4 + j];
-      const float s = sign * sn[j], p = u, q = v;
-      u = p * cs[j] - q * s;
-      v = q * cs[j] + p * s;
-    }
-  }
+  // The E pairs are (x[2 j], x[2 j + 1]) when interleaved, (x[j], x[E + j]) otherwise.
+  __device__ __forceinline__ static float& first(float (&x)[2 * E], int j) { return INTER ? x[2 * j] : x[j]; }
+  __device__ __forceinline__ static float& second(float (&x)[2 * E], int j) { return INTER ? x[2 * j + 1] : x[E + j]; }
 };
 
-template <typename T, typename W, int D, bool NORM>
+// Heads on their way for each lane, and the ring that holds them (n tensors).
+constexpr int kAhead = 4;
+template <typename T, int E>
+constexpr int ring_bytes(int n) { return kAhead * n * 2 * Run<T, E>::BYTES * 256; }
+
+template <typename T, typename W, int D, int E, bool INTER, bool NORM>
 __global__ void __launch_bounds__(256) rope_fwd_kernel(RopeArgs a) {
-  constexpr int LANES = D / 8, GROUPS = 256 / LANES;
+  using R = Run<T, E>;
+  using L = Lane<E, INTER>;
+  constexpr int LANES = D / (2 * E), GROUPS = 256 / LANES, STEP = 2 * R::BYTES * 256;
+  extern __shared__ __align__(16) uint8_t smem[];
   const int l = threadIdx.x % LANES;
   const long long token = (long long)blockIdx.x * GROUPS + threadIdx.x / LANES;
   const bool on = token < (long long)a.s.B * a.s.S;
   const int s = on ? (int)(token % a.s.S) : 0, b = on ? (int)(token / a.s.S) : 0;
   const int key = (int)blockIdx.y >= a.s.q_chunks;
-  const int H = key ? a.s.Hkv : a.s.Hq;
-  const int h0 = ((int)blockIdx.y - (key ? a.s.q_chunks : 0)) * a.s.chunk, h1 = min(H, h0 + a.s.chunk);
-  const Lane<D> lane(a, l, b, s);
-  const bool inter = a.s.interleaved != 0;
+  const int h0 = ((int)blockIdx.y - (key ? a.s.q_chunks : 0)) * a.s.chunk;
+  const int heads = min((key ? a.s.Hkv : a.s.Hq) - h0, a.s.chunk);
+  L lane(a, l);
   const RowView xv = key ? a.x[1] : a.x[0], yv = key ? a.y[1] : a.y[0];
-  const T* x0 = static_cast<const T*>(xv.ptr) + b * xv.sb + s * xv.ss;
-  T* y0 = static_cast<T*>(yv.ptr) + b * yv.sb + s * yv.ss;
-  float w[8];
-  if constexpr (NORM) {
-    const W* wp = static_cast<const W*>(key ? a.w[1] : a.w[0]);
-    load4(wp + lane.c0, w);
-    load4(wp + lane.c1, w + 4);
-  }
-  for (int h = h0; h < h1; ++h) {
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
-      load4(x0 + h * xv.sh + lane.c0, x);
-      load4(x0 + h * xv.sh + lane.c1, x + 4);
+  const T* x0 = static_cast<const T*>(xv.ptr) + b * xv.sb + s * xv.ss + h0 * xv.sh;
+  T* y0 = static_cast<T*>(yv.ptr) + b * yv.sb + s * yv.ss + h0 * yv.sh;
+  const uint32_t ring = tc::smem_u32(smem) + threadIdx.x * R::UNIT;
+  int asked = 0;
+  auto ask = [&](uint32_t slot) {   // a token past the end (which reads the first one's rows) is not written
+    if (asked < heads) {
+      R::copy(slot, x0 + lane.c0);
+      R::copy(slot + STEP / 2, x0 + lane.c1);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++asked;
+    x0 += xv.sh;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) ask(ring + i * STEP);
+  // What the pair (p, q) is multiplied by: u = p A - q B, v = q C + p S, with the weights in them.
+  float A[E], B[E], C[E], Sn[E];
+  {
+    float w[2 * E];
+#pragma unroll
+    for (int j = 0; j < 2 * E; ++j) w[j] = 1.f;
+    if constexpr (NORM) {
+      const W* wp = static_cast<const W*>(key ? a.w[1] : a.w[0]);
+      Run<W, E> run;
+      run.load(wp + lane.c0);
+      run.values(w);
+      run.load(wp + lane.c1);
+      run.values(w + E);
+    }
+    lane.angles(a, l, b, s);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float p = L::first(w, j), q = L::second(w, j);
+      A[j] = lane.turns ? p * lane.cs[j] : p;
+      C[j] = lane.turns ? q * lane.cs[j] : q;
+      B[j] = lane.turns ? q * lane.sn[j] : 0.f;
+      Sn[j] = lane.turns ? p * lane.sn[j] : 0.f;
+    }
+  }
+  unsigned slot = 0;
+  for (int h = 0; h < heads; ++h) {
+    ask(ring + (slot + kAhead - 1) % kAhead * STEP);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    float x[2 * E];
+    {
+      R in;
+      in.fetch(ring + slot * STEP);
+      in.values(x);
+      in.fetch(ring + slot * STEP + STEP / 2);
+      in.values(x + E);
+    }
+    slot = (slot + 1) % kAhead;
+    float r = 1.f;
     if constexpr (NORM) {
       float sq = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
-      const float r = rsqrtf(fmaf(group_sum<LANES>(sq), 1.f / D, a.s.eps));
+      for (int j = 0; j < 2 * E; ++j) sq = fmaf(x[j], x[j], sq);
+      r = rsqrtf(fmaf(group_sum<LANES>(sq), 1.f / D, a.s.eps));
+    }
+    if (lane.turns) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= r * w[j];
+      for (int j = 0; j < E; ++j) {
+        float &u = L::first(x, j), &v = L::second(x, j);
+        const float p = u, q = v;
+        u = fmaf(-q, B[j], p * A[j]);
+        v = fmaf(p, Sn[j], q * C[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        L::first(x, j) *= A[j];
+        L::second(x, j) *= C[j];
+      }
     }
-    if (inter) lane.rotate(x, true, 1.f);
-    else lane.rotate(x, false, 1.f);
+    if constexpr (NORM) {
+#pragma unroll
+      for (int j = 0; j < 2 * E; ++j) x[j] *= r;
+    }
     if (on) {
-      store4(y0 + h * yv.sh + lane.c0, x);
-      store4(y0 + h * yv.sh + lane.c1, x + 4);
+      R out;
+      out.store(y0 + lane.c0, x);
+      out.store(y0 + lane.c1, x + E);
     }
+    y0 += yv.sh;
   }
 }
 
 // As the forward, with the gradient of the output in and that of the input out. A block adds up its
 // rows' weight gradients in registers, then over its groups in shared memory, and writes one row of
 // partial sums, which rope_dw_kernel adds in block order.
-template <typename T, typename W, int D, bool NORM>
+template <typename T, typename W, int D, int E, bool INTER, bool NORM>
 __global__ void __launch_bounds__(256) rope_bwd_kernel(RopeArgs a) {
-  constexpr int LANES = D / 8, GROUPS = 256 / LANES;
+  using R = Run<T, E>;
+  using L = Lane<E, INTER>;
+  constexpr int LANES = D / (2 * E), GROUPS = 256 / LANES, STEP = (NORM ? 4 : 2) * R::BYTES * 256, RUN = R::BYTES * 256;
+  extern __shared__ __align__(16) uint8_t smem[];
   const int l = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const long long token = (long long)blockIdx.x * GROUPS + group;
+  const bool on = token < (long long)a.s.B * a.s.S;
+  const int s = on ? (int)(token % a.s.S) : 0, b = on ? (int)(token / a.s.S) : 0;
   const int key = (int)blockIdx.y >= a.s.q_chunks;
-  const int H = key ? a.s.Hkv : a.s.Hq;
-  const int h0 = ((int)blockIdx.y - (key ? a.s.q_chunks : 0)) * a.s.chunk, h1 = min(H, h0 + a.s.chunk);
-  const bool inter = a.s.interleaved != 0;
+  const int h0 = ((int)blockIdx.y - (key ? a.s.q_chunks : 0)) * a.s.chunk;
+  const int heads = min((key ? a.s.Hkv : a.s.Hq) - h0, a.s.chunk);
+  L lane(a, l);
   const RowView xv = key ? a.x[1] : a.x[0], yv = key ? a.y[1] : a.y[0], gv = key ? a.g[1] : a.g[0];
-  const long long tokens = (long long)a.s.B * a.s.S;
-  float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  int c0 = 0, c1 = 0;
-  for (long long t0 = (long long)blockIdx.x * GROUPS; t0 < tokens; t0 += (long long)gridDim.x * GROUPS) {
-    const long long token = t0 + group;
-    const bool on = token < tokens;
-    const int s = on ? (int)(token % a.s.S) : 0, b = on ? (int)(token / a.s.S) : 0;
-    const Lane<D> lane(a, l, b, s);
-    c0 = lane.c0;
-    c1 = lane.c1;
-    const T* x0 = static_cast<const T*>(xv.ptr) + b * xv.sb + s * xv.ss;
-    const T* g0 = static_cast<const T*>(gv.ptr) + b * gv.sb + s * gv.ss;
-    T* y0 = static_cast<T*>(yv.ptr) + b * yv.sb + s * yv.ss;
-    float w[8];
-    if constexpr (NORM) {
-      const W* wp = static_cast<const W*>(key ? a.w[1] : a.w[0]);
-      load4(wp + c0, w);
-      load4(wp + c1, w + 4);
-    }
-    for (int h = h0; h < h1; ++h) {
-      float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (on) {
-        load4(g0 + h * gv.sh + c0, g);
-        load4(g0 + h * gv.sh + c1, g + 4);
-        if constexpr (NORM) {
-          load4(x0 + h * xv.sh + c0, x);
-          load4(x0 + h * xv.sh + c1, x + 4);
-        }
-      }
-      if (inter) lane.rotate(g, true, -1.f);
-      else lane.rotate(g, false, -1.f);
+  const T* x0 = static_cast<const T*>(xv.ptr) + b * xv.sb + s * xv.ss + h0 * xv.sh;
+  const T* g0 = static_cast<const T*>(gv.ptr) + b * gv.sb + s * gv.ss + h0 * gv.sh;
+  T* y0 = static_cast<T*>(yv.ptr) + b * yv.sb + s * yv.ss + h0 * yv.sh;
+  const uint32_t ring = tc::smem_u32(smem) + threadIdx.x * R::UNIT;
+  int asked = 0;
+  auto ask = [&](uint32_t slot) {
+    if (asked < heads) {
+      R::copy(slot, g0 + lane.c0);
+      R::copy(slot + RUN, g0 + lane.c1);
       if constexpr (NORM) {
-        float sq = 0.f, tx = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          sq = fmaf(x[j], x[j], sq);
-          tx = fmaf(g[j] * w[j], x[j], tx);
-        }
-        sq = group_sum<LANES>(sq);
-        tx = group_sum<LANES>(tx);
-        const float r = rsqrtf(fmaf(sq, 1.f / D, a.s.eps));
-        const float m = tx * (1.f / D) * r * r;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dw[j] = fmaf(g[j], x[j] * r, dw[j]);
-          g[j] = r * fmaf(-x[j], m, g[j] * w[j]);
-        }
-      }
-      if (on) {
-        store4(y0 + h * yv.sh + c0, g);
-        store4(y0 + h * yv.sh + c1, g + 4);
+        R::copy(slot + 2 * RUN, x0 + lane.c0);
+        R::copy(slot + 3 * RUN, x0 + lane.c1);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++asked;
+    g0 += gv.sh;
+    x0 += xv.sh;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) ask(ring + i * STEP);
+  float w[2 * E], dw[2 * E];
+#pragma unroll
+  for (int j = 0; j < 2 * E; ++j) dw[j] = 0.f;
+  if constexpr (NORM) {
+    const W* wp = static_cast<const W*>(key ? a.w[1] : a.w[0]);
+    Run<W, E> run;
+    run.load(wp + lane.c0);
+    run.values(w);
+    run.load(wp + lane.c1);
+    run.values(w + E);
+  }
+  lane.angles(a, l, b, s);
+  unsigned slot = 0;
+  for (int h = 0; h < heads; ++h) {
+    ask(ring + (slot + kAhead - 1) % kAhead * STEP);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    const uint32_t at = ring + slot * STEP;
+    slot = (slot + 1) % kAhead;
+    R in;
+    float g[2 * E];
+    in.fetch(at);
+    in.values(g);
+    in.fetch(at + RUN);
+    in.values(g + E);
+    if (lane.turns) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        float &u = L::first(g, j), &v = L::second(g, j);
+        const float p = u, q = v;
+        u = fmaf(q, lane.sn[j], p * lane.cs[j]);
+        v = fmaf(-p, lane.sn[j], q * lane.cs[j]);
+      }
+    }
+    if constexpr (NORM) {
+      float x[2 * E];
+      in.fetch(at + 2 * RUN);
+      in.values(x);
+      in.fetch(at + 3 * RUN);
+      in.values(x + E);
+      float sq = 0.f, tx = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2 * E; ++j) {
+        sq = fmaf(x[j], x[j], sq);
+        tx = fmaf(g[j] * w[j], x[j], tx);
+      }
+      sq = group_sum<LANES>(sq);
+      tx = group_sum<LANES>(tx);
+      const float r = rsqrtf(fmaf(sq, 1.f / D, a.s.eps));
+      const float m = tx * (1.f / D) * r * r;
+#pragma unroll
+      for (int j = 0; j < 2 * E; ++j) {
+        if (on) dw[j] = fmaf(g[j], x[j] * r, dw[j]);
+        g[j] = r * fmaf(-x[j], m, g[j] * w[j]);
+      }
+    }
+    if (on) {
+      R out;
+      out.store(y0 + lane.c0, g);
+      out.store(y0 + lane.c1, g + E);
+    }
+    y0 += yv.sh;
   }
   if constexpr (NORM) {
-    __shared__ float part[GROUPS][D];
-    store4(&part[group][c0], dw);
-    store4(&part[group][c1], dw + 4);
+    __syncthreads();   // every lane is done with its slots
+    float* part = reinterpret_cast<float*>(smem);   // [GROUPS][D]
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      part[group * D + lane.c0 + j] = dw[j];
+      part[group * D + lane.c1 + j] = dw[E + j];
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += 256) {
       float sum = 0.f;
-      for (int i = 0; i < GROUPS; ++i) sum += part[i][d];
+#pragma unroll 8
+      for (int i = 0; i < GROUPS; ++i) sum += part[i * D + d];
       a.dw[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * D + d] = sum;
     }
   }
 }
 
-// Adds the blocks' partial weight gradients in order: block 0 the queries' rows, block 1 the keys'.
+// Adds the blocks' partial weight gradients in order, 16 features to a block: blockIdx.y 0 the queries' rows, 1 the keys'.
 template <int D>
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ part, int q_rows, int rows,
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ part, long long q_rows, long long rows,
                                                        float* __restrict__ dq_w, float* __restrict__ dk_w) {
-  constexpr int SLICES = 1024 / D;
-  __shared__ float sums[SLICES][D];
-  const int first = blockIdx.x ? q_rows : 0, last = blockIdx.x ? rows : q_rows;
-  const int d = threadIdx.x % D, slice = threadIdx.x / D;
+  __shared__ float sums[64][17];
+  const long long first = blockIdx.y ? q_rows : 0, last = blockIdx.y ? rows : q_rows;
+  const int f = threadIdx.x % 16, slice = threadIdx.x / 16, d = blockIdx.x * 16 + f;
   float sum = 0.f;
 #pragma unroll 8
-  for (int i = first + slice; i < last; i += SLICES) sum += part[(size_t)i * D + d];
-  sums[slice][d] = sum;
+  for (long long i = first + slice; i < last; i += 64) sum += part[i * D + d];
+  sums[slice][f] = sum;
   __syncthreads();
   if (slice != 0) return;
-  for (int i = 1; i < SLICES; ++i) sum += sums[i][d];
-  float* out = blockIdx.x ? dk_w : dq_w;
+#pragma unroll 16
+  for (int i = 1; i < 64; ++i) sum += sums[i][f];
+  float* out = blockIdx.y ? dk_w : dq_w;
   if (out != nullptr) out[d] = sum;
 }
 
@@ -274,20 +409,21 @@ struct RopeGrid {
   unsigned x;
 };
 
-RopeGrid rope_grid(const RopeShape& s, int D, bool backward) {
-  const int groups = 256 / (D / 8);
+// Features of a lane's runs.
+int run_of(const RopeShape& s, int dtype, bool backward) {
+  const bool many = (long long)s.B * s.S * (s.Hq + s.Hkv) >= 1LL << 17;
+  return !backward && dtype == DT_BF16 && s.half % 8 == 0 && many ? 8 : 4;
+}
+
+RopeGrid rope_grid(const RopeShape& s, int D, int run) {
+  const int groups = 256 / (D / (2 * run));
   const long long blocks = ((long long)s.B * s.S + groups - 1) / groups;
-  const long long want = 8LL * sm_count();   // blocks that fill the SMs
+  const long long want = 2LL * sm_count();   // 8 and 1 measured slower where this decides (2042 tokens of 24 heads)
   RopeGrid g{16, 0, 0, 0};
   while (g.chunk > 1 && blocks * ((s.Hq + g.chunk - 1) / g.chunk + (s.Hkv + g.chunk - 1) / g.chunk) < want) g.chunk /= 2;
   g.q_chunks = (s.Hq + g.chunk - 1) / g.chunk;
   g.k_chunks = (s.Hkv + g.chunk - 1) / g.chunk;
-  long long x = blocks;
-  if (backward) {
-    const long long most = (want + g.q_chunks + g.k_chunks - 1) / (g.q_chunks + g.k_chunks);
-    x = x < most ? x : most;
-  }
-  g.x = x > 0x7fffffffLL ? 0u : (unsigned)x;
+  g.x = blocks > 0x7fffffffLL ? 0u : (unsigned)blocks;
   return g;
 }
 
@@ -351,13 +487,31 @@ fa_status check_apart(const Span* out, int n_out, const fa_rope_params* p, const
   return FA_OK;
 }
 
+template <typename K>
+cudaError_t launch_rope(K kernel, int smem, dim3 grid, const RopeArgs& a, cudaStream_t st) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, 256, smem, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
 template <typename F>
-void by_type(const fa_rope_params* p, F f) {
-  using D64 = std::integral_constant<int, 64>;
-  using D128 = std::integral_constant<int, 128>;
+void by_type(const fa_rope_params* p, int run, F f) {
+  auto by_pairs = [&](auto t, auto w, auto dim, auto e) {
+    if (p->interleaved) f(t, w, dim, e, std::true_type{});
+    else f(t, w, dim, e, std::false_type{});
+  };
+  auto by_run = [&](auto t, auto w, auto dim) {
+    if constexpr (std::is_same_v<decltype(t), __nv_bfloat16>)
+      if (run == 8) return by_pairs(t, w, dim, std::integral_constant<int, 8>{});
+    by_pairs(t, w, dim, std::integral_constant<int, 4>{});
+  };
   auto by_dim = [&](auto t, auto w) {
-    if (p->D == 64) f(t, w, D64{});
-    else f(t, w, D128{});
+    if (p->D == 64) by_run(t, w, std::integral_constant<int, 64>{});
+    else by_run(t, w, std::integral_constant<int, 128>{});
   };
   if (p->dtype == FA_F32) by_dim(float{}, float{});
   else if (p->norm && p->w_dtype == FA_F32) by_dim(__nv_bfloat16{}, float{});
@@ -388,7 +542,8 @@ fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_vi
   if ((st = check_buffers(in, n, out, 2)) != FA_OK) return st;
   if ((st = check_apart(out, 2, p, inv_freq, positions)) != FA_OK) return st;
   if (p->S == 0) return FA_OK;
-  const RopeGrid g = rope_grid(a.s, p->D, false);
+  const int run = run_of(a.s, p->dtype, false);
+  const RopeGrid g = rope_grid(a.s, p->D, run);
   if (g.x == 0 || g.q_chunks + g.k_chunks > 65535) { set_error("too many rows for one launch"); return FA_ERR_UNSUPPORTED; }
   a.s.chunk = g.chunk;
   a.s.q_chunks = g.q_chunks;
@@ -399,21 +554,22 @@ fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_vi
   a.positions = positions;
   const dim3 grid(g.x, (unsigned)(g.q_chunks + g.k_chunks));
   cudaStream_t cs = (cudaStream_t)stream;
-  by_type(p, [&](auto t, auto w, auto dim) {
+  cudaError_t e = cudaSuccess;
+  by_type(p, run, [&](auto t, auto w, auto dim, auto e_run, auto inter) {
     using T = decltype(t);
     using W = decltype(w);
-    constexpr int D = decltype(dim)::value;
-    if (p->norm) rope_fwd_kernel<T, W, D, true><<<grid, 256, 0, cs>>>(a);
-    else if constexpr (std::is_same_v<T, W>) rope_fwd_kernel<T, T, D, false><<<grid, 256, 0, cs>>>(a);
+    constexpr int D = decltype(dim)::value, E = decltype(e_run)::value;
+    constexpr bool INTER = decltype(inter)::value;
+    if (p->norm) e = launch_rope(rope_fwd_kernel<T, W, D, E, INTER, true>, ring_bytes<T, E>(1), grid, a, cs);
+    else if constexpr (std::is_same_v<T, W>) e = launch_rope(rope_fwd_kernel<T, T, D, E, INTER, false>, ring_bytes<T, E>(1), grid, a, cs);
   });
-  count_launches(1);
-  return cuda_status(cudaGetLastError(), "norm and rotation launch");
+  return cuda_status(e, "norm and rotation launch");
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params* p) {
   RopeShape s;
   if (check_rope(p, s) != FA_OK || !p->norm || p->S == 0) return 0;
-  const RopeGrid g = rope_grid(s, p->D, true);
+  const RopeGrid g = rope_grid(s, p->D, run_of(s, p->dtype, true));
   return align_up((size_t)g.x * (g.q_chunks + g.k_chunks) * p->D * 4);
 }
 
@@ -453,7 +609,8 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
     if (e == cudaSuccess && out[3].n) e = cudaMemsetAsync(dk_weight, 0, out[3].n, cs);
     return cuda_status(e, "zero weight gradients");
   }
-  const RopeGrid g = rope_grid(a.s, p->D, true);
+  const int run = run_of(a.s, p->dtype, true);
+  const RopeGrid g = rope_grid(a.s, p->D, run);
   if (g.x == 0 || g.q_chunks + g.k_chunks > 65535) { set_error("too many rows for one launch"); return FA_ERR_UNSUPPORTED; }
   a.s.chunk = g.chunk;
   a.s.q_chunks = g.q_chunks;
@@ -465,19 +622,23 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
   a.positions = positions;
   a.dw = static_cast<float*>(ws);
   const dim3 grid(g.x, (unsigned)(g.q_chunks + g.k_chunks));
-  by_type(p, [&](auto t, auto w, auto dim) {
+  cudaError_t e = cudaSuccess;
+  by_type(p, run, [&](auto t, auto w, auto dim, auto e_run, auto inter) {
     using T = decltype(t);
     using W = decltype(w);
-    constexpr int D = decltype(dim)::value;
-    if (p->norm) rope_bwd_kernel<T, W, D, true><<<grid, 256, 0, cs>>>(a);
-    else if constexpr (std::is_same_v<T, W>) rope_bwd_kernel<T, T, D, false><<<grid, 256, 0, cs>>>(a);
+    constexpr int D = decltype(dim)::value, E = decltype(e_run)::value;
+    constexpr bool INTER = decltype(inter)::value;
+    if constexpr (E == 4) {
+      // the ring, which holds the groups' weight gradients at the end: 2 E x 256 floats
+      constexpr int norm = ring_bytes<T, E>(2) > 2 * E * 256 * 4 ? ring_bytes<T, E>(2) : 2 * E * 256 * 4;
+      if (p->norm) e = launch_rope(rope_bwd_kernel<T, W, D, E, INTER, true>, norm, grid, a, cs);
+      else if constexpr (std::is_same_v<T, W>) e = launch_rope(rope_bwd_kernel<T, T, D, E, INTER, false>, ring_bytes<T, E>(1), grid, a, cs);
+    }
   });
-  count_launches(1);
-  cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p->norm) {
-    const int q_rows = (int)g.x * g.q_chunks, rows = q_rows + (int)g.x * g.k_chunks;
-    if (p->D == 64) rope_dw_kernel<64><<<2, 1024, 0, cs>>>(a.dw, q_rows, rows, p->Hq ? dq_weight : nullptr, p->Hkv ? dk_weight : nullptr);
-    else rope_dw_kernel<128><<<2, 1024, 0, cs>>>(a.dw, q_rows, rows, p->Hq ? dq_weight : nullptr, p->Hkv ? dk_weight : nullptr);
+    const long long q_rows = (long long)g.x * g.q_chunks, rows = q_rows + (long long)g.x * g.k_chunks;
+    auto dw = p->D == 64 ? rope_dw_kernel<64> : rope_dw_kernel<128>;
+    dw<<<dim3(p->D / 16, 2), 1024, 0, cs>>>(a.dw, q_rows, rows, p->Hq ? dq_weight : nullptr, p->Hkv ? dk_weight : nullptr);
     count_launches(1);
     e = cudaGetLastError();
   }

@@ -138,20 +138,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_train_bwd_q4.restype = st
     lib.fa_train_bwd_accum_q4.argtypes = [P, vp, K4, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fa_train_bwd_accum_q4.restype = st
-    V, R, C, DP = (ctypes.POINTER(t) for t in (FaView, FaRopeParams, FaCache, FaDecodeParams))
-    lib.fa_qk_norm_rope.argtypes = [R, V, V, vp, vp, vp, vp, V, V, vp]
+    # structures whose addresses the binding passes (vp): several of them may lie in one buffer
+    lib.fa_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.fa_qk_norm_rope.restype = st
-    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [R]
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [vp]
     lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
-    lib.fa_qk_norm_rope_bwd.argtypes = [R, V, V, V, V, vp, vp, vp, vp, V, V, vp, vp, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fa_qk_norm_rope_bwd.restype = st
-    lib.fa_cache_write.argtypes = [C, V, V, i32, i32, vp, i64, vp, vp]
+    lib.fa_cache_write.argtypes = [vp, vp, vp, i32, i32, vp, i64, vp, vp]
     lib.fa_cache_write.restype = st
-    lib.fa_cache_read.argtypes = [C, i64, i32, i32, V, V, vp]
+    lib.fa_cache_read.argtypes = [vp, i64, i32, i32, vp, vp, vp]
     lib.fa_cache_read.restype = st
-    lib.fa_decode_workspace_size.argtypes = [DP, C]
+    lib.fa_decode_workspace_size.argtypes = [vp, vp]
     lib.fa_decode_workspace_size.restype = sz
-    lib.fa_decode.argtypes = [DP, vp, C, vp, vp, vp, vp, sz, vp]
+    lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fa_decode.restype = st
     lib.fa_train_bwd_plan.argtypes = [P, ctypes.POINTER(i32), i32, ctypes.POINTER(i32)]
     lib.fa_train_bwd_plan.restype = st
@@ -301,12 +301,12 @@ def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optiona
     return got
 
 
-def _view(t: torch.Tensor, layout: str) -> FaView:
-    """fa_view of a 4-D tensor in layout "bhsd" or "bshd", read or written where it is."""
+def _rows(t: torch.Tensor, layout: str):
+    """The values of fa_view for a 4-D tensor in layout "bhsd" or "bshd", read or written where it is."""
     b, x, y, d = t.stride()
     if not t.is_cuda or (d != 1 and t.shape[3] > 1):
         raise ValueError("every tensor must be a CUDA tensor whose features are contiguous")
-    return FaView(t.data_ptr(), b, y, x) if layout == "bhsd" else FaView(t.data_ptr(), b, x, y)
+    return (t.data_ptr(), b, y, x) if layout == "bhsd" else (t.data_ptr(), b, x, y)
 
 
 def _launch(device: torch.device, call, *args) -> None:

@@ -48,38 +48,61 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str = "non
     return f.to(torch.float32).to(device or "cpu"), factor
 
 
-def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, factor, offset, layout) -> ft.FaRopeParams:
-    if q.dim() != 4 or k.dim() != 4:
+# fa_rope_params and the call's views side by side, filled in one go: the C ABI gets the address of each.
+_PARAMS = ctypes.sizeof(ft.FaRopeParams)
+_VIEW = ctypes.sizeof(ft.FaView)
+
+
+def _call_type(views: int):
+    fields = list(ft.FaRopeParams._fields_) + [("padding", ctypes.c_int32)]
+    for i in range(views):
+        fields += [(f"{n}{i}", t) for n, t in ft.FaView._fields_]
+    t = type(f"FaRopeCall{views}", (ctypes.Structure,), {"_fields_": fields})
+    assert t.ptr0.offset == _PARAMS and ctypes.sizeof(t) == _PARAMS + views * _VIEW
+    return t
+
+
+_Forward, _Backward = _call_type(4), _call_type(6)
+
+
+def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, factor, offset, layout):
+    """The values of fa_rope_params, after the checks that the C ABI cannot make."""
+    shape = q.shape
+    if len(shape) != 4 or k.dim() != 4:
         raise ValueError(f"q and k must be 4-D (got {q.dim()}-D and {k.dim()}-D)")
+    B, x, y, D = shape
     if layout == "bhsd":
-        B, Hq, S, D = q.shape
-        want = (B, k.shape[1], S, D)
-        Hkv = k.shape[1]
+        Hq, S, Hkv = x, y, k.shape[1]
+        want = (B, Hkv, S, D)
     elif layout == "bshd":
-        B, S, Hq, D = q.shape
-        want = (B, S, k.shape[2], D)
-        Hkv = k.shape[2]
+        S, Hq, Hkv = x, y, k.shape[2]
+        want = (B, S, Hkv, D)
     else:
         raise ValueError(f"layout {layout!r}: 'bhsd' or 'bshd'")
     if k.shape != want:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected {want}")
-    if k.dtype != q.dtype:
-        raise TypeError(f"k has dtype {k.dtype}, expected {q.dtype}")
-    code = ft._dtype_code(q)
+    dtype = q.dtype
+    if k.dtype != dtype:
+        raise TypeError(f"k has dtype {k.dtype}, expected {dtype}")
+    code = w_code = ft._dtype_code(q)
     device = q.device
     if k.device != device:
         raise ValueError(f"k is on {k.device}, q on {device}")
-    w_code = code
-    if (q_weight is None) != (k_weight is None):
+    norm = q_weight is not None
+    if norm != (k_weight is not None):
         raise ValueError("give both q_weight and k_weight (norm and rotation), or neither (rotation alone)")
-    if q_weight is not None:
-        if q_weight.dtype != k_weight.dtype or q_weight.dtype not in (q.dtype, torch.float32):
-            raise TypeError(f"weights of dtype {q_weight.dtype} and {k_weight.dtype}: both {q.dtype} or both float32")
-        w_code = ft._dtype_code(q_weight)
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w.shape != (D,):
-                raise ValueError(f"{name} has shape {tuple(w.shape)}, expected {(D,)}")
-            _small(name, w, device)
+    if norm:
+        w = q_weight.dtype
+        if w != dtype:
+            if w != torch.float32:
+                raise TypeError(f"weights of dtype {w} and {k_weight.dtype}: both {dtype} or both float32")
+            w_code = ft.FA_F32
+        if k_weight.dtype != w:
+            raise TypeError(f"weights of dtype {w} and {k_weight.dtype}: both {dtype} or both float32")
+        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if t.shape != (D,):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(D,)}")
+            _small(name, t, device)
     rot = 0
     if inv_freq is not None:
         if inv_freq.dtype != torch.float32:
@@ -92,12 +115,13 @@ def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, fac
     if positions is not None:
         if positions.dtype != torch.int64:
             raise TypeError(f"positions has dtype {positions.dtype}, expected torch.int64")
-        if positions.shape != (S,) and positions.shape != (B, S):
+        if positions.shape == (B, S):
+            pos_stride = S
+        elif positions.shape != (S,):
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(S,)} or {(B, S)}")
         _small("positions", positions, device)
-        pos_stride = S if positions.dim() == 2 else 0
-    return ft.FaRopeParams(B, S, Hq, Hkv, D, code, w_code, rot, int(bool(interleaved)), int(q_weight is not None), eps,
-                           factor, offset, pos_stride, 0)
+    return (B, S, Hq, Hkv, D, code, w_code, rot, 1 if interleaved else 0, 1 if norm else 0, eps, factor, offset,
+            pos_stride, 0, 0)
 
 
 def _small(name: str, t: torch.Tensor, device) -> None:
@@ -127,19 +151,23 @@ def qk_norm_rope(q, k, inv_freq, positions=None, q_weight=None, k_weight=None, *
     positions: int64 [S] or [B, S]; without, token s is at offset + s. interleaved: pairs (2 i, 2 i + 1) instead of
     (i, i + rotary_dim / 2). factor multiplies cosines and sines (see rope_inv_freq).
     """
-    lib = ft.load_library()
     p = _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, factor, offset, layout)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _same("q_out", q_out, q)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         _same("k_out", k_out, k)
-    views = [ft._view(t, layout) for t in (q, k, q_out, k_out)]
-    ft._launch(q.device, lib.fa_qk_norm_rope, p, views[0], views[1], ft._ptr(q_weight), ft._ptr(k_weight),
-               ft._ptr(inv_freq) if p.rot else None, ft._ptr(positions), views[2], views[3], ft._stream(q.device, stream))
+    c = _Forward(*p, *ft._rows(q, layout), *ft._rows(k, layout), *ft._rows(q_out, layout), *ft._rows(k_out, layout))
+    at = ctypes.addressof(c)
+    v = at + _PARAMS
+    device = q.device
+    ft._launch(device, ft.load_library().fa_qk_norm_rope, at, v, v + _VIEW,
+               None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+               None if inv_freq is None else inv_freq.data_ptr(), None if positions is None else positions.data_ptr(),
+               v + 2 * _VIEW, v + 3 * _VIEW, ft._stream(device, stream))
     return q_out, k_out
 
 
@@ -150,35 +178,39 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, inv_freq, positions=None, q_weight=No
     """Backward of qk_norm_rope: from the gradients of its outputs and its inputs, returns (dq, dk, dq_weight,
     dk_weight), the weights' in float32 and summed in a fixed order (None without weights). The other arguments are
     the forward's; gradients and inputs may be strided like the forward's."""
-    lib = ft.load_library()
     p = _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, factor, offset, layout)
     _same("dq_out", dq_out, q)
     _same("dk_out", dk_out, k)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _same("dq", dq, q)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dk = torch.empty_like(k, memory_format=torch.contiguous_format)
     else:
         _same("dk", dk, k)
+    c = _Backward(*p, *ft._rows(dq_out, layout), *ft._rows(dk_out, layout), *ft._rows(q, layout), *ft._rows(k, layout),
+                  *ft._rows(dq, layout), *ft._rows(dk, layout))
+    at = ctypes.addressof(c)
+    v = at + _PARAMS
+    lib = ft.load_library()
+    device = q.device
     ws, ws_bytes = None, 0
-    if p.norm:
+    if q_weight is not None:
+        D = q.shape[3]
         if dq_weight is None:
-            dq_weight = torch.empty(p.D, dtype=torch.float32, device=q.device)
+            dq_weight = torch.empty(D, dtype=torch.float32, device=device)
         if dk_weight is None:
-            dk_weight = torch.empty(p.D, dtype=torch.float32, device=q.device)
+            dk_weight = torch.empty(D, dtype=torch.float32, device=device)
         for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-            if t.shape != (p.D,) or t.dtype != torch.float32:
-                raise ValueError(f"{name} must be float32 {(p.D,)}")
-            _small(name, t, q.device)
-        ws_bytes = int(lib.fa_qk_norm_rope_bwd_workspace_size(p))
+            if t.shape != (D,) or t.dtype != torch.float32:
+                raise ValueError(f"{name} must be float32 {(D,)}")
+            _small(name, t, device)
+        ws_bytes = lib.fa_qk_norm_rope_bwd_workspace_size(at)
+        ws = ft._scratch(ws_bytes, device, workspace, stream)
     else:
         dq_weight = dk_weight = None
-    views = [ft._view(t, layout) for t in (dq_out, dk_out, q, k, dq, dk)]
-    if ws_bytes:
-        ws = ft._scratch(ws_bytes, q.device, workspace, stream)
-    ft._launch(q.device, lib.fa_qk_norm_rope_bwd, p, views[0], views[1], views[2], views[3], ft._ptr(q_weight),
-               ft._ptr(k_weight), ft._ptr(inv_freq) if p.rot else None, ft._ptr(positions), views[4], views[5],
-               ft._ptr(dq_weight), ft._ptr(dk_weight), ft._ptr(ws), ws_bytes, ft._stream(q.device, stream))
+    ft._launch(device, lib.fa_qk_norm_rope_bwd, at, v, v + _VIEW, v + 2 * _VIEW, v + 3 * _VIEW, ft._ptr(q_weight),
+               ft._ptr(k_weight), ft._ptr(inv_freq), ft._ptr(positions), v + 4 * _VIEW, v + 5 * _VIEW,
+               ft._ptr(dq_weight), ft._ptr(dk_weight), ft._ptr(ws), ws_bytes, ft._stream(device, stream))
     return dq, dk, dq_weight, dk_weight

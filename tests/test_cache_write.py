@@ -1,4 +1,6 @@
 """Writing a quantized K/V cache and reading it back: bit for bit the oracle's blocks, and nothing else touched."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -43,6 +45,10 @@ def lib():
 F = 1 << 34
 
 
+def R(x):
+    return None if x is None else ctypes.byref(x)
+
+
 def cache(**kw):
     c = ft.FaCache(2, 3, 40, 64, ft.FA_KV_Q4_0, 0, F, 2 * F, 3 * F, 4 * F)
     for n, v in kw.items():
@@ -66,23 +72,23 @@ BAD_CACHE = [("B", dict(B=0), 1), ("Hkv", dict(Hkv=70000), 1), ("S", dict(S=0), 
 @pytest.mark.parametrize("name,kw,code", BAD_CACHE, ids=[b[0] for b in BAD_CACHE])
 def test_bad_caches_are_refused_before_launch(lib, name, kw, code):
     c = cache(**kw)
-    assert lib.fa_cache_write(c, view(5), view(6), ft.FA_BF16, 5, None, 0, None, None) == code
+    assert lib.fa_cache_write(R(c), R(view(5)), R(view(6)), ft.FA_BF16, 5, None, 0, None, None) == code
     assert lib.fa_last_error()
-    assert lib.fa_cache_read(c, 0, 5, ft.FA_BF16, view(5), view(6), None) == code
+    assert lib.fa_cache_read(R(c), 0, 5, ft.FA_BF16, R(view(5)), R(view(6)), None) == code
     p = ft.FaDecodeParams(6, 1, 0, 0, 0.125, 0)
-    assert lib.fa_decode(p, 5 * F, c, None, 6 * F, 7 * F, 8 * F, 1 << 33, None) == code
+    assert lib.fa_decode(R(p), 5 * F, R(c), None, 6 * F, 7 * F, 8 * F, 1 << 33, None) == code
 
 
 def test_bad_rows_are_refused_before_launch(lib):
     w = lambda n=5, k=view(5), v=view(6), dt=ft.FA_BF16, at=None, first=0, count=None: lib.fa_cache_write(  # noqa: E731
-        cache(), k, v, dt, n, at, first, count, None)
+        R(cache()), R(k), R(v), dt, n, at, first, count, None)
     for bad in (dict(n=-1), dict(dt=9), dict(first=-1), dict(first=36), dict(n=41), dict(at=8 * F + 4),
                 dict(count=8 * F + 2), dict(k=view(5, ptr=5 * F + 8)), dict(k=None), dict(v=view(6, stride_s=4)),
                 dict(v=view(6, ptr=F + 128)), dict(at=F + 8)):
         assert w(**bad) == ft.FA_ERR_INVALID_ARG, bad
     assert w(n=0) == ft.FA_OK
     r = lambda n=5, k=view(5), v=view(6), dt=ft.FA_BF16, first=0: lib.fa_cache_read(  # noqa: E731
-        cache(), first, n, dt, k, v, None)
+        R(cache()), first, n, dt, R(k), R(v), None)
     for bad in (dict(n=-1), dict(dt=9), dict(first=-1), dict(first=36), dict(k=None), dict(k=view(5, stride_s=32)),
                 dict(v=view(5)), dict(v=view(6, ptr=2 * F + 16)), dict(v=view(6, stride_h=0))):
         assert r(**bad) == ft.FA_ERR_INVALID_ARG, bad

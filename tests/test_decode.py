@@ -10,6 +10,7 @@ the V scales it is summed with): off by 2^-11 / 2 of its value or, where that is
 most W, sum p is at least 1, and the result is rounded to bf16, 2^-8 of its value, so with n keys
     |dO| <= (2^-12 + 2 E + 2^-16) sum p |v| / sum p + n W 2^(-25 - level) + 2^-8 |O|.
 """
+import ctypes
 import math
 
 import numpy as np
@@ -218,6 +219,7 @@ def test_bad_arguments_are_refused_before_launch():
     from backward_adapter_gb300 import build as fbuild
     fbuild.build()
     lib = ft.load_library()
+    R = ctypes.byref
     F = 1 << 34
     c = ft.FaCache(2, 3, 4000, 64, ft.FA_KV_Q8_0, 0, F, 2 * F, 3 * F, 4 * F)
 
@@ -226,15 +228,15 @@ def test_bad_arguments_are_refused_before_launch():
         for n, v in kw.items():
             setattr(x, n, v)
         return x
-    need = lib.fa_decode_workspace_size(p(), c)
+    need = lib.fa_decode_workspace_size(R(p()), R(c))
     assert need > 0
     go = lambda pp=p(), q=5 * F, n=None, o=6 * F, lse=7 * F, ws=8 * F, size=need: lib.fa_decode(  # noqa: E731
-        pp, q, c, n, o, lse, ws, size, None)
+        R(pp), q, R(c), n, o, lse, ws, size, None)
     for kw in (dict(Hq=0), dict(Hq=7), dict(Hq=70000), dict(Sq=-1), dict(Sq=17), dict(window=-1), dict(layout=3),
                dict(scale=float("nan")), dict(reserved=1)):
         assert go(p(**kw)) == ft.FA_ERR_INVALID_ARG, kw
-        assert lib.fa_decode_workspace_size(p(**kw), c) == 0
-    assert lib.fa_decode(None, 5 * F, c, None, 6 * F, 7 * F, 8 * F, need, None) == ft.FA_ERR_INVALID_ARG
+        assert lib.fa_decode_workspace_size(R(p(**kw)), R(c)) == 0
+    assert lib.fa_decode(None, 5 * F, R(c), None, 6 * F, 7 * F, 8 * F, need, None) == ft.FA_ERR_INVALID_ARG
     for kw in (dict(q=None), dict(q=5 * F + 8), dict(o=None), dict(o=F + 64), dict(lse=6 * F), dict(lse=7 * F + 4),
                dict(n=9 * F + 4), dict(n=6 * F + 16), dict(ws=8 * F + 16), dict(ws=5 * F)):
         assert go(**kw) == ft.FA_ERR_INVALID_ARG, kw

@@ -175,6 +175,9 @@ def lib():
     return ft.load_library()
 
 
+R = ctypes.byref
+
+
 def params(**kw):
     p = ft.FaRopeParams(2, 5, 4, 2, 64, ft.FA_BF16, ft.FA_BF16, 64, 0, 1, 1e-6, 1.0, 0, 5, 0)
     for n, v in kw.items():
@@ -200,10 +203,10 @@ def test_bad_parameters_are_refused_before_launch(lib, name, kw, code):
     p, good = params(**kw), params()
     v = views(1 << 32, good, 6)
     f = 1 << 40
-    assert lib.fa_qk_norm_rope(p, v[0], v[1], f, f + 4096, f + 8192, f + 12288, v[2], v[3], None) == code
+    assert lib.fa_qk_norm_rope(R(p), R(v[0]), R(v[1]), f, f + 4096, f + 8192, f + 12288, R(v[2]), R(v[3]), None) == code
     assert lib.fa_last_error()
-    assert lib.fa_qk_norm_rope_bwd_workspace_size(p) == 0
-    assert lib.fa_qk_norm_rope_bwd(p, *v[:4], f, f + 4096, f + 8192, f + 12288, v[4], v[5], f + (1 << 20),
+    assert lib.fa_qk_norm_rope_bwd_workspace_size(R(p)) == 0
+    assert lib.fa_qk_norm_rope_bwd(R(p), *map(R, v[:4]), f, f + 4096, f + 8192, f + 12288, R(v[4]), R(v[5]), f + (1 << 20),
                                    f + (2 << 20), f + (3 << 20), 1 << 30, None) == code
 
 
@@ -217,7 +220,7 @@ def test_bad_views_pointers_and_workspaces_are_refused(lib):
         if change is not None:
             for n, x in change.items():
                 setattr(v[at], n, x)
-        st = lib.fa_qk_norm_rope(p, v[0], v[1], *small, v[2], v[3], None)
+        st = lib.fa_qk_norm_rope(R(p), R(v[0]), R(v[1]), *small, R(v[2]), R(v[3]), None)
         return st, lib.fa_last_error().decode()
 
     for change, at, word in ((dict(ptr=(1 << 32) + 8), 0, "aligned"), (dict(ptr=0), 1, "NULL"),
@@ -232,13 +235,13 @@ def test_bad_views_pointers_and_workspaces_are_refused(lib):
         st, msg = fwd(small=s)
         assert st == ft.FA_ERR_INVALID_ARG, (i, bad, msg)
     v = views(1 << 32, p, 6)
-    need = lib.fa_qk_norm_rope_bwd_workspace_size(p)
+    need = lib.fa_qk_norm_rope_bwd_workspace_size(R(p))
     assert need > 0
-    out = (v[4], v[5], f + (1 << 20), f + (2 << 20))
-    assert lib.fa_qk_norm_rope_bwd(p, *v[:4], *small, *out, f + (3 << 20), need - 1, None) == ft.FA_ERR_WORKSPACE
-    assert lib.fa_qk_norm_rope_bwd(p, *v[:4], *small, *out, None, need, None) == ft.FA_ERR_WORKSPACE
-    assert lib.fa_qk_norm_rope_bwd(p, *v[:4], *small, *out, 1 << 32, need, None) == ft.FA_ERR_INVALID_ARG
-    assert lib.fa_qk_norm_rope(params(S=0), *v[:2], *small, v[2], v[3], None) == ft.FA_OK   # nothing to do
+    out = (R(v[4]), R(v[5]), f + (1 << 20), f + (2 << 20))
+    assert lib.fa_qk_norm_rope_bwd(R(p), *map(R, v[:4]), *small, *out, f + (3 << 20), need - 1, None) == ft.FA_ERR_WORKSPACE
+    assert lib.fa_qk_norm_rope_bwd(R(p), *map(R, v[:4]), *small, *out, None, need, None) == ft.FA_ERR_WORKSPACE
+    assert lib.fa_qk_norm_rope_bwd(R(p), *map(R, v[:4]), *small, *out, 1 << 32, need, None) == ft.FA_ERR_INVALID_ARG
+    assert lib.fa_qk_norm_rope(R(params(S=0)), *map(R, v[:2]), *small, R(v[2]), R(v[3]), None) == ft.FA_OK   # nothing to do
 
 
 def test_struct_layout_matches_header(tmp_path):
