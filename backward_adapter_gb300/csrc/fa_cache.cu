@@ -37,23 +37,22 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
                                             tc::pack_bf16x2(x[4], x[5]), tc::pack_bf16x2(x[6], x[7]));
 }
 
-// A thread quantizes 8 features of one row, four lanes a block of 32. blockIdx.y: 0 for K, 1 for V.
+// A thread quantizes 8 features of a row, four lanes a block of 32. blockIdx.y: 0 for K, 1 for V.
 template <typename T, int D, bool Q4>
-__global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k, RowView v, int n_rows,
+__global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k, RowView v, unsigned rows, unsigned n_rows,
                                                           const int64_t* __restrict__ begin, long long begin_all,
                                                           const int64_t* __restrict__ count, unsigned* status) {
   constexpr int LANES = D / 8;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long g = i / LANES;
-  const int l = (int)(i % LANES);
+  const unsigned g = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int l = threadIdx.x % LANES;
   const RowView src = blockIdx.y ? v : k;
   float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   bool on = false;
   size_t row = 0;
-  if (g < (long long)c.B * c.Hkv * n_rows) {
-    const int r = (int)(g % n_rows), bh = (int)(g / n_rows), h = bh % c.Hkv, b = bh / c.Hkv;
+  if (g < rows) {
+    const unsigned bh = g / n_rows, r = g % n_rows, b = bh / c.Hkv, h = bh % c.Hkv;
     const long long first = begin != nullptr ? __ldg(begin + b) : begin_all;
-    if (count == nullptr || r < __ldg(count + b)) {
+    if (count == nullptr || (long long)r < __ldg(count + b)) {
       if (first < c.S && first + r >= 0 && first + r < c.S) {
         on = true;
         row = (size_t)bh * c.S + (size_t)(first + r);
@@ -78,49 +77,67 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k
   if (part == 0) (blockIdx.y ? c.v_d : c.k_d)[row * (D / 32) + blk] = __half_as_ushort(d);
 }
 
-// A thread reads 16 features of one row: half a block's bytes. blockIdx.y: 0 for K, 1 for V.
-template <typename T, int D, bool Q4>
-__global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long begin, int n_rows, RowView k, RowView v) {
-  constexpr int PARTS = D / 16;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long g = i / PARTS;
-  const int part = (int)(i % PARTS);
-  if (g >= (long long)c.B * c.Hkv * n_rows) return;
-  const int r = (int)(g % n_rows), bh = (int)(g / n_rows), h = bh % c.Hkv, b = bh / c.Hkv;
+// A thread reads 16 features (half a block's bytes) of ROWS rows, all of them on their way at once.
+// blockIdx.y: 0 for K, 1 for V.
+template <typename T, int D, bool Q4, int ROWS>
+__global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long begin, unsigned rows, unsigned n_rows,
+                                                         RowView k, RowView v) {
+  constexpr int PARTS = D / 16, STEP = 256 / PARTS;   // rows a block takes at a time
+  const int part = threadIdx.x % PARTS;
+  const unsigned first = blockIdx.x * (STEP * ROWS) + threadIdx.x / PARTS;
   const RowView dst = blockIdx.y ? v : k;
-  const size_t row = (size_t)bh * c.S + (size_t)(begin + r);
   const uint8_t* values = static_cast<const uint8_t*>(blockIdx.y ? c.v_q : c.k_q);
-  const float d = __half2float(__ushort_as_half(__ldg((blockIdx.y ? c.v_d : c.k_d) + row * (D / 32) + part / 2)));
-  T* out = static_cast<T*>(dst.ptr) + b * dst.sb + r * dst.ss + h * dst.sh;
-  float x[8], y[8];
-  if constexpr (Q4) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(values + row * (D / 2) + 8 * part));
+  const uint16_t* scales = blockIdx.y ? c.v_d : c.k_d;
+  uint4 w[ROWS];
+  uint16_t scale[ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = q4_low(j < 4 ? w.x : w.y, j % 4) * d;
-      y[j] = q4_high(j < 4 ? w.x : w.y, j % 4) * d;
+  for (int i = 0; i < ROWS; ++i) {
+    const unsigned g = first + i * STEP;
+    if (g >= rows) break;
+    const size_t row = (size_t)(g / n_rows) * c.S + (size_t)(begin + g % n_rows);
+    scale[i] = __ldg(scales + row * (D / 32) + part / 2);
+    if constexpr (Q4) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(values + row * (D / 2) + 8 * part));
+      w[i].x = u.x;
+      w[i].y = u.y;
+    } else {
+      w[i] = __ldg(reinterpret_cast<const uint4*>(values + row * D + 16 * part));
     }
-    out += part / 2 * 32 + part % 2 * 8;
-    store8(out, x);
-    store8(out + 16, y);
-  } else {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(values + row * D + 16 * part));
-    const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = s8_to_f32(u[j / 4], j % 4) * d;
-      y[j] = s8_to_f32(u[2 + j / 4], j % 4) * d;
+  for (int i = 0; i < ROWS; ++i) {
+    const unsigned g = first + i * STEP;
+    if (g >= rows) break;
+    const unsigned bh = g / n_rows, r = g % n_rows, b = bh / c.Hkv, h = bh % c.Hkv;
+    const float d = __half2float(__ushort_as_half(scale[i]));
+    T* out = static_cast<T*>(dst.ptr) + b * dst.sb + r * dst.ss + h * dst.sh;
+    float x[8], y[8];
+    if constexpr (Q4) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = q4_low(j < 4 ? w[i].x : w[i].y, j % 4) * d;
+        y[j] = q4_high(j < 4 ? w[i].x : w[i].y, j % 4) * d;
+      }
+      out += part / 2 * 32 + part % 2 * 8;
+      store8(out, x);
+      store8(out + 16, y);
+    } else {
+      const uint32_t u[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = s8_to_f32(u[j / 4], j % 4) * d;
+        y[j] = s8_to_f32(u[2 + j / 4], j % 4) * d;
+      }
+      out += 16 * part;
+      store8(out, x);
+      store8(out + 8, y);
     }
-    out += 16 * part;
-    store8(out, x);
-    store8(out + 8, y);
   }
 }
 
-// Blocks of 256 threads over `per_row` threads for each row; 0 when there are too many for a grid.
-unsigned blocks_for(long long rows, int per_row) {
-  const long long n = (rows * per_row + 255) / 256;
-  return n > 0x7fffffffLL ? 0u : (unsigned)n;
+// Blocks that take `per_block` rows each; 0 when the rows are too many for 32-bit numbers.
+unsigned blocks_for(long long rows, int per_block) {
+  return rows > 0x7fffffffLL ? 0u : (unsigned)((rows + per_block - 1) / per_block);
 }
 
 }  // namespace
@@ -128,9 +145,12 @@ unsigned blocks_for(long long rows, int per_row) {
 cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowView& v, int dtype, int n_rows,
                                const int64_t* begin, long long begin_all, const int64_t* count, unsigned* status,
                                cudaStream_t st) {
-  const unsigned n = blocks_for((long long)c.B * c.Hkv * n_rows, c.D / 8);
+  const long long rows = (long long)c.B * c.Hkv * n_rows;
+  const unsigned n = blocks_for(rows, 256 / (c.D / 8));
   if (n == 0) return cudaErrorInvalidConfiguration;
-  auto go = [&](auto kernel) { kernel<<<dim3(n, 2), 256, 0, st>>>(c, k, v, n_rows, begin, begin_all, count, status); };
+  auto go = [&](auto kernel) {
+    kernel<<<dim3(n, 2), 256, 0, st>>>(c, k, v, (unsigned)rows, (unsigned)n_rows, begin, begin_all, count, status);
+  };
   auto by_format = [&](auto t, auto dim) {
     using T = decltype(t);
     constexpr int D = decltype(dim)::value;
@@ -147,14 +167,17 @@ cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowVi
 
 cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, int dtype, const RowView& k,
                               const RowView& v, cudaStream_t st) {
-  const unsigned n = blocks_for((long long)c.B * c.Hkv * n_rows, c.D / 16);
+  const long long rows = (long long)c.B * c.Hkv * n_rows;
+  const int step = 256 / (c.D / 16);
+  const bool many = rows >= 16LL * step * sm_count();   // eight rows a thread then still leave two blocks for every SM
+  const unsigned n = blocks_for(rows, many ? 8 * step : step);
   if (n == 0) return cudaErrorInvalidConfiguration;
-  auto go = [&](auto kernel) { kernel<<<dim3(n, 2), 256, 0, st>>>(c, begin, n_rows, k, v); };
+  auto go = [&](auto kernel) { kernel<<<dim3(n, 2), 256, 0, st>>>(c, begin, (unsigned)rows, (unsigned)n_rows, k, v); };
   auto by_format = [&](auto t, auto dim) {
     using T = decltype(t);
     constexpr int D = decltype(dim)::value;
-    if (c.q4) go(cache_read_kernel<T, D, true>);
-    else go(cache_read_kernel<T, D, false>);
+    if (c.q4) many ? go(cache_read_kernel<T, D, true, 8>) : go(cache_read_kernel<T, D, true, 1>);
+    else many ? go(cache_read_kernel<T, D, false, 8>) : go(cache_read_kernel<T, D, false, 1>);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
