@@ -4,11 +4,11 @@
 // Mathematics. With G = Hq / Hkv query heads on a key/value head, the R = G * Sq query rows of one
 // head all read the same keys. A block of 32 features of a key is d * n with whole numbers n, so
 //     s_j = scale * sum_blocks d_jb <n_jb, q_b>,   o = sum_j sum_blocks (p_j d_jb) n_jb :
-// the tensor cores multiply the whole numbers, exact as fp16, by q and by p * d, and the scales never
-// touch the 8- or 4-bit data. Scores, softmax statistics and sums are fp32. Query rows are scaled by a
-// power of two to the top of fp16's range, where a bf16 value down to 2^-28 of the row's largest is
-// exact; p * d is rounded to fp16, 2^-12 of its value, with a power of two of its own that keeps it
-// below 2^15 whatever the scales are (see `level`).
+// the tensor cores multiply whole numbers, exact as fp16, by q and by p * d, and K's scales never touch
+// the 8- or 4-bit data. Scores, softmax statistics and sums are fp32. Query rows are scaled by a power of
+// two to the top of fp16's range, where a bf16 value down to 2^-24 of the row's largest is exact; p and
+// p * d are rounded to fp16, 2^-12 of their values each, with a power of two that keeps them below 2^15
+// whatever the scales are (see `level`).
 //
 // What bounds it: the planes are read once, 144 bytes a key for D = 128 in 4 bits, so HBM; next to
 // that the instructions that turn packed bits into operands. Keys are the 16 rows of an
@@ -17,10 +17,12 @@
 // first, four times the bytes that are read.
 //
 // From bits to operands: ldmatrix hands a lane the packed words of its operand rows, for V with two
-// keys side by side (transposed). The bits of two numbers are then put below the leading one of a
-// power of two (one logic instruction: 1024 + b and 64 + b place a low and a high nibble without a
-// shift of their own), and the power and the format's offset are taken off again by a packed
-// subtraction, exact, on the other pipe.
+// keys side by side (transposed). Masked, the four bits b of two bytes are operands already: as fp16 they
+// are b 2^-24 (low nibbles) and b 2^-20 (high ones), exact subnormal numbers; the powers of two are
+// taken into q and into the result. Each pair of numbers costs one logic instruction, and each word a
+// shift. What the format takes off (8, or 128 in 8 bits) is in the products' starting value for K, a
+// multiple of the sum of q over a block; V's numbers get a packed addition, exact and on another pipe than
+// the logic, as sums over many keys that hold a large offset would lose bits.
 //
 // Split: the tiles of 32 keys of all sequences and heads are one list, cut into equal slices, one for
 // each block that the SMs hold at a time, and those into one run of tiles for each warp: the end of one
@@ -47,6 +49,7 @@ constexpr int kMaxTokens = 16;
 constexpr int kMostWarps = 8;
 constexpr int kTile = 32;         // keys a warp takes at a time
 constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
+constexpr float kNoBase = -3e38f; // below every score
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Masks of the low and the high nibbles of bytes 0 and 2. They come as kernel arguments: (x & mask) | one is a
@@ -150,13 +153,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same onto zeros.
-__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
+// From other values than the result's: c0 and c1 in both rows.
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], float c0, float c1, uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -165,34 +168,38 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// x - k for both fp16 halves of x, k the bits of the constant.
-template <uint16_t K>
-__device__ __forceinline__ uint32_t sub_f16(uint32_t x) {
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __halves2half2(__ushort_as_half(K), __ushort_as_half(K)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Fp16 operands from the packed words of a block. 4 bits, one word: the numbers of bytes (0, 2) and
-// (1, 3), first those of the low nibbles, then of the high ones.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t x, uint32_t y) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Fp16 operands, numbers times 2^-24, from the packed words of a block. 4 bits, one word: the numbers of
+// bytes (0, 2) and (1, 3), first those of the low nibbles, then, 16 times as large, of the high ones.
 __device__ __forceinline__ void pairs_q4(uint32_t w, Masks m, uint32_t (&f)[4]) {
   const uint32_t h = w >> 8;
-  f[0] = sub_f16<0x6408>((w & m.low) | 0x64006400u);   // 1024 + b - 1032
-  f[1] = sub_f16<0x6408>((h & m.low) | 0x64006400u);
-  f[2] = sub_f16<0x5480>((w & m.high) | 0x54005400u);   // 64 + b - 72
-  f[3] = sub_f16<0x5480>((h & m.high) | 0x54005400u);
+  f[0] = w & m.low;
+  f[1] = h & m.low;
+  f[2] = w & m.high;
+  f[3] = h & m.high;
 }
-// 8 bits, one word of each half block: bytes (A, B) and (C, D) of the first, then of the second.
+// 8 bits, one word of each half block, numbers + 128: bytes (A, B) and (C, D) of the first, then of the second.
 template <int A, int B, int C, int D>
 __device__ __forceinline__ void pairs_q8(uint32_t w0, uint32_t w1, uint32_t (&f)[4]) {
   const uint32_t a = w0 ^ 0x80808080u, b = w1 ^ 0x80808080u;
-  f[0] = sub_f16<0x6480>(__byte_perm(a, 0x64646464u, 0x4040 | A | B << 8));   // 1024 + (n + 128) - 1152
-  f[1] = sub_f16<0x6480>(__byte_perm(a, 0x64646464u, 0x4040 | C | D << 8));
-  f[2] = sub_f16<0x6480>(__byte_perm(b, 0x64646464u, 0x4040 | A | B << 8));
-  f[3] = sub_f16<0x6480>(__byte_perm(b, 0x64646464u, 0x4040 | C | D << 8));
+  f[0] = __byte_perm(a, 0u, 0x4040 | A | B << 8);
+  f[1] = __byte_perm(a, 0u, 0x4040 | C | D << 8);
+  f[2] = __byte_perm(b, 0u, 0x4040 | A | B << 8);
+  f[3] = __byte_perm(b, 0u, 0x4040 | C | D << 8);
 }
 
 // Where things are in a ring slot, and how a row's 16-byte pieces are permuted there so that the
@@ -207,36 +214,64 @@ struct Slot {
   static constexpr int KD_OFF = 2 * kTile * ROW;
   static constexpr int VD_OFF = KD_OFF + kTile * SC;
   static constexpr int BYTES = VD_OFF + kTile * SC;
-  static constexpr int STAGES = BYTES <= 5120 ? 3 : 2;
+  static constexpr int STAGES = 2;                // 3 measured no faster
   // Piece p of a row is at piece p ^ (row / PER) % PIECES, PER the rows in 128 bytes: the rows of a
   // matrix then meet no bank twice. Rows 8 apart are permuted alike.
   static constexpr int PER = 128 / ROW;
   __device__ static __forceinline__ int permuted(unsigned row) { return (int)(row / PER % PIECES); }
 };
 
-// The scales of a key, as they are and as floats.
+// The scales of a key.
 template <int NB>
-__device__ __forceinline__ uint32_t load_scales(uint32_t at, float (&d)[NB]) {
+__device__ __forceinline__ void load_scales(uint32_t at, float (&d)[NB]) {
+  uint32_t u[NB / 2];
   if constexpr (NB == 4) {
-    const uint2 u = lds64(at);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    d[0] = a.x; d[1] = a.y; d[2] = b.x; d[3] = b.y;
-    return u.x | u.y;
+    const uint2 x = lds64(at);
+    u[0] = x.x; u[1] = x.y;
   } else {
-    const uint32_t u = lds32(at);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u));
-    d[0] = a.x; d[1] = a.y;
-    return u;
+    u[0] = lds32(at);
+  }
+#pragma unroll
+  for (int i = 0; i < NB / 2; ++i) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    d[2 * i] = x.x;
+    d[2 * i + 1] = x.y;
   }
 }
-
-// Warps of a block and blocks an SM holds: as many as registers and the rings of shared memory leave room for
-// (kernels of the widest rows, 128 features in 8 bits, take smaller blocks to fill it).
-constexpr int warps_of(int D, bool q4) { return D == 128 && !q4 ? 4 : 8; }
-constexpr int held_of(int D, bool q4, int nt) {
-  return D == 128 && !q4 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1);
+// Their bits or-ed.
+template <int NB>
+__device__ __forceinline__ uint32_t scale_bits(uint32_t at) {
+  if constexpr (NB == 4) {
+    const uint2 x = lds64(at);
+    return x.x | x.y;
+  } else {
+    return lds32(at);
+  }
 }
+// Those of two keys one after the other, as fp16 pairs of the keys for each block; their bits or-ed.
+template <int NB>
+__device__ __forceinline__ uint32_t load_scale_pairs(uint32_t at, uint32_t (&d)[NB]) {
+  uint32_t u[NB];   // key 0's, key 1's
+  if constexpr (NB == 4) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at));
+  } else {
+    const uint2 x = lds64(at);
+    u[0] = x.x; u[1] = x.y;
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < NB / 2; ++i) {
+    d[2 * i] = __byte_perm(u[i], u[NB / 2 + i], 0x5410);
+    d[2 * i + 1] = __byte_perm(u[i], u[NB / 2 + i], 0x7632);
+    bits |= u[i] | u[NB / 2 + i];
+  }
+  return bits;
+}
+
+// Warps of a block and blocks an SM holds. Rows of 128 features want 168 registers a thread (at 128 they spill: 64
+// sequences of up to 8192 keys in 4 bits took 81 us with 16 warps on an SM, 76 us with these 12).
+constexpr int warps_of(int D) { return D == 128 ? 4 : 8; }
+constexpr int held_of(int D, int nt) { return D == 128 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
 
 // Slices of the list of `total` tiles over n blocks: where slice i begins, and the slice of a tile.
 __device__ __forceinline__ long long slice_begin(int i, long long total, int n) { return i * total / n; }
@@ -297,9 +332,9 @@ __device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int
 // A block's work: SLICES: slice blockIdx.x of the list; else the head blockIdx.x. NT * 8 query rows from
 // blockIdx.y * NT * 8 on.
 template <int D, bool Q4, int NT, bool SLICES>
-__global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) decode_kernel(DecodeArgs a) {
+__global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kernel(DecodeArgs a) {
   using S = Slot<D, Q4>;
-  constexpr int NB = S::NB, kWarps = warps_of(D, Q4), ROWS = NT * 8;
+  constexpr int NB = S::NB, kWarps = warps_of(D), ROWS = NT * 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int list[SLICES ? kMaxListed + 1 : 1];
   // the heads whose sums the block's warps leave unfinished, in the order of their tiles: two for each
@@ -314,9 +349,11 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
   const uint32_t mrow = lane * S::ROW;
   const int mperm = S::permuted(lane);
   const Masks masks = a.masks;
+  // -8 or -128 as fp16 in the units of the first and of the second half of a block: subnormal, minus 8, 128 or 128 steps
+  constexpr uint32_t kOff0 = Q4 ? 0x80088008u : 0x80808080u, kOff1 = 0x80808080u;
 
   float acc[NT][2 * NB][4];   // rows: features 16 i + 2 g (and + 1); columns: query rows 2 t, 2 t + 1
-  float base[NT][2];          // weights are 2^(score - base), base = largest score - level
+  float base[NT][2];          // weights are 2^(score - base)
   float sum[NT][2];           // of this lane's weights
 
   // The sums over tiles [first_tile, first_tile + tiles) of one head.
@@ -373,6 +410,7 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
     // of a key's block hold; each row by a power of two at the top of fp16's range, with the softmax
     // scale's sign
     uint32_t qf[NT][NB][2][2];
+    float bias[NT][NB][2];  // what the numbers' offset makes of a block's q, of columns 2 t and 2 t + 1
     float unscale[NT][2];   // scores in base 2, of columns 2 t and 2 t + 1: the products by this; not negative
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -391,25 +429,34 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
         }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^(14 - e) for a top in [2^e, 2^(e + 1)); exponents held to what 2^x and 2^-x both have
+      // 2^(14 - e) for a top in [2^e, 2^(e + 1)); exponents held to what 2^x and its inverse have room for
       const int e = (int)(__float_as_uint(top) >> 23) - 127;
-      const int up = top > 0.f && e < 128 ? min(14 - e, 126) : 0;
+      const int up = top > 0.f && e < 128 ? max(min(14 - e, 126), -100) : 0;
       const float f = copysignf(__uint_as_float((uint32_t)(127 + up) << 23), a.scale2);
-      const float back = __uint_as_float((uint32_t)(127 - up) << 23) * fabsf(a.scale2);
+      const float back = __uint_as_float((uint32_t)(127 + 24 - up) << 23) * fabsf(a.scale2);
 #pragma unroll
-      for (int k = 0; k < NB; ++k)
+      for (int k = 0; k < NB; ++k) {
+        float q_sum = 0.f;
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           const float x0 = bf16_lo(raw[k][st].x) * f, x1 = bf16_hi(raw[k][st].x) * f;
           const float x2 = bf16_lo(raw[k][st].y) * f, x3 = bf16_hi(raw[k][st].y) * f;
-          qf[n][k][st][0] = Q4 ? pack_f16x2(x0, x2) : pack_f16x2(x0, x1);
-          qf[n][k][st][1] = Q4 ? pack_f16x2(x1, x3) : pack_f16x2(x2, x3);
+          q_sum += (x0 + x1) + (x2 + x3);
+          const float down = Q4 && st == 1 ? 1.f / 16 : 1.f;   // high nibbles are 16 times as large
+          qf[n][k][st][0] = Q4 ? pack_f16x2(x0 * down, x2 * down) : pack_f16x2(x0, x1);
+          qf[n][k][st][1] = Q4 ? pack_f16x2(x1 * down, x3 * down) : pack_f16x2(x2, x3);
         }
+        q_sum += __shfl_xor_sync(0xffffffffu, q_sum, 1);
+        q_sum += __shfl_xor_sync(0xffffffffu, q_sum, 2);
+        q_sum *= Q4 ? -8.f / 16777216 : -128.f / 16777216;
+        bias[n][k][0] = __shfl_sync(0xffffffffu, q_sum, 8 * t);
+        bias[n][k][1] = __shfl_sync(0xffffffffu, q_sum, 8 * t + 4);
+      }
       unscale[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
       unscale[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
 
-    float mx[NT][2];            // largest product seen
+    float limit[NT][2];         // scores up to base + limit fit, limit = level + 8
     uint32_t fields[NT][2];     // exponent fields (at bit 10) of the V scales of all keys seen, or-ed
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -417,8 +464,8 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
       for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][i][j] = 0.f;
-      mx[n][0] = mx[n][1] = base[n][0] = base[n][1] = -CUDART_INF_F;
-      sum[n][0] = sum[n][1] = 0.f;
+      base[n][0] = base[n][1] = kNoBase;
+      sum[n][0] = sum[n][1] = limit[n][0] = limit[n][1] = 0.f;
       fields[n][0] = fields[n][1] = 0;
     }
     // keys that every query row sees: [all_from, all_to]
@@ -429,7 +476,7 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
       constexpr bool EDGE = decltype(on_edge)::value;
       // products of 2 x 16 keys
       float s[NT][2][4];
-      float d[4][NB];   // of keys g, g + 8, g + 16, g + 24
+      float d[4][NB];   // K's scales, of keys g, g + 8, g + 16, g + 24
 #pragma unroll
       for (int i = 0; i < 4; ++i) load_scales<NB>(at + S::KD_OFF + (8 * i + g) * S::SC, d[i]);
 #pragma unroll
@@ -452,7 +499,7 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             float c[4];
-            mma_f16_first(c, f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1], qf[n][k][0][0], qf[n][k][0][1]);
+            mma_f16_from(c, bias[n][k][0], bias[n][k][1], f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1], qf[n][k][0][0], qf[n][k][0][1]);
             mma_f16(c, f[2 * m][2], f[2 * m + 1][2], f[2 * m][3], f[2 * m + 1][3], qf[n][k][1][0], qf[n][k][1][1]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -460,21 +507,16 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
           }
       }
 
-      // The V scales. The level of a column is 29 - (the or of their exponent fields), which is no less than any of
-      // them: a scale is below 2^(15 - level), a weight at most 2^level, and their product below 2^15.
-      uint32_t bits[4];
+      // V's scales, of keys 2 t and 2 t + 1 of each eight, and their exponent fields or-ed.
+      uint32_t dv[4][NB], bits = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t raw = load_scales<NB>(at + S::VD_OFF + (8 * i + g) * S::SC, d[i]);
-        bits[i] = (raw | raw >> 16) & 0x7c00u;
-      }
-      uint32_t all = 0;
-      if constexpr (!EDGE) all = __reduce_or_sync(0xffffffffu, bits[0] | bits[1] | bits[2] | bits[3]);
+      for (int i = 0; i < 4; ++i) bits |= load_scale_pairs<NB>(at + S::VD_OFF + (8 * i + 2 * t) * S::SC, dv[i]);
+      bits = (bits | bits >> 16) & 0x7c00u;
 
-      uint32_t hidden[NT];   // bit 4 m + j: pair j of half m
+      uint32_t pt[NT][4];   // the weights as fp16: of query row g, keys 2 t and 2 t + 1 of each eight
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        hidden[n] = 0;
+        uint32_t hidden = 0;   // bit 4 m + j: pair j of half m
         if constexpr (EDGE) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -486,37 +528,50 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
                 const int key = first + 16 * m + g + 8 * u;
                 if (key > pos || (a.window > 0 && pos - key > a.window)) {
                   s[n][m][2 * u + j] = -CUDART_INF_F;
-                  hidden[n] |= 1u << (4 * m + 2 * u + j);
+                  hidden |= 1u << (4 * m + 2 * u + j);
                 }
               }
           }
         }
-        float now[2];
+        float top[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float top = fmaxf(fmaxf(s[n][0][j], s[n][0][j + 2]), fmaxf(s[n][1][j], s[n][1][j + 2]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          mx[n][j] = fmaxf(mx[n][j], top);
-          if constexpr (EDGE) {   // of the keys that this column sees
-            all = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) all |= (hidden[n] >> (2 * i + j)) & 1u ? 0u : bits[i];
-            all |= __shfl_xor_sync(0xffffffffu, all, 4);
-            all |= __shfl_xor_sync(0xffffffffu, all, 8);
-            all |= __shfl_xor_sync(0xffffffffu, all, 16);
-          }
-          fields[n][j] |= all;
-          const float level = fmaf((float)(int)fields[n][j], -1.f / 1024, 29.f);
-          now[j] = mx[n][j] == -CUDART_INF_F ? -level : fmaf(mx[n][j], unscale[n][j], -level);
-        }
-        if (__any_sync(0xffffffffu, now[0] != base[n][0] || now[1] != base[n][1])) {
+        for (int j = 0; j < 2; ++j) top[j] = fmaxf(fmaxf(s[n][0][j], s[n][0][j + 2]), fmaxf(s[n][1][j], s[n][1][j + 2]));
+        // The weights' reference stays until a score or a scale outgrows it, which no lane has to ask the others for.
+        const bool fits = fmaf(top[0], unscale[n][0], -base[n][0]) <= limit[n][0] &&
+                          fmaf(top[1], unscale[n][1], -base[n][1]) <= limit[n][1] &&
+                          (bits & ~(fields[n][0] & fields[n][1])) == 0;
+        if (EDGE || __any_sync(0xffffffffu, !fits)) {
+          // A column's level is 21 - (the or of the exponent fields of the scales it has seen, no less than any of
+          // them), and at most 7. A scale is below 2^(7 - level), the largest weight is 2^level when the reference is
+          // set and at most 2^(level + 8) later, and their product below 2^15.
+          uint32_t all = 0;
+          if constexpr (!EDGE) all = __reduce_or_sync(0xffffffffu, bits);
           float f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            f[j] = exp2_fast(base[n][j] - now[j]);   // 0 from a base of -inf
-            base[n][j] = now[j];
+            top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
+            top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
+            top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+            if constexpr (EDGE) {   // of the keys that this column sees
+              all = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t x = scale_bits<NB>(at + S::VD_OFF + (8 * i + g) * S::SC);
+                all |= (hidden >> (2 * i + j)) & 1u ? 0u : (x | x >> 16) & 0x7c00u;
+              }
+              all |= __shfl_xor_sync(0xffffffffu, all, 4);
+              all |= __shfl_xor_sync(0xffffffffu, all, 8);
+              all |= __shfl_xor_sync(0xffffffffu, all, 16);
+            }
+            fields[n][j] |= all;
+            const float level = fminf(fmaf((float)(int)fields[n][j], -1.f / 1024, 21.f), 7.f);
+            const float score = top[j] == -CUDART_INF_F ? -CUDART_INF_F : top[j] * unscale[n][j];
+            float now = base[n][j];
+            if (now != kNoBase) now += limit[n][j] - 8.f - level;   // as much as the level has fallen
+            if (score - now > level + 8.f) now = score - level;
+            f[j] = exp2_fast(base[n][j] - now);
+            base[n][j] = now;
+            limit[n][j] = level + 8.f;
             sum[n][j] *= f[j];
           }
 #pragma unroll
@@ -532,10 +587,12 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float p = exp2_fast(fmaf(s[n][m][j], unscale[n][j & 1], -base[n][j & 1]));
-            if constexpr (EDGE) p = (hidden[n] >> (4 * m + j)) & 1u ? 0.f : p;
+            if constexpr (EDGE) p = (hidden >> (4 * m + j)) & 1u ? -0.f : p;   // told from a weight that is small
             s[n][m][j] = p;
             sum[n][j & 1] += p;
           }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pt[n][i] = transpose8x8(pack_f16x2(s[n][i / 2][i % 2 * 2], s[n][i / 2][i % 2 * 2 + 1]));
       }
 
       // o += V^T (p d)
@@ -555,19 +612,28 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
           for (int i = 0; i < 4; ++i) pairs_q8<0, 2, 1, 3>(x[i], y[i], f[i]);
         }
 #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[i][0] = add_f16x2(f[i][0], kOff0);
+          f[i][1] = add_f16x2(f[i][1], kOff0);
+          f[i][2] = add_f16x2(f[i][2], kOff1);
+          f[i][3] = add_f16x2(f[i][3], kOff1);
+        }
+#pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            float w[4];
+            uint32_t w[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              w[j] = s[n][m][j] * d[2 * m + j / 2][k];
-              if constexpr (EDGE) w[j] = (hidden[n] >> (4 * m + j)) & 1u ? 0.f : w[j];   // its scale may be anything
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t p = pt[n][2 * m + i];
+              w[i] = mul_f16x2(p, dv[2 * m + i][k]);
+              if constexpr (EDGE) {   // a hidden key's scale may be anything
+                if ((p & 0xffffu) == 0x8000u) w[i] &= 0xffff0000u;
+                if (p >> 16 == 0x8000u) w[i] &= 0xffffu;
+              }
             }
-            const uint32_t b0 = transpose8x8(pack_f16x2(w[0], w[1]));
-            const uint32_t b1 = transpose8x8(pack_f16x2(w[2], w[3]));
-            mma_f16(acc[n][2 * k], f[2 * m][0], f[2 * m][1], f[2 * m + 1][0], f[2 * m + 1][1], b0, b1);
-            mma_f16(acc[n][2 * k + 1], f[2 * m][2], f[2 * m][3], f[2 * m + 1][2], f[2 * m + 1][3], b0, b1);
+            mma_f16(acc[n][2 * k], f[2 * m][0], f[2 * m][1], f[2 * m + 1][0], f[2 * m + 1][1], w[0], w[1]);
+            mma_f16(acc[n][2 * k + 1], f[2 * m][2], f[2 * m][3], f[2 * m + 1][2], f[2 * m + 1][3], w[0], w[1]);
           }
       }
     };
@@ -593,6 +659,12 @@ __global__ void __launch_bounds__(warps_of(D, Q4) * 32, held_of(D, Q4, NT)) deco
         sum[n][j] += __shfl_xor_sync(0xffffffffu, sum[n][j], 8);
         sum[n][j] += __shfl_xor_sync(0xffffffffu, sum[n][j], 16);
       }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[n][i][j] *= Q4 && i % 2 ? 1048576.f : 16777216.f;   // the operands' 2^-20 and 2^-24
   };
 
   // The sums of the last run as they are, rows of D.
@@ -812,12 +884,12 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
   const long long heads = (long long)c.B * c.Hkv;
   // One head a block when a head is at most four tiles a warp (no second kernel), and when the list of
   // sequences is too long for shared memory (heads enough for every SM then).
-  const int warps = warps_of(c.D, c.q4);
+  const int warps = warps_of(c.D);
   d.slices = tiles > 4 * warps && c.B <= kMaxListed;
   d.blocks = heads;
   if (d.slices) {
     // as many blocks as the SMs hold at a time, no slice below a tile a warp
-    const long long all = (long long)held_of(c.D, c.q4, d.nt) * sm_count() / d.row_blocks, some = heads * tiles / warps;
+    const long long all = (long long)held_of(c.D, d.nt) * sm_count() / d.row_blocks, some = heads * tiles / warps;
     d.blocks = all < some ? all : some;
     if (d.blocks < 1) d.blocks = 1;
     const size_t rows = (size_t)d.row_blocks * d.blocks * d.nt * 8;
@@ -848,7 +920,7 @@ fa_status check_decode(const fa_decode_params* p, const fa_cache* c, CacheView& 
 template <int D, bool Q4, int NT, bool SLICES>
 cudaError_t launch_decode(const DecodeArgs& a, dim3 grid, cudaStream_t st) {
   using S = Slot<D, Q4>;
-  constexpr int kWarps = warps_of(D, Q4), ring = kWarps * S::STAGES * S::BYTES, join = kWarps * NT * 8 * (D * 4 + 8);
+  constexpr int kWarps = warps_of(D), ring = kWarps * S::STAGES * S::BYTES, join = kWarps * NT * 8 * (D * 4 + 8);
   constexpr int bytes = ring > join ? ring : join;
   auto kernel = decode_kernel<D, Q4, NT, SLICES>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

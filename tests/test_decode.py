@@ -4,11 +4,11 @@ Tolerances, from the data of each case. A score is a sum of D products of whole 
 with Q_b the sum of |q| over a block, its partial sums stay below W Q_b (W = 8 in 4 bits, 127 in 8), and one accumulation of
 17 terms is off by at most 17 truncations, 2^-19 of that for the two of a block and the sum over blocks.
 So a score is off by at most E = 2^-19 scale sum_b |d_b| W Q_b over the keys a query sees; LSE by E and
-the roundings of a logarithm near it, 2^-20 (1 + |LSE|). A weight p is off by the factor e^(+-E); p * d is rounded to fp16 in
-units in which the largest weight is 2^level and every product below 2^15, with level = 29 - (the or of the exponent fields of
-the V scales it is summed with): off by 2^-11 / 2 of its value or, where that is subnormal, by 2^-25. The whole numbers are at
-most W, sum p is at least 1, and the result is rounded to bf16, 2^-8 of its value, so with n keys
-    |dO| <= (2^-12 + 2 E + 2^-16) sum p |v| / sum p + n W 2^(-25 - level) + 2^-8 |O|.
+the roundings of a logarithm near it, 2^-20 (1 + |LSE|). A weight p is off by the factor e^(+-E); in units in which the
+largest one is at least 2^level, level = min(7, 21 - (the or of the exponent fields of the V scales it is summed with)), p and then
+p * d are rounded to fp16: each is off by half a step, 2^-12 of its value, or 2^-25 where it is subnormal. The whole numbers
+are at most W, sum p is at least 1, and the result is rounded to bf16, 2^-8 of its value, so with n keys and scales up to d
+    |dO| <= (2^-11 + 2 E + 2^-16) sum p |v| / sum p + n W (1 + d) 2^(-25 - level) + 2^-8 |O|.
 """
 import ctypes
 import math
@@ -49,9 +49,10 @@ def score_error(q, planes, lengths, scale, window):
 
 
 def weight_step(planes, lengths, Hq, Sq, window):
-    """n W 2^(-25 - level) of the module's comment for every (b, head, token)."""
-    bits = planes[3].cpu().numpy().view(np.uint16).astype(np.int64)
-    bits = np.bitwise_or.reduce((bits >> 10) & 31, axis=-1)   # [B, Hkv, S]
+    """n W (1 + d) 2^(-25 - level) of the module's comment for every (b, head, token)."""
+    d = planes[3].cpu().numpy()
+    bits = np.bitwise_or.reduce((d.view(np.uint16).astype(np.int64) >> 10) & 31, axis=-1)   # [B, Hkv, S]
+    d = np.abs(d.astype(np.float64)).max(-1)
     w = 8.0 if planes[0].dtype == torch.uint8 else 127.0
     B, Hkv, _ = bits.shape
     out = np.zeros((B, Hq, Sq))
@@ -61,8 +62,9 @@ def weight_step(planes, lengths, Hq, Sq, window):
             first = max(0, pos - window) if window > 0 else 0
             if pos < first:
                 continue
-            fields = np.bitwise_or.reduce(bits[b, :, first:pos + 1], axis=-1)
-            out[b, :, i] = np.repeat((pos + 1 - first) * w * 2.0 ** (fields - 54.0), Hq // Hkv)
+            level = np.minimum(7.0, 21.0 - np.bitwise_or.reduce(bits[b, :, first:pos + 1], axis=-1))
+            step = (pos + 1 - first) * w * (1 + d[b, :, first:pos + 1].max(-1)) * 2.0 ** (-25.0 - level)
+            out[b, :, i] = np.repeat(step, Hq // Hkv)
     return out
 
 
@@ -79,7 +81,7 @@ def check(q, planes, lengths, got, scale=None, window=0):
     assert not bad.any(), (np.abs(lse - want_lse).max(), E.max())
     e, step = E[..., None], weight_step(planes, n, q.shape[1], q.shape[2], window)[..., None]
     err = np.abs(o - want)
-    assert np.all(err <= (2.0 ** -12 + 2 * e + 2.0 ** -16) * size + step + 2.0 ** -8 * np.abs(want)), err.max()
+    assert np.all(err <= (2.0 ** -11 + 2 * e + 2.0 ** -16) * size + step + 2.0 ** -8 * np.abs(want)), err.max()
     empty = want_lse == 0
     if empty.any():
         assert np.all(o[empty & (np.abs(want).sum(-1) == 0)] == 0)
