@@ -65,8 +65,8 @@ struct DecodeArgs {
   // slices only: what blocks leave of heads that they share, two slots a block, and the list
   float* part_o;         // [row blocks, blocks, 2, rows, D]: unnormalised
   float2* part_ml;       // [row blocks, blocks, 2, rows]: what the weights are relative to (base 2), and their sum
-  float* warp_o;         // what a warp leaves of a head that ends inside its run: as part_o, [row blocks, blocks, warps, rows, D]
-  float2* warp_ml;
+  float* warp_o;         // what a warp leaves of a head that ends inside its run: as part_o, [row blocks, blocks, warps, rows, D];
+  float2* warp_ml;       // not used where shared memory has room for it
   int* list;             // [B + 1]: tiles before sequence b, per key/value head
   unsigned* status;
   float scale2;          // scale * log2(e)
@@ -273,6 +273,12 @@ __device__ __forceinline__ uint32_t load_scale_pairs(uint32_t at, uint32_t (&d)[
 constexpr int warps_of(int D) { return D == 128 ? 4 : 8; }
 constexpr int held_of(int D, int nt) { return D == 128 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
 
+// Bytes of what a block's warps leave: [warps][rows][D] and [warps][rows] pairs. One set of it, of the heads that the
+// warps' runs end in, takes the rings' place at the end. The other, of the heads that end inside a run, has a place of
+// its own where that costs no block on an SM (not beside the rings of 128 features in 8 bits).
+constexpr int left_bytes(int D, int nt) { return warps_of(D) * nt * 8 * (D * 4 + 8); }
+constexpr bool left_in_memory(int D, bool q4, int nt) { return D == 128 && !q4 && nt == 1; }
+
 // Slices of the list of `total` tiles over n blocks: where slice i begins, and the slice of a tile.
 __device__ __forceinline__ long long slice_begin(int i, long long total, int n) { return i * total / n; }
 __device__ __forceinline__ int slice_of(long long tile, long long total, int n) { return (int)(((tile + 1) * n - 1) / total); }
@@ -345,6 +351,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   const int r0 = blockIdx.y * ROWS;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::STAGES * S::BYTES);
   const bool report = r0 == 0 && (!SLICES || blockIdx.x == 0);
+  if constexpr (SLICES) let_next_kernel_start();
   // the matrix row that this lane names: key `lane` of a tile
   const uint32_t mrow = lane * S::ROW;
   const int mperm = S::permuted(lane);
@@ -697,9 +704,16 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
       }
   };
 
-  float* so = reinterpret_cast<float*>(smem);   // [warp][rows][D], once every warp is done with its ring
-  float2* sml = reinterpret_cast<float2*>(smem + kWarps * ROWS * D * 4);
   const size_t block = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+  constexpr int RING = kWarps * S::STAGES * S::BYTES, FIRST = RING > left_bytes(D, NT) ? RING : left_bytes(D, NT);
+  float* so = reinterpret_cast<float*>(smem);   // of the heads that runs end in, once every warp is done with its ring
+  float2* sml = reinterpret_cast<float2*>(smem + kWarps * ROWS * D * 4);
+  float* fo = reinterpret_cast<float*>(smem + FIRST);   // of the heads that end inside a run
+  float2* fml = reinterpret_cast<float2*>(smem + FIRST + kWarps * ROWS * D * 4);
+  if constexpr (SLICES && left_in_memory(D, Q4, NT)) {
+    fo = a.warp_o + block * kWarps * ROWS * D;
+    fml = a.warp_ml + block * kWarps * ROWS;
+  }
   if (lane < 2) left_head[2 * warp + lane] = -1;
   __syncwarp();
 
@@ -743,7 +757,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
         left_head[2 * warp + keep] = b * a.c.Hkv + h;
         left_tiles[2 * warp + keep] = take;
       }
-      if (!keep) put(a.warp_o + (block * kWarps + warp) * ROWS * D, a.warp_ml + (block * kWarps + warp) * ROWS);
+      if (!keep) put(fo + warp * ROWS * D, fml + warp * ROWS);
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -752,7 +766,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   __syncthreads();
 
   // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k, which is of warp
-  // k / 2 (the head its run begins in, in memory, and the one it ends in, in shared memory).
+  // k / 2 (the head its run begins in, and the one it ends in).
   const int my_head = lane < 2 * kWarps ? left_head[lane] : -1;
   const int my_tiles = SLICES && my_head >= 0 ? left_tiles[lane] : 0;
   const int rows = min(ROWS, a.R - r0);
@@ -773,7 +787,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
     for (; unit < rows; unit += kWarps) {
       const int col = unit, r = r0 + col;
       float2 ml = make_float2(-CUDART_INF_F, 0.f);
-      if (mine) ml = (SLICES && !(lane & 1)) ? a.warp_ml[(block * kWarps + lane / 2) * ROWS + col] : sml[lane / 2 * ROWS + col];
+      if (mine) ml = ((SLICES && !(lane & 1)) ? fml : sml)[lane / 2 * ROWS + col];
       const float top = warp_max(ml.x);
       const float w = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
       const float l = warp_sum(w * ml.y);
@@ -784,7 +798,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
       for (uint32_t m = parts; m != 0; m &= m - 1) {
         const int k = __ffs(m) - 1;
         const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* src = k & 1 ? so + k / 2 * ROWS * D : a.warp_o + (block * kWarps + k / 2) * ROWS * D;
+        const float* src = (!SLICES || k & 1 ? so : fo) + k / 2 * ROWS * D;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) o[j] = fmaf(wk, src[col * D + lane * (D / 32) + j], o[j]);
       }
@@ -807,6 +821,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int bloc
   if (row >= all_rows) return;
   const int i = (int)(row % a.Sq), head = (int)(row / a.Sq % a.Hq), b = (int)(row / a.Sq / a.Hq);
   const int h = head / a.G, r = head % a.G * a.Sq + i;   // row of the key/value head
+  wait_for_kernel_before();
   const long long total = (long long)a.list[a.c.B] * a.c.Hkv;
   const int n = a.list[b + 1] - a.list[b];
   const long long begin = (long long)a.list[b] * a.c.Hkv + (long long)h * n;
@@ -895,8 +910,9 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
     const size_t rows = (size_t)d.row_blocks * d.blocks * d.nt * 8;
     d.part_ml = align_up(2 * rows * c.D * 4);
     d.warp_o = d.part_ml + align_up(2 * rows * 8);
-    d.warp_ml = d.warp_o + align_up(warps * rows * c.D * 4);
-    d.list = d.warp_ml + align_up(warps * rows * 8);
+    const size_t left = left_in_memory(c.D, c.q4, d.nt) ? warps * rows : 0;
+    d.warp_ml = d.warp_o + align_up(left * c.D * 4);
+    d.list = d.warp_ml + align_up(left * 8);
     d.total = d.list + align_up(((size_t)c.B + 1) * 4);
   }
   return d;
@@ -920,12 +936,12 @@ fa_status check_decode(const fa_decode_params* p, const fa_cache* c, CacheView& 
 template <int D, bool Q4, int NT, bool SLICES>
 cudaError_t launch_decode(const DecodeArgs& a, dim3 grid, cudaStream_t st) {
   using S = Slot<D, Q4>;
-  constexpr int kWarps = warps_of(D), ring = kWarps * S::STAGES * S::BYTES, join = kWarps * NT * 8 * (D * 4 + 8);
-  constexpr int bytes = ring > join ? ring : join;
+  constexpr int ring = warps_of(D) * S::STAGES * S::BYTES, left = left_bytes(D, NT);
+  constexpr int bytes = (ring > left ? ring : left) + (SLICES && !left_in_memory(D, Q4, NT) ? left : 0);
   auto kernel = decode_kernel<D, Q4, NT, SLICES>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kWarps * 32, bytes, st>>>(a);
+  kernel<<<grid, warps_of(D) * 32, bytes, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -1007,9 +1023,8 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
     const unsigned n = (unsigned)(few ? (rows + 7) / 8 : rows);
     auto join = cv.D == 64 ? (few ? decode_join_kernel<64, 1> : decode_join_kernel<64, 8>)
                            : (few ? decode_join_kernel<128, 1> : decode_join_kernel<128, 8>);
-    join<<<n, 256, 0, cs>>>(a, blocks, per, (long long)rows);
+    e = launch_after(join, dim3(n), 256, cs, a, blocks, per, (long long)rows);
     count_launches(1);
-    e = cudaGetLastError();
   }
   return cuda_status(e, "decode launch");
 }

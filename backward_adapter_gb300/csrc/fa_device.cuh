@@ -28,6 +28,27 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
+// Programmatic dependent launch: a kernel launched by launch_after may start while the one before it in
+// the stream still runs, once every block of that one has called let_next_kernel_start (or ended); what
+// it does before wait_for_kernel_before must not touch what the other writes. The wait ends when the
+// kernel before has finished and its writes are visible.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Threshold at and below which an additive mask value hides a pair (the
 // "mask floor" of the tiled backward in llama.cpp PR #57, commit 86c140d).
 constexpr float kMaskFloor = -1e9f;

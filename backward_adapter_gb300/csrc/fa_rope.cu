@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(RopeArgs a) {
     y0 += yv.sh;
   }
   if constexpr (NORM) {
+    let_next_kernel_start();
     __syncthreads();   // every lane is done with its slots
     float* part = reinterpret_cast<float*>(smem);   // [GROUPS][D]
 #pragma unroll
@@ -388,6 +389,7 @@ template <int D>
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ part, long long q_rows, long long rows,
                                                        float* __restrict__ dq_w, float* __restrict__ dk_w) {
   __shared__ float sums[64][17];
+  wait_for_kernel_before();
   const long long first = blockIdx.y ? q_rows : 0, last = blockIdx.y ? rows : q_rows;
   const int f = threadIdx.x % 16, slice = threadIdx.x / 16, d = blockIdx.x * 16 + f;
   float sum = 0.f;
@@ -638,9 +640,9 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
   if (e == cudaSuccess && p->norm) {
     const long long q_rows = (long long)g.x * g.q_chunks, rows = q_rows + (long long)g.x * g.k_chunks;
     auto dw = p->D == 64 ? rope_dw_kernel<64> : rope_dw_kernel<128>;
-    dw<<<dim3(p->D / 16, 2), 1024, 0, cs>>>(a.dw, q_rows, rows, p->Hq ? dq_weight : nullptr, p->Hkv ? dk_weight : nullptr);
+    e = launch_after(dw, dim3(p->D / 16, 2), 1024, cs, a.dw, q_rows, rows, p->Hq ? dq_weight : nullptr,
+                     p->Hkv ? dk_weight : nullptr);
     count_launches(1);
-    e = cudaGetLastError();
   }
   return cuda_status(e, "norm and rotation backward launch");
 }
