@@ -70,7 +70,7 @@ def _cache(k_q, k_d, v_q, v_d):
     if k_d.shape != scales or v_d.shape != scales:
         raise ValueError(f"k_d, v_d have shapes {tuple(k_d.shape)}, {tuple(v_d.shape)}, expected {scales}")
     on = k_q.get_device()
-    if k_d.get_device() != on or v_q.get_device() != on or v_d.get_device() != on:
+    if not (k_d.get_device() == on == v_q.get_device() == v_d.get_device()):
         raise ValueError("the planes of a cache must be on one device")
     ft._need_cuda(k_q, k_d, v_q, v_d)
     return B, Hkv, S, D, fmt, 0, k_q.data_ptr(), k_d.data_ptr(), v_q.data_ptr(), v_d.data_ptr()
@@ -108,11 +108,10 @@ def cache_write(k, v, k_q, k_d, v_q, v_d, begin, count=None, *, layout: str = "b
     device = k_q.device
     n = k.shape[2 if layout == "bhsd" else 1] if k.dim() == 4 else -1
     shape = _rows_shape(c, n, layout)
-    for name, t in (("k", k), ("v", v)):
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k, v have shapes {tuple(k.shape)}, {tuple(v.shape)}, expected {shape}")
+    if k.get_device() != device.index or v.get_device() != device.index:
+        raise ValueError(f"k is on {k.device}, v on {v.device}, the cache on {device}")
     if v.dtype != k.dtype:
         raise TypeError(f"v has dtype {v.dtype}, expected {k.dtype}")
     if isinstance(begin, torch.Tensor):
@@ -139,7 +138,7 @@ def cache_read(k_q, k_d, v_q, v_d, begin: int = 0, n_rows=None, *, dtype=torch.b
     shape = _rows_shape(c, n, layout)
     given = k is not None or v is not None
     k = torch.empty(shape, dtype=dtype, device=device) if k is None else k
-    v = torch.empty_like(k, memory_format=torch.contiguous_format) if v is None else v
+    v = ft._like(k) if v is None else v
     if given:
         for name, t in (("k", k), ("v", v)):
             if t.shape != shape:

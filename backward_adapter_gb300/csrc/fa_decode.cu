@@ -939,7 +939,8 @@ cudaError_t launch_decode(const DecodeArgs& a, dim3 grid, cudaStream_t st) {
   constexpr int ring = warps_of(D) * S::STAGES * S::BYTES, left = left_bytes(D, NT);
   constexpr int bytes = (ring > left ? ring : left) + (SLICES && !left_in_memory(D, Q4, NT) ? left : 0);
   auto kernel = decode_kernel<D, Q4, NT, SLICES>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(kernel, bytes, allowed);
   if (e != cudaSuccess) return e;
   kernel<<<grid, warps_of(D) * 32, bytes, st>>>(a);
   count_launches(1);

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fa {
 
 enum : int { DT_F32 = 0, DT_BF16 = 1 };
@@ -153,6 +155,21 @@ struct BwdSplit {
 void plan_bwd_split(const Shape& s, BwdSplit& out);
 // The plan as records (see fa_train_bwd_plan): returns the CTA count, writes at most `cap` records.
 int bwd_plan_records(const Shape& s, int32_t* rec, int cap);
+
+// Lets a kernel take `bytes` of dynamic shared memory on the current device: asked of the runtime once per kernel and
+// device (`done` has a bit for each device, one word for each kernel), as the call costs as much as a launch.
+template <typename K>
+cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // Streaming multiprocessors of the current device (queried once).
 int sm_count();

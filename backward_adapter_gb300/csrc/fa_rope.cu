@@ -489,13 +489,12 @@ fa_status check_apart(const Span* out, int n_out, const fa_rope_params* p, const
   return FA_OK;
 }
 
-template <typename K>
-cudaError_t launch_rope(K kernel, int smem, dim3 grid, const RopeArgs& a, cudaStream_t st) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<grid, 256, smem, st>>>(a);
+template <auto KERNEL>
+cudaError_t launch_rope(int smem, dim3 grid, const RopeArgs& a, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(KERNEL, smem, allowed);
+  if (e != cudaSuccess) return e;
+  KERNEL<<<grid, 256, smem, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -562,8 +561,8 @@ fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_vi
     using W = decltype(w);
     constexpr int D = decltype(dim)::value, E = decltype(e_run)::value;
     constexpr bool INTER = decltype(inter)::value;
-    if (p->norm) e = launch_rope(rope_fwd_kernel<T, W, D, E, INTER, true>, ring_bytes<T, E>(1), grid, a, cs);
-    else if constexpr (std::is_same_v<T, W>) e = launch_rope(rope_fwd_kernel<T, T, D, E, INTER, false>, ring_bytes<T, E>(1), grid, a, cs);
+    if (p->norm) e = launch_rope<rope_fwd_kernel<T, W, D, E, INTER, true>>(ring_bytes<T, E>(1), grid, a, cs);
+    else if constexpr (std::is_same_v<T, W>) e = launch_rope<rope_fwd_kernel<T, T, D, E, INTER, false>>(ring_bytes<T, E>(1), grid, a, cs);
   });
   return cuda_status(e, "norm and rotation launch");
 }
@@ -633,8 +632,8 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
     if constexpr (E == 4) {
       // the ring, which holds the groups' weight gradients at the end: 2 E x 256 floats
       constexpr int norm = ring_bytes<T, E>(2) > 2 * E * 256 * 4 ? ring_bytes<T, E>(2) : 2 * E * 256 * 4;
-      if (p->norm) e = launch_rope(rope_bwd_kernel<T, W, D, E, INTER, true>, norm, grid, a, cs);
-      else if constexpr (std::is_same_v<T, W>) e = launch_rope(rope_bwd_kernel<T, T, D, E, INTER, false>, ring_bytes<T, E>(1), grid, a, cs);
+      if (p->norm) e = launch_rope<rope_bwd_kernel<T, W, D, E, INTER, true>>(norm, grid, a, cs);
+      else if constexpr (std::is_same_v<T, W>) e = launch_rope<rope_bwd_kernel<T, T, D, E, INTER, false>>(ring_bytes<T, E>(1), grid, a, cs);
     }
   });
   if (e == cudaSuccess && p->norm) {

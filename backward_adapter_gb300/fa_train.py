@@ -301,6 +301,12 @@ def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optiona
     return got
 
 
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of t's shape, dtype and device. (empty_like's memory_format argument costs more than
+    a launch.)"""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _rows(t: torch.Tensor, layout: str):
     """The values of fa_view for a 4-D tensor in layout "bhsd" or "bshd", read or written where it is."""
     b, x, y, d = t.stride()

@@ -85,9 +85,9 @@ def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, fac
     if k.dtype != dtype:
         raise TypeError(f"k has dtype {k.dtype}, expected {dtype}")
     code = w_code = ft._dtype_code(q)
-    device = q.device
-    if k.device != device:
-        raise ValueError(f"k is on {k.device}, q on {device}")
+    on = q.get_device()
+    if k.get_device() != on:
+        raise ValueError(f"k is on {k.device}, q on {q.device}")
     norm = q_weight is not None
     if norm != (k_weight is not None):
         raise ValueError("give both q_weight and k_weight (norm and rotation), or neither (rotation alone)")
@@ -99,10 +99,10 @@ def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, fac
             w_code = ft.FA_F32
         if k_weight.dtype != w:
             raise TypeError(f"weights of dtype {w} and {k_weight.dtype}: both {dtype} or both float32")
-        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if t.shape != (D,):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(D,)}")
-            _small(name, t, device)
+        if q_weight.shape != (D,) or k_weight.shape != (D,):
+            raise ValueError(f"q_weight, k_weight have shapes {tuple(q_weight.shape)}, {tuple(k_weight.shape)}, expected {(D,)}")
+        if not (q_weight.is_contiguous() and k_weight.is_contiguous() and q_weight.get_device() == on == k_weight.get_device()):
+            raise ValueError(f"q_weight and k_weight must be contiguous and on {q.device}")
     rot = 0
     if inv_freq is not None:
         if inv_freq.dtype != torch.float32:
@@ -110,7 +110,8 @@ def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, fac
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq must be [rotary_dim / 2]")
         rot = 2 * inv_freq.shape[0]
-        _small("inv_freq", inv_freq, device)
+        if inv_freq.get_device() != on or not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq must be contiguous and on {q.device}")
     pos_stride = 0
     if positions is not None:
         if positions.dtype != torch.int64:
@@ -119,16 +120,10 @@ def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, fac
             pos_stride = S
         elif positions.shape != (S,):
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(S,)} or {(B, S)}")
-        _small("positions", positions, device)
+        if positions.get_device() != on or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous and on {q.device}")
     return (B, S, Hq, Hkv, D, code, w_code, rot, 1 if interleaved else 0, 1 if norm else 0, eps, factor, offset,
             pos_stride, 0, 0)
-
-
-def _small(name: str, t: torch.Tensor, device) -> None:
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, q on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def _same(name: str, t: torch.Tensor, like: torch.Tensor) -> None:
@@ -153,11 +148,11 @@ def qk_norm_rope(q, k, inv_freq, positions=None, q_weight=None, k_weight=None, *
     """
     p = _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, factor, offset, layout)
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = ft._like(q)
     else:
         _same("q_out", q_out, q)
     if k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        k_out = ft._like(k)
     else:
         _same("k_out", k_out, k)
     c = _Forward(*p, *ft._rows(q, layout), *ft._rows(k, layout), *ft._rows(q_out, layout), *ft._rows(k_out, layout))
@@ -182,11 +177,11 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, inv_freq, positions=None, q_weight=No
     _same("dq_out", dq_out, q)
     _same("dk_out", dk_out, k)
     if dq is None:
-        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        dq = ft._like(q)
     else:
         _same("dq", dq, q)
     if dk is None:
-        dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+        dk = ft._like(k)
     else:
         _same("dk", dk, k)
     c = _Backward(*p, *ft._rows(dq_out, layout), *ft._rows(dk_out, layout), *ft._rows(q, layout), *ft._rows(k, layout),
@@ -203,9 +198,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, inv_freq, positions=None, q_weight=No
         if dk_weight is None:
             dk_weight = torch.empty(D, dtype=torch.float32, device=device)
         for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-            if t.shape != (D,) or t.dtype != torch.float32:
-                raise ValueError(f"{name} must be float32 {(D,)}")
-            _small(name, t, device)
+            if t.shape != (D,) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+                raise ValueError(f"{name} must be float32 {(D,)}, contiguous and on {device}")
         ws_bytes = lib.fa_qk_norm_rope_bwd_workspace_size(at)
         ws = ft._scratch(ws_bytes, device, workspace, stream)
     else:
