@@ -5,7 +5,7 @@
 // Work: a row (one head of one token) is read once and written once, bound by HBM. D / (2 E) lanes hold
 // it, each with the two runs of E features that form E rotated pairs, so that a rotation never leaves a
 // lane: features E l .. and rot / 2 + E l .. for pairs (i, i + rot / 2), and 2 E l .. for interleaved
-// pairs and for the features that are not rotated. E is 8 in a long bf16 forward (see run_of), else 4. Such a group of lanes stays with one token for several heads, which share the token's cosines
+// pairs and for the features that are not rotated. E is 8 for many rows of bf16 (see run_of), else 4. Such a group of lanes stays with one token for several heads, which share the token's cosines
 // and sines. The next heads' rows are on their way to a ring in shared memory meanwhile, each lane's bytes
 // in slots of its own (cp.async; nothing to wait for but one's own copies): held in registers they would
 // cost the occupancy that hides their latency.
@@ -80,18 +80,25 @@ struct Run {
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(slot + i * 256 * UNIT) : "memory");
     }
   }
-  __device__ __forceinline__ void values(float* x) const {
+  // As pairs of consecutive features.
+  __device__ __forceinline__ void values(uint64_t* x) const {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(u[i]);
-      else x[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    for (int i = 0; i < E / 2; ++i) {
+      if constexpr (sizeof(T) == 4) x[i] = tc::f32x2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+      else x[i] = tc::f32x2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
     }
   }
-  __device__ __forceinline__ void store(T* p, const float* x) {
+  __device__ __forceinline__ void store(T* p, const uint64_t* x) {
 #pragma unroll
-    for (int i = 0; i < BYTES / 4; ++i) {
-      if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(x[i]);
-      else u[i] = tc::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < E / 2; ++i) {
+      float lo, hi;
+      tc::f32x2_split(x[i], lo, hi);
+      if constexpr (sizeof(T) == 4) {
+        u[2 * i] = __float_as_uint(lo);
+        u[2 * i + 1] = __float_as_uint(hi);
+      } else {
+        u[i] = tc::pack_bf16x2(lo, hi);
+      }
     }
     if constexpr (UNIT == 16) {
 #pragma unroll
@@ -152,9 +159,58 @@ struct Lane {
     }
   }
 
-  // The E pairs are (x[2 j], x[2 j + 1]) when interleaved, (x[j], x[E + j]) otherwise.
-  __device__ __forceinline__ static float& first(float (&x)[2 * E], int j) { return INTER ? x[2 * j] : x[j]; }
-  __device__ __forceinline__ static float& second(float (&x)[2 * E], int j) { return INTER ? x[2 * j + 1] : x[E + j]; }
+};
+
+__device__ __forceinline__ uint64_t twice(float x) { return tc::f32x2(x, x); }
+__device__ __forceinline__ uint64_t swapped(uint64_t x) {
+  float lo, hi;
+  tc::f32x2_split(x, lo, hi);
+  return tc::f32x2(hi, lo);
+}
+__device__ __forceinline__ float both(uint64_t x) {
+  float lo, hi;
+  tc::f32x2_split(x, lo, hi);
+  return lo + hi;
+}
+
+// The rotation of a lane's 2 E features, held as E pairs of neighbours x: the rotated pairs (p, q) are the neighbours
+// themselves when interleaved, else neighbours of x[i] with those of x[E / 2 + i]. In both cases
+// x'[i] = x[i] * a[i] + (what x[i] turns with) * b[i], packed.
+template <int E, bool INTER>
+struct Turn {
+  uint64_t a[E], b[E];
+
+  // By the lane's angles, or back; each feature times its weight first (w: as x).
+  template <bool BACK>
+  __device__ __forceinline__ Turn(const Lane<E, INTER>& l, const uint64_t (&w)[E], std::bool_constant<BACK>) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      a[i] = w[i];   // all there is to a lane that does not turn
+      b[i] = 0;
+      if (!l.turns) continue;
+      if constexpr (INTER) {
+        const float s = BACK ? -l.sn[i] : l.sn[i];
+        a[i] = tc::mul_f32x2(w[i], twice(l.cs[i]));
+        b[i] = tc::mul_f32x2(swapped(w[i]), tc::f32x2(-s, s));
+      } else {
+        const int j = i % (E / 2), other = i < E / 2 ? E / 2 + j : j;
+        const float s0 = (i < E / 2) != BACK ? -l.sn[2 * j] : l.sn[2 * j];
+        const float s1 = (i < E / 2) != BACK ? -l.sn[2 * j + 1] : l.sn[2 * j + 1];
+        a[i] = tc::mul_f32x2(w[i], tc::f32x2(l.cs[2 * j], l.cs[2 * j + 1]));
+        b[i] = tc::mul_f32x2(w[other], tc::f32x2(s0, s1));
+      }
+    }
+  }
+  __device__ __forceinline__ void operator()(uint64_t (&x)[E]) const {
+    uint64_t y[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const uint64_t with = INTER ? swapped(x[i]) : x[i < E / 2 ? E / 2 + i : i - E / 2];
+      y[i] = tc::fma_f32x2(with, b[i], tc::mul_f32x2(x[i], a[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = y[i];
+  }
 };
 
 // Heads on their way for each lane, and the ring that holds them (n tensors).
@@ -192,73 +248,53 @@ __global__ void __launch_bounds__(256) rope_fwd_kernel(RopeArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < kAhead - 1; ++i) ask(ring + i * STEP);
-  // What the pair (p, q) is multiplied by: u = p A - q B, v = q C + p S, with the weights in them.
-  float A[E], B[E], C[E], Sn[E];
-  {
-    float w[2 * E];
+  uint64_t w[E];
 #pragma unroll
-    for (int j = 0; j < 2 * E; ++j) w[j] = 1.f;
-    if constexpr (NORM) {
-      const W* wp = static_cast<const W*>(key ? a.w[1] : a.w[0]);
-      Run<W, E> run;
-      run.load(wp + lane.c0);
-      run.values(w);
-      run.load(wp + lane.c1);
-      run.values(w + E);
-    }
-    lane.angles(a, l, b, s);
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float p = L::first(w, j), q = L::second(w, j);
-      A[j] = lane.turns ? p * lane.cs[j] : p;
-      C[j] = lane.turns ? q * lane.cs[j] : q;
-      B[j] = lane.turns ? q * lane.sn[j] : 0.f;
-      Sn[j] = lane.turns ? p * lane.sn[j] : 0.f;
-    }
+  for (int i = 0; i < E; ++i) w[i] = twice(1.f);
+  if constexpr (NORM) {
+    const W* wp = static_cast<const W*>(key ? a.w[1] : a.w[0]);
+    Run<W, E> run;
+    run.load(wp + lane.c0);
+    run.values(w);
+    run.load(wp + lane.c1);
+    run.values(w + E / 2);
   }
+  lane.angles(a, l, b, s);
+  const Turn<E, INTER> turn(lane, w, std::false_type{});   // with the weights
   unsigned slot = 0;
   for (int h = 0; h < heads; ++h) {
     ask(ring + (slot + kAhead - 1) % kAhead * STEP);
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-    float x[2 * E];
+    uint64_t x[E];
     {
       R in;
       in.fetch(ring + slot * STEP);
       in.values(x);
       in.fetch(ring + slot * STEP + STEP / 2);
-      in.values(x + E);
+      in.values(x + E / 2);
     }
     slot = (slot + 1) % kAhead;
-    float r = 1.f;
+    uint64_t r = twice(1.f);
     if constexpr (NORM) {
-      float sq = 0.f;
+      uint64_t sq = tc::mul_f32x2(x[0], x[0]);
 #pragma unroll
-      for (int j = 0; j < 2 * E; ++j) sq = fmaf(x[j], x[j], sq);
-      r = rsqrtf(fmaf(group_sum<LANES>(sq), 1.f / D, a.s.eps));
+      for (int i = 1; i < E; ++i) sq = tc::fma_f32x2(x[i], x[i], sq);
+      r = twice(rsqrtf(fmaf(group_sum<LANES>(both(sq)), 1.f / D, a.s.eps)));
     }
     if (lane.turns) {
+      turn(x);
+    } else if constexpr (NORM) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        float &u = L::first(x, j), &v = L::second(x, j);
-        const float p = u, q = v;
-        u = fmaf(-q, B[j], p * A[j]);
-        v = fmaf(p, Sn[j], q * C[j]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        L::first(x, j) *= A[j];
-        L::second(x, j) *= C[j];
-      }
+      for (int i = 0; i < E; ++i) x[i] = tc::mul_f32x2(x[i], turn.a[i]);
     }
     if constexpr (NORM) {
 #pragma unroll
-      for (int j = 0; j < 2 * E; ++j) x[j] *= r;
+      for (int i = 0; i < E; ++i) x[i] = tc::mul_f32x2(x[i], r);
     }
     if (on) {
       R out;
       out.store(y0 + lane.c0, x);
-      out.store(y0 + lane.c1, x + E);
+      out.store(y0 + lane.c1, x + E / 2);
     }
     y0 += yv.sh;
   }
@@ -303,18 +339,22 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(RopeArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < kAhead - 1; ++i) ask(ring + i * STEP);
-  float w[2 * E], dw[2 * E];
+  uint64_t w[E], dw[E], one[E];
 #pragma unroll
-  for (int j = 0; j < 2 * E; ++j) dw[j] = 0.f;
+  for (int i = 0; i < E; ++i) {
+    dw[i] = 0;
+    one[i] = twice(1.f);
+  }
   if constexpr (NORM) {
     const W* wp = static_cast<const W*>(key ? a.w[1] : a.w[0]);
     Run<W, E> run;
     run.load(wp + lane.c0);
     run.values(w);
     run.load(wp + lane.c1);
-    run.values(w + E);
+    run.values(w + E / 2);
   }
   lane.angles(a, l, b, s);
+  const Turn<E, INTER> turn(lane, one, std::true_type{});
   unsigned slot = 0;
   for (int h = 0; h < heads; ++h) {
     ask(ring + (slot + kAhead - 1) % kAhead * STEP);
@@ -322,46 +362,40 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(RopeArgs a) {
     const uint32_t at = ring + slot * STEP;
     slot = (slot + 1) % kAhead;
     R in;
-    float g[2 * E];
+    uint64_t g[E];
     in.fetch(at);
     in.values(g);
     in.fetch(at + RUN);
-    in.values(g + E);
-    if (lane.turns) {
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        float &u = L::first(g, j), &v = L::second(g, j);
-        const float p = u, q = v;
-        u = fmaf(q, lane.sn[j], p * lane.cs[j]);
-        v = fmaf(-p, lane.sn[j], q * lane.cs[j]);
-      }
-    }
+    in.values(g + E / 2);
+    if (lane.turns) turn(g);
     if constexpr (NORM) {
-      float x[2 * E];
+      uint64_t x[E];
       in.fetch(at + 2 * RUN);
       in.values(x);
       in.fetch(at + 3 * RUN);
-      in.values(x + E);
-      float sq = 0.f, tx = 0.f;
+      in.values(x + E / 2);
+      uint64_t t[E];
 #pragma unroll
-      for (int j = 0; j < 2 * E; ++j) {
-        sq = fmaf(x[j], x[j], sq);
-        tx = fmaf(g[j] * w[j], x[j], tx);
+      for (int i = 0; i < E; ++i) t[i] = tc::mul_f32x2(g[i], w[i]);
+      uint64_t sq2 = tc::mul_f32x2(x[0], x[0]), tx2 = tc::mul_f32x2(t[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < E; ++i) {
+        sq2 = tc::fma_f32x2(x[i], x[i], sq2);
+        tx2 = tc::fma_f32x2(t[i], x[i], tx2);
       }
-      sq = group_sum<LANES>(sq);
-      tx = group_sum<LANES>(tx);
+      const float sq = group_sum<LANES>(both(sq2)), tx = group_sum<LANES>(both(tx2));
       const float r = rsqrtf(fmaf(sq, 1.f / D, a.s.eps));
-      const float m = tx * (1.f / D) * r * r;
+      const uint64_t r2 = twice(r), m2 = twice(-tx * (1.f / D) * r * r);
 #pragma unroll
-      for (int j = 0; j < 2 * E; ++j) {
-        if (on) dw[j] = fmaf(g[j], x[j] * r, dw[j]);
-        g[j] = r * fmaf(-x[j], m, g[j] * w[j]);
+      for (int i = 0; i < E; ++i) {
+        if (on) dw[i] = tc::fma_f32x2(g[i], tc::mul_f32x2(x[i], r2), dw[i]);
+        g[i] = tc::mul_f32x2(r2, tc::fma_f32x2(x[i], m2, t[i]));
       }
     }
     if (on) {
       R out;
       out.store(y0 + lane.c0, g);
-      out.store(y0 + lane.c1, g + E);
+      out.store(y0 + lane.c1, g + E / 2);
     }
     y0 += yv.sh;
   }
@@ -370,9 +404,9 @@ __global__ void __launch_bounds__(256) rope_bwd_kernel(RopeArgs a) {
     __syncthreads();   // every lane is done with its slots
     float* part = reinterpret_cast<float*>(smem);   // [GROUPS][D]
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      part[group * D + lane.c0 + j] = dw[j];
-      part[group * D + lane.c1 + j] = dw[E + j];
+    for (int i = 0; i < E; ++i) {
+      float* at = part + group * D + (i < E / 2 ? lane.c0 + 2 * i : lane.c1 + 2 * i - E);
+      tc::f32x2_split(dw[i], at[0], at[1]);
     }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += 256) {
@@ -411,17 +445,19 @@ struct RopeGrid {
   unsigned x;
 };
 
-// Features of a lane's runs.
-int run_of(const RopeShape& s, int dtype, bool backward) {
+// Features of a lane's runs. 8 make 16-byte copies of bf16 and half the work that a row costs besides its features (4 x 4096
+// tokens of 40 heads: 54 us, 58 with 4; their backward at half the size 45 and 49), 4 take fewer angles and registers (one
+// token of 8 sequences: 2.4 us, 3.1 with 8).
+int run_of(const RopeShape& s, int dtype) {
   const bool many = (long long)s.B * s.S * (s.Hq + s.Hkv) >= 1LL << 17;
-  return !backward && dtype == DT_BF16 && s.half % 8 == 0 && many ? 8 : 4;
+  return dtype == DT_BF16 && s.half % 8 == 0 && many ? 8 : 4;
 }
 
 RopeGrid rope_grid(const RopeShape& s, int D, int run) {
   const int groups = 256 / (D / (2 * run));
   const long long blocks = ((long long)s.B * s.S + groups - 1) / groups;
   const long long want = 2LL * sm_count();   // 8 and 1 measured slower where this decides (2042 tokens of 24 heads)
-  RopeGrid g{16, 0, 0, 0};
+  RopeGrid g{32, 0, 0, 0};
   while (g.chunk > 1 && blocks * ((s.Hq + g.chunk - 1) / g.chunk + (s.Hkv + g.chunk - 1) / g.chunk) < want) g.chunk /= 2;
   g.q_chunks = (s.Hq + g.chunk - 1) / g.chunk;
   g.k_chunks = (s.Hkv + g.chunk - 1) / g.chunk;
@@ -543,7 +579,7 @@ fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_vi
   if ((st = check_buffers(in, n, out, 2)) != FA_OK) return st;
   if ((st = check_apart(out, 2, p, inv_freq, positions)) != FA_OK) return st;
   if (p->S == 0) return FA_OK;
-  const int run = run_of(a.s, p->dtype, false);
+  const int run = run_of(a.s, p->dtype);
   const RopeGrid g = rope_grid(a.s, p->D, run);
   if (g.x == 0 || g.q_chunks + g.k_chunks > 65535) { set_error("too many rows for one launch"); return FA_ERR_UNSUPPORTED; }
   a.s.chunk = g.chunk;
@@ -570,7 +606,7 @@ fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_vi
 size_t fa_qk_norm_rope_bwd_workspace_size(const fa_rope_params* p) {
   RopeShape s;
   if (check_rope(p, s) != FA_OK || !p->norm || p->S == 0) return 0;
-  const RopeGrid g = rope_grid(s, p->D, run_of(s, p->dtype, true));
+  const RopeGrid g = rope_grid(s, p->D, run_of(s, p->dtype));
   return align_up((size_t)g.x * (g.q_chunks + g.k_chunks) * p->D * 4);
 }
 
@@ -610,7 +646,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
     if (e == cudaSuccess && out[3].n) e = cudaMemsetAsync(dk_weight, 0, out[3].n, cs);
     return cuda_status(e, "zero weight gradients");
   }
-  const int run = run_of(a.s, p->dtype, true);
+  const int run = run_of(a.s, p->dtype);
   const RopeGrid g = rope_grid(a.s, p->D, run);
   if (g.x == 0 || g.q_chunks + g.k_chunks > 65535) { set_error("too many rows for one launch"); return FA_ERR_UNSUPPORTED; }
   a.s.chunk = g.chunk;
@@ -629,12 +665,10 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
     using W = decltype(w);
     constexpr int D = decltype(dim)::value, E = decltype(e_run)::value;
     constexpr bool INTER = decltype(inter)::value;
-    if constexpr (E == 4) {
-      // the ring, which holds the groups' weight gradients at the end: 2 E x 256 floats
-      constexpr int norm = ring_bytes<T, E>(2) > 2 * E * 256 * 4 ? ring_bytes<T, E>(2) : 2 * E * 256 * 4;
-      if (p->norm) e = launch_rope<rope_bwd_kernel<T, W, D, E, INTER, true>>(norm, grid, a, cs);
-      else if constexpr (std::is_same_v<T, W>) e = launch_rope<rope_bwd_kernel<T, T, D, E, INTER, false>>(ring_bytes<T, E>(1), grid, a, cs);
-    }
+    // the ring, which holds the groups' weight gradients at the end: 2 E x 256 floats
+    constexpr int norm = ring_bytes<T, E>(2) > 2 * E * 256 * 4 ? ring_bytes<T, E>(2) : 2 * E * 256 * 4;
+    if (p->norm) e = launch_rope<rope_bwd_kernel<T, W, D, E, INTER, true>>(norm, grid, a, cs);
+    else if constexpr (std::is_same_v<T, W>) e = launch_rope<rope_bwd_kernel<T, T, D, E, INTER, false>>(ring_bytes<T, E>(1), grid, a, cs);
   });
   if (e == cudaSuccess && p->norm) {
     const long long q_rows = (long long)g.x * g.q_chunks, rows = q_rows + (long long)g.x * g.k_chunks;
