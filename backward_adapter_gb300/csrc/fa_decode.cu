@@ -27,7 +27,7 @@
 // Split: the tiles of 32 keys of all sequences and heads are one list, cut into equal slices, one for
 // each block that the SMs hold at a time, and those into one run of tiles for each warp: the end of one
 // head, whole heads and the beginning of another. A warp walks its run through its own ring of shared
-// memory (cp.async) with its own running maximum and waits for no other; heads that it shares with its
+// memory (cp.async) with a reference for its weights of its own and waits for no other; heads that it shares with its
 // block's other warps are joined when all are done, those that blocks share by a second kernel. Where
 // every head is a few tiles long a block takes one head, and there is no second kernel.
 #include <cuda_bf16.h>
@@ -52,10 +52,6 @@ constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
 constexpr float kNoBase = -3e38f; // below every score
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Masks of the low and the high nibbles of bytes 0 and 2. They come as kernel arguments: (x & mask) | one is a
-// single instruction with one constant known to the compiler, and two instructions with two.
-struct Masks { uint32_t low, high; };
-
 struct DecodeArgs {
   CacheView c;
   const __nv_bfloat16* q;
@@ -72,7 +68,6 @@ struct DecodeArgs {
   float scale2;          // scale * log2(e)
   int Hq, Sq, window, layout;
   int G, R;              // query heads and rows of a key/value head
-  Masks masks;
 };
 
 // The keys a sequence's queries may see: [lo, len), lo on a tile's border.
@@ -185,12 +180,12 @@ __device__ __forceinline__ uint32_t add_f16x2(uint32_t x, uint32_t y) {
 
 // Fp16 operands, numbers times 2^-24, from the packed words of a block. 4 bits, one word: the numbers of
 // bytes (0, 2) and (1, 3), first those of the low nibbles, then, 16 times as large, of the high ones.
-__device__ __forceinline__ void pairs_q4(uint32_t w, Masks m, uint32_t (&f)[4]) {
+__device__ __forceinline__ void pairs_q4(uint32_t w, uint32_t (&f)[4]) {
   const uint32_t h = w >> 8;
-  f[0] = w & m.low;
-  f[1] = h & m.low;
-  f[2] = w & m.high;
-  f[3] = h & m.high;
+  f[0] = w & 0x000f000fu;
+  f[1] = h & 0x000f000fu;
+  f[2] = w & 0x00f000f0u;
+  f[3] = h & 0x00f000f0u;
 }
 // 8 bits, one word of each half block, numbers + 128: bytes (A, B) and (C, D) of the first, then of the second.
 template <int A, int B, int C, int D>
@@ -355,7 +350,6 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   // the matrix row that this lane names: key `lane` of a tile
   const uint32_t mrow = lane * S::ROW;
   const int mperm = S::permuted(lane);
-  const Masks masks = a.masks;
   // -8 or -128 as fp16 in the units of the first and of the second half of a block: subnormal, minus 8, 128 or 128 steps
   constexpr uint32_t kOff0 = Q4 ? 0x80088008u : 0x80808080u, kOff1 = 0x80808080u;
 
@@ -493,7 +487,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
           uint32_t w[4];
           load_matrices<false>(at + mrow + 16 * (k ^ mperm), w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pairs_q4(w[i], masks, f[i]);
+          for (int i = 0; i < 4; ++i) pairs_q4(w[i], f[i]);
         } else {
           uint32_t w[4], x[4];
           load_matrices<false>(at + mrow + 16 * ((2 * k) ^ mperm), w);
@@ -506,7 +500,8 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             float c[4];
-            mma_f16_from(c, bias[n][k][0], bias[n][k][1], f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1], qf[n][k][0][0], qf[n][k][0][1]);
+            mma_f16_from(c, bias[n][k][0], bias[n][k][1], f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1],
+                         qf[n][k][0][0], qf[n][k][0][1]);
             mma_f16(c, f[2 * m][2], f[2 * m + 1][2], f[2 * m][3], f[2 * m + 1][3], qf[n][k][1][0], qf[n][k][1][1]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -610,7 +605,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
           uint32_t x[4];
           load_matrices<true>(at + S::V_OFF + mrow + 16 * (k ^ mperm), x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pairs_q4(x[i], masks, f[i]);
+          for (int i = 0; i < 4; ++i) pairs_q4(x[i], f[i]);
         } else {
           uint32_t x[4], y[4];
           load_matrices<true>(at + S::V_OFF + mrow + 16 * ((2 * k) ^ mperm), x);
@@ -752,7 +747,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
         finish(b, h);
         continue;
       }
-      keep = at == end;   // the run's last head stays in registers; its first goes to memory
+      keep = at == end;   // the run's last head stays in registers; its first is put away
       if (lane == 0) {
         left_head[2 * warp + keep] = b * a.c.Hkv + h;
         left_tiles[2 * warp + keep] = take;
@@ -1000,7 +995,6 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   a.Sq = p->Sq;
   a.window = p->window;
   a.layout = p->layout;
-  a.masks = Masks{0x000f000fu, 0x00f000f0u};
   a.G = p->Hq / cv.Hkv;
   a.R = a.G * p->Sq;
   if (plan.row_blocks > 65535 || plan.blocks > 0x7fffffffLL || rows > 0x7fffffffULL) { set_error("too many query rows for one launch"); return FA_ERR_UNSUPPORTED; }

@@ -151,11 +151,13 @@ struct Lane {
     const long long p = a.positions != nullptr ? __ldg(a.positions + b * r.pos_stride_b + s) : r.offset + s;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const unsigned long long t = (unsigned long long)p * turn_fraction(__ldg(a.inv_freq + E * l + j));
+      const float f = __ldg(a.inv_freq + E * l + j);
+      const unsigned long long t = (unsigned long long)p * turn_fraction(f);
       // the top 32 bits, signed: half turns of [-1, 1)
       sincospif((float)(int)(t >> 32) * 4.6566128730773926e-10f, &sn[j], &cs[j]);
-      cs[j] *= r.factor;
-      sn[j] *= r.factor;
+      const float by = r.factor + (f - f);   // not a number where f is infinite or none
+      cs[j] *= by;
+      sn[j] *= by;
     }
   }
 

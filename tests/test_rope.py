@@ -358,6 +358,17 @@ def test_weight_gradients_are_the_same_from_run_to_run_and_strided_outputs_are_l
 
 
 @pytest.mark.gpu
+def test_frequencies_that_are_no_numbers_show():
+    q = torch.randn((1, 2, 3, 64), device="cuda")
+    f = rope.rope_inv_freq(64, device="cuda")[0]
+    f[3], f[17] = float("nan"), float("inf")
+    y = rope.qk_norm_rope(q, q[:, :1], f)[0]
+    bad = torch.zeros(64, dtype=torch.bool, device="cuda")
+    bad[[3, 17, 35, 49]] = True
+    assert bool(y[..., bad].isnan().all()) and bool(y[..., ~bad].isfinite().all())
+
+
+@pytest.mark.gpu
 def test_no_tokens_and_broadcast_inputs():
     e = torch.empty((2, 4, 0, 64), dtype=torch.bfloat16, device="cuda")
     f = rope.rope_inv_freq(64, device="cuda")[0]
