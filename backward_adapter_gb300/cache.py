@@ -137,8 +137,9 @@ def cache_read(k_q, k_d, v_q, v_d, begin: int = 0, n_rows=None, *, dtype=torch.b
         raise ValueError(f"rows [{begin}, {begin + n}) outside the {S} keys")
     shape = _rows_shape(c, n, layout)
     given = k is not None or v is not None
-    k = torch.empty(shape, dtype=dtype, device=device) if k is None else k
-    v = ft._like(k) if v is None else v
+    strides = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
+    k = ft._empty(shape, strides, dtype, device) if k is None else k
+    v = ft._empty(shape, strides, k.dtype, device) if v is None else v
     if given:
         for name, t in (("k", k), ("v", v)):
             if t.shape != shape:
@@ -181,13 +182,13 @@ def decode(q, k_q, k_d, v_q, v_d, lengths=None, *, scale=None, window: int = 0, 
         raise ValueError(f"q is on {q.device}, the cache on {device}")
     ft._need_cuda(q)
     if out is None:
-        out = torch.empty_like(q)
+        out = ft._like(q)
     else:
         if out.shape != q.shape or out.dtype != q.dtype or out.device != device:
             raise ValueError(f"out must be {q.dtype} {tuple(q.shape)} on {device}")
         ft._need_cuda(out)
     if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=device)
+        lse = ft._empty((B, Hq, Sq), (Hq * Sq, Sq, 1), torch.float32, device)
     else:
         if lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != device:
             raise ValueError(f"lse must be float32 {(B, Hq, Sq)} on {device}")

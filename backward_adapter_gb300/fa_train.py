@@ -293,18 +293,33 @@ def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> Optional[torc
 def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
     """As _workspace, for a call on a stream of its own too: memory taken here is not handed out again before
     that stream is done with it."""
-    got = _workspace(nbytes, device, ws)
-    if stream is not None and got is not None and got is not ws:
+    if nbytes == 0 or (ws is not None and ws.numel() * ws.element_size() >= nbytes):
+        return ws
+    got = _empty((nbytes,), (1,), torch.uint8, device)
+    if stream is not None:
         s = _stream(device, stream)
         if s != torch.cuda.current_stream(device).cuda_stream:
             got.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(s, device))
     return got
 
 
+# The allocation that PyTorch's own compiled code makes: the caching allocator without the dispatcher and the device
+# guard, which cost several launches' time behind a launch. Where a version lacks it, torch.empty does.
+_empty_strided_cuda = getattr(getattr(torch._C, "_dynamo", None) and torch._C._dynamo.guards, "_empty_strided_cuda", None)
+
+
+def _empty(shape, strides, dtype, device: torch.device) -> torch.Tensor:
+    """A new contiguous tensor; `strides` are the contiguous ones of `shape` (both plain tuples)."""
+    on = device.index   # none for a tensor of the host
+    if on is not None and _empty_strided_cuda is not None and on == torch._C._cuda_getDevice():
+        return _empty_strided_cuda(shape, strides, dtype)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _like(t: torch.Tensor) -> torch.Tensor:
-    """A new contiguous tensor of t's shape, dtype and device. (empty_like's memory_format argument costs more than
-    a launch.)"""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    """A new contiguous tensor of the 4-D t's shape, dtype and device."""
+    b, x, y, z = t.shape
+    return _empty((b, x, y, z), (x * y * z, y * z, z, 1), t.dtype, t.device)
 
 
 def _rows(t: torch.Tensor, layout: str):

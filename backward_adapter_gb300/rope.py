@@ -194,9 +194,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, inv_freq, positions=None, q_weight=No
     if q_weight is not None:
         D = q.shape[3]
         if dq_weight is None:
-            dq_weight = torch.empty(D, dtype=torch.float32, device=device)
+            dq_weight = ft._empty((D,), (1,), torch.float32, device)
         if dk_weight is None:
-            dk_weight = torch.empty(D, dtype=torch.float32, device=device)
+            dk_weight = ft._empty((D,), (1,), torch.float32, device)
         for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
             if t.shape != (D,) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
                 raise ValueError(f"{name} must be float32 {(D,)}, contiguous and on {device}")
