@@ -117,7 +117,7 @@ def cache_write(k, v, k_q, k_d, v_q, v_d, begin, count=None, *, layout: str = "b
     if isinstance(begin, torch.Tensor):
         begins, first = _per_sequence("begin", begin, c[0], device), 0
     else:
-        begins, first = None, int(begin)
+        begins, first = None, ft._held(begin)
     counts = None if count is None else _per_sequence("count", count, c[0], device)
     call = _RowsCall(*c, *ft._rows(k, layout), *ft._rows(v, layout))
     at = ctypes.addressof(call)
@@ -138,8 +138,8 @@ def cache_read(k_q, k_d, v_q, v_d, begin: int = 0, n_rows=None, *, dtype=torch.b
     shape = _rows_shape(c, n, layout)
     given = k is not None or v is not None
     strides = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
-    k = ft._empty(shape, strides, dtype, device) if k is None else k
-    v = ft._empty(shape, strides, k.dtype, device) if v is None else v
+    k = ft._empty(shape, strides, dtype, device, stream) if k is None else k
+    v = ft._empty(shape, strides, k.dtype, device, stream) if v is None else v
     if given:
         for name, t in (("k", k), ("v", v)):
             if t.shape != shape:
@@ -182,19 +182,20 @@ def decode(q, k_q, k_d, v_q, v_d, lengths=None, *, scale=None, window: int = 0, 
         raise ValueError(f"q is on {q.device}, the cache on {device}")
     ft._need_cuda(q)
     if out is None:
-        out = ft._like(q)
+        out = ft._like(q, stream)
     else:
         if out.shape != q.shape or out.dtype != q.dtype or out.device != device:
             raise ValueError(f"out must be {q.dtype} {tuple(q.shape)} on {device}")
         ft._need_cuda(out)
     if lse is None:
-        lse = ft._empty((B, Hq, Sq), (Hq * Sq, Sq, 1), torch.float32, device)
+        lse = ft._empty((B, Hq, Sq), (Hq * Sq, Sq, 1), torch.float32, device, stream)
     else:
         if lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != device:
             raise ValueError(f"lse must be float32 {(B, Hq, Sq)} on {device}")
         ft._need_cuda(lse)
     lens = None if lengths is None else _per_sequence("lengths", lengths, B, device)
-    call = _DecodeCall(*c, Hq, Sq, int(window), code, 1.0 / math.sqrt(D) if scale is None else scale, 0)
+    window = min(max(int(window), -1), 0x7fffffff)   # as a 32-bit number; a longer window than any cache hides nothing
+    call = _DecodeCall(*c, Hq, Sq, window, code, 1.0 / math.sqrt(D) if scale is None else scale, 0)
     at = ctypes.addressof(call)
     lib = ft.load_library()
     ws_bytes = lib.fa_decode_workspace_size(at + _CACHE, at)

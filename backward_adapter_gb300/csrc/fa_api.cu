@@ -105,7 +105,7 @@ bool overlaps(const Span& a, const Span& b) {
   return a0 < b0 + b.n && b0 < a0 + a.n;
 }
 
-fa_status check_buffers(const Span* in, int nin, const Span* out, int nout) {
+fa_status check_buffers(const Span* in, int nin, const Span* out, int nout, bool apart) {
   for (int i = 0; i < nin + nout; ++i) {
     const Span& x = i < nin ? in[i] : out[i - nin];
     if (x.n == 0) continue;
@@ -116,7 +116,7 @@ fa_status check_buffers(const Span* in, int nin, const Span* out, int nout) {
     for (int i = 0; i < nin; ++i)
       if (overlaps(out[o], in[i])) { set_error("output %s overlaps input %s", out[o].name, in[i].name); return FA_ERR_INVALID_ARG; }
     for (int o2 = o + 1; o2 < nout; ++o2)
-      if (overlaps(out[o], out[o2])) { set_error("outputs %s and %s overlap", out[o].name, out[o2].name); return FA_ERR_INVALID_ARG; }
+      if (!(apart && o2 == 1) && overlaps(out[o], out[o2])) { set_error("outputs %s and %s overlap", out[o].name, out[o2].name); return FA_ERR_INVALID_ARG; }
   }
   return FA_OK;
 }
@@ -148,6 +148,17 @@ fa_status check_view(const fa_view* v, int B, int S, int H, int D, size_t es, bo
   out.p = v->ptr;
   out.n = (size_t)extent * es;
   return FA_OK;
+}
+
+bool side_by_side(const fa_view* a, int Ha, const fa_view* b, int Hb, int B, int S, int D, size_t es) {
+  if (a == nullptr || b == nullptr || Ha < 1 || Hb < 1) return false;
+  if ((S > 1 && a->stride_s != b->stride_s) || (B > 1 && a->stride_b != b->stride_b)) return false;
+  const int64_t step = S > 1 ? a->stride_s : a->stride_b;   // every token is a multiple of it after the first
+  if ((S == 1 && B == 1) || step < 1 || (S > 1 && B > 1 && a->stride_b % step != 0)) return false;
+  const int64_t bytes = step * (int64_t)es;
+  auto held = [&](const fa_view* v, int H) { return ((H > 1 ? (H - 1) * v->stride_h : 0) + D) * (int64_t)es; };
+  const int64_t from = ((int64_t)((uintptr_t)b->ptr - (uintptr_t)a->ptr) % bytes + bytes) % bytes;
+  return held(a, Ha) <= from && from + held(b, Hb) <= bytes;
 }
 
 fa_status check_ws(void* ws, size_t ws_bytes, size_t need, const Span* bufs, int n) {

@@ -25,8 +25,9 @@ inline bool too_large(double a, double b, double c, double d) { return a * b * c
 struct Span { const void* p; size_t n; const char* name; };
 
 bool overlaps(const Span& a, const Span& b);
-// Every buffer is there and 16-byte aligned; no output overlaps an input or another output.
-fa_status check_buffers(const Span* in, int nin, const Span* out, int nout);
+// Every buffer is there and 16-byte aligned; no output overlaps an input or another output (of the first two outputs the
+// caller may know it: `apart`).
+fa_status check_buffers(const Span* in, int nin, const Span* out, int nout, bool apart = false);
 // The workspace is large enough, 256-byte aligned and overlaps none of the call's buffers.
 fa_status check_ws(void* ws, size_t ws_bytes, size_t need, const Span* bufs, int n);
 fa_status cuda_status(cudaError_t e, const char* what);
@@ -34,6 +35,9 @@ fa_status cuda_status(cudaError_t e, const char* what);
 // An fa_view of B x S rows of H heads of D features of es bytes: fills `out` with the bytes it
 // spans. `written`: its rows must not overlap. A view without rows spans nothing and may be NULL.
 fa_status check_view(const fa_view* v, int B, int S, int H, int D, size_t es, bool written, const char* name, Span& out);
+// Two views of which no rows overlap, although the bytes they span may: parts of one tensor that lie side by side in each
+// token of it, as those of a fused projection's output do. Both have passed check_view.
+bool side_by_side(const fa_view* a, int Ha, const fa_view* b, int Hb, int B, int S, int D, size_t es);
 inline RowView row_view(const fa_view* v) {
   return v == nullptr ? RowView{nullptr, 0, 0, 0} : RowView{v->ptr, v->stride_b, v->stride_s, v->stride_h};
 }

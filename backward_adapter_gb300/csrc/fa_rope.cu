@@ -578,7 +578,7 @@ fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_vi
   if ((st = check_view(k_out, p->B, p->S, p->Hkv, p->D, es, true, "k_out", out[1])) != FA_OK) return st;
   int n = 2;
   if ((st = check_small(p, q_weight, k_weight, inv_freq, positions, in, n)) != FA_OK) return st;
-  if ((st = check_buffers(in, n, out, 2)) != FA_OK) return st;
+  if ((st = check_buffers(in, n, out, 2, side_by_side(q_out, p->Hq, k_out, p->Hkv, p->B, p->S, p->D, es))) != FA_OK) return st;
   if ((st = check_apart(out, 2, p, inv_freq, positions)) != FA_OK) return st;
   if (p->S == 0) return FA_OK;
   const int run = run_of(a.s, p->dtype);
@@ -635,7 +635,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
   out[3] = {dk_weight, p->norm && p->Hkv ? (size_t)p->D * 4 : 0, "dk_weight"};
   int n = 4;
   if ((st = check_small(p, q_weight, k_weight, inv_freq, positions, in, n)) != FA_OK) return st;
-  if ((st = check_buffers(in, n, out, 4)) != FA_OK) return st;
+  if ((st = check_buffers(in, n, out, 4, side_by_side(dq, p->Hq, dk, p->Hkv, p->B, p->S, p->D, es))) != FA_OK) return st;
   if ((st = check_apart(out, 4, p, inv_freq, positions)) != FA_OK) return st;
   cudaStream_t cs = (cudaStream_t)stream;
   const size_t need = fa_qk_norm_rope_bwd_workspace_size(p);

@@ -291,16 +291,12 @@ def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> Optional[torc
 
 
 def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
-    """As _workspace, for a call on a stream of its own too: memory taken here is not handed out again before
-    that stream is done with it."""
+    """As _workspace, from the memory of the call's stream, and with a look at the tensor that is given."""
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous and on {device}")
     if nbytes == 0 or (ws is not None and ws.numel() * ws.element_size() >= nbytes):
         return ws
-    got = _empty((nbytes,), (1,), torch.uint8, device)
-    if stream is not None:
-        s = _stream(device, stream)
-        if s != torch.cuda.current_stream(device).cuda_stream:
-            got.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(s, device))
-    return got
+    return _empty((nbytes,), (1,), torch.uint8, device, stream)
 
 
 # The allocation that PyTorch's own compiled code makes: the caching allocator without the dispatcher and the device
@@ -308,18 +304,34 @@ def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optiona
 _empty_strided_cuda = getattr(getattr(torch._C, "_dynamo", None) and torch._C._dynamo.guards, "_empty_strided_cuda", None)
 
 
-def _empty(shape, strides, dtype, device: torch.device) -> torch.Tensor:
-    """A new contiguous tensor; `strides` are the contiguous ones of `shape` (both plain tuples)."""
+def _empty(shape, strides, dtype, device: torch.device, stream=None) -> torch.Tensor:
+    """A new contiguous tensor; `strides` are the contiguous ones of `shape` (both plain tuples). With a stream it is
+    memory of that stream, which the current one's work may be using otherwise, and, as the caller gets it on the current
+    stream, not handed out again before both are done with it."""
+    if stream is not None and device.type == "cuda":
+        current = torch.cuda.current_stream(device)
+        s = _stream(device, stream)
+        if s != current.cuda_stream:
+            with torch.cuda.stream(torch.cuda.ExternalStream(s, device)):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
     on = device.index   # none for a tensor of the host
     if on is not None and _empty_strided_cuda is not None and on == torch._C._cuda_getDevice():
         return _empty_strided_cuda(shape, strides, dtype)
     return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _like(t: torch.Tensor) -> torch.Tensor:
+def _like(t: torch.Tensor, stream=None) -> torch.Tensor:
     """A new contiguous tensor of the 4-D t's shape, dtype and device."""
     b, x, y, z = t.shape
-    return _empty((b, x, y, z), (x * y * z, y * z, z, 1), t.dtype, t.device)
+    return _empty((b, x, y, z), (x * y * z, y * z, z, 1), t.dtype, t.device, stream)
+
+
+def _held(n) -> int:
+    """A Python number as the nearest one of an int64's range less its ends, which ctypes would wrap; the C ABI then
+    refuses it as it does any other that is out of its range."""
+    return min(max(int(n), 1 - (1 << 63)), (1 << 63) - 2)
 
 
 def _rows(t: torch.Tensor, layout: str):
@@ -526,13 +538,14 @@ def _fwd_cache(q4, q, k_q, k_d, v_q, v_d, mask, scale, causal, q_offset, window,
     kv = _kv_q4(k_q, k_d, v_q, v_d) if q4 else _kv_q8(k_q, k_d, v_q, v_d)
     p = make_params(q, _cache_shape_view(k_q, layout, q4), mask, scale=scale, causal=causal, q_offset=q_offset,
                     window=window, kv_format=FA_KV_Q4_0 if q4 else FA_KV_Q8_0, layout=layout)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((p.B, p.Hq, p.Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    out = _like(q, stream) if out is None else out
+    if lse is None:
+        lse = _empty((p.B, p.Hq, p.Sq), (p.Hq * p.Sq, p.Sq, 1), torch.float32, q.device, stream)
     _check_tensors(q, **_common_expect(p, layout, q, mask=mask, o=out, lse=lse),
                    **(_q4_expect if q4 else _q8_expect)(p, k_q, k_d, v_q, v_d))
     _need_cuda(q, mview, out, lse, k_q, k_d, v_q, v_d)
     ws_bytes = fwd_workspace_size(p)
-    ws = _workspace(ws_bytes, q.device, workspace)
+    ws = _scratch(ws_bytes, q.device, workspace, stream)
     call = lib.fa_train_fwd_q4 if q4 else lib.fa_train_fwd_q8
     with _on_device(q):
         _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
@@ -549,7 +562,7 @@ def _bwd_cache(q4, q, k_q, k_d, v_q, v_d, o, lse, do, mask, scale, causal, q_off
     p = make_params(q, _cache_shape_view(k_q, layout, q4), mask, scale=scale, causal=causal, q_offset=q_offset,
                     window=window, deterministic=deterministic, kv_format=FA_KV_Q4_0 if q4 else FA_KV_Q8_0,
                     layout=layout)
-    dq = torch.empty_like(q) if dq is None else dq
+    dq = _like(q, stream) if dq is None else dq
     if (dk_acc is None) != (dv_acc is None):
         raise ValueError("give both dk_acc and dv_acc, or neither")
     ks = _kv_shape(p, layout)
@@ -558,15 +571,16 @@ def _bwd_cache(q4, q, k_q, k_d, v_q, v_d, o, lse, do, mask, scale, causal, q_off
                    dv_acc=(dv_acc, ks, torch.float32), dk=(dk, ks, q.dtype), dv=(dv, ks, q.dtype))
     _need_cuda(q, o, lse, do, mview, dq, dk_acc, dv_acc, dk, dv, k_q, k_d, v_q, v_d)
     ws_bytes = bwd_workspace_size(p)
-    ws = _workspace(ws_bytes, q.device, workspace)
+    ws = _scratch(ws_bytes, q.device, workspace, stream)
     if dk_acc is not None:
         call = lib.fa_train_bwd_accum_q4 if q4 else lib.fa_train_bwd_accum_q8
         with _on_device(q):
             _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
                         _ptr(dk_acc), _ptr(dv_acc), _ptr(ws), ws_bytes, _stream(q.device, stream)))
         return dq
-    dk = torch.empty(shape, dtype=q.dtype, device=q.device) if dk is None else dk
-    dv = torch.empty(shape, dtype=q.dtype, device=q.device) if dv is None else dv
+    strides = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
+    dk = _empty(shape, strides, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(shape, strides, q.dtype, q.device, stream) if dv is None else dv
     call = lib.fa_train_bwd_q4 if q4 else lib.fa_train_bwd_q8
     with _on_device(q):
         _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),

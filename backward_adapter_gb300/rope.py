@@ -122,8 +122,8 @@ def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, fac
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(S,)} or {(B, S)}")
         if positions.get_device() != on or not positions.is_contiguous():
             raise ValueError(f"positions must be contiguous and on {q.device}")
-    return (B, S, Hq, Hkv, D, code, w_code, rot, 1 if interleaved else 0, 1 if norm else 0, eps, factor, offset,
-            pos_stride, 0, 0)
+    return (B, S, Hq, Hkv, D, code, w_code, rot, 1 if interleaved else 0, 1 if norm else 0, eps, factor,
+            offset if -(1 << 62) <= offset <= 1 << 62 else ft._held(offset), pos_stride, 0, 0)
 
 
 def _same(name: str, t: torch.Tensor, like: torch.Tensor) -> None:
@@ -148,11 +148,11 @@ def qk_norm_rope(q, k, inv_freq, positions=None, q_weight=None, k_weight=None, *
     """
     p = _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, factor, offset, layout)
     if q_out is None:
-        q_out = ft._like(q)
+        q_out = ft._like(q, stream)
     else:
         _same("q_out", q_out, q)
     if k_out is None:
-        k_out = ft._like(k)
+        k_out = ft._like(k, stream)
     else:
         _same("k_out", k_out, k)
     c = _Forward(*p, *ft._rows(q, layout), *ft._rows(k, layout), *ft._rows(q_out, layout), *ft._rows(k_out, layout))
@@ -172,16 +172,17 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, inv_freq, positions=None, q_weight=No
                      dk_weight: Optional[torch.Tensor] = None, workspace=None, stream=None):
     """Backward of qk_norm_rope: from the gradients of its outputs and its inputs, returns (dq, dk, dq_weight,
     dk_weight), the weights' in float32 and summed in a fixed order (None without weights). The other arguments are
-    the forward's; gradients and inputs may be strided like the forward's."""
+    the forward's; gradients and inputs may be strided like the forward's, and dq and dk may be parts of one tensor, as the
+    gradient of a fused projection's output is."""
     p = _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, factor, offset, layout)
     _same("dq_out", dq_out, q)
     _same("dk_out", dk_out, k)
     if dq is None:
-        dq = ft._like(q)
+        dq = ft._like(q, stream)
     else:
         _same("dq", dq, q)
     if dk is None:
-        dk = ft._like(k)
+        dk = ft._like(k, stream)
     else:
         _same("dk", dk, k)
     c = _Backward(*p, *ft._rows(dq_out, layout), *ft._rows(dk_out, layout), *ft._rows(q, layout), *ft._rows(k, layout),
@@ -194,9 +195,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, inv_freq, positions=None, q_weight=No
     if q_weight is not None:
         D = q.shape[3]
         if dq_weight is None:
-            dq_weight = ft._empty((D,), (1,), torch.float32, device)
+            dq_weight = ft._empty((D,), (1,), torch.float32, device, stream)
         if dk_weight is None:
-            dk_weight = ft._empty((D,), (1,), torch.float32, device)
+            dk_weight = ft._empty((D,), (1,), torch.float32, device, stream)
         for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
             if t.shape != (D,) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
                 raise ValueError(f"{name} must be float32 {(D,)}, contiguous and on {device}")

@@ -282,7 +282,8 @@ typedef struct fa_rope_params {
  * positions: int64 (8-byte aligned; element (b, s) at b * pos_stride_b + s) or NULL; inv_freq:
  * fp32 [rot / 2] (NULL when rot == 0); q_weight, k_weight: [D] in w_dtype, 16-byte aligned (NULL
  * when norm == 0). The views of a side with no heads are not looked at and may be NULL. Outputs
- * overlap neither the inputs nor each other.
+ * overlap neither the inputs nor each other; the two views that are written may lie side by side in
+ * each token of one tensor (a fused projection's output or its gradient).
  */
 FA_API fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_view* k, const void* q_weight,
                                  const void* k_weight, const float* inv_freq, const int64_t* positions,

@@ -264,3 +264,15 @@ def test_offsets_beyond_32_bits(fmt):
         np.testing.assert_array_equal(planes[i + 1][:, :, S - 6:].cpu().numpy(), d)
     q, d = ref.quantize(t.float().cpu().numpy(), fmt)
     np.testing.assert_array_equal(k.float().cpu().numpy(), rows_ref.to_bf16_bits(ref.values(q, d).astype(np.float32)))
+
+
+@pytest.mark.gpu
+def test_begins_that_a_64_bit_number_does_not_hold_are_refused():
+    planes = kv.new_cache(1, 2, 16, 64, "q4_0")
+    before = [t.clone() for t in planes]
+    x = torch.ones((1, 2, 3, 64), dtype=torch.bfloat16, device="cuda")
+    for begin in (14, -1, 1 << 63, 1 << 64, (1 << 64) + 2, -(1 << 64)):
+        with pytest.raises(ft.FaError, match="outside"):
+            kv.cache_write(x, x, *planes, begin)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(planes, before))

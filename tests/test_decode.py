@@ -262,3 +262,24 @@ def test_oracle_is_attention_of_a_causal_chunk():
         r = attn.backward(q, k, v, np.zeros_like(q), 0.125, causal=True, q_offset=17, window=window)
         np.testing.assert_allclose(o, r["o"], atol=1e-13)
         np.testing.assert_allclose(lse, r["lse"], atol=1e-13)
+
+
+@pytest.mark.gpu
+def test_windows_longer_than_any_cache_hide_nothing():
+    q, planes = make(2, 4, 2, 1400, 64, 2, "q4_0", 21)
+    want = kv.decode(q, *planes)
+    for window in (1400, (1 << 31) - 1, 1 << 31, (1 << 32) + 3, 1 << 70):
+        got = kv.decode(q, *planes, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for window in (-1, -(1 << 32) + 5):
+        with pytest.raises(ft.FaError, match="window"):
+            kv.decode(q, *planes, window=window)
+
+
+@pytest.mark.gpu
+def test_workspaces_that_do_not_fit_the_call_are_refused():
+    q, planes = make(2, 4, 2, 1400, 64, 1, "q4_0", 22)
+    for ws in (torch.empty(1 << 22, dtype=torch.uint8),
+               torch.empty((2, 1 << 22), dtype=torch.uint8, device="cuda").t()):
+        with pytest.raises(ValueError, match="workspace"):
+            kv.decode(q, *planes, workspace=ws)

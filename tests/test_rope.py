@@ -346,9 +346,14 @@ def test_weight_gradients_are_the_same_from_run_to_run_and_strided_outputs_are_l
     first = rope.qk_norm_rope_bwd(t["dq"], t["dk"], t["q"], t["k"], t["inv_freq"], **kw)
     whole = torch.full((c["B"], c["S"], c["Hq"] + c["Hkv"] + 3, c["D"]), 9.0, dtype=c["dtype"], device="cuda")
     dq, dk = whole[:, :, 1:1 + c["Hq"]], whole[:, :, 2 + c["Hq"]:2 + c["Hq"] + c["Hkv"]]
-    # the two outputs interleave in one buffer, which the call refuses: their byte ranges overlap
+    # side by side in one buffer they may be written, but not with a head that both have
     with pytest.raises(ft.FaError, match="overlap"):
-        rope.qk_norm_rope_bwd(t["dq"], t["dk"], t["q"], t["k"], t["inv_freq"], dq=dq, dk=dk, **kw)
+        both = whole[:, :, c["Hq"]:c["Hq"] + c["Hkv"]]
+        rope.qk_norm_rope_bwd(t["dq"], t["dk"], t["q"], t["k"], t["inv_freq"], dq=dq, dk=both, **kw)
+    rope.qk_norm_rope_bwd(t["dq"], t["dk"], t["q"], t["k"], t["inv_freq"], dq=dq, dk=dk, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], dq) and torch.equal(first[1], dk)
+    whole.fill_(9.0)
     again = rope.qk_norm_rope_bwd(t["dq"], t["dk"], t["q"], t["k"], t["inv_freq"], dq=dq, **kw)
     torch.cuda.synchronize()
     assert torch.equal(first[0], dq) and all(torch.equal(a, b) for a, b in zip(first[1:], again[1:]))
@@ -383,3 +388,65 @@ def test_no_tokens_and_broadcast_inputs():
     a = rope.qk_norm_rope(q, k1.expand(1, 4, 6, 64), f)[1]
     b = rope.qk_norm_rope(q, k1.expand(1, 4, 6, 64).contiguous(), f)[1]
     assert torch.equal(a, b)
+
+
+def side_views(p, base, shift, token):
+    """Views of p.Hq and p.Hkv heads in tokens of `token` elements, the second `shift` elements after the first."""
+    return [ft.FaView(base + 2 * at, p.S * token, token, p.D) for at in (0, shift)]
+
+
+def test_outputs_side_by_side_must_not_share_elements(lib):
+    """The parts of a fused projection's gradient may not reach into one another, whichever comes first."""
+    p = params()   # 4 and 2 heads of 64, 5 tokens, 2 sequences
+    f = 1 << 40
+    small, x = (f, f + 4096, f + 8192, f + 12288), views(1 << 32, p, 4)
+    sums = (f + (1 << 20), f + (2 << 20), f + (3 << 20), 1 << 30)
+    # one head of q in k; k's last head in the next token's q; k from the next token on, likewise; other strides
+    for shift, token in ((192, 512), (320, 384), (512 + 192, 512), (384 * 5 + 128, 384)):
+        a, b = side_views(p, 1 << 36, shift, token)
+        assert lib.fa_qk_norm_rope(R(p), R(x[0]), R(x[1]), *small, R(a), R(b), None) == ft.FA_ERR_INVALID_ARG
+        assert b"overlap" in lib.fa_last_error()
+        assert lib.fa_qk_norm_rope_bwd(R(p), *map(R, x), *small, R(a), R(b), *sums, None) == ft.FA_ERR_INVALID_ARG
+        assert b"overlap" in lib.fa_last_error()
+    a, b = side_views(p, 1 << 36, 256, 512)
+    b.stride_s = 576
+    assert lib.fa_qk_norm_rope(R(p), R(x[0]), R(x[1]), *small, R(a), R(b), None) == ft.FA_ERR_INVALID_ARG
+    a, b = side_views(p, 1 << 36, 256, 512)
+    a.stride_b = b.stride_b = 5 * 512 + 64   # the second sequence's tokens are elsewhere in the first's
+    assert lib.fa_qk_norm_rope(R(p), R(x[0]), R(x[1]), *small, R(a), R(b), None) == ft.FA_ERR_INVALID_ARG
+    assert b"overlap" in lib.fa_last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["bshd", "bhsd"])
+@pytest.mark.parametrize("B,S", [(1, 1), (3, 1), (1, 9), (2, 300)])
+def test_outputs_side_by_side_in_one_tensor(B, S, layout):
+    """Q and K, and their gradients, written into the parts of a fused projection's tensor; the rest of it stays."""
+    c = case(B, S, 4, 2, 128, 64, layout="bshd", strided=True, seed=20)
+    t = inputs(c)
+    kw = call_kw(c, t)
+    turn = (lambda x: x) if layout == "bshd" else (lambda x: x.transpose(1, 2))
+    kw["layout"] = layout
+    q, k, dq, dk = (turn(t[n]) for n in ("q", "k", "dq", "dk"))
+    want = rope.qk_norm_rope(q, k, t["inv_freq"], **kw)
+    want_bwd = rope.qk_norm_rope_bwd(dq, dk, q, k, t["inv_freq"], **kw)
+    for first in ("q", "k"):
+        parts = (slice(0, 4), slice(4, 6)) if first == "q" else (slice(2, 6), slice(0, 2))
+        whole, grad = (torch.full((B, S, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        a, b = (turn(whole[:, :, x]) for x in parts)
+        rope.qk_norm_rope(q, k, t["inv_freq"], q_out=a, k_out=b, **kw)
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and bool((whole[:, :, 6:] == 3).all())
+        a, b = (turn(grad[:, :, x]) for x in parts)
+        got = rope.qk_norm_rope_bwd(dq, dk, q, k, t["inv_freq"], dq=a, dk=b, **kw)
+        assert got[0] is a and all(torch.equal(x, y) for x, y in zip(got, want_bwd)) and bool((grad[:, :, 6:] == 3).all())
+
+
+def test_offsets_that_a_64_bit_number_does_not_hold_are_refused(lib):
+    t = inputs(case(2, 5, 4, 2, 64, 64), "cpu")
+    for n in (1 << 63, 1 << 64, -(1 << 64), (1 << 62) + 1):
+        v = rope._params(t["q"], t["k"], t["inv_freq"], None, t["qw"], t["kw"], 1e-6, False, 1.0, n, "bhsd")
+        p, good = ft.FaRopeParams(*v[:-1]), params()
+        x = views(1 << 32, good, 4)
+        f = 1 << 40
+        assert lib.fa_qk_norm_rope(R(p), R(x[0]), R(x[1]), f, f + 4096, f + 8192, None, R(x[2]), R(x[3]), None) == 1
+        assert b"offset" in lib.fa_last_error()

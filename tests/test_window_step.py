@@ -182,3 +182,46 @@ def test_training_chunk_over_the_window():
         e = np.abs(n(got) - ref).max()
         assert e <= 2e-2 * np.abs(ref).max() + 2e-3, e
     assert np.abs(n(o) - a["o"]).max() <= 1e-2 * np.abs(a["o"]).max() + 1e-3
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_memory_of_a_call_on_a_stream_of_its_own(handle):
+    """Memory that the current stream's work still reads is not what a call on another stream is given to write, for
+    its results or its scratch; nor is what it wrote given out again while the current stream reads that."""
+    B, Hq, Hkv, S, D = 1, 8, 2, 2048, 128
+    s = step_state(B, Hq, Hkv, S, D, "q4_0", 31)
+    lens = torch.tensor([S], device="cuda")
+    q = torch.randn((B, Hq, 64, D), device="cuda").to(torch.bfloat16)
+    one = q[:, :, :1].contiguous()
+    rot = s["f"]
+    calls = {
+        "decode": lambda st: fa.decode(one, *s["planes"], lens, stream=st),
+        "rope": lambda st: fa.qk_norm_rope(q, q[:, :Hkv], rot, stream=st),
+        "read": lambda st: fa.cache_read(*s["planes"], stream=st),
+        "fwd": lambda st: fa.fwd_q4(q, *s["planes"], stream=st),
+        "bwd": lambda st: fa.bwd_q4(q, *s["planes"], *fwd, q, deterministic=True, stream=st),
+    }
+    fwd = fa.fwd_q4(q, *s["planes"])
+    want = {n: [x.clone() for x in f(None)] for n, f in calls.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for n, f in calls.items():
+        sizes = [x.numel() * x.element_size() for x in want[n]] + [1 << 22, 1 << 24]
+        held, sums = [torch.full((b,), 7, dtype=torch.uint8, device="cuda") for b in sizes], []
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)   # the current stream is behind: it reads these later
+        for h in held:
+            sums.append((h != 7).sum())
+        del held, h                     # its memory is free for what comes on this stream
+        got = f(side.cuda_stream if handle else side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(20_000_000)
+        same = [(a != b).sum() for a, b in zip(got, want[n])]
+        del got                         # likewise, and the side stream goes on
+        with torch.cuda.stream(side):
+            again = [torch.full((b,), 1, dtype=torch.uint8, device="cuda") for b in sizes]
+        torch.cuda.synchronize()
+        assert [int(x) for x in sums] == [0] * len(sums), n
+        assert [int(x) for x in same] == [0] * len(same), n
+        del again
