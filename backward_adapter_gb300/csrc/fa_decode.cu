@@ -58,12 +58,11 @@ struct DecodeArgs {
   __nv_bfloat16* o;
   float* lse;
   const int64_t* lengths;
-  // slices only: what blocks leave of heads that they share, two slots a block, and the list
+  // slices only: what blocks leave of heads that they share, two slots a block
   float* part_o;         // [row blocks, blocks, 2, rows, D]: unnormalised
   float2* part_ml;       // [row blocks, blocks, 2, rows]: what the weights are relative to (base 2), and their sum
   float* warp_o;         // what a warp leaves of a head that ends inside its run: as part_o, [row blocks, blocks, warps, rows, D];
   float2* warp_ml;       // not used where shared memory has room for it
-  int* list;             // [B + 1]: tiles before sequence b, per key/value head
   unsigned* status;
   float scale2;          // scale * log2(e)
   int Hq, Sq, window, layout;
@@ -126,6 +125,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+// Kept where it is among the copies.
+__device__ __forceinline__ uint2 ld_global64(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 // Four 8 x 8 matrices of 16-bit elements, lane i naming row i % 8 of matrix i / 8: of matrix j lane
@@ -274,9 +279,16 @@ constexpr int held_of(int D, int nt) { return D == 128 ? (nt == 1 ? 3 : 2) : (nt
 constexpr int left_bytes(int D, int nt) { return warps_of(D) * nt * 8 * (D * 4 + 8); }
 constexpr bool left_in_memory(int D, bool q4, int nt) { return D == 128 && !q4 && nt == 1; }
 
-// Slices of the list of `total` tiles over n blocks: where slice i begins, and the slice of a tile.
-__device__ __forceinline__ long long slice_begin(int i, long long total, int n) { return i * total / n; }
-__device__ __forceinline__ int slice_of(long long tile, long long total, int n) { return (int)(((tile + 1) * n - 1) / total); }
+// `total` tiles (below 2^30: 2^40 elements at most) cut into n slices that differ by a tile at most, the larger ones first.
+struct Slices {
+  unsigned each, more;
+  __device__ __forceinline__ Slices(unsigned total, unsigned n) : each(total / n), more(total % n) {}
+  __device__ __forceinline__ unsigned begin(unsigned i) const { return i * each + min(i, more); }
+  __device__ __forceinline__ unsigned of(unsigned tile) const {
+    const unsigned large = more * (each + 1);
+    return tile < large ? tile / (each + 1) : more + (tile - large) / each;
+  }
+};
 
 // Tiles before each sequence, per key/value head, into list[0 .. B] in shared memory (all threads).
 __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool report) {
@@ -305,10 +317,21 @@ __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool r
     }
     if (b < a.c.B) list[b] = before + x - n;
     before += all;
+    if (b == a.c.B - 1) list[a.c.B] = before;
     __syncthreads();
   }
-  if (threadIdx.x == 0) list[a.c.B] = before;
-  __syncthreads();
+}
+
+// The sequence that tile `at` of all heads' is of (all lanes of a warp, one answer): the last that begins at or before it.
+__device__ __forceinline__ int sequence_of(const int* list, int B, unsigned heads, unsigned at) {
+  const int lane = threadIdx.x & 31, step = (B + 31) / 32;
+  const int far = lane * step;
+  int b = (__popc(__ballot_sync(0xffffffffu, far < B && list[min(far, B)] * heads <= at)) - 1) * step;
+  if (step > 1) {
+    const int near = b + lane;
+    b += __popc(__ballot_sync(0xffffffffu, lane < step && near < B && list[min(near, B)] * heads <= at)) - 1;
+  }
+  return b;
 }
 
 // Row r of a head from a warp's sums (D / 32 features a lane): the result, or what is left of it.
@@ -318,8 +341,8 @@ __device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int
   constexpr int F = D / 32;
   const int lane = threadIdx.x & 31;
   if (!whole) {
-#pragma unroll
-    for (int j = 0; j < F; ++j) part_o[lane * F + j] = o[j];
+    if constexpr (F == 4) reinterpret_cast<float4*>(part_o)[lane] = make_float4(o[0], o[1], o[2], o[3]);
+    else reinterpret_cast<float2*>(part_o)[lane] = make_float2(o[0], o[1]);
     if (lane == 0) *part_ml = make_float2(top, l);
     return;
   }
@@ -401,6 +424,21 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 
+    // the query rows on their way before the tiles that would hold them up: of row g of each eight the features
+    // 4 t .. 4 t + 3 of every half block
+    uint2 raw[NT][NB][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = r0 + n * 8 + g;
+      const __nv_bfloat16* src = a.q + (r < a.R ? q_offset(a, b, h, r) : 0) + 4 * t;
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          raw[n][k][st] = make_uint2(0, 0);
+          if (r < a.R) raw[n][k][st] = ld_global64(src + 32 * k + 16 * st);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < S::STAGES - 1; ++i) {
       if (i < tiles) load(ring + i * S::BYTES);
@@ -415,18 +453,13 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
     float unscale[NT][2];   // scores in base 2, of columns 2 t and 2 t + 1: the products by this; not negative
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = r0 + n * 8 + g;
-      const __nv_bfloat16* src = a.q + (r < a.R ? q_offset(a, b, h, r) : 0) + 4 * t;
-      uint2 raw[NB][2];   // features 4 t .. 4 t + 3 of each half block
       float top = 0.f;
 #pragma unroll
       for (int k = 0; k < NB; ++k)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-          raw[k][st] = make_uint2(0, 0);
-          if (r < a.R) raw[k][st] = __ldg(reinterpret_cast<const uint2*>(src + 32 * k + 16 * st));
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(raw[k][st].x)), fabsf(bf16_hi(raw[k][st].x))),
-                                 fmaxf(fabsf(bf16_lo(raw[k][st].y)), fabsf(bf16_hi(raw[k][st].y)))));
+          const uint2 x = raw[n][k][st];
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(x.x)), fabsf(bf16_hi(x.x))), fmaxf(fabsf(bf16_lo(x.y)), fabsf(bf16_hi(x.y)))));
         }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -440,8 +473,8 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
         float q_sum = 0.f;
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-          const float x0 = bf16_lo(raw[k][st].x) * f, x1 = bf16_hi(raw[k][st].x) * f;
-          const float x2 = bf16_lo(raw[k][st].y) * f, x3 = bf16_hi(raw[k][st].y) * f;
+          const float x0 = bf16_lo(raw[n][k][st].x) * f, x1 = bf16_hi(raw[n][k][st].x) * f;
+          const float x2 = bf16_lo(raw[n][k][st].y) * f, x3 = bf16_hi(raw[n][k][st].y) * f;
           q_sum += (x0 + x1) + (x2 + x3);
           const float down = Q4 && st == 1 ? 1.f / 16 : 1.f;   // high nibbles are 16 times as large
           qf[n][k][st][0] = Q4 ? pack_f16x2(x0 * down, x2 * down) : pack_f16x2(x0, x1);
@@ -712,7 +745,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   if (lane < 2) left_head[2 * warp + lane] = -1;
   __syncwarp();
 
-  long long slice = 0;   // the first tile of the block
+  unsigned slice = 0;    // the first tile of the block
   bool keep = false;     // the last run is of a head that is left to the block
   if constexpr (!SLICES) {
     const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
@@ -723,27 +756,19 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
     if (lane == 0) left_head[2 * warp + 1] = blockIdx.x;
   } else {
     make_list(a, list, report);
-    if (report)   // for the joining kernel
-      for (int i = threadIdx.x; i <= a.c.B; i += kWarps * 32) a.list[i] = list[i];
-    const long long total = (long long)list[a.c.B] * a.c.Hkv;
-    slice = slice_begin(blockIdx.x, total, gridDim.x);
-    const int tiles = (int)(slice_begin(blockIdx.x + 1, total, gridDim.x) - slice);
-    long long at = slice + (long long)tiles * warp / kWarps;
-    const long long end = slice + (long long)tiles * (warp + 1) / kWarps;
+    const Slices slices((unsigned)list[a.c.B] * a.c.Hkv, gridDim.x);
+    slice = slices.begin(blockIdx.x);
+    const Slices runs(slices.begin(blockIdx.x + 1) - slice, kWarps);
+    unsigned at = slice + runs.begin(warp);
+    const unsigned end = slice + runs.begin(warp + 1);
     while (at < end) {
-      int b = 0, last = a.c.B - 1;   // the last sequence that begins at or before tile `at`
-      while (b < last) {
-        const int mid = (b + last + 1) / 2;
-        if ((long long)list[mid] * a.c.Hkv <= at) b = mid;
-        else last = mid - 1;
-      }
-      const int n = list[b + 1] - list[b];
-      const long long off = at - (long long)list[b] * a.c.Hkv;
+      const int b = sequence_of(list, a.c.B, a.c.Hkv, at);
+      const unsigned n = list[b + 1] - list[b], off = at - (unsigned)list[b] * a.c.Hkv;
       const int h = (int)(off / n), tile = (int)(off % n);
-      const int take = (int)min((long long)(n - tile), end - at);
+      const int take = (int)min(n - tile, end - at);
       run(b, h, key_range(a, b, false), tile, take);
       at += take;
-      if (take == n) {
+      if (take == (int)n) {
         finish(b, h);
         continue;
       }
@@ -760,32 +785,43 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   if (keep) put(so + warp * ROWS * D, sml + warp * ROWS);
   __syncthreads();
 
-  // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k, which is of warp
-  // k / 2 (the head its run begins in, and the one it ends in).
-  const int my_head = lane < 2 * kWarps ? left_head[lane] : -1;
-  const int my_tiles = SLICES && my_head >= 0 ? left_tiles[lane] : 0;
+  // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k (and its lanes k + PARTS, ...
+  // do too), which is of warp k / 2: the head its run begins in, and the one it ends in.
+  constexpr int PARTS = 2 * kWarps;
+  using V = std::conditional_t<D == 128, float4, float2>;
+  const int mine_k = lane % PARTS;
+  const int my_head = left_head[mine_k];
+  const int my_tiles = SLICES && my_head >= 0 && lane < PARTS ? left_tiles[mine_k] : 0;
+  const float2* my_ml = (SLICES && !(mine_k & 1) ? fml : sml) + mine_k / 2 * ROWS;
   const int rows = min(ROWS, a.R - r0);
   int unit = warp;   // counts down the rows until this warp's next one
-  for (uint32_t rest = __ballot_sync(0xffffffffu, my_head >= 0); rest != 0;) {
+  for (uint32_t rest = __ballot_sync(0xffffffffu, my_head >= 0) & ((1u << PARTS) - 1); rest != 0;) {
     const int head = __shfl_sync(0xffffffffu, my_head, __ffs(rest) - 1);
     const bool mine = my_head == head;
-    const uint32_t parts = __ballot_sync(0xffffffffu, mine);
+    const uint32_t parts = __ballot_sync(0xffffffffu, mine) & ((1u << PARTS) - 1);
     rest &= ~parts;
+    if (unit >= rows) {
+      unit -= rows;
+      continue;
+    }
     const int b = head / a.c.Hkv, h = head % a.c.Hkv;
     bool whole = true;
     int part = 0;
     if constexpr (SLICES) {
       const int n = list[b + 1] - list[b];
       whole = __reduce_add_sync(0xffffffffu, mine ? my_tiles : 0) == n;
-      part = (long long)list[b] * a.c.Hkv + (long long)h * n > slice;   // it begins inside the slice
+      part = (unsigned)list[b] * a.c.Hkv + (unsigned)h * n > slice;   // it begins inside the slice
     }
     for (; unit < rows; unit += kWarps) {
       const int col = unit, r = r0 + col;
-      float2 ml = make_float2(-CUDART_INF_F, 0.f);
-      if (mine) ml = ((SLICES && !(lane & 1)) ? fml : sml)[lane / 2 * ROWS + col];
-      const float top = warp_max(ml.x);
+      const float2 ml = mine ? my_ml[col] : make_float2(-CUDART_INF_F, 0.f);
+      float top = ml.x;
+#pragma unroll
+      for (int x = kWarps; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       const float w = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
-      const float l = warp_sum(w * ml.y);
+      float l = w * ml.y;
+#pragma unroll
+      for (int x = kWarps; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
       float o[D / 32];
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
@@ -793,9 +829,13 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
       for (uint32_t m = parts; m != 0; m &= m - 1) {
         const int k = __ffs(m) - 1;
         const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* src = (!SLICES || k & 1 ? so : fo) + k / 2 * ROWS * D;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) o[j] = fmaf(wk, src[col * D + lane * (D / 32) + j], o[j]);
+        const V x = reinterpret_cast<const V*>((!SLICES || k & 1 ? so : fo) + k / 2 * ROWS * D + col * D)[lane];
+        o[0] = fmaf(wk, x.x, o[0]);
+        o[1] = fmaf(wk, x.y, o[1]);
+        if constexpr (D == 128) {
+          o[2] = fmaf(wk, x.z, o[2]);
+          o[3] = fmaf(wk, x.w, o[3]);
+        }
       }
       store_row<D>(a, b, h, r, o, l, top, whole, a.part_o + (block * 2 + part) * ROWS * D + col * D,
                    a.part_ml + (block * 2 + part) * ROWS + col);
@@ -805,53 +845,67 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
 }
 
 // Joins what several blocks left of one query row's head: the row's warps take the parts in turn, and are joined in
-// order. A head that one block had is finished; one without keys is zeros.
+// order. A head that one block had is finished; one without keys is zeros. Where the parts are is known before they are
+// there: only loads and sums are left when the kernel before has ended.
 template <int D, int WARPS>
 __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int blocks, int rows_per, long long all_rows) {
-  constexpr int F = D / 32;
+  constexpr int F = D / 32, AHEAD = 8;
+  using V = std::conditional_t<F == 4, float4, float2>;
+  __shared__ int list[kMaxListed + 1];
   __shared__ float so[8][D];
   __shared__ float2 sml[8];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WARPS;
   const long long row = blockIdx.x * (8LL / WARPS) + (threadIdx.x >> 5) / WARPS;
-  if (row >= all_rows) return;
-  const int i = (int)(row % a.Sq), head = (int)(row / a.Sq % a.Hq), b = (int)(row / a.Sq / a.Hq);
-  const int h = head / a.G, r = head % a.G * a.Sq + i;   // row of the key/value head
-  wait_for_kernel_before();
-  const long long total = (long long)a.list[a.c.B] * a.c.Hkv;
-  const int n = a.list[b + 1] - a.list[b];
-  const long long begin = (long long)a.list[b] * a.c.Hkv + (long long)h * n;
+  const bool in = row < all_rows;
+  const unsigned u = in ? (unsigned)row : 0u, i = u % a.Sq, head = u / a.Sq % a.Hq;
+  const int b = (int)(u / a.Sq / a.Hq), h = (int)(head / a.G), r = (int)(head % a.G * a.Sq + i);   // row of the key/value head
+  make_list(a, list, false);
+  const Slices slices((unsigned)list[a.c.B] * a.c.Hkv, blocks);
+  const unsigned n = list[b + 1] - list[b], begin = (unsigned)list[b] * a.c.Hkv + (unsigned)h * n;
   int c0 = 0, c1 = -1, first_part = 0;
   if (n > 0) {
-    c0 = slice_of(begin, total, blocks);
-    c1 = slice_of(begin + n - 1, total, blocks);
-    if (c0 == c1) return;
-    first_part = slice_begin(c0, total, blocks) != begin;   // of c0: the head its slice begins in, or ends in
+    c0 = (int)slices.of(begin);
+    c1 = (int)slices.of(begin + n - 1);
+    first_part = slices.begin(c0) != begin;   // of c0: the head its slice begins in, or ends in
   }
   const size_t parts = (size_t)(r / rows_per) * blocks;
+  const int col = r % rows_per;
+  auto place = [&](int c) { return ((parts + c) * 2 + (c == c0 ? first_part : 0)) * rows_per + col; };
+  wait_for_kernel_before();
+  if (!in || (n > 0 && c0 == c1)) return;
   float top = -CUDART_INF_F, l = 0.f, o[F];
 #pragma unroll
   for (int j = 0; j < F; ++j) o[j] = 0.f;
   for (int c = c0 + warp; c <= c1; c += 32 * WARPS) {   // 32 parts at a time, one of them for each lane to look at
-    const int mine = c + lane * WARPS;
-    const size_t at = ((parts + mine) * 2 + (mine == c0 ? first_part : 0)) * rows_per + r % rows_per;
+    const int count = min(32, (c1 - c) / WARPS + 1);
     float2 ml = make_float2(-CUDART_INF_F, 0.f);
-    // with more blocks than tiles some have none
-    const bool on = mine <= c1 && slice_begin(mine, total, blocks) != slice_begin(mine + 1, total, blocks);
-    if (on) ml = a.part_ml[at];
+    if (lane < count) ml = a.part_ml[place(c + lane * WARPS)];
+    V v[AHEAD];
+    auto fetch = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (k0 + k < count) v[k] = reinterpret_cast<const V*>(a.part_o + place(c + (k0 + k) * WARPS) * D)[lane];
+    };
+    fetch(0);
     const float now = fmaxf(top, warp_max(ml.x)), back = top == -CUDART_INF_F ? 0.f : exp2_fast(top - now);
-    const float w = on ? exp2_fast(ml.x - now) : 0.f;
+    const float w = lane < count ? exp2_fast(ml.x - now) : 0.f;
     top = now;
     l = l * back + warp_sum(w * ml.y);
 #pragma unroll
     for (int j = 0; j < F; ++j) o[j] *= back;
-    const int count = min(32, (c1 - c) / WARPS + 1);
-#pragma unroll 8
-    for (int k = 0; k < count; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const size_t from = __shfl_sync(0xffffffffu, at, k);
-      if (!__shfl_sync(0xffffffffu, (int)on, k)) continue;
+    for (int k0 = 0; k0 < count; k0 += AHEAD) {
+      if (k0 > 0) fetch(k0);
 #pragma unroll
-      for (int j = 0; j < F; ++j) o[j] = fmaf(wk, a.part_o[from * D + lane * F + j], o[j]);
+      for (int k = 0; k < AHEAD; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+        if (k0 + k >= count) continue;
+        o[0] = fmaf(wk, v[k].x, o[0]);
+        o[1] = fmaf(wk, v[k].y, o[1]);
+        if constexpr (F == 4) {
+          o[2] = fmaf(wk, v[k].z, o[2]);
+          o[3] = fmaf(wk, v[k].w, o[3]);
+        }
+      }
     }
   }
   if constexpr (WARPS > 1) {
@@ -880,7 +934,7 @@ struct DecodePlan {
   int nt, row_blocks;
   bool slices;
   long long blocks;
-  size_t part_ml, warp_o, warp_ml, list, total;   // offsets in the workspace; part_o is at 0
+  size_t part_ml, warp_o, warp_ml, total;   // offsets in the workspace; part_o is at 0
 };
 
 DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
@@ -907,8 +961,7 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
     d.warp_o = d.part_ml + align_up(2 * rows * 8);
     const size_t left = left_in_memory(c.D, c.q4, d.nt) ? warps * rows : 0;
     d.warp_ml = d.warp_o + align_up(left * c.D * 4);
-    d.list = d.warp_ml + align_up(left * 8);
-    d.total = d.list + align_up(((size_t)c.B + 1) * 4);
+    d.total = d.warp_ml + align_up(left * 8);
   }
   return d;
 }
@@ -987,7 +1040,6 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
     a.part_ml = reinterpret_cast<float2*>(w + plan.part_ml);
     a.warp_o = reinterpret_cast<float*>(w + plan.warp_o);
     a.warp_ml = reinterpret_cast<float2*>(w + plan.warp_ml);
-    a.list = reinterpret_cast<int*>(w + plan.list);
   }
   a.status = device_status_ptr();
   a.scale2 = p->scale * 1.4426950408889634f;
