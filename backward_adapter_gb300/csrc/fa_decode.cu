@@ -29,7 +29,15 @@
 // head, whole heads and the beginning of another. A warp walks its run through its own ring of shared
 // memory (cp.async) with a reference for its weights of its own and waits for no other; heads that it shares with its
 // block's other warps are joined when all are done, those that blocks share by a second kernel. Where
-// every head is a few tiles long a block takes one head, and there is no second kernel.
+// every head is a few tiles long a block takes one head, and there is no second kernel. Beginning with a head (its
+// queries, the first tile's way) costs a warp about three tiles' time, which the list counts (64 sequences of 512 to 4096
+// keys in 8 bits, 32 heads on 8: 61.0 us without, 58.6 with; 16 sequences of 500 to 2000 keys in 4 bits 13.7 and 12.5).
+//
+// Measured (device time, captured calls over changing inputs), 4 bits, D = 128: 64 sequences of 1024 to 8192 keys, 32 heads
+// on 8: 64.1 us, 5.3 TB/s, 78% of the measured copy rate; the loop itself runs at that rate, and what is
+// left is the way to the first tile (3.7 us), warps that end before others (2 to 3) and the two joins (4). One sequence of
+// 67584 keys, 16 heads on 4: 16.2 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
+// tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.3 us, launch and latencies.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,6 +57,7 @@ constexpr int kMaxTokens = 16;
 constexpr int kMostWarps = 8;
 constexpr int kTile = 32;         // keys a warp takes at a time
 constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
+constexpr int kStart = 3;         // tiles' time that a head costs the warp that begins with it, measured
 constexpr float kNoBase = -3e38f; // below every score
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -268,8 +277,8 @@ __device__ __forceinline__ uint32_t load_scale_pairs(uint32_t at, uint32_t (&d)[
   return bits;
 }
 
-// Warps of a block and blocks an SM holds. Rows of 128 features want 168 registers a thread (at 128 they spill: 64
-// sequences of up to 8192 keys in 4 bits took 81 us with 16 warps on an SM, 76 us with these 12).
+// Warps of a block and blocks an SM holds. Rows of 128 features want 168 registers a thread (at 128 they spilled in the
+// loop: 64 sequences of up to 8192 keys in 4 bits then took 81 us with 16 warps on an SM and 76 us with 12).
 constexpr int warps_of(int D) { return D == 128 ? 4 : 8; }
 constexpr int held_of(int D, int nt) { return D == 128 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
 
@@ -279,18 +288,20 @@ constexpr int held_of(int D, int nt) { return D == 128 ? (nt == 1 ? 3 : 2) : (nt
 constexpr int left_bytes(int D, int nt) { return warps_of(D) * nt * 8 * (D * 4 + 8); }
 constexpr bool left_in_memory(int D, bool q4, int nt) { return D == 128 && !q4 && nt == 1; }
 
-// `total` tiles (below 2^30: 2^40 elements at most) cut into n slices that differ by a tile at most, the larger ones first.
+// `total` units (below 2^30: a tensor has 2^40 elements at most) cut into n slices that differ by one at most, the larger
+// ones first.
 struct Slices {
   unsigned each, more;
   __device__ __forceinline__ Slices(unsigned total, unsigned n) : each(total / n), more(total % n) {}
   __device__ __forceinline__ unsigned begin(unsigned i) const { return i * each + min(i, more); }
-  __device__ __forceinline__ unsigned of(unsigned tile) const {
+  __device__ __forceinline__ unsigned of(unsigned unit) const {
     const unsigned large = more * (each + 1);
-    return tile < large ? tile / (each + 1) : more + (tile - large) / each;
+    return unit < large ? unit / (each + 1) : more + (unit - large) / each;
   }
 };
 
-// Tiles before each sequence, per key/value head, into list[0 .. B] in shared memory (all threads).
+// Units of the sequences before each, per key/value head, into list[0 .. B] in shared memory (all threads): a head's tiles, and
+// kStart for what it costs a warp to begin with it.
 __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool report) {
   __shared__ int warp_sum[kMostWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -301,6 +312,7 @@ __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool r
     if (b < a.c.B) {
       const Range kr = key_range(a, b, report);
       n = (kr.len - kr.lo + kTile - 1) / kTile;
+      if (n > 0) n += kStart;
     }
     int x = n;
 #pragma unroll
@@ -322,7 +334,7 @@ __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool r
   }
 }
 
-// The sequence that tile `at` of all heads' is of (all lanes of a warp, one answer): the last that begins at or before it.
+// The sequence that unit `at` of all heads' is of (all lanes of a warp, one answer): the last that begins at or before it.
 __device__ __forceinline__ int sequence_of(const int* list, int B, unsigned heads, unsigned at) {
   const int lane = threadIdx.x & 31, step = (B + 31) / 32;
   const int far = lane * step;
@@ -745,7 +757,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   if (lane < 2) left_head[2 * warp + lane] = -1;
   __syncwarp();
 
-  unsigned slice = 0;    // the first tile of the block
+  unsigned slice = 0;    // the first unit of the block
   bool keep = false;     // the last run is of a head that is left to the block
   if constexpr (!SLICES) {
     const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
@@ -764,11 +776,12 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
     while (at < end) {
       const int b = sequence_of(list, a.c.B, a.c.Hkv, at);
       const unsigned n = list[b + 1] - list[b], off = at - (unsigned)list[b] * a.c.Hkv;
-      const int h = (int)(off / n), tile = (int)(off % n);
-      const int take = (int)min(n - tile, end - at);
+      const unsigned from = off % n, to = min(n, from + (end - at));   // of the head's units
+      const int h = (int)(off / n), tile = max((int)from - kStart, 0), take = (int)to - kStart - tile;
+      at += to - from;
+      if (take <= 0) continue;   // no more than the head's beginning
       run(b, h, key_range(a, b, false), tile, take);
-      at += take;
-      if (take == (int)n) {
+      if (take == (int)n - kStart) {
         finish(b, h);
         continue;
       }
@@ -809,7 +822,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
     int part = 0;
     if constexpr (SLICES) {
       const int n = list[b + 1] - list[b];
-      whole = __reduce_add_sync(0xffffffffu, mine ? my_tiles : 0) == n;
+      whole = __reduce_add_sync(0xffffffffu, mine ? my_tiles : 0) == n - kStart;
       part = (unsigned)list[b] * a.c.Hkv + (unsigned)h * n > slice;   // it begins inside the slice
     }
     for (; unit < rows; unit += kWarps) {
@@ -864,9 +877,9 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int bloc
   const unsigned n = list[b + 1] - list[b], begin = (unsigned)list[b] * a.c.Hkv + (unsigned)h * n;
   int c0 = 0, c1 = -1, first_part = 0;
   if (n > 0) {
-    c0 = (int)slices.of(begin);
+    c0 = (int)slices.of(begin + kStart);   // the first tile's, and the last one's
     c1 = (int)slices.of(begin + n - 1);
-    first_part = slices.begin(c0) != begin;   // of c0: the head its slice begins in, or ends in
+    first_part = begin > slices.begin(c0);   // of c0: the head its slice begins in, or ends in
   }
   const size_t parts = (size_t)(r / rows_per) * blocks;
   const int col = r % rows_per;

@@ -283,3 +283,19 @@ def test_workspaces_that_do_not_fit_the_call_are_refused():
                torch.empty((2, 1 << 22), dtype=torch.uint8, device="cuda").t()):
         with pytest.raises(ValueError, match="workspace"):
             kv.decode(q, *planes, workspace=ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,D", [("q4_0", 128), ("q8_0", 64)])
+def test_many_short_sequences_in_a_roomy_cache(fmt, D):
+    """Heads of a few tiles, of one and of none, so that runs and slices begin and end with a head's beginning."""
+    B, S = 90, 2100
+    q, planes = make(B, 6, 2, S, D, 1, fmt, 23)
+    g = torch.Generator().manual_seed(24)
+    lens = torch.randint(0, 130, (B,), generator=g)
+    lens[::7] = 0
+    lens[5], lens[44], lens[-1] = S, 1, 32
+    got = kv.decode(q, *planes, lens.cuda())
+    check(q, planes, lens, got)
+    again = kv.decode(q, *planes, lens.cuda())
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
