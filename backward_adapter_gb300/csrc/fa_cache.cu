@@ -1,7 +1,8 @@
 // Writing and reading back a quantized K/V cache (fa_cache_write, fa_cache_read): the chunk's K and
 // V go into the cached window that the attention entry points read in place (llama.cpp PR #57,
 // commit 2394a4c). Both passes touch every byte once and are bound by HBM, or by their launch when
-// a few rows are written.
+// a few rows are written: 67584 keys of 4 heads of 128 in 4 bits are read back in 27 us, 6.5 TB/s, 96% of the
+// measured copy rate; a token of 32 sequences with 8 heads is written in 2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,6 +36,14 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]),
                                             tc::pack_bf16x2(x[4], x[5]), tc::pack_bf16x2(x[6], x[7]));
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const uint64_t (&x)[4]) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tc::f32x2_split(x[i], y[2 * i], y[2 * i + 1]);
+  store8(p, y);
 }
 
 // A thread quantizes 8 features of a row, four lanes a block of 32. blockIdx.y: 0 for K, 1 for V.
@@ -77,6 +86,23 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k
   if (part == 0) (blockIdx.y ? c.v_d : c.k_d)[row * (D / 32) + blk] = __half_as_ushort(d);
 }
 
+// The values of a word of 4-bit numbers, pairs of neighbours: of its low nibbles to x, of its high ones to y. Masked, a
+// nibble is an fp16 number, n 2^-24 or n 2^-20 (subnormal, exact); less 8 and times the scale, which has the power of two
+// instead, it is exact in fp32. Half the instructions, on other pipes than the logic, of integers made floats one by one.
+__device__ __forceinline__ void values_q4(uint32_t w, uint64_t d24, uint64_t d20, uint64_t* x, uint64_t* y) {
+  const uint32_t h = w >> 8;
+  auto less8 = [](uint32_t n, uint32_t off) {
+    const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&n), *reinterpret_cast<const __half2*>(&off));
+    return __half22float2(r);
+  };
+  const float2 e = less8(w & 0x000f000fu, 0x80088008u), o = less8(h & 0x000f000fu, 0x80088008u);   // bytes (0, 2), (1, 3)
+  x[0] = tc::mul_f32x2(tc::f32x2(e.x, o.x), d24);
+  x[1] = tc::mul_f32x2(tc::f32x2(e.y, o.y), d24);
+  const float2 f = less8(w & 0x00f000f0u, 0x80808080u), p = less8(h & 0x00f000f0u, 0x80808080u);
+  y[0] = tc::mul_f32x2(tc::f32x2(f.x, p.x), d20);
+  y[1] = tc::mul_f32x2(tc::f32x2(f.y, p.y), d20);
+}
+
 // A thread reads 16 features (half a block's bytes) of ROWS rows, all of them on their way at once.
 // blockIdx.y: 0 for K, 1 for V.
 template <typename T, int D, bool Q4, int ROWS>
@@ -88,13 +114,26 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long 
   const RowView dst = blockIdx.y ? v : k;
   const uint8_t* values = static_cast<const uint8_t*>(blockIdx.y ? c.v_q : c.k_q);
   const uint16_t* scales = blockIdx.y ? c.v_d : c.k_d;
+  // f(i, head, row, whether the head is another than the last time)
+  auto each_row = [&](auto f) {
+    unsigned bh = first / n_rows, r = first % n_rows;
+    bool other = true;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (first + i * STEP >= rows) break;
+      f(i, bh, r, other);
+      r += STEP;
+      other = r >= n_rows;
+      if (other) {
+        bh += r / n_rows;
+        r %= n_rows;
+      }
+    }
+  };
   uint4 w[ROWS];
   uint16_t scale[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const unsigned g = first + i * STEP;
-    if (g >= rows) break;
-    const size_t row = (size_t)(g / n_rows) * c.S + (size_t)(begin + g % n_rows);
+  each_row([&](int i, unsigned bh, unsigned r, bool) {
+    const size_t row = (size_t)bh * c.S + (size_t)(begin + r);
     scale[i] = __ldg(scales + row * (D / 32) + part / 2);
     if constexpr (Q4) {
       const uint2 u = __ldg(reinterpret_cast<const uint2*>(values + row * (D / 2) + 8 * part));
@@ -103,25 +142,22 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long 
     } else {
       w[i] = __ldg(reinterpret_cast<const uint4*>(values + row * D + 16 * part));
     }
-  }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const unsigned g = first + i * STEP;
-    if (g >= rows) break;
-    const unsigned bh = g / n_rows, r = g % n_rows, b = bh / c.Hkv, h = bh % c.Hkv;
+  });
+  T* head = nullptr;
+  each_row([&](int i, unsigned bh, unsigned r, bool other) {
+    if (other) head = static_cast<T*>(dst.ptr) + bh / c.Hkv * dst.sb + bh % c.Hkv * dst.sh;
     const float d = __half2float(__ushort_as_half(scale[i]));
-    T* out = static_cast<T*>(dst.ptr) + b * dst.sb + r * dst.ss + h * dst.sh;
-    float x[8], y[8];
+    T* out = head + r * dst.ss;
     if constexpr (Q4) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = q4_low(j < 4 ? w[i].x : w[i].y, j % 4) * d;
-        y[j] = q4_high(j < 4 ? w[i].x : w[i].y, j % 4) * d;
-      }
+      const uint64_t d24 = tc::f32x2(d * 16777216.f, d * 16777216.f), d20 = tc::f32x2(d * 1048576.f, d * 1048576.f);
+      uint64_t x[4], y[4];
+      values_q4(w[i].x, d24, d20, x, y);
+      values_q4(w[i].y, d24, d20, x + 2, y + 2);
       out += part / 2 * 32 + part % 2 * 8;
       store8(out, x);
       store8(out + 16, y);
     } else {
+      float x[8], y[8];
       const uint32_t u[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -132,7 +168,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long 
       store8(out, x);
       store8(out + 8, y);
     }
-  }
+  });
 }
 
 // Blocks that take `per_block` rows each; 0 when the rows are too many for 32-bit numbers.
@@ -169,15 +205,16 @@ cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, i
                               const RowView& v, cudaStream_t st) {
   const long long rows = (long long)c.B * c.Hkv * n_rows;
   const int step = 256 / (c.D / 16);
-  const bool many = rows >= 16LL * step * sm_count();   // eight rows a thread then still leave two blocks for every SM
-  const unsigned n = blocks_for(rows, many ? 8 * step : step);
+  // four rows a thread, where that still leaves blocks for every SM (67584 keys of 4 heads in 4 bits: 27.1 us; one 31.6, eight 27.4)
+  const bool many = rows >= 8LL * step * sm_count();
+  const unsigned n = blocks_for(rows, many ? 4 * step : step);
   if (n == 0) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) { kernel<<<dim3(n, 2), 256, 0, st>>>(c, begin, (unsigned)rows, (unsigned)n_rows, k, v); };
   auto by_format = [&](auto t, auto dim) {
     using T = decltype(t);
     constexpr int D = decltype(dim)::value;
-    if (c.q4) many ? go(cache_read_kernel<T, D, true, 8>) : go(cache_read_kernel<T, D, true, 1>);
-    else many ? go(cache_read_kernel<T, D, false, 8>) : go(cache_read_kernel<T, D, false, 1>);
+    if (c.q4) many ? go(cache_read_kernel<T, D, true, 4>) : go(cache_read_kernel<T, D, true, 1>);
+    else many ? go(cache_read_kernel<T, D, false, 4>) : go(cache_read_kernel<T, D, false, 1>);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;

@@ -62,8 +62,4 @@ __device__ __forceinline__ __half quantize_block(float (&x)[8], uint32_t& lo, ui
   return d;
 }
 
-// Nibbles k and k + 4 bits of a word's bytes as numbers in float: byte k's low (high) four bits - 8.
-__device__ __forceinline__ float q4_low(uint32_t w, int k) { return (float)((int)((w >> (8 * k)) & 15u) - 8); }
-__device__ __forceinline__ float q4_high(uint32_t w, int k) { return (float)((int)((w >> (8 * k + 4)) & 15u) - 8); }
-
 }  // namespace fa
