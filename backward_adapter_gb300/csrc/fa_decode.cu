@@ -7,7 +7,7 @@
 // the tensor cores multiply whole numbers, exact as fp16, by q and by p * d, and K's scales never touch
 // the 8- or 4-bit data. Scores, softmax statistics and sums are fp32. Query rows are scaled by a power of
 // two to the top of fp16's range, where a bf16 value down to 2^-24 of the row's largest is exact; p and
-// p * d are rounded to fp16, 2^-12 of their values each, with a power of two that keeps them below 2^15
+// p * d are rounded to fp16, 2^-11 of their values each at most, with a power of two that keeps them below 2^15
 // whatever the scales are (see `level`).
 //
 // What bounds it: the planes are read once, 144 bytes a key for D = 128 in 4 bits, so HBM; next to

@@ -6,9 +6,10 @@ with Q_b the sum of |q| over a block, its partial sums stay below W Q_b (W = 8 i
 So a score is off by at most E = 2^-19 scale sum_b |d_b| W Q_b over the keys a query sees; LSE by E and
 the roundings of a logarithm near it, 2^-20 (1 + |LSE|). A weight p is off by the factor e^(+-E); in units in which the
 largest one is at least 2^level, level = min(7, 21 - (the or of the exponent fields of the V scales it is summed with)), p and then
-p * d are rounded to fp16: each is off by half a step, 2^-12 of its value, or 2^-25 where it is subnormal. The whole numbers
+p * d are rounded to fp16: each is off by at most half a step, 2^-11 of its value (11 bits: a step is 2^-10 of the power of two
+below it), 2^-10 for both, or 2^-25 where it is subnormal. The whole numbers
 are at most W, sum p is at least 1, and the result is rounded to bf16, 2^-8 of its value, so with n keys and scales up to d
-    |dO| <= (2^-11 + 2 E + 2^-16) sum p |v| / sum p + n W (1 + d) 2^(-25 - level) + 2^-8 |O|.
+    |dO| <= (2^-10 + 2 E + 2^-16) sum p |v| / sum p + n W (1 + d) 2^(-25 - level) + 2^-8 |O|.
 """
 import ctypes
 import math
@@ -81,7 +82,7 @@ def check(q, planes, lengths, got, scale=None, window=0):
     assert not bad.any(), (np.abs(lse - want_lse).max(), E.max())
     e, step = E[..., None], weight_step(planes, n, q.shape[1], q.shape[2], window)[..., None]
     err = np.abs(o - want)
-    assert np.all(err <= (2.0 ** -11 + 2 * e + 2.0 ** -16) * size + step + 2.0 ** -8 * np.abs(want)), err.max()
+    assert np.all(err <= (2.0 ** -10 + 2 * e + 2.0 ** -16) * size + step + 2.0 ** -8 * np.abs(want)), err.max()
     empty = want_lse == 0
     if empty.any():
         assert np.all(o[empty & (np.abs(want).sum(-1) == 0)] == 0)
