@@ -34,7 +34,7 @@
 // keys in 8 bits, 32 heads on 8: 61.0 us without, 58.6 with; 16 sequences of 500 to 2000 keys in 4 bits 13.7 and 12.5).
 //
 // Measured (device time, captured calls over changing inputs), 4 bits, D = 128: 64 sequences of 1024 to 8192 keys, 32 heads
-// on 8: 64.1 us, 5.3 TB/s, 78% of the measured copy rate; the loop itself runs at that rate, and what is
+// on 8: 63.4 us, 5.4 TB/s, 79% of the measured copy rate; the loop itself runs at that rate, and what is
 // left is the way to the first tile (3.7 us), warps that end before others (2 to 3) and the two joins (4). One sequence of
 // 67584 keys, 16 heads on 4: 16.2 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
 // tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.3 us, launch and latencies.
@@ -549,8 +549,11 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
                          qf[n][k][0][0], qf[n][k][0][1]);
             mma_f16(c, f[2 * m][2], f[2 * m + 1][2], f[2 * m][3], f[2 * m + 1][3], qf[n][k][1][0], qf[n][k][1][1]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              s[n][m][j] = k == 0 ? d[2 * m + j / 2][k] * c[j] : fmaf(d[2 * m + j / 2][k], c[j], s[n][m][j]);
+            for (int j = 0; j < 4; j += 2) {   // a key's two columns, packed
+              const uint64_t dd = tc::f32x2(d[2 * m + j / 2][k], d[2 * m + j / 2][k]), cc = tc::f32x2(c[j], c[j + 1]);
+              tc::f32x2_split(k == 0 ? tc::mul_f32x2(dd, cc) : tc::fma_f32x2(dd, cc, tc::f32x2(s[n][m][j], s[n][m][j + 1])),
+                              s[n][m][j], s[n][m][j + 1]);
+            }
           }
       }
 
