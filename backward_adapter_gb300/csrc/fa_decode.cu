@@ -34,9 +34,9 @@
 // keys in 8 bits, 32 heads on 8: 61.0 us without, 58.6 with; 16 sequences of 500 to 2000 keys in 4 bits 13.7 and 12.5).
 //
 // Measured (device time, captured calls over changing inputs), 4 bits, D = 128: 64 sequences of 1024 to 8192 keys, 32 heads
-// on 8: 63.4 us, 5.4 TB/s, 79% of the measured copy rate; the loop itself runs at that rate, and what is
+// on 8: 62.9 us, 5.4 TB/s, 80% of the measured copy rate; the loop itself runs at that rate, and what is
 // left is the way to the first tile (3.7 us), warps that end before others (2 to 3) and the two joins (4). One sequence of
-// 67584 keys, 16 heads on 4: 16.2 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
+// 67584 keys, 16 heads on 4: 15.9 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
 // tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.3 us, launch and latencies.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,7 +54,6 @@ namespace fa {
 namespace {
 
 constexpr int kMaxTokens = 16;
-constexpr int kMostWarps = 8;
 constexpr int kTile = 32;         // keys a warp takes at a time
 constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
 constexpr int kStart = 3;         // tiles' time that a head costs the warp that begins with it, measured
@@ -81,8 +80,7 @@ struct DecodeArgs {
 // The keys a sequence's queries may see: [lo, len), lo on a tile's border.
 struct Range { int len, lo; };
 
-__device__ __forceinline__ Range key_range(const DecodeArgs& a, int b, bool report) {
-  long long n = a.lengths != nullptr ? __ldg(a.lengths + b) : a.c.S;
+__device__ __forceinline__ Range key_range(const DecodeArgs& a, long long n, bool report) {
   if (n < 0 || n > a.c.S) {
     if (report && a.status != nullptr) atomicCAS(a.status, 0u, 0x40000000u | kSiteDecodeLength);
     n = n < 0 ? 0 : a.c.S;
@@ -93,6 +91,10 @@ __device__ __forceinline__ Range key_range(const DecodeArgs& a, int b, bool repo
     r.lo = lo > 0 ? (int)lo & ~(kTile - 1) : 0;
   }
   return r;
+}
+
+__device__ __forceinline__ long long length_of(const DecodeArgs& a, int b) {
+  return a.lengths != nullptr ? __ldg(a.lengths + b) : a.c.S;
 }
 
 // Element offset of query row r (head r / Sq of the group, token r % Sq) in q and o.
@@ -302,36 +304,47 @@ struct Slices {
 
 // Units of the sequences before each, per key/value head, into list[0 .. B] in shared memory (all threads): a head's tiles, and
 // kStart for what it costs a warp to begin with it.
+template <int THREADS>
 __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool report) {
-  __shared__ int warp_sum[kMostWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int before = 0;
-  for (int b0 = 0; b0 < a.c.B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    int n = 0;
-    if (b < a.c.B) {
-      const Range kr = key_range(a, b, report);
-      n = (kr.len - kr.lo + kTile - 1) / kTile;
-      if (n > 0) n += kStart;
-    }
-    int x = n;
+  constexpr int EACH = kMaxListed / THREADS;
+  __shared__ int warp_sum[THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int each = (a.c.B + THREADS - 1) / THREADS, first = threadIdx.x * each;   // this thread's sequences
+  long long length[EACH];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    int all = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) x += warp_sum[w];
-      all += warp_sum[w];
-    }
-    if (b < a.c.B) list[b] = before + x - n;
-    before += all;
-    if (b == a.c.B - 1) list[a.c.B] = before;
-    __syncthreads();
+  for (int i = 0; i < EACH; ++i) {   // all on their way at once
+    if (i >= each) break;
+    length[i] = first + i < a.c.B ? length_of(a, first + i) : 0;
   }
+  int units[EACH], x = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    if (i >= each) break;
+    const Range kr = key_range(a, length[i], report);
+    const int n = (kr.len - kr.lo + kTile - 1) / kTile;
+    units[i] = n > 0 ? n + kStart : 0;
+    x += units[i];
+  }
+  int before = -x;   // less its own: of the threads before this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  before += x;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w)
+    if (w < warp) before += warp_sum[w];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    if (i >= each) break;
+    if (first + i < a.c.B) list[first + i] = before;
+    before += units[i];
+  }
+  if (first < a.c.B && first + each >= a.c.B) list[a.c.B] = before;   // all
+  __syncthreads();
 }
 
 // The sequence that unit `at` of all heads' is of (all lanes of a warp, one answer): the last that begins at or before it.
@@ -764,13 +777,13 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   bool keep = false;     // the last run is of a head that is left to the block
   if constexpr (!SLICES) {
     const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
-    const Range kr = key_range(a, b, report && h == 0 && threadIdx.x == 0);
+    const Range kr = key_range(a, length_of(a, b), report && h == 0 && threadIdx.x == 0);
     const int n = (kr.len - kr.lo + kTile - 1) / kTile, first = n * warp / kWarps;
     run(b, h, kr, first, n * (warp + 1) / kWarps - first);
     keep = true;
     if (lane == 0) left_head[2 * warp + 1] = blockIdx.x;
   } else {
-    make_list(a, list, report);
+    make_list<kWarps * 32>(a, list, report);
     const Slices slices((unsigned)list[a.c.B] * a.c.Hkv, gridDim.x);
     slice = slices.begin(blockIdx.x);
     const Slices runs(slices.begin(blockIdx.x + 1) - slice, kWarps);
@@ -783,7 +796,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
       const int h = (int)(off / n), tile = max((int)from - kStart, 0), take = (int)to - kStart - tile;
       at += to - from;
       if (take <= 0) continue;   // no more than the head's beginning
-      run(b, h, key_range(a, b, false), tile, take);
+      run(b, h, key_range(a, length_of(a, b), false), tile, take);
       if (take == (int)n - kStart) {
         finish(b, h);
         continue;
@@ -875,7 +888,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int bloc
   const bool in = row < all_rows;
   const unsigned u = in ? (unsigned)row : 0u, i = u % a.Sq, head = u / a.Sq % a.Hq;
   const int b = (int)(u / a.Sq / a.Hq), h = (int)(head / a.G), r = (int)(head % a.G * a.Sq + i);   // row of the key/value head
-  make_list(a, list, false);
+  make_list<256>(a, list, false);
   const Slices slices((unsigned)list[a.c.B] * a.c.Hkv, blocks);
   const unsigned n = list[b + 1] - list[b], begin = (unsigned)list[b] * a.c.Hkv + (unsigned)h * n;
   int c0 = 0, c1 = -1, first_part = 0;

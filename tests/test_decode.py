@@ -290,7 +290,7 @@ def test_workspaces_that_do_not_fit_the_call_are_refused():
 @pytest.mark.parametrize("fmt,D", [("q4_0", 128), ("q8_0", 64)])
 def test_many_short_sequences_in_a_roomy_cache(fmt, D):
     """Heads of a few tiles, of one and of none, so that runs and slices begin and end with a head's beginning."""
-    B, S = 90, 2100
+    B, S = 50, 700 if D == 128 else 1056
     q, planes = make(B, 6, 2, S, D, 1, fmt, 23)
     g = torch.Generator().manual_seed(24)
     lens = torch.randint(0, 130, (B,), generator=g)
@@ -300,3 +300,23 @@ def test_many_short_sequences_in_a_roomy_cache(fmt, D):
     check(q, planes, lens, got)
     again = kv.decode(q, *planes, lens.cuda())
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [128, 129, 700, 1024, 1025])
+def test_sequences_on_both_sides_of_the_lists_sizes(B):
+    """Short sequences in a roomy cache against the same in a small one, which takes another path: the same weights,
+    added in another order."""
+    S, D, g = 1056, 64, torch.Generator(device="cuda").manual_seed(B)
+    planes = kv.new_cache(B, 1, S, D, "q4_0")
+    for i in (0, 2):
+        planes[i].random_(0, 256, generator=g)
+        planes[i + 1].copy_(torch.rand(planes[i + 1].shape, device="cuda", generator=g) * 0.1)
+    q = torch.randn((B, 3, 1, D), device="cuda", generator=g).to(torch.bfloat16)
+    lens = torch.randint(0, 65, (B,), device="cuda", generator=g)
+    got = kv.decode(q, *planes, lens)
+    want = kv.decode(q, *(t[:, :, :64].contiguous() for t in planes), lens)
+    torch.cuda.synchronize()
+    assert torch.allclose(got[1], want[1], rtol=2.0 ** -18, atol=2.0 ** -18)
+    assert torch.allclose(got[0].float(), want[0].float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+    assert bool((got[0][lens == 0] == 0).all()) and bool((got[1][lens == 0] == 0).all())
