@@ -29,15 +29,15 @@
 // head, whole heads and the beginning of another. A warp walks its run through its own ring of shared
 // memory (cp.async) with a reference for its weights of its own and waits for no other; heads that it shares with its
 // block's other warps are joined when all are done, those that blocks share by a second kernel. Where
-// every head is a few tiles long a block takes one head, and there is no second kernel. Beginning with a head (its
+// every head is a few tiles long a block takes one head, and there is no second kernel (see plan_decode). Beginning with a head (its
 // queries, the first tile's way) costs a warp about three tiles' time, which the list counts (64 sequences of 512 to 4096
-// keys in 8 bits, 32 heads on 8: 61.0 us without, 58.6 with; 16 sequences of 500 to 2000 keys in 4 bits 13.7 and 12.5).
+// keys in 8 bits, 32 heads on 8: 61.0 us without, 58.6 with; 500 of up to 300 keys in 4 bits, 8 on 2: 21.8 and 18.4).
 //
 // Measured (device time, captured calls over changing inputs), 4 bits, D = 128: 64 sequences of 1024 to 8192 keys, 32 heads
 // on 8: 62.9 us, 5.4 TB/s, 80% of the measured copy rate; the loop itself runs at that rate, and what is
 // left is the way to the first tile (3.7 us), warps that end before others (2 to 3) and the two joins (4). One sequence of
 // 67584 keys, 16 heads on 4: 15.9 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
-// tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.3 us, launch and latencies.
+// tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.1 us, launch and latencies.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -283,11 +283,13 @@ __device__ __forceinline__ uint32_t load_scale_pairs(uint32_t at, uint32_t (&d)[
 // loop: 64 sequences of up to 8192 keys in 4 bits then took 81 us with 16 warps on an SM and 76 us with 12).
 constexpr int warps_of(int D) { return D == 128 ? 4 : 8; }
 constexpr int held_of(int D, int nt) { return D == 128 ? (nt == 1 ? 3 : 2) : (nt == 1 ? 2 : 1); }
+// Warps of a block that has an SM to itself.
+constexpr int wide_of(int D, int nt) { return warps_of(D) * held_of(D, nt); }
 
 // Bytes of what a block's warps leave: [warps][rows][D] and [warps][rows] pairs. One set of it, of the heads that the
 // warps' runs end in, takes the rings' place at the end. The other, of the heads that end inside a run, has a place of
 // its own where that costs no block on an SM (not beside the rings of 128 features in 8 bits).
-constexpr int left_bytes(int D, int nt) { return warps_of(D) * nt * 8 * (D * 4 + 8); }
+constexpr int left_bytes(int warps, int D, int nt) { return warps * nt * 8 * (D * 4 + 8); }
 constexpr bool left_in_memory(int D, bool q4, int nt) { return D == 128 && !q4 && nt == 1; }
 
 // `total` units (below 2^30: a tensor has 2^40 elements at most) cut into n slices that differ by one at most, the larger
@@ -359,6 +361,18 @@ __device__ __forceinline__ int sequence_of(const int* list, int B, unsigned head
   return b;
 }
 
+// A part of a row's sums, by its weight.
+__device__ __forceinline__ void add_part(float (&o)[2], float w, float2 x) {
+  o[0] = fmaf(w, x.x, o[0]);
+  o[1] = fmaf(w, x.y, o[1]);
+}
+__device__ __forceinline__ void add_part(float (&o)[4], float w, float4 x) {
+  o[0] = fmaf(w, x.x, o[0]);
+  o[1] = fmaf(w, x.y, o[1]);
+  o[2] = fmaf(w, x.z, o[2]);
+  o[3] = fmaf(w, x.w, o[3]);
+}
+
 // Row r of a head from a warp's sums (D / 32 features a lane): the result, or what is left of it.
 template <int D>
 __device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int r, const float (&o)[D / 32], float l,
@@ -380,10 +394,11 @@ __device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int
 
 // A block's work: SLICES: slice blockIdx.x of the list; else the head blockIdx.x. NT * 8 query rows from
 // blockIdx.y * NT * 8 on.
-template <int D, bool Q4, int NT, bool SLICES>
-__global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kernel(DecodeArgs a) {
+template <int D, bool Q4, int NT, bool SLICES, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D, NT) : 1) decode_kernel(DecodeArgs a) {
   using S = Slot<D, Q4>;
-  constexpr int NB = S::NB, kWarps = warps_of(D), ROWS = NT * 8;
+  constexpr int NB = S::NB, ROWS = NT * 8;
+  using V = std::conditional_t<D == 128, float4, float2>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int list[SLICES ? kMaxListed + 1 : 1];
   // the heads whose sums the block's warps leave unfinished, in the order of their tiles: two for each
@@ -761,7 +776,7 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
   };
 
   const size_t block = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
-  constexpr int RING = kWarps * S::STAGES * S::BYTES, FIRST = RING > left_bytes(D, NT) ? RING : left_bytes(D, NT);
+  constexpr int RING = kWarps * S::STAGES * S::BYTES, FIRST = RING > left_bytes(kWarps, D, NT) ? RING : left_bytes(kWarps, D, NT);
   float* so = reinterpret_cast<float*>(smem);   // of the heads that runs end in, once every warp is done with its ring
   float2* sml = reinterpret_cast<float2*>(smem + kWarps * ROWS * D * 4);
   float* fo = reinterpret_cast<float*>(smem + FIRST);   // of the heads that end inside a run
@@ -770,22 +785,35 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
     fo = a.warp_o + block * kWarps * ROWS * D;
     fml = a.warp_ml + block * kWarps * ROWS;
   }
-  if (lane < 2) left_head[2 * warp + lane] = -1;
-  __syncwarp();
+  const int rows = min(ROWS, a.R - r0);
 
-  unsigned slice = 0;    // the first unit of the block
-  bool keep = false;     // the last run is of a head that is left to the block
-  if constexpr (!SLICES) {
+  if constexpr (!SLICES) {   // every warp a part of the head's tiles, and then rows of their sums
     const int b = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv;
     const Range kr = key_range(a, length_of(a, b), report && h == 0 && threadIdx.x == 0);
     const int n = (kr.len - kr.lo + kTile - 1) / kTile, first = n * warp / kWarps;
     run(b, h, kr, first, n * (warp + 1) / kWarps - first);
-    keep = true;
-    if (lane == 0) left_head[2 * warp + 1] = blockIdx.x;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    put(so + warp * ROWS * D, sml + warp * ROWS);
+    __syncthreads();
+    for (int col = warp; col < rows; col += kWarps) {
+      const float2 ml = lane < kWarps ? sml[lane * ROWS + col] : make_float2(-CUDART_INF_F, 0.f);
+      const float top = warp_max(ml.x), w = lane < kWarps ? exp2_fast(ml.x - top) : 0.f, l = warp_sum(w * ml.y);
+      float o[D / 32];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < kWarps; ++k) add_part(o, __shfl_sync(0xffffffffu, w, k), reinterpret_cast<const V*>(so + (k * ROWS + col) * D)[lane]);
+      store_row<D>(a, b, h, r0 + col, o, l, top, true, nullptr, nullptr);
+    }
   } else {
+    if (lane < 2) left_head[2 * warp + lane] = -1;
+    __syncwarp();
+
+    bool keep = false;     // the last run is of a head that is left to the block
     make_list<kWarps * 32>(a, list, report);
     const Slices slices((unsigned)list[a.c.B] * a.c.Hkv, gridDim.x);
-    slice = slices.begin(blockIdx.x);
+    const unsigned slice = slices.begin(blockIdx.x);   // the first unit of the block
     const Slices runs(slices.begin(blockIdx.x + 1) - slice, kWarps);
     unsigned at = slice + runs.begin(warp);
     const unsigned end = slice + runs.begin(warp + 1);
@@ -808,68 +836,56 @@ __global__ void __launch_bounds__(warps_of(D) * 32, held_of(D, NT)) decode_kerne
       }
       if (!keep) put(fo + warp * ROWS * D, fml + warp * ROWS);
     }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-  if (keep) put(so + warp * ROWS * D, sml + warp * ROWS);
-  __syncthreads();
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    if (keep) put(so + warp * ROWS * D, sml + warp * ROWS);
+    __syncthreads();
 
-  // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k (and its lanes k + PARTS, ...
-  // do too), which is of warp k / 2: the head its run begins in, and the one it ends in.
-  constexpr int PARTS = 2 * kWarps;
-  using V = std::conditional_t<D == 128, float4, float2>;
-  const int mine_k = lane % PARTS;
-  const int my_head = left_head[mine_k];
-  const int my_tiles = SLICES && my_head >= 0 && lane < PARTS ? left_tiles[mine_k] : 0;
-  const float2* my_ml = (SLICES && !(mine_k & 1) ? fml : sml) + mine_k / 2 * ROWS;
-  const int rows = min(ROWS, a.R - r0);
-  int unit = warp;   // counts down the rows until this warp's next one
-  for (uint32_t rest = __ballot_sync(0xffffffffu, my_head >= 0) & ((1u << PARTS) - 1); rest != 0;) {
-    const int head = __shfl_sync(0xffffffffu, my_head, __ffs(rest) - 1);
-    const bool mine = my_head == head;
-    const uint32_t parts = __ballot_sync(0xffffffffu, mine) & ((1u << PARTS) - 1);
-    rest &= ~parts;
-    if (unit >= rows) {
-      unit -= rows;
-      continue;
-    }
-    const int b = head / a.c.Hkv, h = head % a.c.Hkv;
-    bool whole = true;
-    int part = 0;
-    if constexpr (SLICES) {
-      const int n = list[b + 1] - list[b];
-      whole = __reduce_add_sync(0xffffffffu, mine ? my_tiles : 0) == n - kStart;
-      part = (unsigned)list[b] * a.c.Hkv + (unsigned)h * n > slice;   // it begins inside the slice
-    }
-    for (; unit < rows; unit += kWarps) {
-      const int col = unit, r = r0 + col;
-      const float2 ml = mine ? my_ml[col] : make_float2(-CUDART_INF_F, 0.f);
-      float top = ml.x;
-#pragma unroll
-      for (int x = kWarps; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float w = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
-      float l = w * ml.y;
-#pragma unroll
-      for (int x = kWarps; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-      float o[D / 32];
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
-#pragma unroll 1
-      for (uint32_t m = parts; m != 0; m &= m - 1) {
-        const int k = __ffs(m) - 1;
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const V x = reinterpret_cast<const V*>((!SLICES || k & 1 ? so : fo) + k / 2 * ROWS * D + col * D)[lane];
-        o[0] = fmaf(wk, x.x, o[0]);
-        o[1] = fmaf(wk, x.y, o[1]);
-        if constexpr (D == 128) {
-          o[2] = fmaf(wk, x.z, o[2]);
-          o[3] = fmaf(wk, x.w, o[3]);
-        }
+    // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k (and its lanes k + PARTS, ...
+    // do too), which is of warp k / 2: the head its run begins in, and the one it ends in.
+    constexpr int PARTS = 2 * kWarps;
+    const int mine_k = lane % PARTS;
+    const int my_head = left_head[mine_k];
+    const int my_tiles = my_head >= 0 && lane < PARTS ? left_tiles[mine_k] : 0;
+    const float2* my_ml = (mine_k & 1 ? sml : fml) + mine_k / 2 * ROWS;
+    int unit = warp;   // counts down the rows until this warp's next one
+    for (uint32_t rest = __ballot_sync(0xffffffffu, my_head >= 0) & ((1u << PARTS) - 1); rest != 0;) {
+      const int head = __shfl_sync(0xffffffffu, my_head, __ffs(rest) - 1);
+      const bool mine = my_head == head;
+      const uint32_t parts = __ballot_sync(0xffffffffu, mine) & ((1u << PARTS) - 1);
+      rest &= ~parts;
+      if (unit >= rows) {
+        unit -= rows;
+        continue;
       }
-      store_row<D>(a, b, h, r, o, l, top, whole, a.part_o + (block * 2 + part) * ROWS * D + col * D,
-                   a.part_ml + (block * 2 + part) * ROWS + col);
+      const int b = head / a.c.Hkv, h = head % a.c.Hkv;
+      const int n = list[b + 1] - list[b];
+      const bool whole = __reduce_add_sync(0xffffffffu, mine ? my_tiles : 0) == n - kStart;
+      const int part = (unsigned)list[b] * a.c.Hkv + (unsigned)h * n > slice;   // it begins inside the slice
+      for (; unit < rows; unit += kWarps) {
+        const int col = unit, r = r0 + col;
+        const float2 ml = mine ? my_ml[col] : make_float2(-CUDART_INF_F, 0.f);
+        float top = ml.x;
+#pragma unroll
+        for (int x = kWarps; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float w = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
+        float l = w * ml.y;
+#pragma unroll
+        for (int x = kWarps; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        float o[D / 32];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
+#pragma unroll 1
+        for (uint32_t m = parts; m != 0; m &= m - 1) {
+          const int k = __ffs(m) - 1;
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          add_part(o, wk, reinterpret_cast<const V*>((k & 1 ? so : fo) + k / 2 * ROWS * D + col * D)[lane]);
+        }
+        store_row<D>(a, b, h, r, o, l, top, whole, a.part_o + (block * 2 + part) * ROWS * D + col * D,
+                     a.part_ml + (block * 2 + part) * ROWS + col);
+      }
+      unit -= rows;
     }
-    unit -= rows;
   }
 }
 
@@ -927,13 +943,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int bloc
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-        if (k0 + k >= count) continue;
-        o[0] = fmaf(wk, v[k].x, o[0]);
-        o[1] = fmaf(wk, v[k].y, o[1]);
-        if constexpr (F == 4) {
-          o[2] = fmaf(wk, v[k].z, o[2]);
-          o[3] = fmaf(wk, v[k].w, o[3]);
-        }
+        if (k0 + k < count) add_part(o, wk, v[k]);
       }
     }
   }
@@ -960,7 +970,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(DecodeArgs a, int bloc
 }
 
 struct DecodePlan {
-  int nt, row_blocks;
+  int nt, row_blocks, warps;
   bool slices;
   long long blocks;
   size_t part_ml, warp_o, warp_ml, total;   // offsets in the workspace; part_o is at 0
@@ -975,14 +985,24 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
   const int keys = (int)(most < c.S ? most : c.S);
   const int tiles = (keys + kTile - 1) / kTile;
   const long long heads = (long long)c.B * c.Hkv;
-  // One head a block when a head is at most four tiles a warp (no second kernel), and when the list of
-  // sequences is too long for shared memory (heads enough for every SM then).
-  const int warps = warps_of(c.D);
-  d.slices = tiles > 4 * warps && c.B <= kMaxListed;
+  // One head a block, and no second kernel, when a head is at most four tiles a warp, and when the list of sequences is too
+  // long for shared memory (heads enough for every SM then). Where a block has an SM to itself it has as many warps as that
+  // holds, and slices, which spread the tiles over all SMs, cost list, ends and second kernel, as much as three tiles
+  // of all warps; up to six a warp, as heads may be of any length below S. 128 heads of 128 features in 4 bits with
+  // 825 to 1100 keys took 11.8 us in slices and 8.2 in a block each, 32 heads 8.4 and 8.2, 32 heads of twice the length
+  // 9.9 and 11.1, 128 of 8400 keys 31.2 and 30.6.
+  const int sms = sm_count();
+  const long long blocks = heads * d.row_blocks;
+  const bool alone = blocks <= sms;
+  d.warps = alone ? wide_of(c.D, d.nt) : warps_of(c.D);
+  const bool few = alone ? tiles <= 6 * d.warps && tiles * (sms - blocks) <= 3LL * d.warps * sms : tiles <= 4 * d.warps;
+  d.slices = !few && c.B <= kMaxListed;
+  if (d.slices) d.warps = warps_of(c.D);
+  const int warps = d.warps;
   d.blocks = heads;
   if (d.slices) {
     // as many blocks as the SMs hold at a time, no slice below a tile a warp
-    const long long all = (long long)held_of(c.D, d.nt) * sm_count() / d.row_blocks, some = heads * tiles / warps;
+    const long long all = (long long)held_of(c.D, d.nt) * sms / d.row_blocks, some = heads * tiles / warps;
     d.blocks = all < some ? all : some;
     if (d.blocks < 1) d.blocks = 1;
     const size_t rows = (size_t)d.row_blocks * d.blocks * d.nt * 8;
@@ -1010,16 +1030,16 @@ fa_status check_decode(const fa_decode_params* p, const fa_cache* c, CacheView& 
   return FA_OK;
 }
 
-template <int D, bool Q4, int NT, bool SLICES>
+template <int D, bool Q4, int NT, bool SLICES, int WARPS>
 cudaError_t launch_decode(const DecodeArgs& a, dim3 grid, cudaStream_t st) {
   using S = Slot<D, Q4>;
-  constexpr int ring = warps_of(D) * S::STAGES * S::BYTES, left = left_bytes(D, NT);
+  constexpr int ring = WARPS * S::STAGES * S::BYTES, left = left_bytes(WARPS, D, NT);
   constexpr int bytes = (ring > left ? ring : left) + (SLICES && !left_in_memory(D, Q4, NT) ? left : 0);
-  auto kernel = decode_kernel<D, Q4, NT, SLICES>;
+  auto kernel = decode_kernel<D, Q4, NT, SLICES, WARPS>;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(kernel, bytes, allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, warps_of(D) * 32, bytes, st>>>(a);
+  kernel<<<grid, WARPS * 32, bytes, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -1084,8 +1104,12 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   auto go = [&](auto dim, auto q4) {
     constexpr int D = decltype(dim)::value;
     constexpr bool Q4 = decltype(q4)::value;
-    if (plan.nt == 1) return plan.slices ? launch_decode<D, Q4, 1, true>(a, grid, cs) : launch_decode<D, Q4, 1, false>(a, grid, cs);
-    return plan.slices ? launch_decode<D, Q4, 2, true>(a, grid, cs) : launch_decode<D, Q4, 2, false>(a, grid, cs);
+    auto of = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value, W = warps_of(D), WIDE = wide_of(D, NT);
+      if (plan.slices) return launch_decode<D, Q4, NT, true, W>(a, grid, cs);
+      return plan.warps == W ? launch_decode<D, Q4, NT, false, W>(a, grid, cs) : launch_decode<D, Q4, NT, false, WIDE>(a, grid, cs);
+    };
+    return plan.nt == 1 ? of(std::integral_constant<int, 1>{}) : of(std::integral_constant<int, 2>{});
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;

@@ -291,7 +291,7 @@ def test_workspaces_that_do_not_fit_the_call_are_refused():
 def test_many_short_sequences_in_a_roomy_cache(fmt, D):
     """Heads of a few tiles, of one and of none, so that runs and slices begin and end with a head's beginning."""
     B, S = 50, 700 if D == 128 else 1056
-    q, planes = make(B, 6, 2, S, D, 1, fmt, 23)
+    q, planes = make(B, 8, 4, S, D, 1, fmt, 23)
     g = torch.Generator().manual_seed(24)
     lens = torch.randint(0, 130, (B,), generator=g)
     lens[::7] = 0
@@ -308,11 +308,11 @@ def test_sequences_on_both_sides_of_the_lists_sizes(B):
     """Short sequences in a roomy cache against the same in a small one, which takes another path: the same weights,
     added in another order."""
     S, D, g = 1056, 64, torch.Generator(device="cuda").manual_seed(B)
-    planes = kv.new_cache(B, 1, S, D, "q4_0")
+    planes = kv.new_cache(B, 2, S, D, "q4_0")
     for i in (0, 2):
         planes[i].random_(0, 256, generator=g)
         planes[i + 1].copy_(torch.rand(planes[i + 1].shape, device="cuda", generator=g) * 0.1)
-    q = torch.randn((B, 3, 1, D), device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn((B, 6, 1, D), device="cuda", generator=g).to(torch.bfloat16)
     lens = torch.randint(0, 65, (B,), device="cuda", generator=g)
     got = kv.decode(q, *planes, lens)
     want = kv.decode(q, *(t[:, :, :64].contiguous() for t in planes), lens)
@@ -320,3 +320,15 @@ def test_sequences_on_both_sides_of_the_lists_sizes(B):
     assert torch.allclose(got[1], want[1], rtol=2.0 ** -18, atol=2.0 ** -18)
     assert torch.allclose(got[0].float(), want[0].float(), rtol=2.0 ** -7, atol=2.0 ** -7)
     assert bool((got[0][lens == 0] == 0).all()) and bool((got[1][lens == 0] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("D,Sq", [(64, 1), (128, 1), (64, 5), (128, 5)])
+def test_blocks_with_an_sm_to_themselves(D, Sq, fmt):
+    """Few heads of a moderate length: a wide block for each, with tiles for all of its warps, for some and for none."""
+    q, planes = make(4, 8, 4, 900, D, Sq, fmt, 25)
+    lens = torch.tensor([900, 33, 0, 517])
+    for window in (0, 250):
+        got = kv.decode(q, *planes, lens.cuda(), window=window)
+        check(q, planes, lens, got, window=window)
