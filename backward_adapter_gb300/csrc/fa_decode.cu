@@ -34,7 +34,7 @@
 // keys in 8 bits, 32 heads on 8: 61.0 us without, 58.6 with; 500 of up to 300 keys in 4 bits, 8 on 2: 21.8 and 18.4).
 //
 // Measured (device time, captured calls over changing inputs), 4 bits, D = 128: 64 sequences of 1024 to 8192 keys, 32 heads
-// on 8: 62.9 us, 5.4 TB/s, 80% of the measured copy rate; the loop itself runs at that rate, and what is
+// on 8: 61.6 us, 5.5 TB/s, 82% of the measured copy rate; the loop itself runs at that rate, and what is
 // left is the way to the first tile (3.7 us), warps that end before others (2 to 3) and the two joins (4). One sequence of
 // 67584 keys, 16 heads on 4: 15.9 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
 // tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.1 us, launch and latencies.
@@ -308,7 +308,7 @@ struct Slices {
 // kStart for what it costs a warp to begin with it.
 template <int THREADS>
 __device__ __forceinline__ void make_list(const DecodeArgs& a, int* list, bool report) {
-  constexpr int EACH = kMaxListed / THREADS;
+  constexpr int EACH = (kMaxListed + THREADS - 1) / THREADS;
   __shared__ int warp_sum[THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (a.c.B + THREADS - 1) / THREADS, first = threadIdx.x * each;   // this thread's sequences
@@ -841,18 +841,20 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
     if (keep) put(so + warp * ROWS * D, sml + warp * ROWS);
     __syncthreads();
 
-    // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k (and its lanes k + PARTS, ...
-    // do too), which is of warp k / 2: the head its run begins in, and the one it ends in.
-    constexpr int PARTS = 2 * kWarps;
-    const int mine_k = lane % PARTS;
-    const int my_head = left_head[mine_k];
-    const int my_tiles = my_head >= 0 && lane < PARTS ? left_tiles[mine_k] : 0;
-    const float2* my_ml = (mine_k & 1 ? sml : fml) + mine_k / 2 * ROWS;
+    // Heads that warps share, a row of one of them for each warp in turn: lane k looks after part k, which is of warp k / 2:
+    // the head its run begins in, and the one it ends in. Its lanes k + SPAN, ... do so too, for sums over SPAN lanes.
+    constexpr int PARTS = 2 * kWarps, SPAN = PARTS <= 8 ? 8 : PARTS <= 16 ? 16 : 32;
+    constexpr uint32_t FIRST_LANES = 0xffffffffu >> (32 - SPAN);
+    static_assert(PARTS <= 32, "a part a lane");
+    const int my_part = lane % SPAN;
+    const int my_head = my_part < PARTS ? left_head[my_part] : -1;
+    const int my_tiles = lane < PARTS && my_head >= 0 ? left_tiles[lane] : 0;
+    const float2* my_ml = (my_part & 1 ? sml : fml) + my_part / 2 * ROWS;
     int unit = warp;   // counts down the rows until this warp's next one
-    for (uint32_t rest = __ballot_sync(0xffffffffu, my_head >= 0) & ((1u << PARTS) - 1); rest != 0;) {
+    for (uint32_t rest = __ballot_sync(0xffffffffu, my_head >= 0) & FIRST_LANES; rest != 0;) {
       const int head = __shfl_sync(0xffffffffu, my_head, __ffs(rest) - 1);
       const bool mine = my_head == head;
-      const uint32_t parts = __ballot_sync(0xffffffffu, mine) & ((1u << PARTS) - 1);
+      const uint32_t parts = __ballot_sync(0xffffffffu, mine) & FIRST_LANES;
       rest &= ~parts;
       if (unit >= rows) {
         unit -= rows;
@@ -867,11 +869,11 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
         const float2 ml = mine ? my_ml[col] : make_float2(-CUDART_INF_F, 0.f);
         float top = ml.x;
 #pragma unroll
-        for (int x = kWarps; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float w = ml.x == -CUDART_INF_F ? 0.f : exp2_fast(ml.x - top);   // -inf: a warp without a tile
+        for (int x = SPAN / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float w = mine ? exp2_fast(ml.x - top) : 0.f;
         float l = w * ml.y;
 #pragma unroll
-        for (int x = kWarps; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        for (int x = SPAN / 2; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
         float o[D / 32];
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) o[j] = 0.f;
@@ -997,12 +999,15 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
   d.warps = alone ? wide_of(c.D, d.nt) : warps_of(c.D);
   const bool few = alone ? tiles <= 6 * d.warps && tiles * (sms - blocks) <= 3LL * d.warps * sms : tiles <= 4 * d.warps;
   d.slices = !few && c.B <= kMaxListed;
-  if (d.slices) d.warps = warps_of(c.D);
+  // Wide blocks for slices as well where there are heads enough that most are whole in one (64 sequences of 1024 to 8192 keys in
+  // 4 bits, 32 heads on 8: 61.6 us, 62.9 in narrow ones; one sequence of 67584 keys, 16 heads on 4: 16.2 and 15.9).
+  const bool wide = d.nt == 1 && heads >= 2LL * sms;
+  if (d.slices) d.warps = wide ? wide_of(c.D, d.nt) : warps_of(c.D);
   const int warps = d.warps;
   d.blocks = heads;
   if (d.slices) {
     // as many blocks as the SMs hold at a time, no slice below a tile a warp
-    const long long all = (long long)held_of(c.D, d.nt) * sms / d.row_blocks, some = heads * tiles / warps;
+    const long long all = (long long)(wide ? 1 : held_of(c.D, d.nt)) * sms / d.row_blocks, some = heads * tiles / warps;
     d.blocks = all < some ? all : some;
     if (d.blocks < 1) d.blocks = 1;
     const size_t rows = (size_t)d.row_blocks * d.blocks * d.nt * 8;
@@ -1106,7 +1111,11 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
     constexpr bool Q4 = decltype(q4)::value;
     auto of = [&](auto nt) {
       constexpr int NT = decltype(nt)::value, W = warps_of(D), WIDE = wide_of(D, NT);
-      if (plan.slices) return launch_decode<D, Q4, NT, true, W>(a, grid, cs);
+      if (plan.slices) {
+        if constexpr (NT == 1)
+          if (plan.warps == WIDE) return launch_decode<D, Q4, NT, true, WIDE>(a, grid, cs);
+        return launch_decode<D, Q4, NT, true, W>(a, grid, cs);
+      }
       return plan.warps == W ? launch_decode<D, Q4, NT, false, W>(a, grid, cs) : launch_decode<D, Q4, NT, false, WIDE>(a, grid, cs);
     };
     return plan.nt == 1 ? of(std::integral_constant<int, 1>{}) : of(std::integral_constant<int, 2>{});

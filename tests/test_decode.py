@@ -303,14 +303,15 @@ def test_many_short_sequences_in_a_roomy_cache(fmt, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,fmt", [(64, "q4_0"), (128, "q4_0"), (128, "q8_0")])
 @pytest.mark.parametrize("B", [128, 129, 700, 1024, 1025])
-def test_sequences_on_both_sides_of_the_lists_sizes(B):
+def test_sequences_on_both_sides_of_the_lists_sizes(B, D, fmt):
     """Short sequences in a roomy cache against the same in a small one, which takes another path: the same weights,
     added in another order."""
-    S, D, g = 1056, 64, torch.Generator(device="cuda").manual_seed(B)
-    planes = kv.new_cache(B, 2, S, D, "q4_0")
+    S, g = 1056 if D == 64 else 544, torch.Generator(device="cuda").manual_seed(B)
+    planes = kv.new_cache(B, 2, S, D, fmt)
     for i in (0, 2):
-        planes[i].random_(0, 256, generator=g)
+        planes[i].random_(*((0, 256) if fmt == "q4_0" else (-127, 128)), generator=g)
         planes[i + 1].copy_(torch.rand(planes[i + 1].shape, device="cuda", generator=g) * 0.1)
     q = torch.randn((B, 6, 1, D), device="cuda", generator=g).to(torch.bfloat16)
     lens = torch.randint(0, 65, (B,), device="cuda", generator=g)
@@ -318,7 +319,9 @@ def test_sequences_on_both_sides_of_the_lists_sizes(B):
     want = kv.decode(q, *(t[:, :, :64].contiguous() for t in planes), lens)
     torch.cuda.synchronize()
     assert torch.allclose(got[1], want[1], rtol=2.0 ** -18, atol=2.0 ** -18)
-    assert torch.allclose(got[0].float(), want[0].float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+    # both are off by two fp16 half steps of each weight, 2^-10 of the largest value, and a bf16 half step of the result
+    top = float(planes[3].max()) * (8 if fmt == "q4_0" else 127)
+    assert torch.allclose(got[0].float(), want[0].float(), rtol=2.0 ** -7, atol=2.0 ** -9 * top)
     assert bool((got[0][lens == 0] == 0).all()) and bool((got[1][lens == 0] == 0).all())
 
 
@@ -332,3 +335,28 @@ def test_blocks_with_an_sm_to_themselves(D, Sq, fmt):
     for window in (0, 250):
         got = kv.decode(q, *planes, lens.cuda(), window=window)
         check(q, planes, lens, got, window=window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (128, 12)])
+def test_many_heads_of_any_length(D, G, fmt):
+    """Twice as many heads as SMs and more, cut anywhere, against each sequence by itself, whose few heads take other
+    paths: the same weights, added in another order."""
+    B, Hkv, S = 80, 4, 800 if D == 128 else 1500
+    gen = torch.Generator(device="cuda").manual_seed(26)
+    planes = kv.new_cache(B, Hkv, S, D, fmt)
+    for i in (0, 2):
+        planes[i].random_(*((0, 256) if fmt == "q4_0" else (-127, 128)), generator=gen)
+        planes[i + 1].copy_(torch.rand(planes[i + 1].shape, device="cuda", generator=gen) * (0.1 if fmt == "q4_0" else 0.01))
+    q = torch.randn((B, Hkv * G, 1, D), device="cuda", generator=gen).to(torch.bfloat16)
+    lens = torch.randint(0, S + 1, (B,), device="cuda", generator=gen)
+    lens[3], lens[4], lens[5] = 0, S, 1
+    got = kv.decode(q, *planes, lens)
+    for b in list(range(8)) + [40, 78, 79]:
+        want = kv.decode(q[b:b + 1], *(t[b:b + 1] for t in planes), lens[b:b + 1])
+        assert torch.allclose(got[1][b], want[1][0], rtol=2.0 ** -18, atol=2.0 ** -18)
+        # as above
+        top = float(planes[3][b].max()) * (8 if fmt == "q4_0" else 127)
+        err = (got[0][b].float() - want[0][0].float()).abs()
+        assert bool((err <= 2.0 ** -9 * top + 2.0 ** -7 * want[0][0].float().abs()).all()), float(err.max())
