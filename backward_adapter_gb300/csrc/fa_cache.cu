@@ -1,8 +1,10 @@
 // Writing and reading back a quantized K/V cache (fa_cache_write, fa_cache_read): the chunk's K and
 // V go into the cached window that the attention entry points read in place (llama.cpp PR #57,
 // commit 2394a4c). Both passes touch every byte once and are bound by HBM, or by their launch when
-// a few rows are written: 67584 keys of 4 heads of 128 in 4 bits are read back in 27 us, 6.5 TB/s, 96% of the
-// measured copy rate; a token of 32 sequences with 8 heads is written in 2 us.
+// a few rows are written, and writing many by its instructions. 67584 keys of 4 heads of 128 in 4 bits are read back to bf16 in
+// 27 us, 6.5 TB/s, 96% of the measured copy rate, and written from it in 47 us, 3.8 TB/s (103 with a division for each
+// feature; two lanes a block and one reciprocal leave less than half of the instructions); a token of 32 sequences with 8 heads is
+// written in 2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,47 +17,39 @@
 namespace fa {
 namespace {
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
+    x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = a.z; x[4 * i + 3] = a.w;
   }
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]),
-                                            tc::pack_bf16x2(x[4], x[5]), tc::pack_bf16x2(x[6], x[7]));
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const uint64_t (&x)[4]) {
-  float y[8];
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) tc::f32x2_split(x[i], y[2 * i], y[2 * i + 1]);
-  store8(p, y);
+  for (int i = 0; i < 2; ++i) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
 }
 
-// A thread quantizes 8 features of a row, four lanes a block of 32. blockIdx.y: 0 for K, 1 for V.
+// A thread quantizes 16 features of a row, two lanes a block of 32. blockIdx.y: 0 for K, 1 for V. Two rows a thread measured
+// slower (58.4 us where this takes 47.0, see the head of the file), and lanes of 8 features, with twice the work for a block, 76.4.
 template <typename T, int D, bool Q4>
 __global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k, RowView v, unsigned rows, unsigned n_rows,
                                                           const int64_t* __restrict__ begin, long long begin_all,
                                                           const int64_t* __restrict__ count, unsigned* status) {
-  constexpr int LANES = D / 8;
+  constexpr int LANES = D / 16;
   const unsigned g = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int l = threadIdx.x % LANES;
   const RowView src = blockIdx.y ? v : k;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float x[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) x[j] = 0.f;
   bool on = false;
   size_t row = 0;
   if (g < rows) {
@@ -65,25 +59,47 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k
       if (first < c.S && first + r >= 0 && first + r < c.S) {
         on = true;
         row = (size_t)bh * c.S + (size_t)(first + r);
-        load8(static_cast<const T*>(src.ptr) + b * src.sb + r * src.ss + h * src.sh + 8 * l, x);
+        load16(static_cast<const T*>(src.ptr) + b * src.sb + r * src.ss + h * src.sh + 16 * l, x);
       } else if (l == 0 && status != nullptr) {
         atomicCAS(status, 0u, 0x40000000u | kSiteCacheRow);
       }
     }
   }
-  uint32_t lo, hi;
-  const __half d = quantize_block<Q4>(x, lo, hi);
+  uint32_t w[4], p[2];
+  const __half d = quantize_half_block<Q4>(x, w);
+  const bool second = l & 1;
   if constexpr (Q4) {
-    // lanes 2 and 3 hold features 16 .. 31, whose four bits sit above those of features 0 .. 15
-    lo |= __shfl_down_sync(0xffffffffu, lo, 2) << 4;
-    hi |= __shfl_down_sync(0xffffffffu, hi, 2) << 4;
+    // features 16 .. 31 are the high four bits of features 0 .. 15; the first lane makes bytes 0 .. 7 of the block
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? w[u] : w[2 + u], 1);
+      p[u] = second ? got | w[2 + u] << 4 : w[u] | got << 4;
+    }
   }
   if (!on) return;
-  const int blk = l / 4, part = l % 4;
   uint8_t* values = static_cast<uint8_t*>(blockIdx.y ? c.v_q : c.k_q);
-  if (!Q4 || part < 2)
-    *reinterpret_cast<uint2*>(values + row * (Q4 ? D / 2 : D) + (Q4 ? 16 * blk + 8 * part : 8 * l)) = make_uint2(lo, hi);
-  if (part == 0) (blockIdx.y ? c.v_d : c.k_d)[row * (D / 32) + blk] = __half_as_ushort(d);
+  if constexpr (Q4) *reinterpret_cast<uint2*>(values + row * (D / 2) + 8 * l) = make_uint2(p[0], p[1]);
+  else *reinterpret_cast<uint4*>(values + row * D + 16 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (!second) (blockIdx.y ? c.v_d : c.k_d)[row * (D / 32) + l / 2] = __half_as_ushort(d);
+}
+
+// f(i, head, row, whether the head is another than the last time) for this thread's rows first, first + step, ...,
+// without a division for each.
+template <int ROWS, typename F>
+__device__ __forceinline__ void each_row(unsigned first, unsigned step, unsigned rows, unsigned n_rows, F f) {
+  unsigned bh = first / n_rows, r = first % n_rows;
+  bool other = true;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (first + i * step >= rows) break;
+    f(i, bh, r, other);
+    r += step;
+    other = r >= n_rows;
+    if (other) {
+      bh += r / n_rows;
+      r %= n_rows;
+    }
+  }
 }
 
 // The values of a word of 4-bit numbers, pairs of neighbours: of its low nibbles to x, of its high ones to y. Masked, a
@@ -103,70 +119,71 @@ __device__ __forceinline__ void values_q4(uint32_t w, uint64_t d24, uint64_t d20
   y[1] = tc::mul_f32x2(tc::f32x2(f.y, p.y), d20);
 }
 
-// A thread reads 16 features (half a block's bytes) of ROWS rows, all of them on their way at once.
-// blockIdx.y: 0 for K, 1 for V.
+// 16 bytes of values.
+__device__ __forceinline__ void store16(float* p, const uint64_t (&x)[2]) {
+  float4 v;
+  tc::f32x2_split(x[0], v.x, v.y);
+  tc::f32x2_split(x[1], v.z, v.w);
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint64_t (&x)[4]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    tc::f32x2_split(x[i], lo, hi);
+    u[i] = tc::pack_bf16x2(lo, hi);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// A thread reads N bytes of numbers of ROWS rows, all of them on their way at once, and writes N features of 16 bytes, which
+// with its neighbours' fill whole sectors (q4_0: two times N, of the low and of the high nibbles). blockIdx.y: 0 for K, 1 for V.
 template <typename T, int D, bool Q4, int ROWS>
 __global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long begin, unsigned rows, unsigned n_rows,
                                                          RowView k, RowView v) {
-  constexpr int PARTS = D / 16, STEP = 256 / PARTS;   // rows a block takes at a time
+  constexpr int N = 16 / sizeof(T), PARTS = (Q4 ? D / 2 : D) / N, STEP = 256 / PARTS;   // rows a block takes at a time
   const int part = threadIdx.x % PARTS;
   const unsigned first = blockIdx.x * (STEP * ROWS) + threadIdx.x / PARTS;
   const RowView dst = blockIdx.y ? v : k;
-  const uint8_t* values = static_cast<const uint8_t*>(blockIdx.y ? c.v_q : c.k_q);
-  const uint16_t* scales = blockIdx.y ? c.v_d : c.k_d;
-  // f(i, head, row, whether the head is another than the last time)
-  auto each_row = [&](auto f) {
-    unsigned bh = first / n_rows, r = first % n_rows;
-    bool other = true;
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      if (first + i * STEP >= rows) break;
-      f(i, bh, r, other);
-      r += STEP;
-      other = r >= n_rows;
-      if (other) {
-        bh += r / n_rows;
-        r %= n_rows;
-      }
-    }
-  };
-  uint4 w[ROWS];
+  const uint8_t* values = static_cast<const uint8_t*>(blockIdx.y ? c.v_q : c.k_q) + N * part;
+  const int blk = N * part / (Q4 ? 16 : 32);
+  const uint16_t* scales = (blockIdx.y ? c.v_d : c.k_d) + blk;
+  uint32_t w[ROWS][N / 4];
   uint16_t scale[ROWS];
-  each_row([&](int i, unsigned bh, unsigned r, bool) {
+  each_row<ROWS>(first, STEP, rows, n_rows, [&](int i, unsigned bh, unsigned r, bool) {
     const size_t row = (size_t)bh * c.S + (size_t)(begin + r);
-    scale[i] = __ldg(scales + row * (D / 32) + part / 2);
-    if constexpr (Q4) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(values + row * (D / 2) + 8 * part));
-      w[i].x = u.x;
-      w[i].y = u.y;
+    scale[i] = __ldg(scales + row * (D / 32));
+    const uint8_t* at = values + row * (Q4 ? D / 2 : D);
+    if constexpr (N == 8) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(at));
+      w[i][0] = u.x;
+      w[i][1] = u.y;
     } else {
-      w[i] = __ldg(reinterpret_cast<const uint4*>(values + row * D + 16 * part));
+      w[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
     }
   });
   T* head = nullptr;
-  each_row([&](int i, unsigned bh, unsigned r, bool other) {
-    if (other) head = static_cast<T*>(dst.ptr) + bh / c.Hkv * dst.sb + bh % c.Hkv * dst.sh;
+  each_row<ROWS>(first, STEP, rows, n_rows, [&](int i, unsigned bh, unsigned r, bool other) {
+    if (other) head = static_cast<T*>(dst.ptr) + bh / c.Hkv * dst.sb + bh % c.Hkv * dst.sh + (Q4 ? blk * 32 + N * part % 16 : N * part);
     const float d = __half2float(__ushort_as_half(scale[i]));
     T* out = head + r * dst.ss;
+    uint64_t x[N / 2];
     if constexpr (Q4) {
       const uint64_t d24 = tc::f32x2(d * 16777216.f, d * 16777216.f), d20 = tc::f32x2(d * 1048576.f, d * 1048576.f);
-      uint64_t x[4], y[4];
-      values_q4(w[i].x, d24, d20, x, y);
-      values_q4(w[i].y, d24, d20, x + 2, y + 2);
-      out += part / 2 * 32 + part % 2 * 8;
-      store8(out, x);
-      store8(out + 16, y);
-    } else {
-      float x[8], y[8];
-      const uint32_t u[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
+      uint64_t y[N / 2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = s8_to_f32(u[j / 4], j % 4) * d;
-        y[j] = s8_to_f32(u[2 + j / 4], j % 4) * d;
+      for (int j = 0; j < N / 4; ++j) values_q4(w[i][j], d24, d20, x + 2 * j, y + 2 * j);
+      store16(out, x);
+      store16(out + 16, y);
+    } else {
+      const uint64_t dd = tc::f32x2(d, d);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        const uint32_t u = w[i][j / 2] ^ 0x80808080u;
+        x[j] = tc::mul_f32x2(tc::f32x2(s8_to_f32(u, 2 * j % 4), s8_to_f32(u, 2 * j % 4 + 1)), dd);
       }
-      out += 16 * part;
-      store8(out, x);
-      store8(out + 8, y);
+      store16(out, x);
     }
   });
 }
@@ -182,7 +199,7 @@ cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowVi
                                const int64_t* begin, long long begin_all, const int64_t* count, unsigned* status,
                                cudaStream_t st) {
   const long long rows = (long long)c.B * c.Hkv * n_rows;
-  const unsigned n = blocks_for(rows, 256 / (c.D / 8));
+  const unsigned n = blocks_for(rows, 256 / (c.D / 16));
   if (n == 0) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
     kernel<<<dim3(n, 2), 256, 0, st>>>(c, k, v, (unsigned)rows, (unsigned)n_rows, begin, begin_all, count, status);
@@ -204,8 +221,8 @@ cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowVi
 cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, int dtype, const RowView& k,
                               const RowView& v, cudaStream_t st) {
   const long long rows = (long long)c.B * c.Hkv * n_rows;
-  const int step = 256 / (c.D / 16);
-  // four rows a thread, where that still leaves blocks for every SM (67584 keys of 4 heads in 4 bits: 27.1 us; one 31.6, eight 27.4)
+  const int parts = (c.q4 ? c.D / 2 : c.D) / (dtype == DT_BF16 ? 8 : 4), step = 256 / parts;
+  // four rows a thread, where that still leaves blocks for every SM (67584 keys of 4 heads in 4 bits: 27.2 us; one 31.6, eight 27.4)
   const bool many = rows >= 8LL * step * sm_count();
   const unsigned n = blocks_for(rows, many ? 4 * step : step);
   if (n == 0) return cudaErrorInvalidConfiguration;

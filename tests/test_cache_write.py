@@ -276,3 +276,30 @@ def test_begins_that_a_64_bit_number_does_not_hold_are_refused():
             kv.cache_write(x, x, *planes, begin)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(planes, before))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+def test_quotients_between_two_numbers_and_odd_scales(fmt):
+    """Values half way between two stored numbers, scales that fp16 holds with few bits or not at all, equal magnitudes of both
+    signs in either half of a block, and rows of nothing: the oracle's blocks, bit for bit."""
+    g = np.random.default_rng(7)
+    B, H, n, D = 1, 2, 300, 128
+    half = g.integers(-254, 255, (B, H, n, D)).astype(np.float32) / 2
+    x = half * np.exp2(g.integers(-30, 12, (B, H, n, 1))).astype(np.float32)
+    x[:, :, ::5] = g.integers(-16, 17, x[:, :, ::5].shape) / np.float32(2)
+    x[:, :, 1::50] = 0
+    x[:, :, 2::50] *= np.float32(1e-8)
+    x[:, :, 3::50] *= np.float32(1e30)
+    x[:, 0, 4::50, 3] = np.inf
+    x[:, 1, 4::50, 40] = np.nan
+    y = -x[:, :, ::-1].copy()
+    for dtype in (torch.float32, torch.bfloat16):
+        planes = kv.new_cache(B, H, n, D, fmt)
+        t = [torch.from_numpy(np.ascontiguousarray(a)).to(dtype).cuda() for a in (x, y)]
+        kv.cache_write(t[0], t[1], *planes, 0)
+        torch.cuda.synchronize()
+        for i, a in enumerate(t):
+            q, d = ref.quantize(a.float().cpu().numpy(), fmt)
+            np.testing.assert_array_equal(planes[2 * i].cpu().numpy(), q)
+            np.testing.assert_array_equal(planes[2 * i + 1].cpu().numpy(), d)
