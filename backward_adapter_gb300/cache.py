@@ -194,7 +194,8 @@ def decode(q, k_q, k_d, v_q, v_d, lengths=None, *, scale=None, window: int = 0, 
             raise ValueError(f"lse must be float32 {(B, Hq, Sq)} on {device}")
         ft._need_cuda(lse)
     lens = None if lengths is None else _per_sequence("lengths", lengths, B, device)
-    window = min(max(int(window), -1), 0x7fffffff)   # as a 32-bit number; a longer window than any cache hides nothing
+    if not 0 <= window <= 0x7fffffff:   # as a 32-bit number; a longer window than any cache hides nothing
+        window = -1 if window < 0 else 0x7fffffff
     call = _DecodeCall(*c, Hq, Sq, window, code, 1.0 / math.sqrt(D) if scale is None else scale, 0)
     at = ctypes.addressof(call)
     lib = ft.load_library()

@@ -331,7 +331,10 @@ def _like(t: torch.Tensor, stream=None) -> torch.Tensor:
 def _held(n) -> int:
     """A Python number as the nearest one of an int64's range less its ends, which ctypes would wrap; the C ABI then
     refuses it as it does any other that is out of its range."""
-    return min(max(int(n), 1 - (1 << 63)), (1 << 63) - 2)
+    n = int(n)
+    if -0x7fffffffffffffff < n < 0x7fffffffffffffff:
+        return n
+    return -0x7fffffffffffffff if n < 0 else 0x7ffffffffffffffe
 
 
 def _rows(t: torch.Tensor, layout: str):

@@ -123,7 +123,7 @@ def _params(q, k, inv_freq, positions, q_weight, k_weight, eps, interleaved, fac
         if positions.get_device() != on or not positions.is_contiguous():
             raise ValueError(f"positions must be contiguous and on {q.device}")
     return (B, S, Hq, Hkv, D, code, w_code, rot, 1 if interleaved else 0, 1 if norm else 0, eps, factor,
-            offset if -(1 << 62) <= offset <= 1 << 62 else ft._held(offset), pos_stride, 0, 0)
+            offset if offset == 0 else ft._held(offset), pos_stride, 0, 0)
 
 
 def _same(name: str, t: torch.Tensor, like: torch.Tensor) -> None:
