@@ -6,9 +6,12 @@
 //     s_j = scale * sum_blocks d_jb <n_jb, q_b>,   o = sum_j sum_blocks (p_j d_jb) n_jb :
 // the tensor cores multiply whole numbers, exact as fp16, by q and by p * d, and K's scales never touch
 // the 8- or 4-bit data. Scores, softmax statistics and sums are fp32. Query rows are scaled by a power of
-// two to the top of fp16's range, where a bf16 value down to 2^-24 of the row's largest is exact; p and
-// p * d are rounded to fp16, 2^-11 of their values each at most, with a power of two that keeps them below 2^15
-// whatever the scales are (see `level`).
+// two to the top of fp16's range, where a bf16 value down to 2^-24 of the row's largest is exact; p d_jb is
+// formed in fp32 and rounded once to fp16. Weights are relative to a power of two (base 2, `base`) that follows the largest
+// p d_jb that a query row has met, not the largest p: a first key that takes most of the weight and has small values
+// leaves the others their bits, and so does one large value elsewhere. The largest is at least 2^kSet when base is set
+// and at most 2^kMost later, so a weight down to 2^(-14 - kSet), 2^-24, of the largest in its run is off by 2^-11 of its value
+// at most, and a smaller one by 2^-35 of the largest (a key whose values are all 0 counts with a scale of 2^-32).
 //
 // What bounds it: the planes are read once, 144 bytes a key for D = 128 in 4 bits, so HBM; next to
 // that the instructions that turn packed bits into operands. Keys are the 16 rows of an
@@ -34,10 +37,12 @@
 // keys in 8 bits, 32 heads on 8: 61.0 us without, 58.6 with; 500 of up to 300 keys in 4 bits, 8 on 2: 21.8 and 18.4).
 //
 // Measured (device time, captured calls over changing inputs), 4 bits, D = 128: 64 sequences of 1024 to 8192 keys, 32 heads
-// on 8: 61.6 us, 5.5 TB/s, 82% of the measured copy rate; the loop itself runs at that rate, and what is
+// on 8: 62.3 us, 5.5 TB/s, 81% of the measured copy rate; the loop itself runs at that rate, and what is
 // left is the way to the first tile (3.7 us), warps that end before others (2 to 3) and the two joins (4). One sequence of
-// 67584 keys, 16 heads on 4: 15.9 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
-// tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.1 us, launch and latencies.
+// 67584 keys, 16 heads on 4: 16.2 us against 5.8 for the bytes; a warp has four or five tiles then, and list, first
+// tile and joins are most of it. Four sequences of up to 1000 keys in 8 bits, D = 64: 6.0 us, launch and latencies. (With p and p d
+// each rounded to fp16, relative to p alone, these took 61.6, 15.9 and 6.1 us; the alternatives to single choices
+// below were measured then.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -58,6 +63,8 @@ constexpr int kTile = 32;         // keys a warp takes at a time
 constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
 constexpr int kStart = 3;         // tiles' time that a head costs the warp that begins with it, measured
 constexpr float kNoBase = -3e38f; // below every score
+constexpr float kSet = 10.f;      // the largest weight times scale, base 2, when a row's reference is set,
+constexpr float kMost = 14.f;     // and what it may become before the reference is set again; fp16 ends at 16
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct DecodeArgs {
@@ -109,6 +116,11 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -184,11 +196,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 __device__ __forceinline__ uint32_t add_f16x2(uint32_t x, uint32_t y) {
   const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -249,34 +256,27 @@ __device__ __forceinline__ void load_scales(uint32_t at, float (&d)[NB]) {
     d[2 * i + 1] = x.y;
   }
 }
-// Their bits or-ed.
+// As they are, two a word.
 template <int NB>
-__device__ __forceinline__ uint32_t scale_bits(uint32_t at) {
+__device__ __forceinline__ void load_scale_words(uint32_t at, uint32_t (&u)[NB / 2]) {
   if constexpr (NB == 4) {
-    const uint2 x = lds64(at);
-    return x.x | x.y;
-  } else {
-    return lds32(at);
-  }
-}
-// Those of two keys one after the other, as fp16 pairs of the keys for each block; their bits or-ed.
-template <int NB>
-__device__ __forceinline__ uint32_t load_scale_pairs(uint32_t at, uint32_t (&d)[NB]) {
-  uint32_t u[NB];   // key 0's, key 1's
-  if constexpr (NB == 4) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at));
-  } else {
     const uint2 x = lds64(at);
     u[0] = x.x; u[1] = x.y;
+  } else {
+    u[0] = lds32(at);
   }
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < NB / 2; ++i) {
-    d[2 * i] = __byte_perm(u[i], u[NB / 2 + i], 0x5410);
-    d[2 * i + 1] = __byte_perm(u[i], u[NB / 2 + i], 0x7632);
-    bits |= u[i] | u[NB / 2 + i];
-  }
-  return bits;
+}
+__device__ __forceinline__ float scale_of(uint32_t u, bool high) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&u);
+  return high ? __high2float(x) : __low2float(x);
+}
+// The base 2 logarithm of the largest magnitude among a key's scales, held to [-32, 16]: below fp16's smallest where all are
+// 0, so that a key without values does not set what the others' weights are relative to.
+template <int NB>
+__device__ __forceinline__ float log2_largest(const uint32_t (&u)[NB / 2]) {
+  __half2 x = __habs2(*reinterpret_cast<const __half2*>(&u[0]));
+  if constexpr (NB == 4) x = __hmax2(x, __habs2(*reinterpret_cast<const __half2*>(&u[1])));
+  return fminf(fmaxf(log2_fast(__half2float(__hmax(__low2half(x), __high2half(x)))), -32.f), 16.f);
 }
 
 // Warps of a block and blocks an SM holds. Rows of 128 features want 168 registers a thread (at 128 they spilled in the
@@ -373,6 +373,13 @@ __device__ __forceinline__ void add_part(float (&o)[4], float w, float4 x) {
   o[3] = fmaf(w, x.w, o[3]);
 }
 
+// (base + log2 l) ln 2, l's power of two added first: base is about its negative where the logarithm is small.
+__device__ __forceinline__ float lse_of(float base, float l) {
+  int e;
+  const float m = frexpf(l, &e);
+  return (base + (float)e + log2f(m)) * kLn2;
+}
+
 // Row r of a head from a warp's sums (D / 32 features a lane): the result, or what is left of it.
 template <int D>
 __device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int r, const float (&o)[D / 32], float l,
@@ -389,7 +396,7 @@ __device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + q_offset(a, b, h, r) + lane * F);
 #pragma unroll
   for (int j = 0; j < F; j += 2) dst[j / 2] = tc::pack_bf16x2(o[j] * inv, o[j + 1] * inv);
-  if (lane == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : (top + log2f(l)) * kLn2;
+  if (lane == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : lse_of(top, l);
 }
 
 // A block's work: SLICES: slice blockIdx.x of the list; else the head blockIdx.x. NT * 8 query rows from
@@ -530,8 +537,6 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
       unscale[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
 
-    float limit[NT][2];         // scores up to base + limit fit, limit = level + 8
-    uint32_t fields[NT][2];     // exponent fields (at bit 10) of the V scales of all keys seen, or-ed
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -539,8 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][i][j] = 0.f;
       base[n][0] = base[n][1] = kNoBase;
-      sum[n][0] = sum[n][1] = limit[n][0] = limit[n][1] = 0.f;
-      fields[n][0] = fields[n][1] = 0;
+      sum[n][0] = sum[n][1] = 0.f;
     }
     // keys that every query row sees: [all_from, all_to]
     const int all_to = kr.len - a.Sq, all_from = a.window > 0 ? kr.len - 1 - a.window : 0;
@@ -585,71 +589,53 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
           }
       }
 
-      // V's scales, of keys 2 t and 2 t + 1 of each eight, and their exponent fields or-ed.
-      uint32_t dv[4][NB], bits = 0;
+      // V's scales, of the same keys
+      uint32_t dv[4][NB / 2];
+      float lg[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bits |= load_scale_pairs<NB>(at + S::VD_OFF + (8 * i + 2 * t) * S::SC, dv[i]);
-      bits = (bits | bits >> 16) & 0x7c00u;
+      for (int i = 0; i < 4; ++i) {
+        load_scale_words<NB>(at + S::VD_OFF + (8 * i + g) * S::SC, dv[i]);
+        lg[i] = log2_largest<NB>(dv[i]);
+      }
 
-      uint32_t pt[NT][4];   // the weights as fp16: of query row g, keys 2 t and 2 t + 1 of each eight
+      uint32_t hidden[NT];   // bit 2 i + j: of key 8 i + g and column 2 t + j
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint32_t hidden = 0;   // bit 4 m + j: pair j of half m
+        hidden[n] = 0;
         if constexpr (EDGE) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int pos = kr.len - a.Sq + (r0 + n * 8 + 2 * t + j) % a.Sq;
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int key = first + 16 * m + g + 8 * u;
-                if (key > pos || (a.window > 0 && pos - key > a.window)) {
-                  s[n][m][2 * u + j] = -CUDART_INF_F;
-                  hidden |= 1u << (4 * m + 2 * u + j);
-                }
+            for (int i = 0; i < 4; ++i) {
+              const int key = first + 8 * i + g;
+              if (key > pos || (a.window > 0 && pos - key > a.window)) {
+                s[n][i / 2][i % 2 * 2 + j] = -CUDART_INF_F;
+                hidden[n] |= 1u << (2 * i + j);
               }
+            }
           }
         }
-        float top[2];
+        float top[2];   // of p d, base 2
 #pragma unroll
-        for (int j = 0; j < 2; ++j) top[j] = fmaxf(fmaxf(s[n][0][j], s[n][0][j + 2]), fmaxf(s[n][1][j], s[n][1][j + 2]));
-        // The weights' reference stays until a score or a scale outgrows it, which no lane has to ask the others for.
-        const bool fits = fmaf(top[0], unscale[n][0], -base[n][0]) <= limit[n][0] &&
-                          fmaf(top[1], unscale[n][1], -base[n][1]) <= limit[n][1] &&
-                          (bits & ~(fields[n][0] & fields[n][1])) == 0;
-        if (EDGE || __any_sync(0xffffffffu, !fits)) {
-          // A column's level is 21 - (the or of the exponent fields of the scales it has seen, no less than any of
-          // them), and at most 7. A scale is below 2^(7 - level), the largest weight is 2^level when the reference is
-          // set and at most 2^(level + 8) later, and their product below 2^15.
-          uint32_t all = 0;
-          if constexpr (!EDGE) all = __reduce_or_sync(0xffffffffu, bits);
+        for (int j = 0; j < 2; ++j) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = fmaf(s[n][i / 2][i % 2 * 2 + j], unscale[n][j], lg[i]);
+          top[j] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        }
+        // The reference stays until a weight times its scale outgrows it, which no lane has to ask the others for.
+        const bool fits = top[0] - base[n][0] <= kMost && top[1] - base[n][1] <= kMost;
+        if (__any_sync(0xffffffffu, !fits)) {
           float f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
             top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
             top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-            if constexpr (EDGE) {   // of the keys that this column sees
-              all = 0;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t x = scale_bits<NB>(at + S::VD_OFF + (8 * i + g) * S::SC);
-                all |= (hidden >> (2 * i + j)) & 1u ? 0u : (x | x >> 16) & 0x7c00u;
-              }
-              all |= __shfl_xor_sync(0xffffffffu, all, 4);
-              all |= __shfl_xor_sync(0xffffffffu, all, 8);
-              all |= __shfl_xor_sync(0xffffffffu, all, 16);
-            }
-            fields[n][j] |= all;
-            const float level = fminf(fmaf((float)(int)fields[n][j], -1.f / 1024, 21.f), 7.f);
-            const float score = top[j] == -CUDART_INF_F ? -CUDART_INF_F : top[j] * unscale[n][j];
-            float now = base[n][j];
-            if (now != kNoBase) now += limit[n][j] - 8.f - level;   // as much as the level has fallen
-            if (score - now > level + 8.f) now = score - level;
+            const float now = top[j] - base[n][j] > kMost ? top[j] - kSet : base[n][j];
             f[j] = exp2_fast(base[n][j] - now);
             base[n][j] = now;
-            limit[n][j] = level + 8.f;
             sum[n][j] *= f[j];
           }
 #pragma unroll
@@ -665,12 +651,10 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float p = exp2_fast(fmaf(s[n][m][j], unscale[n][j & 1], -base[n][j & 1]));
-            if constexpr (EDGE) p = (hidden >> (4 * m + j)) & 1u ? -0.f : p;   // told from a weight that is small
+            if constexpr (EDGE) p = (hidden[n] >> (4 * m + j)) & 1u ? 0.f : p;   // -inf times a scale of 0 is no number
             s[n][m][j] = p;
             sum[n][j & 1] += p;
           }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pt[n][i] = transpose8x8(pack_f16x2(s[n][i / 2][i % 2 * 2], s[n][i / 2][i % 2 * 2 + 1]));
       }
 
       // o += V^T (p d)
@@ -697,22 +681,24 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
           f[i][3] = add_f16x2(f[i][3], kOff1);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          uint32_t w[4];   // of query row g, keys 2 t and 2 t + 1 of each eight
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float d = scale_of(dv[i][k / 2], k % 2);
+            float w0 = s[n][i / 2][i % 2 * 2] * d, w1 = s[n][i / 2][i % 2 * 2 + 1] * d;
+            if constexpr (EDGE) {   // a hidden key's scale may be anything
+              w0 = (hidden[n] >> (2 * i)) & 1u ? 0.f : w0;
+              w1 = (hidden[n] >> (2 * i + 1)) & 1u ? 0.f : w1;
+            }
+            w[i] = transpose8x8(pack_f16x2(w0, w1));
+          }
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            uint32_t w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t p = pt[n][2 * m + i];
-              w[i] = mul_f16x2(p, dv[2 * m + i][k]);
-              if constexpr (EDGE) {   // a hidden key's scale may be anything
-                if ((p & 0xffffu) == 0x8000u) w[i] &= 0xffff0000u;
-                if (p >> 16 == 0x8000u) w[i] &= 0xffffu;
-              }
-            }
-            mma_f16(acc[n][2 * k], f[2 * m][0], f[2 * m][1], f[2 * m + 1][0], f[2 * m + 1][1], w[0], w[1]);
-            mma_f16(acc[n][2 * k + 1], f[2 * m][2], f[2 * m][3], f[2 * m + 1][2], f[2 * m + 1][3], w[0], w[1]);
+            mma_f16(acc[n][2 * k], f[2 * m][0], f[2 * m][1], f[2 * m + 1][0], f[2 * m + 1][1], w[2 * m], w[2 * m + 1]);
+            mma_f16(acc[n][2 * k + 1], f[2 * m][2], f[2 * m][3], f[2 * m + 1][2], f[2 * m + 1][3], w[2 * m], w[2 * m + 1]);
           }
+        }
       }
     };
 
@@ -771,7 +757,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
 #pragma unroll
         for (int i = 0; i < 2 * NB; ++i)
           *reinterpret_cast<uint32_t*>(o + 16 * i) = tc::pack_bf16x2(acc[n][i][j] * inv, acc[n][i][j + 2] * inv);
-        if (g == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : (base[n][j] + log2f(l)) * kLn2;
+        if (g == 0) a.lse[((size_t)b * a.Hq + h * a.G) * a.Sq + r] = l == 0.f ? 0.f : lse_of(base[n][j], l);
       }
   };
 

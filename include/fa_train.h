@@ -355,9 +355,11 @@ FA_API fa_status fa_cache_read(const fa_cache* c, int64_t begin, int32_t n_rows,
  * own among them: query i sits at position lengths[b] - Sq + i and sees the keys j at or before it
  * (with window w > 0 only those with position - j <= w). A query that sees no key (a position below
  * zero, a length of 0) gets O = 0 and LSE = 0. Keys at or past a sequence's length are not read.
- * K's products are exact in the stored integers and its scales are applied in 32 bits; a weight and
- * its product with a scale of V are rounded to fp16 (K and V are not rounded to bf16 as they are on
- * the training path). Queries are below 2^114 in magnitude.
+ * K's products are exact in the stored integers and its scales are applied in 32 bits; a weight's
+ * product with a scale of V is rounded once to fp16, off by at most 2^-11 of itself, or, below 2^-24
+ * of the largest such product of its query row, by at most 2^-35 of that (a key whose values are all
+ * 0 counts there with a scale of 2^-32). K and V are not rounded to bf16 as they are on the training
+ * path. Queries are below 2^114 in magnitude.
  */
 typedef struct fa_decode_params {
   int32_t Hq;        /* query heads, a multiple of the cache's Hkv, at most 65535 */
