@@ -290,10 +290,23 @@ def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> Optional[torc
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
-    """As _workspace, from the memory of the call's stream, and with a look at the tensor that is given."""
-    if ws is not None and (ws.device != device or not ws.is_contiguous()):
-        raise ValueError(f"workspace must be contiguous and on {device}")
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the tensor's elements fill its memory without gaps, in whatever order its dimensions are."""
+    if t.is_contiguous():
+        return True
+    expected = 1
+    for stride, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
+        if stride != expected:
+            return False
+        expected *= n
+    return True
+
+
+def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream, any_order: bool = False) -> Optional[torch.Tensor]:
+    """As _workspace, from the memory of the call's stream, and with a look at the tensor that is given: contiguous, or,
+    with any_order, dense with its dimensions in any order (the calls over a cache took such buffers from the start)."""
+    if ws is not None and (ws.device != device or not (_dense(ws) if any_order else ws.is_contiguous())):
+        raise ValueError(f"workspace must be {'dense' if any_order else 'contiguous'} and on {device}")
     if nbytes == 0 or (ws is not None and ws.numel() * ws.element_size() >= nbytes):
         return ws
     return _empty((nbytes,), (1,), torch.uint8, device, stream)
@@ -548,7 +561,7 @@ def _fwd_cache(q4, q, k_q, k_d, v_q, v_d, mask, scale, causal, q_offset, window,
                    **(_q4_expect if q4 else _q8_expect)(p, k_q, k_d, v_q, v_d))
     _need_cuda(q, mview, out, lse, k_q, k_d, v_q, v_d)
     ws_bytes = fwd_workspace_size(p)
-    ws = _scratch(ws_bytes, q.device, workspace, stream)
+    ws = _scratch(ws_bytes, q.device, workspace, stream, any_order=True)
     call = lib.fa_train_fwd_q4 if q4 else lib.fa_train_fwd_q8
     with _on_device(q):
         _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
@@ -574,7 +587,7 @@ def _bwd_cache(q4, q, k_q, k_d, v_q, v_d, o, lse, do, mask, scale, causal, q_off
                    dv_acc=(dv_acc, ks, torch.float32), dk=(dk, ks, q.dtype), dv=(dv, ks, q.dtype))
     _need_cuda(q, o, lse, do, mview, dq, dk_acc, dv_acc, dk, dv, k_q, k_d, v_q, v_d)
     ws_bytes = bwd_workspace_size(p)
-    ws = _scratch(ws_bytes, q.device, workspace, stream)
+    ws = _scratch(ws_bytes, q.device, workspace, stream, any_order=True)
     if dk_acc is not None:
         call = lib.fa_train_bwd_accum_q4 if q4 else lib.fa_train_bwd_accum_q8
         with _on_device(q):
