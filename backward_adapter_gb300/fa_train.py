@@ -282,14 +282,6 @@ def _stream(device: torch.device, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    if nbytes == 0:
-        return ws
-    if ws is not None and ws.numel() * ws.element_size() >= nbytes:
-        return ws
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
-
-
 def _dense(t: torch.Tensor) -> bool:
     """Whether the tensor's elements fill its memory without gaps, in whatever order its dimensions are."""
     if t.is_contiguous():
@@ -303,11 +295,14 @@ def _dense(t: torch.Tensor) -> bool:
 
 
 def _scratch(nbytes: int, device, ws: Optional[torch.Tensor], stream, any_order: bool = False) -> Optional[torch.Tensor]:
-    """As _workspace, from the memory of the call's stream, and with a look at the tensor that is given: contiguous, or,
-    with any_order, dense with its dimensions in any order (the calls over a cache took such buffers from the start)."""
-    if ws is not None and (ws.device != device or not (_dense(ws) if any_order else ws.is_contiguous())):
+    """The call's scratch: the tensor that is given where it is large enough, else memory of the call's stream, which the current
+    one's work may be using otherwise. A given one is contiguous, or, with any_order (the training forms, which look at it
+    only where they write to it), dense with its dimensions in any order."""
+    used = ws is not None and 0 < nbytes <= ws.numel() * ws.element_size()
+    if (used or (ws is not None and not any_order)) and \
+            (ws.device != device or not (_dense(ws) if any_order else ws.is_contiguous())):
         raise ValueError(f"workspace must be {'dense' if any_order else 'contiguous'} and on {device}")
-    if nbytes == 0 or (ws is not None and ws.numel() * ws.element_size() >= nbytes):
+    if nbytes == 0 or used:
         return ws
     return _empty((nbytes,), (1,), torch.uint8, device, stream)
 
@@ -335,10 +330,15 @@ def _empty(shape, strides, dtype, device: torch.device, stream=None) -> torch.Te
     return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty4(shape, dtype, device: torch.device, stream=None) -> torch.Tensor:
+    """A new contiguous 4-D tensor."""
+    b, x, y, z = shape
+    return _empty((b, x, y, z), (x * y * z, y * z, z, 1), dtype, device, stream)
+
+
 def _like(t: torch.Tensor, stream=None) -> torch.Tensor:
     """A new contiguous tensor of the 4-D t's shape, dtype and device."""
-    b, x, y, z = t.shape
-    return _empty((b, x, y, z), (x * y * z, y * z, z, 1), t.dtype, t.device, stream)
+    return _empty4(t.shape, t.dtype, t.device, stream)
 
 
 def _held(n) -> int:
@@ -418,13 +418,13 @@ def fwd(q, k, v, mask=None, *, scale=None, causal=False, q_offset=None, window=0
     p = make_params(q, k, mask, scale=scale, causal=causal, q_offset=q_offset, window=window,
                     deterministic=deterministic, kv_format=_kv_format(q, k, v), layout=layout)
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if lse is None:
-        lse = torch.empty((p.B, p.Hq, p.Sq), dtype=torch.float32, device=q.device)
+        lse = _empty((p.B, p.Hq, p.Sq), (p.Hq * p.Sq, p.Sq, 1), torch.float32, q.device, stream)
     _check_tensors(q, **_common_expect(p, layout, q, k, v, mask, o=out, lse=lse))
     _need_cuda(q, k, v, mview, out, lse)
     ws_bytes = fwd_workspace_size(p)
-    ws = _workspace(ws_bytes, q.device, workspace)
+    ws = _scratch(ws_bytes, q.device, workspace, stream, any_order=True)
     with _on_device(q):
         _check(lib.fa_train_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(mview), _ptr(out), _ptr(lse),
                                 _ptr(ws), ws_bytes, _stream(q.device, stream)))
@@ -438,15 +438,15 @@ def bwd(q, k, v, o, lse, do, mask=None, *, scale=None, causal=False, q_offset=No
     mview, _, _ = _mask_view(mask)
     p = make_params(q, k, mask, scale=scale, causal=causal, q_offset=q_offset, window=window,
                     deterministic=deterministic, kv_format=_kv_format(q, k, v), layout=layout)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k, dtype=q.dtype) if dk is None else dk   # q's dtype for an fp16 cache too
-    dv = torch.empty_like(v, dtype=q.dtype) if dv is None else dv
+    dq = _like(q, stream) if dq is None else dq
+    dk = _empty4(k.shape, q.dtype, q.device, stream) if dk is None else dk   # q's dtype for an fp16 cache too
+    dv = _empty4(k.shape, q.dtype, q.device, stream) if dv is None else dv
     ks = _kv_shape(p, layout)
     _check_tensors(q, **_common_expect(p, layout, q, k, v, mask, o, lse, do, dq), dk=(dk, ks, q.dtype),
                    dv=(dv, ks, q.dtype))
     _need_cuda(q, k, v, o, lse, do, mview, dq, dk, dv)
     ws_bytes = bwd_workspace_size(p)
-    ws = _workspace(ws_bytes, q.device, workspace)
+    ws = _scratch(ws_bytes, q.device, workspace, stream, any_order=True)
     with _on_device(q):
         _check(lib.fa_train_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(mview), _ptr(o), _ptr(lse),
                                 _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws_bytes,
@@ -463,13 +463,13 @@ def bwd_accum(q, k, v, o, lse, do, dk_acc, dv_acc, mask=None, *, scale=None, cau
         raise TypeError("dk_acc and dv_acc must be float32")
     p = make_params(q, k, mask, scale=scale, causal=causal, q_offset=q_offset, window=window,
                     deterministic=deterministic, kv_format=_kv_format(q, k, v), layout=layout)
-    dq = torch.empty_like(q) if dq is None else dq
+    dq = _like(q, stream) if dq is None else dq
     ks = _kv_shape(p, layout)
     _check_tensors(q, **_common_expect(p, layout, q, k, v, mask, o, lse, do, dq),
                    dk_acc=(dk_acc, ks, torch.float32), dv_acc=(dv_acc, ks, torch.float32))
     _need_cuda(q, k, v, o, lse, do, dk_acc, dv_acc, mview, dq)
     ws_bytes = bwd_workspace_size(p)
-    ws = _workspace(ws_bytes, q.device, workspace)
+    ws = _scratch(ws_bytes, q.device, workspace, stream, any_order=True)
     with _on_device(q):
         _check(lib.fa_train_bwd_accum(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(mview), _ptr(o), _ptr(lse),
                                       _ptr(do), _ptr(dq), _ptr(dk_acc), _ptr(dv_acc), _ptr(ws), ws_bytes,
@@ -492,17 +492,17 @@ def bwd_accum_rows(q, k, v, o, lse, do, dk_acc, dv_acc, rows_begin: int, n_rows:
         raise TypeError("dk_acc and dv_acc must be float32")
     p = make_params(q, k, mask, scale=scale, causal=causal, q_offset=q_offset, window=window,
                     deterministic=deterministic, kv_format=_kv_format(q, k, v), layout=layout)
-    dq = torch.empty_like(q) if dq is None else dq
+    dq = _like(q, stream) if dq is None else dq
     shape = _kv_shape(p, layout, rows=int(n_rows))
-    dk_rows = torch.empty(shape, dtype=q.dtype, device=q.device) if dk_rows is None else dk_rows
-    dv_rows = torch.empty(shape, dtype=q.dtype, device=q.device) if dv_rows is None else dv_rows
+    dk_rows = _empty4(shape, q.dtype, q.device, stream) if dk_rows is None else dk_rows
+    dv_rows = _empty4(shape, q.dtype, q.device, stream) if dv_rows is None else dv_rows
     ks = _kv_shape(p, layout)
     _check_tensors(q, **_common_expect(p, layout, q, k, v, mask, o, lse, do, dq),
                    dk_acc=(dk_acc, ks, torch.float32), dv_acc=(dv_acc, ks, torch.float32),
                    dk_rows=(dk_rows, shape, q.dtype), dv_rows=(dv_rows, shape, q.dtype))
     _need_cuda(q, k, v, o, lse, do, dk_acc, dv_acc, mview, dq, dk_rows, dv_rows)
     ws_bytes = bwd_workspace_size(p)
-    ws = _workspace(ws_bytes, q.device, workspace)
+    ws = _scratch(ws_bytes, q.device, workspace, stream, any_order=True)
     with _on_device(q):
         _check(lib.fa_train_bwd_accum_rows(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(mview), _ptr(o), _ptr(lse),
                                            _ptr(do), _ptr(dq), _ptr(dk_acc), _ptr(dv_acc), int(rows_begin), int(n_rows),
@@ -594,9 +594,8 @@ def _bwd_cache(q4, q, k_q, k_d, v_q, v_d, o, lse, do, mask, scale, causal, q_off
             _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
                         _ptr(dk_acc), _ptr(dv_acc), _ptr(ws), ws_bytes, _stream(q.device, stream)))
         return dq
-    strides = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
-    dk = _empty(shape, strides, q.dtype, q.device, stream) if dk is None else dk
-    dv = _empty(shape, strides, q.dtype, q.device, stream) if dv is None else dv
+    dk = _empty4(shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty4(shape, q.dtype, q.device, stream) if dv is None else dv
     call = lib.fa_train_bwd_q4 if q4 else lib.fa_train_bwd_q8
     with _on_device(q):
         _check(call(ctypes.byref(p), _ptr(q), ctypes.byref(kv), _ptr(mview), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
@@ -643,7 +642,7 @@ def set_rows_backward(acc: torch.Tensor, idx: torch.Tensor, out_dtype=torch.bflo
         raise TypeError("idx must be int64 [n_rows]")
     B, H, S, D = acc.shape
     if out is None:
-        out = torch.empty((B, H, idx.shape[0], D), dtype=out_dtype, device=acc.device)
+        out = _empty4((B, H, idx.shape[0], D), out_dtype, acc.device, stream)
     if tuple(out.shape) != (B, H, idx.shape[0], D):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(B, H, idx.shape[0], D)}")
     _need_cuda(acc, idx, out)
@@ -697,9 +696,9 @@ def bwd_noalloc(q, k, v, o, lse, do, mask=None, *, scale=None, causal=False, q_o
     mview, _, _ = _mask_view(mask)
     p = make_params(q, k, mask, scale=scale, causal=causal, q_offset=q_offset, window=window,
                     deterministic=deterministic, kv_format=_kv_format(q, k, v), layout=layout)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k, dtype=q.dtype) if dk is None else dk   # q's dtype for an fp16 cache too
-    dv = torch.empty_like(v, dtype=q.dtype) if dv is None else dv
+    dq = _like(q, stream) if dq is None else dq
+    dk = _empty4(k.shape, q.dtype, q.device, stream) if dk is None else dk   # q's dtype for an fp16 cache too
+    dv = _empty4(k.shape, q.dtype, q.device, stream) if dv is None else dv
     ks = _kv_shape(p, layout)
     _check_tensors(q, **_common_expect(p, layout, q, k, v, mask, o, lse, do, dq), dk=(dk, ks, q.dtype),
                    dv=(dv, ks, q.dtype))
