@@ -275,10 +275,16 @@ def _on_device(t: torch.Tensor):
     return torch.cuda.device(t.device)
 
 
+# The current stream's handle and the current device, by the calls that PyTorch's compiled code makes: building the
+# stream's Python object takes longer than a launch. Where a version lacks them, the public ones do.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+
+
 def _stream(device: torch.device, stream) -> int:
     if stream is None:
-        # the handle alone: building the stream's Python object takes longer than a launch
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _current_stream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -325,7 +331,7 @@ def _empty(shape, strides, dtype, device: torch.device, stream=None) -> torch.Te
             t.record_stream(current)
             return t
     on = device.index   # none for a tensor of the host
-    if on is not None and _empty_strided_cuda is not None and on == torch._C._cuda_getDevice():
+    if on is not None and _empty_strided_cuda is not None and on == _current_device():
         return _empty_strided_cuda(shape, strides, dtype)
     return torch.empty(shape, dtype=dtype, device=device)
 
@@ -361,7 +367,7 @@ def _rows(t: torch.Tensor, layout: str):
 def _launch(device: torch.device, call, *args) -> None:
     """A call of the C ABI on `device`, as _on_device (which costs a few microseconds: skipped where
     the device is current already)."""
-    if device.index == torch._C._cuda_getDevice():
+    if device.index == _current_device():
         status = call(*args)
     else:
         with torch.cuda.device(device):

@@ -90,3 +90,21 @@ def test_memory_of_training_calls_on_a_stream_of_its_own(handle):
         assert [int(x) for x in sums] == [0] * len(sums), n
         assert [int(x) for x in same] == [0] * len(same), n
         del again
+
+
+def test_binding_works_without_torchs_private_calls(monkeypatch):
+    """The current stream and device are found through the public functions where a version lacks the others."""
+    import importlib.util
+    import types
+    for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice", "_dynamo"):
+        monkeypatch.delattr(torch._C, n, raising=False)
+    spec = importlib.util.spec_from_file_location("backward_adapter_gb300._fa_train_again", ft.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: types.SimpleNamespace(cuda_stream=100 + d))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    assert again._stream(torch.device("cuda", 5), None) == 105
+    ran = []
+    again._launch(torch.device("cuda", 3), lambda *a: ran.append(a) or ft.FA_OK, 1, 2)
+    assert ran == [(1, 2)]
+    assert again._empty((2, 3), (3, 1), torch.float32, torch.device("cpu")).shape == (2, 3)
