@@ -637,8 +637,9 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
   }
   if ((st = check_view(dq, p->B, p->S, p->Hq, p->D, es, true, "dq", out[0])) != FA_OK) return st;
   if ((st = check_view(dk, p->B, p->S, p->Hkv, p->D, es, true, "dk", out[1])) != FA_OK) return st;
-  out[2] = {dq_weight, p->norm && p->Hq ? (size_t)p->D * 4 : 0, "dq_weight"};
-  out[3] = {dk_weight, p->norm && p->Hkv ? (size_t)p->D * 4 : 0, "dk_weight"};
+  // of a side without heads: zeros, where it is given
+  out[2] = {dq_weight, p->norm && (p->Hq || dq_weight) ? (size_t)p->D * 4 : 0, "dq_weight"};
+  out[3] = {dk_weight, p->norm && (p->Hkv || dk_weight) ? (size_t)p->D * 4 : 0, "dk_weight"};
   int n = 4;
   if ((st = check_small(p, q_weight, k_weight, inv_freq, positions, in, n)) != FA_OK) return st;
   if ((st = check_buffers(in, n, out, 4, side_by_side(dq, p->Hq, dk, p->Hkv, p->B, p->S, p->D, es))) != FA_OK) return st;
@@ -681,8 +682,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_rope_params* p, const fa_view* dq_out, co
   if (e == cudaSuccess && p->norm) {
     const long long q_rows = (long long)g.x * g.q_chunks, rows = q_rows + (long long)g.x * g.k_chunks;
     auto dw = p->D == 64 ? rope_dw_kernel<64> : rope_dw_kernel<128>;
-    e = launch_after(dw, dim3(p->D / 16, 2), 1024, cs, a.dw, q_rows, rows, p->Hq ? dq_weight : nullptr,
-                     p->Hkv ? dk_weight : nullptr);
+    e = launch_after(dw, dim3(p->D / 16, 2), 1024, cs, a.dw, q_rows, rows, dq_weight, dk_weight);
     count_launches(1);
   }
   return cuda_status(e, "norm and rotation backward launch");

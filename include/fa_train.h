@@ -294,7 +294,8 @@ FA_API fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, cons
  * inputs (rounded once) and, when norm == 1, of the weights (fp32 [D], overwritten): with g = dy
  * rotated back (and times factor), r = 1 / sqrt(mean(x^2) + eps), t = g * w:
  *     dx = r * (t - x * r^2 * mean(t * x));   dw = sum over b, s, h of g * x * r.
- * dw is summed in 32 bits in a fixed order: results are the same from run to run. `ws` is scratch
+ * dw is summed in 32 bits in a fixed order: results are the same from run to run; of a side with no
+ * heads or no tokens it is zeros (NULL is taken for a side with no heads). `ws` is scratch
  * of fa_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned. q and k are not read when
  * norm == 0 (their views may be NULL then, as may ws, dq_weight and dk_weight).
  */
