@@ -153,12 +153,18 @@ fa_status check_view(const fa_view* v, int B, int S, int H, int D, size_t es, bo
 bool side_by_side(const fa_view* a, int Ha, const fa_view* b, int Hb, int B, int S, int D, size_t es) {
   if (a == nullptr || b == nullptr || Ha < 1 || Hb < 1) return false;
   if ((S > 1 && a->stride_s != b->stride_s) || (B > 1 && a->stride_b != b->stride_b)) return false;
-  const int64_t step = S > 1 ? a->stride_s : a->stride_b;   // every token is a multiple of it after the first
-  if ((S == 1 && B == 1) || step < 1 || (S > 1 && B > 1 && a->stride_b % step != 0)) return false;
-  const int64_t bytes = step * (int64_t)es;
-  auto held = [&](const fa_view* v, int H) { return ((H > 1 ? (H - 1) * v->stride_h : 0) + D) * (int64_t)es; };
-  const int64_t from = ((int64_t)((uintptr_t)b->ptr - (uintptr_t)a->ptr) % bytes + bytes) % bytes;
-  return held(a, Ha) <= from && from + held(b, Hb) <= bytes;
+  const int64_t ss = S > 1 ? a->stride_s : 0, sb = B > 1 ? a->stride_b : 0;   // of tokens and sequences, in either order
+  // what each view holds from multiples of `step` on: apart in one step, apart everywhere
+  auto apart = [&](int64_t step, int64_t held_a, int64_t held_b) {
+    if (step < 1 || ss % step != 0 || sb % step != 0) return false;
+    const int64_t e = (int64_t)es, bytes = step * e;
+    const int64_t from = ((int64_t)((uintptr_t)b->ptr - (uintptr_t)a->ptr) % bytes + bytes) % bytes;
+    return held_a * e <= from && from + held_b * e <= bytes;
+  };
+  auto heads = [&](const fa_view* v, int H) { return (H > 1 ? (H - 1) * v->stride_h : 0) + D; };
+  if (apart(ss > 0 && (sb == 0 || ss < sb) ? ss : sb, heads(a, Ha), heads(b, Hb))) return true;   // tokens, all heads of each
+  if (Ha > 1 && Hb > 1 && a->stride_h != b->stride_h) return false;
+  return apart(Ha > 1 ? a->stride_h : Hb > 1 ? b->stride_h : 0, D, D);   // heads, in turn
 }
 
 fa_status check_ws(void* ws, size_t ws_bytes, size_t need, const Span* bufs, int n) {

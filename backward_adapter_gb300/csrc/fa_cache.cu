@@ -329,7 +329,8 @@ fa_status fa_cache_read(const fa_cache* c, int64_t begin, int32_t n_rows, int32_
   }
   if (n_rows == 0) return FA_OK;
   cache_spans(cv, in);
-  if ((st = check_buffers(in, 4, out, 2)) != FA_OK) return st;
+  const size_t es = dtype == FA_BF16 ? 2 : 4;
+  if ((st = check_buffers(in, 4, out, 2, side_by_side(k, cv.Hkv, v, cv.Hkv, cv.B, n_rows, cv.D, es))) != FA_OK) return st;
   return cuda_status(launch_cache_read(cv, begin, n_rows, dtype, row_view(k), row_view(v), (cudaStream_t)stream),
                      "cache read launch");
 }

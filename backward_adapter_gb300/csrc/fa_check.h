@@ -36,7 +36,8 @@ fa_status cuda_status(cudaError_t e, const char* what);
 // spans. `written`: its rows must not overlap. A view without rows spans nothing and may be NULL.
 fa_status check_view(const fa_view* v, int B, int S, int H, int D, size_t es, bool written, const char* name, Span& out);
 // Two views of which no rows overlap, although the bytes they span may: parts of one tensor that lie side by side in each
-// token of it, as those of a fused projection's output do. Both have passed check_view.
+// token of it, as those of a fused projection's output do (tokens of a sequence after one another or of all sequences), or
+// in turn head by head. Both have passed check_view.
 bool side_by_side(const fa_view* a, int Ha, const fa_view* b, int Hb, int B, int S, int D, size_t es);
 inline RowView row_view(const fa_view* v) {
   return v == nullptr ? RowView{nullptr, 0, 0, 0} : RowView{v->ptr, v->stride_b, v->stride_s, v->stride_h};

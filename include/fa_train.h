@@ -283,7 +283,9 @@ typedef struct fa_rope_params {
  * fp32 [rot / 2] (NULL when rot == 0); q_weight, k_weight: [D] in w_dtype, 16-byte aligned (NULL
  * when norm == 0). The views of a side with no heads are not looked at and may be NULL. Outputs
  * overlap neither the inputs nor each other; the two views that are written may lie side by side in
- * each token of one tensor (a fused projection's output or its gradient).
+ * each token of one tensor (a fused projection's output or its gradient), all heads of one after all
+ * heads of the other or in turn head by head, where each of the two strides of tokens and sequences is a
+ * multiple of the smaller one (of the heads' stride, for heads in turn).
  */
 FA_API fa_status fa_qk_norm_rope(const fa_rope_params* p, const fa_view* q, const fa_view* k, const void* q_weight,
                                  const void* k_weight, const float* inv_freq, const int64_t* positions,
@@ -345,7 +347,8 @@ FA_API fa_status fa_cache_write(const fa_cache* c, const fa_view* k, const fa_vi
 
 /*
  * Reads keys begin .. begin + n_rows - 1 of every sequence and head back as values (d * q, rounded
- * once to dtype) into views with S = n_rows, H = Hkv. Needs 0 <= begin, begin + n_rows <= S.
+ * once to dtype) into views with S = n_rows, H = Hkv, which may lie side by side in one tensor as the
+ * outputs of fa_qk_norm_rope may. Needs 0 <= begin, begin + n_rows <= S.
  */
 FA_API fa_status fa_cache_read(const fa_cache* c, int64_t begin, int32_t n_rows, int32_t dtype, const fa_view* k,
                                const fa_view* v, void* stream);
