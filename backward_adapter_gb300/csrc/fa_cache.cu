@@ -188,9 +188,11 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long 
   });
 }
 
-// Blocks that take `per_block` rows each; 0 when the rows are too many for 32-bit numbers.
+constexpr long long kMaxRows = 0x7fffffffLL;   // the kernels count rows in 32 bits
+
+// Blocks that take `per_block` rows each; 0 when the rows are too many.
 unsigned blocks_for(long long rows, int per_block) {
-  return rows > 0x7fffffffLL ? 0u : (unsigned)((rows + per_block - 1) / per_block);
+  return rows > kMaxRows ? 0u : (unsigned)((rows + per_block - 1) / per_block);
 }
 
 }  // namespace
@@ -277,6 +279,7 @@ fa_status check_rows(const CacheView& c, const fa_view* k, const fa_view* v, int
   if (too_large(c.B, c.Hkv, n_rows, c.D)) {
     set_error("K or V would hold more than 2^40 elements"); return FA_ERR_INVALID_ARG;
   }
+  if ((long long)c.B * c.Hkv * n_rows > kMaxRows) { set_error("too many rows for one launch"); return FA_ERR_UNSUPPORTED; }
   const size_t es = dtype == FA_BF16 ? 2 : 4;
   fa_status st = check_view(k, c.B, n_rows, c.Hkv, c.D, es, written, "k", out[0]);
   return st != FA_OK ? st : check_view(v, c.B, n_rows, c.Hkv, c.D, es, written, "v", out[1]);

@@ -340,7 +340,8 @@ typedef struct fa_cache {
  * not a number counts as 0, an infinite one as the largest finite number of its sign. A begin or
  * count from device memory cannot be checked before the launch: a row whose key would lie outside
  * [0, S) is not written, and 0x40000000 | 951 is recorded in the status word (a count outside
- * [0, n_rows] is taken as the nearer end of that range). n_rows == 0 is a no-op.
+ * [0, n_rows] is taken as the nearer end of that range). n_rows == 0 is a no-op. B x Hkv x n_rows is
+ * below 2^31 here and in fa_cache_read (else FA_ERR_UNSUPPORTED).
  */
 FA_API fa_status fa_cache_write(const fa_cache* c, const fa_view* k, const fa_view* v, int32_t dtype, int32_t n_rows,
                                 const int64_t* begin, int64_t begin_all, const int64_t* count, void* stream);
