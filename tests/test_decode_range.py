@@ -116,3 +116,69 @@ def test_blocks_of_different_scales_and_keys_without_values(D, fmt):
         planes[3].zero_()
         if n == 1:
             planes = kv.new_cache(*planes[0].shape[:3], D, fmt)
+
+
+# B, Hq, Hkv, S, Sq, lengths, window, range of log2 of V's scales
+SCALES = {
+    "whole_range": (3, 8, 2, 1500, 1, [1500, 700, 33], 0, (-24, 16)),
+    "whole_range_draft_in_a_window": (2, 8, 2, 900, 3, [900, 2], 100, (-24, 16)),
+    "subnormal": (2, 4, 4, 2100, 1, [2100, 64], 0, (-24, -14)),
+    "large": (1, 16, 1, 600, 2, [600], 0, (0, 16)),
+    "many_heads": (50, 16, 8, 800, 1, None, 0, (-24, 16)),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("name", SCALES)
+def test_scales_anywhere_in_fp16(name, D, fmt):
+    """V's scales of any sign and size, a third of the keys without values, scores some tens of nats apart. Here products far
+    below the largest one occur too: T = max p max_b |d_b| of a query row (a key without values counts with 2^-32) is at least the
+    largest product of each of the row's runs, and what is below 2^-24 of that is off by at most 2^-35 of it, so n keys
+    add n W 2^-35 T / sum p to the module's bound."""
+    B, Hq, Hkv, S, Sq, lens, window, (lo, hi) = SCALES[name]
+    g = torch.Generator(device="cuda").manual_seed(D)
+    r = lambda t: torch.rand(t.shape, generator=g, device="cuda")  # noqa: E731
+    planes = kv.new_cache(B, Hkv, S, D, fmt)
+    W = 8.0 if fmt == "q4_0" else 127.0
+    for i in (0, 2):
+        planes[i].random_(*((0, 256) if fmt == "q4_0" else (-127, 128)), generator=g)
+    planes[1].copy_((2 * r(planes[1]) - 1) * 2 / W)
+    planes[3].copy_(torch.exp2(lo + (hi - lo) * r(planes[3])).clamp(max=65504) * torch.where(r(planes[3]) < 0.5, -1.0, 1.0))
+    planes[3].masked_fill_(r(planes[3][..., :1]) < 1 / 3, 0)
+    q = torch.randn((B, Hq, Sq, D), generator=g, device="cuda").to(torch.bfloat16)
+    n = torch.full((B,), S, device="cuda") if lens is None else torch.tensor(lens, device="cuda")
+    o, lse = kv.decode(q, *planes, n, window=window)
+    torch.cuda.synchronize()
+    scale, G = 1 / math.sqrt(D), Hq // Hkv
+
+    def values(x, d):
+        if x.dtype == torch.uint8:
+            b = x.unflatten(-1, (-1, 16))
+            x = torch.cat([b & 15, b >> 4], -1).double() - 8
+        else:
+            x = x.unflatten(-1, (-1, 32)).double()
+        return (x * d.double()[..., None]).flatten(-2)
+    k, v = (values(planes[i], planes[i + 1]).repeat_interleave(G, 1) for i in (0, 2))
+    at, j = n[:, None] - Sq + torch.arange(Sq, device="cuda"), torch.arange(S, device="cuda")
+    seen = j <= at[..., None]
+    if window > 0:
+        seen &= at[..., None] - j <= window
+    seen = seen[:, None]
+    s = (scale * q.double() @ k.transpose(-1, -2)).masked_fill(~seen, -math.inf)
+    top = s.amax(-1, keepdim=True).clamp(min=-1e300)
+    p = torch.exp(s - top)
+    total = p.sum(-1, keepdim=True)
+    one = torch.where(total > 0, total, torch.ones_like(total))
+    want, size = p @ v / one, p @ v.abs() / one
+    d = planes[3].double().abs().amax(-1).repeat_interleave(G, 1)[:, :, None]
+    T = (p * torch.where(d == 0, 2.0 ** -32, d)).amax(-1, keepdim=True) / one
+    Q = q.double().abs().unflatten(-1, (-1, 32)).sum(-1)
+    E = 2.0 ** -19 * scale * W * (Q @ planes[1].double().abs().repeat_interleave(G, 1).transpose(-1, -2))
+    E = E.masked_fill(~seen, 0).amax(-1, keepdim=True)
+    bound = (2.0 ** -10 + 2 * E) * size + seen.sum(-1, keepdim=True) * W * 2.0 ** -35 * T + 2.0 ** -8 * want.abs()
+    err = (o.double() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+    want_lse = torch.where(total > 0, top + torch.log(one), torch.zeros_like(one))[..., 0]
+    assert bool(((lse.double() - want_lse).abs() <= E[..., 0] + 2.0 ** -18 + 2.0 ** -20 * (1 + want_lse.abs())).all())
