@@ -4,7 +4,7 @@
 // a few rows are written, and writing many by its instructions. 67584 keys of 4 heads of 128 in 4 bits are read back to bf16 in
 // 27 us, 6.5 TB/s, 96% of the measured copy rate, and written from it in 47 us, 3.8 TB/s (103 with a division for each
 // feature; two lanes a block and one reciprocal leave less than half of the instructions); a token of 32 sequences with 8 heads is
-// written in 2 us.
+// written in 2 us. Counters of the write of a whole window: issue 71% busy, ALU pipe 56%, DRAM 42%.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -1,6 +1,5 @@
 // The blocks of a quantized K/V cache (q8_0, q4_0): storing 32 features as an fp16 scale and 8- or
-// 4-bit numbers, and their values. Four consecutive lanes hold a block when it is written, 8
-// features each.
+// 4-bit numbers. Two neighbouring lanes hold a block when it is written, 16 features each.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -38,6 +38,8 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str = "non
     elif scaling == "yarn":
         def pair(turns):   # the pair that turns so often over original_length
             return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        # The method's ramp is over pairs' indices. The upper bound, rotary_dim - 1 although pairs end at rotary_dim / 2 - 1, and
+        # the least width, 1e-3, are those that models with these frequencies were trained with: kept, so that angles agree.
         low = max(math.floor(pair(beta_fast)), 0)
         high = min(math.ceil(pair(beta_slow)), rotary_dim - 1)
         ramp = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)

@@ -223,7 +223,8 @@ typedef struct fa_kv_q4 {
  * The op with K and V read from a q4_0 cache: as the _q8 entry points, with p->kv_format ==
  * FA_KV_Q4_0 and p->dtype == FA_BF16 (else FA_ERR_UNSUPPORTED). The values are rounded to bf16 (to
  * nearest even) and the op computes on that bf16 K/V; dK and dV are the gradients with respect to
- * it. Forward and backward both expand the cache once into a bf16 copy in their workspace
+ * it. As on every bf16 path, P and dS are rounded to bf16 for the products that take them. Forward
+ * and backward both expand the cache once into a bf16 copy in their workspace
  * (2 x B x Hkv x Sk x D x 2 bytes, included in the workspace-size queries).
  */
 FA_API fa_status fa_train_fwd_q4(const fa_params* p, const void* q, const fa_kv_q4* kv, const void* mask,
@@ -257,8 +258,9 @@ typedef struct fa_view {
  *     (y[a], y[b]) = factor * (n[a] cos t - n[b] sin t, n[b] cos t + n[a] sin t),  t = p * inv_freq[i]
  * for the pairs i < rot / 2 of the first `rot` features: (a, b) = (i, i + rot / 2), or
  * (2 i, 2 i + 1) when interleaved; the features at rot and above are n. Statistics and products are
- * 32-bit, the angle's reduction is exact for |p| < 2^31, and y is rounded once. inv_freq carries any
- * scaling for long contexts; `factor` is the one that goes with it (1 without).
+ * 32-bit, an angle is off by at most |p| (1 + |inv_freq| / 4) 2^-64 + 2^-32 turns before sine and
+ * cosine (2^-31 turns for |p| < 2^31 and frequencies up to 1), and y is rounded once. inv_freq
+ * carries any scaling for long contexts; `factor` is the one that goes with it (1 without).
  */
 typedef struct fa_rope_params {
   int32_t B;           /* 1 .. 65535 */
