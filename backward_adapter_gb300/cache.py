@@ -60,6 +60,8 @@ def _cache(k_q, k_d, v_q, v_d):
         fmt = ft.FA_KV_Q8_0
     else:
         raise TypeError(f"k_q has dtype {kind}: int8 (q8_0) or uint8 (q4_0)")
+    if max(shape) > 0x7fffffff:   # the C ABI's numbers are 32-bit ones, and ctypes would wrap it
+        raise ValueError(f"k_q has shape {tuple(shape)}: every dimension below 2^31")
     if v_q.dtype != kind:
         raise TypeError(f"v_q has dtype {v_q.dtype}, expected {kind}")
     if k_d.dtype != torch.float16 or v_d.dtype != torch.float16:
@@ -121,8 +123,8 @@ def cache_write(k, v, k_q, k_d, v_q, v_d, begin, count=None, *, layout: str = "b
     counts = None if count is None else _per_sequence("count", count, c[0], device)
     call = _RowsCall(*c, *ft._rows(k, layout), *ft._rows(v, layout))
     at = ctypes.addressof(call)
-    ft._launch(device, ft.load_library().fa_cache_write, at, at + _CACHE, at + _CACHE + _VIEW, ft._dtype_code(k), n,
-               begins, first, counts, ft._stream(device, stream))
+    ft._launch(device, ft.load_library().fa_cache_write, at, at + _CACHE, at + _CACHE + _VIEW, ft._dtype_code(k),
+               min(n, 0x7fffffff), begins, first, counts, ft._stream(device, stream))
 
 
 def cache_read(k_q, k_d, v_q, v_d, begin: int = 0, n_rows=None, *, dtype=torch.bfloat16, layout: str = "bhsd", k=None,
