@@ -121,6 +121,13 @@ fa_status check_buffers(const Span* in, int nin, const Span* out, int nout, bool
   return FA_OK;
 }
 
+fa_status check_apart(const Span* in, int nin, const Span* out, int nout) {
+  for (int o = 0; o < nout; ++o)
+    for (int i = 0; i < nin; ++i)
+      if (overlaps(out[o], in[i])) { set_error("output %s overlaps input %s", out[o].name, in[i].name); return FA_ERR_INVALID_ARG; }
+  return FA_OK;
+}
+
 // Bytes from the first to the last element of the view's rows, the dimensions ordered by stride.
 fa_status check_view(const fa_view* v, int B, int S, int H, int D, size_t es, bool written, const char* name, Span& out) {
   out = Span{nullptr, 0, name};

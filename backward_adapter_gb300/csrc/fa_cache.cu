@@ -12,6 +12,7 @@
 
 #include "fa_check.h"
 #include "fa_device.cuh"
+#include "kv_pages.cuh"
 #include "kv_quant.cuh"
 
 namespace fa {
@@ -39,10 +40,12 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
 
 // A thread quantizes 16 features of a row, two lanes a block of 32. blockIdx.y: 0 for K, 1 for V. Two rows a thread measured
 // slower (58.4 us where this takes 47.0, see the head of the file), and lanes of 8 features, with twice the work for a block, 76.4.
-template <typename T, int D, bool Q4>
-__global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k, RowView v, unsigned rows, unsigned n_rows,
-                                                          const int64_t* __restrict__ begin, long long begin_all,
-                                                          const int64_t* __restrict__ count, unsigned* status) {
+// PAGED: the rows' places are found through the page table, each row's for itself.
+template <typename T, int D, bool Q4, bool PAGED>
+__global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, PageView pages, RowView k, RowView v, unsigned rows,
+                                                          unsigned n_rows, const int64_t* __restrict__ begin,
+                                                          long long begin_all, const int64_t* __restrict__ count,
+                                                          unsigned* status) {
   constexpr int LANES = D / 16;
   const unsigned g = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int l = threadIdx.x % LANES;
@@ -58,8 +61,15 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheView c, RowView k
     if (count == nullptr || (long long)r < __ldg(count + b)) {
       if (first < c.S && first + r >= 0 && first + r < c.S) {
         on = true;
-        row = (size_t)bh * c.S + (size_t)(first + r);
-        load16(static_cast<const T*>(src.ptr) + b * src.sb + r * src.ss + h * src.sh + 16 * l, x);
+        if constexpr (PAGED) {
+          const unsigned key = (unsigned)(first + r);
+          const long long at = page_row(pages, c.Hkv, (int)b, (int)h, key & ~15u, l == 0 ? status : nullptr);
+          on = at >= 0;
+          row = (size_t)at + (key & 15u);
+        } else {
+          row = (size_t)bh * c.S + (size_t)(first + r);
+        }
+        if (on) load16(static_cast<const T*>(src.ptr) + b * src.sb + r * src.ss + h * src.sh + 16 * l, x);
       } else if (l == 0 && status != nullptr) {
         atomicCAS(status, 0u, 0x40000000u | kSiteCacheRow);
       }
@@ -139,9 +149,12 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint64_t (&x)[4]
 
 // A thread reads N bytes of numbers of ROWS rows, all of them on their way at once, and writes N features of 16 bytes, which
 // with its neighbours' fill whole sectors (q4_0: two times N, of the low and of the high nibbles). blockIdx.y: 0 for K, 1 for V.
-template <typename T, int D, bool Q4, int ROWS>
-__global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long begin, unsigned rows, unsigned n_rows,
-                                                         RowView k, RowView v) {
+// PLACED: rows are found through a page table, or from a begin of each sequence's own, or both; one that the cache does not
+// have is read as zeros.
+template <typename T, int D, bool Q4, int ROWS, bool PLACED>
+__global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, PageView pages, const int64_t* __restrict__ begins,
+                                                         long long begin, unsigned rows, unsigned n_rows, RowView k,
+                                                         RowView v, unsigned* status) {
   constexpr int N = 16 / sizeof(T), PARTS = (Q4 ? D / 2 : D) / N, STEP = 256 / PARTS;   // rows a block takes at a time
   const int part = threadIdx.x % PARTS;
   const unsigned first = blockIdx.x * (STEP * ROWS) + threadIdx.x / PARTS;
@@ -152,7 +165,24 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheView c, long long 
   uint32_t w[ROWS][N / 4];
   uint16_t scale[ROWS];
   each_row<ROWS>(first, STEP, rows, n_rows, [&](int i, unsigned bh, unsigned r, bool) {
-    const size_t row = (size_t)bh * c.S + (size_t)(begin + r);
+    size_t row = (size_t)bh * c.S + (size_t)(begin + r);
+    if constexpr (PLACED) {
+      const unsigned b = bh / c.Hkv, h = bh % c.Hkv;
+      const long long from = begins != nullptr ? __ldg(begins + b) : begin;
+      const bool inside = from < c.S && from + r >= 0 && from + r < c.S;
+      if (!inside && part == 0 && status != nullptr) atomicCAS(status, 0u, 0x40000000u | kSiteCacheRow);
+      const unsigned key = inside ? (unsigned)(from + r) : 0u;
+      long long at = inside ? (long long)bh * c.S + key : -1;
+      if (inside && pages.table != nullptr) {
+        at = page_row(pages, c.Hkv, (int)b, (int)h, key & ~15u, part == 0 ? status : nullptr);
+        if (at >= 0) at += key & 15u;
+      }
+      scale[i] = 0;
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) w[i][j] = Q4 ? 0x88888888u : 0u;
+      if (at < 0) return;
+      row = (size_t)at;
+    }
     scale[i] = __ldg(scales + row * (D / 32));
     const uint8_t* at = values + row * (Q4 ? D / 2 : D);
     if constexpr (N == 8) {
@@ -197,20 +227,21 @@ unsigned blocks_for(long long rows, int per_block) {
 
 }  // namespace
 
-cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowView& v, int dtype, int n_rows,
-                               const int64_t* begin, long long begin_all, const int64_t* count, unsigned* status,
-                               cudaStream_t st) {
+cudaError_t launch_cache_write(const CacheView& c, const PageView& pages, const RowView& k, const RowView& v, int dtype,
+                               int n_rows, const int64_t* begin, long long begin_all, const int64_t* count,
+                               unsigned* status, cudaStream_t st) {
   const long long rows = (long long)c.B * c.Hkv * n_rows;
   const unsigned n = blocks_for(rows, 256 / (c.D / 16));
   if (n == 0) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
-    kernel<<<dim3(n, 2), 256, 0, st>>>(c, k, v, (unsigned)rows, (unsigned)n_rows, begin, begin_all, count, status);
+    kernel<<<dim3(n, 2), 256, 0, st>>>(c, pages, k, v, (unsigned)rows, (unsigned)n_rows, begin, begin_all, count, status);
   };
+  const bool paged = pages.table != nullptr;
   auto by_format = [&](auto t, auto dim) {
     using T = decltype(t);
     constexpr int D = decltype(dim)::value;
-    if (c.q4) go(cache_write_kernel<T, D, true>);
-    else go(cache_write_kernel<T, D, false>);
+    if (c.q4) paged ? go(cache_write_kernel<T, D, true, true>) : go(cache_write_kernel<T, D, true, false>);
+    else paged ? go(cache_write_kernel<T, D, false, true>) : go(cache_write_kernel<T, D, false, false>);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
@@ -220,20 +251,25 @@ cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowVi
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, int dtype, const RowView& k,
-                              const RowView& v, cudaStream_t st) {
+namespace {
+
+template <bool PLACED>
+cudaError_t read_rows(const CacheView& c, const PageView& pages, const int64_t* begins, long long begin, int n_rows, int dtype,
+                      const RowView& k, const RowView& v, unsigned* status, cudaStream_t st) {
   const long long rows = (long long)c.B * c.Hkv * n_rows;
   const int parts = (c.q4 ? c.D / 2 : c.D) / (dtype == DT_BF16 ? 8 : 4), step = 256 / parts;
   // four rows a thread, where that still leaves blocks for every SM (67584 keys of 4 heads in 4 bits: 27.2 us; one 31.6, eight 27.4)
   const bool many = rows >= 8LL * step * sm_count();
   const unsigned n = blocks_for(rows, many ? 4 * step : step);
   if (n == 0) return cudaErrorInvalidConfiguration;
-  auto go = [&](auto kernel) { kernel<<<dim3(n, 2), 256, 0, st>>>(c, begin, (unsigned)rows, (unsigned)n_rows, k, v); };
+  auto go = [&](auto kernel) {
+    kernel<<<dim3(n, 2), 256, 0, st>>>(c, pages, begins, begin, (unsigned)rows, (unsigned)n_rows, k, v, status);
+  };
   auto by_format = [&](auto t, auto dim) {
     using T = decltype(t);
     constexpr int D = decltype(dim)::value;
-    if (c.q4) many ? go(cache_read_kernel<T, D, true, 4>) : go(cache_read_kernel<T, D, true, 1>);
-    else many ? go(cache_read_kernel<T, D, false, 4>) : go(cache_read_kernel<T, D, false, 1>);
+    if (c.q4) many ? go(cache_read_kernel<T, D, true, 4, PLACED>) : go(cache_read_kernel<T, D, true, 1, PLACED>);
+    else many ? go(cache_read_kernel<T, D, false, 4, PLACED>) : go(cache_read_kernel<T, D, false, 1, PLACED>);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
@@ -243,9 +279,18 @@ cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, i
   return cudaGetLastError();
 }
 
-fa_status check_cache(const fa_cache* c, CacheView& out) {
+}  // namespace
+
+cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, int dtype, const RowView& k,
+                              const RowView& v, cudaStream_t st) {
+  return read_rows<false>(c, PageView{}, nullptr, begin, n_rows, dtype, k, v, nullptr, st);
+}
+
+namespace {
+
+fa_status check_planes(const fa_cache* c, bool pool, CacheView& out) {
   if (c == nullptr) { set_error("cache is NULL"); return FA_ERR_INVALID_ARG; }
-  if (c->B < 1 || c->B > 65535 || c->Hkv < 1 || c->Hkv > 65535) {
+  if (c->B < 1 || (c->B > 65535 && !pool) || c->Hkv < 1 || c->Hkv > 65535) {
     set_error("cache B=%d, Hkv=%d: each in [1, 65535]", c->B, c->Hkv); return FA_ERR_INVALID_ARG;
   }
   if (c->S < 1 || c->S > kMaxSeq) { set_error("cache S=%d outside [1, %d]", c->S, kMaxSeq); return FA_ERR_INVALID_ARG; }
@@ -259,6 +304,42 @@ fa_status check_cache(const fa_cache* c, CacheView& out) {
     set_error("a cache of these shapes would hold more than 2^40 elements"); return FA_ERR_INVALID_ARG;
   }
   out = CacheView{c->B, c->Hkv, c->S, c->D, c->kv_format == FA_KV_Q4_0, c->k_q, c->k_d, c->v_q, c->v_d};
+  return FA_OK;
+}
+
+}  // namespace
+
+fa_status check_cache(const fa_cache* c, CacheView& out) { return check_planes(c, false, out); }
+
+fa_status check_paged(const fa_cache* c, const fa_pages* pages, CacheView& held, CacheView& seen, PageView& view, Span& table) {
+  const fa_status st = check_planes(c, pages != nullptr, held);
+  if (st != FA_OK) return st;
+  seen = held;
+  view = PageView{};
+  table = Span{nullptr, 0, "table"};
+  if (pages == nullptr) return FA_OK;
+  if (pages->B < 1 || pages->B > 65535) { set_error("pages B=%d outside [1, 65535]", pages->B); return FA_ERR_INVALID_ARG; }
+  if (held.S % 16 != 0) { set_error("pages of %d keys: a multiple of 16", held.S); return FA_ERR_INVALID_ARG; }
+  if (pages->M < 1 || (long long)pages->M * held.S > kMaxSeq) {
+    set_error("%d pages of %d keys a sequence: 1 to %d keys", pages->M, held.S, kMaxSeq); return FA_ERR_INVALID_ARG;
+  }
+  if (pages->table == nullptr || (uintptr_t)pages->table % 4 != 0) {
+    set_error("table is NULL or not 4-byte aligned"); return FA_ERR_INVALID_ARG;
+  }
+  if (pages->B > 1 && (pages->stride < pages->M || (double)pages->stride * pages->B > kMaxElems)) {
+    set_error("table stride of %lld: at least its %d pages, and at most 2^40 elements in all", (long long)pages->stride, pages->M);
+    return FA_ERR_INVALID_ARG;
+  }
+  seen.B = pages->B;
+  seen.S = pages->M * held.S;
+  if (too_large(seen.B, seen.Hkv, seen.S, seen.D)) {
+    set_error("the sequences' keys would be more than 2^40 elements"); return FA_ERR_INVALID_ARG;
+  }
+  const unsigned long long units = (unsigned)held.S / 16;
+  view = PageView{pages->table, pages->B > 1 ? (long long)pages->stride : 0, ((1ull << 40) + units - 1) / units, (unsigned)held.S,
+                  (unsigned)held.B};
+  table.p = pages->table;
+  table.n = ((size_t)view.stride * (pages->B - 1) + pages->M) * 4;
   return FA_OK;
 }
 
@@ -292,13 +373,14 @@ using namespace fa;
 
 extern "C" {
 
-fa_status fa_cache_write(const fa_cache* c, const fa_view* k, const fa_view* v, int32_t dtype, int32_t n_rows,
-                         const int64_t* begin, int64_t begin_all, const int64_t* count, void* stream) {
+fa_status fa_cache_write_pages(const fa_cache* c, const fa_pages* pages, const fa_view* k, const fa_view* v, int32_t dtype,
+                               int32_t n_rows, const int64_t* begin, int64_t begin_all, const int64_t* count, void* stream) {
   clear_error();
-  CacheView cv;
-  fa_status st = check_cache(c, cv);
+  CacheView held, cv;
+  PageView pv;
+  Span in[5], out[4];
+  fa_status st = check_paged(c, pages, held, cv, pv, in[4]);
   if (st != FA_OK) return st;
-  Span in[4], out[4];
   if ((st = check_rows(cv, k, v, dtype, n_rows, false, in)) != FA_OK) return st;
   if (begin == nullptr && (begin_all < 0 || begin_all > cv.S - n_rows)) {
     set_error("rows [%lld, +%d) outside the %d keys", (long long)begin_all, n_rows, cv.S); return FA_ERR_INVALID_ARG;
@@ -307,35 +389,51 @@ fa_status fa_cache_write(const fa_cache* c, const fa_view* k, const fa_view* v, 
     set_error("begin and count must be 8-byte aligned"); return FA_ERR_INVALID_ARG;
   }
   if (n_rows == 0) return FA_OK;
-  cache_spans(cv, out);
+  cache_spans(held, out);
   if ((st = check_buffers(in, 2, out, 4)) != FA_OK) return st;
-  in[2] = {begin, (size_t)cv.B * 8, "begin"};
-  in[3] = {count, (size_t)cv.B * 8, "count"};
-  for (int o = 0; o < 4; ++o)
-    for (int i = 2; i < 4; ++i)
-      if (overlaps(out[o], in[i])) { set_error("output %s overlaps input %s", out[o].name, in[i].name); return FA_ERR_INVALID_ARG; }
-  return cuda_status(launch_cache_write(cv, row_view(k), row_view(v), dtype, n_rows, begin, begin_all, count,
+  in[2] = {begin, begin != nullptr ? (size_t)cv.B * 8 : 0, "begin"};
+  in[3] = {count, count != nullptr ? (size_t)cv.B * 8 : 0, "count"};
+  if ((st = check_apart(in + 2, 3, out, 4)) != FA_OK) return st;
+  return cuda_status(launch_cache_write(cv, pv, row_view(k), row_view(v), dtype, n_rows, begin, begin_all, count,
                                         device_status_ptr(), (cudaStream_t)stream),
                      "cache write launch");
 }
 
-fa_status fa_cache_read(const fa_cache* c, int64_t begin, int32_t n_rows, int32_t dtype, const fa_view* k,
-                        const fa_view* v, void* stream) {
+fa_status fa_cache_write(const fa_cache* c, const fa_view* k, const fa_view* v, int32_t dtype, int32_t n_rows,
+                         const int64_t* begin, int64_t begin_all, const int64_t* count, void* stream) {
+  return fa_cache_write_pages(c, nullptr, k, v, dtype, n_rows, begin, begin_all, count, stream);
+}
+
+fa_status fa_cache_read_pages(const fa_cache* c, const fa_pages* pages, const int64_t* begins, int64_t begin, int32_t n_rows,
+                              int32_t dtype, const fa_view* k, const fa_view* v, void* stream) {
   clear_error();
-  CacheView cv;
-  fa_status st = check_cache(c, cv);
+  CacheView held, cv;
+  PageView pv;
+  Span in[6], out[2];
+  fa_status st = check_paged(c, pages, held, cv, pv, in[4]);
   if (st != FA_OK) return st;
-  Span in[4], out[2];
   if ((st = check_rows(cv, k, v, dtype, n_rows, true, out)) != FA_OK) return st;
-  if (begin < 0 || begin > cv.S - n_rows) {
+  if (begins == nullptr && (begin < 0 || begin > cv.S - n_rows)) {
     set_error("rows [%lld, +%d) outside the %d keys", (long long)begin, n_rows, cv.S); return FA_ERR_INVALID_ARG;
   }
+  if ((uintptr_t)begins % 8 != 0) { set_error("begin must be 8-byte aligned"); return FA_ERR_INVALID_ARG; }
   if (n_rows == 0) return FA_OK;
-  cache_spans(cv, in);
+  cache_spans(held, in);
   const size_t es = dtype == FA_BF16 ? 2 : 4;
   if ((st = check_buffers(in, 4, out, 2, side_by_side(k, cv.Hkv, v, cv.Hkv, cv.B, n_rows, cv.D, es))) != FA_OK) return st;
-  return cuda_status(launch_cache_read(cv, begin, n_rows, dtype, row_view(k), row_view(v), (cudaStream_t)stream),
-                     "cache read launch");
+  in[5] = {begins, begins != nullptr ? (size_t)cv.B * 8 : 0, "begin"};
+  if ((st = check_apart(in + 4, 2, out, 2)) != FA_OK) return st;
+  const RowView kr = row_view(k), vr = row_view(v);
+  const cudaStream_t cs = (cudaStream_t)stream;
+  const cudaError_t e = pages == nullptr && begins == nullptr
+                            ? launch_cache_read(cv, begin, n_rows, dtype, kr, vr, cs)
+                            : read_rows<true>(cv, pv, begins, begin, n_rows, dtype, kr, vr, device_status_ptr(), cs);
+  return cuda_status(e, "cache read launch");
+}
+
+fa_status fa_cache_read(const fa_cache* c, int64_t begin, int32_t n_rows, int32_t dtype, const fa_view* k,
+                        const fa_view* v, void* stream) {
+  return fa_cache_read_pages(c, nullptr, nullptr, begin, n_rows, dtype, k, v, stream);
 }
 
 }  // extern "C"

@@ -28,6 +28,8 @@ bool overlaps(const Span& a, const Span& b);
 // Every buffer is there and 16-byte aligned; no output overlaps an input or another output (of the first two outputs the
 // caller may know it: `apart`).
 fa_status check_buffers(const Span* in, int nin, const Span* out, int nout, bool apart = false);
+// No output overlaps one of the inputs, which may be of any alignment and, where they have no bytes, not there.
+fa_status check_apart(const Span* in, int nin, const Span* out, int nout);
 // The workspace is large enough, 256-byte aligned and overlaps none of the call's buffers.
 fa_status check_ws(void* ws, size_t ws_bytes, size_t need, const Span* bufs, int n);
 fa_status cuda_status(cudaError_t e, const char* what);
@@ -46,5 +48,11 @@ inline RowView row_view(const fa_view* v) {
 // Checks an fa_cache and fills `out`; the byte ranges of its four planes.
 fa_status check_cache(const fa_cache* c, CacheView& out);
 void cache_spans(const CacheView& c, Span out[4]);
+// Checks a cache with its page table, or one without (pages == NULL): `held`: the planes as they are (their B pages of S
+// keys), `seen`: the sequences and the keys that they have room for; the byte range of the table.
+fa_status check_paged(const fa_cache* c, const fa_pages* pages, CacheView& held, CacheView& seen, PageView& view, Span& table);
+
+// Checks the numbers of an fa_prefill_params for a cache's sequences.
+fa_status check_chunk(const fa_prefill_params* p, const CacheView& seen);
 
 }  // namespace fa

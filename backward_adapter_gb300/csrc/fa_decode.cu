@@ -52,6 +52,7 @@
 
 #include "fa_check.h"
 #include "fa_device.cuh"
+#include "kv_pages.cuh"
 #include "kv_q8.cuh"
 #include "tc_ptx.cuh"
 
@@ -69,6 +70,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct DecodeArgs {
   CacheView c;
+  PageView pages;
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
@@ -401,7 +403,7 @@ __device__ __forceinline__ void store_row(const DecodeArgs& a, int b, int h, int
 
 // A block's work: SLICES: slice blockIdx.x of the list; else the head blockIdx.x. NT * 8 query rows from
 // blockIdx.y * NT * 8 on.
-template <int D, bool Q4, int NT, bool SLICES, int kWarps>
+template <int D, bool Q4, int NT, bool SLICES, int kWarps, bool PAGED>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D, NT) : 1) decode_kernel(DecodeArgs a) {
   using S = Slot<D, Q4>;
   constexpr int NB = S::NB, ROWS = NT * 8;
@@ -433,13 +435,56 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == warps_of(D) ? held_of(D
     // lane's part of a tile's loads: pieces lane, lane + 32, ... of the numbers, key `lane`'s scales
     const unsigned lrow = (unsigned)lane / S::PIECES;
     const int lpiece = lane % S::PIECES;
-    const size_t begin = ((size_t)b * a.c.Hkv + h) * a.c.S + k0;
+    const size_t begin = PAGED ? 0 : ((size_t)b * a.c.Hkv + h) * a.c.S + k0;
     const uint8_t* kq = static_cast<const uint8_t*>(a.c.k_q) + begin * S::ROW + 16 * lane;
     const uint8_t* vq = static_cast<const uint8_t*>(a.c.v_q) + begin * S::ROW + 16 * lane;
-    const uint16_t* kd = a.c.k_d + (begin + lane) * NB;
-    const uint16_t* vd = a.c.v_d + (begin + lane) * NB;
+    const uint16_t* kd = a.c.k_d + (begin + (PAGED ? 0 : lane)) * NB;
+    const uint16_t* vd = a.c.v_d + (begin + (PAGED ? 0 : lane)) * NB;
     int loaded = k0;   // the first key of the next tile to load
+    // Pages: a tile is two runs of 16 keys, each in one page. Lane i looks up the run i of the next 16 tiles, once for all.
+    long long runs = -1;
+    auto look_up = [&] {
+      const int key = loaded + 16 * lane, past = k0 + tiles * kTile;
+      runs = key < min(kr.len, past) ? page_row(a.pages, a.c.Hkv, b, h, key, a.status) : -1;
+    };
+    if constexpr (PAGED) look_up();
     auto load = [&](uint32_t at) {
+      if constexpr (PAGED) {
+        const int first = (loaded - k0) / 16 & 31;
+        if (first == 0 && loaded != k0) look_up();
+        const long long row0 = __shfl_sync(0xffffffffu, runs, first), row1 = __shfl_sync(0xffffffffu, runs, first + 1);
+        const bool whole = loaded + kTile <= kr.len && row0 >= 0 && row1 >= 0;
+        // of the second run as if the first had been before it
+        const long long off0 = row0 * S::ROW, off1 = (row1 - 16) * S::ROW;
+        const long long mine = lane < 16 ? row0 + lane : row1 + lane - 16;
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < S::PIECES; ++i) {
+            const unsigned row = lrow + i * (32 / S::PIECES);
+            const uint32_t dst = at + row * S::ROW + 16 * (lpiece ^ S::permuted(row));
+            const long long src = (2 * i < S::PIECES ? off0 : off1) + 512 * i;
+            cp_async16(dst, kq + src);
+            cp_async16(dst + S::V_OFF, vq + src);
+          }
+          cp_async_small<S::SC>(at + S::KD_OFF + lane * S::SC, kd + mine * NB);
+          cp_async_small<S::SC>(at + S::VD_OFF + lane * S::SC, vd + mine * NB);
+        } else {   // keys past the end, and of pages that are none, are zeros, and not read
+#pragma unroll
+          for (int i = 0; i < S::PIECES; ++i) {
+            const unsigned row = lrow + i * (32 / S::PIECES);
+            const uint32_t dst = at + row * S::ROW + 16 * (lpiece ^ S::permuted(row));
+            const bool on = loaded + (int)row < kr.len && (2 * i < S::PIECES ? row0 : row1) >= 0;
+            const long long src = on ? (2 * i < S::PIECES ? off0 : off1) + 512 * i : -16 * lane;
+            cp_async16_if(dst, kq + src, on);
+            cp_async16_if(dst + S::V_OFF, vq + src, on);
+          }
+          const bool on = loaded + lane < kr.len && (lane < 16 ? row0 : row1) >= 0;
+          cp_async_small_if<S::SC>(at + S::KD_OFF + lane * S::SC, on ? kd + mine * NB : kd, on);
+          cp_async_small_if<S::SC>(at + S::VD_OFF + lane * S::SC, on ? vd + mine * NB : vd, on);
+        }
+        loaded += kTile;
+        return;
+      }
       if (loaded + kTile <= kr.len) {
 #pragma unroll
         for (int i = 0; i < S::PIECES; ++i) {
@@ -1006,10 +1051,12 @@ DecodePlan plan_decode(const fa_decode_params* p, const CacheView& c) {
   return d;
 }
 
-fa_status check_decode(const fa_decode_params* p, const fa_cache* c, CacheView& cv) {
+// `held`: the planes as they are; `cv`: the sequences and the keys they have room for.
+fa_status check_decode(const fa_decode_params* p, const fa_cache* c, const fa_pages* pages, CacheView& held, CacheView& cv,
+                       PageView& pv, Span& table) {
   clear_error();
   if (p == nullptr) { set_error("params is NULL"); return FA_ERR_INVALID_ARG; }
-  const fa_status st = check_cache(c, cv);
+  const fa_status st = check_paged(c, pages, held, cv, pv, table);
   if (st != FA_OK) return st;
   if (p->Hq < 1 || p->Hq > 65535) { set_error("Hq=%d outside [1, 65535]", p->Hq); return FA_ERR_INVALID_ARG; }
   if (p->Hq % cv.Hkv != 0) { set_error("Hq=%d is not a multiple of Hkv=%d", p->Hq, cv.Hkv); return FA_ERR_INVALID_ARG; }
@@ -1021,12 +1068,12 @@ fa_status check_decode(const fa_decode_params* p, const fa_cache* c, CacheView& 
   return FA_OK;
 }
 
-template <int D, bool Q4, int NT, bool SLICES, int WARPS>
+template <int D, bool Q4, int NT, bool SLICES, int WARPS, bool PAGED>
 cudaError_t launch_decode(const DecodeArgs& a, dim3 grid, cudaStream_t st) {
   using S = Slot<D, Q4>;
   constexpr int ring = WARPS * S::STAGES * S::BYTES, left = left_bytes(WARPS, D, NT);
   constexpr int bytes = (ring > left ? ring : left) + (SLICES && !left_in_memory(D, Q4, NT) ? left : 0);
-  auto kernel = decode_kernel<D, Q4, NT, SLICES, WARPS>;
+  auto kernel = decode_kernel<D, Q4, NT, SLICES, WARPS, PAGED>;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(kernel, bytes, allowed);
   if (e != cudaSuccess) return e;
@@ -1042,20 +1089,32 @@ using namespace fa;
 
 extern "C" {
 
-size_t fa_decode_workspace_size(const fa_decode_params* p, const fa_cache* c) {
-  CacheView cv;
-  if (check_decode(p, c, cv) != FA_OK || p->Sq == 0) return 0;
+size_t fa_decode_pages_workspace_size(const fa_decode_params* p, const fa_cache* c, const fa_pages* pages) {
+  CacheView held, cv;
+  PageView pv;
+  Span table;
+  if (check_decode(p, c, pages, held, cv, pv, table) != FA_OK || p->Sq == 0) return 0;
   return plan_decode(p, cv).total;
+}
+
+size_t fa_decode_workspace_size(const fa_decode_params* p, const fa_cache* c) {
+  return fa_decode_pages_workspace_size(p, c, nullptr);
 }
 
 fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c, const int64_t* lengths, void* o,
                     float* lse, void* ws, size_t ws_bytes, void* stream) {
-  CacheView cv;
-  fa_status st = check_decode(p, c, cv);
+  return fa_decode_pages(p, q, c, nullptr, lengths, o, lse, ws, ws_bytes, stream);
+}
+
+fa_status fa_decode_pages(const fa_decode_params* p, const void* q, const fa_cache* c, const fa_pages* pages,
+                          const int64_t* lengths, void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  CacheView held, cv;
+  PageView pv;
+  Span all[9];
+  fa_status st = check_decode(p, c, pages, held, cv, pv, all[8]);
   if (st != FA_OK) return st;
   const size_t rows = (size_t)cv.B * p->Hq * p->Sq;
-  Span all[8];
-  cache_spans(cv, all);
+  cache_spans(held, all);
   all[4] = {q, rows * cv.D * 2, "q"};
   Span* out = all + 5;
   out[0] = {o, rows * cv.D * 2, "o"};
@@ -1063,13 +1122,13 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   all[7] = {lengths, lengths != nullptr ? (size_t)cv.B * 8 : 0, "lengths"};
   if ((st = check_buffers(all, 5, out, 2)) != FA_OK) return st;
   if ((uintptr_t)lengths % 8 != 0) { set_error("lengths must be 8-byte aligned"); return FA_ERR_INVALID_ARG; }
-  for (int i = 0; i < 2; ++i)
-    if (overlaps(out[i], all[7])) { set_error("output %s overlaps input lengths", out[i].name); return FA_ERR_INVALID_ARG; }
+  if ((st = check_apart(all + 7, 2, out, 2)) != FA_OK) return st;
   if (p->Sq == 0) return FA_OK;
   const DecodePlan plan = plan_decode(p, cv);
-  if ((st = check_ws(ws, ws_bytes, plan.total, all, 8)) != FA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, plan.total, all, 9)) != FA_OK) return st;
   DecodeArgs a{};
   a.c = cv;
+  a.pages = pv;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
@@ -1095,16 +1154,20 @@ fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_cache* c,
   auto go = [&](auto dim, auto q4) {
     constexpr int D = decltype(dim)::value;
     constexpr bool Q4 = decltype(q4)::value;
-    auto of = [&](auto nt) {
+    auto of = [&](auto nt, auto paged) {
       constexpr int NT = decltype(nt)::value, W = warps_of(D), WIDE = wide_of(D, NT);
+      constexpr bool P = decltype(paged)::value;
       if (plan.slices) {
         if constexpr (NT == 1)
-          if (plan.warps == WIDE) return launch_decode<D, Q4, NT, true, WIDE>(a, grid, cs);
-        return launch_decode<D, Q4, NT, true, W>(a, grid, cs);
+          if (plan.warps == WIDE) return launch_decode<D, Q4, NT, true, WIDE, P>(a, grid, cs);
+        return launch_decode<D, Q4, NT, true, W, P>(a, grid, cs);
       }
-      return plan.warps == W ? launch_decode<D, Q4, NT, false, W>(a, grid, cs) : launch_decode<D, Q4, NT, false, WIDE>(a, grid, cs);
+      return plan.warps == W ? launch_decode<D, Q4, NT, false, W, P>(a, grid, cs) : launch_decode<D, Q4, NT, false, WIDE, P>(a, grid, cs);
     };
-    return plan.nt == 1 ? of(std::integral_constant<int, 1>{}) : of(std::integral_constant<int, 2>{});
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (pages != nullptr) return plan.nt == 1 ? of(One{}, std::true_type{}) : of(Two{}, std::true_type{});
+    return plan.nt == 1 ? of(One{}, std::false_type{}) : of(Two{}, std::false_type{});
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;

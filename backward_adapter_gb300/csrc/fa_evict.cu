@@ -1,0 +1,372 @@
+// Eviction from a quantized cache by accumulated attention weight (fa_cache_evict): of each head's keys the ones that matter
+// are found and moved together, in one kernel.
+//
+// A cluster of blocks has one head of one sequence, a run of its keys for each block. The border between what stays and what
+// goes is found a digit of 8 bits at a time, the highest first: every block counts its keys' digits, the counts are added
+// over the cluster through its shared memory, and the digit in which the wanted number is reached is the border's. Keys
+// above the border stay, and the first of those at it: with the counts of both in the blocks and threads before, every key knows
+// its new place, and writes its index there (kept). Then the rows are moved in waves, a wave of places loaded by the whole
+// cluster before any of it is stored: a key never moves up, so a wave's places hold none of a later wave's keys, and the
+// pages may be the same.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "fa_check.h"
+#include "fa_device.cuh"
+#include "kv_pages.cuh"
+#include "tc_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kCluster = 8;        // blocks of a head, at most
+constexpr int kCached = 10240;     // keys whose weights a block holds in shared memory, within 48 KB; more are read again
+constexpr int kEach = 4;           // keys a thread looks at in turn
+constexpr int kStep = kThreads * kEach;
+
+struct EvictArgs {
+  CacheView c;
+  PageView from, to;
+  const float* weights;
+  const int64_t* lengths;
+  float* weights_out;
+  int32_t* kept;
+  int64_t* new_lengths;
+  unsigned* status;
+  long long W;
+  int keep, sinks, recent;
+  int cached;
+};
+
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// What the cluster's threads wrote before, to shared or global memory, is there for all of them after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ unsigned read_of(unsigned rank, const unsigned* p) {
+  unsigned at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Weights as whole numbers in the same order; no number is the least, and -0 is 0.
+__device__ __forceinline__ unsigned ordered(float w) {
+  if (w != w) return 0u;
+  const unsigned u = w == 0.f ? 0u : __float_as_uint(w);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Exclusive sum of x over the block's threads, and of all; `sums` has a word for each warp.
+__device__ __forceinline__ unsigned block_sum_before(unsigned x, unsigned* sums, unsigned& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  __syncthreads();   // the last call's sums are read
+  if (lane == 31) sums[warp] = y;
+  __syncthreads();
+  unsigned before = y - x;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const unsigned s = sums[w];
+    if (w < warp) before += s;
+    all += s;
+  }
+  return before;
+}
+
+template <int D, bool Q4, bool PAGED>
+__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ unsigned cache[];   // [cached]: the order of this block's first keys
+  __shared__ unsigned counts[4][256], total[256], sums[kThreads / 32], found[2], own[2];
+  const unsigned rank = cluster_rank(), blocks = cluster_size();
+  const unsigned bh = blockIdx.x / blocks;
+  const int b = bh / a.c.Hkv, h = bh % a.c.Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  const long long length = __ldg(a.lengths + b);
+  const int len = (int)min(max(length, 0LL), min((long long)a.c.S, a.W));
+  const int left = min(len, a.keep);
+  if (rank == 0 && h == 0 && threadIdx.x == 0) {
+    if (len != length && a.status != nullptr) atomicCAS(a.status, 0u, 0x40000000u | kSiteDecodeLength);
+    a.new_lengths[b] = left;
+  }
+  const float* weights = a.weights + (size_t)bh * a.W;
+  float* weights_out = a.weights_out + (size_t)bh * a.W;
+  int32_t* kept = a.kept + (size_t)bh * a.keep;
+  const int all_threads = blocks * kThreads, me = rank * kThreads + threadIdx.x;
+
+  if (len <= a.keep) {
+    for (int i = me; i < a.keep; i += all_threads) kept[i] = i < len ? i : -1;
+  } else {
+    // the sinks and the last ones; between them this block's keys [first, first + n)
+    for (int i = me; i < a.sinks; i += all_threads) kept[i] = i;
+    for (int i = me; i < a.recent; i += all_threads) kept[a.keep - a.recent + i] = len - a.recent + i;
+    const int middle = len - a.sinks - a.recent, per = (middle + blocks - 1) / blocks;
+    const int first = min((int)rank * per, middle), n = min(per, middle - first);
+    const float* w = weights + a.sinks + first;
+    for (int i = threadIdx.x; i < min(n, a.cached); i += kThreads) cache[i] = ordered(w[i]);
+    for (int i = threadIdx.x; i < 4 * 256; i += kThreads) counts[i / 256][i % 256] = 0;
+    __syncthreads();
+    auto key = [&](int i) { return i < a.cached ? cache[i] : ordered(w[i]); };
+
+    unsigned border = 0xffffffffu, at_border = 0;   // above every weight: nothing is wanted
+    unsigned wanted = a.keep - a.sinks - a.recent;
+    if (wanted > 0) {
+      border = 0;
+#pragma unroll 1
+      for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+          const int i = i0 + threadIdx.x;
+          const unsigned u = i < n ? key(i) : 0u;
+          const bool in = i < n && (pass == 0 || (u ^ border) >> (shift + 8) == 0);
+          const unsigned digit = u >> shift & 255u;
+          const unsigned lanes = __ballot_sync(0xffffffffu, in);
+          if (lanes == 0) continue;
+          // weights are often alike in their high digits: one count for the lanes that agree with the first, then one each
+          const unsigned common = __shfl_sync(0xffffffffu, digit, __ffs(lanes) - 1);
+          const unsigned agree = __ballot_sync(0xffffffffu, in && digit == common);
+          if (lane == __ffs(agree) - 1) atomicAdd(&counts[pass][common], (unsigned)__popc(agree));
+          if (in && digit != common) atomicAdd(&counts[pass][digit], 1u);
+        }
+        cluster_sync();
+        if (threadIdx.x < 256) {
+          unsigned x = 0;
+          for (unsigned r = 0; r < blocks; ++r) x += read_of(r, &counts[pass][threadIdx.x]);
+          total[threadIdx.x] = x;
+        }
+        __syncthreads();
+        if (warp == 0) {   // lane l has the digits 255 - 8 l and the seven below
+          unsigned x = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x += total[255 - 8 * lane - k];
+          unsigned y = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+          }
+          if (y >= wanted && y - x < wanted) {   // one lane
+            unsigned rest = wanted - (y - x);
+            int digit = 255 - 8 * lane;
+            while (total[digit] < rest) rest -= total[digit--];
+            found[0] = border | (unsigned)digit << shift;
+            found[1] = rest;
+          }
+        }
+        __syncthreads();
+        border = found[0];
+        wanted = found[1];
+      }
+      at_border = wanted;
+    }
+
+    // keys above and at the border, of the blocks before and of the threads before
+    unsigned above = 0, equal = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const unsigned u = key(i);
+      above += u > border;
+      equal += u == border;
+    }
+    unsigned all_above, all_equal;
+    block_sum_before(above, sums, all_above);
+    block_sum_before(equal, sums, all_equal);
+    if (threadIdx.x == 0) {
+      own[0] = all_above;
+      own[1] = all_equal;
+    }
+    cluster_sync();
+    unsigned above_before = 0, equal_before = 0;
+    for (unsigned r = 0; r < rank; ++r) {
+      above_before += read_of(r, &own[0]);
+      equal_before += read_of(r, &own[1]);
+    }
+    for (int i0 = 0; i0 < n; i0 += kStep) {
+      const int i1 = i0 + threadIdx.x * kEach;
+      unsigned u[kEach], x = 0;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        u[k] = i1 + k < n ? key(i1 + k) : 0u;
+        if (i1 + k < n) x += u[k] > border ? 1u << 16 : u[k] == border ? 1u : 0u;
+      }
+      unsigned all;
+      const unsigned before = block_sum_before(x, sums, all);
+      unsigned g = above_before + (before >> 16), e = equal_before + (before & 0xffffu);
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        if (i1 + k >= n) break;
+        const bool more = u[k] > border, same = u[k] == border;
+        if (more || (same && e < at_border)) kept[a.sinks + g + min(e, at_border)] = a.sinks + first + i1 + k;
+        g += more;
+        e += same;
+      }
+      above_before += all >> 16;
+      equal_before += all & 0xffffu;
+    }
+  }
+  cluster_sync();   // kept is there
+
+  // The rows, 16 bytes of numbers for a thread, K's and V's; the first threads of a row have its scales too.
+  constexpr int ROW = Q4 ? D / 2 : D, PIECES = ROW / 16, LANES = 2 * PIECES, NB = D / 32, AHEAD = 4;
+  using Scales = std::conditional_t<NB == 4, uint2, uint32_t>;
+  constexpr int PER = kThreads / LANES;   // rows of a block at a time
+  const int piece = threadIdx.x % LANES % PIECES;
+  const bool second = threadIdx.x % LANES >= PIECES;   // V
+  uint8_t* values = static_cast<uint8_t*>(second ? a.c.v_q : a.c.k_q) + 16 * piece;
+  uint16_t* scales = second ? a.c.v_d : a.c.k_d;
+  auto place = [&](const PageView& pages, int j) -> long long {
+    if constexpr (!PAGED) return (long long)bh * a.c.S + j;
+    const long long row = page_row(pages, a.c.Hkv, b, h, j & ~15, a.status);
+    return row < 0 ? -1 : row + (j & 15);
+  };
+  const int wave = PER * AHEAD * blocks;
+  for (int i0 = 0; i0 < left; i0 += wave) {
+    uint4 x[AHEAD];
+    Scales d[AHEAD];
+    float w[AHEAD];
+    long long to[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + (k * blocks + rank) * PER + threadIdx.x / LANES;
+      to[k] = -1;
+      if (i >= left) continue;
+      const int j = kept[i];
+      if (piece == 0 && !second) w[k] = weights[j];
+      const long long from = place(a.from, j);
+      to[k] = place(a.to, i);
+      if (from == to[k]) {   // it stays where it is
+        to[k] = -1;
+        continue;
+      }
+      x[k] = make_uint4(Q4 ? 0x88888888u : 0u, Q4 ? 0x88888888u : 0u, Q4 ? 0x88888888u : 0u, Q4 ? 0x88888888u : 0u);
+      d[k] = Scales{};
+      if (from >= 0) {
+        x[k] = *reinterpret_cast<const uint4*>(values + from * ROW);
+        if (piece == 0) d[k] = *reinterpret_cast<const Scales*>(scales + from * NB);
+      }
+    }
+    cluster_sync();   // all of the wave is read
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + (k * blocks + rank) * PER + threadIdx.x / LANES;
+      if (i < left && piece == 0 && !second) weights_out[i] = w[k];
+      if (to[k] < 0) continue;
+      *reinterpret_cast<uint4*>(values + to[k] * ROW) = x[k];
+      if (piece == 0) *reinterpret_cast<Scales*>(scales + to[k] * NB) = d[k];
+    }
+  }
+  for (long long i = left + me; i < a.W; i += all_threads) weights_out[i] = 0.f;
+}
+
+template <int D, bool Q4, bool PAGED>
+cudaError_t launch_evict(const EvictArgs& a, long long heads, int blocks, cudaStream_t st) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = blocks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(heads * blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)a.cached * 4;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  auto kernel = evict_kernel<D, Q4, PAGED>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" fa_status fa_cache_evict(const fa_evict_params* p, const fa_cache* c, const fa_pages* pages, const fa_pages* to,
+                                    const float* weights, int64_t W, const int64_t* lengths, float* weights_out,
+                                    int32_t* kept, int64_t* new_lengths, void* stream) {
+  clear_error();
+  if (p == nullptr) { set_error("params is NULL"); return FA_ERR_INVALID_ARG; }
+  CacheView held, cv, there;
+  PageView from, dst;
+  Span in[4], out[7];
+  fa_status st = check_paged(c, pages, held, cv, from, in[0]);
+  if (st != FA_OK) return st;
+  if (to != nullptr && pages == nullptr) { set_error("a second table needs a first one"); return FA_ERR_INVALID_ARG; }
+  if ((st = check_paged(c, to != nullptr ? to : pages, held, there, dst, in[1])) != FA_OK) return st;
+  if (there.B != cv.B) { set_error("tables of %d and %d sequences", cv.B, there.B); return FA_ERR_INVALID_ARG; }
+  if (p->reserved != 0) { set_error("reserved field must be 0"); return FA_ERR_INVALID_ARG; }
+  if (p->keep < 1 || p->keep > kMaxSeq) { set_error("keep=%d outside [1, %d]", p->keep, kMaxSeq); return FA_ERR_INVALID_ARG; }
+  if (p->sinks < 0 || p->recent < 0 || (long long)p->sinks + p->recent > p->keep) {
+    set_error("sinks=%d, recent=%d: not negative, together at most keep=%d", p->sinks, p->recent, p->keep); return FA_ERR_INVALID_ARG;
+  }
+  if (to != nullptr && there.S < p->keep) {
+    set_error("the second table has room for %d keys of %d", there.S, p->keep); return FA_ERR_INVALID_ARG;
+  }
+  if (W < 1 || W > 0x7fffffffLL) { set_error("W=%lld outside [1, 2^31 - 1]", (long long)W); return FA_ERR_INVALID_ARG; }
+  const long long heads = (long long)cv.B * cv.Hkv;
+  if (heads * kCluster > 0x7fffffffLL) { set_error("too many heads for one launch"); return FA_ERR_UNSUPPORTED; }
+  const size_t bytes = (size_t)heads * (size_t)W * 4;
+  in[2] = {lengths, (size_t)cv.B * 8, "lengths"};
+  in[3] = {weights, weights != weights_out ? bytes : 0, "weights"};
+  cache_spans(held, out);
+  out[4] = {weights_out, bytes, "weights_out"};
+  out[5] = {kept, (size_t)heads * p->keep * 4, "kept"};
+  out[6] = {new_lengths, (size_t)cv.B * 8, "new_lengths"};
+  if (lengths == nullptr || new_lengths == nullptr || (uintptr_t)lengths % 8 != 0 || (uintptr_t)new_lengths % 8 != 0) {
+    set_error("lengths and new_lengths: there, and 8-byte aligned"); return FA_ERR_INVALID_ARG;
+  }
+  if (weights == nullptr || (uintptr_t)weights % 16 != 0) { set_error("weights is NULL or not 16-byte aligned"); return FA_ERR_INVALID_ARG; }
+  if ((st = check_buffers(nullptr, 0, out, 6)) != FA_OK) return st;
+  if ((st = check_apart(out, 6, out + 6, 1)) != FA_OK) return st;
+  if ((st = check_apart(in, 4, out, 7)) != FA_OK) return st;
+  EvictArgs a{};
+  a.c = cv;
+  a.from = from;
+  a.to = dst;
+  a.weights = weights;
+  a.lengths = lengths;
+  a.weights_out = weights_out;
+  a.kept = kept;
+  a.new_lengths = new_lengths;
+  a.status = device_status_ptr();
+  a.W = W;
+  a.keep = p->keep;
+  a.sinks = p->sinks;
+  a.recent = p->recent;
+  // As many blocks for a head as fill the SMs, none with less than 1024 keys.
+  const long long keys = W < cv.S ? W : cv.S;
+  int blocks = 1;
+  while (blocks < kCluster && heads * blocks * 2 <= 2LL * sm_count() && keys >= 2048LL * blocks) blocks *= 2;
+  const long long per = (keys + blocks - 1) / blocks;
+  a.cached = (int)(per < kCached ? per : kCached);
+  auto go = [&](auto dim, auto q4) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool Q4 = decltype(q4)::value;
+    cudaStream_t cs = (cudaStream_t)stream;
+    return pages != nullptr ? launch_evict<D, Q4, true>(a, heads, blocks, cs) : launch_evict<D, Q4, false>(a, heads, blocks, cs);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  cudaError_t e;
+  if (cv.q4) e = cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
+  else e = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
+  return cuda_status(e, "cache evict launch");
+}

@@ -209,12 +209,21 @@ struct CacheView {
   void* v_q;
   uint16_t* v_d;
 };
+// The pages of a paged cache (fa_pages): then CacheView's B and S are the sequences and the keys that the table has
+// room for, and rows are found with page_row (kv_pages.cuh). Without a table: table == nullptr.
+struct PageView {
+  const int32_t* table;
+  long long stride;           // between the tables of two sequences
+  unsigned long long magic;   // ceil(2^40 / (P / 16))
+  unsigned P, pages;          // keys of a page, pages of the pool
+};
 constexpr unsigned kSiteCacheRow = 951;
 constexpr unsigned kSiteDecodeLength = 952;
+constexpr unsigned kSitePage = 953;
 // fa_cache_write: begin (device) or begin_all when NULL; count (device) or n_rows when NULL.
-cudaError_t launch_cache_write(const CacheView& c, const RowView& k, const RowView& v, int dtype, int n_rows,
-                               const int64_t* begin, long long begin_all, const int64_t* count, unsigned* status,
-                               cudaStream_t st);
+cudaError_t launch_cache_write(const CacheView& c, const PageView& pages, const RowView& k, const RowView& v, int dtype,
+                               int n_rows, const int64_t* begin, long long begin_all, const int64_t* count,
+                               unsigned* status, cudaStream_t st);
 // fa_cache_read: keys [begin, begin + n_rows) of every head as values in dtype.
 cudaError_t launch_cache_read(const CacheView& c, long long begin, int n_rows, int dtype, const RowView& k,
                               const RowView& v, cudaStream_t st);

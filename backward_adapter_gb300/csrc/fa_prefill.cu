@@ -1,0 +1,880 @@
+// Attention of a chunk of new tokens of every sequence, a ragged batch, over its quantized cache, in pages or in one piece
+// (fa_prefill): the serving form of the forward, on the 5th-generation tensor cores.
+//
+// Mathematics. The G = Hq / Hkv query heads of a key/value head and its tokens are the rows of one matrix, token by token, so
+// that a tile of 128 rows covers few positions and skips what lies behind the last. With K and V rounded to bf16:
+// S = scale Q K^T, hidden pairs -inf, O = softmax(S) V by tiles of 128 keys with a running maximum (followed only when it
+// grows by 2^8) and sum, in 32 bits; P is rounded to bf16 for its product.
+//
+// Split. A unit is 256 rows (two tiles) of one sequence's key/value head. The tiles of 128 keys of all units form one list,
+// cut into equal slices, one for each SM: the end of one unit, whole units, the beginning of another. A unit that several
+// slices share leaves its parts (unnormalised O, reference and sum) in the workspace, and a second kernel joins them. So one
+// row block over a long window and a batch of short ones fill the machine alike, without a choice of splits; a block
+// finds its place in the list from the lengths, on the device.
+//
+// A block of 16 warps: warps 4-7 read the packed bytes and write the bf16 operands (kv_tile.cuh), one tile of K and the V of
+// the tile before into each stage of a ring; one thread of warp 0 issues the MMAs (S_t = Q_t K^T, O_t += P_t V); warps 8-11
+// and 12-15 have a row of Q_0 and Q_1 for each thread: they load Q, turn scores into P in TMEM, and write O at the end.
+// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256, 256+D), O1 [256+D, 256+2D).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cmath>
+#include <type_traits>
+
+#include "fa_check.h"
+#include "fa_device.cuh"
+#include "kv_tile.cuh"
+#include "tc_ptx.cuh"
+
+namespace fa {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128;          // rows of a tile
+constexpr int kUnit = 2 * kBM;    // rows of a unit
+constexpr int kBN = kTileKeys;
+constexpr int kThreads = 512;
+constexpr int kListed = 1024;     // sequences of a launch; more are more launches
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.f;   // log2 units: the reference follows the maximum when that has grown by more
+constexpr int kRegsIssue = 40, kRegsLoad = 104, kRegsSoftmax = 184;
+static_assert((kRegsIssue + kRegsLoad + 2 * kRegsSoftmax) * 128 <= kThreads * 128, "register split exceeds the launch's");
+
+struct Record {   // a unit that slices c0 .. c1 share (c1 < 0: none)
+  int b, h, unit, c0, c1, padding[3];
+};
+
+struct PrefillArgs {
+  CacheView c;
+  PageView pages;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  const int64_t* lengths;
+  const int64_t* count;
+  float* part_o;     // [slices, 2, part_rows, D], unnormalised: of the unit a slice begins inside of, of the one it ends in
+  float2* part_ml;   // [slices, 2, part_rows]: what the weights are relative to (base 2), and their sum
+  Record* records;   // [slices]: the unit that a slice is the second of
+  unsigned* status;
+  float sl2;         // |scale| log2(e); the sign, or a scale of 0, is in the two masks
+  uint32_t q_and, q_xor;
+  int Hq, Sq, window, layout, G, part_rows;
+};
+
+// A sequence's keys and tokens.
+struct Seq { int len, n; };
+
+__device__ __forceinline__ Seq seq_of(const PrefillArgs& a, int b, bool report) {
+  const long long len = a.lengths != nullptr ? __ldg(a.lengths + b) : a.c.S;
+  const long long n = a.count != nullptr ? __ldg(a.count + b) : a.Sq;
+  const Seq s{(int)min(max(len, 0LL), (long long)a.c.S), (int)min(max(n, 0LL), (long long)a.Sq)};
+  if (report && (s.len != len || s.n != n) && a.status != nullptr) atomicCAS(a.status, 0u, 0x40000000u | kSiteDecodeLength);
+  return s;
+}
+
+__device__ __forceinline__ int units_of(const PrefillArgs& a, Seq s) { return (s.n * a.G + kUnit - 1) / kUnit; }
+
+// The tiles of keys that a unit's rows see: at least one, so that rows which see nothing are written by someone.
+struct Tiles { int begin, end; };
+
+__device__ __forceinline__ Tiles tiles_of(const PrefillArgs& a, Seq s, int unit) {
+  const int first = unit * kUnit / a.G, last = (min(unit * kUnit + kUnit, s.n * a.G) - 1) / a.G;   // tokens
+  const int before = s.len - s.n;
+  Tiles t;
+  t.begin = a.window > 0 ? max(before + first - a.window, 0) / kBN : 0;
+  t.end = max((max(before + last + 1, 0) + kBN - 1) / kBN, t.begin + 1);
+  return t;
+}
+
+// `total` tiles cut into n slices that differ by one at most, the larger ones first.
+struct Slices {
+  long long each, more;
+  __device__ __forceinline__ Slices(long long total, int n) : each(total / n), more(total % n) {}
+  __device__ __forceinline__ long long begin(long long i) const { return i * each + min(i, more); }
+  __device__ __forceinline__ int of(long long tile) const {
+    const long long large = more * (each + 1);
+    return (int)(tile < large ? tile / (each + 1) : more + (tile - large) / each);
+  }
+};
+
+// What every role of a block knows of the list.
+struct Plan {
+  Seq seq[kListed];
+  long long before[kListed + 1];   // tiles of the sequences before, all heads
+  int b, h, unit, off;             // where the slice begins
+  long long tiles;                 // how many it has
+};
+
+__device__ __forceinline__ long long warp_sum_ll(long long x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Fills the plan (all threads of the block).
+__device__ __forceinline__ void make_plan(const PrefillArgs& a, Plan& plan, int slice, int slices) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = threadIdx.x; b < a.c.B; b += kThreads) plan.seq[b] = seq_of(a, b, slice == 0);
+  __syncthreads();
+  for (int b = warp; b < a.c.B; b += kThreads / 32) {
+    const Seq s = plan.seq[b];
+    const int n = units_of(a, s);
+    long long x = 0;
+    for (int u = lane; u < n; u += 32) {
+      const Tiles t = tiles_of(a, s, u);
+      x += t.end - t.begin;
+    }
+    x = warp_sum_ll(x);
+    if (lane == 0) plan.before[b] = x * a.c.Hkv;
+  }
+  __syncthreads();
+  if (warp != 0) {
+    __syncthreads();
+    return;
+  }
+  long long all = 0;   // an exclusive sum in place
+  for (int b0 = 0; b0 < a.c.B; b0 += 32) {
+    const long long own = b0 + lane < a.c.B ? plan.before[b0 + lane] : 0;
+    long long x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (b0 + lane < a.c.B) plan.before[b0 + lane] = all + x - own;
+    all += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) plan.before[a.c.B] = all;
+  __syncwarp();
+  const Slices cut(all, slices);
+  const long long at = cut.begin(slice), tiles = cut.begin(slice + 1) - at;
+  Record rec{0, 0, 0, 0, -1, {0, 0, 0}};
+  if (tiles > 0) {
+    int b = 0;   // the last sequence that begins at or before the slice; one without tiles begins where the next does
+    for (int b0 = 0; b0 < a.c.B; b0 += 32) b += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.c.B && plan.before[b0 + lane] <= at));
+    --b;
+    const Seq s = plan.seq[b];
+    const long long head = (plan.before[b + 1] - plan.before[b]) / a.c.Hkv, off = at - plan.before[b];
+    const int h = (int)(off / head), n = units_of(a, s);
+    long long rest = off % head;   // tiles of the head before the slice
+    int unit = 0, inside = 0, length = 0;
+    for (int u0 = 0; u0 < n; u0 += 32) {
+      const int u = u0 + lane;
+      int own = 0;
+      if (u < n) {
+        const Tiles t = tiles_of(a, s, u);
+        own = t.end - t.begin;
+      }
+      long long x = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, x > rest);   // units that end behind the slice's first tile
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        unit = u0 + l;
+        inside = (int)(rest - __shfl_sync(0xffffffffu, x - own, l));
+        length = __shfl_sync(0xffffffffu, own, l);
+        break;
+      }
+      rest -= __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      plan.b = b;
+      plan.h = h;
+      plan.unit = unit;
+      plan.off = inside;
+    }
+    if (inside > 0 && cut.begin(slice - 1) <= at - inside) rec = Record{b, h, unit, slice - 1, cut.of(at - inside + length - 1), {0, 0, 0}};
+  }
+  if (lane == 0) {
+    plan.tiles = tiles;
+    if (a.records != nullptr) a.records[slice] = rec;
+  }
+  __syncthreads();
+}
+
+// A slice's part of one unit.
+struct Piece {
+  int b, h, unit;
+  int tile, tiles;    // the first one, and how many
+  int rows;           // live rows of the unit
+  bool starts, ends;  // the unit's first, last tile is among them
+  Seq s;
+};
+
+// The pieces of a slice, one after the other; every role walks them for itself.
+struct Walk {
+  const PrefillArgs& a;
+  const Plan& plan;
+  int b, h, unit, off;
+  long long left;
+  __device__ __forceinline__ Walk(const PrefillArgs& a_, const Plan& p)
+      : a(a_), plan(p), b(p.b), h(p.h), unit(p.unit), off(p.off), left(p.tiles) {}
+  __device__ __forceinline__ bool next(Piece& x) {
+    if (left <= 0) return false;
+    x.s = plan.seq[b];
+    const Tiles t = tiles_of(a, x.s, unit);
+    x.b = b;
+    x.h = h;
+    x.unit = unit;
+    x.tile = t.begin + off;
+    x.tiles = (int)min((long long)(t.end - x.tile), left);
+    x.rows = min(x.s.n * a.G - unit * kUnit, kUnit);
+    x.starts = off == 0;
+    x.ends = x.tile + x.tiles == t.end;
+    left -= x.tiles;
+    off = 0;
+    if (++unit == units_of(a, x.s)) {
+      unit = 0;
+      if (++h == a.c.Hkv) {
+        h = 0;
+        do ++b;
+        while (b < a.c.B && plan.seq[b].n == 0);
+      }
+    }
+    return true;
+  }
+};
+
+// Element offset of a unit's row in q and o, and its place in lse.
+struct RowPlace {
+  int token;
+  size_t at, log;
+};
+__device__ __forceinline__ RowPlace place_of(const PrefillArgs& a, int b, int h, int row) {
+  const int i = row / a.G, head = h * a.G + row % a.G;
+  RowPlace p;
+  p.token = i;
+  p.at = (a.layout ? ((size_t)b * a.Sq + i) * a.Hq + head : ((size_t)b * a.Hq + head) * a.Sq + i) * a.c.D;
+  p.log = ((size_t)b * a.Hq + head) * a.Sq + i;
+  return p;
+}
+
+template <int D>
+struct PrefillSmem {
+  static constexpr int kBoxBytes = 128 * 128;
+  static constexpr int kTileBytes = kBM * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;   // a stage: the V of one tile of keys and the K of the next
+  static constexpr int kKVOff = 2 * kTileBytes;
+  static constexpr int kBarOff = kKVOff + 2 * kStages * kTileBytes;
+  static constexpr int kPlanOff = kBarOff + 256;
+  static constexpr int kBytes = kPlanOff + (int)sizeof(Plan) + 1024;
+};
+
+template <int D, bool Q4, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
+  using L = PrefillSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + L::kKVOff);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* bar_q = bars;                         // [2]: tile t of a unit's Q written
+  uint64_t* bar_s = bars + 2;                     // [2]: scores of tile t there
+  uint64_t* bar_p = bars + 4;                     // [2]: weights of tile t there
+  uint64_t* bar_o = bars + 6;                     // [2]: the last product of tile t done
+  uint64_t* bar_full = bars + 8;                  // [kStages]: stage written
+  uint64_t* bar_empty = bar_full + L::kStages;    // [kStages]: its MMAs done
+  uint64_t* bar_done = bar_empty + L::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Plan& plan = *reinterpret_cast<Plan*>(smem + L::kPlanOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  let_next_kernel_start();
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar_q[t], 4);
+      mbar_init(&bar_s[t], 1);
+      mbar_init(&bar_p[t], 4);
+      mbar_init(&bar_o[t], 1);
+    }
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&bar_full[i], 4);
+      mbar_init(&bar_empty[i], 1);
+    }
+    mbar_init(bar_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  make_plan(a, plan, blockIdx.x, gridDim.x);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) {
+    regs_dec<kRegsIssue>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------------- MMA issuer
+      const uint32_t idesc_qk = idesc_bf16_f32(kBM, kBN, 0, 0);
+      const uint32_t idesc_pv = idesc_bf16_f32(kBM, D, 0, 1);
+      auto issue_pv = [&](int t, int slot, bool first) {
+        const uint64_t dv0 = smem_desc_sw128(sKV + slot * L::kTileBytes, L::kBoxBytes, 1024);
+        const uint32_t d_tmem = tmem + 256 + t * D, a_tmem = tmem + t * 128;
+#pragma unroll
+        for (int k = 0; k < kBN / 16; ++k)
+          mma_ts(d_tmem, a_tmem + k * 8, desc_add(dv0, k * 2048), idesc_pv, (!first || k > 0) ? 1u : 0u);
+      };
+      auto issue_s = [&](int t, int slot) {
+        const uint64_t dq0 = smem_desc_sw128(sQ + t * L::kTileBytes, 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(sKV + slot * L::kTileBytes, 16, 1024);
+        const uint32_t d_tmem = tmem + t * 128;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
+          mma_ss(d_tmem, desc_add(dq0, off), desc_add(dk0, off), idesc_qk, k > 0 ? 1u : 0u);
+        }
+        mma_commit(&bar_s[t]);
+      };
+      // The pieces' tiles are one stream: stage i holds the K of its tile i and the V of tile i - 1. Within a piece a tile of
+      // rows gets its P V of the last tile of keys and then its next S, one tile of rows after the other; where a piece ends
+      // both products come first.
+      bool ok = true;
+      int stage = 0;                    // tiles of the stream so far
+      int scores[2] = {0, 0};           // of bar_s and bar_p: completions so far
+      int pieces[2] = {0, 0};           // of bar_q
+      int pending = 0;                  // tiles of rows of the last tile of keys whose product is to come
+      bool pending_first = false, pending_last = false;   // it is its piece's first, last
+      auto product = [&](int t, int slot) -> bool {
+        if (!mbar_wait<true>(&bar_p[t], (scores[t] - 1) & 1, abort_flag, a.status, 1001)) return false;
+        tc_fence_after();
+        issue_pv(t, slot, pending_first);
+        if (pending_last) mma_commit(&bar_o[t]);
+        return true;
+      };
+      Walk walk(a, plan);
+      Piece x;
+      while (ok && walk.next(x)) {
+        const int live = x.rows > kBM ? 2 : 1;
+        for (int j = 0; ok && j < x.tiles; ++j) {
+          const int sb = stage % L::kStages;
+          if (!(ok = mbar_wait<true>(&bar_full[sb], (stage / L::kStages) & 1, abort_flag, a.status, 1002))) break;
+          tc_fence_after();
+          if (j == 0) {
+            for (int t = 0; ok && t < pending; ++t) ok = product(t, 2 * sb + 1);
+            for (int t = 0; ok && t < live; ++t) {
+              if (!(ok = mbar_wait<true>(&bar_q[t], pieces[t] & 1, abort_flag, a.status, 1003))) break;
+              tc_fence_after();
+              ++pieces[t];
+              issue_s(t, 2 * sb);
+              ++scores[t];
+            }
+          } else {
+            for (int t = 0; ok && t < live; ++t) {
+              if (!(ok = product(t, 2 * sb + 1))) break;
+              issue_s(t, 2 * sb);
+              ++scores[t];
+            }
+          }
+          if (!ok) break;
+          mma_commit(&bar_empty[sb]);
+          pending = live;
+          pending_first = j == 0;
+          pending_last = j == x.tiles - 1;
+          ++stage;
+        }
+      }
+      if (ok && pending > 0) {   // the stream's last stage holds only V
+        const int sb = stage % L::kStages;
+        ok = mbar_wait<true>(&bar_full[sb], (stage / L::kStages) & 1, abort_flag, a.status, 1004);
+        tc_fence_after();
+        for (int t = 0; ok && t < pending; ++t) ok = product(t, 2 * sb + 1);
+      }
+      // every MMA of this thread is complete before TMEM is given back
+      mma_commit(bar_done);
+      mbar_wait<true>(bar_done, 0, nullptr, a.status, 1005);
+    }
+  } else if (warp < 8) {
+    regs_dec<kRegsLoad>();
+    // ------------------------------------------------------------------ K and V: from bytes to operands
+    const int w = warp - 4;
+    Walk walk(a, plan);
+    Piece x;
+    x.tiles = 0;
+    int j = 0;
+    // where this warp's rows of the next tile of the stream lie; false behind the last
+    auto next_rows = [&](TileRows& t) -> bool {
+      if (j == x.tiles) {
+        if (!walk.next(x)) return false;
+        j = 0;
+      }
+      t = tile_rows<PAGED>(a.c, a.pages, x.b, x.h, (x.tile + j) * kBN + 32 * w, x.s.len, a.status);
+      ++j;
+      return true;
+    };
+    TileRows now, then;
+    TileBytes<D, Q4> k, v;
+    bool has_k = next_rows(now), has_v = false;
+    if (has_k) k.load(a.c.k_q, a.c.k_d, now);
+    for (int stage = 0; has_k || has_v; ++stage) {
+      // K of the tile `now` is on its way, and V of the one before it if there is one
+      const int sb = stage % L::kStages;
+      const bool more = has_k && next_rows(then);
+      if (stage >= L::kStages &&
+          !__all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[sb], (stage / L::kStages - 1) & 1, abort_flag, a.status, 1006)))
+        break;
+      const uint32_t at = sKV + 2 * sb * L::kTileBytes;
+      if (has_k) {
+        k.template store<false>(at, w);
+        if (more) k.load(a.c.k_q, a.c.k_d, then);
+      }
+      if (has_v) v.template store<true>(at + L::kTileBytes, w);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_full[sb]);
+      if (has_k) v.load(a.c.v_q, a.c.v_d, now);
+      has_v = has_k;
+      has_k = more;
+      now = then;
+    }
+  } else {
+    regs_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------------ softmax, a row for each thread
+    const int t = (warp - 8) / 4, wq = warp & 3;
+    const int r = wq * 32 + lane;   // row of the tile
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * D + lane_off;
+    const uint32_t my_q = sQ + t * L::kTileBytes + r * 128;
+    const float sl2 = a.sl2;
+    // the next piece with live rows in this tile
+    Walk walk(a, plan);
+    auto next_live = [&](Piece& x) -> bool {
+      while (walk.next(x))
+        if (x.rows > t * kBM) return true;
+      return false;
+    };
+    auto load_q = [&](const Piece& x) {
+      const int row = x.unit * kUnit + t * kBM + r;
+      const bool on = t * kBM + r < x.rows;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (on ? place_of(a, x.b, x.h, row).at : 0));
+#pragma unroll
+      for (int c0 = 0; c0 < D / 8; c0 += 8) {
+        uint4 u[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) u[c] = on ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4(my_q + (c0 / 8) * L::kBoxBytes + ((c ^ (r & 7)) << 4), (u[c].x & a.q_and) ^ a.q_xor,
+                       (u[c].y & a.q_and) ^ a.q_xor, (u[c].z & a.q_and) ^ a.q_xor, (u[c].w & a.q_and) ^ a.q_xor);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_q[t]);
+    };
+    bool ok = true;
+    int tiles = 0, pieces = 0;   // completions of bar_s and bar_o so far
+    Piece x, ahead;
+    bool has = next_live(x);
+    if (has) load_q(x);
+    while (has && ok) {
+      const int row = x.unit * kUnit + t * kBM + r;
+      const bool live = t * kBM + r < x.rows;
+      const RowPlace place = place_of(a, x.b, x.h, live ? row : 0);
+      // the keys this row sees: [key_lo, key_hi]
+      const int key_hi = live ? min(x.s.len - x.s.n + place.token, x.s.len - 1) : -1;
+      const int key_lo = a.window > 0 ? key_hi - a.window : 0;
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int j = 0; j < x.tiles; ++j) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[t], tiles & 1, abort_flag, a.status, 1007)))) break;
+        ++tiles;
+        tc_fence_after();
+        const int key0 = (x.tile + j) * kBN;
+        const int lo = min(max(key_lo - key0, 0), kBN), lim = max(min(key_hi - key0, kBN - 1), -1);
+        const bool full = lo == 0 && lim == kBN - 1;
+        float s[kBN];
+        auto masked = [&](const uint32_t (&raw)[32], int c0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[c0 + e] = __uint_as_float(raw[e]);
+          if (!full) {
+            const int from = max(lo - c0, 0), to = min(lim - c0 + 1, 32);
+            const uint32_t seen = to <= from ? 0u : (uint32_t)(((1ull << to) - 1ull) & ~((1ull << from) - 1ull));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[c0 + e] = (seen >> e) & 1u ? s[c0 + e] : -CUDART_INF_F;
+          }
+        };
+        {
+          uint32_t raw[2][32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            tmem_ld32(tS + half * 64, raw[0]);
+            tmem_ld32(tS + half * 64 + 32, raw[1]);
+            tmem_wait_ld();
+            reg_fence(raw[0]);
+            reg_fence(raw[1]);
+            masked(raw[0], half * 64);
+            masked(raw[1], half * 64 + 32);
+          }
+        }
+        float top4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int e = 0; e < kBN; e += 2) top4[(e >> 1) & 3] = max3f(top4[(e >> 1) & 3], s[e], s[e + 1]);
+        const float top_s = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+        const float m_new = fmaxf(m, top_s * sl2);
+        const bool rescale = m_new > m + kRescale;   // false while nothing is seen
+        const float m_use = rescale ? m_new : m;
+        const float alpha = rescale ? ex2_approx(m - m_new) : 1.f;
+        const float m_sub = m_use == -CUDART_INF_F ? 0.f : m_use;
+        const uint64_t sl2_2 = f32x2(sl2, sl2), negm_2 = f32x2(-m_sub, -m_sub);
+        uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+#pragma unroll
+        for (int cch = 0; cch < kBN / 32; ++cch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float t0, t1;
+            f32x2_split(fma_f32x2(f32x2(s[cch * 32 + 2 * e], s[cch * 32 + 2 * e + 1]), sl2_2, negm_2), t0, t1);
+            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+            sum2[e & 1] = add_f32x2(sum2[e & 1], f32x2(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tS + cch * 16, pk);
+        }
+        float s0, s1, s2, s3;
+        f32x2_split(sum2[0], s0, s1);
+        f32x2_split(sum2[1], s2, s3);
+        l = l * alpha + ((s0 + s1) + (s2 + s3));
+        m = m_use;
+        if (__any_sync(0xffffffffu, rescale) && j > 0) {   // alpha is 1 for rows that keep their reference
+          // O holds the products of the tiles before: their MMAs ended before these scores did
+#pragma unroll
+          for (int cch = 0; cch < D / 32; ++cch) {
+            uint32_t ov[32];
+            tmem_ld32(tO + cch * 32, ov);
+            tmem_wait_ld();
+            reg_fence(ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st32(tO + cch * 32, ov);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_p[t]);
+      }
+      if (!ok) break;
+      // The scores of the piece's last tile are there, so nothing reads its Q any more: the next one's takes its place.
+      const bool next = next_live(ahead);
+      if (next) load_q(ahead);
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_o[t], pieces & 1, abort_flag, a.status, 1008)))) break;
+      ++pieces;
+      tc_fence_after();
+      const bool alive = l != 0.f;   // a sum that is no number is one
+      const bool whole = x.starts && x.ends;
+      const float inv = !whole ? 1.f : alive ? 1.f / l : 0.f;
+      uint4* out = reinterpret_cast<uint4*>(a.o + place.at);
+      const size_t part = ((size_t)blockIdx.x * 2 + (x.starts ? 1 : 0)) * a.part_rows + t * kBM + r;
+      float4* left = reinterpret_cast<float4*>(a.part_o + part * D);
+#pragma unroll
+      for (int cch = 0; cch < D / 32; ++cch) {
+        uint32_t ov[32];
+        tmem_ld32(tO + cch * 32, ov);
+        tmem_wait_ld();
+        reg_fence(ov);
+        if (!live) continue;
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = alive ? __uint_as_float(ov[e]) * inv : 0.f;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            out[cch * 4 + e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                          pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) left[cch * 8 + e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+        }
+      }
+      tc_fence_before();   // these reads of O come before the next piece's product, which waits for bar_p
+      if (live) {
+        if (whole) a.lse[place.log] = alive ? (m + log2f(l)) * kLn2 : 0.f;
+        else a.part_ml[part] = make_float2(alive ? m : -CUDART_INF_F, l);
+      }
+      x = ahead;
+      has = next;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the units that slices share: of each row the parts by their weights, in the order of the slices. Units
+// of few parts have a warp for each row, of many a block; the rows of all units are one list over the blocks.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a, int slices) {
+  constexpr int F = D / 32, AHEAD = 8, kMany = 24;   // parts
+  using V = std::conditional_t<F == 4, float4, float2>;
+  extern __shared__ int first_item[];   // [slices + 1]
+  __shared__ float so[8][D];
+  __shared__ float2 sml[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_for_kernel_before();
+  auto items = [&](int rows, int parts) { return parts > kMany ? rows : (rows + 7) / 8; };
+  auto rows_of = [&](const Record& rec) { return min(seq_of(a, rec.b, false).n * a.G - rec.unit * kUnit, kUnit); };
+  if (warp == 0) {
+    int all = 0;
+    for (int c0 = 0; c0 < slices; c0 += 32) {
+      int own = 0;
+      if (c0 + lane < slices) {
+        const Record rec = a.records[c0 + lane];
+        if (rec.c1 >= 0) own = items(rows_of(rec), rec.c1 - rec.c0 + 1);
+      }
+      int x = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (c0 + lane < slices) first_item[c0 + lane] = all + x - own;
+      all += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) first_item[slices] = all;
+  }
+  __syncthreads();
+  const int all = first_item[slices];
+  for (int item = blockIdx.x; item < all; item += gridDim.x) {
+    int c = 0, past = slices;   // the last record that begins at or before the item (those without items begin where the next do)
+    while (past - c > 1) {
+      const int mid = (c + past) / 2;
+      if (first_item[mid] <= item) c = mid;
+      else past = mid;
+    }
+    const Record rec = a.records[c];
+    const int parts = rec.c1 - rec.c0 + 1, off = item - first_item[c], rows = rows_of(rec);
+    const bool many = parts > kMany;
+    const int row = many ? off : off * 8 + warp;
+    const int first = many ? warp : 0, step = many ? 8 : 1;
+    float top = -CUDART_INF_F, l = 0.f, o[F];
+#pragma unroll
+    for (int j = 0; j < F; ++j) o[j] = 0.f;
+    if (row < rows) {
+      auto place = [&](int p) { return ((size_t)(rec.c0 + p) * 2 + (p == 0 ? 1 : 0)) * a.part_rows + row; };
+      for (int p0 = first; p0 < parts; p0 += 32 * step) {   // 32 parts at a time, one for each lane to look at
+        const int n = min(32, (parts - p0 + step - 1) / step);
+        const float2 ml = lane < n ? a.part_ml[place(p0 + lane * step)] : make_float2(-CUDART_INF_F, 0.f);
+        const float now = fmaxf(top, warp_max(ml.x)), ref = now == -CUDART_INF_F ? 0.f : now;
+        const float back = ex2_approx(top - ref), mine = ex2_approx(ml.x - ref);
+        top = now;
+        l = l * back + warp_sum(mine * ml.y);
+#pragma unroll
+        for (int j = 0; j < F; ++j) o[j] *= back;
+        for (int k0 = 0; k0 < n; k0 += AHEAD) {
+          V v[AHEAD];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+            if (k0 + k < n) v[k] = reinterpret_cast<const V*>(a.part_o + place(p0 + (k0 + k) * step) * D)[lane];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, mine, (k0 + k) & 31);
+            if (k0 + k < n) {
+              o[0] = fmaf(wk, v[k].x, o[0]);
+              o[1] = fmaf(wk, v[k].y, o[1]);
+              if constexpr (F == 4) {
+                o[2] = fmaf(wk, v[k].z, o[2]);
+                o[3] = fmaf(wk, v[k].w, o[3]);
+              }
+            }
+          }
+        }
+      }
+    }
+    if (many) {
+      __syncthreads();   // the last item's sums are read
+      if (lane == 0) sml[warp] = make_float2(top, l);
+#pragma unroll
+      for (int j = 0; j < F; ++j) so[warp][lane * F + j] = o[j];
+      __syncthreads();
+      if (warp != 0) continue;
+      const float2 ml = lane < 8 ? sml[lane] : make_float2(-CUDART_INF_F, 0.f);
+      top = warp_max(ml.x);
+      const float mine = ex2_approx(ml.x - (top == -CUDART_INF_F ? 0.f : top));
+      l = warp_sum(mine * ml.y);
+#pragma unroll
+      for (int j = 0; j < F; ++j) o[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, mine, k);
+#pragma unroll
+        for (int j = 0; j < F; ++j) o[j] = fmaf(wk, so[k][lane * F + j], o[j]);
+      }
+    }
+    if (row >= rows) continue;
+    const RowPlace place = place_of(a, rec.b, rec.h, rec.unit * kUnit + row);
+    const bool alive = l != 0.f;
+    const float inv = alive ? 1.f / l : 0.f;
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + place.at + lane * F);
+#pragma unroll
+    for (int j = 0; j < F; j += 2) out[j / 2] = pack_bf16x2(o[j] * inv, o[j + 1] * inv);
+    if (lane == 0) a.lse[place.log] = alive ? (top + log2f(l)) * kLn2 : 0.f;
+  }
+}
+
+struct PrefillPlan {
+  int slices, part_rows;
+  size_t part_ml, records, total;   // offsets in the workspace; part_o is at 0
+};
+
+PrefillPlan plan_prefill(const fa_prefill_params* p, const CacheView& c) {
+  PrefillPlan x{};
+  x.slices = sm_count();
+  const long long rows = (long long)(p->Hq / c.Hkv) * p->Sq;
+  x.part_rows = (int)(rows < kUnit ? rows : kUnit);
+  const size_t n = (size_t)x.slices * 2 * x.part_rows;
+  x.part_ml = align_up(n * c.D * 4);
+  x.records = x.part_ml + align_up(n * 8);
+  x.total = x.records + align_up(x.slices * sizeof(Record));
+  return x;
+}
+
+fa_status check_prefill(const fa_prefill_params* p, const fa_cache* c, const fa_pages* pages, CacheView& held, CacheView& cv,
+                        PageView& pv, Span& table) {
+  clear_error();
+  if (p == nullptr) { set_error("params is NULL"); return FA_ERR_INVALID_ARG; }
+  const fa_status st = check_paged(c, pages, held, cv, pv, table);
+  return st != FA_OK ? st : check_chunk(p, cv);
+}
+
+template <int D, bool Q4, bool PAGED>
+cudaError_t launch_prefill(const PrefillArgs& a, int slices, cudaStream_t st) {
+  constexpr int bytes = PrefillSmem<D>::kBytes;
+  static_assert(bytes <= 232448, "shared memory of a block");
+  auto kernel = prefill_kernel<D, Q4, PAGED>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared(kernel, bytes, allowed);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)slices, kThreads, bytes, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+fa_status check_chunk(const fa_prefill_params* p, const CacheView& cv) {
+  if (p->Hq < 1 || p->Hq > 65535) { set_error("Hq=%d outside [1, 65535]", p->Hq); return FA_ERR_INVALID_ARG; }
+  if (p->Hq % cv.Hkv != 0) { set_error("Hq=%d is not a multiple of Hkv=%d", p->Hq, cv.Hkv); return FA_ERR_INVALID_ARG; }
+  if (p->Sq < 0 || p->Sq > kMaxSeq) { set_error("Sq=%d outside [0, %d]", p->Sq, kMaxSeq); return FA_ERR_INVALID_ARG; }
+  if (p->window < 0) { set_error("window=%d must be >= 0 (0 = no window)", p->window); return FA_ERR_INVALID_ARG; }
+  if (p->layout != FA_LAYOUT_BHSD && p->layout != FA_LAYOUT_BSHD) { set_error("layout=%d invalid", p->layout); return FA_ERR_INVALID_ARG; }
+  if (!std::isfinite(p->scale)) { set_error("scale is not finite"); return FA_ERR_INVALID_ARG; }
+  if (p->reserved != 0) { set_error("reserved field must be 0"); return FA_ERR_INVALID_ARG; }
+  if (too_large(cv.B, p->Hq, p->Sq, cv.D)) { set_error("Q would hold more than 2^40 elements"); return FA_ERR_INVALID_ARG; }
+  if ((long long)cv.B * p->Hq * p->Sq > 0x7fffffffLL - kUnit) { set_error("too many query rows for one call"); return FA_ERR_UNSUPPORTED; }
+  return FA_OK;
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_prefill_workspace_size(const fa_prefill_params* p, const fa_cache* c, const fa_pages* pages) {
+  CacheView held, cv;
+  PageView pv;
+  Span table;
+  if (check_prefill(p, c, pages, held, cv, pv, table) != FA_OK || p->Sq == 0) return 0;
+  return plan_prefill(p, cv).total;
+}
+
+fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_cache* c, const fa_pages* pages,
+                     const int64_t* lengths, const int64_t* count, void* o, float* lse, void* ws, size_t ws_bytes,
+                     void* stream) {
+  CacheView held, cv;
+  PageView pv;
+  Span all[10];
+  fa_status st = check_prefill(p, c, pages, held, cv, pv, all[9]);
+  if (st != FA_OK) return st;
+  const size_t rows = (size_t)cv.B * p->Hq * p->Sq;
+  cache_spans(held, all);
+  all[4] = {q, rows * cv.D * 2, "q"};
+  Span* out = all + 5;
+  out[0] = {o, rows * cv.D * 2, "o"};
+  out[1] = {lse, rows * 4, "lse"};
+  all[7] = {lengths, lengths != nullptr ? (size_t)cv.B * 8 : 0, "lengths"};
+  all[8] = {count, count != nullptr ? (size_t)cv.B * 8 : 0, "count"};
+  if ((st = check_buffers(all, 5, out, 2)) != FA_OK) return st;
+  if ((uintptr_t)lengths % 8 != 0 || (uintptr_t)count % 8 != 0) {
+    set_error("lengths and count must be 8-byte aligned"); return FA_ERR_INVALID_ARG;
+  }
+  if ((st = check_apart(all + 7, 3, out, 2)) != FA_OK) return st;
+  if (p->Sq == 0) return FA_OK;
+  const PrefillPlan plan = plan_prefill(p, cv);
+  if ((st = check_ws(ws, ws_bytes, plan.total, all, 10)) != FA_OK) return st;
+  char* w = static_cast<char*>(ws);
+  PrefillArgs a{};
+  a.pages = pv;
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(w + plan.part_ml);
+  a.records = reinterpret_cast<Record*>(w + plan.records);
+  a.part_rows = plan.part_rows;
+  if ((a.status = device_status_ptr()) == nullptr) return cuda_status(cudaErrorUnknown, "status word");
+  a.sl2 = p->scale == 0.f ? 1.f : fminf(fabsf(p->scale) * kLog2e, FLT_MAX);
+  a.q_and = p->scale == 0.f ? 0u : 0xffffffffu;
+  a.q_xor = p->scale < 0.f ? 0x80008000u : 0u;
+  a.Hq = p->Hq;
+  a.Sq = p->Sq;
+  a.window = p->window < 2 * kMaxSeq ? p->window : 2 * kMaxSeq;
+  a.layout = p->layout;
+  a.G = p->Hq / cv.Hkv;
+  cudaStream_t cs = (cudaStream_t)stream;
+  const size_t per = (size_t)p->Hq * p->Sq;   // rows of a sequence
+  for (int b0 = 0; b0 < cv.B; b0 += kListed) {
+    a.c = cv;
+    a.c.B = cv.B - b0 < kListed ? cv.B - b0 : kListed;
+    a.q = static_cast<const __nv_bfloat16*>(q) + b0 * per * cv.D;
+    a.o = static_cast<__nv_bfloat16*>(o) + b0 * per * cv.D;
+    a.lse = lse + b0 * per;
+    a.lengths = lengths != nullptr ? lengths + b0 : nullptr;
+    a.count = count != nullptr ? count + b0 : nullptr;
+    if (pages != nullptr) {
+      a.pages.table = pv.table + b0 * pv.stride;
+    } else {   // sequence 0 of this launch
+      const size_t keys = (size_t)b0 * cv.Hkv * cv.S;
+      a.c.k_q = static_cast<uint8_t*>(cv.k_q) + keys * (cv.q4 ? cv.D / 2 : cv.D);
+      a.c.v_q = static_cast<uint8_t*>(cv.v_q) + keys * (cv.q4 ? cv.D / 2 : cv.D);
+      a.c.k_d = cv.k_d + keys * (cv.D / 32);
+      a.c.v_d = cv.v_d + keys * (cv.D / 32);
+    }
+    auto go = [&](auto dim, auto q4) {
+      constexpr int D = decltype(dim)::value;
+      constexpr bool Q4 = decltype(q4)::value;
+      return pages != nullptr ? launch_prefill<D, Q4, true>(a, plan.slices, cs) : launch_prefill<D, Q4, false>(a, plan.slices, cs);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    cudaError_t e;
+    if (cv.q4) e = cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
+    else e = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
+    if (e == cudaSuccess) {
+      cudaLaunchAttribute at{};
+      at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at.val.programmaticStreamSerializationAllowed = 1;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(4 * plan.slices);
+      cfg.blockDim = dim3(256);
+      cfg.dynamicSmemBytes = (plan.slices + 1) * sizeof(int);
+      cfg.stream = cs;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      e = cudaLaunchKernelEx(&cfg, cv.D == 64 ? prefill_join_kernel<64> : prefill_join_kernel<128>, a, plan.slices);
+      count_launches(1);
+    }
+    if (e != cudaSuccess) return cuda_status(e, "prefill launch");
+  }
+  return FA_OK;
+}
+
+}  // extern "C"

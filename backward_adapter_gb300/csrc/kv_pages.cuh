@@ -1,0 +1,24 @@
+// Where a key of a paged cache lies: key j of sequence b is row j % P of page table[b, j / P] of the pool (fa_pages).
+#pragma once
+
+#include <stdint.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// Row of the pool's planes that holds key j of head h of sequence b; -1, and a report, where the table names no page of the
+// pool. Keys j .. j + 15 of a j that is a multiple of 16 lie in one page, as P is one too: their rows follow each other.
+// j / P is a product: with n = j / 16 and e = magic P / 16 - 2^40, both below 2^20, n magic / 2^40 is n / (P / 16) and less
+// than n e / 2^40 / (P / 16) < 1 / (P / 16) more, which cannot reach the next whole number.
+__device__ __forceinline__ long long page_row(const PageView& p, int Hkv, int b, int h, unsigned j, unsigned* status) {
+  const unsigned m = (unsigned)(((unsigned long long)(j >> 4) * p.magic) >> 40);
+  const int page = __ldg(p.table + b * p.stride + m);
+  if ((unsigned)page >= p.pages) {
+    if (status != nullptr) atomicCAS(status, 0u, 0x40000000u | kSitePage);
+    return -1;
+  }
+  return ((long long)page * Hkv + h) * p.P + (j - m * p.P);
+}
+
+}  // namespace fa

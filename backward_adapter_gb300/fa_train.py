@@ -29,7 +29,9 @@ EXPORTED = ("fa_train_fwd_workspace_size", "fa_train_bwd_workspace_size", "fa_tr
             "fa_set_rows_backward", "fa_train_bwd_accum_rows", "fa_train_fwd_q8", "fa_train_bwd_q8",
             "fa_train_bwd_accum_q8", "fa_train_bwd_plan", "fa_train_fwd_plan", "fa_train_fwd_q4", "fa_train_bwd_q4",
             "fa_train_bwd_accum_q4", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
-            "fa_cache_write", "fa_cache_read", "fa_decode", "fa_decode_workspace_size")
+            "fa_cache_write", "fa_cache_read", "fa_decode", "fa_decode_workspace_size", "fa_cache_write_pages",
+            "fa_cache_read_pages", "fa_decode_pages", "fa_decode_pages_workspace_size", "fa_prefill",
+            "fa_prefill_workspace_size", "fa_cache_weights", "fa_cache_evict")
 FA_KERNEL_FWD, FA_KERNEL_BWD_MAIN, FA_KERNEL_BWD_DSUM, FA_KERNEL_BWD_DQ_CONVERT, FA_KERNEL_MASK_CLASSIFY = range(5)
 
 
@@ -74,6 +76,19 @@ class FaCache(ctypes.Structure):
 class FaDecodeParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("Hq", "Sq", "window", "layout")] + \
                [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class FaPages(ctypes.Structure):
+    """fa_pages: the page table of a cache."""
+    _fields_ = [("table", ctypes.c_void_p), ("stride", ctypes.c_int64), ("B", ctypes.c_int32), ("M", ctypes.c_int32)]
+
+
+class FaPrefillParams(ctypes.Structure):
+    _fields_ = list(FaDecodeParams._fields_)
+
+
+class FaEvictParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("keep", "sinks", "recent", "reserved")]
 
 
 class FaError(RuntimeError):
@@ -153,6 +168,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_decode_workspace_size.restype = sz
     lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fa_decode.restype = st
+    lib.fa_cache_write_pages.argtypes = [vp, vp, vp, vp, i32, i32, vp, i64, vp, vp]
+    lib.fa_cache_write_pages.restype = st
+    lib.fa_cache_read_pages.argtypes = [vp, vp, vp, i64, i32, i32, vp, vp, vp]
+    lib.fa_cache_read_pages.restype = st
+    lib.fa_decode_pages_workspace_size.argtypes = [vp, vp, vp]
+    lib.fa_decode_pages_workspace_size.restype = sz
+    lib.fa_decode_pages.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fa_decode_pages.restype = st
+    lib.fa_prefill_workspace_size.argtypes = [vp, vp, vp]
+    lib.fa_prefill_workspace_size.restype = sz
+    lib.fa_prefill.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fa_prefill.restype = st
+    lib.fa_cache_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
+    lib.fa_cache_weights.restype = st
+    lib.fa_cache_evict.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    lib.fa_cache_evict.restype = st
     lib.fa_train_bwd_plan.argtypes = [P, ctypes.POINTER(i32), i32, ctypes.POINTER(i32)]
     lib.fa_train_bwd_plan.restype = st
     lib.fa_train_fwd_plan.argtypes = [P, ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)]

@@ -389,6 +389,101 @@ FA_API fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_ca
                            void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * The pages of a cache. The planes are then a pool: fa_cache.B is its pages (up to 2^31 - 1 of them), fa_cache.S the keys of
+ * a page, a multiple of 16; key j of sequence b is row j % S of page table[b * stride + j / S]. A sequence has room for M * S
+ * keys, at most 2^24. Entries behind a sequence's keys are not looked at. What the device finds cannot be checked before the
+ * launch: keys of an entry outside [0, fa_cache.B) count as zeros and are not written, and 0x40000000 | 953 is recorded
+ * in the status word. A page may be in several places of the table as long as nothing is written to it there.
+ * Where an entry point takes pages, NULL stands for a cache without: then sequence b is fa_cache's b, with S keys.
+ */
+typedef struct fa_pages {
+  const int32_t* table; /* DEVICE pointer, 4-byte aligned */
+  int64_t stride;       /* entries from one sequence's to the next one's, at least M (not looked at when B is 1) */
+  int32_t B;            /* sequences, 1 .. 65535 */
+  int32_t M;            /* pages of a sequence, >= 1 */
+} fa_pages;
+
+/* fa_cache_write, fa_cache_read and fa_decode through a page table. Keys, lengths and rows are counted within a sequence.
+ * begins (int64 [B] in device memory, or NULL: `begin` for every sequence, which the call checks): the first key that is
+ * read of each sequence; a row outside its M * S keys is read as zeros, and 0x40000000 | 951 recorded. */
+FA_API fa_status fa_cache_write_pages(const fa_cache* c, const fa_pages* pages, const fa_view* k, const fa_view* v,
+                                      int32_t dtype, int32_t n_rows, const int64_t* begin, int64_t begin_all,
+                                      const int64_t* count, void* stream);
+FA_API fa_status fa_cache_read_pages(const fa_cache* c, const fa_pages* pages, const int64_t* begins, int64_t begin,
+                                     int32_t n_rows, int32_t dtype, const fa_view* k, const fa_view* v, void* stream);
+FA_API size_t fa_decode_pages_workspace_size(const fa_decode_params* p, const fa_cache* c, const fa_pages* pages);
+FA_API fa_status fa_decode_pages(const fa_decode_params* p, const void* q, const fa_cache* c, const fa_pages* pages,
+                                 const int64_t* lengths, void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of a chunk of new tokens of every sequence, a ragged batch, over its quantized cache, with or without pages: the
+ * serving form of fa_train_fwd_q8 / fa_train_fwd_q4 for any number of tokens (fa_decode is the one for up to 16). Of
+ * sequence b's Sq rows the first count[b] are tokens, the last of its lengths[b] keys their own: token i sits at position
+ * lengths[b] - count[b] + i and sees the keys j at or before it (with window w > 0 only those with position - j <= w). A token
+ * that sees no key gets O = 0 and LSE = 0. The rows from count[b] on are neither read nor written, keys at or past a
+ * sequence's length not read. As on the training path K and V are rounded to bf16 and the weights of V too; scores, statistics
+ * and sums are 32-bit. A scale of V that is not finite counts as 0.
+ */
+typedef struct fa_prefill_params {
+  int32_t Hq;        /* query heads, a multiple of the cache's Hkv, at most 65535 */
+  int32_t Sq;        /* rows of each sequence, 0 .. 2^24 (0 makes the call a no-op) */
+  int32_t window;    /* 0: none */
+  int32_t layout;    /* fa_layout of q and o (contiguous, bf16); lse is [B, Hq, Sq] */
+  float scale;       /* softmax scale, finite */
+  int32_t reserved;  /* must be 0 */
+} fa_prefill_params;
+
+/* Bytes of scratch fa_prefill needs (256-byte aligned; 0 when none). */
+FA_API size_t fa_prefill_workspace_size(const fa_prefill_params* p, const fa_cache* c, const fa_pages* pages);
+
+/*
+ * lengths, count: int64 [B] in device memory, or NULL: all keys that a sequence has room for, and all Sq rows. A length or a
+ * count outside [0, room] or [0, Sq] is taken as the nearer end, and 0x40000000 | 952 is recorded in the status word.
+ * o: bf16, lse: fp32.
+ */
+FA_API fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_cache* c, const fa_pages* pages,
+                            const int64_t* lengths, const int64_t* count, void* o, float* lse, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * The weight that every key got from the new tokens: with the tokens, positions and visible keys of fa_prefill, and lse as
+ * fa_prefill or fa_decode left it,
+ *     out[b, h, j] = weights[b, h, j] + sum over the query heads g of head h and the tokens i that see key j
+ *                                       of exp(scale <q_gi, k_j> - lse_gi)
+ * for every j below W (room for at least the sequences' lengths: a key at or past W is left out, and 0x40000000 | 952
+ * recorded). K is rounded to bf16; products, exponentials and sums are 32-bit, added in a fixed order. weights: fp32 [B, Hkv,
+ * W], or NULL: zeros; out: fp32 [B, Hkv, W], which may be weights. V's planes are not looked at.
+ */
+FA_API fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, const float* lse, const fa_cache* c,
+                                  const fa_pages* pages, const int64_t* lengths, const int64_t* count, const float* weights,
+                                  int64_t W, float* out, void* stream);
+
+/*
+ * Eviction: of every sequence with more than `keep` keys, `keep` of each head stay: those below `sinks`, the last `recent`, and
+ * of the others the ones with the largest weights (of equal ones the lowest index; a weight that is not a number is below
+ * every other). They become the keys 0 .. keep - 1 in the order they had, moved as they are stored; a sequence with no
+ * more than `keep` keeps all. Written are
+ *   the rows of the planes, to the same pages (to == NULL), or to those of the table `to` (for the same sequences, room for
+ *     `keep` keys), which then leaves the pages moved from as they are. A page written to is no page of the table read from,
+ *     unless it is in the same place of both, and in no other place of either;
+ *   kept int32 [B, Hkv, keep]: the index each key had, -1 behind the last one;
+ *   weights_out fp32 [B, Hkv, W]: the weights of the keys that stay, 0 behind them; may be weights;
+ *   new_lengths int64 [B]: min(length, keep).
+ * lengths: int64 [B]; one outside [0, room] or above W is taken as the nearer end, and 0x40000000 | 952 recorded.
+ * 0 <= sinks, recent; sinks + recent <= keep; 1 <= keep.
+ */
+typedef struct fa_evict_params {
+  int32_t keep;
+  int32_t sinks;
+  int32_t recent;
+  int32_t reserved;  /* must be 0 */
+} fa_evict_params;
+
+FA_API fa_status fa_cache_evict(const fa_evict_params* p, const fa_cache* c, const fa_pages* pages, const fa_pages* to,
+                                const float* weights, int64_t W, const int64_t* lengths, float* weights_out, int32_t* kept,
+                                int64_t* new_lengths, void* stream);
+
+/*
  * SET_ROWS backward: the gradient of the rows a chunk wrote into its cached K/V window
  * (llama.cpp PR #57, commit 2394a4c: the written source's gradient is the result's
  * gradient at the written rows; the destination, a cache, carries none). With the
@@ -482,7 +577,9 @@ FA_API fa_status fa_train_bwd_noalloc(const fa_params* p, const void* q, const v
  * `site` ran out of its time limit (the kernel then stopped early and its outputs
  * are invalid), 0x40000000 | site when a kernel met a device-side argument it
  * could not use (site 950: a row index of fa_set_rows_backward outside [0, S); 951: a row of
- * fa_cache_write outside the cache; 952: a length of fa_decode outside [0, S]).
+ * fa_cache_write outside the cache; 952: a length or count of fa_decode, fa_prefill,
+ * fa_cache_weights or fa_cache_evict out of its range; 953: an entry of a page table that is
+ * no page of the pool).
  * Synchronous (waits for the device to finish the copy). Returns FA_ERR_CUDA if
  * no device is usable.
  */
