@@ -12,9 +12,12 @@
 // row block over a long window and a batch of short ones fill the machine alike, without a choice of splits; a block
 // finds its place in the list from the lengths, on the device.
 //
-// A block of 16 warps: warps 4-7 read the packed bytes and write the bf16 operands (kv_tile.cuh), one tile of K and the V of
-// the tile before into each stage of a ring; one thread of warp 0 issues the MMAs (S_t = Q_t K^T, O_t += P_t V); warps 8-11
-// and 12-15 have a row of Q_0 and Q_1 for each thread: they load Q, turn scores into P in TMEM, and write O at the end.
+// A block of 20 warps: one thread of warp 0 issues the MMAs (S_t = Q_t K^T, O_t += P_t V) and walks the list for all; warps 4-11
+// read the packed bytes and write the bf16 operands (kv_tile.cuh), a run of 16 keys each, one tile of K and the V of the tile
+// before into each stage of a ring; warps 12-15 and 16-19 have a row of Q_0 and Q_1 for each thread: they load Q, turn scores
+// into P in TMEM, and write O at the end. They read the scores twice, for the maximum and for the exponentials, 32 at a
+// time: a row of 128 in registers leaves so few to the others that these spill, and what is spilled is in L2, as shared memory
+// takes what L1 has.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256, 256+D), O1 [256+D, 256+2D).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,13 +39,15 @@ using namespace tc;
 constexpr int kBM = 128;          // rows of a tile
 constexpr int kUnit = 2 * kBM;    // rows of a unit
 constexpr int kBN = kTileKeys;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kLoaders = 8;       // warps that make operands
 constexpr int kListed = 1024;     // sequences of a launch; more are more launches
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;   // log2 units: the reference follows the maximum when that has grown by more
-constexpr int kRegsIssue = 40, kRegsLoad = 104, kRegsSoftmax = 184;
-static_assert((kRegsIssue + kRegsLoad + 2 * kRegsSoftmax) * 128 <= kThreads * 128, "register split exceeds the launch's");
+// Registers of a thread: what 640 are launched with, and what warps 0-3, those that load and those that have rows make of it.
+constexpr int kRegsLaunch = 96, kRegsIssue = 80, kRegsLoad = 88, kRegsSoftmax = 112;
+static_assert(kRegsIssue + 2 * kRegsLoad + 2 * kRegsSoftmax <= 5 * kRegsLaunch, "register split exceeds the launch's");
 
 struct Record {   // a unit that slices c0 .. c1 share (c1 < 0: none)
   int b, h, unit, c0, c1, padding[3];
@@ -200,16 +205,17 @@ __device__ __forceinline__ void make_plan(const PrefillArgs& a, Plan& plan, int 
   __syncthreads();
 }
 
-// A slice's part of one unit.
+// A slice's part of one unit, as the roles of a block find it in shared memory: the issuing thread walks the list and writes
+// the parts one after the other into a ring, four ahead, so that nobody else has the walk's state in registers.
 struct Piece {
   int b, h, unit;
-  int tile, tiles;    // the first one, and how many
-  int rows;           // live rows of the unit
-  bool starts, ends;  // the unit's first, last tile is among them
-  Seq s;
+  int tile, tiles;      // the first one, and how many; none: the list has ended
+  int rows;             // live rows of the unit
+  int len, n;           // the sequence's keys and tokens
+  int starts, ends;     // the unit's first, last tile is among them
 };
+constexpr int kPieces = 8;
 
-// The pieces of a slice, one after the other; every role walks them for itself.
 struct Walk {
   const PrefillArgs& a;
   const Plan& plan;
@@ -217,21 +223,25 @@ struct Walk {
   long long left;
   __device__ __forceinline__ Walk(const PrefillArgs& a_, const Plan& p)
       : a(a_), plan(p), b(p.b), h(p.h), unit(p.unit), off(p.off), left(p.tiles) {}
-  __device__ __forceinline__ bool next(Piece& x) {
-    if (left <= 0) return false;
-    x.s = plan.seq[b];
-    const Tiles t = tiles_of(a, x.s, unit);
+  __device__ __forceinline__ void next(Piece& x) {
+    x.tiles = 0;
+    if (left <= 0) return;
+    const Seq s = plan.seq[b];
+    const Tiles t = tiles_of(a, s, unit);
     x.b = b;
     x.h = h;
     x.unit = unit;
     x.tile = t.begin + off;
-    x.tiles = (int)min((long long)(t.end - x.tile), left);
-    x.rows = min(x.s.n * a.G - unit * kUnit, kUnit);
+    x.rows = min(s.n * a.G - unit * kUnit, kUnit);
+    x.len = s.len;
+    x.n = s.n;
+    const int tiles = (int)min((long long)(t.end - t.begin - off), left);
     x.starts = off == 0;
-    x.ends = x.tile + x.tiles == t.end;
-    left -= x.tiles;
+    x.ends = off + tiles == t.end - t.begin;
+    x.tiles = tiles;
+    left -= tiles;
     off = 0;
-    if (++unit == units_of(a, x.s)) {
+    if (++unit == units_of(a, s)) {
       unit = 0;
       if (++h == a.c.Hkv) {
         h = 0;
@@ -239,7 +249,6 @@ struct Walk {
         while (b < a.c.B && plan.seq[b].n == 0);
       }
     }
-    return true;
   }
 };
 
@@ -264,7 +273,8 @@ struct PrefillSmem {
   static constexpr int kStages = D == 128 ? 2 : 4;   // a stage: the V of one tile of keys and the K of the next
   static constexpr int kKVOff = 2 * kTileBytes;
   static constexpr int kBarOff = kKVOff + 2 * kStages * kTileBytes;
-  static constexpr int kPlanOff = kBarOff + 256;
+  static constexpr int kPieceOff = kBarOff + 320;
+  static constexpr int kPlanOff = kPieceOff + 384;
   static constexpr int kBytes = kPlanOff + (int)sizeof(Plan) + 1024;
 };
 
@@ -281,9 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   uint64_t* bar_o = bars + 6;                     // [2]: the last product of tile t done
   uint64_t* bar_full = bars + 8;                  // [kStages]: stage written
   uint64_t* bar_empty = bar_full + L::kStages;    // [kStages]: its MMAs done
-  uint64_t* bar_done = bar_empty + L::kStages;
+  uint64_t* bar_piece = bar_empty + L::kStages;   // [kPieces]: part of a unit described
+  uint64_t* bar_past = bar_piece + kPieces;       // [kPieces]: nobody looks at it any more
+  uint64_t* bar_done = bar_past + kPieces;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(8 * (8 + 2 * L::kStages + 2 * kPieces + 1) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
+  Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPieceOff);
   Plan& plan = *reinterpret_cast<Plan*>(smem + L::kPlanOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -296,8 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(&bar_o[t], 1);
     }
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&bar_full[i], 4);
+      mbar_init(&bar_full[i], kLoaders);
       mbar_init(&bar_empty[i], 1);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&bar_piece[i], 1);
+      mbar_init(&bar_past[i], kLoaders + 8);   // the warps that load and that have rows
     }
     mbar_init(bar_done, 1);
     *abort_flag = 0;
@@ -309,38 +327,60 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // part i of the slice is there (all lanes of a warp have one answer)
+  auto part_there = [&](int i) { return mbar_wait<true>(&bar_piece[i % kPieces], (i / kPieces) & 1, abort_flag, a.status, 1009); };
 
   if (warp < 4) {
     regs_dec<kRegsIssue>();
     if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------------- MMA issuer
+      // ---------------------------------------------------------------- the list, and the MMAs
+      Walk walk(a, plan);
+      int listed = 0;
+      bool listed_all = false, ok = true;
+      auto list_part = [&] {   // one more
+        if (listed_all || !ok) return;
+        if (listed >= kPieces && !(ok = mbar_wait<true>(&bar_past[listed % kPieces], (listed / kPieces - 1) & 1, abort_flag, a.status, 1010))) return;
+        Piece& x = pieces[listed % kPieces];
+        walk.next(x);
+        listed_all = x.tiles == 0;
+        mbar_arrive(&bar_piece[listed % kPieces]);
+        ++listed;
+      };
+      // Some parts ahead: a warp that loads looks at the tile behind the one that it completes the stage of, which may be
+      // another part's; it would wait for that part, and this thread for the stage.
+      for (int i = 0; i < 4; ++i) list_part();
       const uint32_t idesc_qk = idesc_bf16_f32(kBM, kBN, 0, 0);
       const uint32_t idesc_pv = idesc_bf16_f32(kBM, D, 0, 1);
+      // The descriptors' low words are made anew each time: held in registers, as the compiler would, they spill.
+      auto fresh = [](uint32_t x) {
+        asm volatile("" : "+r"(x));
+        return x;
+      };
+      constexpr uint32_t kHighQk = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;   // smem_desc_sw128's high words
+      auto desc = [](uint32_t low, uint32_t bytes) { return (uint64_t)kHighQk << 32 | (low + (bytes >> 4)); };
       auto issue_pv = [&](int t, int slot, bool first) {
-        const uint64_t dv0 = smem_desc_sw128(sKV + slot * L::kTileBytes, L::kBoxBytes, 1024);
-        const uint32_t d_tmem = tmem + 256 + t * D, a_tmem = tmem + t * 128;
+        const uint32_t v = fresh(((sKV + slot * L::kTileBytes) >> 4 & 0x3fffu) | (uint32_t)(L::kBoxBytes >> 4) << 16);
+        const uint32_t d_tmem = fresh(tmem + 256 + t * D), a_tmem = fresh(tmem + t * 128);
 #pragma unroll
-        for (int k = 0; k < kBN / 16; ++k)
-          mma_ts(d_tmem, a_tmem + k * 8, desc_add(dv0, k * 2048), idesc_pv, (!first || k > 0) ? 1u : 0u);
+        for (int k = 0; k < kBN / 16; ++k) mma_ts(d_tmem, a_tmem + k * 8, desc(v, k * 2048), idesc_pv, (!first || k > 0) ? 1u : 0u);
       };
       auto issue_s = [&](int t, int slot) {
-        const uint64_t dq0 = smem_desc_sw128(sQ + t * L::kTileBytes, 16, 1024);
-        const uint64_t dk0 = smem_desc_sw128(sKV + slot * L::kTileBytes, 16, 1024);
-        const uint32_t d_tmem = tmem + t * 128;
+        const uint32_t q = fresh(((sQ + t * L::kTileBytes) >> 4 & 0x3fffu) | 1u << 16);
+        const uint32_t k0 = fresh(((sKV + slot * L::kTileBytes) >> 4 & 0x3fffu) | 1u << 16);
+        const uint32_t d_tmem = fresh(tmem + t * 128);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
-          mma_ss(d_tmem, desc_add(dq0, off), desc_add(dk0, off), idesc_qk, k > 0 ? 1u : 0u);
+          mma_ss(d_tmem, desc(q, off), desc(k0, off), idesc_qk, k > 0 ? 1u : 0u);
         }
         mma_commit(&bar_s[t]);
       };
       // The pieces' tiles are one stream: stage i holds the K of its tile i and the V of tile i - 1. Within a piece a tile of
       // rows gets its P V of the last tile of keys and then its next S, one tile of rows after the other; where a piece ends
       // both products come first.
-      bool ok = true;
       int stage = 0;                    // tiles of the stream so far
       int scores[2] = {0, 0};           // of bar_s and bar_p: completions so far
-      int pieces[2] = {0, 0};           // of bar_q
+      int loads[2] = {0, 0};            // of bar_q
       int pending = 0;                  // tiles of rows of the last tile of keys whose product is to come
       bool pending_first = false, pending_last = false;   // it is its piece's first, last
       auto product = [&](int t, int slot) -> bool {
@@ -350,23 +390,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (pending_last) mma_commit(&bar_o[t]);
         return true;
       };
-      Walk walk(a, plan);
-      Piece x;
-      while (ok && walk.next(x)) {
-        const int live = x.rows > kBM ? 2 : 1;
-        for (int j = 0; ok && j < x.tiles; ++j) {
+      for (int i = 0; ok; ++i) {
+        const int live = pieces[i % kPieces].rows > kBM ? 2 : 1, tiles = pieces[i % kPieces].tiles;   // listed by this thread
+        if (tiles == 0) break;
+        for (int j = 0; ok && j < tiles; ++j) {
           const int sb = stage % L::kStages;
           if (!(ok = mbar_wait<true>(&bar_full[sb], (stage / L::kStages) & 1, abort_flag, a.status, 1002))) break;
           tc_fence_after();
           if (j == 0) {
             for (int t = 0; ok && t < pending; ++t) ok = product(t, 2 * sb + 1);
             for (int t = 0; ok && t < live; ++t) {
-              if (!(ok = mbar_wait<true>(&bar_q[t], pieces[t] & 1, abort_flag, a.status, 1003))) break;
+              if (!(ok = mbar_wait<true>(&bar_q[t], loads[t] & 1, abort_flag, a.status, 1003))) break;
               tc_fence_after();
-              ++pieces[t];
+              ++loads[t];
               issue_s(t, 2 * sb);
               ++scores[t];
             }
+            list_part();
           } else {
             for (int t = 0; ok && t < live; ++t) {
               if (!(ok = product(t, 2 * sb + 1))) break;
@@ -378,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           mma_commit(&bar_empty[sb]);
           pending = live;
           pending_first = j == 0;
-          pending_last = j == x.tiles - 1;
+          pending_last = j == tiles - 1;
           ++stage;
         }
       }
@@ -392,64 +432,102 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mma_commit(bar_done);
       mbar_wait<true>(bar_done, 0, nullptr, a.status, 1005);
     }
-  } else if (warp < 8) {
+  } else if (warp < 4 + kLoaders) {
     regs_dec<kRegsLoad>();
     // ------------------------------------------------------------------ K and V: from bytes to operands
-    const int w = warp - 4;
-    Walk walk(a, plan);
-    Piece x;
-    x.tiles = 0;
-    int j = 0;
-    // where this warp's rows of the next tile of the stream lie; false behind the last
-    auto next_rows = [&](TileRows& t) -> bool {
-      if (j == x.tiles) {
-        if (!walk.next(x)) return false;
-        j = 0;
+    const int run = warp - 4;
+    int part = 0, left = 0, key = 0, b = 0, h = 0, len = 0;   // of the part: tiles to come, and this warp's first key of the next
+    int entries = 0, ahead = 0;   // pages: lane i has the table's entry for this run of the i-th tile of 32, counted down
+    // The next tile of the stream, its page's number on its way; false behind the last.
+    auto next_tile = [&]() -> bool {
+      if (left == 0) {
+        if (!__all_sync(0xffffffffu, part_there(part))) return false;
+        const Piece& x = pieces[part % kPieces];
+        left = x.tiles;
+        key = x.tile * kBN + kRun * run - kBN;
+        b = x.b;
+        h = x.h;
+        len = x.len;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
+        ++part;
+        if (left == 0) return false;
+        ahead = 0;
       }
-      t = tile_rows<PAGED>(a.c, a.pages, x.b, x.h, (x.tile + j) * kBN + 32 * w, x.s.len, a.status);
-      ++j;
+      key += kBN;
+      --left;
+      if constexpr (PAGED) {
+        if (--ahead < 0) {
+          ahead = 31;
+          const int mine = key + lane * kBN;
+          if (mine < len && lane <= left) entries = __ldg(a.pages.table + b * a.pages.stride + page_index(a.pages, mine));
+        }
+      }
       return true;
     };
-    TileRows now, then;
-    TileBytes<D, Q4> k, v;
-    bool has_k = next_rows(now), has_v = false;
-    if (has_k) k.load(a.c.k_q, a.c.k_d, now);
+    // Where its run lies.
+    auto row_of_tile = [&]() -> long long {
+      if constexpr (!PAGED) return ((long long)b * a.c.Hkv + h) * a.c.S + key;
+      const int page = __shfl_sync(0xffffffffu, entries, 31 - ahead);
+      return key < len ? row_in_page(a.pages, page, a.c.Hkv, h, key, lane == 0 ? a.status : nullptr) : -1;
+    };
+    RunBytes<D, Q4> k, v;
+    long long row = 0;
+    int keys = 0;
+    bool has_k = next_tile(), has_v = false;
+    if (has_k) {
+      row = row_of_tile();
+      keys = len - key;
+      k.load(a.c.k_q, a.c.k_d, row, keys);
+    }
     for (int stage = 0; has_k || has_v; ++stage) {
-      // K of the tile `now` is on its way, and V of the one before it if there is one
+      // K of a tile is on its way, and V of the one before it if there is one
       const int sb = stage % L::kStages;
-      const bool more = has_k && next_rows(then);
+      const bool more = has_k && next_tile();
       if (stage >= L::kStages &&
           !__all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[sb], (stage / L::kStages - 1) & 1, abort_flag, a.status, 1006)))
         break;
       const uint32_t at = sKV + 2 * sb * L::kTileBytes;
+      long long next_row = 0;
+      int next_keys = 0;
       if (has_k) {
-        k.template store<false>(at, w);
-        if (more) k.load(a.c.k_q, a.c.k_d, then);
+        k.template store<false>(at, run);
+        if (more) {
+          next_row = row_of_tile();
+          next_keys = len - key;
+          k.load(a.c.k_q, a.c.k_d, next_row, next_keys);
+        }
       }
-      if (has_v) v.template store<true>(at + L::kTileBytes, w);
+      if (has_v) v.template store<true>(at + L::kTileBytes, run);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_full[sb]);
-      if (has_k) v.load(a.c.v_q, a.c.v_d, now);
+      if (has_k) v.load(a.c.v_q, a.c.v_d, row, keys);
       has_v = has_k;
       has_k = more;
-      now = then;
+      row = next_row;
+      keys = next_keys;
     }
   } else {
     regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax, a row for each thread
-    const int t = (warp - 8) / 4, wq = warp & 3;
+    const int t = (warp - 4 - kLoaders) / 4, wq = warp & 3;
     const int r = wq * 32 + lane;   // row of the tile
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * D + lane_off;
     const uint32_t my_q = sQ + t * L::kTileBytes + r * 128;
     const float sl2 = a.sl2;
-    // the next piece with live rows in this tile
-    Walk walk(a, plan);
-    auto next_live = [&](Piece& x) -> bool {
-      while (walk.next(x))
-        if (x.rows > t * kBM) return true;
-      return false;
+    // the next part with live rows in this tile of rows, from part `i` on; false behind the last
+    auto next_live = [&](int& i) -> bool {
+      for (;; ++i) {
+        if (!__all_sync(0xffffffffu, part_there(i))) return false;
+        const Piece& x = pieces[i % kPieces];
+        const int rows = x.rows, tiles = x.tiles;
+        if (tiles != 0 && rows > t * kBM) return true;
+        if (tiles == 0) return false;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_past[i % kPieces]);
+      }
     };
     auto load_q = [&](const Piece& x) {
       const int row = x.unit * kUnit + t * kBM + r;
@@ -470,52 +548,48 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (lane == 0) mbar_arrive(&bar_q[t]);
     };
     bool ok = true;
-    int tiles = 0, pieces = 0;   // completions of bar_s and bar_o so far
-    Piece x, ahead;
-    bool has = next_live(x);
-    if (has) load_q(x);
+    int scored = 0, finished = 0;   // completions of bar_s and bar_o so far
+    int part = 0;
+    bool has = next_live(part);
+    if (has) load_q(pieces[part % kPieces]);
     while (has && ok) {
-      const int row = x.unit * kUnit + t * kBM + r;
-      const bool live = t * kBM + r < x.rows;
-      const RowPlace place = place_of(a, x.b, x.h, live ? row : 0);
-      // the keys this row sees: [key_lo, key_hi]
-      const int key_hi = live ? min(x.s.len - x.s.n + place.token, x.s.len - 1) : -1;
+      int key0, key_hi, left;   // of the next tile: its first key, and the last one that this row sees
+      {
+        const Piece& x = pieces[part % kPieces];
+        const bool live = t * kBM + r < x.rows;
+        key0 = x.tile * kBN;
+        key_hi = live ? x.len - x.n + (x.unit * kUnit + t * kBM + r) / a.G : -1;
+        left = x.tiles;
+      }
       const int key_lo = a.window > 0 ? key_hi - a.window : 0;
       float m = -CUDART_INF_F, l = 0.f;
-      for (int j = 0; j < x.tiles; ++j) {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[t], tiles & 1, abort_flag, a.status, 1007)))) break;
-        ++tiles;
+      bool first = true;
+      for (; left > 0; --left, key0 += kBN, first = false) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[t], scored & 1, abort_flag, a.status, 1007)))) break;
+        ++scored;
         tc_fence_after();
-        const int key0 = (x.tile + j) * kBN;
         const int lo = min(max(key_lo - key0, 0), kBN), lim = max(min(key_hi - key0, kBN - 1), -1);
         const bool full = lo == 0 && lim == kBN - 1;
-        float s[kBN];
-        auto masked = [&](const uint32_t (&raw)[32], int c0) {
+        // scores 32 c .. of the row, hidden ones -inf
+        auto masked = [&](uint32_t (&x)[32], int c) {
+          if (full) return;
+          const int from = max(lo - 32 * c, 0), to = min(lim - 32 * c + 1, 32);
+          const uint32_t seen = to <= from ? 0u : (uint32_t)(((1ull << to) - 1ull) & ~((1ull << from) - 1ull));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[c0 + e] = __uint_as_float(raw[e]);
-          if (!full) {
-            const int from = max(lo - c0, 0), to = min(lim - c0 + 1, 32);
-            const uint32_t seen = to <= from ? 0u : (uint32_t)(((1ull << to) - 1ull) & ~((1ull << from) - 1ull));
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[c0 + e] = (seen >> e) & 1u ? s[c0 + e] : -CUDART_INF_F;
-          }
+          for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? x[e] : 0xff800000u;
         };
-        {
-          uint32_t raw[2][32];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tmem_ld32(tS + half * 64, raw[0]);
-            tmem_ld32(tS + half * 64 + 32, raw[1]);
-            tmem_wait_ld();
-            reg_fence(raw[0]);
-            reg_fence(raw[1]);
-            masked(raw[0], half * 64);
-            masked(raw[1], half * 64 + 32);
-          }
-        }
+        uint32_t raw[2][32];
         float top4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+        tmem_ld32(tS, raw[0]);
 #pragma unroll
-        for (int e = 0; e < kBN; e += 2) top4[(e >> 1) & 3] = max3f(top4[(e >> 1) & 3], s[e], s[e + 1]);
+        for (int c = 0; c < kBN / 32; ++c) {   // the next ones on their way meanwhile; at the end the first again
+          tmem_wait_ld();
+          reg_fence(raw[c & 1]);
+          tmem_ld32(tS + (c + 1) % 4 * 32, raw[(c + 1) & 1]);
+          masked(raw[c & 1], c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top4[(e >> 1) & 3] = max3f(top4[(e >> 1) & 3], __uint_as_float(raw[c & 1][e]), __uint_as_float(raw[c & 1][e + 1]));
+        }
         const float top_s = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
         const float m_new = fmaxf(m, top_s * sl2);
         const bool rescale = m_new > m + kRescale;   // false while nothing is seen
@@ -525,24 +599,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const uint64_t sl2_2 = f32x2(sl2, sl2), negm_2 = f32x2(-m_sub, -m_sub);
         uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll
-        for (int cch = 0; cch < kBN / 32; ++cch) {
+        for (int c = 0; c < kBN / 32; ++c) {
+          tmem_wait_ld();
+          reg_fence(raw[c & 1]);
+          if (c + 1 < kBN / 32) tmem_ld32(tS + (c + 1) * 32, raw[(c + 1) & 1]);
+          masked(raw[c & 1], c);
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float t0, t1;
-            f32x2_split(fma_f32x2(f32x2(s[cch * 32 + 2 * e], s[cch * 32 + 2 * e + 1]), sl2_2, negm_2), t0, t1);
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[c & 1][2 * e]), __uint_as_float(raw[c & 1][2 * e + 1])), sl2_2, negm_2), t0, t1);
             const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
             sum2[e & 1] = add_f32x2(sum2[e & 1], f32x2(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
           }
-          tmem_st16(tS + cch * 16, pk);
+          tmem_st16(tS + c * 16, pk);   // over scores that have been read
         }
         float s0, s1, s2, s3;
         f32x2_split(sum2[0], s0, s1);
         f32x2_split(sum2[1], s2, s3);
         l = l * alpha + ((s0 + s1) + (s2 + s3));
         m = m_use;
-        if (__any_sync(0xffffffffu, rescale) && j > 0) {   // alpha is 1 for rows that keep their reference
+        if (__any_sync(0xffffffffu, rescale) && !first) {   // alpha is 1 for rows that keep their reference
           // O holds the products of the tiles before: their MMAs ended before these scores did
 #pragma unroll
           for (int cch = 0; cch < D / 32; ++cch) {
@@ -561,18 +639,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (lane == 0) mbar_arrive(&bar_p[t]);
       }
       if (!ok) break;
-      // The scores of the piece's last tile are there, so nothing reads its Q any more: the next one's takes its place.
-      const bool next = next_live(ahead);
-      if (next) load_q(ahead);
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_o[t], pieces & 1, abort_flag, a.status, 1008)))) break;
-      ++pieces;
+      // The scores of the part's last tile are there, so nothing reads its Q any more: the next one's takes its place.
+      int next = part + 1;
+      const bool more = next_live(next);
+      if (more) load_q(pieces[next % kPieces]);
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_o[t], finished & 1, abort_flag, a.status, 1008)))) break;
+      ++finished;
       tc_fence_after();
+      const Piece& x = pieces[part % kPieces];
+      const bool live = t * kBM + r < x.rows, whole = x.starts && x.ends;
+      const RowPlace place = place_of(a, x.b, x.h, live ? x.unit * kUnit + t * kBM + r : 0);
       const bool alive = l != 0.f;   // a sum that is no number is one
-      const bool whole = x.starts && x.ends;
       const float inv = !whole ? 1.f : alive ? 1.f / l : 0.f;
       uint4* out = reinterpret_cast<uint4*>(a.o + place.at);
-      const size_t part = ((size_t)blockIdx.x * 2 + (x.starts ? 1 : 0)) * a.part_rows + t * kBM + r;
-      float4* left = reinterpret_cast<float4*>(a.part_o + part * D);
+      const size_t slot = ((size_t)blockIdx.x * 2 + (x.starts ? 1 : 0)) * a.part_rows + t * kBM + r;
+      float4* left_o = reinterpret_cast<float4*>(a.part_o + slot * D);
 #pragma unroll
       for (int cch = 0; cch < D / 32; ++cch) {
         uint32_t ov[32];
@@ -590,16 +671,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                           pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) left[cch * 8 + e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+          for (int e = 0; e < 8; ++e) left_o[cch * 8 + e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
         }
       }
-      tc_fence_before();   // these reads of O come before the next piece's product, which waits for bar_p
+      tc_fence_before();   // these reads of O come before the next part's product, which waits for bar_p
       if (live) {
         if (whole) a.lse[place.log] = alive ? (m + log2f(l)) * kLn2 : 0.f;
-        else a.part_ml[part] = make_float2(alive ? m : -CUDART_INF_F, l);
+        else a.part_ml[slot] = make_float2(alive ? m : -CUDART_INF_F, l);
       }
-      x = ahead;
-      has = next;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
+      part = next;
+      has = more;
     }
   }
 
@@ -753,7 +836,13 @@ cudaError_t launch_prefill(const PrefillArgs& a, int slices, cudaStream_t st) {
   static_assert(bytes <= 232448, "shared memory of a block");
   auto kernel = prefill_kernel<D, Q4, PAGED>;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_shared(kernel, bytes, allowed);
+  if (allowed.load(std::memory_order_acquire) == 0) {   // the split of registers holds for what the kernel is launched with
+    cudaFuncAttributes at;
+    const cudaError_t got = cudaFuncGetAttributes(&at, kernel);
+    if (got != cudaSuccess) return got;
+    if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+  }
+  const cudaError_t e = allow_shared(kernel, bytes, allowed);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)slices, kThreads, bytes, st>>>(a);
   count_launches(1);

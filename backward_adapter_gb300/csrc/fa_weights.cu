@@ -4,8 +4,8 @@
 // key j. With K as the left operand the products S^T = K Q^T have a key for each lane of TMEM and a row for each column, so
 // that a thread adds up a key's weights along its lane, in registers: no atomics, no second pass, a fixed order.
 //
-// A block has one tile of 128 keys of a sequence's head: warps 0-3 make its bf16 operand from the packed bytes (kv_tile.cuh)
-// and then own a key for each thread; warps 4-7 bring the rows, 128 (or 16, where there are no more) at a time, and one
+// A block has one tile of 128 keys of a sequence's head: warps 0-7 make its bf16 operand from the packed bytes (kv_tile.cuh);
+// then warps 0-3 own a key for each thread, warps 4-7 bring the rows, 128 (or 16, where there are no more) at a time, and one
 // thread of warp 8 issues the MMAs; the products are in two buffers, so that they and the exponentials overlap.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     if (threadIdx.x == 0) {
-      mbar_init(bar_k, 4);
+      mbar_init(bar_k, 8);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bar_q[i], 4);
         mbar_init(&bar_s[i], 1);
@@ -105,15 +105,18 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
     const uint32_t tmem = *tmem_slot;
     const int tiles = (rows + NQ - 1) / NQ;
 
+    if (warp < 8) {   // this warp's run of K
+      const int run = key0 + kRun * warp;
+      long long row = -1;
+      if (run < len) row = PAGED ? page_row(a.pages, a.c.Hkv, b, h, run, a.status) : (long long)bh * a.c.S + run;
+      RunBytes<D, Q4> k;
+      k.load(a.c.k_q, a.c.k_d, row, min(len - run, kRun));
+      k.template store<false>(sK, warp);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_k);
+    }
     if (warp < 4) {
-      {
-        TileBytes<D, Q4> k;
-        k.load(a.c.k_q, a.c.k_d, tile_rows<PAGED>(a.c, a.pages, b, h, key0 + 32 * warp, len, a.status));
-        k.template store<false>(sK, warp);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_k);
-      }
       const int key = key0 + 32 * warp + lane;
       const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16);
       const uint64_t sl2 = f32x2(a.sl2, a.sl2);

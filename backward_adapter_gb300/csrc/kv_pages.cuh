@@ -11,14 +11,19 @@ namespace fa {
 // pool. Keys j .. j + 15 of a j that is a multiple of 16 lie in one page, as P is one too: their rows follow each other.
 // j / P is a product: with n = j / 16 and e = magic P / 16 - 2^40, both below 2^20, n magic / 2^40 is n / (P / 16) and less
 // than n e / 2^40 / (P / 16) < 1 / (P / 16) more, which cannot reach the next whole number.
-__device__ __forceinline__ long long page_row(const PageView& p, int Hkv, int b, int h, unsigned j, unsigned* status) {
-  const unsigned m = (unsigned)(((unsigned long long)(j >> 4) * p.magic) >> 40);
-  const int page = __ldg(p.table + b * p.stride + m);
+__device__ __forceinline__ unsigned page_index(const PageView& p, unsigned j) {
+  return (unsigned)(((unsigned long long)(j >> 4) * p.magic) >> 40);
+}
+// ... with the table's entry for key j at hand.
+__device__ __forceinline__ long long row_in_page(const PageView& p, int page, int Hkv, int h, unsigned j, unsigned* status) {
   if ((unsigned)page >= p.pages) {
     if (status != nullptr) atomicCAS(status, 0u, 0x40000000u | kSitePage);
     return -1;
   }
-  return ((long long)page * Hkv + h) * p.P + (j - m * p.P);
+  return ((long long)page * Hkv + h) * p.P + (j - page_index(p, j) * p.P);
+}
+__device__ __forceinline__ long long page_row(const PageView& p, int Hkv, int b, int h, unsigned j, unsigned* status) {
+  return row_in_page(p, __ldg(p.table + b * p.stride + page_index(p, j)), Hkv, h, j, status);
 }
 
 }  // namespace fa

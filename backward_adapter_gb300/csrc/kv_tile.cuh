@@ -1,5 +1,5 @@
-// A tile of 128 keys of a quantized plane as the bf16 operand of tcgen05.mma: four warps read 32 rows each, 16 bytes a lane
-// and load, and write them in the 128-byte-swizzled layout that TMA would have written (64-feature boxes of 128 rows x 128
+// A tile of 128 keys of a quantized plane as the bf16 operand of tcgen05.mma: eight warps read a run of 16 rows each, 16 bytes a
+// lane and load, and write them in the 128-byte-swizzled layout that TMA would have written (64-feature boxes of 128 rows x 128
 // bytes, 16-byte chunk c of row r at chunk c ^ (r & 7)). Eight neighbouring lanes hold eight rows, so that their stores meet
 // no bank twice.
 //
@@ -18,29 +18,7 @@
 namespace fa {
 
 constexpr int kTileKeys = 128;
-
-// What a warp reads for its rows 32 w .. 32 w + 31 of a tile: where the two runs of 16 rows begin in a plane (-1: no page),
-// and how many of the 32 keys there are.
-struct TileRows {
-  long long row0, row1;
-  int keys;
-};
-
-// Of sequence b's head h, keys key0 .. key0 + 31, `len` keys in all.
-template <bool PAGED>
-__device__ __forceinline__ TileRows tile_rows(const CacheView& c, const PageView& pages, int b, int h, int key0, int len,
-                                              unsigned* status) {
-  TileRows t;
-  t.keys = min(max(len - key0, 0), 32);
-  if constexpr (PAGED) {
-    t.row0 = t.keys > 0 ? page_row(pages, c.Hkv, b, h, key0, status) : -1;
-    t.row1 = t.keys > 16 ? page_row(pages, c.Hkv, b, h, key0 + 16, status) : -1;
-  } else {
-    t.row0 = ((long long)b * c.Hkv + h) * c.S + key0;
-    t.row1 = t.row0 + 16;
-  }
-  return t;
-}
+constexpr int kRun = 16;   // keys of a run: they lie in one page
 
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t x, uint32_t y) {
   uint32_t z;
@@ -58,52 +36,56 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t x, uint32_t y, uint32_t 
   return z;
 }
 
-// The bytes of a warp's rows, in registers.
+// The bytes of a run, in a warp's registers.
 template <int D, bool Q4>
-struct TileBytes {
-  static constexpr int ROW = Q4 ? D / 2 : D;   // bytes of a row
-  static constexpr int N = ROW / 16;           // pieces of 16 bytes in a row, and loads of a lane
-  static constexpr int BOX = 128 * 128;        // bytes of a 64-feature box of the tile
+struct RunBytes {
+  static constexpr int ROW = Q4 ? D / 2 : D;    // bytes of a row
+  static constexpr int PIECES = ROW / 16;
+  static constexpr int N = kRun * PIECES / 32;  // loads of a lane
+  static constexpr int NB = D / 32;
+  static constexpr int BOX = 128 * 128;         // bytes of a 64-feature box of the tile
   uint32_t w[N][4];
   uint16_t d[N];
 
-  // Load i: the lane's row among the 32, and which piece of it.
+  // Load i: the lane's row of the run, and which piece of it.
   __device__ static __forceinline__ int row_of(int i, int lane) {
-    return N == 2 ? 16 * i + 8 * (lane >> 4) + (lane & 7) : N == 4 ? 8 * i + (lane & 7) : 8 * (i >> 1) + (lane & 7);
+    return PIECES == 2 ? 8 * (lane >> 4) + (lane & 7) : PIECES == 4 ? 8 * i + (lane & 7) : 8 * (i >> 1) + (lane & 7);
   }
   __device__ static __forceinline__ int piece_of(int i, int lane) {
-    return N == 2 ? (lane >> 3) & 1 : N == 4 ? lane >> 3 : 4 * (i & 1) + (lane >> 3);
+    return PIECES == 2 ? (lane >> 3) & 1 : PIECES == 4 ? lane >> 3 : 4 * (i & 1) + (lane >> 3);
   }
 
-  // Kept in this place among the waits; rows that are not there are zeros, and not read.
-  __device__ __forceinline__ void load(const void* values, const uint16_t* scales, const TileRows& t) {
+  // The first `keys` rows from row `first` of a plane on; the others, and all where that is negative, are zeros, and not
+  // read. The loads stay in this place among the waits.
+  __device__ __forceinline__ void load(const void* values, const uint16_t* scales, long long first, int keys) {
     const int lane = threadIdx.x & 31;
+    const int at = row_of(0, lane) * ROW + 16 * piece_of(0, lane), scale_at = row_of(0, lane) * NB + piece_of(0, lane) / (Q4 ? 1 : 2);
+    const uint8_t* v = static_cast<const uint8_t*>(values) + first * ROW + at;
+    const uint16_t* s = scales + first * NB + scale_at;
+    if (first < 0) keys = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int row = row_of(i, lane), piece = piece_of(i, lane);
-      const long long first = (i < N / 2 ? t.row0 : t.row1 - 16);   // of the second run as if the first had been before it
-      const bool on = row < t.keys && (i < N / 2 ? t.row0 : t.row1) >= 0;
+      const int rows = PIECES == 4 ? 8 * i : PIECES == 8 ? 8 * (i >> 1) : 0, more = PIECES == 8 ? 4 * (i & 1) : 0;   // of the first load
       w[i][0] = w[i][1] = w[i][2] = w[i][3] = Q4 ? 0x88888888u : 0u;
       d[i] = 0;
-      if (on) {
-        const uint8_t* src = static_cast<const uint8_t*>(values) + (first + row) * ROW + 16 * piece;
-        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]) : "l"(src));
-        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(d[i]) : "l"(scales + (first + row) * (D / 32) + (Q4 ? piece : piece / 2)));
+      if (row_of(i, lane) < keys) {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]) : "l"(v + rows * ROW + 16 * more));
+        asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(d[i]) : "l"(s + rows * NB + more / 2));
       }
     }
   }
 
-  // Into rows 32 w .. of the tile at `tile` (shared memory). FINITE: a scale that is not finite counts as 0.
+  // Into run `run` of the tile at `tile` (shared memory). FINITE: a scale that is not finite counts as 0.
   template <bool FINITE>
-  __device__ __forceinline__ void store(uint32_t tile, int warp) const {
+  __device__ __forceinline__ void store(uint32_t tile, int run) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int piece = piece_of(i, lane);
       float df = __half2float(__ushort_as_half(d[i]));
       if (FINITE && !(fabsf(df) <= 65504.f)) df = 0.f;
-      const uint32_t at = tile + (32 * warp + row_of(i, lane)) * 128;
+      const uint32_t at = tile + (kRun * run + row_of(i, lane)) * 128;
       auto put = [&](int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t e) {
         tc::st_shared_v4(at + (chunk >> 3) * BOX + (((chunk & 7) ^ (lane & 7)) << 4), a, b, c, e);
       };
