@@ -3,8 +3,10 @@
 //
 // Mathematics. The G = Hq / Hkv query heads of a key/value head and its tokens are the rows of one matrix, token by token, so
 // that a tile of 128 rows covers few positions and skips what lies behind the last. With K and V rounded to bf16:
-// S = scale Q K^T, hidden pairs -inf, O = softmax(S) V by tiles of 128 keys with a running maximum (followed only when it
-// grows by 2^8) and sum, in 32 bits; P is rounded to bf16 for its product.
+// S = scale Q K^T, hidden pairs -inf, O = softmax(S) V by tiles of 128 keys with a running reference and sum, in 32 bits; P is
+// rounded to bf16 for its product, which has fp32's range: so the reference is any number near the maximum, is set by a unit's
+// first 32 scores, and follows only when the maximum is more than 2^30 above it. Weights, sums and O hold that without loss (O
+// stays below 2^30 * 2^24 keys * 2^23), and scores are read once, with nothing to wait for between their maximum and their exponentials.
 //
 // Split. A unit is 256 rows (two tiles) of one sequence's key/value head. The tiles of 128 keys of all units form one list,
 // cut into equal slices, one for each SM: the end of one unit, whole units, the beginning of another. A unit that several
@@ -15,9 +17,8 @@
 // A block of 20 warps: one thread of warp 0 issues the MMAs (S_t = Q_t K^T, O_t += P_t V) and walks the list for all; warps 4-11
 // read the packed bytes and write the bf16 operands (kv_tile.cuh), a run of 16 keys each, one tile of K and the V of the tile
 // before into each stage of a ring; warps 12-15 and 16-19 have a row of Q_0 and Q_1 for each thread: they load Q, turn scores
-// into P in TMEM, and write O at the end. They read the scores twice, for the maximum and for the exponentials, 32 at a
-// time: a row of 128 in registers leaves so few to the others that these spill, and what is spilled is in L2, as shared memory
-// takes what L1 has.
+// into P in TMEM, and write O at the end. They hold 32 scores at a time and the next 32 on their way: a row of 128 in registers
+// leaves so few to the others that these spill, and what is spilled is in L2, as shared memory takes what L1 has.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256, 256+D), O1 [256+D, 256+2D).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -44,7 +45,7 @@ constexpr int kLoaders = 8;       // warps that make operands
 constexpr int kListed = 1024;     // sequences of a launch; more are more launches
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescale = 8.f;   // log2 units: the reference follows the maximum when that has grown by more
+constexpr float kRescale = 30.f;   // log2 units: the reference follows the maximum when that is more above it
 // Registers of a thread: what 640 are launched with, and what warps 0-3, those that load and those that have rows make of it.
 constexpr int kRegsLaunch = 96, kRegsIssue = 80, kRegsLoad = 88, kRegsSoftmax = 112;
 static_assert(kRegsIssue + 2 * kRegsLoad + 2 * kRegsSoftmax <= 5 * kRegsLaunch, "register split exceeds the launch's");
@@ -578,37 +579,62 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? x[e] : 0xff800000u;
         };
+        const uint64_t sl2_2 = f32x2(sl2, sl2);
+        uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         uint32_t raw[2][32];
-        float top4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
         tmem_ld32(tS, raw[0]);
 #pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) {   // the next ones on their way meanwhile; at the end the first again
-          tmem_wait_ld();
-          reg_fence(raw[c & 1]);
-          tmem_ld32(tS + (c + 1) % 4 * 32, raw[(c + 1) & 1]);
-          masked(raw[c & 1], c);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) top4[(e >> 1) & 3] = max3f(top4[(e >> 1) & 3], __uint_as_float(raw[c & 1][e]), __uint_as_float(raw[c & 1][e + 1]));
-        }
-        const float top_s = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-        const float m_new = fmaxf(m, top_s * sl2);
-        const bool rescale = m_new > m + kRescale;   // false while nothing is seen
-        const float m_use = rescale ? m_new : m;
-        const float alpha = rescale ? ex2_approx(m - m_new) : 1.f;
-        const float m_sub = m_use == -CUDART_INF_F ? 0.f : m_use;
-        const uint64_t sl2_2 = f32x2(sl2, sl2), negm_2 = f32x2(-m_sub, -m_sub);
-        uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-#pragma unroll
         for (int c = 0; c < kBN / 32; ++c) {
+          uint32_t (&x)[32] = raw[c & 1];
           tmem_wait_ld();
-          reg_fence(raw[c & 1]);
+          reg_fence(x);
+          masked(x, c);
+          float top2[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top2[(e >> 1) & 1] = max3f(top2[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          const float top = fmaxf(top2[0], top2[1]) * sl2;
+          if (__any_sync(0xffffffffu, top > m + kRescale)) {   // rare, but for a unit's first scores
+            // a whole number: what there is changes by a power of two, so nothing is rounded again
+            const float m_new = top > m + kRescale ? ceilf(top) : m;
+            const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
+            m = m_new;
+            l *= alpha;
+            const uint64_t alpha_2 = f32x2(alpha, alpha);
+            sum2[0] = mul_f32x2(sum2[0], alpha_2);
+            sum2[1] = mul_f32x2(sum2[1], alpha_2);
+            const uint32_t alpha_16 = pack_bf16x2(alpha, alpha);
+#pragma unroll
+            for (int d = 0; d < c; ++d) {   // weights of this tile that are stored already
+              uint32_t pk[16];
+              tmem_wait_st();
+              tmem_ld16(tS + d * 16, pk);
+              tmem_wait_ld();
+              reg_fence16(pk);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = mul_bf16x2(pk[e], alpha_16);
+              tmem_st16(tS + d * 16, pk);
+            }
+            if (!first) {   // O holds the products of the tiles before: their MMAs ended before these scores did
+#pragma unroll 1
+              for (int d = 0; d < D / 16; ++d) {
+                uint32_t ov[16];
+                tmem_ld16(tO + d * 16, ov);
+                tmem_wait_ld();
+                reg_fence16(ov);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                tmem_st16(tO + d * 16, ov);
+              }
+            }
+          }
           if (c + 1 < kBN / 32) tmem_ld32(tS + (c + 1) * 32, raw[(c + 1) & 1]);
-          masked(raw[c & 1], c);
+          const float less = m == -CUDART_INF_F ? 0.f : -m;
+          const uint64_t less_2 = f32x2(less, less);
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float t0, t1;
-            f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[c & 1][2 * e]), __uint_as_float(raw[c & 1][2 * e + 1])), sl2_2, negm_2), t0, t1);
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2_2, less_2), t0, t1);
             const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
             sum2[e & 1] = add_f32x2(sum2[e & 1], f32x2(p0, p1));
             pk[e] = pack_bf16x2(p0, p1);
@@ -618,21 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         float s0, s1, s2, s3;
         f32x2_split(sum2[0], s0, s1);
         f32x2_split(sum2[1], s2, s3);
-        l = l * alpha + ((s0 + s1) + (s2 + s3));
-        m = m_use;
-        if (__any_sync(0xffffffffu, rescale) && !first) {   // alpha is 1 for rows that keep their reference
-          // O holds the products of the tiles before: their MMAs ended before these scores did
-#pragma unroll
-          for (int cch = 0; cch < D / 32; ++cch) {
-            uint32_t ov[32];
-            tmem_ld32(tO + cch * 32, ov);
-            tmem_wait_ld();
-            reg_fence(ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st32(tO + cch * 32, ov);
-          }
-        }
+        l += (s0 + s1) + (s2 + s3);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
