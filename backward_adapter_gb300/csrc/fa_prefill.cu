@@ -47,7 +47,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 30.f;   // log2 units: the reference follows the maximum when that is more above it
 // Registers of a thread: what 640 are launched with, and what warps 0-3, those that load and those that have rows make of it.
-constexpr int kRegsLaunch = 96, kRegsIssue = 80, kRegsLoad = 88, kRegsSoftmax = 112;
+constexpr int kRegsLaunch = 96, kRegsIssue = 48, kRegsLoad = 88, kRegsSoftmax = 128;
 static_assert(kRegsIssue + 2 * kRegsLoad + 2 * kRegsSoftmax <= 5 * kRegsLaunch, "register split exceeds the launch's");
 
 struct Record {   // a unit that slices c0 .. c1 share (c1 < 0: none)
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   static_assert(8 * (8 + 2 * L::kStages + 2 * kPieces + 1) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPieceOff);
   Plan& plan = *reinterpret_cast<Plan*>(smem + L::kPlanOff);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   let_next_kernel_start();
   if (threadIdx.x == 0) {
@@ -327,96 +327,108 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);   // one number to the compiler too
   // part i of the slice is there (all lanes of a warp have one answer)
   auto part_there = [&](int i) { return mbar_wait<true>(&bar_piece[i % kPieces], (i / kPieces) & 1, abort_flag, a.status, 1009); };
 
   if (warp < 4) {
     regs_dec<kRegsIssue>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------------------------- the list, and the MMAs
+      // All lanes go this way together, and the first issues: descriptors then are the warp's, in uniform registers, where
+      // the issue of one lane alone takes each word there first (and is what the tensor cores wait for).
+      const uint32_t lead = lane == 0 ? 1u : 0u;
       Walk walk(a, plan);
       int listed = 0;
       bool listed_all = false, ok = true;
       auto list_part = [&] {   // one more
         if (listed_all || !ok) return;
-        if (listed >= kPieces && !(ok = mbar_wait<true>(&bar_past[listed % kPieces], (listed / kPieces - 1) & 1, abort_flag, a.status, 1010))) return;
-        Piece& x = pieces[listed % kPieces];
+        if (listed >= kPieces &&
+            !(ok = mbar_wait_warp(&bar_past[listed % kPieces], (listed / kPieces - 1) & 1, abort_flag, a.status, 1010)))
+          return;
+        Piece x;
         walk.next(x);
-        listed_all = x.tiles == 0;
-        mbar_arrive(&bar_piece[listed % kPieces]);
+        if (lane == 0) {
+          pieces[listed % kPieces] = x;
+          mbar_arrive(&bar_piece[listed % kPieces]);
+        }
+        __syncwarp();
+        listed_all = __shfl_sync(0xffffffffu, x.tiles, 0) == 0;
         ++listed;
       };
       // Some parts ahead: a warp that loads looks at the tile behind the one that it completes the stage of, which may be
-      // another part's; it would wait for that part, and this thread for the stage.
+      // another part's; it would wait for that part, and this warp for the stage.
       for (int i = 0; i < 4; ++i) list_part();
       const uint32_t idesc_qk = idesc_bf16_f32(kBM, kBN, 0, 0);
       const uint32_t idesc_pv = idesc_bf16_f32(kBM, D, 0, 1);
-      // The descriptors' low words are made anew each time: held in registers, as the compiler would, they spill.
-      auto fresh = [](uint32_t x) {
-        asm volatile("" : "+r"(x));
-        return x;
-      };
-      constexpr uint32_t kHighQk = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;   // smem_desc_sw128's high words
-      auto desc = [](uint32_t low, uint32_t bytes) { return (uint64_t)kHighQk << 32 | (low + (bytes >> 4)); };
+      const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sKV, 16, 1024), dv = smem_desc_sw128(sKV, L::kBoxBytes, 1024);
       auto issue_pv = [&](int t, int slot, bool first) {
-        const uint32_t v = fresh(((sKV + slot * L::kTileBytes) >> 4 & 0x3fffu) | (uint32_t)(L::kBoxBytes >> 4) << 16);
-        const uint32_t d_tmem = fresh(tmem + 256 + t * D), a_tmem = fresh(tmem + t * 128);
+        const uint64_t v = desc_add(dv, slot * L::kTileBytes);
 #pragma unroll
-        for (int k = 0; k < kBN / 16; ++k) mma_ts(d_tmem, a_tmem + k * 8, desc(v, k * 2048), idesc_pv, (!first || k > 0) ? 1u : 0u);
+        for (int k = 0; k < kBN / 16; ++k)
+          mma_ts_if(lead, tmem + 256 + t * D, tmem + t * 128 + k * 8, desc_add(v, k * 2048), idesc_pv,
+                    (!first || k > 0) ? 1u : 0u);
       };
       auto issue_s = [&](int t, int slot) {
-        const uint32_t q = fresh(((sQ + t * L::kTileBytes) >> 4 & 0x3fffu) | 1u << 16);
-        const uint32_t k0 = fresh(((sKV + slot * L::kTileBytes) >> 4 & 0x3fffu) | 1u << 16);
-        const uint32_t d_tmem = fresh(tmem + t * 128);
+        const uint64_t q = desc_add(dq, t * L::kTileBytes), k0 = desc_add(dk, slot * L::kTileBytes);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
-          mma_ss(d_tmem, desc(q, off), desc(k0, off), idesc_qk, k > 0 ? 1u : 0u);
+          mma_ss_if(lead, tmem + t * 128, desc_add(q, off), desc_add(k0, off), idesc_qk, k > 0 ? 1u : 0u);
         }
-        mma_commit(&bar_s[t]);
+        mma_commit_if(lead, &bar_s[t]);
       };
-      // The pieces' tiles are one stream: stage i holds the K of its tile i and the V of tile i - 1. Within a piece a tile of
-      // rows gets its P V of the last tile of keys and then its next S, one tile of rows after the other; where a piece ends
+      auto wait = [&](uint64_t* bar, int phase, unsigned site) {
+        return mbar_wait_warp(bar, phase & 1, abort_flag, a.status, site);
+      };
+      // The parts' tiles are one stream: stage i holds the K of its tile i and the V of tile i - 1. Within a part a tile of
+      // rows gets its P V of the last tile of keys and then its next S, one tile of rows after the other; where a part ends
       // both products come first.
       int stage = 0;                    // tiles of the stream so far
-      int scores[2] = {0, 0};           // of bar_s and bar_p: completions so far
-      int loads[2] = {0, 0};            // of bar_q
+      int scores0 = 0, scores1 = 0;     // of bar_s and bar_p: completions so far
+      int loads0 = 0, loads1 = 0;       // of bar_q
       int pending = 0;                  // tiles of rows of the last tile of keys whose product is to come
-      bool pending_first = false, pending_last = false;   // it is its piece's first, last
+      bool pending_first = false, pending_last = false;   // it is its part's first, last
       auto product = [&](int t, int slot) -> bool {
-        if (!mbar_wait<true>(&bar_p[t], (scores[t] - 1) & 1, abort_flag, a.status, 1001)) return false;
+        if (!wait(&bar_p[t], (t ? scores1 : scores0) - 1, 1001)) return false;
         tc_fence_after();
         issue_pv(t, slot, pending_first);
-        if (pending_last) mma_commit(&bar_o[t]);
+        if (pending_last) mma_commit_if(lead, &bar_o[t]);
+        return true;
+      };
+      auto scores = [&](int t, int slot) {
+        issue_s(t, slot);
+        if (t) ++scores1;
+        else ++scores0;
+      };
+      auto first_scores = [&](int t, int slot) -> bool {
+        if (!wait(&bar_q[t], t ? loads1 : loads0, 1003)) return false;
+        tc_fence_after();
+        if (t) ++loads1;
+        else ++loads0;
+        scores(t, slot);
         return true;
       };
       for (int i = 0; ok; ++i) {
-        const int live = pieces[i % kPieces].rows > kBM ? 2 : 1, tiles = pieces[i % kPieces].tiles;   // listed by this thread
+        const int live = __shfl_sync(0xffffffffu, pieces[i % kPieces].rows, 0) > kBM ? 2 : 1;   // listed by this warp
+        const int tiles = __shfl_sync(0xffffffffu, pieces[i % kPieces].tiles, 0);
         if (tiles == 0) break;
         for (int j = 0; ok && j < tiles; ++j) {
           const int sb = stage % L::kStages;
-          if (!(ok = mbar_wait<true>(&bar_full[sb], (stage / L::kStages) & 1, abort_flag, a.status, 1002))) break;
+          if (!(ok = wait(&bar_full[sb], stage / L::kStages, 1002))) break;
           tc_fence_after();
           if (j == 0) {
-            for (int t = 0; ok && t < pending; ++t) ok = product(t, 2 * sb + 1);
-            for (int t = 0; ok && t < live; ++t) {
-              if (!(ok = mbar_wait<true>(&bar_q[t], loads[t] & 1, abort_flag, a.status, 1003))) break;
-              tc_fence_after();
-              ++loads[t];
-              issue_s(t, 2 * sb);
-              ++scores[t];
-            }
+            if (pending > 0) ok = product(0, 2 * sb + 1);
+            if (ok && pending > 1) ok = product(1, 2 * sb + 1);
+            if (ok) ok = first_scores(0, 2 * sb);
+            if (ok && live > 1) ok = first_scores(1, 2 * sb);
             list_part();
           } else {
-            for (int t = 0; ok && t < live; ++t) {
-              if (!(ok = product(t, 2 * sb + 1))) break;
-              issue_s(t, 2 * sb);
-              ++scores[t];
-            }
+            if ((ok = product(0, 2 * sb + 1))) scores(0, 2 * sb);
+            if (ok && live > 1 && (ok = product(1, 2 * sb + 1))) scores(1, 2 * sb);
           }
           if (!ok) break;
-          mma_commit(&bar_empty[sb]);
+          mma_commit_if(lead, &bar_empty[sb]);
           pending = live;
           pending_first = j == 0;
           pending_last = j == tiles - 1;
@@ -425,13 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (ok && pending > 0) {   // the stream's last stage holds only V
         const int sb = stage % L::kStages;
-        ok = mbar_wait<true>(&bar_full[sb], (stage / L::kStages) & 1, abort_flag, a.status, 1004);
+        ok = wait(&bar_full[sb], stage / L::kStages, 1004);
         tc_fence_after();
-        for (int t = 0; ok && t < pending; ++t) ok = product(t, 2 * sb + 1);
+        if (ok) ok = product(0, 2 * sb + 1);
+        if (ok && pending > 1) ok = product(1, 2 * sb + 1);
       }
-      // every MMA of this thread is complete before TMEM is given back
-      mma_commit(bar_done);
+      // every MMA of this warp is complete before TMEM is given back
+      mma_commit_if(lead, bar_done);
       mbar_wait<true>(bar_done, 0, nullptr, a.status, 1005);
+      __syncwarp();
     }
   } else if (warp < 4 + kLoaders) {
     regs_dec<kRegsLoad>();
