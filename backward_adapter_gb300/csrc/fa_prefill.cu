@@ -14,11 +14,12 @@
 // row block over a long window and a batch of short ones fill the machine alike, without a choice of splits; a block
 // finds its place in the list from the lengths, on the device.
 //
-// A block of 20 warps: one thread of warp 0 issues the MMAs (S_t = Q_t K^T, O_t += P_t V) and walks the list for all; warps 4-11
-// read the packed bytes and write the bf16 operands (kv_tile.cuh), a run of 16 keys each, one tile of K and the V of the tile
-// before into each stage of a ring; warps 12-15 and 16-19 have a row of Q_0 and Q_1 for each thread: they load Q, turn scores
-// into P in TMEM, and write O at the end. They hold 32 scores at a time and the next 32 on their way: a row of 128 in registers
-// leaves so few to the others that these spill, and what is spilled is in L2, as shared memory takes what L1 has.
+// A block of 20 warps. Warp 0 issues the MMAs (S_t = Q_t K^T, O_t += P_t V) and walks the list for all. Eight warps read the
+// packed bytes and write the bf16 operands (kv_tile.cuh), a run of 16 keys each, one tile of K and the V of the tile before into
+// each stage of a ring; none of them is on the scheduler of warp 0, which the tensor cores wait for. Warps 4 and 8 bring Q_0 and
+// Q_1, as soon as the last product with the ones before is done. Warps 12-15 and 16-19 have a row of Q_0 and Q_1 for each thread:
+// they turn scores into P in TMEM, and write O at the end. They hold 32 scores at a time and the next 32 on their way: a row of
+// 128 in registers leaves so few to the others that these spill, and what is spilled is in L2, as shared memory takes what L1 has.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256, 256+D), O1 [256+D, 256+2D).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,12 +47,12 @@ constexpr int kListed = 1024;     // sequences of a launch; more are more launch
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 30.f;   // log2 units: the reference follows the maximum when that is more above it
-// Registers of a thread: what 640 are launched with, and what warps 0-3, those that load and those that have rows make of it.
-constexpr int kRegsLaunch = 96, kRegsIssue = 48, kRegsLoad = 88, kRegsSoftmax = 128;
-static_assert(kRegsIssue + 2 * kRegsLoad + 2 * kRegsSoftmax <= 5 * kRegsLaunch, "register split exceeds the launch's");
+// Registers of a thread: what 640 are launched with, and what warps 0-11 and those that have rows make of it.
+constexpr int kRegsLaunch = 96, kRegsLoad = 80, kRegsSoftmax = 120;
+static_assert(3 * kRegsLoad + 2 * kRegsSoftmax <= 5 * kRegsLaunch, "register split exceeds the launch's");
 
 struct Record {   // a unit that slices c0 .. c1 share (c1 < 0: none)
-  int b, h, unit, c0, c1, padding[3];
+  int b, h, unit, rows, c0, c1, padding[2];
 };
 
 struct PrefillArgs {
@@ -158,7 +159,7 @@ __device__ __forceinline__ void make_plan(const PrefillArgs& a, Plan& plan, int 
   __syncwarp();
   const Slices cut(all, slices);
   const long long at = cut.begin(slice), tiles = cut.begin(slice + 1) - at;
-  Record rec{0, 0, 0, 0, -1, {0, 0, 0}};
+  Record rec{0, 0, 0, 0, 0, -1, {0, 0}};
   if (tiles > 0) {
     int b = 0;   // the last sequence that begins at or before the slice; one without tiles begins where the next does
     for (int b0 = 0; b0 < a.c.B; b0 += 32) b += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.c.B && plan.before[b0 + lane] <= at));
@@ -197,7 +198,8 @@ __device__ __forceinline__ void make_plan(const PrefillArgs& a, Plan& plan, int 
       plan.unit = unit;
       plan.off = inside;
     }
-    if (inside > 0 && cut.begin(slice - 1) <= at - inside) rec = Record{b, h, unit, slice - 1, cut.of(at - inside + length - 1), {0, 0, 0}};
+    if (inside > 0 && cut.begin(slice - 1) <= at - inside)
+      rec = Record{b, h, unit, min(s.n * a.G - unit * kUnit, kUnit), slice - 1, cut.of(at - inside + length - 1), {0, 0}};
   }
   if (lane == 0) {
     plan.tiles = tiles;
@@ -294,10 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   uint64_t* bar_empty = bar_full + L::kStages;    // [kStages]: its MMAs done
   uint64_t* bar_piece = bar_empty + L::kStages;   // [kPieces]: part of a unit described
   uint64_t* bar_past = bar_piece + kPieces;       // [kPieces]: nobody looks at it any more
-  uint64_t* bar_done = bar_past + kPieces;
+  uint64_t* bar_read = bar_past + kPieces;        // [2]: the last product with tile t of a unit's Q done
+  uint64_t* bar_done = bar_read + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (8 + 2 * L::kStages + 2 * kPieces + 1) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
+  static_assert(8 * (8 + 2 * L::kStages + 2 * kPieces + 3) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPieceOff);
   Plan& plan = *reinterpret_cast<Plan*>(smem + L::kPlanOff);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -305,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   let_next_kernel_start();
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bar_q[t], 4);
+      mbar_init(&bar_q[t], 1);
+      mbar_init(&bar_read[t], 1);
       mbar_init(&bar_s[t], 1);
       mbar_init(&bar_p[t], 4);
       mbar_init(&bar_o[t], 1);
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&bar_piece[i], 1);
-      mbar_init(&bar_past[i], kLoaders + 8);   // the warps that load and that have rows
+      mbar_init(&bar_past[i], kLoaders + 2 + 8);   // the warps that load and that have rows
     }
     mbar_init(bar_done, 1);
     *abort_flag = 0;
@@ -331,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   // part i of the slice is there (all lanes of a warp have one answer)
   auto part_there = [&](int i) { return mbar_wait<true>(&bar_piece[i % kPieces], (i / kPieces) & 1, abort_flag, a.status, 1009); };
 
-  if (warp < 4) {
-    regs_dec<kRegsIssue>();
+  if (warp < 12) {
+    regs_dec<kRegsLoad>();
     if (warp == 0) {
       // ---------------------------------------------------------------- the list, and the MMAs
       // All lanes go this way together, and the first issues: descriptors then are the warp's, in uniform registers, where
@@ -396,17 +400,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (pending_last) mma_commit_if(lead, &bar_o[t]);
         return true;
       };
-      auto scores = [&](int t, int slot) {
+      auto scores = [&](int t, int slot, bool last) {
         issue_s(t, slot);
+        if (last) mma_commit_if(lead, &bar_read[t]);
         if (t) ++scores1;
         else ++scores0;
       };
-      auto first_scores = [&](int t, int slot) -> bool {
+      auto first_scores = [&](int t, int slot, bool last) -> bool {
         if (!wait(&bar_q[t], t ? loads1 : loads0, 1003)) return false;
         tc_fence_after();
         if (t) ++loads1;
         else ++loads0;
-        scores(t, slot);
+        scores(t, slot, last);
         return true;
       };
       for (int i = 0; ok; ++i) {
@@ -417,21 +422,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const int sb = stage % L::kStages;
           if (!(ok = wait(&bar_full[sb], stage / L::kStages, 1002))) break;
           tc_fence_after();
+          const bool last = j == tiles - 1;
           if (j == 0) {
             if (pending > 0) ok = product(0, 2 * sb + 1);
             if (ok && pending > 1) ok = product(1, 2 * sb + 1);
-            if (ok) ok = first_scores(0, 2 * sb);
-            if (ok && live > 1) ok = first_scores(1, 2 * sb);
+            if (ok) ok = first_scores(0, 2 * sb, last);
+            if (ok && live > 1) ok = first_scores(1, 2 * sb, last);
             list_part();
           } else {
-            if ((ok = product(0, 2 * sb + 1))) scores(0, 2 * sb);
-            if (ok && live > 1 && (ok = product(1, 2 * sb + 1))) scores(1, 2 * sb);
+            if ((ok = product(0, 2 * sb + 1))) scores(0, 2 * sb, last);
+            if (ok && live > 1 && (ok = product(1, 2 * sb + 1))) scores(1, 2 * sb, last);
           }
           if (!ok) break;
           mma_commit_if(lead, &bar_empty[sb]);
           pending = live;
           pending_first = j == 0;
-          pending_last = j == tiles - 1;
+          pending_last = last;
           ++stage;
         }
       }
@@ -447,8 +453,49 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_wait<true>(bar_done, 0, nullptr, a.status, 1005);
       __syncwarp();
     }
-  } else if (warp < 4 + kLoaders) {
-    regs_dec<kRegsLoad>();
+    else if (warp == 1 || warp == 2) {
+      // ---------------------------------------------------------------- Q
+      const int t = warp - 1;
+      constexpr int CHUNKS = D / 8, STEP = 32 / CHUNKS;   // 16-byte chunks of a row, rows of a step
+      const int chunk = lane % CHUNKS;
+      const long long by_token = (long long)(a.layout ? a.Hq : 1) * D, by_head = (long long)(a.layout ? 1 : a.Sq) * D;
+      const uint32_t box = sQ + t * L::kTileBytes + (chunk >> 3) * L::kBoxBytes;
+      int loads = 0;
+      for (int part = 0;; ++part) {
+        if (!__all_sync(0xffffffffu, part_there(part))) break;
+        const Piece x = pieces[part % kPieces];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
+        if (x.tiles == 0) break;
+        const int rows = x.rows - t * kBM;
+        if (rows <= 0) continue;
+        if (loads > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bar_read[t], (loads - 1) & 1, abort_flag, a.status, 1011))) break;
+        ++loads;
+        int r = lane / CHUNKS;
+        int token = (x.unit * kUnit + t * kBM + r) / a.G, head = (x.unit * kUnit + t * kBM + r) % a.G;
+        const __nv_bfloat16* first = a.q + ((size_t)x.b * a.Hq * a.Sq + (a.layout ? (size_t)x.h * a.G : (size_t)x.h * a.G * a.Sq)) * D + 8 * chunk;
+#pragma unroll 4
+        for (; r < kBM; r += STEP) {   // rows behind the last are zeros
+          const bool on = r < rows;
+          const __nv_bfloat16* src = on ? first + token * by_token + head * by_head : a.q;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)), "l"(src), "r"(on ? 16 : 0)
+                       : "memory");
+          for (head += STEP; head >= a.G; head -= a.G) ++token;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (a.q_xor != 0u || a.q_and != 0xffffffffu) {   // a scale that is not positive: this lane's own chunks again
+          for (r = lane / CHUNKS; r < kBM; r += STEP) {
+            const uint32_t at = box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+            const float4 f = ld_shared_f4(at);
+            st_shared_v4(at, (__float_as_uint(f.x) & a.q_and) ^ a.q_xor, (__float_as_uint(f.y) & a.q_and) ^ a.q_xor,
+                         (__float_as_uint(f.z) & a.q_and) ^ a.q_xor, (__float_as_uint(f.w) & a.q_and) ^ a.q_xor);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_q[t]);
+      }
+    } else if (warp >= 4) {
     // ------------------------------------------------------------------ K and V: from bytes to operands
     const int run = warp - 4;
     int part = 0, left = 0, key = 0, b = 0, h = 0, len = 0;   // of the part: tiles to come, and this warp's first key of the next
@@ -523,14 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       row = next_row;
       keys = next_keys;
     }
+    }
   } else {
     regs_inc<kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax, a row for each thread
-    const int t = (warp - 4 - kLoaders) / 4, wq = warp & 3;
+    const int t = (warp - 12) / 4, wq = warp & 3;
     const int r = wq * 32 + lane;   // row of the tile
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * D + lane_off;
-    const uint32_t my_q = sQ + t * L::kTileBytes + r * 128;
     const float sl2 = a.sl2;
     // the next part with live rows in this tile of rows, from part `i` on; false behind the last
     auto next_live = [&](int& i) -> bool {
@@ -544,30 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (lane == 0) mbar_arrive(&bar_past[i % kPieces]);
       }
     };
-    auto load_q = [&](const Piece& x) {
-      const int row = x.unit * kUnit + t * kBM + r;
-      const bool on = t * kBM + r < x.rows;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (on ? place_of(a, x.b, x.h, row).at : 0));
-#pragma unroll
-      for (int c0 = 0; c0 < D / 8; c0 += 8) {
-        uint4 u[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) u[c] = on ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          st_shared_v4(my_q + (c0 / 8) * L::kBoxBytes + ((c ^ (r & 7)) << 4), (u[c].x & a.q_and) ^ a.q_xor,
-                       (u[c].y & a.q_and) ^ a.q_xor, (u[c].z & a.q_and) ^ a.q_xor, (u[c].w & a.q_and) ^ a.q_xor);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_q[t]);
-    };
     bool ok = true;
     int scored = 0, finished = 0;   // completions of bar_s and bar_o so far
     int part = 0;
-    bool has = next_live(part);
-    if (has) load_q(pieces[part % kPieces]);
-    while (has && ok) {
+    for (; next_live(part); ++part) {
       int key0, key_hi, left;   // of the next tile: its first key, and the last one that this row sees
       {
         const Piece& x = pieces[part % kPieces];
@@ -665,10 +692,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (lane == 0) mbar_arrive(&bar_p[t]);
       }
       if (!ok) break;
-      // The scores of the part's last tile are there, so nothing reads its Q any more: the next one's takes its place.
-      int next = part + 1;
-      const bool more = next_live(next);
-      if (more) load_q(pieces[next % kPieces]);
       if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_o[t], finished & 1, abort_flag, a.status, 1008)))) break;
       ++finished;
       tc_fence_after();
@@ -707,8 +730,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
-      part = next;
-      has = more;
     }
   }
 
@@ -724,22 +745,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 // of few parts have a warp for each row, of many a block; the rows of all units are one list over the blocks.
 template <int D>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a, int slices) {
-  constexpr int F = D / 32, AHEAD = 8, kMany = 24;   // parts
+  constexpr int F = D / 32, kMany = 24;   // features of a lane; parts from which on a row is a block's
   using V = std::conditional_t<F == 4, float4, float2>;
-  extern __shared__ int first_item[];   // [slices + 1]
+  extern __shared__ __align__(16) Record records[];   // [slices], then first_item
+  int* first_item = reinterpret_cast<int*>(records + slices);   // [slices + 1]
   __shared__ float so[8][D];
   __shared__ float2 sml[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_kernel_before();
-  auto items = [&](int rows, int parts) { return parts > kMany ? rows : (rows + 7) / 8; };
-  auto rows_of = [&](const Record& rec) { return min(seq_of(a, rec.b, false).n * a.G - rec.unit * kUnit, kUnit); };
-  if (warp == 0) {
+  for (int i = threadIdx.x; i < 2 * slices; i += 256) reinterpret_cast<int4*>(records)[i] = reinterpret_cast<const int4*>(a.records)[i];
+  __syncthreads();
+  if (warp == 0) {   // an item: 32 rows of a unit, four for each warp, or one
     int all = 0;
     for (int c0 = 0; c0 < slices; c0 += 32) {
       int own = 0;
       if (c0 + lane < slices) {
-        const Record rec = a.records[c0 + lane];
-        if (rec.c1 >= 0) own = items(rows_of(rec), rec.c1 - rec.c0 + 1);
+        const Record& rec = records[c0 + lane];
+        if (rec.c1 >= 0) own = rec.c1 - rec.c0 + 1 > kMany ? rec.rows : (rec.rows + 31) / 32;
       }
       int x = own;
 #pragma unroll
@@ -754,73 +776,15 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
   }
   __syncthreads();
   const int all = first_item[slices];
-  for (int item = blockIdx.x; item < all; item += gridDim.x) {
-    int c = 0, past = slices;   // the last record that begins at or before the item (those without items begin where the next do)
-    while (past - c > 1) {
-      const int mid = (c + past) / 2;
-      if (first_item[mid] <= item) c = mid;
-      else past = mid;
+  auto add = [](float (&o)[F], float w, const V& v) {
+    o[0] = fmaf(w, v.x, o[0]);
+    o[1] = fmaf(w, v.y, o[1]);
+    if constexpr (F == 4) {
+      o[2] = fmaf(w, v.z, o[2]);
+      o[3] = fmaf(w, v.w, o[3]);
     }
-    const Record rec = a.records[c];
-    const int parts = rec.c1 - rec.c0 + 1, off = item - first_item[c], rows = rows_of(rec);
-    const bool many = parts > kMany;
-    const int row = many ? off : off * 8 + warp;
-    const int first = many ? warp : 0, step = many ? 8 : 1;
-    float top = -CUDART_INF_F, l = 0.f, o[F];
-#pragma unroll
-    for (int j = 0; j < F; ++j) o[j] = 0.f;
-    if (row < rows) {
-      auto place = [&](int p) { return ((size_t)(rec.c0 + p) * 2 + (p == 0 ? 1 : 0)) * a.part_rows + row; };
-      for (int p0 = first; p0 < parts; p0 += 32 * step) {   // 32 parts at a time, one for each lane to look at
-        const int n = min(32, (parts - p0 + step - 1) / step);
-        const float2 ml = lane < n ? a.part_ml[place(p0 + lane * step)] : make_float2(-CUDART_INF_F, 0.f);
-        const float now = fmaxf(top, warp_max(ml.x)), ref = now == -CUDART_INF_F ? 0.f : now;
-        const float back = ex2_approx(top - ref), mine = ex2_approx(ml.x - ref);
-        top = now;
-        l = l * back + warp_sum(mine * ml.y);
-#pragma unroll
-        for (int j = 0; j < F; ++j) o[j] *= back;
-        for (int k0 = 0; k0 < n; k0 += AHEAD) {
-          V v[AHEAD];
-#pragma unroll
-          for (int k = 0; k < AHEAD; ++k)
-            if (k0 + k < n) v[k] = reinterpret_cast<const V*>(a.part_o + place(p0 + (k0 + k) * step) * D)[lane];
-#pragma unroll
-          for (int k = 0; k < AHEAD; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, mine, (k0 + k) & 31);
-            if (k0 + k < n) {
-              o[0] = fmaf(wk, v[k].x, o[0]);
-              o[1] = fmaf(wk, v[k].y, o[1]);
-              if constexpr (F == 4) {
-                o[2] = fmaf(wk, v[k].z, o[2]);
-                o[3] = fmaf(wk, v[k].w, o[3]);
-              }
-            }
-          }
-        }
-      }
-    }
-    if (many) {
-      __syncthreads();   // the last item's sums are read
-      if (lane == 0) sml[warp] = make_float2(top, l);
-#pragma unroll
-      for (int j = 0; j < F; ++j) so[warp][lane * F + j] = o[j];
-      __syncthreads();
-      if (warp != 0) continue;
-      const float2 ml = lane < 8 ? sml[lane] : make_float2(-CUDART_INF_F, 0.f);
-      top = warp_max(ml.x);
-      const float mine = ex2_approx(ml.x - (top == -CUDART_INF_F ? 0.f : top));
-      l = warp_sum(mine * ml.y);
-#pragma unroll
-      for (int j = 0; j < F; ++j) o[j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, mine, k);
-#pragma unroll
-        for (int j = 0; j < F; ++j) o[j] = fmaf(wk, so[k][lane * F + j], o[j]);
-      }
-    }
-    if (row >= rows) continue;
+  };
+  auto finish = [&](const Record& rec, int row, const float (&o)[F], float top, float l) {
     const RowPlace place = place_of(a, rec.b, rec.h, rec.unit * kUnit + row);
     const bool alive = l != 0.f;
     const float inv = alive ? 1.f / l : 0.f;
@@ -828,6 +792,111 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
 #pragma unroll
     for (int j = 0; j < F; j += 2) out[j / 2] = pack_bf16x2(o[j] * inv, o[j + 1] * inv);
     if (lane == 0) a.lse[place.log] = alive ? (top + log2f(l)) * kLn2 : 0.f;
+  };
+  for (int item = blockIdx.x; item < all; item += gridDim.x) {
+    int c = 0, past = slices;   // the last record that begins at or before the item (those without items begin where the next do)
+    while (past - c > 1) {
+      const int mid = (c + past) / 2;
+      if (first_item[mid] <= item) c = mid;
+      else past = mid;
+    }
+    const Record& rec = records[c];
+    const int parts = rec.c1 - rec.c0 + 1, off = item - first_item[c], rows = rec.rows;
+    auto place = [&](int p, int row) { return ((size_t)(rec.c0 + p) * 2 + (p == 0 ? 1 : 0)) * a.part_rows + row; };
+    if (parts <= kMany) {   // four rows of a warp side by side, eight parts at a time: lane (part, row) looks at one's reference
+      const int row0 = off * 32 + warp * 4;
+      const int mine = row0 + (lane & 3);
+      float top = -CUDART_INF_F, l = 0.f, o[4][F];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) o[i][j] = 0.f;
+      for (int p0 = 0; p0 < parts && row0 < rows; p0 += 8) {
+        const int p = p0 + (lane >> 2);
+        const float2 ml = p < parts && mine < rows ? a.part_ml[place(p, mine)] : make_float2(-CUDART_INF_F, 0.f);
+        float now = ml.x;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+        now = fmaxf(now, top);
+        const float ref = now == -CUDART_INF_F ? 0.f : now, back = ex2_approx(top - ref), w = ex2_approx(ml.x - ref);
+        float sum = w * ml.y;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        top = now;
+        l = l * back + sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float bi = __shfl_sync(0xffffffffu, back, i);
+#pragma unroll
+          for (int j = 0; j < F; ++j) o[i][j] *= bi;
+        }
+        for (int k0 = 0; k0 < 8 && p0 + k0 < parts; k0 += 2) {
+          V v[2][4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (p0 + k0 + k < parts && row0 + i < rows) v[k][i] = reinterpret_cast<const V*>(a.part_o + place(p0 + k0 + k, row0 + i) * D)[lane];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float wi = __shfl_sync(0xffffffffu, w, 4 * (k0 + k) + i);
+              if (p0 + k0 + k < parts && row0 + i < rows) add(o[i], wi, v[k][i]);
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ti = __shfl_sync(0xffffffffu, top, i), li = __shfl_sync(0xffffffffu, l, i);
+        if (row0 + i < rows) finish(rec, row0 + i, o[i], ti, li);
+      }
+      continue;
+    }
+    // a row for the block: its warps take the parts in turn, 32 at a time, one of them for each lane to look at
+    float top = -CUDART_INF_F, l = 0.f, o[F];
+#pragma unroll
+    for (int j = 0; j < F; ++j) o[j] = 0.f;
+    for (int p0 = warp; p0 < parts; p0 += 256) {
+      const int n = min(32, (parts - p0 + 7) / 8);
+      const float2 ml = lane < n ? a.part_ml[place(p0 + lane * 8, off)] : make_float2(-CUDART_INF_F, 0.f);
+      const float now = fmaxf(top, warp_max(ml.x)), ref = now == -CUDART_INF_F ? 0.f : now;
+      const float back = ex2_approx(top - ref), w = ex2_approx(ml.x - ref);
+      top = now;
+      l = l * back + warp_sum(w * ml.y);
+#pragma unroll
+      for (int j = 0; j < F; ++j) o[j] *= back;
+      for (int k0 = 0; k0 < n; k0 += 8) {
+        V v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k < n) v[k] = reinterpret_cast<const V*>(a.part_o + place(p0 + (k0 + k) * 8, off) * D)[lane];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+          if (k0 + k < n) add(o, wk, v[k]);
+        }
+      }
+    }
+    __syncthreads();   // the last item's sums are read
+    if (lane == 0) sml[warp] = make_float2(top, l);
+#pragma unroll
+    for (int j = 0; j < F; ++j) so[warp][lane * F + j] = o[j];
+    __syncthreads();
+    if (warp != 0) continue;
+    const float2 ml = lane < 8 ? sml[lane] : make_float2(-CUDART_INF_F, 0.f);
+    top = warp_max(ml.x);
+    const float w = ex2_approx(ml.x - (top == -CUDART_INF_F ? 0.f : top));
+    l = warp_sum(w * ml.y);
+#pragma unroll
+    for (int j = 0; j < F; ++j) o[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+      for (int j = 0; j < F; ++j) o[j] = fmaf(wk, so[k][lane * F + j], o[j]);
+    }
+    finish(rec, off, o, top, l);
   }
 }
 
@@ -978,9 +1047,9 @@ fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_cache* 
       at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
       at.val.programmaticStreamSerializationAllowed = 1;
       cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(4 * plan.slices);
+      cfg.gridDim = dim3(3 * plan.slices);   // what the SMs hold at a time
       cfg.blockDim = dim3(256);
-      cfg.dynamicSmemBytes = (plan.slices + 1) * sizeof(int);
+      cfg.dynamicSmemBytes = plan.slices * sizeof(Record) + (plan.slices + 1) * sizeof(int);
       cfg.stream = cs;
       cfg.attrs = &at;
       cfg.numAttrs = 1;

@@ -111,13 +111,15 @@ struct RunBytes {
         put(4 * piece + 2, hi[0], hi[1], hi[2], hi[3]);
         put(4 * piece + 3, hi[4], hi[5], hi[6], hi[7]);
       } else {
-        const uint64_t dd = tc::f32x2(df, df);
+        const uint64_t dd = tc::f32x2(df, df), less = tc::f32x2(-8388736.f, -8388736.f);   // 2^23 + 128
         uint32_t x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8; ++j) {   // bytes, 128 more, as the low bits of 2^23 (see s8_to_f32), two at a time
           const uint32_t u = w[i][j / 2] ^ 0x80808080u;
+          const uint64_t n = tc::add_f32x2(tc::f32x2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | (2 * j % 4))),
+                                                     __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | (2 * j % 4 + 1)))), less);
           float lo, hi;
-          tc::f32x2_split(tc::mul_f32x2(tc::f32x2(s8_to_f32(u, 2 * j % 4), s8_to_f32(u, 2 * j % 4 + 1)), dd), lo, hi);
+          tc::f32x2_split(tc::mul_f32x2(n, dd), lo, hi);
           x[j] = tc::pack_bf16x2(lo, hi);
         }
         put(2 * piece, x[0], x[1], x[2], x[3]);
