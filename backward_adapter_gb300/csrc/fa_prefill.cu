@@ -16,7 +16,7 @@
 //
 // A block of 20 warps. Warp 0 issues the MMAs (S_t = Q_t K^T, O_t += P_t V) and walks the list for all. Eight warps read the
 // packed bytes and write the bf16 operands (kv_tile.cuh), a run of 16 keys each, one tile of K and the V of the tile before into
-// each stage of a ring; none of them is on the scheduler of warp 0, which the tensor cores wait for. Warps 4 and 8 bring Q_0 and
+// each stage of a ring. Warps 1-3 bring Q_0 and
 // Q_1, as soon as the last product with the ones before is done. Warps 12-15 and 16-19 have a row of Q_0 and Q_1 for each thread:
 // they turn scores into P in TMEM, and write O at the end. They hold 32 scores at a time and the next 32 on their way: a row of
 // 128 in registers leaves so few to the others that these spill, and what is spilled is in L2, as shared memory takes what L1 has.
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   let_next_kernel_start();
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bar_q[t], 1);
+      mbar_init(&bar_q[t], 3);
       mbar_init(&bar_read[t], 1);
       mbar_init(&bar_s[t], 1);
       mbar_init(&bar_p[t], 4);
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&bar_piece[i], 1);
-      mbar_init(&bar_past[i], kLoaders + 2 + 8);   // the warps that load and that have rows
+      mbar_init(&bar_past[i], 3 + kLoaders + 8);   // the warps that bring Q, that load and that have rows
     }
     mbar_init(bar_done, 1);
     *abort_flag = 0;
@@ -453,39 +453,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_wait<true>(bar_done, 0, nullptr, a.status, 1005);
       __syncwarp();
     }
-    else if (warp == 1 || warp == 2) {
-      // ---------------------------------------------------------------- Q
-      const int t = warp - 1;
-      constexpr int CHUNKS = D / 8, STEP = 32 / CHUNKS;   // 16-byte chunks of a row, rows of a step
-      const int chunk = lane % CHUNKS;
+    else if (warp < 4) {
+      // ---------------------------------------------------------------- Q, rows of both tiles for each of warps 1-3
+      constexpr int CHUNKS = D / 8, ROWS = 32 / CHUNKS, STEP = 3 * ROWS;   // 16-byte chunks of a row, rows of a load, of a step
+      const int chunk = lane % CHUNKS, r0 = (warp - 1) * ROWS + lane / CHUNKS;
+      // elements from a row to the one STEP rows on, and what there is to add where that passes the last head
+      const int tokens = STEP / a.G, heads = STEP % a.G;
       const long long by_token = (long long)(a.layout ? a.Hq : 1) * D, by_head = (long long)(a.layout ? 1 : a.Sq) * D;
-      const uint32_t box = sQ + t * L::kTileBytes + (chunk >> 3) * L::kBoxBytes;
-      int loads = 0;
-      for (int part = 0;; ++part) {
-        if (!__all_sync(0xffffffffu, part_there(part))) break;
-        const Piece x = pieces[part % kPieces];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
-        if (x.tiles == 0) break;
+      const long long on_by = tokens * by_token + heads * by_head, over = by_token - a.G * by_head;
+      const uint32_t place = (chunk >> 3) * L::kBoxBytes;
+      int loads0 = 0, loads1 = 0;   // of each tile so far
+      bool ok = true;
+      auto load = [&](const Piece& x, int t, int& loads) {
         const int rows = x.rows - t * kBM;
-        if (rows <= 0) continue;
-        if (loads > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bar_read[t], (loads - 1) & 1, abort_flag, a.status, 1011))) break;
+        if (rows <= 0) return false;
+        if (loads > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_read[t], (loads - 1) & 1, abort_flag, a.status, 1011)))) return false;
         ++loads;
-        int r = lane / CHUNKS;
-        int token = (x.unit * kUnit + t * kBM + r) / a.G, head = (x.unit * kUnit + t * kBM + r) % a.G;
-        const __nv_bfloat16* first = a.q + ((size_t)x.b * a.Hq * a.Sq + (a.layout ? (size_t)x.h * a.G : (size_t)x.h * a.G * a.Sq)) * D + 8 * chunk;
-#pragma unroll 4
-        for (; r < kBM; r += STEP) {   // rows behind the last are zeros
+        const int row = x.unit * kUnit + t * kBM + r0;
+        int head = row % a.G;
+        const __nv_bfloat16* src = a.q + ((size_t)x.b * a.Hq * a.Sq) * D + (row / a.G) * by_token + (x.h * a.G + head) * by_head + 8 * chunk;
+        const uint32_t box = sQ + t * L::kTileBytes + place;
+#pragma unroll 2
+        for (int r = r0; r < kBM; r += STEP) {   // rows behind the last are zeros
           const bool on = r < rows;
-          const __nv_bfloat16* src = on ? first + token * by_token + head * by_head : a.q;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)), "l"(src), "r"(on ? 16 : 0)
-                       : "memory");
-          for (head += STEP; head >= a.G; head -= a.G) ++token;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)),
+                       "l"(on ? src : a.q), "r"(on ? 16 : 0) : "memory");
+          src += on_by;
+          head += heads;
+          if (head >= a.G) {
+            head -= a.G;
+            src += over;
+          }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        return true;
+      };
+      auto there = [&](int t) {
         if (a.q_xor != 0u || a.q_and != 0xffffffffu) {   // a scale that is not positive: this lane's own chunks again
-          for (r = lane / CHUNKS; r < kBM; r += STEP) {
-            const uint32_t at = box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+          for (int r = r0; r < kBM; r += STEP) {
+            const uint32_t at = sQ + t * L::kTileBytes + place + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
             const float4 f = ld_shared_f4(at);
             st_shared_v4(at, (__float_as_uint(f.x) & a.q_and) ^ a.q_xor, (__float_as_uint(f.y) & a.q_and) ^ a.q_xor,
                          (__float_as_uint(f.z) & a.q_and) ^ a.q_xor, (__float_as_uint(f.w) & a.q_and) ^ a.q_xor);
@@ -494,6 +499,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_q[t]);
+      };
+      for (int part = 0; ok; ++part) {
+        if (!__all_sync(0xffffffffu, part_there(part))) break;
+        const Piece x = pieces[part % kPieces];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
+        if (x.tiles == 0) break;
+        load(x, 0, loads0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const bool both = ok && load(x, 1, loads1);
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+        if (ok) there(0);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (both) there(1);
       }
     } else if (warp >= 4) {
     // ------------------------------------------------------------------ K and V: from bytes to operands
