@@ -514,81 +514,81 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (both) there(1);
       }
-    } else if (warp >= 4) {
-    // ------------------------------------------------------------------ K and V: from bytes to operands
-    const int run = warp - 4;
-    int part = 0, left = 0, key = 0, b = 0, h = 0, len = 0;   // of the part: tiles to come, and this warp's first key of the next
-    int entries = 0, ahead = 0;   // pages: lane i has the table's entry for this run of the i-th tile of 32, counted down
-    // The next tile of the stream, its page's number on its way; false behind the last.
-    auto next_tile = [&]() -> bool {
-      if (left == 0) {
-        if (!__all_sync(0xffffffffu, part_there(part))) return false;
-        const Piece& x = pieces[part % kPieces];
-        left = x.tiles;
-        key = x.tile * kBN + kRun * run - kBN;
-        b = x.b;
-        h = x.h;
-        len = x.len;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
-        ++part;
-        if (left == 0) return false;
-        ahead = 0;
-      }
-      key += kBN;
-      --left;
-      if constexpr (PAGED) {
-        if (--ahead < 0) {
-          ahead = 31;
-          const int mine = key + lane * kBN;
-          if (mine < len && lane <= left) entries = __ldg(a.pages.table + b * a.pages.stride + page_index(a.pages, mine));
+    } else {
+      // ------------------------------------------------------------------ K and V: from bytes to operands
+      const int run = warp - 4;
+      int part = 0, left = 0, key = 0, b = 0, h = 0, len = 0;   // of the part: tiles to come, and this warp's first key of the next
+      int entries = 0, ahead = 0;   // pages: lane i has the table's entry for this run of the i-th tile of 32, counted down
+      // The next tile of the stream, its page's number on its way; false behind the last.
+      auto next_tile = [&]() -> bool {
+        if (left == 0) {
+          if (!__all_sync(0xffffffffu, part_there(part))) return false;
+          const Piece& x = pieces[part % kPieces];
+          left = x.tiles;
+          key = x.tile * kBN + kRun * run - kBN;
+          b = x.b;
+          h = x.h;
+          len = x.len;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_past[part % kPieces]);
+          ++part;
+          if (left == 0) return false;
+          ahead = 0;
         }
-      }
-      return true;
-    };
-    // Where its run lies.
-    auto row_of_tile = [&]() -> long long {
-      if constexpr (!PAGED) return ((long long)b * a.c.Hkv + h) * a.c.S + key;
-      const int page = __shfl_sync(0xffffffffu, entries, 31 - ahead);
-      return key < len ? row_in_page(a.pages, page, a.c.Hkv, h, key, lane == 0 ? a.status : nullptr) : -1;
-    };
-    RunBytes<D, Q4> k, v;
-    long long row = 0;
-    int keys = 0;
-    bool has_k = next_tile(), has_v = false;
-    if (has_k) {
-      row = row_of_tile();
-      keys = len - key;
-      k.load(a.c.k_q, a.c.k_d, row, keys);
-    }
-    for (int stage = 0; has_k || has_v; ++stage) {
-      // K of a tile is on its way, and V of the one before it if there is one
-      const int sb = stage % L::kStages;
-      const bool more = has_k && next_tile();
-      if (stage >= L::kStages &&
-          !__all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[sb], (stage / L::kStages - 1) & 1, abort_flag, a.status, 1006)))
-        break;
-      const uint32_t at = sKV + 2 * sb * L::kTileBytes;
-      long long next_row = 0;
-      int next_keys = 0;
+        key += kBN;
+        --left;
+        if constexpr (PAGED) {
+          if (--ahead < 0) {
+            ahead = 31;
+            const int mine = key + lane * kBN;
+            if (mine < len && lane <= left) entries = __ldg(a.pages.table + b * a.pages.stride + page_index(a.pages, mine));
+          }
+        }
+        return true;
+      };
+      // Where its run lies.
+      auto row_of_tile = [&]() -> long long {
+        if constexpr (!PAGED) return ((long long)b * a.c.Hkv + h) * a.c.S + key;
+        const int page = __shfl_sync(0xffffffffu, entries, 31 - ahead);
+        return key < len ? row_in_page(a.pages, page, a.c.Hkv, h, key, lane == 0 ? a.status : nullptr) : -1;
+      };
+      RunBytes<D, Q4> k, v;
+      long long row = 0;
+      int keys = 0;
+      bool has_k = next_tile(), has_v = false;
       if (has_k) {
-        k.template store<false>(at, run);
-        if (more) {
-          next_row = row_of_tile();
-          next_keys = len - key;
-          k.load(a.c.k_q, a.c.k_d, next_row, next_keys);
-        }
+        row = row_of_tile();
+        keys = len - key;
+        k.load(a.c.k_q, a.c.k_d, row, keys);
       }
-      if (has_v) v.template store<true>(at + L::kTileBytes, run);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_full[sb]);
-      if (has_k) v.load(a.c.v_q, a.c.v_d, row, keys);
-      has_v = has_k;
-      has_k = more;
-      row = next_row;
-      keys = next_keys;
-    }
+      for (int stage = 0; has_k || has_v; ++stage) {
+        // K of a tile is on its way, and V of the one before it if there is one
+        const int sb = stage % L::kStages;
+        const bool more = has_k && next_tile();
+        if (stage >= L::kStages &&
+            !__all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[sb], (stage / L::kStages - 1) & 1, abort_flag, a.status, 1006)))
+          break;
+        const uint32_t at = sKV + 2 * sb * L::kTileBytes;
+        long long next_row = 0;
+        int next_keys = 0;
+        if (has_k) {
+          k.store(at, run, false);
+          if (more) {
+            next_row = row_of_tile();
+            next_keys = len - key;
+            k.load(a.c.k_q, a.c.k_d, next_row, next_keys);
+          }
+        }
+        if (has_v) v.store(at + L::kTileBytes, run, true);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_full[sb]);
+        if (has_k) v.load(a.c.v_q, a.c.v_d, row, keys);
+        has_v = has_k;
+        has_k = more;
+        row = next_row;
+        keys = next_keys;
+      }
     }
   } else {
     regs_inc<kRegsSoftmax>();
@@ -643,63 +643,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         uint32_t raw[2][32];
         tmem_ld32(tS, raw[0]);
-#pragma unroll
-        for (int c = 0; c < kBN / 32; ++c) {
-          uint32_t (&x)[32] = raw[c & 1];
-          tmem_wait_ld();
-          reg_fence(x);
-          masked(x, c);
-          float top2[2] = {-CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) top2[(e >> 1) & 1] = max3f(top2[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-          const float top = fmaxf(top2[0], top2[1]) * sl2;
-          if (__any_sync(0xffffffffu, top > m + kRescale)) {   // rare, but for a unit's first scores
-            // a whole number: what there is changes by a power of two, so nothing is rounded again
-            const float m_new = top > m + kRescale ? ceilf(top) : m;
-            const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
-            m = m_new;
-            l *= alpha;
-            const uint64_t alpha_2 = f32x2(alpha, alpha);
-            sum2[0] = mul_f32x2(sum2[0], alpha_2);
-            sum2[1] = mul_f32x2(sum2[1], alpha_2);
-            const uint32_t alpha_16 = pack_bf16x2(alpha, alpha);
-#pragma unroll
-            for (int d = 0; d < c; ++d) {   // weights of this tile that are stored already
-              uint32_t pk[16];
-              tmem_wait_st();
-              tmem_ld16(tS + d * 16, pk);
-              tmem_wait_ld();
-              reg_fence16(pk);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = mul_bf16x2(pk[e], alpha_16);
-              tmem_st16(tS + d * 16, pk);
-            }
-            if (!first) {   // O holds the products of the tiles before: their MMAs ended before these scores did
 #pragma unroll 1
-              for (int d = 0; d < D / 16; ++d) {
-                uint32_t ov[16];
-                tmem_ld16(tO + d * 16, ov);
-                tmem_wait_ld();
-                reg_fence16(ov);
+        for (int c0 = 0; c0 < kBN / 32; c0 += 2) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                tmem_st16(tO + d * 16, ov);
+          for (int i = 0; i < 2; ++i) {
+            const int c = c0 + i;
+            uint32_t (&x)[32] = raw[i];
+            tmem_wait_ld();
+            reg_fence(x);
+            masked(x, c);
+            float top2[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) top2[(e >> 1) & 1] = max3f(top2[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            const float top = fmaxf(top2[0], top2[1]) * sl2;
+            if (__any_sync(0xffffffffu, top > m + kRescale)) {   // rare, but for a unit's first scores
+              // a whole number: what there is changes by a power of two, so nothing is rounded again
+              const float m_new = top > m + kRescale ? ceilf(top) : m;
+              const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
+              m = m_new;
+              l *= alpha;
+              const uint64_t alpha_2 = f32x2(alpha, alpha);
+              sum2[0] = mul_f32x2(sum2[0], alpha_2);
+              sum2[1] = mul_f32x2(sum2[1], alpha_2);
+              const uint32_t alpha_16 = pack_bf16x2(alpha, alpha);
+              tmem_wait_st();
+#pragma unroll 1
+              for (int d = 0; d < c; ++d) {   // weights of this tile that are stored already
+                uint32_t pk[16];
+                tmem_ld16(tS + d * 16, pk);
+                tmem_wait_ld();
+                reg_fence16(pk);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = mul_bf16x2(pk[e], alpha_16);
+                tmem_st16(tS + d * 16, pk);
+              }
+              if (!first) {   // O holds the products of the tiles before: their MMAs ended before these scores did
+#pragma unroll 1
+                for (int d = 0; d < D / 16; ++d) {
+                  uint32_t ov[16];
+                  tmem_ld16(tO + d * 16, ov);
+                  tmem_wait_ld();
+                  reg_fence16(ov);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                  tmem_st16(tO + d * 16, ov);
+                }
               }
             }
-          }
-          if (c + 1 < kBN / 32) tmem_ld32(tS + (c + 1) * 32, raw[(c + 1) & 1]);
-          const float less = m == -CUDART_INF_F ? 0.f : -m;
-          const uint64_t less_2 = f32x2(less, less);
-          uint32_t pk[16];
+            if (c + 1 < kBN / 32) tmem_ld32(tS + (c + 1) * 32, raw[1 - i]);
+            const float less = m == -CUDART_INF_F ? 0.f : -m;
+            const uint64_t less_2 = f32x2(less, less);
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float t0, t1;
-            f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2_2, less_2), t0, t1);
-            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-            sum2[e & 1] = add_f32x2(sum2[e & 1], f32x2(p0, p1));
-            pk[e] = pack_bf16x2(p0, p1);
+            for (int e = 0; e < 16; ++e) {
+              float t0, t1;
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2_2, less_2), t0, t1);
+              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+              sum2[e & 1] = add_f32x2(sum2[e & 1], f32x2(p0, p1));
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tS + c * 16, pk);   // over scores that have been read
           }
-          tmem_st16(tS + c * 16, pk);   // over scores that have been read
         }
         float s0, s1, s2, s3;
         f32x2_split(sum2[0], s0, s1);

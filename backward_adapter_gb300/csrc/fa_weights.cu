@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant
       if (run < len) row = PAGED ? page_row(a.pages, a.c.Hkv, b, h, run, a.status) : (long long)bh * a.c.S + run;
       RunBytes<D, Q4> k;
       k.load(a.c.k_q, a.c.k_d, row, min(len - run, kRun));
-      k.template store<false>(sK, warp);
+      k.store(sK, warp, false);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_k);

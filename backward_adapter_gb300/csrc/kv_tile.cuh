@@ -76,15 +76,14 @@ struct RunBytes {
     }
   }
 
-  // Into run `run` of the tile at `tile` (shared memory). FINITE: a scale that is not finite counts as 0.
-  template <bool FINITE>
-  __device__ __forceinline__ void store(uint32_t tile, int run) const {
+  // Into run `run` of the tile at `tile` (shared memory). finite: a scale that is not counts as 0.
+  __device__ __forceinline__ void store(uint32_t tile, int run, bool finite) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int piece = piece_of(i, lane);
       float df = __half2float(__ushort_as_half(d[i]));
-      if (FINITE && !(fabsf(df) <= 65504.f)) df = 0.f;
+      if (finite && !(fabsf(df) <= 65504.f)) df = 0.f;
       const uint32_t at = tile + (kRun * run + row_of(i, lane)) * 128;
       auto put = [&](int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t e) {
         tc::st_shared_v4(at + (chunk >> 3) * BOX + (((chunk & 7) ^ (lane & 7)) << 4), a, b, c, e);
