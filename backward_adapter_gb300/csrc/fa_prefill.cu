@@ -18,7 +18,7 @@
 // packed bytes and write the bf16 operands (kv_tile.cuh), a run of 16 keys each, one tile of K and the V of the tile before into
 // each stage of a ring. Warps 1-3 bring Q_0 and
 // Q_1, as soon as the last product with the ones before is done. Warps 12-15 and 16-19 have a row of Q_0 and Q_1 for each thread:
-// they turn scores into P in TMEM, and write O at the end. They hold 32 scores at a time and the next 32 on their way: a row of
+// they turn scores into P in TMEM, and write O at the end. They hold 32 scores at a time: a row of
 // 128 in registers leaves so few to the others that these spill, and what is spilled is in L2, as shared memory takes what L1 has.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256, 256+D), O1 [256+D, 256+2D).
 #include <cuda_bf16.h>
@@ -70,6 +70,7 @@ struct PrefillArgs {
   float sl2;         // |scale| log2(e); the sign, or a scale of 0, is in the two masks
   uint32_t q_and, q_xor;
   int Hq, Sq, window, layout, G, part_rows;
+  bool wide;         // o is 32-byte aligned
 };
 
 // A sequence's keys and tokens.
@@ -267,6 +268,18 @@ __device__ __forceinline__ RowPlace place_of(const PrefillArgs& a, int b, int h,
   p.at = (a.layout ? ((size_t)b * a.Sq + i) * a.Hq + head : ((size_t)b * a.Hq + head) * a.Sq + i) * a.c.D;
   p.log = ((size_t)b * a.Hq + head) * a.Sq + i;
   return p;
+}
+
+// 32 bytes: a sector of L2 whole where they are one (two prompts of 4096 tokens in 8 bits: 371 us in halves, 349 so).
+__device__ __forceinline__ void st_global_32(bool whole, uint4* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                             uint32_t g, uint32_t h) {
+  if (!whole) {
+    p[0] = make_uint4(a, b, c, d);
+    p[1] = make_uint4(e, f, g, h);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f),
+               "r"(g), "r"(h) : "memory");
 }
 
 template <int D>
@@ -641,69 +654,63 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
         const uint64_t sl2_2 = f32x2(sl2, sl2);
         uint64_t sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-        uint32_t raw[2][32];
-        tmem_ld32(tS, raw[0]);
 #pragma unroll 1
-        for (int c0 = 0; c0 < kBN / 32; c0 += 2) {
+        for (int c = 0; c < kBN / 32; ++c) {   // rolled, like the loaders: what warps go through has to come from the instruction caches
+          uint32_t x[32];
+          tmem_ld32(tS + c * 32, x);
+          tmem_wait_ld();
+          reg_fence(x);
+          masked(x, c);
+          float top2[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = c0 + i;
-            uint32_t (&x)[32] = raw[i];
-            tmem_wait_ld();
-            reg_fence(x);
-            masked(x, c);
-            float top2[2] = {-CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) top2[(e >> 1) & 1] = max3f(top2[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            const float top = fmaxf(top2[0], top2[1]) * sl2;
-            if (__any_sync(0xffffffffu, top > m + kRescale)) {   // rare, but for a unit's first scores
-              // a whole number: what there is changes by a power of two, so nothing is rounded again
-              const float m_new = top > m + kRescale ? ceilf(top) : m;
-              const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
-              m = m_new;
-              l *= alpha;
-              const uint64_t alpha_2 = f32x2(alpha, alpha);
-              sum2[0] = mul_f32x2(sum2[0], alpha_2);
-              sum2[1] = mul_f32x2(sum2[1], alpha_2);
-              const uint32_t alpha_16 = pack_bf16x2(alpha, alpha);
-              tmem_wait_st();
+          for (int e = 0; e < 32; e += 2) top2[(e >> 1) & 1] = max3f(top2[(e >> 1) & 1], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          const float top = fmaxf(top2[0], top2[1]) * sl2;
+          if (__any_sync(0xffffffffu, top > m + kRescale)) {   // rare, but for a unit's first scores
+            // a whole number: what there is changes by a power of two, so nothing is rounded again
+            const float m_new = top > m + kRescale ? ceilf(top) : m;
+            const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
+            m = m_new;
+            l *= alpha;
+            const uint64_t alpha_2 = f32x2(alpha, alpha);
+            sum2[0] = mul_f32x2(sum2[0], alpha_2);
+            sum2[1] = mul_f32x2(sum2[1], alpha_2);
+            const uint32_t alpha_16 = pack_bf16x2(alpha, alpha);
+            tmem_wait_st();
 #pragma unroll 1
-              for (int d = 0; d < c; ++d) {   // weights of this tile that are stored already
-                uint32_t pk[16];
-                tmem_ld16(tS + d * 16, pk);
+            for (int d = 0; d < c; ++d) {   // weights of this tile that are stored already
+              uint32_t pk[16];
+              tmem_ld16(tS + d * 16, pk);
+              tmem_wait_ld();
+              reg_fence16(pk);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = mul_bf16x2(pk[e], alpha_16);
+              tmem_st16(tS + d * 16, pk);
+            }
+            if (!first) {   // O holds the products of the tiles before: their MMAs ended before these scores did
+#pragma unroll 1
+              for (int d = 0; d < D / 16; ++d) {
+                uint32_t ov[16];
+                tmem_ld16(tO + d * 16, ov);
                 tmem_wait_ld();
-                reg_fence16(pk);
+                reg_fence16(ov);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = mul_bf16x2(pk[e], alpha_16);
-                tmem_st16(tS + d * 16, pk);
-              }
-              if (!first) {   // O holds the products of the tiles before: their MMAs ended before these scores did
-#pragma unroll 1
-                for (int d = 0; d < D / 16; ++d) {
-                  uint32_t ov[16];
-                  tmem_ld16(tO + d * 16, ov);
-                  tmem_wait_ld();
-                  reg_fence16(ov);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                  tmem_st16(tO + d * 16, ov);
-                }
+                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                tmem_st16(tO + d * 16, ov);
               }
             }
-            if (c + 1 < kBN / 32) tmem_ld32(tS + (c + 1) * 32, raw[1 - i]);
-            const float less = m == -CUDART_INF_F ? 0.f : -m;
-            const uint64_t less_2 = f32x2(less, less);
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float t0, t1;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2_2, less_2), t0, t1);
-              const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-              sum2[e & 1] = add_f32x2(sum2[e & 1], f32x2(p0, p1));
-              pk[e] = pack_bf16x2(p0, p1);
-            }
-            tmem_st16(tS + c * 16, pk);   // over scores that have been read
           }
+          const float less = m == -CUDART_INF_F ? 0.f : -m;
+          const uint64_t less_2 = f32x2(less, less);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float t0, t1;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2_2, less_2), t0, t1);
+            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+            sum2[e & 1] = add_f32x2(sum2[e & 1], f32x2(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tS + c * 16, pk);   // over scores that have been read
         }
         float s0, s1, s2, s3;
         f32x2_split(sum2[0], s0, s1);
@@ -725,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const float inv = !whole ? 1.f : alive ? 1.f / l : 0.f;
       uint4* out = reinterpret_cast<uint4*>(a.o + place.at);
       const size_t slot = ((size_t)blockIdx.x * 2 + (x.starts ? 1 : 0)) * a.part_rows + t * kBM + r;
-      float4* left_o = reinterpret_cast<float4*>(a.part_o + slot * D);
+      uint4* left_o = reinterpret_cast<uint4*>(a.part_o + slot * D);
 #pragma unroll
       for (int cch = 0; cch < D / 32; ++cch) {
         uint32_t ov[32];
@@ -738,12 +745,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int e = 0; e < 32; ++e) f[e] = alive ? __uint_as_float(ov[e]) * inv : 0.f;
         if (whole) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            out[cch * 4 + e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                          pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+          for (int e = 0; e < 2; ++e)
+            st_global_32(a.wide, out + cch * 4 + 2 * e, pack_bf16x2(f[16 * e], f[16 * e + 1]), pack_bf16x2(f[16 * e + 2], f[16 * e + 3]),
+                         pack_bf16x2(f[16 * e + 4], f[16 * e + 5]), pack_bf16x2(f[16 * e + 6], f[16 * e + 7]),
+                         pack_bf16x2(f[16 * e + 8], f[16 * e + 9]), pack_bf16x2(f[16 * e + 10], f[16 * e + 11]),
+                         pack_bf16x2(f[16 * e + 12], f[16 * e + 13]), pack_bf16x2(f[16 * e + 14], f[16 * e + 15]));
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) left_o[cch * 8 + e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+          for (int e = 0; e < 4; ++e)
+            st_global_32(true, left_o + cch * 8 + 2 * e, __float_as_uint(f[8 * e]), __float_as_uint(f[8 * e + 1]), __float_as_uint(f[8 * e + 2]),
+                         __float_as_uint(f[8 * e + 3]), __float_as_uint(f[8 * e + 4]), __float_as_uint(f[8 * e + 5]),
+                         __float_as_uint(f[8 * e + 6]), __float_as_uint(f[8 * e + 7]));
         }
       }
       tc_fence_before();   // these reads of O come before the next part's product, which waits for bar_p
@@ -1036,6 +1048,7 @@ fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_cache* 
   a.window = p->window < 2 * kMaxSeq ? p->window : 2 * kMaxSeq;
   a.layout = p->layout;
   a.G = p->Hq / cv.Hkv;
+  a.wide = (uintptr_t)o % 32 == 0;
   cudaStream_t cs = (cudaStream_t)stream;
   const size_t per = (size_t)p->Hq * p->Sq;   // rows of a sequence
   for (int b0 = 0; b0 < cv.B; b0 += kListed) {

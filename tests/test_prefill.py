@@ -122,6 +122,20 @@ def test_prefill_without_lengths_and_counts():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_of_tensors_at_any_multiple_of_16_bytes(D):
+    planes, pool, table = pu.make(2, 2, 90, D, "q4_0", 16, 4)
+    q = pu.queries(2, 4, 37, D, 5)
+    want = kv.prefill(q, *pool, table=table)
+    for first in (8, 16, 24):   # bf16 elements
+        hold = [torch.zeros(q.numel() + 64, dtype=q.dtype, device="cuda")[first:first + q.numel()].view(q.shape) for _ in range(2)]
+        lse = torch.zeros(want[1].numel() + 16, device="cuda")[4:4 + want[1].numel()].view(want[1].shape)
+        hold[0].copy_(q)
+        kv.prefill(hold[0], *pool, table=table, out=hold[1], lse=lse)
+        assert torch.equal(hold[1], want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
 def test_prefill_is_the_training_forward_over_the_same_cache():
     """One chunk of one length: fwd_q4's values, both within their roundings of each other, the weights' and the output's."""
     planes, pool, table = pu.make(2, 2, 512, 128, "q4_0", 64, 5)
