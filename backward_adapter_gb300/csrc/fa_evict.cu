@@ -320,7 +320,7 @@ extern "C" fa_status fa_cache_evict(const fa_evict_params* p, const fa_cache* c,
   if (to != nullptr && there.S < p->keep) {
     set_error("the second table has room for %d keys of %d", there.S, p->keep); return FA_ERR_INVALID_ARG;
   }
-  if (W < 1 || W > 0x7fffffffLL) { set_error("W=%lld outside [1, 2^31 - 1]", (long long)W); return FA_ERR_INVALID_ARG; }
+  if (W < 1 || W > 1LL << 30) { set_error("W=%lld outside [1, 2^30]", (long long)W); return FA_ERR_INVALID_ARG; }
   const long long heads = (long long)cv.B * cv.Hkv;
   if (heads * kCluster > 0x7fffffffLL) { set_error("too many heads for one launch"); return FA_ERR_UNSUPPORTED; }
   const size_t bytes = (size_t)heads * (size_t)W * 4;

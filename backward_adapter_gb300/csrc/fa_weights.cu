@@ -4,9 +4,15 @@
 // key j. With K as the left operand the products S^T = K Q^T have a key for each lane of TMEM and a row for each column, so
 // that a thread adds up a key's weights along its lane, in registers: no atomics, no second pass, a fixed order.
 //
-// A block has one tile of 128 keys of a sequence's head: warps 0-7 make its bf16 operand from the packed bytes (kv_tile.cuh);
-// then warps 0-3 own a key for each thread, warps 4-7 bring the rows, 128 (or 16, where there are no more) at a time, and one
-// thread of warp 8 issues the MMAs; the products are in two buffers, so that they and the exponentials overlap.
+// Up to 16 rows (a step's tokens): the keys' bytes are what there is to read, 72 a key for D = 128 in 4 bits, and turning them
+// into bf16 what there is to do. A warp has the keys of a chunk, 16 at a time as the rows of mma.sync m16n8k16, its lanes a
+// quarter of a row each, from memory to operand without shared memory: which features a lane has in which step is its own
+// choice, as long as it has the same ones of q. A tcgen05 tile would take the operands through shared memory and two barriers.
+//
+// More rows: a block has 256 keys at a time, two tiles of 128, made bf16 operands once (kv_tile.cuh), and all rows that see one
+// of them go by, 128 at a time, which halves what the blocks read of Q from L2 against 128 keys. A block stays on its SM for all
+// its keys: warps 4-7 make the next 256 operands meanwhile, warps 1-3 bring the rows into a ring, warp 0 issues the MMAs, and
+// warps 8-15 own a key for each thread and add up; each tile's products are in two buffers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,7 +30,7 @@ namespace {
 using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 288;
+constexpr int kThreads = 512;
 
 struct WeightArgs {
   CacheView c;
@@ -42,212 +48,509 @@ struct WeightArgs {
   int Hq, Sq, window, layout, G;
 };
 
-template <int D, int NQ>
-struct WeightSmem {
-  static constexpr int kBox = 128 * 128;               // 64 features of 128 rows
-  static constexpr int kK = 128 * D * 2;
-  static constexpr int kQBox = NQ * 128, kQ = NQ * D * 2;
-  static constexpr int kQOff = kK, kLogOff = kQOff + 2 * kQ, kPosOff = kLogOff + 2 * NQ * 4, kBarOff = kPosOff + 2 * NQ * 4;
-  static constexpr int kBytes = kBarOff + 128 + 1024;
-  static constexpr int kColumns = NQ < 32 ? 64 : 2 * NQ;   // of TMEM
-};
-
-template <int D, bool Q4, bool PAGED, int NQ>
-__global__ void __launch_bounds__(kThreads) weights_kernel(const __grid_constant__ WeightArgs a) {
-  using L = WeightSmem<D, NQ>;
-  constexpr int STEP = L::kColumns / 2;   // columns from one buffer of products to the other
-  extern __shared__ uint8_t smem_raw[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads = a.c.B * a.c.Hkv;
-  const int bh = blockIdx.x % heads, b = bh / a.c.Hkv, h = bh % a.c.Hkv;
-  const int key0 = blockIdx.x / heads * kTileKeys;
-
+// The sequence's keys and tokens, and a report of what is out of range.
+__device__ __forceinline__ void read_lengths(const WeightArgs& a, int b, bool report, int& len, int& n) {
   const long long length = a.lengths != nullptr ? __ldg(a.lengths + b) : a.c.S;
   const long long tokens = a.count != nullptr ? __ldg(a.count + b) : a.Sq;
-  const int len = (int)min(max(length, 0LL), (long long)a.c.S), n = (int)min(max(tokens, 0LL), (long long)a.Sq);
-  if (key0 == 0 && h == 0 && threadIdx.x == 0 && (len != length || n != tokens || len > a.W) && a.status != nullptr)
-    atomicCAS(a.status, 0u, 0x40000000u | kSiteDecodeLength);
-  // the rows that see one of the keys: tokens [first, last]
-  const int before = len - n;
-  const int first = max(key0 - before, 0);
-  const int last = a.window > 0 ? min(n - 1, min(key0 + kTileKeys, len) - 1 + a.window - before) : n - 1;
-  const int row0 = first * a.G, rows = key0 < len ? max((last + 1) * a.G - row0, 0) : 0;
-  float sum = 0.f;
+  len = (int)min(max(length, 0LL), (long long)a.c.S);
+  n = (int)min(max(tokens, 0LL), (long long)a.Sq);
+  if (report && (len != length || n != tokens || len > a.W) && a.status != nullptr) atomicCAS(a.status, 0u, 0x40000000u | kSiteDecodeLength);
+}
 
-  if (rows > 0) {   // the whole block has one answer
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + L::kQOff);
-    float* sLog = reinterpret_cast<float*>(smem + L::kLogOff);   // [2][NQ]: -lse, base 2; -inf in columns without a row
-    int* sPos = reinterpret_cast<int*>(smem + L::kPosOff);       // [2][NQ]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
-    uint64_t* bar_k = bars;          // K written
-    uint64_t* bar_q = bars + 1;      // [2]: rows written
-    uint64_t* bar_s = bars + 3;      // [2]: products there
-    uint64_t* bar_free = bars + 5;   // [2]: products and rows read
-    uint64_t* bar_done = bars + 7;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    if (threadIdx.x == 0) {
-      mbar_init(bar_k, 8);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&bar_q[i], 4);
-        mbar_init(&bar_s[i], 1);
-        mbar_init(&bar_free[i], 4);
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A lane's quarter of rows g and g + 8 of a run of 16 keys, as it is stored.
+template <int D, bool Q4>
+struct Quarter {
+  static constexpr int ROW = Q4 ? D / 2 : D, W = ROW / 16;   // bytes of a row, words of a quarter
+  uint32_t w[2][W];
+  uint16_t d[2];
+  __device__ __forceinline__ void load(const WeightArgs& a, long long row, int keys) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[i][j] = Q4 ? 0x88888888u : 0u;
+      d[i] = 0;
+      if (row >= 0 && r < keys) {
+        const uint8_t* src = static_cast<const uint8_t*>(a.c.k_q) + (row + r) * ROW + t * (ROW / 4);
+        if constexpr (W == 2) {
+          asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "l"(src));
+        } else {
+#pragma unroll
+          for (int j = 0; j < W; j += 4)
+            asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i][j]), "=r"(w[i][j + 1]), "=r"(w[i][j + 2]), "=r"(w[i][j + 3]) : "l"(src + 4 * j));
+        }
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(d[i]) : "l"(a.c.k_d + (row + r) * (D / 32) + (D == 128 ? t : t / 2)));
       }
-      mbar_init(bar_done, 1);
-      *abort_flag = 0;
-      fence_barrier_init();
     }
-    if (warp == 8) tmem_alloc(tmem_slot, L::kColumns);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const int tiles = (rows + NQ - 1) / NQ;
+  }
+};
 
-    if (warp < 8) {   // this warp's run of K
-      const int run = key0 + kRun * warp;
-      long long row = -1;
-      if (run < len) row = PAGED ? page_row(a.pages, a.c.Hkv, b, h, run, a.status) : (long long)bh * a.c.S + run;
-      RunBytes<D, Q4> k;
-      k.load(a.c.k_q, a.c.k_d, row, min(len - run, kRun));
-      k.store(sK, warp, false);
+// The steps' first pairs of a word as bf16 values, of 4 bits the numbers of bytes (0, 2), (1, 3) low, then high (two steps); of 8
+// bits bytes (0, 1), (2, 3) (one step). As in kv_tile.cuh.
+struct Scale4 {
+  uint32_t dh, dl;
+  __device__ __forceinline__ explicit Scale4(uint16_t d) {
+    const float f = __half2float(__ushort_as_half(d));
+    dh = pack_bf16x2(f, f);
+    const float rest = f - __uint_as_float(dh << 16);
+    dl = pack_bf16x2(rest, rest);
+  }
+  __device__ __forceinline__ uint32_t value(uint32_t nibbles) const {
+    const uint32_t n = add_bf16x2((nibbles & 0x000f000fu) | 0x43004300u, 0xc308c308u);
+    return fma_bf16x2(n, dh, mul_bf16x2(n, dl));
+  }
+};
+__device__ __forceinline__ uint32_t value_q8(uint32_t u, int k, uint64_t dd) {   // bytes k, k + 1, 128 more
+  const uint64_t n = add_f32x2(f32x2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | k)),
+                                     __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | (k + 1)))), f32x2(-8388736.f, -8388736.f));
+  float lo, hi;
+  f32x2_split(mul_f32x2(n, dd), lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+
+// NT * 8 rows at most. A warp has `runs` runs of 16 keys.
+template <int D, bool Q4, bool PAGED, int NT>
+__global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant__ WeightArgs a, int runs, unsigned chunks, unsigned warps) {
+  constexpr int W = Quarter<D, Q4>::W, STEPS = D / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const unsigned id = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (id >= warps) return;
+  const unsigned bh = id / chunks;
+  const int b = bh / a.c.Hkv, h = bh % a.c.Hkv, key0 = (int)(id % chunks) * runs * kRun;
+  int len, n;
+  read_lengths(a, b, id % chunks == 0 && h == 0 && lane == 0, len, n);
+  const int before = len - n;   // the first token's position
+  // the runs with a key that some token sees: [first, past)
+  const int end = min(key0 + runs * kRun, len);
+  const int first = max(key0, a.window > 0 ? max(before - a.window, 0) & ~(kRun - 1) : 0), past = n > 0 ? end : first;
+  int entry = -1;   // lane i: the page of the chunk's run i
+  if (PAGED && lane < runs && key0 + lane * kRun < past)
+    entry = __ldg(a.pages.table + b * a.pages.stride + page_index(a.pages, key0 + lane * kRun));
+  auto row_of = [&](int key) -> long long {
+    if constexpr (!PAGED) return (long long)bh * a.c.S + key;
+    return row_in_page(a.pages, __shfl_sync(0xffffffffu, entry, (key - key0) / kRun), a.c.Hkv, h, key, lane == 0 ? a.status : nullptr);
+  };
+  Quarter<D, Q4> now, then;
+  if (first < past) now.load(a, row_of(first), past - first);
+
+  // q: of row 8 m + g this lane's quarter, as the steps take it; of rows 8 m + 2 t and the next their LSE and position
+  uint32_t q[NT][STEPS][2];
+  float less[NT][2];
+  int pos[NT][2];
+#pragma unroll
+  for (int m = 0; m < NT; ++m) {
+    auto place = [&](int r) -> size_t {   // row of q, and of lse in one layout
+      const int i = r / a.G, head = h * a.G + r % a.G;
+      return a.layout ? ((size_t)b * a.Sq + i) * a.Hq + head : ((size_t)b * a.Hq + head) * a.Sq + i;
+    };
+    const int r = 8 * m + g;
+    const bool on = first < past && r < n * a.G;
+    const uint2* src = reinterpret_cast<const uint2*>(a.q + (on ? place(r) * D : 0));
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      // the step's four features: of 4 bits those of the low, then of the high nibbles of word j / 2; of 8 bits of word j
+      const int f = Q4 ? (D == 128 ? 32 * t + 4 * (j / 2) : 32 * (t / 2) + 8 * (t & 1) + 4 * (j / 2)) + 16 * (j & 1) : (D / 4) * t + 4 * j;
+      uint2 x = on ? __ldg(src + f / 4) : make_uint2(0, 0);
+      x.x = (x.x & a.q_and) ^ a.q_xor;
+      x.y = (x.y & a.q_and) ^ a.q_xor;
+      q[m][j][0] = Q4 ? __byte_perm(x.x, x.y, 0x5410) : x.x;
+      q[m][j][1] = Q4 ? __byte_perm(x.x, x.y, 0x7632) : x.y;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = 8 * m + 2 * t + j;
+      const bool live = c < n * a.G;
+      const int i = c / a.G, head = h * a.G + c % a.G;
+      less[m][j] = live && first < past ? -__ldg(a.lse + ((size_t)b * a.Hq + head) * a.Sq + i) * kLog2e : -CUDART_INF_F;
+      pos[m][j] = live ? before + i : -1;
+    }
+  }
+
+  float* out = a.out + (size_t)bh * a.W;
+  const float* weights = a.weights != nullptr ? a.weights + (size_t)bh * a.W : nullptr;
+  auto put = [&](int key, float x) {   // lanes t = 0 and 1: of keys g and g + 8
+    const int k = key + g + 8 * t;
+    if (t < 2 && k < a.W) out[k] = (weights != nullptr ? weights[k] : 0.f) + x;
+  };
+  auto step = [&](const Quarter<D, Q4>& x, int key) {
+    float c[NT][4];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
+    if constexpr (Q4) {
+      const Scale4 d0(x.d[0]), d1(x.d[1]);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const uint32_t u = x.w[0][j], v = x.w[1][j];
+        const uint32_t u0 = d0.value(u), u1 = d0.value(u >> 8), v0 = d1.value(v), v1 = d1.value(v >> 8);
+        const uint32_t u2 = d0.value(u >> 4), u3 = d0.value(u >> 12), v2 = d1.value(v >> 4), v3 = d1.value(v >> 12);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          mma_bf16(c[m], u0, v0, u1, v1, q[m][2 * j][0], q[m][2 * j][1]);
+          mma_bf16(c[m], u2, v2, u3, v3, q[m][2 * j + 1][0], q[m][2 * j + 1][1]);
+        }
+      }
+    } else {
+      const float f0 = __half2float(__ushort_as_half(x.d[0])), f1 = __half2float(__ushort_as_half(x.d[1]));
+      const uint64_t d0 = f32x2(f0, f0), d1 = f32x2(f1, f1);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const uint32_t u = x.w[0][j] ^ 0x80808080u, v = x.w[1][j] ^ 0x80808080u;
+        const uint32_t u0 = value_q8(u, 0, d0), u1 = value_q8(u, 2, d0), v0 = value_q8(v, 0, d1), v1 = value_q8(v, 2, d1);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) mma_bf16(c[m], u0, v0, u1, v1, q[m][j][0], q[m][j][1]);
+      }
+    }
+    const bool edge = key + kRun - 1 > before || (a.window > 0 && before + n - 1 - key > a.window);   // some token does not see all 16
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float p = ex2_approx(fmaf(c[m][j], a.sl2, less[m][j & 1]));
+        if (edge) {
+          const int k = key + g + 8 * (j >> 1), at = pos[m][j & 1];
+          if (k > at || (a.window > 0 && at - k > a.window)) p = 0.f;
+        }
+        sum[j >> 1] += p;
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    }
+    put(key, t == 0 ? sum[0] : sum[1]);
+  };
+  const int all = (int)min((long long)key0 + runs * kRun, (a.W + kRun - 1) / kRun * kRun);
+  for (int key = key0; key < min(first, all); key += kRun) put(key, 0.f);
+  int key = first;
+  for (; key < past; key += 2 * kRun) {   // the next run on its way while one is worked on
+    if (key + kRun < past) then.load(a, row_of(key + kRun), past - key - kRun);
+    step(now, key);
+    if (key + kRun >= past) {
+      key += kRun;
+      break;
+    }
+    if (key + 2 * kRun < past) now.load(a, row_of(key + 2 * kRun), past - key - 2 * kRun);
+    step(then, key + kRun);
+  }
+  for (key = max(key, key0); key < all; key += kRun) put(key, 0.f);
+}
+
+constexpr int kUnit = 2 * kTileKeys;   // keys of a block at a time
+constexpr int kRows = 128;             // rows of a tile
+constexpr int kUnits = 4;              // descriptions of units in shared memory
+
+// What the roles of a block know of 256 keys and the rows that see one of them: rows [row0, row0 + rows) of the key/value head.
+struct Unit { int b, h, key0, before, row0, rows, padding[2]; };
+
+template <int D>
+struct WeightSmem {
+  static constexpr int kBox = 128 * 128;            // 64 features of 128 rows
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kRing = 3;                   // tiles of rows
+  static constexpr int kQOff = 4 * kTile;           // two units of keys
+  static constexpr int kLogOff = kQOff + kRing * kTile, kBarOff = kLogOff + kRing * kRows * 4;
+  static constexpr int kBytes = kBarOff + 512 + 1024;
+};
+
+template <int D, bool Q4, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ WeightArgs a, unsigned total) {
+  using L = WeightSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + L::kQOff);
+  float* sLog = reinterpret_cast<float*>(smem + L::kLogOff);   // [ring][128]: -lse, base 2; -inf in columns without a row
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* bar_k = bars;               // [2]: a unit's K written
+  uint64_t* bar_kfree = bars + 2;       // [2]: its products done
+  uint64_t* bar_q = bars + 4;           // [ring]: rows written
+  uint64_t* bar_qfree = bars + 7;       // [ring]: products done, and the rows' LSE read
+  uint64_t* bar_s = bars + 10;          // [2 tiles of keys][2]: products there
+  uint64_t* bar_sfree = bars + 14;      // [2][2]: read
+  uint64_t* bar_unit = bars + 18;       // [kUnits]: described
+  uint64_t* bar_done = bars + 22;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Unit* units = reinterpret_cast<Unit*>(smem + L::kBarOff + 256);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const unsigned heads = (unsigned)a.c.B * a.c.Hkv;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_k[i], 4);
+      mbar_init(&bar_kfree[i], 1);
+    }
+    for (int i = 0; i < L::kRing; ++i) {
+      mbar_init(&bar_q[i], 3);
+      mbar_init(&bar_qfree[i], 1 + 8);   // the products and the warps that add
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_sfree[i], 4);
+      mbar_init(&bar_unit[i], 1);
+    }
+    mbar_init(bar_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  // Unit i of those with rows is described; one without rows is the end. A description is read when its unit begins: it is
+  // written over for unit i + 4, when unit i + 2 is done, whose last products came after unit i's had been taken.
+  auto unit_there = [&](int i) { return mbar_wait_warp(&bar_unit[i % kUnits], (i / kUnits) & 1, abort_flag, a.status, 1101); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ MMAs, the lanes together
+    const uint32_t lead = lane == 0 ? 1u : 0u, idesc = idesc_bf16_f32(128, kRows, 0, 0);
+    const uint64_t dk = smem_desc_sw128(sK, 16, 1024), dq = smem_desc_sw128(sQ, 16, 1024);
+    bool ok = true;
+    int x = 0, slot = 0, laps = 0;   // tiles of rows so far; of the ring: the place, and how often it has gone round
+    for (int i = 0; ok; ++i) {
+      if (!(ok = unit_there(i))) break;
+      const int rows = __shfl_sync(0xffffffffu, units[i % kUnits].rows, 0);
+      if (rows == 0) break;
+      if (!(ok = mbar_wait_warp(&bar_k[i & 1], (i >> 1) & 1, abort_flag, a.status, 1102))) break;
+      for (int r = 0; ok && r < rows; r += kRows, ++x) {
+        if (!(ok = mbar_wait_warp(&bar_q[slot], laps & 1, abort_flag, a.status, 1103))) break;
+        for (int m = 0; ok && m < 2; ++m) {
+          const int buf = 2 * m + (x & 1);
+          if (x >= 2 && !(ok = mbar_wait_warp(&bar_sfree[buf], ((x >> 1) - 1) & 1, abort_flag, a.status, 1104))) break;
+          tc_fence_after();
+          const uint64_t k0 = desc_add(dk, (2 * (i & 1) + m) * L::kTile), q0 = desc_add(dq, slot * L::kTile);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss_if(lead, tmem + buf * kRows, desc_add(k0, (k >> 2) * L::kBox + (k & 3) * 32), desc_add(q0, (k >> 2) * L::kBox + (k & 3) * 32),
+                      idesc, k > 0 ? 1u : 0u);
+          mma_commit_if(lead, &bar_s[buf]);
+        }
+        if (!ok) break;
+        mma_commit_if(lead, &bar_qfree[slot]);
+        if (++slot == L::kRing) {
+          slot = 0;
+          ++laps;
+        }
+      }
+      if (ok) mma_commit_if(lead, &bar_kfree[i & 1]);
+    }
+    mma_commit_if(lead, bar_done);
+    mbar_wait<true>(bar_done, 0, nullptr, a.status, 1105);
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ the rows, of every tile for each of the three warps
+    constexpr int CHUNKS = D / 8, ROWS = 32 / CHUNKS, STEP = 3 * ROWS;   // 16-byte chunks of a row, rows of a load, of a step
+    const int chunk = lane % CHUNKS, r0 = (warp - 1) * ROWS + lane / CHUNKS;
+    const int tokens = STEP / a.G, over_heads = STEP % a.G;
+    const long long by_token = (long long)(a.layout ? a.Hq : 1) * D, by_head = (long long)(a.layout ? 1 : a.Sq) * D;
+    const long long on_by = tokens * by_token + over_heads * by_head, over = by_token - a.G * by_head;
+    int slot = 0, laps = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!(ok = unit_there(i))) break;
+      const Unit u = units[i % kUnits];
+      if (u.rows == 0) break;
+      for (int first = 0; first < u.rows; first += kRows) {
+        if (laps > 0 && !(ok = mbar_wait_warp(&bar_qfree[slot], (laps - 1) & 1, abort_flag, a.status, 1106))) break;
+        const int rows = u.rows - first, row = u.row0 + first + r0;
+        int head = row % a.G;
+        const __nv_bfloat16* src = a.q + ((size_t)u.b * a.Hq * a.Sq) * D + (row / a.G) * by_token + (u.h * a.G + head) * by_head + 8 * chunk;
+        const uint32_t box = sQ + slot * L::kTile + (chunk >> 3) * L::kBox;
+#pragma unroll 2
+        for (int r = r0; r < kRows; r += STEP) {   // rows behind the last are zeros
+          const bool on = r < rows;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)),
+                       "l"(on ? src : a.q), "r"(on ? 16 : 0) : "memory");
+          src += on_by;
+          head += over_heads;
+          if (head >= a.G) {
+            head -= a.G;
+            src += over;
+          }
+        }
+        for (int r = (warp - 1) * 32 + lane; r < kRows; r += 96) {
+          const int at = u.row0 + first + r, token = at / a.G;
+          sLog[slot * kRows + r] =
+              r < rows ? -__ldg(a.lse + ((size_t)u.b * a.Hq + u.h * a.G + at % a.G) * a.Sq + token) * kLog2e : -CUDART_INF_F;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (a.q_xor != 0u || a.q_and != 0xffffffffu) {   // a scale that is not positive: this lane's own chunks again
+          for (int r = r0; r < kRows; r += STEP) {
+            const uint32_t at = box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+            const float4 f = ld_shared_f4(at);
+            st_shared_v4(at, (__float_as_uint(f.x) & a.q_and) ^ a.q_xor, (__float_as_uint(f.y) & a.q_and) ^ a.q_xor,
+                         (__float_as_uint(f.z) & a.q_and) ^ a.q_xor, (__float_as_uint(f.w) & a.q_and) ^ a.q_xor);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_q[slot]);
+        if (++slot == L::kRing) {
+          slot = 0;
+          ++laps;
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ the units, and their K
+    const int w = warp - 4;
+    int i = 0;
+    bool ok = true;
+    for (unsigned id = blockIdx.x; ok && id < total; id += gridDim.x) {
+      const int bh = id % heads, b = bh / a.c.Hkv, h = bh % a.c.Hkv, key0 = (int)(id / heads) * kUnit;
+      int len, n;
+      read_lengths(a, b, key0 == 0 && h == 0 && w == 0 && lane == 0, len, n);
+      const int before = len - n, first = max(key0 - before, 0);   // tokens [first, last] see one of the keys
+      const int last = a.window > 0 ? min(n - 1, min(key0 + kUnit, len) - 1 + a.window - before) : n - 1;
+      const int row0 = first * a.G, rows = key0 < len ? max((last + 1) * a.G - row0, 0) : 0;
+      if (rows == 0) {   // nobody sees them
+        for (int k = w * 32 + lane; k < kUnit; k += 128) {
+          const size_t at = (size_t)bh * a.W + key0 + k;
+          if (key0 + k < a.W) a.out[at] = a.weights != nullptr ? a.weights[at] : 0.f;
+        }
+        continue;
+      }
+      if (i >= 2 && !(ok = mbar_wait_warp(&bar_kfree[i & 1], ((i >> 1) - 1) & 1, abort_flag, a.status, 1107))) break;
+      if (w == 0 && lane == 0) {
+        units[i % kUnits] = Unit{b, h, key0, before, row0, rows, {0, 0}};
+        mbar_arrive(&bar_unit[i % kUnits]);
+      }
+      RunBytes<D, Q4> k[2];   // a warp's four runs, two of them on their way at a time
+      auto load = [&](int r) {
+        const int run = key0 + kRun * (4 * w + r);
+        long long row = -1;
+        if (run < len) row = PAGED ? page_row(a.pages, a.c.Hkv, b, h, run, lane == 0 ? a.status : nullptr) : (long long)bh * a.c.S + run;
+        k[r & 1].load(a.c.k_q, a.c.k_d, row, len - run);
+      };
+      load(0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r < 3) load(r + 1);
+        const int run = 4 * w + r;
+        k[r & 1].store(sK + (2 * (i & 1) + run / 8) * L::kTile, run % 8, false);
+      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_k);
+      if (lane == 0) mbar_arrive(&bar_k[i & 1]);
+      ++i;
     }
-    if (warp < 4) {
-      const int key = key0 + 32 * warp + lane;
-      const uint32_t tS = tmem + ((uint32_t)(warp * 32) << 16);
-      const uint64_t sl2 = f32x2(a.sl2, a.sl2);
-      for (int i = 0; i < tiles; ++i) {
-        const int buf = i & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait<true>(&bar_s[buf], (i >> 1) & 1, abort_flag, a.status, 1101))) break;
+    if (ok && i >= 2) ok = mbar_wait_warp(&bar_kfree[i & 1], ((i >> 1) - 1) & 1, abort_flag, a.status, 1107);
+    if (w == 0 && lane == 0) {   // the end
+      units[i % kUnits].rows = 0;
+      mbar_arrive(&bar_unit[i % kUnits]);
+    }
+  } else {
+    // ------------------------------------------------------------------ exponentials and sums, a key for each thread
+    const int m = (warp - 8) / 4, wq = warp & 3;
+    const uint32_t tS = tmem + 2 * m * kRows + ((uint32_t)(wq * 32) << 16);
+    const uint64_t sl2 = f32x2(a.sl2, a.sl2);
+    int x = 0, slot = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!(ok = unit_there(i))) break;
+      const Unit u = units[i % kUnits];
+      if (u.rows == 0) break;
+      const int key = u.key0 + m * kTileKeys + wq * 32 + lane;
+      const size_t at = ((size_t)u.b * a.c.Hkv + u.h) * a.W + key;
+      const float had = a.weights != nullptr && key < a.W ? a.weights[at] : 0.f;
+      float sum = 0.f;
+      for (int first = 0; first < u.rows; first += kRows, ++x) {
+        const int buf = x & 1, here = min(u.rows - first, kRows);
+        if (!(ok = mbar_wait_warp(&bar_s[2 * m + buf], (x >> 1) & 1, abort_flag, a.status, 1108))) break;
         tc_fence_after();
-        const float* log = sLog + buf * NQ;
-        const int* pos = sPos + buf * NQ;
-        const int here = min(rows - i * NQ, NQ);
-        const bool edge = pos[0] < key0 + kTileKeys - 1 || (a.window > 0 && pos[here - 1] - key0 > a.window);
+        const float* log = sLog + slot * kRows;
+        const int row = u.row0 + first;
+        const int pos0 = u.before + row / a.G, pos1 = u.before + (row + here - 1) / a.G;   // of the first and the last row's token
+        const bool edge = pos0 < u.key0 + (m + 1) * kTileKeys - 1 || (a.window > 0 && pos1 - (u.key0 + m * kTileKeys) > a.window);
         uint64_t part[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-        auto add = [&](const auto& raw, int c0, auto on_edge) {
-          constexpr int N = sizeof(raw) / 4;
-#pragma unroll
-          for (int e = 0; e < N; e += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(log + c0 + e);
-            const float gs[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              float t0, t1;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[e + k]), __uint_as_float(raw[e + k + 1])), sl2, f32x2(gs[k], gs[k + 1])), t0, t1);
-              float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-              if constexpr (decltype(on_edge)::value) {
-                const int at0 = pos[c0 + e + k], at1 = pos[c0 + e + k + 1];
-                if (key > at0 || (a.window > 0 && at0 - key > a.window)) p0 = 0.f;
-                if (key > at1 || (a.window > 0 && at1 - key > a.window)) p1 = 0.f;
-              }
-              part[k / 2] = add_f32x2(part[k / 2], f32x2(p0, p1));
-            }
-          }
-        };
-        auto all = [&](auto on_edge) {
-          if constexpr (NQ == 16) {
-            uint32_t raw[16];
-            tmem_ld16(tS + buf * STEP, raw);
-            tmem_wait_ld();
-            reg_fence16(raw);
-            add(raw, 0, on_edge);
-          } else {
+        int pos = pos0, head = row % a.G;   // of the column at hand, where some pairs are hidden
+        auto add = [&](auto on_edge) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < here; c0 += 32) {
-              uint32_t raw[32];
-              tmem_ld32(tS + buf * STEP + c0, raw);
-              tmem_wait_ld();
-              reg_fence(raw);
-              add(raw, c0, on_edge);
+          for (int c0 = 0; c0 < here; c0 += 32) {
+            uint32_t raw[32];
+            tmem_ld32(tS + buf * kRows + c0, raw);
+            tmem_wait_ld();
+            reg_fence(raw);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 g = *reinterpret_cast<const float4*>(log + c0 + e);
+              float p[4];
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), sl2, f32x2(g.x, g.y)), p[0], p[1]);
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), sl2, f32x2(g.z, g.w)), p[2], p[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                p[k] = ex2_approx(p[k]);
+                if constexpr (decltype(on_edge)::value) {   // hidden: no weight, whatever came out
+                  if (key > pos || (a.window > 0 && pos - key > a.window)) p[k] = 0.f;
+                  if (++head == a.G) {
+                    head = 0;
+                    ++pos;
+                  }
+                }
+              }
+              part[0] = add_f32x2(part[0], f32x2(p[0], p[1]));
+              part[1] = add_f32x2(part[1], f32x2(p[2], p[3]));
             }
           }
         };
-        if (edge) all(std::true_type{});
-        else all(std::false_type{});
+        if (edge) add(std::true_type{});
+        else add(std::false_type{});
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_free[buf]);
+        if (lane == 0) {
+          mbar_arrive(&bar_sfree[2 * m + buf]);
+          mbar_arrive(&bar_qfree[slot]);
+        }
+        slot = slot == L::kRing - 1 ? 0 : slot + 1;
         float s0, s1, s2, s3;
         f32x2_split(part[0], s0, s1);
         f32x2_split(part[1], s2, s3);
         sum += (s0 + s1) + (s2 + s3);
       }
-    } else if (warp < 8) {
-      const int r = threadIdx.x - 128;   // the row of a tile that this thread brings
-      for (int i = 0; i < tiles; ++i) {
-        const int buf = i & 1;
-        if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait<true>(&bar_free[buf], ((i >> 1) - 1) & 1, abort_flag, a.status, 1102))) break;
-        if (r < NQ) {
-          const int row = row0 + i * NQ + r, token = row / a.G;
-          const bool on = i * NQ + r < rows;
-          const int head = h * a.G + row % a.G;
-          const size_t at = on ? (a.layout ? ((size_t)b * a.Sq + token) * a.Hq + head : ((size_t)b * a.Hq + head) * a.Sq + token) * D : 0;
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + at);
-          const uint32_t dst = sQ + buf * L::kQ + r * 128;
-          const float log = on ? __ldg(a.lse + ((size_t)b * a.Hq + head) * a.Sq + token) : 0.f;
-#pragma unroll
-          for (int c0 = 0; c0 < D / 8; c0 += 8) {
-            uint4 u[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) u[c] = on ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              st_shared_v4(dst + (c0 / 8) * L::kQBox + ((c ^ (r & 7)) << 4), (u[c].x & a.q_and) ^ a.q_xor,
-                           (u[c].y & a.q_and) ^ a.q_xor, (u[c].z & a.q_and) ^ a.q_xor, (u[c].w & a.q_and) ^ a.q_xor);
-          }
-          sLog[buf * NQ + r] = on ? -log * kLog2e : -CUDART_INF_F;
-          sPos[buf * NQ + r] = on ? before + token : -1;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_q[buf]);
-      }
-    } else if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, NQ, 0, 0);
-      bool ok = mbar_wait<true>(bar_k, 0, abort_flag, a.status, 1103);
-      const uint64_t dk0 = smem_desc_sw128(sK, 16, 1024);
-      for (int i = 0; ok && i < tiles; ++i) {
-        const int buf = i & 1;
-        if (!(ok = mbar_wait<true>(&bar_q[buf], (i >> 1) & 1, abort_flag, a.status, 1104))) break;
-        tc_fence_after();
-        const uint64_t dq0 = smem_desc_sw128(sQ + buf * L::kQ, 16, 1024);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + buf * STEP, desc_add(dk0, (k >> 2) * L::kBox + (k & 3) * 32),
-                 desc_add(dq0, (k >> 2) * L::kQBox + (k & 3) * 32), idesc, k > 0 ? 1u : 0u);
-        mma_commit(&bar_s[buf]);
-      }
-      mma_commit(bar_done);
-      mbar_wait<true>(bar_done, 0, nullptr, a.status, 1105);
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 8) {
-      tc_fence_after();
-      tmem_dealloc(tmem, L::kColumns);
+      if (ok && key < a.W) a.out[at] = had + sum;
     }
   }
-  const long long key = (long long)key0 + threadIdx.x;
-  if (warp < 4 && key < a.W) {
-    const size_t at = (size_t)bh * a.W + key;
-    a.out[at] = (a.weights != nullptr ? a.weights[at] : 0.f) + sum;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, bool Q4, bool PAGED, int NQ>
-cudaError_t launch_weights(const WeightArgs& a, unsigned blocks, cudaStream_t st) {
-  constexpr int bytes = WeightSmem<D, NQ>::kBytes;
-  auto kernel = weights_kernel<D, Q4, PAGED, NQ>;
+template <int D, bool Q4, bool PAGED, int NT>
+cudaError_t launch_weights_few(const WeightArgs& a, long long heads, cudaStream_t st) {
+  // 256 keys a warp, so that what comes before the first costs little, where that leaves eight warps for each SM at least, else 64
+  const int runs = heads * ((a.W + 255) / 256) >= 8LL * sm_count() ? 16 : 4;
+  const long long chunks = (a.W + runs * kRun - 1) / (runs * kRun), warps = heads * chunks;
+  if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  weights_few_kernel<D, Q4, PAGED, NT><<<(unsigned)((warps + 3) / 4), 128, 0, st>>>(a, runs, (unsigned)chunks, (unsigned)warps);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <int D, bool Q4, bool PAGED>
+cudaError_t launch_weights(const WeightArgs& a, long long heads, cudaStream_t st) {
+  constexpr int bytes = WeightSmem<D>::kBytes;
+  static_assert(bytes <= 232448, "shared memory of a block");
+  auto kernel = weights_kernel<D, Q4, PAGED>;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(kernel, bytes, allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<blocks, kThreads, bytes, st>>>(a);
+  const long long total = heads * ((a.W + kUnit - 1) / kUnit);
+  if (total > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned blocks = (unsigned)(total < sm_count() ? total : sm_count());
+  kernel<<<blocks, kThreads, bytes, st>>>(a, (unsigned)total);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -269,9 +572,8 @@ extern "C" fa_status fa_cache_weights(const fa_prefill_params* p, const void* q,
   if (st != FA_OK) return st;
   if ((st = check_chunk(p, cv)) != FA_OK) return st;
   const long long heads = (long long)cv.B * cv.Hkv;
-  if (W < 1 || W > (1LL << 31) - kTileKeys) { set_error("W=%lld outside [1, 2^31 - 128]", (long long)W); return FA_ERR_INVALID_ARG; }
-  const long long blocks = (W + kTileKeys - 1) / kTileKeys * heads;
-  if (blocks > 0x7fffffffLL) { set_error("too many keys for one launch"); return FA_ERR_UNSUPPORTED; }
+  if (W < 1 || W > 1LL << 30) { set_error("W=%lld outside [1, 2^30]", (long long)W); return FA_ERR_INVALID_ARG; }
+  if ((W + 63) / 64 * heads > 0x7fffffffLL) { set_error("too many keys for one launch"); return FA_ERR_UNSUPPORTED; }   // of 64 at least
   const size_t rows = (size_t)cv.B * p->Hq * p->Sq, bytes = (size_t)heads * (size_t)W * 4;
   cache_spans(held, planes);
   in[0] = planes[0];
@@ -309,14 +611,18 @@ extern "C" fa_status fa_cache_weights(const fa_prefill_params* p, const void* q,
   a.window = p->window < 2 * kMaxSeq ? p->window : 2 * kMaxSeq;
   a.layout = p->layout;
   a.G = p->Hq / cv.Hkv;
-  const bool few = (long long)a.G * p->Sq <= 16;
+  const long long rows_of_head = (long long)a.G * p->Sq;
   auto go = [&](auto dim, auto q4) {
     constexpr int D = decltype(dim)::value;
     constexpr bool Q4 = decltype(q4)::value;
-    const unsigned n = (unsigned)blocks;
     cudaStream_t cs = (cudaStream_t)stream;
-    if (pages != nullptr) return few ? launch_weights<D, Q4, true, 16>(a, n, cs) : launch_weights<D, Q4, true, 128>(a, n, cs);
-    return few ? launch_weights<D, Q4, false, 16>(a, n, cs) : launch_weights<D, Q4, false, 128>(a, n, cs);
+    auto of = [&](auto paged) {
+      constexpr bool P = decltype(paged)::value;
+      if (rows_of_head <= 8) return launch_weights_few<D, Q4, P, 1>(a, heads, cs);
+      if (rows_of_head <= 16) return launch_weights_few<D, Q4, P, 2>(a, heads, cs);
+      return launch_weights<D, Q4, P>(a, heads, cs);
+    };
+    return pages != nullptr ? of(std::true_type{}) : of(std::false_type{});
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;

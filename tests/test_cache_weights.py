@@ -74,6 +74,10 @@ SHAPES = {
     "window_of_one": (1, 3, 1, 300, 128, 300, 16, [300], None, 1),
     "group_of_300": (1, 300, 1, 90, 64, 3, 16, [77], None, 0),
     "many_rows": (1, 8, 1, 256, 64, 250, 16, [256], None, 0),
+    "nine_rows": (3, 9, 1, 130, 64, 1, 16, [130, 1, 33], None, 0),
+    "sixteen_rows_in_a_window": (2, 8, 2, 400, 128, 4, 48, [399, 77], [4, 1], 50),
+    "many_heads": (60, 8, 4, 300, 64, 3, 16, [1 + (37 * i) % 300 for i in range(60)], [i % 4 for i in range(60)], 0),
+    "several_units_a_block": (4, 20, 20, 900, 64, 40, 64, [900, 257, 0, 600], [40, 33, 0, 40], 300),
 }
 
 
@@ -205,11 +209,11 @@ def test_c_abi_refuses_buffers_of_weights():
     t = ft.FaPages(5 * F, 4, 2, 4)
     go = lambda q=6 * F, lse=7 * F, n=None, m=None, w=None, W=64, out=8 * F: lib.fa_cache_weights(  # noqa: E731
         R(p), q, lse, R(c), R(t), n, m, w, W, out, None)
-    assert go(q=None) == 1 and go(lse=None) == 1 and go(out=None) == 1 and go(out=8 * F + 4) == 1 and go(W=0) == 1 and go(W=1 << 31) == 1
+    assert go(q=None) == 1 and go(lse=None) == 1 and go(out=None) == 1 and go(out=8 * F + 4) == 1 and go(W=0) == 1 and go(W=(1 << 30) + 1) == 1
     assert go(n=10 * F + 4) == 1 and go(m=10 * F + 4) == 1 and go(w=9 * F + 8) == 1 and go(w=8 * F + 16) == 1 and go(out=F) == 1
     assert go(out=6 * F) == 1 and go(out=7 * F) == 1 and go(out=5 * F) == 1 and go(n=8 * F) == 1 and go(m=8 * F) == 1
     t.B, t.stride = 65535, 4
-    assert go(W=(1 << 31) - 128) == ft.FA_ERR_UNSUPPORTED
+    assert go(W=1 << 30) == ft.FA_ERR_UNSUPPORTED
     assert lib.fa_cache_weights(None, 6 * F, 7 * F, R(c), R(t), None, None, None, 64, 8 * F, None) == 1
 
 
