@@ -139,8 +139,13 @@ __global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant_
     if constexpr (!PAGED) return (long long)bh * a.c.S + key;
     return row_in_page(a.pages, __shfl_sync(0xffffffffu, entry, (key - key0) / kRun), a.c.Hkv, h, key, lane == 0 ? a.status : nullptr);
   };
-  Quarter<D, Q4> now, then;
-  if (first < past) now.load(a, row_of(first), past - first);
+  // Groups of four runs from the chunk's beginning; `from`: the first group with a run to do.
+  const int from = key0 + ((first - key0) & ~(4 * kRun - 1));
+  Quarter<D, Q4> ring[2];   // a run worked on, the next on its way
+  auto load = [&](Quarter<D, Q4>& x, int key) {
+    if (key < past) x.load(a, key < first ? -1 : row_of(key), past - key);
+  };
+  if (first < past) load(ring[0], from);
 
   // q: of row 8 m + g this lane's quarter, as the steps take it; of rows 8 m + 2 t and the next their LSE and position
   uint32_t q[NT][STEPS][2];
@@ -177,11 +182,7 @@ __global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant_
 
   float* out = a.out + (size_t)bh * a.W;
   const float* weights = a.weights != nullptr ? a.weights + (size_t)bh * a.W : nullptr;
-  auto put = [&](int key, float x) {   // lanes t = 0 and 1: of keys g and g + 8
-    const int k = key + g + 8 * t;
-    if (t < 2 && k < a.W) out[k] = (weights != nullptr ? weights[k] : 0.f) + x;
-  };
-  auto step = [&](const Quarter<D, Q4>& x, int key) {
+  auto step = [&](const Quarter<D, Q4>& x, int key, float& kept0, float& kept1, bool keep) {
     float c[NT][4];
 #pragma unroll
     for (int m = 0; m < NT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
@@ -227,22 +228,29 @@ __global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant_
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
       sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
     }
-    put(key, t == 0 ? sum[0] : sum[1]);
-  };
-  const int all = (int)min((long long)key0 + runs * kRun, (a.W + kRun - 1) / kRun * kRun);
-  for (int key = key0; key < min(first, all); key += kRun) put(key, 0.f);
-  int key = first;
-  for (; key < past; key += 2 * kRun) {   // the next run on its way while one is worked on
-    if (key + kRun < past) then.load(a, row_of(key + kRun), past - key - kRun);
-    step(now, key);
-    if (key + kRun >= past) {
-      key += kRun;
-      break;
+    if (keep) {
+      kept0 = sum[0];
+      kept1 = sum[1];
     }
-    if (key + 2 * kRun < past) now.load(a, row_of(key + 2 * kRun), past - key - 2 * kRun);
-    step(then, key + kRun);
+  };
+  // Lane (g, t) has what there was, and what is added, of keys g and g + 8 of run t of a group.
+  const int all = (int)min((long long)key0 + runs * kRun, a.W);
+  for (int key = key0; key < all; key += 4 * kRun) {
+    const int k0 = key + kRun * t + g, k1 = k0 + 8;
+    const float had0 = weights != nullptr && k0 < all ? weights[k0] : 0.f, had1 = weights != nullptr && k1 < all ? weights[k1] : 0.f;
+    float sum0 = 0.f, sum1 = 0.f;
+    if (key >= from && key < past) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = key + i * kRun;
+        if (at >= past) break;
+        load(ring[(i + 1) & 1], at + kRun);
+        if (at >= first) step(ring[i & 1], at, sum0, sum1, t == i);
+      }
+    }
+    if (k0 < all) out[k0] = had0 + sum0;
+    if (k1 < all) out[k1] = had1 + sum1;
   }
-  for (key = max(key, key0); key < all; key += kRun) put(key, 0.f);
 }
 
 constexpr int kUnit = 2 * kTileKeys;   // keys of a block at a time
@@ -355,8 +363,27 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     const long long by_token = (long long)(a.layout ? a.Hq : 1) * D, by_head = (long long)(a.layout ? 1 : a.Sq) * D;
     const long long on_by = tokens * by_token + over_heads * by_head, over = by_token - a.G * by_head;
     int slot = 0, laps = 0;
+    int last = -1, last_rows = 0;   // the tile before, of which the copies are still on their way: its place, and its rows
     bool ok = true;
+    auto complete = [&] {
+      for (int r = (warp - 1) * 32 + lane; r < kRows; r += 96) {
+        float& x = sLog[last * kRows + r];
+        x = r < last_rows ? -x * kLog2e : -CUDART_INF_F;
+      }
+      if (a.q_xor != 0u || a.q_and != 0xffffffffu) {   // a scale that is not positive: this lane's own chunks again
+        for (int r = r0; r < kRows; r += STEP) {
+          const uint32_t at = sQ + last * L::kTile + (chunk >> 3) * L::kBox + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+          const float4 f = ld_shared_f4(at);
+          st_shared_v4(at, (__float_as_uint(f.x) & a.q_and) ^ a.q_xor, (__float_as_uint(f.y) & a.q_and) ^ a.q_xor,
+                       (__float_as_uint(f.z) & a.q_and) ^ a.q_xor, (__float_as_uint(f.w) & a.q_and) ^ a.q_xor);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_q[last]);
+    };
     for (int i = 0; ok; ++i) {
+      // The next unit is described when the one before the last is done, whatever tile is still on its way here.
       if (!(ok = unit_there(i))) break;
       const Unit u = units[i % kUnits];
       if (u.rows == 0) break;
@@ -378,29 +405,23 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             src += over;
           }
         }
-        for (int r = (warp - 1) * 32 + lane; r < kRows; r += 96) {
-          const int at = u.row0 + first + r, token = at / a.G;
-          sLog[slot * kRows + r] =
-              r < rows ? -__ldg(a.lse + ((size_t)u.b * a.Hq + u.h * a.G + at % a.G) * a.Sq + token) * kLog2e : -CUDART_INF_F;
+        for (int r = (warp - 1) * 32 + lane; r < min(rows, kRows); r += 96) {
+          const int at = u.row0 + first + r;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sLog + slot * kRows + r)),
+                       "l"(a.lse + ((size_t)u.b * a.Hq + u.h * a.G + at % a.G) * a.Sq + at / a.G) : "memory");
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (a.q_xor != 0u || a.q_and != 0xffffffffu) {   // a scale that is not positive: this lane's own chunks again
-          for (int r = r0; r < kRows; r += STEP) {
-            const uint32_t at = box + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-            const float4 f = ld_shared_f4(at);
-            st_shared_v4(at, (__float_as_uint(f.x) & a.q_and) ^ a.q_xor, (__float_as_uint(f.y) & a.q_and) ^ a.q_xor,
-                         (__float_as_uint(f.z) & a.q_and) ^ a.q_xor, (__float_as_uint(f.w) & a.q_and) ^ a.q_xor);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_q[slot]);
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+        if (last >= 0) complete();
+        last = slot;
+        last_rows = rows;
         if (++slot == L::kRing) {
           slot = 0;
           ++laps;
         }
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (last >= 0) complete();
   } else if (warp < 8) {
     // ------------------------------------------------------------------ the units, and their K
     const int w = warp - 4;
@@ -474,37 +495,47 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const bool edge = pos0 < u.key0 + (m + 1) * kTileKeys - 1 || (a.window > 0 && pos1 - (u.key0 + m * kTileKeys) > a.window);
         uint64_t part[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         int pos = pos0, head = row % a.G;   // of the column at hand, where some pairs are hidden
-        auto add = [&](auto on_edge) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < here; c0 += 32) {
-            uint32_t raw[32];
-            tmem_ld32(tS + buf * kRows + c0, raw);
-            tmem_wait_ld();
-            reg_fence(raw);
+        auto add = [&](const uint32_t (&raw)[32], int c0, auto on_edge) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 g = *reinterpret_cast<const float4*>(log + c0 + e);
-              float p[4];
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), sl2, f32x2(g.x, g.y)), p[0], p[1]);
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), sl2, f32x2(g.z, g.w)), p[2], p[3]);
+          for (int e = 0; e < 32; e += 4) {
+            const float4 g = *reinterpret_cast<const float4*>(log + c0 + e);
+            float p[4];
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), sl2, f32x2(g.x, g.y)), p[0], p[1]);
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), sl2, f32x2(g.z, g.w)), p[2], p[3]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                p[k] = ex2_approx(p[k]);
-                if constexpr (decltype(on_edge)::value) {   // hidden: no weight, whatever came out
-                  if (key > pos || (a.window > 0 && pos - key > a.window)) p[k] = 0.f;
-                  if (++head == a.G) {
-                    head = 0;
-                    ++pos;
-                  }
+            for (int k = 0; k < 4; ++k) {
+              p[k] = ex2_approx(p[k]);
+              if constexpr (decltype(on_edge)::value) {   // hidden: no weight, whatever came out
+                if (key > pos || (a.window > 0 && pos - key > a.window)) p[k] = 0.f;
+                if (++head == a.G) {
+                  head = 0;
+                  ++pos;
                 }
               }
-              part[0] = add_f32x2(part[0], f32x2(p[0], p[1]));
-              part[1] = add_f32x2(part[1], f32x2(p[2], p[3]));
             }
+            part[0] = add_f32x2(part[0], f32x2(p[0], p[1]));
+            part[1] = add_f32x2(part[1], f32x2(p[2], p[3]));
           }
         };
-        if (edge) add(std::true_type{});
-        else add(std::false_type{});
+        uint32_t raw[2][32];
+        tmem_ld32(tS + buf * kRows, raw[0]);
+        if (edge) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < here; c0 += 32) {
+            tmem_wait_ld();
+            reg_fence(raw[0]);
+            add(raw[0], c0, std::true_type{});
+            if (c0 + 32 < here) tmem_ld32(tS + buf * kRows + c0 + 32, raw[0]);
+          }
+        } else {   // all 128 columns, those without a row too: the next ones on their way meanwhile
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld();
+            reg_fence(raw[c & 1]);
+            if (c < 3) tmem_ld32(tS + buf * kRows + 32 * (c + 1), raw[(c + 1) & 1]);
+            add(raw[c & 1], 32 * c, std::false_type{});
+          }
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -530,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 
 template <int D, bool Q4, bool PAGED, int NT>
 cudaError_t launch_weights_few(const WeightArgs& a, long long heads, cudaStream_t st) {
-  // 256 keys a warp, so that what comes before the first costs little, where that leaves eight warps for each SM at least, else 64
+  // 256 keys a warp, so that what comes before the first costs little, where that leaves eight warps for each SM at least, else 64 (groups of four runs)
   const int runs = heads * ((a.W + 255) / 256) >= 8LL * sm_count() ? 16 : 4;
   const long long chunks = (a.W + runs * kRun - 1) / (runs * kRun), warps = heads * chunks;
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
