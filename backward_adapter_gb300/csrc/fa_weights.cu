@@ -11,8 +11,8 @@
 //
 // More rows: a block has 256 keys at a time, two tiles of 128, made bf16 operands once (kv_tile.cuh), and all rows that see one
 // of them go by, 128 at a time, which halves what the blocks read of Q from L2 against 128 keys. A block stays on its SM for all
-// its keys: warps 4-7 make the next 256 operands meanwhile, warps 1-3 bring the rows into a ring, warp 0 issues the MMAs, and
-// warps 8-15 own a key for each thread and add up; each tile's products are in two buffers.
+// its keys: warps 1-7 bring the rows into a ring and make the operands of the next 256 keys in between, warp 0 issues the MMAs,
+// and warps 8-15 own a key for each thread and add up; each tile's products are in two buffers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,6 +31,7 @@ using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 512;
+constexpr int kLoaders = 7;             // warps that bring rows and make operands
 
 struct WeightArgs {
   CacheView c;
@@ -294,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_k[i], 4);
+      mbar_init(&bar_k[i], kLoaders);
       mbar_init(&bar_kfree[i], 1);
     }
     for (int i = 0; i < L::kRing; ++i) {
-      mbar_init(&bar_q[i], 3);
+      mbar_init(&bar_q[i], kLoaders);
       mbar_init(&bar_qfree[i], 1 + 8);   // the products and the warps that add
     }
     for (int i = 0; i < 4; ++i) {
@@ -355,18 +356,69 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     mma_commit_if(lead, bar_done);
     mbar_wait<true>(bar_done, 0, nullptr, a.status, 1105);
     __syncwarp();
-  } else if (warp < 4) {
-    // ------------------------------------------------------------------ the rows, of every tile for each of the three warps
-    constexpr int CHUNKS = D / 8, ROWS = 32 / CHUNKS, STEP = 3 * ROWS;   // 16-byte chunks of a row, rows of a load, of a step
-    const int chunk = lane % CHUNKS, r0 = (warp - 1) * ROWS + lane / CHUNKS;
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ the units, their K, and the rows: a part of each for every warp
+    constexpr int CHUNKS = D / 8, ROWS = 32 / CHUNKS, STEP = kLoaders * ROWS;   // 16-byte chunks of a row, rows of a load, of a step
+    const int w = warp - 1, me = w * 32 + lane;
+    const int chunk = lane % CHUNKS, r0 = w * ROWS + lane / CHUNKS;
     const int tokens = STEP / a.G, over_heads = STEP % a.G;
     const long long by_token = (long long)(a.layout ? a.Hq : 1) * D, by_head = (long long)(a.layout ? 1 : a.Sq) * D;
     const long long on_by = tokens * by_token + over_heads * by_head, over = by_token - a.G * by_head;
     int slot = 0, laps = 0;
     int last = -1, last_rows = 0;   // the tile before, of which the copies are still on their way: its place, and its rows
     bool ok = true;
+    unsigned id = blockIdx.x;
+    int units_so_far = 0, len = 0;
+    // The next unit with rows, its place described, its K made; the end where there is none. It takes the place of the unit two
+    // before, whose products have to be done.
+    auto next_unit = [&](Unit& u) -> bool {
+      u.rows = 0;
+      for (; id < total && u.rows == 0; id += gridDim.x) {
+        const int bh = id % heads, b = bh / a.c.Hkv, h = bh % a.c.Hkv, key0 = (int)(id / heads) * kUnit;
+        int n;
+        read_lengths(a, b, key0 == 0 && h == 0 && me == 0, len, n);
+        const int before = len - n, first = max(key0 - before, 0);   // tokens [first, past) see one of the keys
+        const int past = a.window > 0 ? min(n, min(key0 + kUnit, len) + a.window - before) : n;
+        u = Unit{b, h, key0, before, first * a.G, key0 < len ? max(past - first, 0) * a.G : 0, {0, 0}};
+        if (u.rows == 0) {   // nobody sees them
+          for (int k = me; k < kUnit; k += 32 * kLoaders) {
+            const size_t at = (size_t)bh * a.W + key0 + k;
+            if (key0 + k < a.W) a.out[at] = a.weights != nullptr ? a.weights[at] : 0.f;
+          }
+        }
+      }
+      const int i = units_so_far++;
+      if (i >= 2 && !(ok = mbar_wait_warp(&bar_kfree[i & 1], ((i >> 1) - 1) & 1, abort_flag, a.status, 1107))) return false;
+      if (me == 0) {
+        units[i % kUnits] = u;
+        mbar_arrive(&bar_unit[i % kUnits]);
+      }
+      if (u.rows == 0) return false;
+      RunBytes<D, Q4> k[2];
+      auto load = [&](RunBytes<D, Q4>& x, int r) {
+        if (r >= kUnit / kRun) return;
+        const int run = u.key0 + kRun * r;
+        long long row = -1;
+        if (run < len) row = PAGED ? page_row(a.pages, a.c.Hkv, u.b, u.h, run, lane == 0 ? a.status : nullptr) : ((long long)u.b * a.c.Hkv + u.h) * a.c.S + run;
+        x.load(a.c.k_q, a.c.k_d, row, len - run);
+      };
+      auto store = [&](const RunBytes<D, Q4>& x, int r) {
+        if (r < kUnit / kRun) x.store(sK + (2 * (i & 1) + r / 8) * L::kTile, r % 8, false);
+      };
+      static_assert(kUnit / kRun <= 3 * kLoaders, "a warp has three runs at most");
+      load(k[0], w);
+      load(k[1], w + kLoaders);
+      store(k[0], w);
+      load(k[0], w + 2 * kLoaders);
+      store(k[1], w + kLoaders);
+      store(k[0], w + 2 * kLoaders);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_k[i & 1]);
+      return true;
+    };
     auto complete = [&] {
-      for (int r = (warp - 1) * 32 + lane; r < kRows; r += 96) {
+      for (int r = me; r < kRows; r += 32 * kLoaders) {
         float& x = sLog[last * kRows + r];
         x = r < last_rows ? -x * kLog2e : -CUDART_INF_F;
       }
@@ -381,14 +433,20 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_q[last]);
+      last = -1;
     };
-    for (int i = 0; ok; ++i) {
-      // The next unit is described when the one before the last is done, whatever tile is still on its way here.
-      if (!(ok = unit_there(i))) break;
-      const Unit u = units[i % kUnits];
-      if (u.rows == 0) break;
+    Unit u, then;
+    bool has = next_unit(u);
+    while (has && ok) {
+      bool prepared = false, more = false;
       for (int first = 0; first < u.rows; first += kRows) {
-        if (laps > 0 && !(ok = mbar_wait_warp(&bar_qfree[slot], (laps - 1) & 1, abort_flag, a.status, 1106))) break;
+        if (laps > 0) {
+          if (last >= 0 && !__all_sync(0xffffffffu, mbar_test(&bar_qfree[slot], (laps - 1) & 1))) {   // no place yet: see the last tile in first
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            complete();
+          }
+          if (!(ok = mbar_wait_warp(&bar_qfree[slot], (laps - 1) & 1, abort_flag, a.status, 1106))) break;
+        }
         const int rows = u.rows - first, row = u.row0 + first + r0;
         int head = row % a.G;
         const __nv_bfloat16* src = a.q + ((size_t)u.b * a.Hq * a.Sq) * D + (row / a.G) * by_token + (u.h * a.G + head) * by_head + 8 * chunk;
@@ -405,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             src += over;
           }
         }
-        for (int r = (warp - 1) * 32 + lane; r < min(rows, kRows); r += 96) {
+        for (int r = me; r < min(rows, kRows); r += 32 * kLoaders) {
           const int at = u.row0 + first + r;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sLog + slot * kRows + r)),
                        "l"(a.lse + ((size_t)u.b * a.Hq + u.h * a.G + at % a.G) * a.Sq + at / a.G) : "memory");
@@ -418,58 +476,22 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           slot = 0;
           ++laps;
         }
+        // The next unit when this one's fourth tile is on its way: the products of the one before are done then, as the first
+        // tile's place was free. Where there are not so many tiles, they are all there before it is waited for that.
+        if (!prepared && (first == 3 * kRows || first + kRows >= u.rows)) {
+          if (first < 3 * kRows) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            complete();   // the last tile, just asked for
+          }
+          more = next_unit(then);
+          prepared = true;
+        }
       }
+      u = then;
+      has = more;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (last >= 0) complete();
-  } else if (warp < 8) {
-    // ------------------------------------------------------------------ the units, and their K
-    const int w = warp - 4;
-    int i = 0;
-    bool ok = true;
-    for (unsigned id = blockIdx.x; ok && id < total; id += gridDim.x) {
-      const int bh = id % heads, b = bh / a.c.Hkv, h = bh % a.c.Hkv, key0 = (int)(id / heads) * kUnit;
-      int len, n;
-      read_lengths(a, b, key0 == 0 && h == 0 && w == 0 && lane == 0, len, n);
-      const int before = len - n, first = max(key0 - before, 0);   // tokens [first, last] see one of the keys
-      const int last = a.window > 0 ? min(n - 1, min(key0 + kUnit, len) - 1 + a.window - before) : n - 1;
-      const int row0 = first * a.G, rows = key0 < len ? max((last + 1) * a.G - row0, 0) : 0;
-      if (rows == 0) {   // nobody sees them
-        for (int k = w * 32 + lane; k < kUnit; k += 128) {
-          const size_t at = (size_t)bh * a.W + key0 + k;
-          if (key0 + k < a.W) a.out[at] = a.weights != nullptr ? a.weights[at] : 0.f;
-        }
-        continue;
-      }
-      if (i >= 2 && !(ok = mbar_wait_warp(&bar_kfree[i & 1], ((i >> 1) - 1) & 1, abort_flag, a.status, 1107))) break;
-      if (w == 0 && lane == 0) {
-        units[i % kUnits] = Unit{b, h, key0, before, row0, rows, {0, 0}};
-        mbar_arrive(&bar_unit[i % kUnits]);
-      }
-      RunBytes<D, Q4> k[2];   // a warp's four runs, two of them on their way at a time
-      auto load = [&](int r) {
-        const int run = key0 + kRun * (4 * w + r);
-        long long row = -1;
-        if (run < len) row = PAGED ? page_row(a.pages, a.c.Hkv, b, h, run, lane == 0 ? a.status : nullptr) : (long long)bh * a.c.S + run;
-        k[r & 1].load(a.c.k_q, a.c.k_d, row, len - run);
-      };
-      load(0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (r < 3) load(r + 1);
-        const int run = 4 * w + r;
-        k[r & 1].store(sK + (2 * (i & 1) + run / 8) * L::kTile, run % 8, false);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_k[i & 1]);
-      ++i;
-    }
-    if (ok && i >= 2) ok = mbar_wait_warp(&bar_kfree[i & 1], ((i >> 1) - 1) & 1, abort_flag, a.status, 1107);
-    if (w == 0 && lane == 0) {   // the end
-      units[i % kUnits].rows = 0;
-      mbar_arrive(&bar_unit[i % kUnits]);
-    }
   } else {
     // ------------------------------------------------------------------ exponentials and sums, a key for each thread
     const int m = (warp - 8) / 4, wq = warp & 3;
