@@ -1,13 +1,16 @@
 // Eviction from a quantized cache by accumulated attention weight (fa_cache_evict): of each head's keys the ones that matter
-// are found and moved together, in one kernel.
+// are found and moved together.
 //
 // A cluster of blocks has one head of one sequence, a run of its keys for each block. The border between what stays and what
 // goes is found a digit of 8 bits at a time, the highest first: every block counts its keys' digits, the counts are added
 // over the cluster through its shared memory, and the digit in which the wanted number is reached is the border's. Keys
 // above the border stay, and the first of those at it: with the counts of both in the blocks and threads before, every key knows
-// its new place, and writes its index there (kept). Then the rows are moved in waves, a wave of places loaded by the whole
-// cluster before any of it is stored: a key never moves up, so a wave's places hold none of a later wave's keys, and the
-// pages may be the same.
+// its new place, and writes its index there (kept).
+//
+// Moved is in waves where places and sources may be the same memory (the rows of the same pages, the weights in place): a
+// wave of places is loaded by the whole cluster before any of it is stored; a key never moves up, so a wave's places hold none
+// of a later wave's keys. Rows that go to other pages are a kernel's of their own, all rows at once: the heads of one sequence
+// do not fill the machine, and there is nothing to wait for.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -54,6 +57,11 @@ __device__ __forceinline__ unsigned cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// ... of one block's threads where it is a cluster by itself, without what makes global memory the others'.
+__device__ __forceinline__ void sync_all(unsigned blocks) {
+  if (blocks == 1) __syncthreads();
+  else cluster_sync();
+}
 __device__ __forceinline__ unsigned read_of(unsigned rank, const unsigned* p) {
   unsigned at, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
@@ -91,7 +99,46 @@ __device__ __forceinline__ unsigned block_sum_before(unsigned x, unsigned* sums,
   return before;
 }
 
-template <int D, bool Q4, bool PAGED>
+// Row of the planes that holds key j of head h of sequence b: -1 where the table names no page.
+template <bool PAGED>
+__device__ __forceinline__ long long place_of(const EvictArgs& a, const PageView& pages, unsigned bh, int b, int h, int j) {
+  if constexpr (!PAGED) return (long long)bh * a.c.S + j;
+  const long long row = page_row(pages, a.c.Hkv, b, h, j & ~15, a.status);
+  return row < 0 ? -1 : row + (j & 15);
+}
+
+// A thread's part of a key's row: 16 bytes of the numbers of K or of V, with the first ones their scales.
+template <int D, bool Q4>
+struct RowParts {
+  static constexpr int ROW = Q4 ? D / 2 : D, PIECES = ROW / 16, LANES = 2 * PIECES, NB = D / 32;
+  using Scales = std::conditional_t<NB == 4, uint2, uint32_t>;
+  struct Data { uint4 x; Scales d; };
+  uint8_t* values;
+  uint16_t* scales;
+  bool first;
+  __device__ __forceinline__ RowParts(const CacheView& c, int lane) {
+    const bool v = lane >= PIECES;
+    first = lane % PIECES == 0;
+    values = static_cast<uint8_t*>(v ? c.v_q : c.k_q) + 16 * (lane % PIECES);
+    scales = v ? c.v_d : c.k_d;
+  }
+  __device__ __forceinline__ Data load(long long row) const {   // of no row: zeros
+    const uint32_t zero = Q4 ? 0x88888888u : 0u;
+    Data r{make_uint4(zero, zero, zero, zero), Scales{}};
+    if (row >= 0) {
+      r.x = *reinterpret_cast<const uint4*>(values + row * ROW);
+      if (first) r.d = *reinterpret_cast<const Scales*>(scales + row * NB);
+    }
+    return r;
+  }
+  __device__ __forceinline__ void store(long long row, const Data& r) const {
+    *reinterpret_cast<uint4*>(values + row * ROW) = r.x;
+    if (first) *reinterpret_cast<Scales*>(scales + row * NB) = r.d;
+  }
+};
+
+// MOVE: the rows too, in place.
+template <int D, bool Q4, bool PAGED, bool MOVE>
 __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ unsigned cache[];   // [cached]: the order of this block's first keys
   __shared__ unsigned counts[4][256], total[256], sums[kThreads / 32], found[2], own[2];
@@ -100,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   const int b = bh / a.c.Hkv, h = bh % a.c.Hkv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
+  let_next_kernel_start();
   const long long length = __ldg(a.lengths + b);
   const int len = (int)min(max(length, 0LL), min((long long)a.c.S, a.W));
   const int left = min(len, a.keep);
@@ -146,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
           if (lane == __ffs(agree) - 1) atomicAdd(&counts[pass][common], (unsigned)__popc(agree));
           if (in && digit != common) atomicAdd(&counts[pass][digit], 1u);
         }
-        cluster_sync();
+        sync_all(blocks);
         if (threadIdx.x < 256) {
           unsigned x = 0;
           for (unsigned r = 0; r < blocks; ++r) x += read_of(r, &counts[pass][threadIdx.x]);
@@ -192,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       own[0] = all_above;
       own[1] = all_equal;
     }
-    cluster_sync();
+    sync_all(blocks);
     unsigned above_before = 0, equal_before = 0;
     for (unsigned r = 0; r < rank; ++r) {
       above_before += read_of(r, &own[0]);
@@ -221,61 +269,77 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
       equal_before += all & 0xffffu;
     }
   }
-  cluster_sync();   // kept is there
+  sync_all(blocks);   // kept is there
 
-  // The rows, 16 bytes of numbers for a thread, K's and V's; the first threads of a row have its scales too.
-  constexpr int ROW = Q4 ? D / 2 : D, PIECES = ROW / 16, LANES = 2 * PIECES, NB = D / 32, AHEAD = 4;
-  using Scales = std::conditional_t<NB == 4, uint2, uint32_t>;
-  constexpr int PER = kThreads / LANES;   // rows of a block at a time
-  const int piece = threadIdx.x % LANES % PIECES;
-  const bool second = threadIdx.x % LANES >= PIECES;   // V
-  uint8_t* values = static_cast<uint8_t*>(second ? a.c.v_q : a.c.k_q) + 16 * piece;
-  uint16_t* scales = second ? a.c.v_d : a.c.k_d;
-  auto place = [&](const PageView& pages, int j) -> long long {
-    if constexpr (!PAGED) return (long long)bh * a.c.S + j;
-    const long long row = page_row(pages, a.c.Hkv, b, h, j & ~15, a.status);
-    return row < 0 ? -1 : row + (j & 15);
-  };
-  const int wave = PER * AHEAD * blocks;
-  for (int i0 = 0; i0 < left; i0 += wave) {
-    uint4 x[AHEAD];
-    Scales d[AHEAD];
-    float w[AHEAD];
-    long long to[AHEAD];
+  if constexpr (MOVE) {   // the rows: a thread has 16 bytes of K's or V's numbers, the first one of a row its scales too
+    using R = RowParts<D, Q4>;
+    constexpr int PER = kThreads / R::LANES, AHEAD = 4;   // rows of a block at a time, and on their way
+    const R part(a.c, threadIdx.x % R::LANES);
+    const int wave = PER * AHEAD * blocks;
+    for (int i0 = 0; i0 < left; i0 += wave) {
+      typename R::Data x[AHEAD];
+      long long to[AHEAD];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int i = i0 + (k * blocks + rank) * PER + threadIdx.x / LANES;
-      to[k] = -1;
-      if (i >= left) continue;
-      const int j = kept[i];
-      if (piece == 0 && !second) w[k] = weights[j];
-      const long long from = place(a.from, j);
-      to[k] = place(a.to, i);
-      if (from == to[k]) {   // it stays where it is
+      for (int k = 0; k < AHEAD; ++k) {
+        const int i = i0 + (k * blocks + rank) * PER + threadIdx.x / R::LANES;
         to[k] = -1;
-        continue;
+        if (i >= left) continue;
+        const int j = kept[i];
+        if (j == i) continue;   // it stays where it is
+        to[k] = place_of<PAGED>(a, a.to, bh, b, h, i);
+        x[k] = part.load(place_of<PAGED>(a, a.from, bh, b, h, j));
       }
-      x[k] = make_uint4(Q4 ? 0x88888888u : 0u, Q4 ? 0x88888888u : 0u, Q4 ? 0x88888888u : 0u, Q4 ? 0x88888888u : 0u);
-      d[k] = Scales{};
-      if (from >= 0) {
-        x[k] = *reinterpret_cast<const uint4*>(values + from * ROW);
-        if (piece == 0) d[k] = *reinterpret_cast<const Scales*>(scales + from * NB);
-      }
-    }
-    cluster_sync();   // all of the wave is read
+      sync_all(blocks);   // all of the wave is read
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int i = i0 + (k * blocks + rank) * PER + threadIdx.x / LANES;
-      if (i < left && piece == 0 && !second) weights_out[i] = w[k];
-      if (to[k] < 0) continue;
-      *reinterpret_cast<uint4*>(values + to[k] * ROW) = x[k];
-      if (piece == 0) *reinterpret_cast<Scales*>(scales + to[k] * NB) = d[k];
+      for (int k = 0; k < AHEAD; ++k)
+        if (to[k] >= 0) part.store(to[k], x[k]);
+    }
+  }
+  constexpr int SOME = 4;   // the weights: four of a thread at a time
+  for (int i0 = 0; i0 < left; i0 += SOME * all_threads) {
+    float x[SOME];
+#pragma unroll
+    for (int k = 0; k < SOME; ++k) {
+      const int i = i0 + k * all_threads + me;
+      if (i < left) x[k] = weights[kept[i]];
+    }
+    sync_all(blocks);
+#pragma unroll
+    for (int k = 0; k < SOME; ++k) {
+      const int i = i0 + k * all_threads + me;
+      if (i < left) weights_out[i] = x[k];
     }
   }
   for (long long i = left + me; i < a.W; i += all_threads) weights_out[i] = 0.f;
+  if (blocks > 1) cluster_sync();   // nobody ends while another block may read its counts
 }
 
-template <int D, bool Q4, bool PAGED>
+// The rows to other pages, in the order of their places.
+template <int D, bool Q4>
+__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictArgs a, unsigned rows) {
+  using R = RowParts<D, Q4>;
+  constexpr int PER = 256 / R::LANES, AHEAD = 4;
+  const R part(a.c, threadIdx.x % R::LANES);
+  const unsigned first = blockIdx.x * (PER * AHEAD) + threadIdx.x / R::LANES;
+  wait_for_kernel_before();
+  int j[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) j[k] = first + k * PER < rows ? a.kept[first + k * PER] : -1;
+  typename R::Data x[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    const unsigned bh = (first + k * PER) / a.keep;
+    if (j[k] >= 0) x[k] = part.load(place_of<true>(a, a.from, bh, bh / a.c.Hkv, bh % a.c.Hkv, j[k]));
+  }
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    const unsigned bh = (first + k * PER) / a.keep, i = (first + k * PER) % a.keep;
+    const long long to = j[k] >= 0 ? place_of<true>(a, a.to, bh, bh / a.c.Hkv, bh % a.c.Hkv, i) : -1;
+    if (to >= 0) part.store(to, x[k]);
+  }
+}
+
+template <int D, bool Q4, bool PAGED, bool MOVE>
 cudaError_t launch_evict(const EvictArgs& a, long long heads, int blocks, cudaStream_t st) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -288,9 +352,16 @@ cudaError_t launch_evict(const EvictArgs& a, long long heads, int blocks, cudaSt
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  auto kernel = evict_kernel<D, Q4, PAGED>;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  auto kernel = evict_kernel<D, Q4, PAGED, MOVE>;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   count_launches(1);
+  if constexpr (!MOVE) {
+    if (e != cudaSuccess) return e;
+    constexpr int PER = 256 / RowParts<D, Q4>::LANES * 4;
+    const unsigned rows = (unsigned)(heads * a.keep);
+    e = launch_after(evict_move_kernel<D, Q4>, dim3((rows + PER - 1) / PER), 256, st, a, rows);
+    count_launches(1);
+  }
   return e;
 }
 
@@ -322,7 +393,7 @@ extern "C" fa_status fa_cache_evict(const fa_evict_params* p, const fa_cache* c,
   }
   if (W < 1 || W > 1LL << 30) { set_error("W=%lld outside [1, 2^30]", (long long)W); return FA_ERR_INVALID_ARG; }
   const long long heads = (long long)cv.B * cv.Hkv;
-  if (heads * kCluster > 0x7fffffffLL) { set_error("too many heads for one launch"); return FA_ERR_UNSUPPORTED; }
+  if (heads * kCluster > 0x7fffffffLL || heads * p->keep > 0x7fffffffLL - 512) { set_error("too many heads for one launch"); return FA_ERR_UNSUPPORTED; }
   const size_t bytes = (size_t)heads * (size_t)W * 4;
   in[2] = {lengths, (size_t)cv.B * 8, "lengths"};
   in[3] = {weights, weights != weights_out ? bytes : 0, "weights"};
@@ -361,7 +432,8 @@ extern "C" fa_status fa_cache_evict(const fa_evict_params* p, const fa_cache* c,
     constexpr int D = decltype(dim)::value;
     constexpr bool Q4 = decltype(q4)::value;
     cudaStream_t cs = (cudaStream_t)stream;
-    return pages != nullptr ? launch_evict<D, Q4, true>(a, heads, blocks, cs) : launch_evict<D, Q4, false>(a, heads, blocks, cs);
+    if (to != nullptr) return launch_evict<D, Q4, true, false>(a, heads, blocks, cs);
+    return pages != nullptr ? launch_evict<D, Q4, true, true>(a, heads, blocks, cs) : launch_evict<D, Q4, false, true>(a, heads, blocks, cs);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;

@@ -464,8 +464,8 @@ FA_API fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, con
  * every other). They become the keys 0 .. keep - 1 in the order they had, moved as they are stored; a sequence with no
  * more than `keep` keeps all. Written are
  *   the rows of the planes, to the same pages (to == NULL), or to those of the table `to` (for the same sequences, room for
- *     `keep` keys), which then leaves the pages moved from as they are. A page written to is no page of the table read from,
- *     unless it is in the same place of both, and in no other place of either;
+ *     `keep` keys), which leaves the pages moved from as they are. A page written to is in no other place that is written to, and
+ *     none of those of `to` is one that is read from;
  *   kept int32 [B, Hkv, keep]: the index each key had, -1 behind the last one;
  *   weights_out fp32 [B, Hkv, W]: the weights of the keys that stay, 0 behind them; may be weights;
  *   new_lengths int64 [B]: min(length, keep).
