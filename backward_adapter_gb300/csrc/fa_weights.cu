@@ -12,7 +12,7 @@
 // More rows: a block has 256 keys at a time, two tiles of 128, made bf16 operands once (kv_tile.cuh), and all rows that see one
 // of them go by, 128 at a time, which halves what the blocks read of Q from L2 against 128 keys. A block stays on its SM for all
 // its keys: warps 1-7 bring the rows into a ring and make the operands of the next 256 keys in between, warp 0 issues the MMAs,
-// and warps 8-15 own a key for each thread and add up; each tile's products are in two buffers.
+// and of warps 8-23 two threads own a key, each half of the rows; each tile's products are in two buffers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,8 +30,11 @@ namespace {
 using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kLoaders = 7;             // warps that bring rows and make operands
+// Registers of a thread: what 768 are launched with, and what warps 0-7 and those that add make of it.
+constexpr int kRegsLaunch = 80, kRegsLoad = 112, kRegsAdd = 64;
+static_assert(2 * kRegsLoad + 4 * kRegsAdd <= 6 * kRegsLaunch, "register split exceeds the launch's");
 
 struct WeightArgs {
   CacheView c;
@@ -44,8 +47,7 @@ struct WeightArgs {
   float* out;
   unsigned* status;
   long long W;
-  float sl2;         // |scale| log2(e); the sign, or a scale of 0, is in the two masks
-  uint32_t q_and, q_xor;
+  float sl2;         // scale log2(e)
   int Hq, Sq, window, layout, G;
 };
 
@@ -165,9 +167,7 @@ __global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant_
     for (int j = 0; j < STEPS; ++j) {
       // the step's four features: of 4 bits those of the low, then of the high nibbles of word j / 2; of 8 bits of word j
       const int f = Q4 ? (D == 128 ? 32 * t + 4 * (j / 2) : 32 * (t / 2) + 8 * (t & 1) + 4 * (j / 2)) + 16 * (j & 1) : (D / 4) * t + 4 * j;
-      uint2 x = on ? __ldg(src + f / 4) : make_uint2(0, 0);
-      x.x = (x.x & a.q_and) ^ a.q_xor;
-      x.y = (x.y & a.q_and) ^ a.q_xor;
+      const uint2 x = on ? __ldg(src + f / 4) : make_uint2(0, 0);
       q[m][j][0] = Q4 ? __byte_perm(x.x, x.y, 0x5410) : x.x;
       q[m][j][1] = Q4 ? __byte_perm(x.x, x.y, 0x7632) : x.y;
     }
@@ -267,27 +267,27 @@ struct WeightSmem {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kRing = 3;                   // tiles of rows
   static constexpr int kQOff = 4 * kTile;           // two units of keys
-  static constexpr int kLogOff = kQOff + kRing * kTile, kBarOff = kLogOff + kRing * kRows * 4;
-  static constexpr int kBytes = kBarOff + 512 + 1024;
+  static constexpr int kLogOff = kQOff + kRing * kTile, kSumOff = kLogOff + kRing * kRows * 4, kBarOff = kSumOff + kUnit * 4;
+  static constexpr int kBytes = kBarOff + 512;
 };
 
 template <int D, bool Q4, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ WeightArgs a, unsigned total) {
   using L = WeightSmem<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + L::kQOff);
   float* sLog = reinterpret_cast<float*>(smem + L::kLogOff);   // [ring][128]: -lse, base 2; -inf in columns without a row
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* bar_k = bars;               // [2]: a unit's K written
   uint64_t* bar_kfree = bars + 2;       // [2]: its products done
   uint64_t* bar_q = bars + 4;           // [ring]: rows written
-  uint64_t* bar_qfree = bars + 7;       // [ring]: products done, and the rows' LSE read
-  uint64_t* bar_s = bars + 10;          // [2 tiles of keys][2]: products there
-  uint64_t* bar_sfree = bars + 14;      // [2][2]: read
-  uint64_t* bar_unit = bars + 18;       // [kUnits]: described
-  uint64_t* bar_done = bars + 22;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
+  uint64_t* bar_qfree = bars + 7;       // [ring]: products done
+  uint64_t* bar_log = bars + 10;        // [ring]: the rows' LSE read
+  uint64_t* bar_s = bars + 13;          // [2 tiles of keys][2]: products there
+  uint64_t* bar_sfree = bars + 17;      // [2][2]: read
+  uint64_t* bar_unit = bars + 21;       // [kUnits]: described
+  uint64_t* bar_done = bars + 25;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Unit* units = reinterpret_cast<Unit*>(smem + L::kBarOff + 256);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -300,11 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     }
     for (int i = 0; i < L::kRing; ++i) {
       mbar_init(&bar_q[i], kLoaders);
-      mbar_init(&bar_qfree[i], 1 + 8);   // the products and the warps that add
+      mbar_init(&bar_qfree[i], 1);
+      mbar_init(&bar_log[i], 16);   // the warps that add
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_sfree[i], 4);
+      mbar_init(&bar_sfree[i], 8);
       mbar_init(&bar_unit[i], 1);
     }
     mbar_init(bar_done, 1);
@@ -320,6 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   // written over for unit i + 4, when unit i + 2 is done, whose last products came after unit i's had been taken.
   auto unit_there = [&](int i) { return mbar_wait_warp(&bar_unit[i % kUnits], (i / kUnits) & 1, abort_flag, a.status, 1101); };
 
+  if (warp < 8) regs_inc<kRegsLoad>();
+  else regs_dec<kRegsAdd>();
   if (warp == 0) {
     // ------------------------------------------------------------------ MMAs, the lanes together
     const uint32_t lead = lane == 0 ? 1u : 0u, idesc = idesc_bf16_f32(128, kRows, 0, 0);
@@ -422,14 +425,6 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         float& x = sLog[last * kRows + r];
         x = r < last_rows ? -x * kLog2e : -CUDART_INF_F;
       }
-      if (a.q_xor != 0u || a.q_and != 0xffffffffu) {   // a scale that is not positive: this lane's own chunks again
-        for (int r = r0; r < kRows; r += STEP) {
-          const uint32_t at = sQ + last * L::kTile + (chunk >> 3) * L::kBox + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-          const float4 f = ld_shared_f4(at);
-          st_shared_v4(at, (__float_as_uint(f.x) & a.q_and) ^ a.q_xor, (__float_as_uint(f.y) & a.q_and) ^ a.q_xor,
-                       (__float_as_uint(f.z) & a.q_and) ^ a.q_xor, (__float_as_uint(f.w) & a.q_and) ^ a.q_xor);
-        }
-      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_q[last]);
@@ -441,11 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
       bool prepared = false, more = false;
       for (int first = 0; first < u.rows; first += kRows) {
         if (laps > 0) {
-          if (last >= 0 && !__all_sync(0xffffffffu, mbar_test(&bar_qfree[slot], (laps - 1) & 1))) {   // no place yet: see the last tile in first
-            asm volatile("cp.async.wait_all;" ::: "memory");
+          if (last >= 0 && !__all_sync(0xffffffffu, mbar_test(&bar_qfree[slot], (laps - 1) & 1) && mbar_test(&bar_log[slot], (laps - 1) & 1))) {
+            asm volatile("cp.async.wait_all;" ::: "memory");   // no place yet: see the last tile in first
             complete();
           }
           if (!(ok = mbar_wait_warp(&bar_qfree[slot], (laps - 1) & 1, abort_flag, a.status, 1106))) break;
+          if (!(ok = mbar_wait_warp(&bar_log[slot], (laps - 1) & 1, abort_flag, a.status, 1109))) break;
         }
         const int rows = u.rows - first, row = u.row0 + first + r0;
         int head = row % a.G;
@@ -493,31 +489,36 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (last >= 0) complete();
   } else {
-    // ------------------------------------------------------------------ exponentials and sums, a key for each thread
-    const int m = (warp - 8) / 4, wq = warp & 3;
-    const uint32_t tS = tmem + 2 * m * kRows + ((uint32_t)(wq * 32) << 16);
+    // ------------------------------------------------------------------ exponentials and sums: a key, and half of the rows, for each thread
+    const int m = (warp - 8) / 8, half = (warp - 8) / 4 & 1, wq = warp & 3;
+    const uint32_t tS = tmem + 2 * m * kRows + half * 64 + ((uint32_t)(wq * 32) << 16);
     const uint64_t sl2 = f32x2(a.sl2, a.sl2);
+    float* sums = reinterpret_cast<float*>(smem + L::kSumOff) + m * kTileKeys + wq * 32 + lane;   // what the second half's thread has
+    const int pair = 1 + m * 4 + wq;   // the barrier of the two warps that have the same keys: they go the same way, in what fails too
     int x = 0, slot = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      if (!(ok = unit_there(i))) break;
+    for (int i = 0;; ++i) {
+      bool ok = named_bar_and(pair, 64, unit_there(i));
       const Unit u = units[i % kUnits];
-      if (u.rows == 0) break;
+      if (!ok || u.rows == 0) break;
       const int key = u.key0 + m * kTileKeys + wq * 32 + lane;
       const size_t at = ((size_t)u.b * a.c.Hkv + u.h) * a.W + key;
-      const float had = a.weights != nullptr && key < a.W ? a.weights[at] : 0.f;
+      const float had = half == 0 && a.weights != nullptr && key < a.W ? a.weights[at] : 0.f;
       float sum = 0.f;
       for (int first = 0; first < u.rows; first += kRows, ++x) {
-        const int buf = x & 1, here = min(u.rows - first, kRows);
+        const int buf = x & 1, here = min(u.rows - first - half * 64, 64);   // columns with a row
         if (!(ok = mbar_wait_warp(&bar_s[2 * m + buf], (x >> 1) & 1, abort_flag, a.status, 1108))) break;
         tc_fence_after();
-        const float* log = sLog + slot * kRows;
-        const int row = u.row0 + first;
-        const int pos0 = u.before + row / a.G, pos1 = u.before + (row + here - 1) / a.G;   // of the first and the last row's token
-        const bool edge = pos0 < u.key0 + (m + 1) * kTileKeys - 1 || (a.window > 0 && pos1 - (u.key0 + m * kTileKeys) > a.window);
+        const float* log = sLog + slot * kRows + half * 64;
+        const int row = u.row0 + first + half * 64;
+        int pos = u.before + row / a.G, head = row % a.G;   // of the column at hand
+        const int pos1 = u.before + (row + here - 1) / a.G;   // of the last one
+        const bool edge = pos < u.key0 + (m + 1) * kTileKeys - 1 || (a.window > 0 && pos1 - (u.key0 + m * kTileKeys) > a.window);
         uint64_t part[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-        int pos = pos0, head = row % a.G;   // of the column at hand, where some pairs are hidden
-        auto add = [&](const uint32_t (&raw)[32], int c0, auto on_edge) {
+        auto add = [&](int c0, auto on_edge) {
+          uint32_t raw[32];
+          tmem_ld32(tS + buf * kRows + c0, raw);
+          tmem_wait_ld();
+          reg_fence(raw);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 g = *reinterpret_cast<const float4*>(log + c0 + e);
@@ -539,30 +540,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             part[1] = add_f32x2(part[1], f32x2(p[2], p[3]));
           }
         };
-        uint32_t raw[2][32];
-        tmem_ld32(tS + buf * kRows, raw[0]);
         if (edge) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < here; c0 += 32) {
-            tmem_wait_ld();
-            reg_fence(raw[0]);
-            add(raw[0], c0, std::true_type{});
-            if (c0 + 32 < here) tmem_ld32(tS + buf * kRows + c0 + 32, raw[0]);
-          }
-        } else {   // all 128 columns, those without a row too: the next ones on their way meanwhile
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_wait_ld();
-            reg_fence(raw[c & 1]);
-            if (c < 3) tmem_ld32(tS + buf * kRows + 32 * (c + 1), raw[(c + 1) & 1]);
-            add(raw[c & 1], 32 * c, std::false_type{});
-          }
+          for (int c0 = 0; c0 < here; c0 += 32) add(c0, std::true_type{});
+        } else {
+#pragma unroll 1
+          for (int c0 = 0; c0 < here; c0 += 32) add(c0, std::false_type{});
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&bar_sfree[2 * m + buf]);
-          mbar_arrive(&bar_qfree[slot]);
+          mbar_arrive(&bar_log[slot]);
         }
         slot = slot == L::kRing - 1 ? 0 : slot + 1;
         float s0, s1, s2, s3;
@@ -570,7 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         f32x2_split(part[1], s2, s3);
         sum += (s0 + s1) + (s2 + s3);
       }
-      if (ok && key < a.W) a.out[at] = had + sum;
+      if (half == 1) *sums = sum;
+      if (!named_bar_and(pair, 64, ok)) break;
+      if (half == 0 && key < a.W) a.out[at] = had + (sum + *sums);
     }
   }
   tc_fence_before();
@@ -598,6 +589,12 @@ cudaError_t launch_weights(const WeightArgs& a, long long heads, cudaStream_t st
   static_assert(bytes <= 232448, "shared memory of a block");
   auto kernel = weights_kernel<D, Q4, PAGED>;
   static std::atomic<uint64_t> allowed{0};
+  if (allowed.load(std::memory_order_acquire) == 0) {   // the split of registers holds for what the kernel is launched with
+    cudaFuncAttributes at;
+    const cudaError_t got = cudaFuncGetAttributes(&at, kernel);
+    if (got != cudaSuccess) return got;
+    if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+  }
   const cudaError_t e = allow_shared(kernel, bytes, allowed);
   if (e != cudaSuccess) return e;
   const long long total = heads * ((a.W + kUnit - 1) / kUnit);
@@ -656,9 +653,7 @@ extern "C" fa_status fa_cache_weights(const fa_prefill_params* p, const void* q,
   a.out = out;
   if ((a.status = device_status_ptr()) == nullptr) return cuda_status(cudaErrorUnknown, "status word");
   a.W = W;
-  a.sl2 = p->scale == 0.f ? 1.f : fminf(fabsf(p->scale) * kLog2e, FLT_MAX);
-  a.q_and = p->scale == 0.f ? 0u : 0xffffffffu;
-  a.q_xor = p->scale < 0.f ? 0x80008000u : 0u;
+  a.sl2 = fmaxf(fminf(p->scale * kLog2e, FLT_MAX), -FLT_MAX);
   a.Hq = p->Hq;
   a.Sq = p->Sq;
   a.window = p->window < 2 * kMaxSeq ? p->window : 2 * kMaxSeq;
