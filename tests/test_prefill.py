@@ -94,6 +94,9 @@ SHAPES = {
     "window_of_one": (1, 4, 2, 300, 128, 300, 16, [300], None, 1),
     "long_window": (1, 4, 1, 400, 128, 70, 16, [400], None, 1 << 30),
     "shared": (1, 4, 2, 3000, 128, 8, 64, [2999], None, 0),
+    "one_tile_of_rows_over_many_keys": (12, 16, 16, 1500, 64, 9, 48, [1500, 1, 0, 700, 512, 513, 640, 641, 1300, 1499, 129, 900], [9, 1, 3] * 4, 0),
+    "the_same_wide": (7, 8, 2, 1300, 128, 32, 16, [1300, 31, 520, 1024, 1025, 700, 1299], [32, 32, 1, 31, 20, 8, 32], 0),
+    "one_tile_of_rows_in_a_window": (4, 8, 8, 2500, 64, 20, 16, [2500, 1100, 640, 2000], [20, 3, 20, 1], 900),
     "shared_by_many": (1, 1, 1, 9000, 64, 2, 256, [8999], None, 0),
     "many_sequences": (70, 2, 1, 48, 64, 4, 16, list(range(1, 48)) + [48] * 23, [1 + i % 4 for i in range(70)], 0),
 }
