@@ -1,0 +1,176 @@
+"""The operators over a cache in pages one after the other, as a serving program uses them: a ragged prompt (norm and rotation, write,
+attention of the chunk, the weights its keys got), tokens one by one that add to the weights, eviction into other pages and in
+place, and tokens behind it, whose position is no longer their place in the cache; on streams and in captured graphs."""
+import numpy as np
+import pytest
+import torch
+
+import backward_adapter_gb300 as fa
+from backward_adapter_gb300 import fa_train as ft
+from tests import paged_util as pu
+from tests import test_cache_evict, test_cache_weights, test_decode, test_prefill
+
+ROOM, P = 320, 32
+
+
+class Session:
+    """Sequences over a pool that has the pages of two tables for each, in an order of the seed's."""
+
+    def __init__(self, B, Hq, Hkv, D, fmt, seed):
+        self.Hq, self.Hkv, self.D = Hq, Hkv, D
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+        M = ROOM // P
+        self.pool = fa.new_cache(2 * B * M + 1, Hkv, P, D, fmt)
+        at = torch.from_numpy(np.random.default_rng(seed).permutation(2 * B * M + 1)[:2 * B * M].astype(np.int32)).cuda()
+        self.table, self.other = at.view(2, B, M)
+        self.f = fa.rope_inv_freq(D, device="cuda")[0]
+        self.w = [(1 + 0.2 * self.r(D).float()).to(torch.bfloat16) for _ in range(2)]
+        self.weights = torch.zeros((B, Hkv, ROOM), device="cuda")
+        self.lengths = torch.zeros(B, dtype=torch.int64, device="cuda")   # keys in the cache
+        self.seen = self.lengths.clone()                                  # tokens so far
+        self.qkv = None
+
+    def copy(self):
+        twin = object.__new__(Session)
+        twin.__dict__ = {k: v.clone() if isinstance(v, torch.Tensor) else [t.clone() for t in v] if isinstance(v, (list, tuple)) else v
+                         for k, v in self.__dict__.items()}
+        return twin
+
+    def rotated(self, qkv, pos):
+        q, k, v = qkv.split([self.Hq, self.Hkv, self.Hkv], dim=2)
+        return *fa.qk_norm_rope(q, k, self.f, pos, *self.w, layout="bshd"), v
+
+    def prompt(self, qkv, count):
+        q, k, v = self.rotated(qkv, self.seen[:, None] + torch.arange(qkv.shape[1], device="cuda"))
+        fa.cache_write(k, v, *self.pool, self.lengths, count, table=self.table, layout="bshd")
+        self.lengths += count
+        self.seen += count
+        o, lse = fa.prefill(q, *self.pool, self.lengths, count, table=self.table, layout="bshd",
+                            out=torch.zeros_like(q), lse=torch.zeros((q.shape[0], self.Hq, q.shape[1]), device="cuda"))
+        fa.cache_weights(q, lse, self.pool[0], self.pool[1], self.lengths, count, weights=self.weights, out=self.weights, table=self.table,
+                         layout="bshd")
+        return q, o, lse
+
+    def token(self):
+        """One more of every sequence that has any."""
+        one = self.lengths.clamp(max=1)
+        q, k, v = self.rotated(self.qkv, self.seen[:, None])
+        fa.cache_write(k, v, *self.pool, self.lengths, one, table=self.table, layout="bshd")
+        self.lengths += one
+        self.seen += one
+        o, lse = fa.decode(q, *self.pool, self.lengths, table=self.table, layout="bshd")
+        fa.cache_weights(q, lse, self.pool[0], self.pool[1], self.lengths, one, weights=self.weights, out=self.weights, table=self.table,
+                         layout="bshd")
+        return q, o, lse
+
+    def evict(self, keep, **kw):
+        kept, left = fa.cache_evict(*self.pool, self.weights, self.lengths, keep, sinks=4, recent=16, table=self.table, **kw)
+        self.lengths.copy_(left)
+        return kept
+
+    def planes(self, table=None):
+        return [pu.gathered(p, self.table if table is None else table).clone() for p in self.pool]
+
+
+def session(fmt, seed, D=128):
+    s = Session(4, 8, 2, D, fmt, seed)
+    s.qkv = s.r(4, 1, s.Hq + 2 * s.Hkv, D)
+    return s, s.r(4, 260, s.Hq + 2 * s.Hkv, D), pu.i64([260, 0, 61, 133])
+
+
+def tokens(s, n):
+    """n of them, each against the oracle over what the pool holds."""
+    for _ in range(n):
+        before, lengths = s.weights.clone(), s.lengths.clone()
+        q, o, lse = s.token()
+        planes, lens = s.planes(), s.lengths.tolist()
+        test_decode.check(q.transpose(1, 2).contiguous(), planes, s.lengths, (o.transpose(1, 2), lse))
+        test_cache_weights.check(q, lse, planes, lens, [min(x, 1) for x in lens], s.weights, before, layout="bshd")
+        assert torch.equal(s.lengths, torch.where(lengths > 0, lengths + 1, lengths))
+        s.qkv = s.qkv.roll(1, -1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,D", [("q4_0", 128), ("q8_0", 64)])
+def test_prompts_tokens_and_eviction(fmt, D):
+    s, qkv, count = session(fmt, 3, D)
+    counts = count.tolist()
+    q, o, lse = s.prompt(qkv, count)
+    test_prefill.check(q, s.planes(), counts, counts, (o, lse), layout="bshd")
+    test_cache_weights.check(q, lse, s.planes(), counts, counts, s.weights, None, layout="bshd")
+    tokens(s, 3)
+
+    def cut(keep, table_out=None):
+        lens, w, planes = s.lengths.tolist(), s.weights.cpu(), s.planes()
+        kept, left, weights, moved = test_cache_evict.expected(planes, w, lens, keep, 4, 16)
+        got = s.evict(keep, table_out=table_out)
+        s.table = s.table if table_out is None else table_out
+        assert torch.equal(got.cpu(), kept) and torch.equal(s.lengths.cpu(), left) and torch.equal(s.weights.cpu(), weights)
+        for a, b in zip(s.planes(), moved):
+            assert all(torch.equal(a[i, :, :n].cpu(), b[i, :, :n]) for i, n in enumerate(left.tolist()))
+
+    cut(100, s.other)
+    tokens(s, 3)
+    cut(64)
+    tokens(s, 2)
+    # a second chunk behind what was left
+    more = pu.i64([40, 0, 7, 1])
+    before = s.weights.clone()
+    q, o, lse = s.prompt(qkv[:, :40].contiguous(), more)
+    lens = s.lengths.tolist()
+    test_prefill.check(q, s.planes(), lens, more.tolist(), (o, lse), layout="bshd")
+    test_cache_weights.check(q, lse, s.planes(), lens, more.tolist(), s.weights, before, layout="bshd")
+    assert ft.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_captured_steps_with_eviction():
+    """Tokens and eviction in two graphs over two sessions, replayed in turn, against eager ones, bit for bit."""
+    sessions, twins, graphs, outs = [], [], [], []
+    for i, fmt in enumerate(("q4_0", "q8_0")):
+        s, qkv, count = session(fmt, 10 + i)
+        s.prompt(qkv, count)
+        twin = s.copy()
+        s.copy().token()   # what a first call loads
+        warm = s.copy()
+        warm.evict(70)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((*s.token(), s.evict(70)))
+        for x in (sessions, s), (twins, twin), (graphs, g):
+            x[0].append(x[1])
+    for turn in range(4):
+        for g in graphs:
+            g.replay()
+        for s, t, out in zip(sessions, twins, outs):
+            want = (*t.token(), t.evict(70))
+            assert all(torch.equal(a, b) for a, b in zip(out, want)), turn
+            assert all(torch.equal(a, b) for a, b in zip(s.pool, t.pool)) and torch.equal(s.weights, t.weights)
+            assert torch.equal(s.lengths, t.lengths) and int(s.lengths.max()) == 70
+            s.qkv.copy_(s.qkv.roll(1, -1))
+            t.qkv.copy_(s.qkv)
+    assert ft.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_sessions_side_by_side_on_streams():
+    """Two sessions on streams of their own, neither waiting for the other, give what each gives alone."""
+    pairs = [session("q4_0", 20 + i) for i in range(2)]
+    alone = []
+    for s, qkv, count in pairs:
+        t = s.copy()
+        alone.append((t, [t.prompt(qkv, count), t.token(), t.evict(90), t.token()]))
+    torch.cuda.synchronize()
+    got, streams = [], [torch.cuda.Stream() for _ in pairs]
+    for (s, qkv, count), st in zip(pairs, streams):
+        with torch.cuda.stream(st):
+            got.append([s.prompt(qkv, count), s.token(), s.evict(90), s.token()])
+    torch.cuda.synchronize()
+    for (s, *_), a, (t, b) in zip(pairs, got, alone):
+        for x, y in zip(a, b):
+            x, y = (x, y) if isinstance(x, tuple) else ((x,), (y,))
+            assert all(torch.equal(i, j) for i, j in zip(x, y))
+        assert all(torch.equal(i, j) for i, j in zip(s.pool, t.pool)) and torch.equal(s.weights, t.weights)
+    assert ft.device_status() == 0
