@@ -465,8 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mma_commit_if(lead, bar_done);
       mbar_wait<true>(bar_done, 0, nullptr, a.status, 1005);
       __syncwarp();
-    }
-    else if (warp < 4) {
+    } else if (warp < 4) {
       // ---------------------------------------------------------------- Q, rows of both tiles for each of warps 1-3
       constexpr int CHUNKS = D / 8, ROWS = 32 / CHUNKS, STEP = 3 * ROWS;   // 16-byte chunks of a row, rows of a load, of a step
       const int chunk = lane % CHUNKS, r0 = (warp - 1) * ROWS + lane / CHUNKS;

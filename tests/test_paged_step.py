@@ -174,3 +174,29 @@ def test_sessions_side_by_side_on_streams():
             assert all(torch.equal(i, j) for i, j in zip(x, y))
         assert all(torch.equal(i, j) for i, j in zip(s.pool, t.pool)) and torch.equal(s.weights, t.weights)
     assert ft.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", ["q4_0", "q8_0"])
+@pytest.mark.parametrize("n", [3, 40])
+def test_planes_of_any_room(fmt, D, n):
+    """Planes whose room is no multiple of anything, so that a head's keys begin anywhere: the bits of the same keys in pages."""
+    B, Hq, Hkv, S = 3, 9, 3, 333
+    padded, pool, table = pu.make(B, Hkv, S, D, fmt, 48, n)
+    planes = [p[:, :, :S].contiguous() for p in padded]
+    q, lens, count = pu.queries(B, Hq, n, D, 1), pu.i64([S, 17, 150]), pu.i64([n, n, n - 1])
+    out = lambda: dict(out=torch.zeros_like(q), lse=torch.zeros((B, Hq, n), device="cuda"))  # noqa: E731
+    got, want = fa.prefill(q, *planes, lens, count, **out()), fa.prefill(q, *pool, lens, count, table=table, **out())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    had = torch.rand((B, Hkv, S), generator=torch.Generator().manual_seed(2)).cuda()
+    w, want = (fa.cache_weights(q, got[1], p[0], p[1], lens, count, weights=had, **kw)
+               for p, kw in ((planes, {}), (pool, dict(table=table))))
+    assert torch.equal(w, want)
+    none = q[:, :, :0].contiguous()
+    assert torch.equal(fa.cache_weights(none, got[1][:, :, :0].contiguous(), *planes[:2], lens, weights=had), had)
+    a, b = fa.cache_evict(*planes, w, lens, 101, sinks=3, recent=20), fa.cache_evict(*pool, want, lens, 101, sinks=3, recent=20, table=table)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(w, want)
+    for x, y in zip(planes, pool):
+        assert torch.equal(x, pu.gathered(y, table)[:, :, :S])
+    assert ft.device_status() == 0
