@@ -159,16 +159,19 @@ int bwd_plan_records(const Shape& s, int32_t* rec, int cap);
 // Lets a kernel take `bytes` of dynamic shared memory on the current device: asked of the runtime once per kernel and
 // device (`done` has a bit for each device, one word for each kernel), as the call costs as much as a launch.
 template <typename K>
-cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
+cudaError_t allow(K kernel, cudaFuncAttribute what, int value, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(kernel, what, value);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+template <typename K>
+cudaError_t allow_shared(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  return bytes <= 48 * 1024 ? cudaSuccess : allow(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
 }
 
 // Streaming multiprocessors of the current device (queried once).

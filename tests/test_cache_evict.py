@@ -64,6 +64,7 @@ CASES = {
     "clusters": (1, 2, 5000, 128, 64, 5000, [5000], 1300, 4, 100),
     "large_clusters": (1, 1, 20000, 64, 128, 20000, [19999], 4001, 16, 1000),
     "more_than_cached": (1, 1, 100000, 64, 256, 100000, [99999], 60000, 4, 77),
+    "more_than_a_large_cluster_caches": (1, 1, 180000, 64, 256, 180000, [179999], 90000, 4, 77),
     "many_heads": (40, 4, 100, 64, 16, 100, [1 + (13 * i) % 100 for i in range(40)], 30, 2, 5),
 }
 
