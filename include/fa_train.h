@@ -422,7 +422,7 @@ FA_API fa_status fa_decode_pages(const fa_decode_params* p, const void* q, const
  * lengths[b] - count[b] + i and sees the keys j at or before it (with window w > 0 only those with position - j <= w). A token
  * that sees no key gets O = 0 and LSE = 0. The rows from count[b] on are neither read nor written, keys at or past a
  * sequence's length not read. As on the training path K and V are rounded to bf16 and the weights of V too; scores, statistics
- * and sums are 32-bit. A scale of V that is not finite counts as 0.
+ * and sums are 32-bit. A scale of V that is not finite counts as 0; one of K makes the scores of its key infinite or no numbers.
  */
 typedef struct fa_prefill_params {
   int32_t Hq;        /* query heads, a multiple of the cache's Hkv, at most 65535 */
@@ -452,7 +452,7 @@ FA_API fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_
  *                                       of exp(scale <q_gi, k_j> - lse_gi)
  * for every j below W (room for at least the sequences' lengths: a key at or past W is left out, and 0x40000000 | 952
  * recorded). K is rounded to bf16; products, exponentials and sums are 32-bit, added in a fixed order. weights: fp32 [B, Hkv,
- * W], or NULL: zeros; out: fp32 [B, Hkv, W], which may be weights. V's planes are not looked at.
+ * W], or NULL: zeros; out: fp32 [B, Hkv, W], which may be weights. 1 <= W <= 2^30. V's planes are not looked at.
  */
 FA_API fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, const float* lse, const fa_cache* c,
                                   const fa_pages* pages, const int64_t* lengths, const int64_t* count, const float* weights,
@@ -464,13 +464,13 @@ FA_API fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, con
  * every other). They become the keys 0 .. keep - 1 in the order they had, moved as they are stored; a sequence with no
  * more than `keep` keeps all. Written are
  *   the rows of the planes, to the same pages (to == NULL), or to those of the table `to` (for the same sequences, room for
- *     `keep` keys), which leaves the pages moved from as they are. A page written to is in no other place that is written to, and
- *     none of those of `to` is one that is read from;
+ *     `keep` keys), which leaves the pages moved from as they are. The caller sees to it that a page written to is in one place
+ *     of one table only: where sequences share pages, those that are cut need a table `to` of pages of their own;
  *   kept int32 [B, Hkv, keep]: the index each key had, -1 behind the last one;
  *   weights_out fp32 [B, Hkv, W]: the weights of the keys that stay, 0 behind them; may be weights;
  *   new_lengths int64 [B]: min(length, keep).
  * lengths: int64 [B]; one outside [0, room] or above W is taken as the nearer end, and 0x40000000 | 952 recorded.
- * 0 <= sinks, recent; sinks + recent <= keep; 1 <= keep.
+ * 0 <= sinks, recent; sinks + recent <= keep; 1 <= keep <= 2^24; 1 <= W <= 2^30.
  */
 typedef struct fa_evict_params {
   int32_t keep;

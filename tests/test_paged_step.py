@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import backward_adapter_gb300 as fa
+from backward_adapter_gb300 import cache as kv
 from backward_adapter_gb300 import fa_train as ft
 from tests import paged_util as pu
 from tests import test_cache_evict, test_cache_weights, test_decode, test_prefill
@@ -89,6 +90,39 @@ def tokens(s, n):
         test_cache_weights.check(q, lse, planes, lens, [min(x, 1) for x in lens], s.weights, before, layout="bshd")
         assert torch.equal(s.lengths, torch.where(lengths > 0, lengths + 1, lengths))
         s.qkv = s.qkv.roll(1, -1)
+
+
+@pytest.mark.parametrize("name", ["read", "decode", "prefill", "weights", "evict"])
+def test_results_and_scratch_come_from_the_calls_stream(name, monkeypatch):
+    """On the host, with a library that does nothing: no call allocates but through the one function that takes the stream."""
+    z = lambda *s, dt=torch.int8: torch.zeros(s, dtype=dt)  # noqa: E731
+    pool = (z(9, 2, 16, 64), z(9, 2, 16, 2, dt=torch.float16)) * 2
+    q, lse, n, table = z(2, 4, 5, 64, dt=torch.bfloat16), z(2, 4, 5, dt=torch.float32), z(2, dt=torch.int64), z(2, 4, dt=torch.int32)
+    w, plain, asked = z(2, 2, 64, dt=torch.float32), torch.empty, []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 1000 if name.endswith("workspace_size") else 0
+
+    def empty(shape, strides, dtype, device, stream=None):
+        asked.append(stream)
+        return plain(shape, dtype=dtype, device=device)
+
+    def refused(*a, **kw):
+        raise AssertionError("memory beside the call's stream")
+    monkeypatch.setattr(ft, "load_library", Library)
+    monkeypatch.setattr(ft, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(ft, "_rows", lambda t, layout: (0, 0, 0, 0))
+    monkeypatch.setattr(ft, "_launch", lambda *a: None)
+    monkeypatch.setattr(ft, "_empty", empty)
+    for f in ("empty", "zeros", "empty_like", "zeros_like"):
+        monkeypatch.setattr(torch, f, refused)
+    {"read": lambda: kv.cache_read(*pool, n, 3, table=table, stream=77),
+     "decode": lambda: kv.decode(q, *pool, n, table=table, stream=77),
+     "prefill": lambda: kv.prefill(q, *pool, n, n, table=table, stream=77),
+     "weights": lambda: kv.cache_weights(q, lse, *pool[:2], n, n, table=table, stream=77),
+     "evict": lambda: kv.cache_evict(*pool, w, n, 9, table=table, stream=77)}[name]()
+    assert asked and set(asked) == {77}
 
 
 @pytest.mark.gpu
