@@ -24,7 +24,7 @@
 //
 // Measured (device time, captured calls over changing inputs): 512 tokens over 67,584 keys in 4 bits, 16 heads on 4, D = 128: 253 us,
 // 1.12 PFLOP/s, 58% of the measured dense rate; two prompts of 4096 tokens in 8 bits, 32 heads on 8: 337 to 343 us, 0.8 PFLOP/s of visible
-// pairs; 24 tokens of 8 sequences of 500 to 4000 keys in 4 bits: 36 us; chunks of 1 to 777 tokens of 6 sequences of 300 to 9000 keys in 8
+// pairs; 24 tokens of 8 sequences of 500 to 4000 keys in 4 bits: 33 us; chunks of 1 to 777 tokens of 6 sequences of 300 to 9000 keys in 8
 // bits, D = 64, in a sliding window of 1024: 51 us. What bounds it: a tile of keys and 256 rows takes 4400 cycles, of which the tensor cores are busy for half:
 // each tile of rows goes from S to softmax (2400 cycles for 128 scores a row) to P V and back, and two of them on that way
 // do not fill the pipe; in copies without softmax the first case takes 204 us, without operands made from bytes as well 169. With few
@@ -302,7 +302,9 @@ struct PrefillSmem {
   static constexpr int kBytes = kPlanOff + (int)sizeof(Plan) + 1024;
 };
 
-template <int D, bool Q4, bool PAGED>
+// ALONE: no unit has more than one tile of rows. Such a tile has both buffers of S: its next scores are made, and softmax goes on to
+// them, while its product is (24 tokens of 8 sequences: 32.8 us, 35.5 without; of one of 67,584 keys, 4 heads: 43.1 and 49.8).
+template <int D, bool Q4, bool PAGED, bool ALONE>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
   using L = PrefillSmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -310,10 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + L::kKVOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
   uint64_t* bar_q = bars;                         // [2]: tile t of a unit's Q written
-  uint64_t* bar_s = bars + 2;                     // [2]: scores of tile t there
-  uint64_t* bar_p = bars + 4;                     // [2]: weights of tile t there
+  uint64_t* bar_s = bars + 2;                     // [2]: scores of tile t there; ALONE: of even and odd tiles of keys
+  uint64_t* bar_p = bars + 4;                     // [2]: weights there, likewise
   uint64_t* bar_o = bars + 6;                     // [2]: the last product of tile t done
-  uint64_t* bar_full = bars + 8;                  // [kStages]: stage written
+  uint64_t* bar_v = bars + 8;                     // ALONE: a product done
+  uint64_t* bar_full = bars + 9;                  // [kStages]: stage written
   uint64_t* bar_empty = bar_full + L::kStages;    // [kStages]: its MMAs done
   uint64_t* bar_piece = bar_empty + L::kStages;   // [kPieces]: part of a unit described
   uint64_t* bar_past = bar_piece + kPieces;       // [kPieces]: nobody looks at it any more
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   uint64_t* bar_done = bar_read + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (8 + 2 * L::kStages + 2 * kPieces + 3) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
+  static_assert(8 * (9 + 2 * L::kStages + 2 * kPieces + 3) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPieceOff);
   Plan& plan = *reinterpret_cast<Plan*>(smem + L::kPlanOff);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -335,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(&bar_p[t], 4);
       mbar_init(&bar_o[t], 1);
     }
+    mbar_init(bar_v, 1);
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&bar_full[i], kLoaders);
       mbar_init(&bar_empty[i], 1);
@@ -387,87 +391,91 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const uint32_t idesc_qk = idesc_bf16_f32(kBM, kBN, 0, 0);
       const uint32_t idesc_pv = idesc_bf16_f32(kBM, D, 0, 1);
       const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sKV, 16, 1024), dv = smem_desc_sw128(sKV, L::kBoxBytes, 1024);
-      auto issue_pv = [&](int t, int slot, bool first) {
+      // buffer b of S and P
+      auto issue_pv = [&](int t, int b, int slot, bool first) {
         const uint64_t v = desc_add(dv, slot * L::kTileBytes);
 #pragma unroll
         for (int k = 0; k < kBN / 16; ++k)
-          mma_ts_if(lead, tmem + 256 + t * D, tmem + t * 128 + k * 8, desc_add(v, k * 2048), idesc_pv,
+          mma_ts_if(lead, tmem + 256 + t * D, tmem + b * 128 + k * 8, desc_add(v, k * 2048), idesc_pv,
                     (!first || k > 0) ? 1u : 0u);
       };
-      auto issue_s = [&](int t, int slot) {
+      auto issue_s = [&](int t, int b, int slot) {
         const uint64_t q = desc_add(dq, t * L::kTileBytes), k0 = desc_add(dk, slot * L::kTileBytes);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
-          mma_ss_if(lead, tmem + t * 128, desc_add(q, off), desc_add(k0, off), idesc_qk, k > 0 ? 1u : 0u);
+          mma_ss_if(lead, tmem + b * 128, desc_add(q, off), desc_add(k0, off), idesc_qk, k > 0 ? 1u : 0u);
         }
-        mma_commit_if(lead, &bar_s[t]);
+        mma_commit_if(lead, &bar_s[b]);
       };
       auto wait = [&](uint64_t* bar, int phase, unsigned site) {
         return mbar_wait_warp(bar, phase & 1, abort_flag, a.status, site);
       };
       // The parts' tiles are one stream: stage i holds the K of its tile i and the V of tile i - 1. Within a part a tile of
       // rows gets its P V of the last tile of keys and then its next S, one tile of rows after the other; where a part ends
-      // both products come first.
+      // both products come first. ALONE: the next S into the other buffer, and then the product.
       int stage = 0;                    // tiles of the stream so far
       int scores0 = 0, scores1 = 0;     // of bar_s and bar_p: completions so far
       int loads0 = 0, loads1 = 0;       // of bar_q
       int pending = 0;                  // tiles of rows of the last tile of keys whose product is to come
       bool pending_first = false, pending_last = false;   // it is its part's first, last
+      int pending_b = 0;   // ALONE: its buffer
       auto product = [&](int t, int slot) -> bool {
-        if (!wait(&bar_p[t], (t ? scores1 : scores0) - 1, 1001)) return false;
+        const int b = ALONE ? pending_b : t;
+        if (!wait(&bar_p[b], (b ? scores1 : scores0) - 1, 1001)) return false;
         tc_fence_after();
-        issue_pv(t, slot, pending_first);
+        issue_pv(t, b, slot, pending_first);
+        if (ALONE) mma_commit_if(lead, bar_v);
         if (pending_last) mma_commit_if(lead, &bar_o[t]);
         return true;
       };
-      auto scores = [&](int t, int slot, bool last) {
-        issue_s(t, slot);
+      auto scores = [&](int t, int b, int slot, bool last) {
+        issue_s(t, b, slot);
         if (last) mma_commit_if(lead, &bar_read[t]);
-        if (t) ++scores1;
+        if (b) ++scores1;
         else ++scores0;
       };
-      auto first_scores = [&](int t, int slot, bool last) -> bool {
-        if (!wait(&bar_q[t], t ? loads1 : loads0, 1003)) return false;
-        tc_fence_after();
-        if (t) ++loads1;
-        else ++loads0;
-        scores(t, slot, last);
-        return true;
-      };
       for (int i = 0; ok; ++i) {
-        const int live = __shfl_sync(0xffffffffu, pieces[i % kPieces].rows, 0) > kBM ? 2 : 1;   // listed by this warp
+        const int rows = __shfl_sync(0xffffffffu, pieces[i % kPieces].rows, 0);   // listed by this warp
         const int tiles = __shfl_sync(0xffffffffu, pieces[i % kPieces].tiles, 0);
-        if (tiles == 0) break;
-        for (int j = 0; ok && j < tiles; ++j) {
+        if (tiles == 0 && pending == 0) break;
+        const int live = tiles == 0 ? 0 : rows > kBM ? 2 : 1;
+        for (int j = 0; ok && j < max(tiles, 1); ++j) {   // behind the last part a stage that holds only V
           const int sb = stage % L::kStages;
           if (!(ok = wait(&bar_full[sb], stage / L::kStages, 1002))) break;
           tc_fence_after();
           const bool last = j == tiles - 1;
-          if (j == 0) {
-            if (pending > 0) ok = product(0, 2 * sb + 1);
-            if (ok && pending > 1) ok = product(1, 2 * sb + 1);
-            if (ok) ok = first_scores(0, 2 * sb, last);
-            if (ok && live > 1) ok = first_scores(1, 2 * sb, last);
+          if (j == 0) {   // rolled: what warps go through has to come from the instruction caches
+#pragma unroll 1
+            for (int x = 0; ok && x < 4; ++x) {
+              const int t = x & 1;
+              if (x < 2) {
+                if (t < pending) ok = product(t, 2 * sb + 1);
+              } else if (t < live) {
+                if (!(ok = wait(&bar_q[t], t ? loads1 : loads0, 1003))) break;
+                tc_fence_after();
+                if (t) ++loads1;
+                else ++loads0;
+                scores(t, t, 2 * sb, last);
+              }
+            }
             list_part();
+          } else if constexpr (ALONE) {
+            scores(0, j & 1, 2 * sb, last);
+            ok = product(0, 2 * sb + 1);
           } else {
-            if ((ok = product(0, 2 * sb + 1))) scores(0, 2 * sb, last);
-            if (ok && live > 1 && (ok = product(1, 2 * sb + 1))) scores(1, 2 * sb, last);
+            if ((ok = product(0, 2 * sb + 1))) scores(0, 0, 2 * sb, last);
+            if (ok && live > 1 && (ok = product(1, 2 * sb + 1))) scores(1, 1, 2 * sb, last);
           }
           if (!ok) break;
           mma_commit_if(lead, &bar_empty[sb]);
           pending = live;
+          if (ALONE) pending_b = j & 1;
           pending_first = j == 0;
           pending_last = last;
           ++stage;
         }
-      }
-      if (ok && pending > 0) {   // the stream's last stage holds only V
-        const int sb = stage % L::kStages;
-        ok = wait(&bar_full[sb], stage / L::kStages, 1004);
-        tc_fence_after();
-        if (ok) ok = product(0, 2 * sb + 1);
-        if (ok && pending > 1) ok = product(1, 2 * sb + 1);
+        if (tiles == 0) break;
       }
       // every MMA of this warp is complete before TMEM is given back
       mma_commit_if(lead, bar_done);
@@ -616,7 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int t = (warp - 12) / 4, wq = warp & 3;
     const int r = wq * 32 + lane;   // row of the tile
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * D + lane_off;
+    uint32_t tS = tmem + t * 128 + lane_off;   // ALONE: of the buffer at hand
+    const uint32_t tO = tmem + 256 + t * D + lane_off;
     const float sl2 = a.sl2;
     // the next part with live rows in this tile of rows, from part `i` on; false behind the last
     auto next_live = [&](int& i) -> bool {
@@ -632,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     bool ok = true;
     int scored = 0, finished = 0;   // completions of bar_s and bar_o so far
+    int b = t, scored1 = 0, made = 0;   // ALONE: the buffer at hand; of bar_s[1]; of bar_v, with those to come for weights that are there
     int part = 0;
     for (; next_live(part); ++part) {
       int key0, key_hi, left;   // of the next tile: its first key, and the last one that this row sees
@@ -645,9 +655,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int key_lo = a.window > 0 ? key_hi - a.window : 0;
       float m = -CUDART_INF_F, l = 0.f;
       bool first = true;
+      if constexpr (ALONE) {
+        b = 0;
+        tS = tmem + lane_off;
+      }
       for (; left > 0; --left, key0 += kBN, first = false) {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[t], scored & 1, abort_flag, a.status, 1007)))) break;
-        ++scored;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[b], (ALONE && b ? scored1 : scored) & 1, abort_flag, a.status, 1007)))) break;
+        if (ALONE && b) ++scored1;
+        else ++scored;
         tc_fence_after();
         const int lo = min(max(key_lo - key0, 0), kBN), lim = max(min(key_hi - key0, kBN - 1), -1);
         const bool full = lo == 0 && lim == kBN - 1;
@@ -694,6 +709,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               tmem_st16(tS + d * 16, pk);
             }
             if (!first) {   // O holds the products of the tiles before: their MMAs ended before these scores did
+              if constexpr (ALONE) {   // ... but for the last one's, and that of the one before is what bar_v may still be at
+                const bool there = mbar_wait<true>(bar_v, made & 1, abort_flag, a.status, 1012) &&
+                                   mbar_wait<true>(bar_v, (made - 1) & 1, abort_flag, a.status, 1012);
+                ok = __all_sync(0xffffffffu, there) && ok;
+                tc_fence_after();
+              }
 #pragma unroll 1
               for (int d = 0; d < D / 16; ++d) {
                 uint32_t ov[16];
@@ -726,7 +747,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_p[t]);
+        if (lane == 0) mbar_arrive(&bar_p[b]);
+        if constexpr (ALONE) {
+          if (!ok) break;
+          ++made;
+          b ^= 1;
+          tS = tmem + b * 128 + lane_off;
+        }
       }
       if (!ok) break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_o[t], finished & 1, abort_flag, a.status, 1008)))) break;
@@ -967,11 +994,11 @@ fa_status check_prefill(const fa_prefill_params* p, const fa_cache* c, const fa_
   return st != FA_OK ? st : check_chunk(p, cv);
 }
 
-template <int D, bool Q4, bool PAGED>
+template <int D, bool Q4, bool PAGED, bool ALONE>
 cudaError_t launch_prefill(const PrefillArgs& a, int slices, cudaStream_t st) {
   constexpr int bytes = PrefillSmem<D>::kBytes;
   static_assert(bytes <= 232448, "shared memory of a block");
-  auto kernel = prefill_kernel<D, Q4, PAGED>;
+  auto kernel = prefill_kernel<D, Q4, PAGED, ALONE>;
   static std::atomic<uint64_t> allowed{0};
   if (allowed.load(std::memory_order_acquire) == 0) {   // the split of registers holds for what the kernel is launched with
     cudaFuncAttributes at;
@@ -1078,7 +1105,9 @@ fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_cache* 
     auto go = [&](auto dim, auto q4) {
       constexpr int D = decltype(dim)::value;
       constexpr bool Q4 = decltype(q4)::value;
-      return pages != nullptr ? launch_prefill<D, Q4, true>(a, plan.slices, cs) : launch_prefill<D, Q4, false>(a, plan.slices, cs);
+      if ((long long)a.G * p->Sq <= kBM)
+        return pages != nullptr ? launch_prefill<D, Q4, true, true>(a, plan.slices, cs) : launch_prefill<D, Q4, false, true>(a, plan.slices, cs);
+      return pages != nullptr ? launch_prefill<D, Q4, true, false>(a, plan.slices, cs) : launch_prefill<D, Q4, false, false>(a, plan.slices, cs);
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;

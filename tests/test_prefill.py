@@ -6,6 +6,9 @@ each: E = 2^-17 scale sum_d |q_d k_d|, the largest over the keys a row sees. LSE
 terms near it, 2^-20 (1 + |LSE| + max |s|). A weight is off by the factor e^(+-E) and rounded to bf16 once, half a step, 2^-8 of its
 value; the sum that divides is of unrounded ones. The result is rounded to bf16, 2^-8 of its value:
     |dO| <= (2^-8 + 2 E + 2^-16) sum p |v| / sum p + 2^-8 |O|.
+What underflows: an exponential below 2^-126 is 0. It is relative to a reference of which the row's scores are at most 30 above and
+the largest at most 1 below (base 2), in a part of the row and where parts are joined, so a key loses less than 2^(-126 + 30) / 2^-1 of the
+row's sum, and all of them 2^-95 (number of keys) max |v| of O.
 """
 import ctypes
 import math
@@ -50,7 +53,8 @@ def check(q, planes, lengths, counts, got, scale=None, window=0, layout="bhsd"):
         err = np.abs(lse[b, :, :n] - want_lse[b, :, :n])
         assert np.all(err <= e + 2.0 ** -20 * (1 + np.abs(want_lse[b, :, :n]) + top[b, :, :n])), (b, err.max(), e.max())
         err, bound = np.abs(o[b, :, :n] - want[b, :, :n]), (2.0 ** -8 + 2 * e[..., None] + 2.0 ** -16) * size[b, :, :n]
-        assert np.all(err <= bound + 2.0 ** -8 * np.abs(want[b, :, :n])), (b, err.max())
+        lost = 2.0 ** -95 * k.shape[2] * np.abs(v[b]).max()
+        assert np.all(err <= bound + 2.0 ** -8 * np.abs(want[b, :, :n]) + lost), (b, err.max())
         none = size[b, :, :n].sum(-1) == 0
         assert np.all(o[b, :, :n][none] == 0) and np.all(lse[b, :, :n][none] == 0)
 
@@ -203,6 +207,25 @@ def test_prefill_of_padding_that_is_no_number():
     dirty = kv.prefill(q, *pool, pu.i64([200, 150]), pu.i64(counts), table=table)
     for b, n in enumerate(counts):
         assert torch.equal(clean[0][b, :, :n], dirty[0][b, :, :n]) and torch.equal(clean[1][b, :, :n], dirty[1][b, :, :n])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("n,D", [(20, 64), (20, 128), (130, 64), (130, 128)], ids=lambda x: str(x))
+def test_prefill_scores_that_rise_from_tile_to_tile(n, D, fmt):
+    """By more than 2^30 each 32 keys, for some rows all the way and for others now and then, so that what there is follows again
+    and again; rows of one tile and of several."""
+    B, Hq, Hkv, S = 2, 4, 2, 1500
+    rng = np.random.default_rng(D + n)
+    k = np.broadcast_to(np.arange(S)[None, None, :, None] * 0.1, (B, Hkv, S, D)).astype(np.float32).copy()
+    k[:, 1] *= np.where(rng.random((B, S, 1)) < 0.02, 1.0, 0.5)
+    k[1] = k[1, :, ::-1]   # falling: the first scores stay the reference
+    planes = pu.planes_of(k, rng.standard_normal(k.shape).astype(np.float32), fmt)
+    q = (1 + 0.05 * pu.queries(B, Hq, n, D, 4).float()).to(torch.bfloat16)
+    lens = [S, S - 77]
+    got = kv.prefill(q, *planes, pu.i64(lens), scale=8 / D)
+    assert ft.device_status() == 0
+    check(q, planes, lens, [n, n], got, scale=8 / D)
 
 
 @pytest.mark.gpu
