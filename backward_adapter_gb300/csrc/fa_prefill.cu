@@ -25,10 +25,10 @@
 // Measured (device time, captured calls over changing inputs): 512 tokens over 67,584 keys in 4 bits, 16 heads on 4, D = 128: 253 us,
 // 1.12 PFLOP/s, 58% of the measured dense rate; two prompts of 4096 tokens in 8 bits, 32 heads on 8: 337 to 343 us, 0.8 PFLOP/s of visible
 // pairs; 24 tokens of 8 sequences of 500 to 4000 keys in 4 bits: 33 us; chunks of 1 to 777 tokens of 6 sequences of 300 to 9000 keys in 8
-// bits, D = 64, in a sliding window of 1024: 51 us. What bounds it: a tile of keys and 256 rows takes 4400 cycles, of which the tensor cores are busy for half:
-// each tile of rows goes from S to softmax (2400 cycles for 128 scores a row) to P V and back, and two of them on that way
+// bits, D = 64, in a sliding window of 1024: 51 us. What bounds it: a tile of keys and 256 rows takes 4400 cycles, of which the
+// tensor cores are busy for half: each tile of rows goes from S to softmax (2400 cycles for 128 scores a row) to P V and back, and two of them on that way
 // do not fill the pipe; in copies without softmax the first case takes 204 us, without operands made from bytes as well 169. With few
-// tokens it is the way: 2.7 us for the list, 1.5 to the first bytes, 2.2 for each tile of keys, 1.5 for O, and the join.
+// tokens it is the way: 2.7 us for the list, 1.5 to the first bytes, 1.5 to 2 for each tile of keys, 1.5 for O, and the join.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
