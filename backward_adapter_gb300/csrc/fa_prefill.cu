@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   uint64_t* bar_s = bars + 2;                     // [2]: scores of tile t there; ALONE: of even and odd tiles of keys
   uint64_t* bar_p = bars + 4;                     // [2]: weights there, likewise
   uint64_t* bar_o = bars + 6;                     // [2]: the last product of tile t done
-  uint64_t* bar_v = bars + 8;                     // ALONE: a product done
-  uint64_t* bar_full = bars + 9;                  // [kStages]: stage written
+  uint64_t* bar_v = bars + 8;                     // [2], ALONE: an even, an odd product done
+  uint64_t* bar_full = bars + 10;                 // [kStages]: stage written
   uint64_t* bar_empty = bar_full + L::kStages;    // [kStages]: its MMAs done
   uint64_t* bar_piece = bar_empty + L::kStages;   // [kPieces]: part of a unit described
   uint64_t* bar_past = bar_piece + kPieces;       // [kPieces]: nobody looks at it any more
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   uint64_t* bar_done = bar_read + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (9 + 2 * L::kStages + 2 * kPieces + 3) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
+  static_assert(8 * (10 + 2 * L::kStages + 2 * kPieces + 3) + 8 <= 256 + 64 && kPieces * sizeof(Piece) <= 320, "shared memory of barriers and parts");
   Piece* pieces = reinterpret_cast<Piece*>(smem + L::kPieceOff);
   Plan& plan = *reinterpret_cast<Plan*>(smem + L::kPlanOff);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(&bar_s[t], 1);
       mbar_init(&bar_p[t], 4);
       mbar_init(&bar_o[t], 1);
+      mbar_init(&bar_v[t], 1);
     }
-    mbar_init(bar_v, 1);
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&bar_full[i], kLoaders);
       mbar_init(&bar_empty[i], 1);
@@ -419,13 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       int loads0 = 0, loads1 = 0;       // of bar_q
       int pending = 0;                  // tiles of rows of the last tile of keys whose product is to come
       bool pending_first = false, pending_last = false;   // it is its part's first, last
-      int pending_b = 0;   // ALONE: its buffer
+      int pending_b = 0, products = 0;   // ALONE: its buffer; products so far
       auto product = [&](int t, int slot) -> bool {
         const int b = ALONE ? pending_b : t;
         if (!wait(&bar_p[b], (b ? scores1 : scores0) - 1, 1001)) return false;
         tc_fence_after();
         issue_pv(t, b, slot, pending_first);
-        if (ALONE) mma_commit_if(lead, bar_v);
+        if (ALONE) mma_commit_if(lead, &bar_v[products++ & 1]);
         if (pending_last) mma_commit_if(lead, &bar_o[t]);
         return true;
       };
@@ -443,6 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int j = 0; ok && j < max(tiles, 1); ++j) {   // behind the last part a stage that holds only V
           const int sb = stage % L::kStages;
           if (!(ok = wait(&bar_full[sb], stage / L::kStages, 1002))) break;
+          // The last product but one has ended and is seen before more scores are made, so that who waits for the last one's barrier
+          // meets it one completion short or complete, never two short, which a phase's parity cannot tell from complete.
+          if (ALONE && products >= 2 && !(ok = wait(&bar_v[products & 1], products / 2 - 1, 1013))) break;
           tc_fence_after();
           const bool last = j == tiles - 1;
           if (j == 0) {   // rolled: what warps go through has to come from the instruction caches
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     bool ok = true;
     int scored = 0, finished = 0;   // completions of bar_s and bar_o so far
-    int b = t, scored1 = 0, made = 0;   // ALONE: the buffer at hand; of bar_s[1]; of bar_v, with those to come for weights that are there
+    int b = t, scored1 = 0, made = 0;   // ALONE: the buffer at hand; of bar_s[1]; products of weights that are there, done or to come
     int part = 0;
     for (; next_live(part); ++part) {
       int key0, key_hi, left;   // of the next tile: its first key, and the last one that this row sees
@@ -709,9 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               tmem_st16(tS + d * 16, pk);
             }
             if (!first) {   // O holds the products of the tiles before: their MMAs ended before these scores did
-              if constexpr (ALONE) {   // ... but for the last one's, and that of the one before is what bar_v may still be at
-                const bool there = mbar_wait<true>(bar_v, made & 1, abort_flag, a.status, 1012) &&
-                                   mbar_wait<true>(bar_v, (made - 1) & 1, abort_flag, a.status, 1012);
+              if constexpr (ALONE) {   // ... but for the last one's, product made - 1; what a wait has seen passes at once again
+                const bool there = mbar_wait<true>(&bar_v[(made - 1) & 1], ((made - 1) >> 1) & 1, abort_flag, a.status, 1012);
                 ok = __all_sync(0xffffffffu, there) && ok;
                 tc_fence_after();
               }
