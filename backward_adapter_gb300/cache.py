@@ -351,7 +351,7 @@ def cache_evict(k_q, k_d, v_q, v_d, weights, lengths, keep: int, *, sinks: int =
     h had, -1 behind the last. lengths: int64 [B] on the device. The rows move to the first pages of table, or to those of
     table_out (int32 [B, ...] with room for `keep` keys), which leaves the pages of table as they are; without a table,
     to the front of the sequence. A page that rows move to is in one place of one table only: sequences that share pages
-    need a table_out. The weights of the keys that stay go to weights_out (default: weights itself), 0 behind them.
+    need a table_out (table itself, or its first columns, means in place). The weights of the keys that stay go to weights_out (default: weights itself), 0 behind them.
     """
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device

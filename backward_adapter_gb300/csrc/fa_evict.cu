@@ -378,6 +378,20 @@ cudaError_t launch_evict(const EvictArgs& a, long long heads, int blocks, cudaSt
   return e;
 }
 
+// Whether two tables of the same sequences have an entry of memory in common.
+bool share_entries(const fa_pages& x, const fa_pages& y) {
+  const long long sx = x.B > 1 ? x.stride : x.M, sy = y.B > 1 ? y.stride : y.M;
+  const long long off = ((long long)(intptr_t)y.table - (long long)(intptr_t)x.table) / 4;   // both are 4-byte aligned
+  if (off >= sx * (x.B - 1) + x.M || off + sy * (y.B - 1) + y.M <= 0) return false;
+  for (int b = 0; b < y.B; ++b) {
+    const long long from = off + b * sy, past = from + y.M;   // of y's row b, in entries from x's first on
+    const long long row = from < 0 ? -1 : from / sx;          // x's last row that begins at or before it
+    if (row >= 0 && row < x.B && from - row * sx < x.M) return true;
+    if (row + 1 < x.B && (row + 1) * sx < past) return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -404,6 +418,9 @@ extern "C" fa_status fa_cache_evict(const fa_evict_params* p, const fa_cache* c,
   if (to != nullptr && there.S < p->keep) {
     set_error("the second table has room for %d keys of %d", there.S, p->keep); return FA_ERR_INVALID_ARG;
   }
+  // the same table again: in place
+  const bool move = to == nullptr || (to->table == pages->table && (to->B == 1 || to->stride == pages->stride));
+  if (!move && share_entries(*pages, *to)) { set_error("the two tables share entries"); return FA_ERR_INVALID_ARG; }
   if (W < 1 || W > 1LL << 30) { set_error("W=%lld outside [1, 2^30]", (long long)W); return FA_ERR_INVALID_ARG; }
   const long long heads = (long long)cv.B * cv.Hkv;
   if (heads * p->keep > 0x7fffffffLL - 512) { set_error("too many heads for one launch"); return FA_ERR_UNSUPPORTED; }
@@ -445,7 +462,7 @@ extern "C" fa_status fa_cache_evict(const fa_evict_params* p, const fa_cache* c,
     constexpr int D = decltype(dim)::value;
     constexpr bool Q4 = decltype(q4)::value;
     cudaStream_t cs = (cudaStream_t)stream;
-    if (to != nullptr) return launch_evict<D, Q4, true, false>(a, heads, blocks, cs);
+    if (!move) return launch_evict<D, Q4, true, false>(a, heads, blocks, cs);
     return pages != nullptr ? launch_evict<D, Q4, true, true>(a, heads, blocks, cs) : launch_evict<D, Q4, false, true>(a, heads, blocks, cs);
   };
   using D64 = std::integral_constant<int, 64>;

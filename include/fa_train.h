@@ -465,7 +465,8 @@ FA_API fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, con
  * more than `keep` keeps all. Written are
  *   the rows of the planes, to the same pages (to == NULL), or to those of the table `to` (for the same sequences, room for
  *     `keep` keys), which leaves the pages moved from as they are. The caller sees to it that a page written to is in one place
- *     of one table only: where sequences share pages, those that are cut need a table `to` of pages of their own;
+ *     of one table only: where sequences share pages, those that are cut need a table `to` of pages of their own (the same table
+ *     again, or its first columns, means the same pages; two tables that have other entries in common are refused);
  *   kept int32 [B, Hkv, keep]: the index each key had, -1 behind the last one;
  *   weights_out fp32 [B, Hkv, W]: the weights of the keys that stay, 0 behind them; may be weights;
  *   new_lengths int64 [B]: min(length, keep).
