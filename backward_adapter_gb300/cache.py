@@ -158,13 +158,16 @@ def cache_read(k_q, k_d, v_q, v_d, begin=0, n_rows=None, *, table=None, dtype=to
                k=None, v=None, stream=None):
     """The values of keys begin .. begin + n_rows - 1 (default: to the end) of every sequence and head: (k, v)
     [B, Hkv, n_rows, D] (or [B, n_rows, Hkv, D]) in dtype (bfloat16 or float32), or written into the given k and v.
-    begin: an int for every sequence, or int64 [B] on the device (with n_rows; a row outside the cache is read as zeros and
-    is reported by device_status()). table: the planes are a pool of pages (see new_cache)."""
+    begin: a number for every sequence (in a tensor too), or int64 [B] on the device (with n_rows; a row outside
+    the cache is read as zeros and is reported by device_status()). table: the planes are a pool of pages (see new_cache)."""
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device
     seen, pages, held = _paged(c, table, device)
     S = seen[2]
     begins = None
+    if isinstance(begin, torch.Tensor) and begin.numel() == 1 and \
+            (begin.dim() == 0 or n_rows is None or begin.dtype != torch.int64 or begin.device != device):
+        begin = int(begin)   # a number, for every sequence
     if isinstance(begin, torch.Tensor):
         if n_rows is None:
             raise ValueError("n_rows is needed where every sequence has its own begin")
