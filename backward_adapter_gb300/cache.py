@@ -21,7 +21,8 @@ def new_cache(B: int, Hkv: int, S: int, D: int, fmt: str = "q8_0", device="cuda"
 
     A pool of pages is the same with B pages of S keys (a multiple of 16); the calls that take a `table` find key j of
     sequence b at row j % S of page table[b, j // S] of it (int32 [sequences, pages of a sequence] on the device; entries
-    behind a sequence's keys are not looked at, one that is no page is reported by device_status())."""
+    behind a sequence's keys are not looked at, one that is no page is reported by device_status(); in place of a page that a
+    window hides and that was given up any page of the pool will do)."""
     if fmt not in FORMATS:
         raise ValueError(f"fmt {fmt!r}: 'q8_0' or 'q4_0'")
     if D % 32 != 0:

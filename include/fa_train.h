@@ -391,7 +391,8 @@ FA_API fa_status fa_decode(const fa_decode_params* p, const void* q, const fa_ca
 /*
  * The pages of a cache. The planes are then a pool: fa_cache.B is its pages (up to 2^31 - 1 of them), fa_cache.S the keys of
  * a page, a multiple of 16; key j of sequence b is row j % S of page table[b * stride + j / S]. A sequence has room for M * S
- * keys, at most 2^24. Entries behind a sequence's keys are not looked at. What the device finds cannot be checked before the
+ * keys, at most 2^24. Entries behind a sequence's keys are not looked at; those of keys that a window hides may be: in place of
+ * a page that was given up any page of the pool will do, whatever it holds. What the device finds cannot be checked before the
  * launch: keys of an entry outside [0, fa_cache.B) count as zeros and are not written, and 0x40000000 | 953 is recorded
  * in the status word. A page may be in several places of the table as long as nothing is written to it there.
  * Where an entry point takes pages, NULL stands for a cache without: then sequence b is fa_cache's b, with S keys.
