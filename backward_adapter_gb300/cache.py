@@ -313,14 +313,17 @@ def _key_weights(name: str, t, B: int, Hkv: int, device) -> int:
 
 
 def cache_weights(q, lse, k_q, k_d, lengths=None, count=None, *, weights=None, out=None, table=None, scale=None,
-                  window: int = 0, layout: str = "bhsd", stream=None):
+                  window: int = 0, layout: str = "bhsd", decoded: bool = False, stream=None):
     """The attention weight that every key got from the new tokens, added to `weights`: float32 [B, Hkv, W].
 
     out[b, h, j] = weights[b, h, j] + sum of exp(scale q k_j - lse) over the tokens that see key j and the query heads of
-    head h. q, lengths, count, table, scale, window and layout are those of prefill (or of decode, whose Sq tokens are all of
-    them), lse [B, Hq, Sq] is what it returned. weights: W at least the longest length (without: zeros, W what a
+    head h. q, lengths, count, table, scale, window and layout are those of prefill, lse [B, Hq, Sq] is what it returned, and K is
+    rounded to bf16 as there. decoded: they are those of decode (up to 16 tokens, all of them: no count), which does not round K,
+    and the weights go with its LSE. weights: W at least the longest length (without: zeros, W what a
     sequence has room for). out may be weights; without, it is a new tensor.
     """
+    if decoded and count is not None:
+        raise ValueError("decode attends with all of q's tokens: no count")
     c = _cache(k_q, k_d, k_q, k_d)
     device = k_q.device
     seen, pages, held = _paged(c, table, device)
@@ -340,8 +343,9 @@ def cache_weights(q, lse, k_q, k_d, lengths=None, count=None, *, weights=None, o
     counts = None if count is None else _per_sequence("count", count, B, device)
     call = _DecodeCall(*c, Hq, min(Sq, 0x7fffffff), _window(window), code, 1.0 / math.sqrt(D) if scale is None else scale, 0)
     at = ctypes.addressof(call)
-    ft._launch(device, ft.load_library().fa_cache_weights, at + _CACHE, q.data_ptr(), lse.data_ptr(), at, pages, lens, counts,
-               ft._ptr(weights), W, out.data_ptr(), ft._stream(device, stream))
+    lib, which = ft.load_library(), (lens,) if decoded else (lens, counts)
+    ft._launch(device, lib.fa_cache_weights_decoded if decoded else lib.fa_cache_weights, at + _CACHE, q.data_ptr(), lse.data_ptr(),
+               at, pages, *which, ft._ptr(weights), W, out.data_ptr(), ft._stream(device, stream))
     return out
 
 

@@ -59,7 +59,6 @@
 namespace fa {
 namespace {
 
-constexpr int kMaxTokens = 16;
 constexpr int kTile = 32;         // keys a warp takes at a time
 constexpr int kMaxListed = 1024;  // sequences whose lengths a block lists
 constexpr int kStart = 3;         // tiles' time that a head costs the warp that begins with it, measured
@@ -1060,7 +1059,7 @@ fa_status check_decode(const fa_decode_params* p, const fa_cache* c, const fa_pa
   if (st != FA_OK) return st;
   if (p->Hq < 1 || p->Hq > 65535) { set_error("Hq=%d outside [1, 65535]", p->Hq); return FA_ERR_INVALID_ARG; }
   if (p->Hq % cv.Hkv != 0) { set_error("Hq=%d is not a multiple of Hkv=%d", p->Hq, cv.Hkv); return FA_ERR_INVALID_ARG; }
-  if (p->Sq < 0 || p->Sq > kMaxTokens) { set_error("Sq=%d outside [0, %d]", p->Sq, kMaxTokens); return FA_ERR_INVALID_ARG; }
+  if (p->Sq < 0 || p->Sq > kDecodeTokens) { set_error("Sq=%d outside [0, %d]", p->Sq, kDecodeTokens); return FA_ERR_INVALID_ARG; }
   if (p->window < 0) { set_error("window=%d must be >= 0 (0 = no window)", p->window); return FA_ERR_INVALID_ARG; }
   if (p->layout != FA_LAYOUT_BHSD && p->layout != FA_LAYOUT_BSHD) { set_error("layout=%d invalid", p->layout); return FA_ERR_INVALID_ARG; }
   if (!std::isfinite(p->scale)) { set_error("scale is not finite"); return FA_ERR_INVALID_ARG; }

@@ -222,6 +222,7 @@ struct PageView {
 };
 constexpr unsigned kSiteCacheRow = 951;
 constexpr unsigned kSiteDecodeLength = 952;
+constexpr int kDecodeTokens = 16;   // of a sequence in fa_decode, at most
 constexpr unsigned kSitePage = 953;
 // fa_cache_write: begin (device) or begin_all when NULL; count (device) or n_rows when NULL.
 cudaError_t launch_cache_write(const CacheView& c, const PageView& pages, const RowView& k, const RowView& v, int dtype,

@@ -1,4 +1,5 @@
-// The attention weight that every key of a quantized cache got from a chunk of new tokens (fa_cache_weights).
+// The attention weight that every key of a quantized cache got from a chunk of new tokens (fa_cache_weights), or from decoded ones
+// (fa_cache_weights_decoded).
 //
 // Mathematics. P_ij = exp(scale <q_i, k_j> - lse_i) summed over the rows i (tokens and query heads of the key's head) that see
 // key j. With K as the left operand the products S^T = K Q^T have a key for each lane of TMEM and a row for each column, so
@@ -116,6 +117,12 @@ struct Scale4 {
     const uint32_t n = add_bf16x2((nibbles & 0x000f000fu) | 0x43004300u, 0xc308c308u);
     return fma_bf16x2(n, dh, mul_bf16x2(n, dl));
   }
+  // ... and what is left of d n, which `value` rounds: n dh less that, and with n dl, have no more than seven bits each.
+  __device__ __forceinline__ uint32_t value(uint32_t nibbles, uint32_t& rest) const {
+    const uint32_t n = add_bf16x2((nibbles & 0x000f000fu) | 0x43004300u, 0xc308c308u), v = fma_bf16x2(n, dh, mul_bf16x2(n, dl));
+    rest = fma_bf16x2(n, dl, fma_bf16x2(n, dh, v ^ 0x80008000u));
+    return v;
+  }
 };
 __device__ __forceinline__ uint32_t value_q8(uint32_t u, int k, uint64_t dd) {   // bytes k, k + 1, 128 more
   const uint64_t n = add_f32x2(f32x2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | k)),
@@ -124,10 +131,21 @@ __device__ __forceinline__ uint32_t value_q8(uint32_t u, int k, uint64_t dd) {  
   f32x2_split(mul_f32x2(n, dd), lo, hi);
   return pack_bf16x2(lo, hi);
 }
+__device__ __forceinline__ uint32_t value_q8(uint32_t u, int k, uint64_t dd, uint32_t& rest) {   // ... and the rest of d n, rounded
+  const uint64_t n = add_f32x2(f32x2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | k)),
+                                     __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | (k + 1)))), f32x2(-8388736.f, -8388736.f));
+  float lo, hi;
+  f32x2_split(mul_f32x2(n, dd), lo, hi);
+  const uint32_t v = pack_bf16x2(lo, hi);
+  rest = pack_bf16x2(lo - __uint_as_float(v << 16), hi - __uint_as_float(v & 0xffff0000u));
+  return v;
+}
 
-// NT * 8 rows at most. A warp has `runs` runs of 16 keys.
-template <int D, bool Q4, bool PAGED, int NT>
-__global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant__ WeightArgs a, int runs, unsigned chunks, unsigned warps) {
+// NT * 8 rows at most, from row0 on. A warp has `runs` runs of 16 keys. STORED: keys are not rounded: of d n, a product of 11 and
+// 4 (8) bits, the bf16 number and what that leaves, in 4 bits one as well, in 8 to 2^-17 of d n, are operands of two products, summed up
+// apart (a token of 64 sequences of 1024 to 8192 keys, 32 heads on 8, D = 128: 110 us where rounded keys take 84, in 8 bits 131 and 91).
+template <int D, bool Q4, bool PAGED, int NT, bool STORED>
+__global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant__ WeightArgs a, int runs, unsigned chunks, unsigned warps, int row0) {
   constexpr int W = Quarter<D, Q4>::W, STEPS = D / 16;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const unsigned id = blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -165,7 +183,7 @@ __global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant_
       const int i = r / a.G, head = h * a.G + r % a.G;
       return a.layout ? ((size_t)b * a.Sq + i) * a.Hq + head : ((size_t)b * a.Hq + head) * a.Sq + i;
     };
-    const int r = 8 * m + g;
+    const int r = (STORED ? row0 : 0) + 8 * m + g;
     const bool on = first < past && r < n * a.G;
     const uint2* src = reinterpret_cast<const uint2*>(a.q + (on ? place(r) * D : 0));
 #pragma unroll
@@ -178,7 +196,7 @@ __global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant_
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int c = 8 * m + 2 * t + j;
+      const int c = (STORED ? row0 : 0) + 8 * m + 2 * t + j;
       const bool live = c < n * a.G;
       const int i = c / a.G, head = h * a.G + c % a.G;
       less[m][j] = live && first < past ? -__ldg(a.lse + ((size_t)b * a.Hq + head) * a.Sq + i) * kLog2e : -CUDART_INF_F;
@@ -192,7 +210,51 @@ __global__ void __launch_bounds__(128) weights_few_kernel(const __grid_constant_
     float c[NT][4];
 #pragma unroll
     for (int m = 0; m < NT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
-    if constexpr (Q4) {
+    if constexpr (STORED) {
+      float rest[NT][4];
+#pragma unroll
+      for (int m = 0; m < NT; ++m) rest[m][0] = rest[m][1] = rest[m][2] = rest[m][3] = 0.f;
+      // a step: the pairs of both rows, and their products with the step's pairs of q
+      auto product = [&](int j, const uint32_t (&v)[4], const uint32_t (&w)[4]) {
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          mma_bf16(c[m], v[0], v[1], v[2], v[3], q[m][j][0], q[m][j][1]);
+          mma_bf16(rest[m], w[0], w[1], w[2], w[3], q[m][j][0], q[m][j][1]);
+        }
+      };
+      uint32_t v[4], w[4];
+      if constexpr (Q4) {
+        const Scale4 d0(x.d[0]), d1(x.d[1]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t r0 = x.w[0][j] >> (4 * half), r1 = x.w[1][j] >> (4 * half);
+            v[0] = d0.value(r0, w[0]);
+            v[1] = d1.value(r1, w[1]);
+            v[2] = d0.value(r0 >> 8, w[2]);
+            v[3] = d1.value(r1 >> 8, w[3]);
+            product(2 * j + half, v, w);
+          }
+        }
+      } else {
+        const float f0 = __half2float(__ushort_as_half(x.d[0])), f1 = __half2float(__ushort_as_half(x.d[1]));
+        const uint64_t d0 = f32x2(f0, f0), d1 = f32x2(f1, f1);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const uint32_t r0 = x.w[0][j] ^ 0x80808080u, r1 = x.w[1][j] ^ 0x80808080u;
+          v[0] = value_q8(r0, 0, d0, w[0]);
+          v[1] = value_q8(r1, 0, d1, w[1]);
+          v[2] = value_q8(r0, 2, d0, w[2]);
+          v[3] = value_q8(r1, 2, d1, w[3]);
+          product(j, v, w);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[m][j] += rest[m][j];
+    } else if constexpr (Q4) {
       const Scale4 d0(x.d[0]), d1(x.d[1]);
 #pragma unroll
       for (int j = 0; j < W; ++j) {
@@ -577,13 +639,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   }
 }
 
-template <int D, bool Q4, bool PAGED, int NT>
-cudaError_t launch_weights_few(const WeightArgs& a, long long heads, cudaStream_t st) {
+template <int D, bool Q4, bool PAGED, int NT, bool STORED>
+cudaError_t launch_weights_few(const WeightArgs& a, long long heads, cudaStream_t st, int row0 = 0) {
   // 256 keys a warp, so that what comes before the first costs little, where that leaves eight warps for each SM at least, else 64 (groups of four runs)
   const int runs = heads * ((a.W + 255) / 256) >= 8LL * sm_count() ? 16 : 4;
   const long long chunks = (a.W + runs * kRun - 1) / (runs * kRun), warps = heads * chunks;
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  weights_few_kernel<D, Q4, PAGED, NT><<<(unsigned)((warps + 3) / 4), 128, 0, st>>>(a, runs, (unsigned)chunks, (unsigned)warps);
+  weights_few_kernel<D, Q4, PAGED, NT, STORED><<<(unsigned)((warps + 3) / 4), 128, 0, st>>>(a, runs, (unsigned)chunks, (unsigned)warps, row0);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -615,11 +677,12 @@ cudaError_t launch_weights(const WeightArgs& a, long long heads, cudaStream_t st
 
 using namespace fa;
 
-extern "C" fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, const float* lse, const fa_cache* c,
-                                      const fa_pages* pages, const int64_t* lengths, const int64_t* count,
-                                      const float* weights, int64_t W, float* out, void* stream) {
-  clear_error();
-  if (p == nullptr) { set_error("params is NULL"); return FA_ERR_INVALID_ARG; }
+namespace {
+
+// stored: the LSE was made with keys as they are stored, which then are not rounded.
+fa_status key_weights(const fa_prefill_params* p, const void* q, const float* lse, const fa_cache* c, const fa_pages* pages,
+                      const int64_t* lengths, const int64_t* count, const float* weights, int64_t W, float* out, bool stored,
+                      void* stream) {
   CacheView held, cv;
   PageView pv;
   Span in[8], planes[4], outs[1];
@@ -671,8 +734,18 @@ extern "C" fa_status fa_cache_weights(const fa_prefill_params* p, const void* q,
     cudaStream_t cs = (cudaStream_t)stream;
     auto of = [&](auto paged) {
       constexpr bool P = decltype(paged)::value;
-      if (rows_of_head <= 8) return launch_weights_few<D, Q4, P, 1>(a, heads, cs);
-      if (rows_of_head <= 16) return launch_weights_few<D, Q4, P, 2>(a, heads, cs);
+      if (stored) {   // 16 rows after the other, each launch's weights on top of the last one's
+        WeightArgs x = a;
+        for (long long row0 = 0;; row0 += 16) {
+          const bool few = rows_of_head - row0 <= 8;
+          const cudaError_t e = few ? launch_weights_few<D, Q4, P, 1, true>(x, heads, cs, (int)row0)
+                                    : launch_weights_few<D, Q4, P, 2, true>(x, heads, cs, (int)row0);
+          if (e != cudaSuccess || row0 + 16 >= rows_of_head) return e;
+          x.weights = x.out;
+        }
+      }
+      if (rows_of_head <= 8) return launch_weights_few<D, Q4, P, 1, false>(a, heads, cs);
+      if (rows_of_head <= 16) return launch_weights_few<D, Q4, P, 2, false>(a, heads, cs);
       return launch_weights<D, Q4, P>(a, heads, cs);
     };
     return pages != nullptr ? of(std::true_type{}) : of(std::false_type{});
@@ -684,3 +757,27 @@ extern "C" fa_status fa_cache_weights(const fa_prefill_params* p, const void* q,
   else e = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
   return cuda_status(e, "cache weights launch");
 }
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, const float* lse, const fa_cache* c, const fa_pages* pages,
+                           const int64_t* lengths, const int64_t* count, const float* weights, int64_t W, float* out,
+                           void* stream) {
+  clear_error();
+  if (p == nullptr) { set_error("params is NULL"); return FA_ERR_INVALID_ARG; }
+  return key_weights(p, q, lse, c, pages, lengths, count, weights, W, out, false, stream);
+}
+
+fa_status fa_cache_weights_decoded(const fa_decode_params* p, const void* q, const float* lse, const fa_cache* c,
+                                   const fa_pages* pages, const int64_t* lengths, const float* weights, int64_t W, float* out,
+                                   void* stream) {
+  clear_error();
+  if (p == nullptr) { set_error("params is NULL"); return FA_ERR_INVALID_ARG; }
+  if (p->Sq > kDecodeTokens) { set_error("Sq=%d outside [0, %d]", p->Sq, kDecodeTokens); return FA_ERR_INVALID_ARG; }
+  const fa_prefill_params x{p->Hq, p->Sq, p->window, p->layout, p->scale, p->reserved};
+  return key_weights(&x, q, lse, c, pages, lengths, nullptr, weights, W, out, true, stream);
+}
+
+}  // extern "C"

@@ -31,7 +31,7 @@ EXPORTED = ("fa_train_fwd_workspace_size", "fa_train_bwd_workspace_size", "fa_tr
             "fa_train_bwd_accum_q4", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
             "fa_cache_write", "fa_cache_read", "fa_decode", "fa_decode_workspace_size", "fa_cache_write_pages",
             "fa_cache_read_pages", "fa_decode_pages", "fa_decode_pages_workspace_size", "fa_prefill",
-            "fa_prefill_workspace_size", "fa_cache_weights", "fa_cache_evict")
+            "fa_prefill_workspace_size", "fa_cache_weights", "fa_cache_weights_decoded", "fa_cache_evict")
 FA_KERNEL_FWD, FA_KERNEL_BWD_MAIN, FA_KERNEL_BWD_DSUM, FA_KERNEL_BWD_DQ_CONVERT, FA_KERNEL_MASK_CLASSIFY = range(5)
 
 
@@ -182,6 +182,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_prefill.restype = st
     lib.fa_cache_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
     lib.fa_cache_weights.restype = st
+    lib.fa_cache_weights_decoded.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
+    lib.fa_cache_weights_decoded.restype = st
     lib.fa_cache_evict.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     lib.fa_cache_evict.restype = st
     lib.fa_train_bwd_plan.argtypes = [P, ctypes.POINTER(i32), i32, ctypes.POINTER(i32)]

@@ -448,7 +448,7 @@ FA_API fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_
 
 /*
  * The weight that every key got from the new tokens: with the tokens, positions and visible keys of fa_prefill, and lse as
- * fa_prefill or fa_decode left it,
+ * fa_prefill left it,
  *     out[b, h, j] = weights[b, h, j] + sum over the query heads g of head h and the tokens i that see key j
  *                                       of exp(scale <q_gi, k_j> - lse_gi)
  * for every j below W (room for at least the sequences' lengths: a key at or past W is left out, and 0x40000000 | 952
@@ -458,6 +458,16 @@ FA_API fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_
 FA_API fa_status fa_cache_weights(const fa_prefill_params* p, const void* q, const float* lse, const fa_cache* c,
                                   const fa_pages* pages, const int64_t* lengths, const int64_t* count, const float* weights,
                                   int64_t W, float* out, void* stream);
+
+/*
+ * The same after fa_decode (p and lengths as there; all Sq tokens, up to 16, of every sequence), whose K is not rounded to bf16
+ * and whose LSE so belongs to other scores: here K is what is stored (8 bits: each value to within 2^-17), and a token's weights add
+ * up to 1 as closely as 32-bit scores let them. (Given fa_decode's LSE, fa_cache_weights is off by a factor of up to
+ * exp(2^-8 |scale| sum_d |q_d k_d|) for each key.) More than 16 query rows of a key/value head take 16 at a time.
+ */
+FA_API fa_status fa_cache_weights_decoded(const fa_decode_params* p, const void* q, const float* lse, const fa_cache* c,
+                                          const fa_pages* pages, const int64_t* lengths, const float* weights, int64_t W,
+                                          float* out, void* stream);
 
 /*
  * Eviction: of every sequence with more than `keep` keys, `keep` of each head stay: those below `sinks`, the last `recent`, and
