@@ -191,6 +191,12 @@ fa_status cuda_status(cudaError_t e, const char* what) {
   return FA_ERR_CUDA;
 }
 
+fa_status check_split(const char* what, int registers, int need) {
+  if (registers == need) return FA_OK;
+  set_error("%s: compiled to %d registers a thread where its warps divide %d; build with the CUDA 13.0 compiler", what, registers, need);
+  return FA_ERR_UNSUPPORTED;
+}
+
 namespace {
 
 // The tcgen05 path takes bf16 inputs; fp32 inputs stay on the SIMT fp32 path.

@@ -33,6 +33,15 @@ fa_status check_apart(const Span* in, int nin, const Span* out, int nout);
 // The workspace is large enough, 256-byte aligned and overlaps none of the call's buffers.
 fa_status check_ws(void* ws, size_t ws_bytes, size_t need, const Span* bufs, int n);
 fa_status cuda_status(cudaError_t e, const char* what);
+// Whether a kernel whose warps divide its registers among them was compiled with the `need` a thread that they count on: with fewer
+// a warp that asks for its share would wait for ever.
+fa_status check_split(const char* what, int registers, int need);
+template <typename K>
+fa_status check_split(K kernel, const char* what, int need) {
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+  return e != cudaSuccess ? cuda_status(e, what) : check_split(what, at.numRegs, need);
+}
 
 // An fa_view of B x S rows of H heads of D features of es bytes: fills `out` with the bytes it
 // spans. `written`: its rows must not overlap. A view without rows spans nothing and may be NULL.

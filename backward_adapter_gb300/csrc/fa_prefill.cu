@@ -997,22 +997,20 @@ fa_status check_prefill(const fa_prefill_params* p, const fa_cache* c, const fa_
 }
 
 template <int D, bool Q4, bool PAGED, bool ALONE>
-cudaError_t launch_prefill(const PrefillArgs& a, int slices, cudaStream_t st) {
+fa_status launch_prefill(const PrefillArgs& a, int slices, cudaStream_t st) {
   constexpr int bytes = PrefillSmem<D>::kBytes;
   static_assert(bytes <= 232448, "shared memory of a block");
   auto kernel = prefill_kernel<D, Q4, PAGED, ALONE>;
   static std::atomic<uint64_t> allowed{0};
-  if (allowed.load(std::memory_order_acquire) == 0) {   // the split of registers holds for what the kernel is launched with
-    cudaFuncAttributes at;
-    const cudaError_t got = cudaFuncGetAttributes(&at, kernel);
-    if (got != cudaSuccess) return got;
-    if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+  if (allowed.load(std::memory_order_acquire) == 0) {
+    const fa_status got = check_split(kernel, "prefill launch", kRegsLaunch);
+    if (got != FA_OK) return got;
   }
   const cudaError_t e = allow_shared(kernel, bytes, allowed);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess) return cuda_status(e, "prefill launch");
   kernel<<<(unsigned)slices, kThreads, bytes, st>>>(a);
   count_launches(1);
-  return cudaGetLastError();
+  return cuda_status(cudaGetLastError(), "prefill launch");
 }
 
 }  // namespace
@@ -1113,23 +1111,21 @@ fa_status fa_prefill(const fa_prefill_params* p, const void* q, const fa_cache* 
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;
-    cudaError_t e;
-    if (cv.q4) e = cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
-    else e = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
-    if (e == cudaSuccess) {
-      cudaLaunchAttribute at{};
-      at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      at.val.programmaticStreamSerializationAllowed = 1;
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(3 * plan.slices);   // what the SMs hold at a time
-      cfg.blockDim = dim3(256);
-      cfg.dynamicSmemBytes = plan.slices * sizeof(Record) + (plan.slices + 1) * sizeof(int);
-      cfg.stream = cs;
-      cfg.attrs = &at;
-      cfg.numAttrs = 1;
-      e = cudaLaunchKernelEx(&cfg, cv.D == 64 ? prefill_join_kernel<64> : prefill_join_kernel<128>, a, plan.slices);
-      count_launches(1);
-    }
+    if (cv.q4) st = cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
+    else st = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
+    if (st != FA_OK) return st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(3 * plan.slices);   // what the SMs hold at a time
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = plan.slices * sizeof(Record) + (plan.slices + 1) * sizeof(int);
+    cfg.stream = cs;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cv.D == 64 ? prefill_join_kernel<64> : prefill_join_kernel<128>, a, plan.slices);
+    count_launches(1);
     if (e != cudaSuccess) return cuda_status(e, "prefill launch");
   }
   return FA_OK;

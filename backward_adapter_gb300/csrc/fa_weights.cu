@@ -640,36 +640,34 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 }
 
 template <int D, bool Q4, bool PAGED, int NT, bool STORED>
-cudaError_t launch_weights_few(const WeightArgs& a, long long heads, cudaStream_t st, int row0 = 0) {
+fa_status launch_weights_few(const WeightArgs& a, long long heads, cudaStream_t st, int row0 = 0) {
   // 256 keys a warp, so that what comes before the first costs little, where that leaves eight warps for each SM at least, else 64 (groups of four runs)
   const int runs = heads * ((a.W + 255) / 256) >= 8LL * sm_count() ? 16 : 4;
   const long long chunks = (a.W + runs * kRun - 1) / (runs * kRun), warps = heads * chunks;
-  if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (warps > 0x7fffffffLL) return cuda_status(cudaErrorInvalidConfiguration, "cache weights launch");
   weights_few_kernel<D, Q4, PAGED, NT, STORED><<<(unsigned)((warps + 3) / 4), 128, 0, st>>>(a, runs, (unsigned)chunks, (unsigned)warps, row0);
   count_launches(1);
-  return cudaGetLastError();
+  return cuda_status(cudaGetLastError(), "cache weights launch");
 }
 
 template <int D, bool Q4, bool PAGED>
-cudaError_t launch_weights(const WeightArgs& a, long long heads, cudaStream_t st) {
+fa_status launch_weights(const WeightArgs& a, long long heads, cudaStream_t st) {
   constexpr int bytes = WeightSmem<D>::kBytes;
   static_assert(bytes <= 232448, "shared memory of a block");
   auto kernel = weights_kernel<D, Q4, PAGED>;
   static std::atomic<uint64_t> allowed{0};
-  if (allowed.load(std::memory_order_acquire) == 0) {   // the split of registers holds for what the kernel is launched with
-    cudaFuncAttributes at;
-    const cudaError_t got = cudaFuncGetAttributes(&at, kernel);
-    if (got != cudaSuccess) return got;
-    if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+  if (allowed.load(std::memory_order_acquire) == 0) {
+    const fa_status got = check_split(kernel, "cache weights launch", kRegsLaunch);
+    if (got != FA_OK) return got;
   }
   const cudaError_t e = allow_shared(kernel, bytes, allowed);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess) return cuda_status(e, "cache weights launch");
   const long long total = heads * ((a.W + kUnit - 1) / kUnit);
-  if (total > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (total > 0x7fffffffLL) return cuda_status(cudaErrorInvalidConfiguration, "cache weights launch");
   const unsigned blocks = (unsigned)(total < sm_count() ? total : sm_count());
   kernel<<<blocks, kThreads, bytes, st>>>(a, (unsigned)total);
   count_launches(1);
-  return cudaGetLastError();
+  return cuda_status(cudaGetLastError(), "cache weights launch");
 }
 
 }  // namespace
@@ -738,9 +736,9 @@ fa_status key_weights(const fa_prefill_params* p, const void* q, const float* ls
         WeightArgs x = a;
         for (long long row0 = 0;; row0 += 16) {
           const bool few = rows_of_head - row0 <= 8;
-          const cudaError_t e = few ? launch_weights_few<D, Q4, P, 1, true>(x, heads, cs, (int)row0)
+          const fa_status got = few ? launch_weights_few<D, Q4, P, 1, true>(x, heads, cs, (int)row0)
                                     : launch_weights_few<D, Q4, P, 2, true>(x, heads, cs, (int)row0);
-          if (e != cudaSuccess || row0 + 16 >= rows_of_head) return e;
+          if (got != FA_OK || row0 + 16 >= rows_of_head) return got;
           x.weights = x.out;
         }
       }
@@ -752,10 +750,8 @@ fa_status key_weights(const fa_prefill_params* p, const void* q, const float* ls
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
-  cudaError_t e;
-  if (cv.q4) e = cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
-  else e = cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
-  return cuda_status(e, "cache weights launch");
+  if (cv.q4) return cv.D == 64 ? go(D64{}, std::true_type{}) : go(D128{}, std::true_type{});
+  return cv.D == 64 ? go(D64{}, std::false_type{}) : go(D128{}, std::false_type{});
 }
 
 }  // namespace
