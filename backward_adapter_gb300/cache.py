@@ -85,10 +85,9 @@ def _cache(k_q, k_d, v_q, v_d):
 
 
 def _paged(c, table, device):
-    """(the sequences and the keys they have room for: (B, Hkv, S, D), the address of fa_pages or None, what holds it) of a
-    cache's values c and its page table."""
-    if table is None:
-        return c[:4], None, None
+    """(the sequences and the keys they have room for: (B, Hkv, S, D), the address of fa_pages, what holds it) of a cache's
+    values c and its page table. Without a table they are the first four of c, which the callers take without a call: one
+    costs a tenth of a launch."""
     if table.dtype != torch.int32:
         raise TypeError(f"table has dtype {table.dtype}, expected torch.int32")
     if table.dim() != 2:
@@ -135,7 +134,7 @@ def cache_write(k, v, k_q, k_d, v_q, v_d, begin, count=None, *, table=None, layo
     """
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device
-    seen, pages, held = _paged(c, table, device)
+    seen, pages, held = _paged(c, table, device) if table is not None else (c, None, None)
     n = k.shape[2 if layout == "bhsd" else 1] if k.dim() == 4 else -1
     shape = _rows_shape(seen, n, layout)
     if k.shape != shape or v.shape != shape:
@@ -163,13 +162,13 @@ def cache_read(k_q, k_d, v_q, v_d, begin=0, n_rows=None, *, table=None, dtype=to
     the cache is read as zeros and is reported by device_status()). table: the planes are a pool of pages (see new_cache)."""
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device
-    seen, pages, held = _paged(c, table, device)
+    seen, pages, held = _paged(c, table, device) if table is not None else (c, None, None)
     S = seen[2]
     begins = None
-    if isinstance(begin, torch.Tensor) and begin.numel() == 1 and \
-            (begin.dim() == 0 or n_rows is None or begin.dtype != torch.int64 or begin.device != device):
-        begin = int(begin)   # a number, for every sequence
-    if isinstance(begin, torch.Tensor):
+    own = type(begin) is not int and isinstance(begin, torch.Tensor)   # of each sequence, or a number in a tensor
+    if own and begin.numel() == 1 and (begin.dim() == 0 or n_rows is None or begin.dtype != torch.int64 or begin.device != device):
+        own = False
+    if own:
         if n_rows is None:
             raise ValueError("n_rows is needed where every sequence has its own begin")
         begins, first, n = _per_sequence("begin", begin, seen[0], device), 0, int(n_rows)
@@ -200,8 +199,9 @@ def cache_read(k_q, k_d, v_q, v_d, begin=0, n_rows=None, *, table=None, dtype=to
     return k, v
 
 
-def _queries(q, seen, device, layout: str, limit=None):
-    """(Hq, Sq, the layout's code) of q [B, Hq, Sq, D] or [B, Sq, Hq, D] over a cache of shape `seen`."""
+def _queries(q, seen, device, layout: str, out, lse, stream, attend: bool = True):
+    """(Hq, Sq, the layout's code, out, lse) of q [B, Hq, Sq, D] or [B, Sq, Hq, D] over a cache of shape `seen`: of a call that
+    attends the results, new ones where none are given. (One function, as a call of Python's costs a tenth of a launch.)"""
     if q.dtype != torch.bfloat16:
         raise TypeError(f"q has dtype {q.dtype}, expected torch.bfloat16")
     if q.dim() != 4:
@@ -217,12 +217,8 @@ def _queries(q, seen, device, layout: str, limit=None):
     if q.device != device:
         raise ValueError(f"q is on {q.device}, the cache on {device}")
     ft._need_cuda(q)
-    return Hq, Sq, code
-
-
-def _results(q, out, lse, Hq: int, Sq: int, stream):
-    """(out, lse) of an attention call: new ones, or those that are given."""
-    device, B = q.device, q.shape[0]
+    if not attend:
+        return Hq, Sq, code, out, lse
     if out is None:
         out = ft._like(q, stream)
     else:
@@ -235,14 +231,12 @@ def _results(q, out, lse, Hq: int, Sq: int, stream):
         if lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != device:
             raise ValueError(f"lse must be float32 {(B, Hq, Sq)} on {device}")
         ft._need_cuda(lse)
-    return out, lse
+    return Hq, Sq, code, out, lse
 
 
 def _window(window: int) -> int:
-    """As a 32-bit number; a longer window than any cache hides nothing."""
-    if not 0 <= window <= 0x7fffffff:
-        return -1 if window < 0 else 0x7fffffff
-    return window
+    """One that is no 32-bit number as one; a longer window than any cache hides nothing."""
+    return -1 if window < 0 else 0x7fffffff
 
 
 def decode(q, k_q, k_d, v_q, v_d, lengths=None, *, table=None, scale=None, window: int = 0, layout: str = "bhsd", out=None,
@@ -256,11 +250,10 @@ def decode(q, k_q, k_d, v_q, v_d, lengths=None, *, table=None, scale=None, windo
     """
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device
-    seen, pages, held = _paged(c, table, device)
-    Hq, Sq, code = _queries(q, seen, device, layout)
-    out, lse = _results(q, out, lse, Hq, Sq, stream)
+    seen, pages, held = _paged(c, table, device) if table is not None else (c, None, None)
+    Hq, Sq, code, out, lse = _queries(q, seen, device, layout, out, lse, stream)
     lens = None if lengths is None else _per_sequence("lengths", lengths, seen[0], device)
-    call = _DecodeCall(*c, Hq, Sq, _window(window), code, 1.0 / math.sqrt(c[3]) if scale is None else scale, 0)
+    call = _DecodeCall(*c, Hq, Sq, window if 0 <= window <= 0x7fffffff else _window(window), code, 1.0 / math.sqrt(c[3]) if scale is None else scale, 0)
     at = ctypes.addressof(call)
     lib = ft.load_library()
     ws_bytes = lib.fa_decode_pages_workspace_size(at + _CACHE, at, pages)
@@ -284,12 +277,11 @@ def prefill(q, k_q, k_d, v_q, v_d, lengths=None, count=None, *, table=None, scal
     """
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device
-    seen, pages, held = _paged(c, table, device)
-    Hq, Sq, code = _queries(q, seen, device, layout)
-    out, lse = _results(q, out, lse, Hq, Sq, stream)
+    seen, pages, held = _paged(c, table, device) if table is not None else (c, None, None)
+    Hq, Sq, code, out, lse = _queries(q, seen, device, layout, out, lse, stream)
     lens = None if lengths is None else _per_sequence("lengths", lengths, seen[0], device)
     counts = None if count is None else _per_sequence("count", count, seen[0], device)
-    call = _DecodeCall(*c, Hq, min(Sq, 0x7fffffff), _window(window), code,
+    call = _DecodeCall(*c, Hq, min(Sq, 0x7fffffff), window if 0 <= window <= 0x7fffffff else _window(window), code,
                        1.0 / math.sqrt(c[3]) if scale is None else scale, 0)
     at = ctypes.addressof(call)
     lib = ft.load_library()
@@ -326,9 +318,9 @@ def cache_weights(q, lse, k_q, k_d, lengths=None, count=None, *, weights=None, o
         raise ValueError("decode attends with all of q's tokens: no count")
     c = _cache(k_q, k_d, k_q, k_d)
     device = k_q.device
-    seen, pages, held = _paged(c, table, device)
-    B, Hkv, S, D = seen
-    Hq, Sq, code = _queries(q, seen, device, layout)
+    seen, pages, held = _paged(c, table, device) if table is not None else (c, None, None)
+    B, Hkv, S, D = seen[:4]
+    Hq, Sq, code, out, lse = _queries(q, seen, device, layout, out, lse, stream, attend=False)
     if lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or lse.device != device:
         raise ValueError(f"lse must be float32 {(B, Hq, Sq)} on {device}")
     ft._need_cuda(lse)
@@ -341,7 +333,7 @@ def cache_weights(q, lse, k_q, k_d, lengths=None, count=None, *, weights=None, o
         W = out.shape[2]
     lens = None if lengths is None else _per_sequence("lengths", lengths, B, device)
     counts = None if count is None else _per_sequence("count", count, B, device)
-    call = _DecodeCall(*c, Hq, min(Sq, 0x7fffffff), _window(window), code, 1.0 / math.sqrt(D) if scale is None else scale, 0)
+    call = _DecodeCall(*c, Hq, min(Sq, 0x7fffffff), window if 0 <= window <= 0x7fffffff else _window(window), code, 1.0 / math.sqrt(D) if scale is None else scale, 0)
     at = ctypes.addressof(call)
     lib, which = ft.load_library(), (lens,) if decoded else (lens, counts)
     ft._launch(device, lib.fa_cache_weights_decoded if decoded else lib.fa_cache_weights, at + _CACHE, q.data_ptr(), lse.data_ptr(),
@@ -363,7 +355,7 @@ def cache_evict(k_q, k_d, v_q, v_d, weights, lengths, keep: int, *, sinks: int =
     """
     c = _cache(k_q, k_d, v_q, v_d)
     device = k_q.device
-    seen, pages, held = _paged(c, table, device)
+    seen, pages, held = _paged(c, table, device) if table is not None else (c, None, None)
     if table_out is not None and table is None:
         raise ValueError("table_out needs a table")
     to, to_held = None, None
