@@ -17,8 +17,9 @@
 //
 // Measured (device time): a token of 64 sequences of 1024 to 8192 keys, 32 heads on 8, D = 128 in 4 bits: 85 us, 2.4 TB/s of K and
 // weights, 36% of the measured copy rate (issue 60% busy, ALU 51%: turning bits into operands, with 20 warps an SM to wait for
-// memory; by tcgen05 tiles 274). 512 tokens over 67,584 keys in 8 bits, 16 heads on 4: 184 us, 0.77 PFLOP/s; its 551 million
-// exponentials alone would be 116 us at 16 a cycle and SM, and a copy without them takes 129.
+// memory; by tcgen05 tiles 295). 512 tokens over 67,584 keys in 8 bits, 16 heads on 4: 184 us, 0.77 PFLOP/s. No unit bounds it: the
+// products are 73 us (tensor cores 33% busy), its 551 million exponentials 57 at the measured 32 a cycle and SM (XU 36%), and issue is
+// 64% busy; a copy without exponentials takes 129. It is the way of each tile of rows from L2 to operands, products, TMEM and sums.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -641,7 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 
 template <int D, bool Q4, bool PAGED, int NT, bool STORED>
 fa_status launch_weights_few(const WeightArgs& a, long long heads, cudaStream_t st, int row0 = 0) {
-  // 256 keys a warp, so that what comes before the first costs little, where that leaves eight warps for each SM at least, else 64 (groups of four runs)
+  // 256 keys a warp, so that what comes before the first costs little, where that leaves eight warps for each SM at least, else 64
+  // (groups of four runs). In 4 bits, D = 128, 8 heads, with 256 and with 64, of 4 rows and of 16: 64 sequences of 1024 to 8192 keys
+  // 83.5 and 93.6 us, 107 and 130; one of 67,584 22.1 and 21.2, 25.9 and 29.7; 16 of 1024 to 4096 21.4 and 16.4, 25.2 and 22.0 (fourteen
+  // warps an SM, of different lengths); 8 of 1000 to 4000 (seven) 17.5 and 10.0, 17.8 and 13.8; 2 of 500 to 1000 12.1 and 5.5, 13.7 and 6.9.
   const int runs = heads * ((a.W + 255) / 256) >= 8LL * sm_count() ? 16 : 4;
   const long long chunks = (a.W + runs * kRun - 1) / (runs * kRun), warps = heads * chunks;
   if (warps > 0x7fffffffLL) return cuda_status(cudaErrorInvalidConfiguration, "cache weights launch");
@@ -742,6 +746,10 @@ fa_status key_weights(const fa_prefill_params* p, const void* q, const float* ls
           x.weights = x.out;
         }
       }
+      // Up to 16 rows by way of registers, more by tcgen05 tiles: a step of 64 sequences of 1024 to 8192 keys, 8 heads, D = 128, takes
+      // with 4, 8 and 16 rows 83, 84 and 107 us against 295 to 297 in 4 bits, 91, 92 and 109 against 347 to 352 in 8; one sequence of
+      // 67,584 keys 22 (4 rows) and 26 (16) against 60. The two meet further on: 20, 24 and 32 rows (which are not built) 148, 148 and
+      // 168 against 300, and 42 to 47 against 60.
       if (rows_of_head <= 8) return launch_weights_few<D, Q4, P, 1, false>(a, heads, cs);
       if (rows_of_head <= 16) return launch_weights_few<D, Q4, P, 2, false>(a, heads, cs);
       return launch_weights<D, Q4, P>(a, heads, cs);

@@ -589,8 +589,8 @@ FA_API fa_status fa_train_bwd_noalloc(const fa_params* p, const void* q, const v
  * `site` ran out of its time limit (the kernel then stopped early and its outputs
  * are invalid), 0x40000000 | site when a kernel met a device-side argument it
  * could not use (site 950: a row index of fa_set_rows_backward outside [0, S); 951: a row of
- * fa_cache_write outside the cache; 952: a length or count of fa_decode, fa_prefill,
- * fa_cache_weights or fa_cache_evict out of its range; 953: an entry of a page table that is
+ * fa_cache_write or fa_cache_read outside the cache; 952: a length or count of fa_decode, fa_prefill,
+ * fa_cache_weights (or _decoded) or fa_cache_evict out of its range; 953: an entry of a page table that is
  * no page of the pool).
  * Synchronous (waits for the device to finish the copy). Returns FA_ERR_CUDA if
  * no device is usable.
