@@ -148,3 +148,38 @@ def test_prefill_scores_that_rise_over_several_tiles(n, window, D, fmt):
     again = kv.prefill(q, *planes, pu.i64(lengths), scale=8 / D, window=window)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
     assert ft.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["a_short_window", "all_keys", "a_short_window_250"])
+def test_several_tiles_of_a_slice_on_two_streams_and_in_a_graph(name):
+    Hq, Hkv, n, lengths, counts, window = CASES[name]
+    B = len(lengths)
+    _, pool, table = pu.make_any(B, Hkv, max(lengths), 128, "q4_0", 48, 5)
+    qs, lens, cnts = [pu.queries(B, Hq, n, 128, s) for s in (1, 2)], pu.i64(lengths), pu.i64(counts)
+    outs = [(torch.zeros_like(q), torch.zeros((B, Hq, n), device="cuda")) for q in qs]
+    go = lambda q, o, **kw: kv.prefill(q, *pool, lens, cnts, table=table, window=window, out=o[0], lse=o[1], **kw)  # noqa: E731
+    for q, o in zip(qs, outs):
+        go(q, o)
+    want = [[t.clone() for t in o] for o in outs]
+    same = lambda: all(torch.equal(t, w) for o, x in zip(outs, want) for t, w in zip(o, x))  # noqa: E731
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        for o in outs:
+            o[0].zero_()
+        torch.cuda.synchronize()
+        for s, q, o in zip(streams, qs, outs):
+            go(q, o, stream=s)
+        torch.cuda.synchronize()
+        assert same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for q, o in zip(qs, outs):
+            go(q, o)
+    for _ in range(5):
+        for o in outs:
+            o[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same()
+    assert ft.device_status() == 0
