@@ -371,8 +371,8 @@ def cache_evict(k_q, k_d, v_q, v_d, weights, lengths, keep: int, *, sinks: int =
         raise ValueError(f"weights_out has shape {tuple(weights_out.shape)}, weights {tuple(weights.shape)}")
     lens = _per_sequence("lengths", lengths, B, device)
     keep, sinks, recent = (max(-1, min(int(n), 0x7fffffff)) for n in (keep, sinks, recent))
-    if keep < 1:
-        raise ValueError(f"keep {keep}: at least 1")
+    if not 1 <= keep <= 1 << 24:   # before `kept` is made as large
+        raise ValueError(f"keep {keep}: 1 to 2^24")
     if kept is None:
         kept = ft._empty((B, Hkv, keep), (Hkv * keep, keep, 1), torch.int32, device, stream)
     else:

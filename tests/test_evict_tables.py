@@ -61,3 +61,15 @@ def test_columns_of_one_tensor_are_two_tables(B):
         with pytest.raises(ft.FaError, match="share entries"):
             kv.cache_evict(*pool, w, lens, keep, table=a, table_out=bad)
     assert ft.device_status() == 0
+
+
+@pytest.mark.parametrize("keep", [(1 << 24) + 1, 1 << 31, 1 << 60])
+def test_more_keys_to_keep_than_a_cache_holds_are_refused_before_memory_is_asked_for(keep, monkeypatch):
+    planes = (torch.zeros(2, 2, 16, 64, dtype=torch.int8), torch.zeros(2, 2, 16, 2, dtype=torch.float16)) * 2
+
+    def memory(*a):
+        raise AssertionError("memory")
+    monkeypatch.setattr(ft, "_need_cuda", lambda *a: None)
+    monkeypatch.setattr(ft, "_empty", memory)
+    with pytest.raises(ValueError, match="keep"):
+        kv.cache_evict(*planes, torch.zeros(2, 2, 16), torch.zeros(2, dtype=torch.int64), keep, stream=0)
